@@ -490,6 +490,76 @@ nvfp4moe_status moe_grouped_gemm_mxfp8(nvfp4moe_epilogue epi, const uint8_t* a, 
                                        size_t ws_bytes, void* stream);
 size_t moe_grouped_gemm_mxfp8_workspace_size(int32_t rows, int32_t E, int32_t Nw, int32_t K);
 
+/* ---------------------------------------------------------------------------
+ * nvfp4_matvec, mxfp4_matvec -- products of up to 16 rows with one 4-bit weight matrix, for the
+ * dense layers and the shared experts beside the routed ones at decode sizes; one launch, no
+ * workspace, 16-bit activations with either weight format ([P2] "The NVFP4 Pivot": W4A16).
+ *     P = X . W^T  (float32 accumulation of exact products; NVFP4: * w_g[0])
+ *     EPI_NONE  : out = P + add                                 [T, Nw]
+ *     EPI_SWIGLU: out = silu(P[:, :Nw/2]) * P[:, Nw/2:] + add   [T, Nw/2]
+ * rounded once, to out_dtype.
+ *
+ *   x, ldx      device bf16 [T, K], rows ldx elements apart: 16-byte aligned, ldx % 8 == 0,
+ *               K <= ldx < 2^26.
+ *   T           1 <= T <= 16.
+ *   w_codes, w_scales   device, one matrix [Nw, K] in the tiled storage of nvfp4_weights_tile
+ *               (mxfp4_matvec: of mxfp4_weights_tile), 16-byte aligned; w_g device float[1].
+ *   Nw, K       Nw >= 16, Nw % 16 == 0 (EPI_SWIGLU: >= 32, % 32, gate rows first), K >= 32,
+ *               K % 32 == 0; Nw * K / 2 < 2^31 (K rounded up to a multiple of 128).
+ *   add, add_dtype, ld_add   device F32 or BF16 [T, n], n the columns of out, rows ld_add >= n
+ *               elements apart; or NULL. May be out itself (same type and row distance).
+ *   out, out_dtype, ld_out   device F32 or BF16 [T, n] (output), rows ld_out >= n elements
+ *               apart; what lies between the rows is not written.
+ * A row's result does not depend on the other rows, except that up to 4 and more than 4 rows
+ * may sum in another order; a NaN or Inf in one row stays in that row.
+ * ------------------------------------------------------------------------- */
+nvfp4moe_status nvfp4_matvec(nvfp4moe_epilogue epi, const void* x, int64_t ldx, int32_t T, const uint8_t* w_codes,
+                             const uint8_t* w_scales, const float* w_g, int32_t Nw, int32_t K, const void* add,
+                             nvfp4moe_dtype add_dtype, int64_t ld_add, void* out, nvfp4moe_dtype out_dtype,
+                             int64_t ld_out, void* stream);
+nvfp4moe_status mxfp4_matvec(nvfp4moe_epilogue epi, const void* x, int64_t ldx, int32_t T, const uint8_t* w_codes,
+                             const uint8_t* w_scales, int32_t Nw, int32_t K, const void* add,
+                             nvfp4moe_dtype add_dtype, int64_t ld_add, void* out, nvfp4moe_dtype out_dtype,
+                             int64_t ld_out, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_layer_few_nvfp4, moe_layer_few_mxfp4 -- the whole mixture-of-experts layer of up to 16
+ * tokens in two launches, where the launches of the separate calls (moe_dispatch_w4a16, two
+ * GEMMs with the preparation of h between them, moe_unpermute_reduce) cost as much as the
+ * weights' traffic. [P1] section 3 (launch overhead of many small kernels), [P3] "Discovering
+ * the sgl_kernel Alternative" (a fused MoE). 16-bit activations with either weight format.
+ *     ids, w as moe_route_permute(logits, T, E, k) gives them
+ *     h[t,j] = silu(x'_t W_gate^T) * (x'_t W_up^T) of expert ids[t,j]
+ *     out[t] = bf16( sum_j w[t,j] * h[t,j] W_down^T )
+ * with x' = x, or (fp8_act) x after the FP8 E4M3 round trip of act_fp8_e4m3_roundtrip, whose
+ * scale is taken over all T rows. Sums are float32; h is held between the launches as f16 with
+ * a power of two for every 16 columns (NVFP4) or as bf16 (MXFP4); out is rounded once.
+ *
+ *   logits      device float [T, E], finite.
+ *   x           device bf16 [T, H], 16-byte aligned.
+ *   T, E, k     1 <= T <= 16, 1 <= k <= min(E, 64), E <= 1024.
+ *   H, F        multiples of 32, >= 32; H < 2^26, T * k * F * 2 < 2^31, and 2 * F * H / 2 < 2^31
+ *               (H rounded up to a multiple of 128, and likewise H * F / 2 with F).
+ *   fp8_act     0 or 1.
+ *   w13_*, w2_* device, the E matrices [2F, H] (gate rows first) and [H, F] in the tiled storage
+ *               (nvfp4_weights_tile or mxfp4_weights_tile), 16-byte aligned; w13_g, w2_g
+ *               device float [E].
+ *   out         device bf16 [T, H] (output).
+ *   ws          moe_layer_few_*_workspace_size(T, E, k, H, F) bytes, 16-byte aligned, caller-owned
+ *               scratch (the sizes that the call refuses give 0). Calls that may overlap need
+ *               a workspace each.
+ * ------------------------------------------------------------------------- */
+nvfp4moe_status moe_layer_few_nvfp4(const float* logits, const void* x, int32_t T, int32_t E, int32_t k, int32_t H,
+                                    int32_t F, int32_t fp8_act, const uint8_t* w13_codes, const uint8_t* w13_scales,
+                                    const float* w13_g, const uint8_t* w2_codes, const uint8_t* w2_scales,
+                                    const float* w2_g, void* out, void* ws, size_t ws_bytes, void* stream);
+size_t moe_layer_few_nvfp4_workspace_size(int32_t T, int32_t E, int32_t k, int32_t H, int32_t F);
+nvfp4moe_status moe_layer_few_mxfp4(const float* logits, const void* x, int32_t T, int32_t E, int32_t k, int32_t H,
+                                    int32_t F, const uint8_t* w13_codes, const uint8_t* w13_scales,
+                                    const uint8_t* w2_codes, const uint8_t* w2_scales, void* out, void* ws,
+                                    size_t ws_bytes, void* stream);
+size_t moe_layer_few_mxfp4_workspace_size(int32_t T, int32_t E, int32_t k, int32_t H, int32_t F);
+
 /* Thread-local message describing the last non-OK status ("" if none). Never NULL. */
 const char* nvfp4moe_last_error(void);
 /* nvfp4moe_path of the last moe_grouped_gemm_nvfp4 call on this thread. */

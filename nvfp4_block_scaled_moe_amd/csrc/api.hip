@@ -897,3 +897,179 @@ nvfp4moe_status moe_grouped_gemm_mxfp8(nvfp4moe_epilogue epi, const uint8_t* a, 
 }
 
 }  // extern "C"
+
+// ------------------------------------------------------------------ a few rows
+namespace {
+// The checks shared by the products of a few rows: sizes of the matrices and their tiled storage.
+nvfp4moe_status few_matrix_checks(const char* fn, const char* what, const uint8_t* codes, const uint8_t* scales,
+                                  int32_t Nw, int32_t K, int32_t step) {
+  if (!codes || !scales) return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: null %s pointer", fn, what);
+  if (!aligned(codes, 16) || !aligned(scales, 16))
+    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: the tiled %s must be 16-byte aligned", fn, what);
+  if (Nw < step || Nw % step != 0 || K < 32 || K % 32 != 0)
+    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: %s: need Nw >= %d, Nw %% %d == 0, K >= 32, K %% 32 == 0 (Nw=%d K=%d)", fn,
+                what, step, step, Nw, K);
+  // a matrix's tiles are addressed with 31-bit offsets
+  if ((int64_t)Nw * ((K + 127) / 128 * 64) >= (int64_t(1) << 31) ||
+      (int64_t)Nw * ((K + 1023) / 1024 * 64) >= (int64_t(1) << 31))
+    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: %s: Nw * K / 2 must be < 2^31", fn, what);
+  return NVFP4MOE_OK;
+}
+
+nvfp4moe_status few_matvec(const char* fn, bool mx, nvfp4moe_epilogue epi, const void* x, int64_t ldx, int32_t T,
+                           const uint8_t* w_codes, const uint8_t* w_scales, const float* w_g, int32_t Nw, int32_t K,
+                           const void* add, nvfp4moe_dtype add_dtype, int64_t ld_add, void* out,
+                           nvfp4moe_dtype out_dtype, int64_t ld_out, void* stream) {
+  if (epi != NVFP4MOE_EPI_NONE && epi != NVFP4MOE_EPI_SWIGLU)
+    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: bad epilogue %d", fn, (int)epi);
+  const bool swiglu = epi == NVFP4MOE_EPI_SWIGLU;
+  if ((out_dtype != NVFP4MOE_F32 && out_dtype != NVFP4MOE_BF16) ||
+      (add && add_dtype != NVFP4MOE_F32 && add_dtype != NVFP4MOE_BF16))
+    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: out_dtype and add_dtype must be F32 or BF16", fn);
+  if (!x || !out || (!mx && !w_g)) return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: null tensor pointer", fn);
+  if (T < 1 || T > kFewMaxTokens)
+    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: need 1 <= T <= %d (T=%d)", fn, kFewMaxTokens, T);
+  const nvfp4moe_status chk = few_matrix_checks(fn, "weights", w_codes, w_scales, Nw, K, swiglu ? 32 : 16);
+  if (chk != NVFP4MOE_OK) return chk;
+  if (ldx < K || ldx % 8 != 0 || ldx >= (int64_t(1) << 26) || !aligned(x, 16))
+    return fail(NVFP4MOE_ERR_INVALID_ARG,
+                "%s: x must be 16-byte aligned with K <= ldx < 2^26, ldx %% 8 == 0 (K=%d ldx=%lld)", fn, K,
+                (long long)ldx);
+  const int32_t n = swiglu ? Nw / 2 : Nw;
+  if (ld_out < n || (add && ld_add < n))
+    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: ld_out and ld_add must be at least %d", fn, n);
+  if (!aligned(out, out_dtype == NVFP4MOE_F32 ? 4 : 2) || (add && !aligned(add, add_dtype == NVFP4MOE_F32 ? 4 : 2)) ||
+      !aligned(w_g, 4))
+    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: out, add and w_g must be aligned to their elements", fn);
+  FewArgs a{};
+  a.x = static_cast<const uint16_t*>(x);
+  a.ldx = ldx;
+  a.T = T;
+  a.K = K;
+  a.codes = w_codes;
+  a.scales = w_scales;
+  a.g = w_g;
+  a.Nw = Nw;
+  a.add = add;
+  a.add_bf16 = add_dtype == NVFP4MOE_BF16;
+  a.ld_add = ld_add;
+  a.out = out;
+  a.out_bf16 = out_dtype == NVFP4MOE_BF16;
+  a.ld_out = ld_out;
+  return hip_status(launch_few_matvec(a, mx, swiglu, static_cast<hipStream_t>(stream)), fn);
+}
+
+bool few_layer_sizes_ok(int32_t T, int32_t E, int32_t k, int32_t H, int32_t F) {
+  return T >= 1 && T <= kFewMaxTokens && E >= 1 && E <= kMaxExperts && k >= 1 && k <= E && k <= kMaxTopK && H >= 32 &&
+         H % 32 == 0 && F >= 32 && F % 32 == 0 && H < (1 << 26) && (int64_t)T * k * F * 2 < (int64_t(1) << 31);
+}
+
+// Workspace: the item list, h, and (NVFP4) the exponents of its blocks of 16 columns.
+struct FewLayerWs {
+  size_t plan, h, hexp, total;
+};
+FewLayerWs few_layer_ws(int32_t T, int32_t k, int32_t F, bool mx) {
+  FewLayerWs w{};
+  w.plan = round_up(sizeof(FewPlan));
+  w.h = round_up((size_t)T * k * F * 2);
+  w.hexp = mx ? 0 : round_up((size_t)T * k * (F / 16));
+  w.total = w.plan + w.h + w.hexp;
+  return w;
+}
+
+nvfp4moe_status few_layer(const char* fn, bool mx, const float* logits, const void* x, int32_t T, int32_t E, int32_t k,
+                          int32_t H, int32_t F, int32_t fp8_act, const uint8_t* w13_codes, const uint8_t* w13_scales,
+                          const float* w13_g, const uint8_t* w2_codes, const uint8_t* w2_scales, const float* w2_g,
+                          void* out, void* ws, size_t ws_bytes, void* stream) {
+  if (!logits || !x || !out || (!mx && (!w13_g || !w2_g)))
+    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: null tensor pointer", fn);
+  if (T < 1 || T > kFewMaxTokens || E < 1 || E > kMaxExperts || k < 1 || k > E || k > kMaxTopK)
+    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: need 1 <= T <= %d, 1 <= k <= min(E, %d), E <= %d (T=%d E=%d k=%d)", fn,
+                kFewMaxTokens, kMaxTopK, kMaxExperts, T, E, k);
+  if (fp8_act != 0 && fp8_act != 1) return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: fp8_act must be 0 or 1", fn);
+  if (!few_layer_sizes_ok(T, E, k, H, F))
+    return fail(NVFP4MOE_ERR_INVALID_ARG,
+                "%s: need H and F multiples of 32, H < 2^26 and T * k * F * 2 < 2^31 (H=%d F=%d)", fn, H, F);
+  nvfp4moe_status chk = few_matrix_checks(fn, "w13", w13_codes, w13_scales, 2 * F, H, 64);
+  if (chk == NVFP4MOE_OK) chk = few_matrix_checks(fn, "w2", w2_codes, w2_scales, H, F, 32);
+  if (chk != NVFP4MOE_OK) return chk;
+  if (!aligned(x, 16) || !aligned(logits, 4) || !aligned(out, 2) || !aligned(w13_g, 4) || !aligned(w2_g, 4))
+    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: x must be 16-byte aligned, the others aligned to their elements", fn);
+  const FewLayerWs lay = few_layer_ws(T, k, F, mx);
+  if (!ws || ws_bytes < lay.total)
+    return fail(NVFP4MOE_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, lay.total, ws_bytes);
+  if (!aligned(ws, 16)) return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
+  char* base = static_cast<char*>(ws);
+  FewArgs up{};
+  up.x = static_cast<const uint16_t*>(x);
+  up.ldx = H;
+  up.T = T;
+  up.K = H;
+  up.codes = w13_codes;
+  up.scales = w13_scales;
+  up.g = w13_g;
+  up.Nw = 2 * F;
+  up.logits = logits;
+  up.E = E;
+  up.k = k;
+  up.g_down = w2_g;
+  up.fp8 = fp8_act;
+  up.plan = reinterpret_cast<FewPlan*>(base);
+  up.h = base + lay.plan;
+  up.hexp = mx ? nullptr : reinterpret_cast<int8_t*>(base + lay.plan + lay.h);
+  FewArgs down = up;
+  down.K = F;
+  down.codes = w2_codes;
+  down.scales = w2_scales;
+  down.g = w2_g;
+  down.Nw = H;
+  down.out = out;
+  down.out_bf16 = 1;
+  down.ld_out = H;
+  return hip_status(launch_few_layer(up, down, mx, static_cast<hipStream_t>(stream)), fn);
+}
+}  // namespace
+
+extern "C" {
+
+nvfp4moe_status nvfp4_matvec(nvfp4moe_epilogue epi, const void* x, int64_t ldx, int32_t T, const uint8_t* w_codes,
+                             const uint8_t* w_scales, const float* w_g, int32_t Nw, int32_t K, const void* add,
+                             nvfp4moe_dtype add_dtype, int64_t ld_add, void* out, nvfp4moe_dtype out_dtype,
+                             int64_t ld_out, void* stream) {
+  return few_matvec("nvfp4_matvec", false, epi, x, ldx, T, w_codes, w_scales, w_g, Nw, K, add, add_dtype, ld_add, out,
+                    out_dtype, ld_out, stream);
+}
+
+nvfp4moe_status mxfp4_matvec(nvfp4moe_epilogue epi, const void* x, int64_t ldx, int32_t T, const uint8_t* w_codes,
+                             const uint8_t* w_scales, int32_t Nw, int32_t K, const void* add,
+                             nvfp4moe_dtype add_dtype, int64_t ld_add, void* out, nvfp4moe_dtype out_dtype,
+                             int64_t ld_out, void* stream) {
+  return few_matvec("mxfp4_matvec", true, epi, x, ldx, T, w_codes, w_scales, nullptr, Nw, K, add, add_dtype, ld_add,
+                    out, out_dtype, ld_out, stream);
+}
+
+size_t moe_layer_few_nvfp4_workspace_size(int32_t T, int32_t E, int32_t k, int32_t H, int32_t F) {
+  return few_layer_sizes_ok(T, E, k, H, F) ? few_layer_ws(T, k, F, false).total : 0;
+}
+
+size_t moe_layer_few_mxfp4_workspace_size(int32_t T, int32_t E, int32_t k, int32_t H, int32_t F) {
+  return few_layer_sizes_ok(T, E, k, H, F) ? few_layer_ws(T, k, F, true).total : 0;
+}
+
+nvfp4moe_status moe_layer_few_nvfp4(const float* logits, const void* x, int32_t T, int32_t E, int32_t k, int32_t H,
+                                    int32_t F, int32_t fp8_act, const uint8_t* w13_codes, const uint8_t* w13_scales,
+                                    const float* w13_g, const uint8_t* w2_codes, const uint8_t* w2_scales,
+                                    const float* w2_g, void* out, void* ws, size_t ws_bytes, void* stream) {
+  return few_layer("moe_layer_few_nvfp4", false, logits, x, T, E, k, H, F, fp8_act, w13_codes, w13_scales, w13_g,
+                   w2_codes, w2_scales, w2_g, out, ws, ws_bytes, stream);
+}
+
+nvfp4moe_status moe_layer_few_mxfp4(const float* logits, const void* x, int32_t T, int32_t E, int32_t k, int32_t H,
+                                    int32_t F, const uint8_t* w13_codes, const uint8_t* w13_scales,
+                                    const uint8_t* w2_codes, const uint8_t* w2_scales, void* out, void* ws,
+                                    size_t ws_bytes, void* stream) {
+  return few_layer("moe_layer_few_mxfp4", true, logits, x, T, E, k, H, F, 0, w13_codes, w13_scales, nullptr, w2_codes,
+                   w2_scales, nullptr, out, ws, ws_bytes, stream);
+}
+
+}  // extern "C"

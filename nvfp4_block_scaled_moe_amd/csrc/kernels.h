@@ -151,6 +151,44 @@ hipError_t launch_gemm_mx(const GemmArgs& a, int max_mtiles, int bits, hipStream
 int mx_ksplit(int max_mtiles, int Nw, int K);
 hipError_t launch_zero_f32(float* p, int n, hipStream_t stream);
 
+// ---- few_rows.hip: up to kFewMaxTokens rows
+constexpr int kFewMaxTokens = 16;
+constexpr int kFewMaxSlots = kFewMaxTokens * kMaxTopK;
+// What the layer's first launch leaves for its second: the items (expert << 16 | mask of its
+// tokens) with the first of their rows in h, and for every row of h its routing weight (NVFP4:
+// times the global scale of the expert's second matrix).
+struct FewPlan {
+  int n_items;
+  uint32_t item[kFewMaxSlots];
+  uint16_t row0[kFewMaxSlots];
+  float weight[kFewMaxSlots];
+};
+struct FewArgs {
+  const uint16_t* x;      // bf16 [T, K], rows ldx elements apart (matvec, the layer's first launch)
+  int64_t ldx;
+  int T, K;               // K: columns of the matrices (H, or F in the layer's second launch)
+  const uint8_t* codes;   // tiled matrices [Nw, K], one per expert
+  const uint8_t* scales;
+  const float* g;         // their global scales (NVFP4)
+  int Nw;
+  int ks_log;             // set by the launcher
+  const void* add;        // matvec: float32 or bf16 [T, n], rows ld_add apart, or null
+  int add_bf16;
+  int64_t ld_add;
+  void* out;              // matvec: float32 or bf16; the layer's second launch: bf16
+  int out_bf16;
+  int64_t ld_out;
+  const float* logits;    // layer: [T, E]
+  int E, k;
+  const float* g_down;    // layer, NVFP4: global scales of the second matrices
+  int fp8;                // layer, NVFP4: the rows first take the FP8 E4M3 round trip
+  FewPlan* plan;          // layer workspace
+  void* h;                // [T * k, F] f16 (NVFP4) or bf16 (MXFP4)
+  int8_t* hexp;           // NVFP4: [T * k, F / 16] exponents of h's blocks of 16 columns
+};
+hipError_t launch_few_matvec(FewArgs a, bool mx, bool swiglu, hipStream_t stream);
+hipError_t launch_few_layer(FewArgs up, FewArgs down, bool mx, hipStream_t stream);
+
 // ---- reduce.hip
 hipError_t launch_unpermute_reduce(const void* y, bool y_bf16, const int* slot_to_row,
                                    const float* topk_w, int T, int k, int H, uint16_t* out,

@@ -7,6 +7,7 @@ computation runs in the library's HIP kernels; a failed call raises NVFP4MoEErro
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 from dataclasses import dataclass
@@ -441,6 +442,138 @@ def moe_grouped_gemm_mxfp8(epi: int, a: torch.Tensor, a_scales: torch.Tensor, w:
         _ptr(out), _DT[out.dtype], _ptr(amax), _ptr(ws), ws.numel(), _stream())
     _lib.check("moe_grouped_gemm_mxfp8", st)
     return (out, amax) if want_amax else out
+
+
+# ------------------------------------------------------------------ a few rows
+_NO_GUARD = contextlib.nullcontext()
+
+
+def _gpu(fn: str, *ts) -> int:
+    """Index of the GPU that holds every given tensor (None entries aside)."""
+    dev = ts[0].device
+    for t in ts:
+        if t is not None and (t.device != dev or not t.is_cuda):
+            raise ValueError(f"{fn}: all tensors must be on one GPU")
+    return dev.index
+
+
+def _on(index: int):
+    """The tensors' GPU made current for the call (launches go to the current one)."""
+    return _NO_GUARD if torch.cuda.current_device() == index else torch.cuda.device(index)
+
+
+def _rows(fn: str, what: str, t: torch.Tensor, n: int, align: int = 1):
+    """(t, row distance): a 2-D tensor [rows, n] whose rows are contiguous, in place if its
+    row distance and address allow, else as a contiguous copy."""
+    if t.dim() != 2 or t.shape[1] != n:
+        raise ValueError(f"{fn}: {what} must be [rows, {n}], got {tuple(t.shape)}")
+    one = t.shape[0] <= 1
+    if t.stride(1) != 1 or (not one and (t.stride(0) < n or t.stride(0) % align)) or \
+            t.data_ptr() % (align * t.element_size()):
+        t = t.contiguous()
+        if t.data_ptr() % (align * t.element_size()):   # a view with an offset that was contiguous already
+            t = t.clone()
+    return t, (n if one or t.is_contiguous() else t.stride(0))
+
+
+def _out_rows(fn: str, out, T: int, n: int, dtype, device):
+    """(out, row distance) of an output [T, n]: allocated, or the caller's with contiguous rows."""
+    if out is None:
+        return torch.empty((T, n), dtype=dtype, device=device), n
+    if out.shape != (T, n) or out.dtype not in _DT or (n > 1 and out.stride(1) != 1) or \
+            (T > 1 and out.stride(0) < n):
+        raise ValueError(f"{fn}: out must be float32 or bf16 [{T}, {n}] with contiguous rows")
+    return out, (out.stride(0) if T > 1 else n)
+
+
+def _matvec(fn: str, x, w, epi, add, out_dtype, out, g):
+    if x.dtype != torch.bfloat16:
+        raise ValueError(f"{fn}: x must be bf16, got {x.dtype}")
+    if w.B != 1:
+        raise ValueError(f"{fn}: one weight matrix is needed, got {w.B}")
+    if out_dtype not in _DT or (add is not None and add.dtype not in _DT):
+        raise ValueError(f"{fn}: out_dtype and add must be float32 or bf16")
+    idx = _gpu(fn, x, w.codes, w.scales, g, add, out)
+    Nw, K = w.R, w.C
+    x, ldx = _rows(fn, "x", x, K, 8)
+    T = x.shape[0]
+    n = Nw // 2 if epi == EPI_SWIGLU else Nw
+    ld_add = n
+    if add is not None:
+        if add.shape[0] != T:
+            raise ValueError(f"{fn}: add must be [{T}, {n}], got {tuple(add.shape)}")
+        add, ld_add = _rows(fn, "add", add, n)
+    with _on(idx):
+        out, ld_out = _out_rows(fn, out, T, n, out_dtype, x.device)
+        rest = (Nw, K, None if add is None else add.data_ptr(), F32 if add is None else _DT[add.dtype], ld_add,
+                out.data_ptr(), _DT[out.dtype], ld_out, torch.cuda.current_stream().cuda_stream)
+        lib = _lib.load()
+        head = (epi, x.data_ptr(), ldx, T, w.codes.data_ptr(), w.scales.data_ptr())
+        st = lib.nvfp4_matvec(*head, g.data_ptr(), *rest) if g is not None else lib.mxfp4_matvec(*head, *rest)
+    _lib.check(fn, st)
+    return out
+
+
+def nvfp4_matvec(x: torch.Tensor, w: TiledWeights, epi: int = EPI_NONE, *, add: torch.Tensor | None = None,
+                 out_dtype=torch.bfloat16, out: torch.Tensor | None = None):
+    """Up to 16 bf16 rows ``x`` [T, K] times one NVFP4 matrix ``w`` [Nw, K] (tiled):
+    x W^T (+ add), or with EPI_SWIGLU silu(gate) * up (+ add), in one launch. ``add`` [T, n]
+    float32 or bf16 (may be ``out``); rows of x, add and out may lie apart."""
+    return _matvec("nvfp4_matvec", x, w, epi, add, out_dtype, out, w.g)
+
+
+def mxfp4_matvec(x: torch.Tensor, w: MxTiledWeights, epi: int = EPI_NONE, *, add: torch.Tensor | None = None,
+                 out_dtype=torch.bfloat16, out: torch.Tensor | None = None):
+    """nvfp4_matvec with one MXFP4 matrix ``w`` (mxfp4_weights_tile)."""
+    return _matvec("mxfp4_matvec", x, w, epi, add, out_dtype, out, None)
+
+
+def _layer_few(fn: str, x, logits, k, w13, w2, g13, g2, fp8_acts, out):
+    if x.dtype != torch.bfloat16 or x.dim() != 2 or logits.dim() != 2 or logits.shape[0] != x.shape[0]:
+        raise ValueError(f"{fn}: x must be bf16 [T, H] and logits [T, E]")
+    (T, H), E, F = x.shape, logits.shape[1], w2.C
+    if w13.B != E or w2.B != E or w13.C != H or w2.R != H or w13.R != 2 * F:
+        raise ValueError(f"{fn}: weights [{w13.B}, {w13.R}, {w13.C}] and [{w2.B}, {w2.R}, {w2.C}] do not fit "
+                         f"logits [T, {E}] and x [T, {H}]")
+    idx = _gpu(fn, x, logits, w13.codes, w13.scales, w2.codes, w2.scales, g13, g2, out)
+    logits = logits.contiguous().float()
+    x, ldx = _rows(fn, "x", x, H, 8)
+    if ldx != H:
+        x = x.contiguous()
+    if out is not None and (out.shape != (T, H) or out.dtype != torch.bfloat16 or not out.is_contiguous()):
+        raise ValueError(f"{fn}: out must be contiguous bf16 [{T}, {H}]")
+    lib = _lib.load()
+    with _on(idx):
+        if out is None:
+            out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+        stream = torch.cuda.current_stream().cuda_stream
+        if g13 is not None:
+            ws = _ws(lib.moe_layer_few_nvfp4_workspace_size(T, E, k, H, F), x.device)
+            st = lib.moe_layer_few_nvfp4(logits.data_ptr(), x.data_ptr(), T, E, k, H, F, int(fp8_acts),
+                                         w13.codes.data_ptr(), w13.scales.data_ptr(), g13.data_ptr(),
+                                         w2.codes.data_ptr(), w2.scales.data_ptr(), g2.data_ptr(), out.data_ptr(),
+                                         ws.data_ptr(), ws.numel(), stream)
+        else:
+            ws = _ws(lib.moe_layer_few_mxfp4_workspace_size(T, E, k, H, F), x.device)
+            st = lib.moe_layer_few_mxfp4(logits.data_ptr(), x.data_ptr(), T, E, k, H, F, w13.codes.data_ptr(),
+                                         w13.scales.data_ptr(), w2.codes.data_ptr(), w2.scales.data_ptr(),
+                                         out.data_ptr(), ws.data_ptr(), ws.numel(), stream)
+    _lib.check(fn, st)
+    return out
+
+
+def moe_layer_few_nvfp4(x: torch.Tensor, logits: torch.Tensor, k: int, w13: TiledWeights, w2: TiledWeights, *,
+                        fp8_acts: bool = False, out: torch.Tensor | None = None):
+    """The whole MoE layer of up to 16 tokens in two launches: top-``k`` of ``logits`` [T, E],
+    SwiGLU experts ``w13`` (E matrices [2F, H]) and ``w2`` (E matrices [H, F]), weighted sum.
+    ``x`` bf16 [T, H] (after the FP8 E4M3 round trip with ``fp8_acts``) -> bf16 [T, H]."""
+    return _layer_few("moe_layer_few_nvfp4", x, logits, k, w13, w2, w13.g, w2.g, fp8_acts, out)
+
+
+def moe_layer_few_mxfp4(x: torch.Tensor, logits: torch.Tensor, k: int, w13: MxTiledWeights, w2: MxTiledWeights, *,
+                        out: torch.Tensor | None = None):
+    """moe_layer_few_nvfp4 with MXFP4 experts (16-bit activations)."""
+    return _layer_few("moe_layer_few_mxfp4", x, logits, k, w13, w2, None, None, False, out)
 
 
 def last_dispatch() -> int:
