@@ -538,7 +538,7 @@ nvfp4moe_status mxfp4_matvec(nvfp4moe_epilogue epi, const void* x, int64_t ldx, 
  *   logits      device float [T, E], finite.
  *   x           device bf16 [T, H], 16-byte aligned.
  *   T, E, k     1 <= T <= 16, 1 <= k <= min(E, 64), E <= 1024.
- *   H, F        multiples of 32, >= 32; H < 2^26, T * k * F * 2 < 2^31, and 2 * F * H / 2 < 2^31
+ *   H, F        multiples of 32, >= 32; H <= 32768, T * k * F * 2 < 2^31, and 2 * F * H / 2 < 2^31
  *               (H rounded up to a multiple of 128, and likewise H * F / 2 with F).
  *   fp8_act     0 or 1.
  *   w13_*, w2_* device, the E matrices [2F, H] (gate rows first) and [H, F] in the tiled storage

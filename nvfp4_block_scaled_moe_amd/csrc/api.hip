@@ -961,7 +961,7 @@ nvfp4moe_status few_matvec(const char* fn, bool mx, nvfp4moe_epilogue epi, const
 
 bool few_layer_sizes_ok(int32_t T, int32_t E, int32_t k, int32_t H, int32_t F) {
   return T >= 1 && T <= kFewMaxTokens && E >= 1 && E <= kMaxExperts && k >= 1 && k <= E && k <= kMaxTopK && H >= 32 &&
-         H % 32 == 0 && F >= 32 && F % 32 == 0 && H < (1 << 26) && (int64_t)T * k * F * 2 < (int64_t(1) << 31);
+         H % 32 == 0 && H <= kFewMaxHidden && F >= 32 && F % 32 == 0 && (int64_t)T * k * F * 2 < (int64_t(1) << 31);
 }
 
 // Workspace: the item list, h, and (NVFP4) the exponents of its blocks of 16 columns.
@@ -972,7 +972,7 @@ FewLayerWs few_layer_ws(int32_t T, int32_t k, int32_t F, bool mx) {
   FewLayerWs w{};
   w.plan = round_up(sizeof(FewPlan));
   w.h = round_up((size_t)T * k * F * 2);
-  w.hexp = mx ? 0 : round_up((size_t)T * k * (F / 16));
+  w.hexp = mx ? 0 : round_up((size_t)T * k * ((F + 127) / 128) * 8);
   w.total = w.plan + w.h + w.hexp;
   return w;
 }
@@ -989,7 +989,7 @@ nvfp4moe_status few_layer(const char* fn, bool mx, const float* logits, const vo
   if (fp8_act != 0 && fp8_act != 1) return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: fp8_act must be 0 or 1", fn);
   if (!few_layer_sizes_ok(T, E, k, H, F))
     return fail(NVFP4MOE_ERR_INVALID_ARG,
-                "%s: need H and F multiples of 32, H < 2^26 and T * k * F * 2 < 2^31 (H=%d F=%d)", fn, H, F);
+                "%s: need H and F multiples of 32, H <= %d and T * k * F * 2 < 2^31 (H=%d F=%d)", fn, kFewMaxHidden, H, F);
   nvfp4moe_status chk = few_matrix_checks(fn, "w13", w13_codes, w13_scales, 2 * F, H, 64);
   if (chk == NVFP4MOE_OK) chk = few_matrix_checks(fn, "w2", w2_codes, w2_scales, H, F, 32);
   if (chk != NVFP4MOE_OK) return chk;

@@ -53,6 +53,10 @@ constexpr int kNT = kW * kWave;
 constexpr int kGrid = 512;               // persistent workgroups: 2 on each of the 256 CUs
 constexpr int kRowBytes = 256 + 16;      // LDS bytes of one row's chunk (padded: conflict-free reads)
 constexpr int kItemTok = 4;              // tokens of one item of the layer
+template <bool B>
+struct Flag {
+  static constexpr bool value = B;
+};
 constexpr int kNoExp = -120;             // exponent of a block of h without a finite non-zero value
 
 // ------------------------------------------------------------------ operand decode
@@ -68,6 +72,8 @@ __device__ __forceinline__ float e8m0_to_f32(uint32_t s) {
   const uint32_t bits = s == 255u ? 0x7fc00000u : s == 0u ? 0x00400000u : s << 23;
   return __uint_as_float(bits);
 }
+
+__host__ __device__ __forceinline__ int nch_of(int K) { return (K + kChunk - 1) / kChunk; }
 
 // Max over the 16 lanes of a row, in all of them.
 __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
@@ -107,16 +113,26 @@ struct Decode<true> {
   }
 };
 
-// Byte offset of the lane's scale bytes of (16-row block blk, chunk c) in the tiled scales.
+// Offset of the dword that holds the lane's scale bytes of (16-row block blk, chunk c) in the
+// tiled scales, and the bytes taken out of it. (Whole dwords: a narrower load's zero extension
+// would be placed, and waited for, at the end of the loop body instead of at its use.)
 template <bool MX>
-__device__ __forceinline__ uint32_t scale_off(uint32_t blk, uint32_t nch, uint32_t c, uint32_t lane) {
-  if (MX) return (blk * ((nch + 15) >> 4) + (c >> 4)) * 1024u + 16u * lane + (c & 15);
-  return (blk * ((nch + 7) >> 3) + (c >> 3)) * 1024u + 16u * lane + 2u * (c & 7);
+__device__ __forceinline__ uint32_t scale_off(uint32_t blk, uint32_t nch, uint32_t c) {
+  if (MX) return (blk * ((nch + 15) >> 4) + (c >> 4)) * 1024u + (c & 12);
+  return (blk * ((nch + 7) >> 3) + (c >> 3)) * 1024u + 2u * (c & 6);
 }
 template <bool MX>
-__device__ __forceinline__ uint32_t ld_scale(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-  if (MX) return (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(r, off, 0, 0);
-  return ld16(r, off, 0);
+__device__ __forceinline__ uint32_t scale_of(uint32_t dword, uint32_t c) {
+  return MX ? (dword >> (8u * (c & 3))) & 0xffu : dword >> (16u * (c & 1));
+}
+__device__ __forceinline__ uint32_t ld32(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+}
+// An offset as a value of its own: keeps the compiler from turning a select of offsets into
+// branches with a load in each, after which it could only wait for all loads at once.
+__device__ __forceinline__ uint32_t settled(uint32_t off) {
+  asm("" : "+v"(off));
+  return off;
 }
 
 // Eight bf16 elements of a row's chunk, held by 16 lanes together, as f16 scaled by a power of
@@ -148,33 +164,89 @@ __device__ __forceinline__ f16x8 chunk_to_f16(const u32x4& v, float& unscale) {
   return o;
 }
 
-// ------------------------------------------------------------------ matvec, and the layer's first launch
-// Waves deal out the chunks ks at a time (ks = 1, 2, 4 or 8: kW / ks groups of waves, each
-// with RB row blocks of its own, when K has fewer than 8 chunks).
-template <bool MX, bool LAYER, bool SWIGLU, int R, int RB, int D>
+// Power of two (as a float) that takes a row's largest finite magnitude, given as bf16 bits,
+// into [2^14, 2^15), and the one that takes it back.
+__device__ __forceinline__ uint32_t row_exponent(uint32_t top) { return max(top >> 7, 15u); }
+__device__ __forceinline__ float row_scale(uint32_t top) { return __uint_as_float((268u - row_exponent(top)) << 23); }
+__device__ __forceinline__ float row_unscale(uint32_t top) { return __uint_as_float((row_exponent(top) - 14u) << 23); }
+// Largest finite magnitude of eight bf16 values, as bf16 bits.
+__device__ __forceinline__ uint32_t finite_top(const u32x4& v) {
+  uint32_t t = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = v[i] & 0x7fffu, hi = (v[i] >> 16) & 0x7fffu;
+    t = max(t, lo < 0x7f80u ? lo : 0u);
+    t = max(t, hi < 0x7f80u ? hi : 0u);
+  }
+  return t;
+}
+__device__ __forceinline__ f16x8 scaled_f16(const u32x4& v, float scale) {
+  f16x8 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[2 * i] = (f16)(bf16_to_f32(v[i] & 0xffffu) * scale);
+    o[2 * i + 1] = (f16)(__uint_as_float(v[i] & 0xffff0000u) * scale);
+  }
+  return o;
+}
+
+// First column block of wave group rg's b-th row block in a tile: gate blocks, then their up blocks.
+template <bool SWIGLU, int RB>
+__device__ __forceinline__ uint32_t tile_block(uint32_t sub, int b, uint32_t nblk) {
+  return SWIGLU ? sub * (RB / 2) + b % (RB / 2) + (b < RB / 2 ? 0 : nblk / 2) : sub * RB + b;
+}
+// Whether that block exists: the last tile may be short.
+template <bool SWIGLU, int RB>
+__device__ __forceinline__ bool tile_block_in(uint32_t sub, int b, uint32_t nblk) {
+  return SWIGLU ? sub * (RB / 2) + b % (RB / 2) < nblk / 2 : sub * RB + b < nblk;
+}
+
+// The output of one element of a matvec.
+__device__ __forceinline__ void put_matvec(const FewArgs& p, int col, size_t n0, float v) {
+  if (p.add) {
+    const size_t ao = (size_t)col * p.ld_add + n0;
+    v += p.add_bf16 ? bf16_to_f32(static_cast<const uint16_t*>(p.add)[ao]) : static_cast<const float*>(p.add)[ao];
+  }
+  const size_t o = (size_t)col * p.ld_out + n0;
+  if (p.out_bf16)
+    static_cast<__bf16*>(p.out)[o] = (__bf16)v;
+  else
+    static_cast<float*>(p.out)[o] = v;
+}
+
+// ------------------------------------------------------------------ resident rows: matvec, and the layer's first launch
+// The rows (the item's, or all of them once when they fit) stay in LDS as matrix operands, f16
+// with one power of two a row (NVFP4) or bf16 (MXFP4): turned once, they serve every tile of
+// the item. Waves deal out the chunks ks at a time (ks = 1, 2, 4 or 8: kW / ks groups of
+// waves, each with RB row blocks of its own, when K has fewer than 8 chunks).
+constexpr int kPassBatch = 4;   // pieces a thread requests together
+
+template <bool MX, bool LAYER, bool FP8, bool SWIGLU, int NTOK, int RB, int D>
 __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
   typedef Decode<MX> Dec;
   typedef typename Dec::Op Op;
   static_assert(!SWIGLU || RB == 2, "a gate block and its up block");
-  static_assert(!LAYER || (SWIGLU && R == 1), "items of up to 4 tokens");
-  constexpr int NTOK = 4 * R;
-  constexpr int BUF = R > 1 ? 1 : 2;
+  static_assert(!LAYER || (SWIGLU && NTOK == kItemTok), "the layer's items");
+  static_assert(!FP8 || (LAYER && !MX), "FP8 activations: the NVFP4 layer");
+  constexpr int BUF = NTOK > 4 ? 1 : 2;
   constexpr int REDF = kW * RB * NTOK * 16;
-  __shared__ __attribute__((aligned(16))) unsigned char s_row[kW][NTOK * kRowBytes];
-  __shared__ float s_unscale[kW][NTOK];
+  extern __shared__ __attribute__((aligned(16))) unsigned char s_rows[];   // [rows][K128 * 2 + 16]
   __shared__ __attribute__((aligned(16))) float s_red[BUF][REDF];
+  __shared__ uint32_t s_top[NTOK];                          // largest finite magnitude of each row
   __shared__ uint32_t s_item[LAYER ? kFewMaxSlots : 1];     // expert << 16 | token mask
   __shared__ uint16_t s_row0[LAYER ? kFewMaxSlots : 1];     // first row of the item in h
   __shared__ uint32_t s_first[LAYER ? kMaxExperts : 1];     // token mask, then item << 16 | row
   __shared__ int s_ids[LAYER ? kFewMaxSlots : 1];
   __shared__ float s_w[LAYER ? kFewMaxSlots : 1];
-  __shared__ uint32_t s_n[2];
+  __shared__ float s_amax[kW];
+  __shared__ uint32_t s_n;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   const int T = p.T, K = p.K;
   const uint32_t nch = (uint32_t)(K + kChunk - 1) / kChunk;
+  const uint32_t stride = nch * 256u + 16u;              // LDS bytes of a row
   const int KS = 1 << p.ks_log, RG = kW >> p.ks_log;
   const int ksl = wave & (KS - 1), rg = wave >> p.ks_log;
   const int cpw = ((int)nch + KS - 1) >> p.ks_log;       // chunks of a tile for each wave
@@ -183,15 +255,74 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
   const int tpi = (nsub + RG - 1) / RG;                  // tiles of an item
   const uint32_t wbytes = nblk * nch * 1024u;
   const uint32_t sbytes = nblk * (MX ? (nch + 15) >> 4 : (nch + 7) >> 3) * 1024u;
+  const bool all_rows = !LAYER || T <= p.item_tok;       // every row fits: staged once
   float fp8_s = 1.0f;
 
+  // ---- rows (all_rows: every row, else those of mask) into LDS, in two passes over them by any
+  // number nt of threads: their largest magnitudes (NVFP4), then, after a barrier, the operands.
+  // The second pass reads the rows again, from the caches: kept in registers between the passes
+  // they would cost the ring its depth.
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(p.x, (uint32_t)((p.ldx * (T - 1) + K) * 2));
+  const uint32_t ppr = nch * 16u;   // 16-byte pieces of a row
+  auto pass = [&](auto put_c, uint32_t mask, int first, int nt) {
+    constexpr bool PUT = decltype(put_c)::value;
+    const int nrow = all_rows ? T : __popc(mask);
+    const uint32_t total = (uint32_t)nrow * ppr;
+    for (uint32_t i0 = (uint32_t)first; i0 < total; i0 += kPassBatch * nt) {
+      u32x4 v[kPassBatch];
+      uint32_t row[kPassBatch], q[kPassBatch];
+#pragma unroll
+      for (int i = 0; i < kPassBatch; ++i) {
+        const uint32_t idx = i0 + i * nt;
+        row[i] = idx / ppr;
+        q[i] = idx - row[i] * ppr;
+        uint32_t tok = row[i];
+        if (LAYER && !all_rows) {
+          uint32_t m = mask;
+#pragma unroll
+          for (uint32_t j = 0; j < (uint32_t)kItemTok - 1; ++j) m = j < row[i] ? m & (m - 1) : m;
+          tok = (uint32_t)__ffs(m) - 1u;
+        }
+        const bool in = idx < total && 8u * q[i] < (uint32_t)K;
+        v[i] = ld128(xr, settled(in ? tok * (uint32_t)p.ldx * 2u + 16u * q[i] : kOOB), 0);
+      }
+#pragma unroll
+      for (int i = 0; i < kPassBatch; ++i) {
+        const bool in = i0 + i * nt < total;
+        if (FP8) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            v[i][j] = fp8_roundtrip_bits(bf16_to_f32(v[i][j] & 0xffffu), fp8_s) |
+                      fp8_roundtrip_bits(__uint_as_float(v[i][j] & 0xffff0000u), fp8_s) << 16;
+        }
+        if (!PUT) {
+          const uint32_t top = row16_max(finite_top(v[i]));   // (a row's pieces come in whole sixteens)
+          if (l16 == 0 && in) atomicMax(&s_top[row[i]], top);
+        } else if (in) {
+          unsigned char* at = s_rows + row[i] * stride + 16u * q[i];
+          if (MX)
+            *reinterpret_cast<u32x4*>(at) = v[i];
+          else
+            *reinterpret_cast<f16x8*>(at) = scaled_f16(v[i], row_scale(s_top[row[i]]));
+        }
+      }
+    }
+    // Every load has arrived (they are newer than any of the ring's): without the wait here the
+    // compiler would place it in the main loop, for the lanes that used none of theirs.
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+  };
+  const Flag<false> find_top;
+  const Flag<true> put;
+
   int nitems = 1;
+  if (tid < NTOK) s_top[tid] = 0;
   if constexpr (LAYER) {
     // ---- routing: a wave per token, then the list of items in ascending expert order
     static_assert(BUF * REDF >= kW * 3 * kWave, "the routing scratch fits");
     const int E = p.E, k = p.k, S = T * k;
     uint32_t* scratch = reinterpret_cast<uint32_t*>(&s_red[0][0]) + wave * 3 * kWave;
     for (int e = tid; e < E; e += kNT) s_first[e] = 0;
+    __syncthreads();   // s_top and s_first are cleared
     for (int t = wave; t < T; t += kW) {
       const float* row = p.logits + (size_t)t * E;
       if (E <= 256)
@@ -201,8 +332,10 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
       else
         route_token_thresh<16>(row, E, k, lane, s_ids + t * k, s_w + t * k, nullptr, scratch);
     }
+    // (at most kItemTok tokens when all rows fit: the other waves look at the rows meanwhile)
+    if (!MX && !FP8 && all_rows && wave >= kItemTok) pass(find_top, 0, tid - kItemTok * kWave, kNT - kItemTok * kWave);
     float amax = 0.0f;
-    if (!MX && p.fp8) {   // one scale for all the rows, from the largest finite magnitude
+    if (FP8) {   // one scale for all the rows, from the largest finite magnitude
       const int per = K / 8;
       for (int i = tid; i < T * per; i += kNT) {
         const int t = i / per;
@@ -211,22 +344,25 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
         amax = bf16x8_finite_max(w, amax);
       }
       amax = wave_max(amax);
-      if (lane == 0) s_unscale[wave][0] = amax;
+      if (lane == 0) s_amax[wave] = amax;
     }
     __syncthreads();
-    if (!MX && p.fp8) {
-      for (int w = 0; w < kW; ++w) amax = fmaxf(amax, s_unscale[w][0]);
+    if (FP8) {
+      for (int w = 0; w < kW; ++w) amax = fmaxf(amax, s_amax[w]);
       fp8_s = fp8_scale(amax);
     }
     for (int s = tid; s < S; s += kNT) atomicOr(&s_first[s_ids[s]], 1u << (s / k));
     __syncthreads();
+    if (FP8 && all_rows && wave > 0) pass(find_top, 0, tid - kWave, kNT - kWave);
+    if (!FP8 && all_rows && wave > 0) pass(put, 0, tid - kWave, kNT - kWave);
     if (wave == 0) {
       const int per = (E + kWave - 1) / kWave;
+      const uint32_t cap = (uint32_t)p.item_tok;
       uint32_t cnt = 0;   // items << 16 | rows of this lane's experts
       for (int i = 0; i < per; ++i) {
         const int e = lane * per + i;
         const uint32_t n = e < E ? (uint32_t)__popc(s_first[e]) : 0u;
-        cnt += ((n + kItemTok - 1) / kItemTok) << 16 | n;
+        cnt += ((n + cap - 1) / cap) << 16 | n;
       }
       uint32_t incl = cnt;
 #pragma unroll
@@ -241,20 +377,19 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
         uint32_t m = s_first[e];
         s_first[e] = at;
         while (m) {
-          uint32_t part = m;   // the lowest kItemTok tokens of m
-#pragma unroll
-          for (int j = 0; j < kItemTok; ++j) part &= part - 1;
-          part = m & ~part;
+          uint32_t rest = m;   // m without its lowest `cap` tokens
+          for (uint32_t j = 0; j < cap; ++j) rest &= rest - 1;
+          const uint32_t part = m & ~rest;
           s_item[at >> 16] = (uint32_t)e << 16 | part;
           s_row0[at >> 16] = (uint16_t)(at & 0xffffu);
           at += 0x10000u + (uint32_t)__popc(part);
-          m &= ~part;
+          m = rest;
         }
       }
-      if (lane == kWave - 1) s_n[0] = incl >> 16;
+      if (lane == kWave - 1) s_n = incl >> 16;
     }
     __syncthreads();
-    nitems = __builtin_amdgcn_readfirstlane((int)s_n[0]);
+    nitems = __builtin_amdgcn_readfirstlane((int)s_n);
     if (blockIdx.x == 0) {   // the list for the second launch
       for (int i = tid; i < nitems; i += kNT) p.plan->item[i] = s_item[i];
       for (int i = tid; i < nitems; i += kNT) p.plan->row0[i] = s_row0[i];
@@ -270,126 +405,117 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
     }
   }
 
-  // ---- this workgroup's tiles, as one flat sequence of chunks
+  // ---- this workgroup's tiles, in runs of one item's, each a flat sequence of steps (a chunk of
+  // RB weight tiles) padded to whole turns of the ring
   const int64_t ntiles = (int64_t)nitems * tpi;
   const int t0 = (int)(ntiles * blockIdx.x / gridDim.x);
   const int t1 = (int)(ntiles * (blockIdx.x + 1) / gridDim.x);
   if (t0 >= t1) return;
-  const int nst = (t1 - t0) * cpw;
 
-  const __amdgpu_buffer_rsrc_t xr = make_rsrc(p.x, (uint32_t)((p.ldx * (T - 1) + K) * 2));
   __amdgpu_buffer_rsrc_t wr, sr;
-  uint32_t xoff[R];
   auto item_word = [&](int it) -> uint32_t {
     return LAYER ? (uint32_t)__builtin_amdgcn_readfirstlane((int)s_item[it]) : (1u << T) - 1u;
   };
-  auto open_item = [&](int it) {   // the loads' side of an item: its matrix and its token rows
-    const uint32_t w = item_word(it);
-    const size_t e = LAYER ? w >> 16 : 0;
+  u32x4 wring[D][RB];
+  uint32_t sring[D][RB];
+  // The loads' position: the item, its tile and the step in it, and what is left of the run.
+  int it_l = t0 / tpi, tile_l = t0 - it_l * tpi, step_l = 0, tiles_l = t1 - t0, run_l = 0, pad_l = 0;
+  auto open_run = [&]() {   // the tiles left in the loads' item
+    const size_t e = LAYER ? item_word(it_l) >> 16 : 0;
     wr = make_rsrc(p.codes + e * wbytes, wbytes);
     sr = make_rsrc(p.scales + e * sbytes, sbytes);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      int tok = -1;
-      if (LAYER) {
-        uint32_t m = w & 0xffffu;
-        for (int q = 0; m; ++q, m &= m - 1) tok = q == g ? __builtin_ctz(m) : tok;
-      } else {
-        tok = 4 * r + g < T ? 4 * r + g : -1;
-      }
-      xoff[r] = tok >= 0 ? (uint32_t)(tok * p.ldx * 2) + 16u * l16 : kOOB;
-    }
+    const int n = min(tiles_l, tpi - tile_l);
+    tiles_l -= n;
+    run_l = n * cpw;
+    pad_l = (run_l + D - 1) / D * D - run_l;
   };
-
-  u32x4 wring[D][RB], xring[D][R];
-  uint32_t sring[D][RB];
-  int it_l = t0 / tpi, tile_l = t0 - it_l * tpi, step_l = 0, left_l = nst;   // the loads' position
-  open_item(it_l);
+  open_run();
   auto issue = [&](int d) {
     const uint32_t c = (uint32_t)(ksl + (step_l << p.ks_log));
     const uint32_t sub = (uint32_t)(tile_l * RG + rg);
-    const bool ok = left_l > 0 && c < nch && sub < (uint32_t)nsub;
+    const bool ok = run_l > 0 && c < nch && sub < (uint32_t)nsub;
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
-      const uint32_t blk = SWIGLU ? sub + (b ? nblk / 2 : 0) : sub * RB + b;
-      const bool in = ok && blk < nblk;
-      wring[d][b] = ld128(wr, in ? 16u * lane + (blk * nch + c) * 1024u : kOOB, 0);
-      sring[d][b] = ld_scale<MX>(sr, in ? scale_off<MX>(blk, nch, c, lane) : kOOB);
+      const uint32_t blk = tile_block<SWIGLU, RB>(sub, b, nblk);
+      const bool in = ok && tile_block_in<SWIGLU, RB>(sub, b, nblk);
+      wring[d][b] = ld128(wr, settled(16u * lane + (in ? (blk * nch + c) * 1024u : kOOB)), 0);
+      sring[d][b] = ld32(sr, settled(16u * lane + (in ? scale_off<MX>(blk, nch, c) : kOOB)));
     }
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-      xring[d][r] = ld128(xr, ok && (int)(c * kChunk) + 8 * l16 < K && xoff[r] != kOOB ? xoff[r] + c * 256u : kOOB, 0);
-    --left_l;
-    if (++step_l == cpw) {
-      step_l = 0;
-      if (++tile_l == tpi) {
-        tile_l = 0;
-        if (left_l > 0) open_item(++it_l);
-      }
+    // (arithmetic instead of branches: a branch here would send the position through memory)
+    const int real = run_l > 0 ? 1 : 0, wrap = real && step_l + 1 == cpw ? 1 : 0;
+    run_l -= real;
+    pad_l -= 1 - real;
+    step_l = wrap ? 0 : step_l + real;
+    tile_l += wrap;
+    if (run_l == 0 && pad_l == 0 && tiles_l > 0) {
+      tile_l = 0;
+      ++it_l;
+      open_run();
     }
   };
+
+  int it = it_l, tile = tile_l, step = 0, done = 0, buf = 0, left = t1 - t0;
+  if (!LAYER) __syncthreads();   // s_top is cleared
+  if (!MX && !LAYER) pass(find_top, 0, tid, kNT);
 #pragma unroll
   for (int d = 0; d < D; ++d) issue(d);
 
-  int it = t0 / tpi, tile = t0 - it * tpi, step = 0, done = 0, buf = 0;
   f32x4 tot[RB];
 #pragma unroll
   for (int b = 0; b < RB; ++b) tot[b] = (f32x4){0.f, 0.f, 0.f, 0.f};
-  unsigned char* row = s_row[wave];
-  const int ntok = LAYER ? NTOK : T;
-
-  for (int s = 0; s < nst; s += D) {
+  for (bool first = true; left > 0; first = false) {
+    const uint32_t word = item_word(it);
+    const int ncol = __popc(word & 0xffffu);
+    if (LAYER && !all_rows) {
+      if (!first) {
+        __syncthreads();   // the last epilogue has read the last item's rows
+        if (tid < NTOK) s_top[tid] = 0;
+        __syncthreads();
+      }
+      if (!MX) {
+        pass(find_top, word & 0xffffu, tid, kNT);
+        __syncthreads();
+      }
+      pass(put, word & 0xffffu, tid, kNT);
+      __syncthreads();
+    } else if (first && (!LAYER || FP8)) {
+      if (!MX && !LAYER) __syncthreads();
+      pass(put, 0, tid, kNT);
+      __syncthreads();
+    }
+    // The staged row of column col (the col-th token of the item; the last one past them).
+    auto row_of = [&](int col) -> uint32_t {
+      const int q = col < ncol ? col : ncol - 1;
+      if (!LAYER || !all_rows) return (uint32_t)q;
+      uint32_t rest = word & 0xffffu;
+      for (int j = 0; j < q; ++j) rest &= rest - 1;
+      return (uint32_t)__builtin_ctz(rest);
+    };
+    const uint32_t frow = settled(row_of(l16) * stride + 64u * g);
+    const float alpha = MX ? 1.0f : ld_const(p.g, LAYER ? word >> 16 : 0);
+    const int run = min(left, tpi - tile), nst = run * cpw;
+    left -= run;
+    for (int s = 0; s < nst; s += D) {
 #pragma unroll
-    for (int d = 0; d < D; ++d) {
-      if (s + d < nst) {
-        const uint32_t c = (uint32_t)(ksl + (step << p.ks_log));
-        const int sub = tile * RG + rg;
-        if (c < nch && sub < nsub) {
-          // the rows' chunk into the wave's LDS
+      for (int d = 0; d < D; ++d) {
+        if (s + d < nst) {
+          const uint32_t c = (uint32_t)(ksl + (step << p.ks_log));
+          if (c < nch && tile * RG + rg < nsub) {
+            Op bf[4];
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            if (R == 1 || 4 * r < T) {
-              u32x4 v = xring[d][r];
-              if (MX) {
-                *reinterpret_cast<u32x4*>(row + (4 * r + g) * kRowBytes + 16 * l16) = v;
-              } else {
-                if (LAYER && p.fp8) {
+            for (int j = 0; j < 4; ++j) bf[j] = *reinterpret_cast<const Op*>(s_rows + frow + c * 256u + 16 * j);
 #pragma unroll
-                  for (int i = 0; i < 4; ++i)
-                    v[i] = fp8_roundtrip_bits(bf16_to_f32(v[i] & 0xffffu), fp8_s) |
-                           fp8_roundtrip_bits(__uint_as_float(v[i] & 0xffff0000u), fp8_s) << 16;
-                }
-                float un;
-                const f16x8 h = chunk_to_f16(v, un);
-                *reinterpret_cast<f16x8*>(row + (4 * r + g) * kRowBytes + 16 * l16) = h;
-                if (l16 == 0) s_unscale[wave][4 * r + g] = un;
-              }
-            }
-          }
-          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-          const int fr = l16 & (NTOK - 1);
-          Op bf[4];
+            for (int b = 0; b < RB; ++b) {
+              Op wf[4];
+              Dec::run(wring[d][b], scale_of<MX>(sring[d][b], c), wf);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            bf[j] = *reinterpret_cast<const Op*>(row + fr * kRowBytes + 64 * g + 16 * j);
-          const float un = MX ? 1.0f : s_unscale[wave][fr];
-          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-          for (int b = 0; b < RB; ++b) {
-            Op wf[4];
-            Dec::run(wring[d][b], sring[d][b], wf);
-            f32x4 a = MX ? tot[b] : (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) a = Dec::mfma(wf[j], bf[j], a);
-            if (MX) {
-              tot[b] = a;
-            } else {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) tot[b][i] = fmaf(a[i], un, tot[b][i]);
+              for (int j = 0; j < 4; ++j) tot[b] = Dec::mfma(wf[j], bf[j], tot[b]);
             }
           }
         }
-        if (++step == cpw) {
+        issue(d);
+        step += s + d < nst ? 1 : 0;
+        if (step == cpw) {
           // ---- a tile is complete: the waves' sums, then the epilogue
           step = 0;
           float* red = s_red[buf];
@@ -401,15 +527,12 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
 #pragma unroll
           for (int b = 0; b < RB; ++b) tot[b] = (f32x4){0.f, 0.f, 0.f, 0.f};
           __syncthreads();
-          const uint32_t iw = item_word(it);
-          const int n = LAYER ? __popc(iw & 0xffffu) : ntok;
-          const float alpha = MX ? 1.0f : ld_const(p.g, LAYER ? iw >> 16 : 0);
           constexpr int NB = SWIGLU ? 1 : RB;
-          const int total = RG * NB * n * 16;
+          const int total = RG * NB * ncol * 16;
           // a different wave starts each tile, so that short epilogues spread over the SIMDs
           for (int i = (tid + kWave * done) & (kNT - 1); i < total; i += kNT) {
             const int r16 = i & 15, q = i >> 4;
-            const int grp = q / (NB * n), b = (q / n) % NB, col = q % n;
+            const int grp = q / (NB * ncol), b = (q / ncol) % NB, col = q % ncol;
             const int osub = tile * RG + grp;
             float v = 0.0f, u = 0.0f;
             for (int w = 0; w < KS; ++w) {
@@ -417,48 +540,176 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
               v += a[0];
               if (SWIGLU) u += a[NTOK * 16];
             }
-            v *= alpha;
-            if (SWIGLU) v = swiglu1(v, u * alpha);
+            const float un = MX ? 1.0f : row_unscale(s_top[row_of(col)]);
+            v = v * alpha * un;
+            if (SWIGLU) v = swiglu1(v, u * alpha * un);
             if constexpr (LAYER) {
               const uint32_t hr = (uint32_t)s_row0[it] + (uint32_t)col;
               const int F = p.Nw / 2, f = osub * 16 + r16;
               if (MX) {
-                if (osub < nsub) static_cast<uint16_t*>(p.h)[(size_t)hr * F + f] = (uint16_t)f32_to_bf16(v);
+                if (osub < nsub) static_cast<__bf16*>(p.h)[(size_t)hr * F + f] = (__bf16)v;
               } else {
                 const uint32_t top = row16_max(finite_abs_bits(v));
                 const int e2 = top ? max((int)(top >> 23) - 141, kNoExp) : kNoExp;
                 if (osub < nsub) {
                   static_cast<f16*>(p.h)[(size_t)hr * F + f] = (f16)ldexpf(v, -e2);
-                  if (r16 == 0) p.hexp[(size_t)hr * (F / 16) + osub] = (int8_t)e2;
+                  if (r16 == 0) p.hexp[(size_t)hr * (nch_of(F) * 8) + osub] = (int8_t)e2;
                 }
               }
-            } else {
-              const uint32_t blk = SWIGLU ? (uint32_t)osub : (uint32_t)(osub * RB + b);
-              if (osub < nsub && blk < (SWIGLU ? nblk / 2 : nblk)) {
-                const size_t n0 = (size_t)blk * 16 + r16;
-                if (p.add) {
-                  const size_t ao = (size_t)col * p.ld_add + n0;
-                  v += p.add_bf16 ? bf16_to_f32(static_cast<const uint16_t*>(p.add)[ao])
-                                  : static_cast<const float*>(p.add)[ao];
-                }
-                const size_t o = (size_t)col * p.ld_out + n0;
-                if (p.out_bf16)
-                  static_cast<uint16_t*>(p.out)[o] = (uint16_t)f32_to_bf16(v);
-                else
-                  static_cast<float*>(p.out)[o] = v;
-              }
+            } else if (osub < nsub && tile_block_in<SWIGLU, RB>(osub, b, nblk)) {
+              put_matvec(p, col, (size_t)tile_block<SWIGLU, RB>(osub, b, nblk) * 16 + r16, v);
             }
           }
           if (BUF == 1) __syncthreads();
           else buf ^= 1;
           ++done;
-          if (++tile == tpi) {
-            tile = 0;
-            ++it;
+          ++tile;
+        }
+      }
+    }
+    tile = 0;
+    ++it;
+  }
+}
+
+// ------------------------------------------------------------------ matvec of rows that do not fit
+// Up to 16 rows of any length: each wave turns its chunk of the rows itself, in a piece of LDS of
+// its own, with a power of two for every (row, chunk). The turning costs about as much as the
+// decode of four weight tiles, so a wave takes up to RB = 8 row blocks a chunk.
+template <bool MX, bool SWIGLU, int RB, int D, int WPS>
+__global__ __launch_bounds__(kNT, WPS) void few_long_kernel(const FewArgs p) {
+  typedef Decode<MX> Dec;
+  typedef typename Dec::Op Op;
+  constexpr int R = kFewMaxTokens / 4;
+  constexpr int HB = SWIGLU ? RB / 2 : RB;
+  __shared__ __attribute__((aligned(16))) unsigned char s_row[kW][kFewMaxTokens * kRowBytes];
+  __shared__ float s_unscale[kW][kFewMaxTokens];
+  __shared__ __attribute__((aligned(16))) float s_red[kW * RB][16 * 16];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, g = lane >> 4;
+  const int T = p.T, K = p.K;
+  const uint32_t nch = (uint32_t)nch_of(K);
+  const int cpw = ((int)nch + kW - 1) / kW;
+  const uint32_t nblk = (uint32_t)p.Nw / 16;
+  const int ntiles = ((int)(SWIGLU ? nblk / 2 : nblk) + HB - 1) / HB;
+  const uint32_t wbytes = nblk * nch * 1024u;
+  const uint32_t sbytes = nblk * (MX ? (nch + 15) >> 4 : (nch + 7) >> 3) * 1024u;
+  const int t0 = (int)((int64_t)ntiles * blockIdx.x / gridDim.x);
+  const int t1 = (int)((int64_t)ntiles * (blockIdx.x + 1) / gridDim.x);
+  const int nst = (t1 - t0) * cpw;
+
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(p.x, (uint32_t)((p.ldx * (T - 1) + K) * 2));
+  const __amdgpu_buffer_rsrc_t wr = make_rsrc(p.codes, wbytes), sr = make_rsrc(p.scales, sbytes);
+  uint32_t xoff[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) xoff[r] = 4 * r + g < T ? (uint32_t)((4 * r + g) * p.ldx * 2) + 16u * l16 : kOOB;
+
+  u32x4 wring[D][RB], xring[D][R];
+  uint32_t sring[D][RB];
+  int tile_l = t0, step_l = 0, left_l = nst;   // the loads' position
+  // A tile's blocks are refilled one by one as they are consumed, the rows' pieces before them.
+  uint32_t c_l = 0;
+  bool ok_l = false;
+  auto issue_rows = [&](int d) {
+    c_l = (uint32_t)(wave + step_l * kW);
+    ok_l = left_l > 0 && c_l < nch;
+    const bool cols = ok_l && (int)(c_l * kChunk) + 8 * l16 < K;
+#pragma unroll
+    for (int r = 0; r < R; ++r) xring[d][r] = ld128(xr, settled(cols ? xoff[r] + c_l * 256u : kOOB), 0);
+  };
+  auto issue_block = [&](int d, int b) {
+    const uint32_t blk = tile_block<SWIGLU, RB>(tile_l, b, nblk);
+    const bool in = ok_l && tile_block_in<SWIGLU, RB>(tile_l, b, nblk);
+    wring[d][b] = ld128(wr, settled(16u * lane + (in ? (blk * nch + c_l) * 1024u : kOOB)), 0);
+    sring[d][b] = ld32(sr, settled(16u * lane + (in ? scale_off<MX>(blk, nch, c_l) : kOOB)));
+  };
+  auto issue_end = [&]() {
+    --left_l;
+    const int wrap = step_l + 1 == cpw ? 1 : 0;
+    step_l = wrap ? 0 : step_l + 1;
+    tile_l += wrap;
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d) {
+    issue_rows(d);
+#pragma unroll
+    for (int b = 0; b < RB; ++b) issue_block(d, b);
+    issue_end();
+  }
+
+  f32x4 tot[RB];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) tot[b] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  unsigned char* row = s_row[wave];
+  int tile = t0, step = 0;
+  for (int s = 0; s < nst; s += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      // (chunks past the last have loaded zeros, rows and weights, and add nothing)
+      const uint32_t c = (uint32_t)(wave + step * kW);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (4 * r < T) {
+          if (MX) {
+            *reinterpret_cast<u32x4*>(row + (4 * r + g) * kRowBytes + 16 * l16) = xring[d][r];
+          } else {
+            float un;
+            *reinterpret_cast<f16x8*>(row + (4 * r + g) * kRowBytes + 16 * l16) = chunk_to_f16(xring[d][r], un);
+            if (l16 == 0) s_unscale[wave][4 * r + g] = un;
           }
         }
       }
-      issue(d);
+      issue_rows(d);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      Op bf[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) bf[j] = *reinterpret_cast<const Op*>(row + l16 * kRowBytes + 64 * g + 16 * j);
+      const float un = MX ? 1.0f : s_unscale[wave][l16];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+      for (int b = 0; b < RB; ++b) {
+        Op wf[4];
+        Dec::run(wring[d][b], scale_of<MX>(sring[d][b], c), wf);
+        issue_block(d, b);
+        f32x4 a = MX ? tot[b] : (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a = Dec::mfma(wf[j], bf[j], a);
+        if (MX) {
+          tot[b] = a;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tot[b][i] = fmaf(a[i], un, tot[b][i]);
+        }
+      }
+      issue_end();
+      step += s + d < nst ? 1 : 0;
+      if (step == cpw) {
+        step = 0;
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+          *reinterpret_cast<f32x4*>(&s_red[wave * RB + b][l16 * 16 + 4 * g]) = tot[b];
+          tot[b] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        }
+        __syncthreads();
+        const float alpha = MX ? 1.0f : ld_const(p.g, 0);
+        for (int i = tid; i < HB * T * 16; i += kNT) {
+          const int r16 = i & 15, q = i >> 4, b = q / T, col = q - b * T;
+          if (!tile_block_in<SWIGLU, RB>(tile, b, nblk)) continue;
+          float v = 0.0f, u = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kW; ++w) {
+            v += s_red[w * RB + b][col * 16 + r16];
+            if (SWIGLU) u += s_red[w * RB + b + HB][col * 16 + r16];
+          }
+          v *= alpha;
+          if (SWIGLU) v = swiglu1(v, u * alpha);
+          put_matvec(p, col, (size_t)tile_block<SWIGLU, RB>(tile, b, nblk) * 16 + r16, v);
+        }
+        __syncthreads();
+        ++tile;
+      }
     }
   }
 }
@@ -470,11 +721,11 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
   typedef Decode<MX> Dec;
   typedef typename Dec::Op Op;
   __shared__ __attribute__((aligned(16))) unsigned char s_row[kW][kItemTok * kRowBytes];
-  __shared__ float s_mul[kW][kItemTok];
   __shared__ __attribute__((aligned(16))) float s_red[kW * RB][16 * 16];
   __shared__ uint32_t s_item[kFewMaxSlots];
   __shared__ uint16_t s_row0[kFewMaxSlots];
-  __shared__ float s_w[kFewMaxSlots];
+  __shared__ float s_mul[kFewMaxSlots];      // what a row's products are multiplied with
+  __shared__ int8_t s_top[kFewMaxSlots];     // NVFP4: the largest exponent of a row's blocks
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -488,24 +739,26 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
   const int nitems = __builtin_amdgcn_readfirstlane(p.plan->n_items);
   for (int i = tid; i < nitems; i += kNT) s_item[i] = p.plan->item[i];
   for (int i = tid; i < nitems; i += kNT) s_row0[i] = p.plan->row0[i];
-  for (int i = tid; i < S; i += kNT) s_w[i] = p.plan->weight[i];
   __syncthreads();
 
   const int npair = nitems * (int)nch;
   const int nst = wave < npair ? (npair - wave + kW - 1) / kW : 0;   // this wave's pairs
   const __amdgpu_buffer_rsrc_t hr = make_rsrc(p.h, (uint32_t)S * (uint32_t)F * 2u);
-  const __amdgpu_buffer_rsrc_t er = make_rsrc(p.hexp, (uint32_t)S * (uint32_t)(F / 16));
+  const __amdgpu_buffer_rsrc_t er = make_rsrc(p.hexp, (uint32_t)S * nch * 8u);
   __amdgpu_buffer_rsrc_t wr, sr;
-  uint32_t hrow = 0;   // row of h for this lane's 16-lane group (kOOB: none)
+  uint32_t hoff = kOOB, eoff = kOOB;   // this lane's place in a row of h and of its exponents
   auto open_item = [&](int a) {
     const uint32_t w = (uint32_t)__builtin_amdgcn_readfirstlane((int)s_item[a]);
     wr = make_rsrc(p.codes + (size_t)(w >> 16) * wbytes, wbytes);
     sr = make_rsrc(p.scales + (size_t)(w >> 16) * sbytes, sbytes);
-    hrow = g < __popc(w & 0xffffu) ? (uint32_t)s_row0[a] + (uint32_t)g : kOOB;
+    const bool in = g < __popc(w & 0xffffu);
+    const uint32_t hrow = (uint32_t)s_row0[a] + (uint32_t)g;
+    hoff = in ? (hrow * (uint32_t)F + 8u * l16) * 2u : kOOB;
+    eoff = in ? hrow * (nch * 8u) + (l16 >> 3) * 4u : kOOB;
   };
   u32x4 wring[D][RB], xring[D];
   uint32_t sring[D][RB];
-  int ering[D];
+  uint32_t ering[D];   // the exponents of four blocks of 16 columns, the lane's own among them
   int a_l = wave / (int)nch, c_l = wave - a_l * (int)nch, left_l = nst;
   if (nst > 0) open_item(a_l);
   auto issue = [&](int d) {
@@ -515,12 +768,12 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
     for (int b = 0; b < RB; ++b) {
       const uint32_t blk = blockIdx.x * RB + b;
       const bool in = ok && blk < nblk;
-      wring[d][b] = ld128(wr, in ? 16u * lane + (blk * nch + c) * 1024u : kOOB, 0);
-      sring[d][b] = ld_scale<MX>(sr, in ? scale_off<MX>(blk, nch, c, lane) : kOOB);
+      wring[d][b] = ld128(wr, settled(16u * lane + (in ? (blk * nch + c) * 1024u : kOOB)), 0);
+      sring[d][b] = ld32(sr, settled(16u * lane + (in ? scale_off<MX>(blk, nch, c) : kOOB)));
     }
-    const bool in = ok && hrow != kOOB && (int)(c * kChunk) + 8 * l16 < F;
-    xring[d] = ld128(hr, in ? (hrow * (uint32_t)F + c * kChunk + 8u * l16) * 2u : kOOB, 0);
-    if (!MX) ering[d] = (int)(int8_t)__builtin_amdgcn_raw_buffer_load_b8(er, in ? hrow * (uint32_t)(F / 16) + c * 8u + l16 / 2u : kOOB, 0, 0);
+    const bool in = ok && (int)(c * kChunk) + 8 * l16 < F;
+    xring[d] = ld128(hr, settled(in ? hoff + c * 256u : kOOB), 0);
+    if (!MX) ering[d] = ld32(er, settled(in ? eoff + c * 8u : kOOB));
     --left_l;
     c_l += kW;
     if (c_l >= (int)nch) {
@@ -536,66 +789,94 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
     for (int d = 0; d < D; ++d) issue(d);
   }
 
-  f32x4 tot[RB];
+  // What each row is multiplied with: its weight, and for NVFP4 the largest of its blocks'
+  // exponents, to which its blocks are brought as they are read.
+  for (int r = tid; r < S; r += kNT) {
+    int top = kNoExp;
+    if (!MX) {
+      for (uint32_t c = 0; c < nch; ++c) {
+        const uint2 q = *reinterpret_cast<const uint2*>(p.hexp + (size_t)r * (nch * 8u) + c * 8u);
+        const int used = min(8, F / 16 - (int)c * 8);
 #pragma unroll
-  for (int b = 0; b < RB; ++b) tot[b] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < 8; ++j) {
+          const int e2 = (int)(int8_t)((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
+          top = j < used ? max(top, e2) : top;
+        }
+      }
+      s_top[r] = (int8_t)top;
+    }
+    s_mul[r] = MX ? p.plan->weight[r] : ldexpf(p.plan->weight[r], top);
+  }
+  __syncthreads();
+
+  f32x4 tot[RB], acc[RB];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) tot[b] = acc[b] = (f32x4){0.f, 0.f, 0.f, 0.f};
   int a = wave / (int)nch, c = wave - a * (int)nch;
   bool has = false;     // the lane's token is one of the item's
-  int fr = 0;           // and its place among them
-  float mul = 0.0f;     // the weight (times the global scale) of the row of this lane's group
+  uint32_t frow = 0;    // the bytes of its row in the wave's LDS
+  float mul = 0.0f;     // and what its products are multiplied with
+  int top = 0;          // the exponent of the row that the lane reads (its 16-lane group's)
   auto take_item = [&](int i) {
     const uint32_t w = (uint32_t)__builtin_amdgcn_readfirstlane((int)s_item[i]);
+    const uint32_t r0 = s_row0[i];
     has = (w >> l16) & 1u;
-    fr = __popc(w & ((1u << l16) - 1u)) & (kItemTok - 1);
-    mul = g < __popc(w & 0xffffu) ? s_w[s_row0[i] + g] : 0.0f;
+    const uint32_t fr = (uint32_t)__popc(w & ((1u << l16) - 1u)) & (kItemTok - 1);
+    frow = settled(fr * kRowBytes + 64u * g);
+    mul = has ? s_mul[r0 + fr] : 0.0f;
+    if (!MX) top = g < __popc(w & 0xffffu) ? s_top[r0 + g] : 0;
+  };
+  // The item's sums into the token's: only the item's own tokens, the other columns hold
+  // products that mean nothing.
+  auto fold = [&]() {
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tot[b][i] = has ? fmaf(acc[b][i], mul, tot[b][i]) : tot[b][i];
+      acc[b] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    }
   };
   if (nst > 0) take_item(a);
   unsigned char* row = s_row[wave];
   for (int s = 0; s < nst; s += D) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      if (s + d < nst) {
-        if (MX) {
-          *reinterpret_cast<u32x4*>(row + g * kRowBytes + 16 * l16) = xring[d];
-          if (l16 == 0) s_mul[wave][g] = mul;
-        } else {
-          // the chunk's blocks of 16 columns to one power of two
-          const int e2 = c * kChunk + 8 * l16 < F ? ering[d] : kNoExp;
-          const int top = (int)row16_max((uint32_t)(e2 + 256)) - 256;
-          const f16 f = (f16)ldexpf(1.0f, e2 - top);
-          const f16x8 v = __builtin_bit_cast(f16x8, xring[d]) * f;
-          *reinterpret_cast<f16x8*>(row + g * kRowBytes + 16 * l16) = v;
-          if (l16 == 0) s_mul[wave][g] = ldexpf(mul, top);
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        Op bf[4];
+      // Steps past the last pair have loaded zeros and add nothing.
+      const uint32_t cc = (uint32_t)c;
+      if (MX) {
+        *reinterpret_cast<u32x4*>(row + g * kRowBytes + 16 * l16) = xring[d];
+      } else {
+        const int e2 = (int)(int8_t)(ering[d] >> (4u * (l16 & 6)));
+        const f16 f = (f16)ldexpf(1.0f, min(e2 - top, 0));   // (no exponent past the row's columns)
+        *reinterpret_cast<f16x8*>(row + g * kRowBytes + 16 * l16) = __builtin_bit_cast(f16x8, xring[d]) * f;
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      Op bf[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) bf[j] = *reinterpret_cast<const Op*>(row + fr * kRowBytes + 64 * g + 16 * j);
-        const float m = s_mul[wave][fr];
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      for (int j = 0; j < 4; ++j) bf[j] = *reinterpret_cast<const Op*>(row + frow + 16 * j);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-        for (int b = 0; b < RB; ++b) {
-          Op wf[4];
-          Dec::run(wring[d][b], sring[d][b], wf);
-          f32x4 acc = (f32x4){0.f, 0.f, 0.f, 0.f};
+      for (int b = 0; b < RB; ++b) {
+        Op wf[4];
+        Dec::run(wring[d][b], scale_of<MX>(sring[d][b], cc), wf);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc = Dec::mfma(wf[j], bf[j], acc);
-          // only the item's own tokens: the other columns hold products that mean nothing
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tot[b][i] = has ? fmaf(acc[i], m, tot[b][i]) : tot[b][i];
-        }
-        c += kW;
-        if (c >= (int)nch) {
-          do {
-            c -= (int)nch;
-            ++a;
-          } while (c >= (int)nch);
-          if (s + d + 1 < nst) take_item(a);
+        for (int j = 0; j < 4; ++j) acc[b] = Dec::mfma(wf[j], bf[j], acc[b]);
+      }
+      c += kW;
+      if (c >= (int)nch) {
+        do {
+          c -= (int)nch;
+          ++a;
+        } while (c >= (int)nch);
+        if (s + d + 1 < nst) {   // (else the last item stays)
+          fold();
+          take_item(a);
         }
       }
       issue(d);
     }
   }
+  fold();
 
 #pragma unroll
   for (int b = 0; b < RB; ++b) *reinterpret_cast<f32x4*>(&s_red[wave * RB + b][l16 * 16 + 4 * g]) = tot[b];
@@ -607,29 +888,55 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
     float v = 0.0f;
 #pragma unroll
     for (int w = 0; w < kW; ++w) v += s_red[w * RB + b][t * 16 + r16];
-    static_cast<uint16_t*>(p.out)[(size_t)t * p.ld_out + blk * 16 + r16] = (uint16_t)f32_to_bf16(v);
+    static_cast<__bf16*>(p.out)[(size_t)t * p.ld_out + blk * 16 + r16] = (__bf16)v;
   }
 }
 
-// Groups of chunks a wave of the workgroup takes its turn in: 8 when every wave then has a chunk.
+// Chunks dealt out at a time: 8 when every wave then has one, else fewer, so that the waves
+// left over take row blocks of their own.
 int ks_log_for(int K) {
-  const int nch = (K + kChunk - 1) / kChunk;
+  const int nch = nch_of(K);
   return nch >= 8 ? 3 : nch >= 4 ? 2 : nch >= 2 ? 1 : 0;
 }
 
-template <bool MX, bool SWIGLU, int R, int RB, int D>
+// LDS for resident rows: what two workgroups a CU leave of its 160 KB.
+constexpr int kResidentBytes = 64 * 1024;
+int row_lds_bytes(int K) { return nch_of(K) * 256 + 16; }
+// Rows of K columns that fit.
+int resident_rows(int K) { return kResidentBytes / (nch_of(K) * 256); }
+
+template <bool MX, bool LAYER, bool FP8, bool SWIGLU, int NTOK, int RB, int D>
+hipError_t launch_up(const FewArgs& a, int rows, int grid, hipStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  auto* kernel = few_up_kernel<MX, LAYER, FP8, SWIGLU, NTOK, RB, D>;
+  const hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(kernel), kResidentBytes + 16 * 16, done);
+  if (e != hipSuccess) return e;
+  kernel<<<grid, kNT, rows * row_lds_bytes(a.K), stream>>>(a);
+  return hipGetLastError();
+}
+
+template <bool MX, bool SWIGLU, int NTOK, int RB, int D>
 hipError_t launch_mv(const FewArgs& a, hipStream_t stream) {
   const int nblk = a.Nw / 16, rg = kW >> a.ks_log;
   const int nsub = SWIGLU ? nblk / 2 : (nblk + RB - 1) / RB;
   const int tiles = (nsub + rg - 1) / rg;
-  few_up_kernel<MX, false, SWIGLU, R, RB, D><<<tiles < kGrid ? tiles : kGrid, kNT, 0, stream>>>(a);
+  return launch_up<MX, false, false, SWIGLU, NTOK, RB, D>(a, a.T, tiles < kGrid ? tiles : kGrid, stream);
+}
+
+template <bool MX, bool SWIGLU, int RB, int D, int WPS>
+hipError_t launch_long(const FewArgs& a, hipStream_t stream) {
+  const int hb = SWIGLU ? RB / 2 : RB;
+  const int tiles = ((SWIGLU ? a.Nw / 32 : a.Nw / 16) + hb - 1) / hb, most = 128 * WPS / 2 * 2;
+  few_long_kernel<MX, SWIGLU, RB, D, WPS><<<tiles < most ? tiles : most, kNT, 0, stream>>>(a);
   return hipGetLastError();
 }
 
 template <bool MX, bool SWIGLU>
 hipError_t launch_mv_rows(const FewArgs& a, hipStream_t stream) {
-  if (a.T <= 4) return launch_mv<MX, SWIGLU, 1, 2, 4>(a, stream);
-  return launch_mv<MX, SWIGLU, 4, 2, 2>(a, stream);
+  if (a.T <= resident_rows(a.K))
+    return a.T <= 4 ? launch_mv<MX, SWIGLU, 4, 2, 4>(a, stream) : launch_mv<MX, SWIGLU, 16, 2, 4>(a, stream);
+  if (a.Nw / 16 >= 8 * 256) return launch_long<MX, SWIGLU, 8, 1, 2>(a, stream);
+  return launch_long<MX, SWIGLU, 2, 2, 4>(a, stream);
 }
 
 }  // namespace
@@ -642,14 +949,15 @@ hipError_t launch_few_matvec(FewArgs a, bool mx, bool swiglu, hipStream_t stream
 
 hipError_t launch_few_layer(FewArgs up, FewArgs down, bool mx, hipStream_t stream) {
   up.ks_log = ks_log_for(up.K);
+  const int fit = resident_rows(up.K);   // >= 1 by the limit on H
+  up.item_tok = fit < kItemTok ? fit : kItemTok;
   const int rg = kW >> up.ks_log, nsub = up.Nw / 32;
   const int64_t tiles = (int64_t)up.T * up.k * ((nsub + rg - 1) / rg);   // bound: every slot an item
   const int grid = tiles < kGrid ? (int)tiles : kGrid;
-  if (mx)
-    few_up_kernel<true, true, true, 1, 2, 4><<<grid, kNT, 0, stream>>>(up);
-  else
-    few_up_kernel<false, true, true, 1, 2, 4><<<grid, kNT, 0, stream>>>(up);
-  const hipError_t e = hipGetLastError();
+  const int rows = up.T < up.item_tok ? up.T : up.item_tok;
+  const hipError_t e = mx       ? launch_up<true, true, false, true, kItemTok, 2, 4>(up, rows, grid, stream)
+                       : up.fp8 ? launch_up<false, true, true, true, kItemTok, 2, 4>(up, rows, grid, stream)
+                                : launch_up<false, true, false, true, kItemTok, 2, 4>(up, rows, grid, stream);
   if (e != hipSuccess) return e;
   constexpr int RB = 1;
   const int wgs = (down.Nw / 16 + RB - 1) / RB;

@@ -154,6 +154,7 @@ hipError_t launch_zero_f32(float* p, int n, hipStream_t stream);
 // ---- few_rows.hip: up to kFewMaxTokens rows
 constexpr int kFewMaxTokens = 16;
 constexpr int kFewMaxSlots = kFewMaxTokens * kMaxTopK;
+constexpr int kFewMaxHidden = 32768;   // H of the layer: at least one row stays in LDS
 // What the layer's first launch leaves for its second: the items (expert << 16 | mask of its
 // tokens) with the first of their rows in h, and for every row of h its routing weight (NVFP4:
 // times the global scale of the expert's second matrix).
@@ -171,7 +172,7 @@ struct FewArgs {
   const uint8_t* scales;
   const float* g;         // their global scales (NVFP4)
   int Nw;
-  int ks_log;             // set by the launcher
+  int ks_log, item_tok;   // set by the launcher
   const void* add;        // matvec: float32 or bf16 [T, n], rows ld_add apart, or null
   int add_bf16;
   int64_t ld_add;
@@ -184,7 +185,7 @@ struct FewArgs {
   int fp8;                // layer, NVFP4: the rows first take the FP8 E4M3 round trip
   FewPlan* plan;          // layer workspace
   void* h;                // [T * k, F] f16 (NVFP4) or bf16 (MXFP4)
-  int8_t* hexp;           // NVFP4: [T * k, F / 16] exponents of h's blocks of 16 columns
+  int8_t* hexp;           // NVFP4: [T * k, 8 ceil(F / 128)] exponents of h's blocks of 16 columns
 };
 hipError_t launch_few_matvec(FewArgs a, bool mx, bool swiglu, hipStream_t stream);
 hipError_t launch_few_layer(FewArgs up, FewArgs down, bool mx, hipStream_t stream);

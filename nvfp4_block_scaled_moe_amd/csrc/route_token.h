@@ -44,6 +44,7 @@ __device__ __forceinline__ void route_token_thresh(const float* __restrict__ row
 #pragma unroll
     for (int i = 0; i < PL; ++i) cnt += wave_count(key[i] >= cand);
     if (cnt >= k) th = cand;
+    if (cnt == k) break;   // exactly the kept ones lie at or above th
   }
   int need = k;
 #pragma unroll
