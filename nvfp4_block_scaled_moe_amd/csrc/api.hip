@@ -964,16 +964,18 @@ bool few_layer_sizes_ok(int32_t T, int32_t E, int32_t k, int32_t H, int32_t F) {
          H % 32 == 0 && H <= kFewMaxHidden && F >= 32 && F % 32 == 0 && (int64_t)T * k * F * 2 < (int64_t(1) << 31);
 }
 
-// Workspace: the item list, h, and (NVFP4) the exponents of its blocks of 16 columns.
+// Workspace: the item list, h, (NVFP4) the exponents of its blocks of 16 columns, and the parts
+// of the tiles that workgroups of the second launch share.
 struct FewLayerWs {
-  size_t plan, h, hexp, total;
+  size_t plan, h, hexp, part, total;
 };
-FewLayerWs few_layer_ws(int32_t T, int32_t k, int32_t F, bool mx) {
+FewLayerWs few_layer_ws(int32_t T, int32_t k, int32_t H, int32_t F, bool mx) {
   FewLayerWs w{};
   w.plan = round_up(sizeof(FewPlan));
   w.h = round_up((size_t)T * k * F * 2);
   w.hexp = mx ? 0 : round_up((size_t)T * k * ((F + 127) / 128) * 8);
-  w.total = w.plan + w.h + w.hexp;
+  w.part = round_up((size_t)few_down_parts(T, k, H, F) * T * H * 4);
+  w.total = w.plan + w.h + w.hexp + w.part;
   return w;
 }
 
@@ -995,7 +997,7 @@ nvfp4moe_status few_layer(const char* fn, bool mx, const float* logits, const vo
   if (chk != NVFP4MOE_OK) return chk;
   if (!aligned(x, 16) || !aligned(logits, 4) || !aligned(out, 2) || !aligned(w13_g, 4) || !aligned(w2_g, 4))
     return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: x must be 16-byte aligned, the others aligned to their elements", fn);
-  const FewLayerWs lay = few_layer_ws(T, k, F, mx);
+  const FewLayerWs lay = few_layer_ws(T, k, H, F, mx);
   if (!ws || ws_bytes < lay.total)
     return fail(NVFP4MOE_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, lay.total, ws_bytes);
   if (!aligned(ws, 16)) return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
@@ -1017,6 +1019,9 @@ nvfp4moe_status few_layer(const char* fn, bool mx, const float* logits, const vo
   up.plan = reinterpret_cast<FewPlan*>(base);
   up.h = base + lay.plan;
   up.hexp = mx ? nullptr : reinterpret_cast<int8_t*>(base + lay.plan + lay.h);
+  up.down_tiles = H / (16 * kFewDownBlocks);
+  up.part = reinterpret_cast<float*>(base + lay.plan + lay.h + lay.hexp);
+  up.most_parts = few_down_parts(T, k, H, F);
   FewArgs down = up;
   down.K = F;
   down.codes = w2_codes;
@@ -1049,11 +1054,11 @@ nvfp4moe_status mxfp4_matvec(nvfp4moe_epilogue epi, const void* x, int64_t ldx, 
 }
 
 size_t moe_layer_few_nvfp4_workspace_size(int32_t T, int32_t E, int32_t k, int32_t H, int32_t F) {
-  return few_layer_sizes_ok(T, E, k, H, F) ? few_layer_ws(T, k, F, false).total : 0;
+  return few_layer_sizes_ok(T, E, k, H, F) ? few_layer_ws(T, k, H, F, false).total : 0;
 }
 
 size_t moe_layer_few_mxfp4_workspace_size(int32_t T, int32_t E, int32_t k, int32_t H, int32_t F) {
-  return few_layer_sizes_ok(T, E, k, H, F) ? few_layer_ws(T, k, F, true).total : 0;
+  return few_layer_sizes_ok(T, E, k, H, F) ? few_layer_ws(T, k, H, F, true).total : 0;
 }
 
 nvfp4moe_status moe_layer_few_nvfp4(const float* logits, const void* x, int32_t T, int32_t E, int32_t k, int32_t H,

@@ -27,7 +27,7 @@
 //     power back when it is added to the float32 sum. MXFP4 weights are decoded exactly to
 //     bf16 (whose exponent holds every E8M0 scale), so bf16 rows are used as they are.
 //   * The layer's first launch routes in every workgroup (a wave per token; a few microseconds
-//     that replace a launch), the second reads the list that workgroup 0 left. An item is an
+//     that replace a launch), the second reads the list that one of them left. An item is an
 //     expert with up to 4 of its tokens; an expert with more tokens takes several items.
 //   * h between the launches: f16 with a power of two for each 16 columns (NVFP4), bf16 (MXFP4,
 //     as its matrix operand needs; the same rounding as h of the W4A16 layer).
@@ -48,10 +48,13 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kW = 8;                    // waves per workgroup
+constexpr int kW = 16;                   // waves per workgroup: a CU's worth at 128 registers
 constexpr int kNT = kW * kWave;
-constexpr int kGrid = 512;               // persistent workgroups: 2 on each of the 256 CUs
+constexpr int kGrid = 256;               // persistent workgroups: one on each of the 256 CUs
+constexpr int kLongW = 8;                // waves per workgroup of few_long_kernel
+constexpr int kLongNT = kLongW * kWave;
 constexpr int kRowBytes = 256 + 16;      // LDS bytes of one row's chunk (padded: conflict-free reads)
+constexpr int kDownLeast = 128;          // pairs of the second launch that are worth a workgroup
 constexpr int kItemTok = 4;              // tokens of one item of the layer
 template <bool B>
 struct Flag {
@@ -169,14 +172,15 @@ __device__ __forceinline__ f16x8 chunk_to_f16(const u32x4& v, float& unscale) {
 __device__ __forceinline__ uint32_t row_exponent(uint32_t top) { return max(top >> 7, 15u); }
 __device__ __forceinline__ float row_scale(uint32_t top) { return __uint_as_float((268u - row_exponent(top)) << 23); }
 __device__ __forceinline__ float row_unscale(uint32_t top) { return __uint_as_float((row_exponent(top) - 14u) << 23); }
-// Largest finite magnitude of eight bf16 values, as bf16 bits.
-__device__ __forceinline__ uint32_t finite_top(const u32x4& v) {
+// Largest magnitude below `end` of eight bf16 values, as bf16 bits (0x7f80: of the finite ones,
+// 0x7f81: Inf counts).
+__device__ __forceinline__ uint32_t top_of(const u32x4& v, uint32_t end) {
   uint32_t t = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t lo = v[i] & 0x7fffu, hi = (v[i] >> 16) & 0x7fffu;
-    t = max(t, lo < 0x7f80u ? lo : 0u);
-    t = max(t, hi < 0x7f80u ? hi : 0u);
+    t = max(t, lo < end ? lo : 0u);
+    t = max(t, hi < end ? hi : 0u);
   }
   return t;
 }
@@ -188,6 +192,22 @@ __device__ __forceinline__ f16x8 scaled_f16(const u32x4& v, float scale) {
     o[2 * i + 1] = (f16)(__uint_as_float(v[i] & 0xffff0000u) * scale);
   }
   return o;
+}
+
+// fp8_roundtrip_bits of two bf16 values (packed low, high), as packed bf16: the quotient v / s
+// as (float)((double)v * inv) with inv the double nearest 1 / s. That rounds correctly: the
+// product is within 2^-52 of v / s, and v / s, with v of 8 and s of 24 significant bits, is never
+// within 2^-49 of the middle of two floats. Infinite values go to the largest code; NaN stays.
+__device__ __forceinline__ uint32_t fp8_pair(uint32_t w, float s, double inv) {
+  float q[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float v = __uint_as_float(i ? w & 0xffff0000u : w << 16);
+    const float r = (float)((double)v * inv);
+    q[i] = v != v ? v : fminf(fmaxf(r, -448.0f), 448.0f);
+  }
+  const f32x2 f = __builtin_amdgcn_cvt_pk_f32_fp8(__builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false), false);
+  return bf16x2(f[0] * s, f[1] * s);
 }
 
 // First column block of wave group rg's b-th row block in a tile: gate blocks, then their up blocks.
@@ -217,9 +237,9 @@ __device__ __forceinline__ void put_matvec(const FewArgs& p, int col, size_t n0,
 // ------------------------------------------------------------------ resident rows: matvec, and the layer's first launch
 // The rows (the item's, or all of them once when they fit) stay in LDS as matrix operands, f16
 // with one power of two a row (NVFP4) or bf16 (MXFP4): turned once, they serve every tile of
-// the item. Waves deal out the chunks ks at a time (ks = 1, 2, 4 or 8: kW / ks groups of
-// waves, each with RB row blocks of its own, when K has fewer than 8 chunks).
-constexpr int kPassBatch = 4;   // pieces a thread requests together
+// the item. Waves deal out the chunks ks at a time (ks = 1 .. 16: kW / ks groups of
+// waves, each with RB row blocks of its own).
+constexpr int pass_batch(bool fp8) { return fp8 ? 2 : 4; }   // pieces a thread requests together
 
 template <bool MX, bool LAYER, bool FP8, bool SWIGLU, int NTOK, int RB, int D>
 __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
@@ -229,6 +249,7 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
   static_assert(!LAYER || (SWIGLU && NTOK == kItemTok), "the layer's items");
   static_assert(!FP8 || (LAYER && !MX), "FP8 activations: the NVFP4 layer");
   constexpr int BUF = NTOK > 4 ? 1 : 2;
+  constexpr int kPassBatch = pass_batch(FP8);
   constexpr int REDF = kW * RB * NTOK * 16;
   extern __shared__ __attribute__((aligned(16))) unsigned char s_rows[];   // [rows][K128 * 2 + 16]
   __shared__ __attribute__((aligned(16))) float s_red[BUF][REDF];
@@ -238,7 +259,6 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
   __shared__ uint32_t s_first[LAYER ? kMaxExperts : 1];     // token mask, then item << 16 | row
   __shared__ int s_ids[LAYER ? kFewMaxSlots : 1];
   __shared__ float s_w[LAYER ? kFewMaxSlots : 1];
-  __shared__ float s_amax[kW];
   __shared__ uint32_t s_n;
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -256,209 +276,271 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
   const uint32_t wbytes = nblk * nch * 1024u;
   const uint32_t sbytes = nblk * (MX ? (nch + 15) >> 4 : (nch + 7) >> 3) * 1024u;
   const bool all_rows = !LAYER || T <= p.item_tok;       // every row fits: staged once
-  float fp8_s = 1.0f;
 
-  // ---- rows (all_rows: every row, else those of mask) into LDS, in two passes over them by any
-  // number nt of threads: their largest magnitudes (NVFP4), then, after a barrier, the operands.
-  // The second pass reads the rows again, from the caches: kept in registers between the passes
-  // they would cost the ring its depth.
+  // ---- rows (all_rows: every row, else those of mask) into LDS, by nt threads (this one the
+  // first-th), in batches of kPassBatch pieces a thread: their largest magnitudes (find_tops),
+  // then, after a barrier, the operands (put_rows). A second reading, from the caches, is needed
+  // only for rows of more than one batch.
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(p.x, (uint32_t)((p.ldx * (T - 1) + K) * 2));
   const uint32_t ppr = nch * 16u;   // 16-byte pieces of a row
-  auto pass = [&](auto put_c, uint32_t mask, int first, int nt) {
-    constexpr bool PUT = decltype(put_c)::value;
-    const int nrow = all_rows ? T : __popc(mask);
-    const uint32_t total = (uint32_t)nrow * ppr;
-    for (uint32_t i0 = (uint32_t)first; i0 < total; i0 += kPassBatch * nt) {
-      u32x4 v[kPassBatch];
-      uint32_t row[kPassBatch], q[kPassBatch];
+  auto row_at = [&](uint32_t piece) { return __umulhi(piece, p.ppr_inv); };   // piece / ppr (host: ppr_inverse)
+  u32x4 pv[kPassBatch];
+  auto load_batch = [&](uint32_t mask, uint32_t total, uint32_t i0, uint32_t nt) {
+#pragma unroll
+    for (int i = 0; i < kPassBatch; ++i) {
+      const uint32_t idx = i0 + i * nt, r = row_at(idx), q = idx - r * ppr;
+      uint32_t tok = r;
+      if (LAYER && !all_rows) {
+        uint32_t m = mask;
+#pragma unroll
+        for (uint32_t j = 0; j < (uint32_t)kItemTok - 1; ++j) m = j < r ? m & (m - 1) : m;
+        tok = (uint32_t)__ffs(m) - 1u;
+      }
+      const bool in = idx < total && 8u * q < (uint32_t)K;
+      pv[i] = ld128(xr, settled(in ? tok * (uint32_t)p.ldx * 2u + 16u * q : kOOB), 0);
+    }
+  };
+  uint32_t amax = 0;   // FP8: the largest finite magnitude that this thread has seen
+  auto find_tops = [&](uint32_t mask, uint32_t total, uint32_t first, uint32_t nt) {
+    for (uint32_t i0 = first; i0 < total; i0 += kPassBatch * nt) {
+      load_batch(mask, total, i0, nt);
 #pragma unroll
       for (int i = 0; i < kPassBatch; ++i) {
         const uint32_t idx = i0 + i * nt;
-        row[i] = idx / ppr;
-        q[i] = idx - row[i] * ppr;
-        uint32_t tok = row[i];
-        if (LAYER && !all_rows) {
-          uint32_t m = mask;
-#pragma unroll
-          for (uint32_t j = 0; j < (uint32_t)kItemTok - 1; ++j) m = j < row[i] ? m & (m - 1) : m;
-          tok = (uint32_t)__ffs(m) - 1u;
-        }
-        const bool in = idx < total && 8u * q[i] < (uint32_t)K;
-        v[i] = ld128(xr, settled(in ? tok * (uint32_t)p.ldx * 2u + 16u * q[i] : kOOB), 0);
+        const uint32_t top = row16_max(top_of(pv[i], FP8 ? 0x7f81u : 0x7f80u));   // (a row's pieces come in sixteens)
+        if (l16 == 0 && idx < total) atomicMax(&s_top[row_at(idx)], top);
+        if (FP8) amax = max(amax, top_of(pv[i], 0x7f80u));
       }
+    }
+  };
+  float fp8_s = 1.0f;
+  double fp8_inv = 1.0;
+  // FP8: the first n rows' largest magnitudes as they are after the round trip (which keeps the order).
+  auto fp8_tops = [&](int n) {
+    if (FP8) {
+      if (tid < n) s_top[tid] = fp8_pair(s_top[tid], fp8_s, fp8_inv) & 0x7fffu;
+      __syncthreads();
+    }
+  };
+  auto put_batch = [&](uint32_t total, uint32_t i0, uint32_t nt) {
 #pragma unroll
-      for (int i = 0; i < kPassBatch; ++i) {
-        const bool in = i0 + i * nt < total;
-        if (FP8) {
+    for (int i = 0; i < kPassBatch; ++i) {
+      const uint32_t idx = i0 + i * nt, r = row_at(idx);
+      if (idx < total) {
+        unsigned char* at = s_rows + r * stride + 16u * (idx - r * ppr);
+        if (MX) {
+          *reinterpret_cast<u32x4*>(at) = pv[i];
+        } else {
+          u32x4 v = pv[i];
+          if (FP8) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            v[i][j] = fp8_roundtrip_bits(bf16_to_f32(v[i][j] & 0xffffu), fp8_s) |
-                      fp8_roundtrip_bits(__uint_as_float(v[i][j] & 0xffff0000u), fp8_s) << 16;
-        }
-        if (!PUT) {
-          const uint32_t top = row16_max(finite_top(v[i]));   // (a row's pieces come in whole sixteens)
-          if (l16 == 0 && in) atomicMax(&s_top[row[i]], top);
-        } else if (in) {
-          unsigned char* at = s_rows + row[i] * stride + 16u * q[i];
-          if (MX)
-            *reinterpret_cast<u32x4*>(at) = v[i];
-          else
-            *reinterpret_cast<f16x8*>(at) = scaled_f16(v[i], row_scale(s_top[row[i]]));
+            for (int j = 0; j < 4; ++j) v[j] = fp8_pair(v[j], fp8_s, fp8_inv);
+          }
+          *reinterpret_cast<f16x8*>(at) = scaled_f16(v, row_scale(s_top[r]));
         }
       }
     }
-    // Every load has arrived (they are newer than any of the ring's): without the wait here the
-    // compiler would place it in the main loop, for the lanes that used none of theirs.
-    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
   };
-  const Flag<false> find_top;
-  const Flag<true> put;
+  auto put_rows = [&](uint32_t mask, uint32_t total, uint32_t first, uint32_t nt) {
+    if (total <= kPassBatch * nt) {   // find_tops (MXFP4: load_batch) has left them in registers
+      put_batch(total, first, nt);
+    } else {
+      for (uint32_t i0 = first; i0 < total; i0 += kPassBatch * nt) {
+        load_batch(mask, total, i0, nt);
+        put_batch(total, i0, nt);
+      }
+      // Every load has arrived: without the wait here the compiler would place it in the main
+      // loop, for the lanes that used none of theirs.
+      __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+    }
+  };
 
   int nitems = 1;
+  const uint32_t all = all_rows ? (uint32_t)T * ppr : 0u;   // pieces staged once
+  // The threads that stage them: in the layer those of the waves that route no token (all of
+  // them when every wave does).
+  const uint32_t st0 = LAYER && T < kW ? (uint32_t)T * kWave : 0u;
+  const uint32_t stn = (uint32_t)kNT - st0;
   if (tid < NTOK) s_top[tid] = 0;
   if constexpr (LAYER) {
-    // ---- routing: a wave per token, then the list of items in ascending expert order
+    // ---- routing: a wave per token
     static_assert(BUF * REDF >= kW * 3 * kWave, "the routing scratch fits");
+    static_assert(kFewMaxTokens <= kW, "a wave per token");
     const int E = p.E, k = p.k, S = T * k;
-    uint32_t* scratch = reinterpret_cast<uint32_t*>(&s_red[0][0]) + wave * 3 * kWave;
     for (int e = tid; e < E; e += kNT) s_first[e] = 0;
-    __syncthreads();   // s_top and s_first are cleared
-    for (int t = wave; t < T; t += kW) {
-      const float* row = p.logits + (size_t)t * E;
+    if (tid == 0) s_n = 0;
+    __syncthreads();
+    if (wave < T) {
+      const float* row = p.logits + (size_t)wave * E;
+      uint32_t* scratch = reinterpret_cast<uint32_t*>(&s_red[0][0]) + wave * 3 * kWave;
       if (E <= 256)
-        route_token_thresh<4>(row, E, k, lane, s_ids + t * k, s_w + t * k, nullptr, scratch);
+        route_token_thresh<4>(row, E, k, lane, s_ids + wave * k, s_w + wave * k, nullptr, scratch);
       else if (E <= 512)
-        route_token_thresh<8>(row, E, k, lane, s_ids + t * k, s_w + t * k, nullptr, scratch);
+        route_token_thresh<8>(row, E, k, lane, s_ids + wave * k, s_w + wave * k, nullptr, scratch);
       else
-        route_token_thresh<16>(row, E, k, lane, s_ids + t * k, s_w + t * k, nullptr, scratch);
+        route_token_thresh<16>(row, E, k, lane, s_ids + wave * k, s_w + wave * k, nullptr, scratch);
     }
-    // (at most kItemTok tokens when all rows fit: the other waves look at the rows meanwhile)
-    if (!MX && !FP8 && all_rows && wave >= kItemTok) pass(find_top, 0, tid - kItemTok * kWave, kNT - kItemTok * kWave);
-    float amax = 0.0f;
-    if (FP8) {   // one scale for all the rows, from the largest finite magnitude
-      const int per = K / 8;
-      for (int i = tid; i < T * per; i += kNT) {
-        const int t = i / per;
-        const uint4 q = *reinterpret_cast<const uint4*>(p.x + (size_t)t * p.ldx + 8 * (i - t * per));
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-        amax = bf16x8_finite_max(w, amax);
+    if (MX && all && (uint32_t)tid >= st0) load_batch(0, all, (uint32_t)tid - st0, stn);
+    if (!MX && (uint32_t)tid >= st0) {
+      if (all) find_tops(0, all, (uint32_t)tid - st0, stn);
+      if (FP8 && !all_rows) {   // the scale is taken over every row
+        const uint32_t total = (uint32_t)T * ppr;
+        for (uint32_t i = (uint32_t)tid - st0; i < total; i += stn) {
+          const uint32_t t = row_at(i), q = i - t * ppr;
+          const u32x4 v = ld128(xr, settled(8u * q < (uint32_t)K ? t * (uint32_t)p.ldx * 2u + 16u * q : kOOB), 0);
+          amax = max(amax, top_of(v, 0x7f80u));
+        }
       }
-      amax = wave_max(amax);
-      if (lane == 0) s_amax[wave] = amax;
+      if (FP8) {
+        amax = row16_max(amax);
+        if (l16 == 0) atomicMax(&s_n, amax);
+      }
     }
     __syncthreads();
     if (FP8) {
-      for (int w = 0; w < kW; ++w) amax = fmaxf(amax, s_amax[w]);
-      fp8_s = fp8_scale(amax);
+      fp8_s = fp8_scale(bf16_to_f32(s_n));
+      fp8_inv = 1.0 / (double)fp8_s;
+      if (all_rows) fp8_tops(T);
     }
-    for (int s = tid; s < S; s += kNT) atomicOr(&s_first[s_ids[s]], 1u << (s / k));
-    __syncthreads();
-    if (FP8 && all_rows && wave > 0) pass(find_top, 0, tid - kWave, kNT - kWave);
-    if (!FP8 && all_rows && wave > 0) pass(put, 0, tid - kWave, kNT - kWave);
-    if (wave == 0) {
-      const int per = (E + kWave - 1) / kWave;
-      const uint32_t cap = (uint32_t)p.item_tok;
-      uint32_t cnt = 0;   // items << 16 | rows of this lane's experts
-      for (int i = 0; i < per; ++i) {
-        const int e = lane * per + i;
-        const uint32_t n = e < E ? (uint32_t)__popc(s_first[e]) : 0u;
-        cnt += ((n + cap - 1) / cap) << 16 | n;
+    if (T == 1) {   // an item for each kept expert
+      if (tid < k) {
+        s_item[tid] = (uint32_t)s_ids[tid] << 16 | 1u;
+        s_row0[tid] = (uint16_t)tid;
       }
-      uint32_t incl = cnt;
-#pragma unroll
-      for (int o = 1; o < kWave; o <<= 1) {
-        const uint32_t up = __shfl_up(incl, o, kWave);
-        if (lane >= o) incl += up;
-      }
-      uint32_t at = incl - cnt;
-      for (int i = 0; i < per; ++i) {
-        const int e = lane * per + i;
-        if (e >= E) break;
-        uint32_t m = s_first[e];
-        s_first[e] = at;
-        while (m) {
-          uint32_t rest = m;   // m without its lowest `cap` tokens
-          for (uint32_t j = 0; j < cap; ++j) rest &= rest - 1;
-          const uint32_t part = m & ~rest;
-          s_item[at >> 16] = (uint32_t)e << 16 | part;
-          s_row0[at >> 16] = (uint16_t)(at & 0xffffu);
-          at += 0x10000u + (uint32_t)__popc(part);
-          m = rest;
+      nitems = k;
+    } else {
+      // ---- the items in ascending expert order
+      for (int s = tid; s < S; s += kNT) atomicOr(&s_first[s_ids[s]], 1u << (s / k));
+      __syncthreads();
+      if (wave == 0) {
+        const int per = (E + kWave - 1) / kWave;
+        const uint32_t cap = (uint32_t)p.item_tok;
+        uint32_t cnt = 0;   // items << 16 | rows of this lane's experts
+        for (int i = 0; i < per; ++i) {
+          const int e = lane * per + i;
+          const uint32_t n = e < E ? (uint32_t)__popc(s_first[e]) : 0u;
+          cnt += ((n + cap - 1) / cap) << 16 | n;
         }
+        uint32_t incl = cnt;
+#pragma unroll
+        for (int o = 1; o < kWave; o <<= 1) {
+          const uint32_t up = __shfl_up(incl, o, kWave);
+          if (lane >= o) incl += up;
+        }
+        uint32_t at = incl - cnt;
+        for (int i = 0; i < per; ++i) {
+          const int e = lane * per + i;
+          if (e >= E) break;
+          uint32_t m = s_first[e];
+          s_first[e] = at;
+          while (m) {
+            uint32_t rest = m;   // m without its lowest `cap` tokens
+            for (uint32_t j = 0; j < cap; ++j) rest &= rest - 1;
+            const uint32_t part = m & ~rest;
+            s_item[at >> 16] = (uint32_t)e << 16 | part;
+            s_row0[at >> 16] = (uint16_t)(at & 0xffffu);
+            at += 0x10000u + (uint32_t)__popc(part);
+            m = rest;
+          }
+        }
+        if (lane == kWave - 1) s_n = incl >> 16;
       }
-      if (lane == kWave - 1) s_n = incl >> 16;
     }
     __syncthreads();
-    nitems = __builtin_amdgcn_readfirstlane((int)s_n);
-    if (blockIdx.x == 0) {   // the list for the second launch
-      for (int i = tid; i < nitems; i += kNT) p.plan->item[i] = s_item[i];
-      for (int i = tid; i < nitems; i += kNT) p.plan->row0[i] = s_row0[i];
-      if (tid == 0) p.plan->n_items = nitems;
-      for (int s = tid; s < S; s += kNT) {
-        const int t = s / k, e = s_ids[s];
-        const uint32_t before = (1u << t) - 1u;
-        int rank = 0;   // tokens before t with the same expert
-        for (int i = (int)(s_first[e] >> 16); i < nitems && (int)(s_item[i] >> 16) == e; ++i)
-          rank += __popc(s_item[i] & before);
-        p.plan->weight[(s_first[e] & 0xffffu) + rank] = MX ? s_w[s] : s_w[s] * p.g_down[e];
-      }
-    }
+    if (T > 1) nitems = __builtin_amdgcn_readfirstlane((int)s_n);
   }
 
-  // ---- this workgroup's tiles, in runs of one item's, each a flat sequence of steps (a chunk of
-  // RB weight tiles) padded to whole turns of the ring
+  auto write_plan = [&]() {   // the list for the second launch
+    const int k = p.k;
+    for (int i = tid; i < nitems; i += kNT) p.plan->item[i] = s_item[i];
+    for (int i = tid; i < nitems; i += kNT) p.plan->row0[i] = s_row0[i];
+    if (tid == 0) p.plan->n_items = nitems;
+    for (int i = tid; i < p.down_tiles; i += kNT) p.plan->arrived[i] = 0;
+    for (int s = tid; s < T * k; s += kNT) {
+      const int t = s / k, e = s_ids[s];
+      int at = s;   // T == 1: the rows in the kept order
+      if (T > 1) {
+        const uint32_t before = (1u << t) - 1u;   // tokens before t with the same expert
+        at = (int)(s_first[e] & 0xffffu);
+        for (int i = (int)(s_first[e] >> 16); i < nitems && (int)(s_item[i] >> 16) == e; ++i)
+          at += __popc(s_item[i] & before);
+      }
+      p.plan->weight[at] = MX ? s_w[s] : s_w[s] * p.g_down[e];
+    }
+  };
+
+  // ---- this workgroup's tiles, in runs of one item's: a flat sequence of steps (a chunk of RB
+  // weight tiles), D of them a turn of the ring. A tile takes at least D steps, so that at most
+  // one is completed in a turn; a run is padded to whole turns.
   const int64_t ntiles = (int64_t)nitems * tpi;
   const int t0 = (int)(ntiles * blockIdx.x / gridDim.x);
   const int t1 = (int)(ntiles * (blockIdx.x + 1) / gridDim.x);
-  if (t0 >= t1) return;
+  if (t0 >= t1) return;   // fewer tiles than workgroups
 
   __amdgpu_buffer_rsrc_t wr, sr;
   auto item_word = [&](int it) -> uint32_t {
     return LAYER ? (uint32_t)__builtin_amdgcn_readfirstlane((int)s_item[it]) : (1u << T) - 1u;
   };
-  u32x4 wring[D][RB];
-  uint32_t sring[D][RB];
-  // The loads' position: the item, its tile and the step in it, and what is left of the run.
-  int it_l = t0 / tpi, tile_l = t0 - it_l * tpi, step_l = 0, tiles_l = t1 - t0, run_l = 0, pad_l = 0;
-  auto open_run = [&]() {   // the tiles left in the loads' item
+  const int spt = cpw > D ? cpw : D;   // steps of a tile
+  // The loads' position: the item, its row block group and chunk, and the steps left of the run.
+  int it_l = t0 / tpi, tile_l = t0 - it_l * tpi, tiles_l = t1 - t0, sub_l = 0, step_l = 0, steps_l = 0;
+  auto open_run = [&]() {
     const size_t e = LAYER ? item_word(it_l) >> 16 : 0;
     wr = make_rsrc(p.codes + e * wbytes, wbytes);
     sr = make_rsrc(p.scales + e * sbytes, sbytes);
     const int n = min(tiles_l, tpi - tile_l);
     tiles_l -= n;
-    run_l = n * cpw;
-    pad_l = (run_l + D - 1) / D * D - run_l;
+    steps_l = n * spt;
+    sub_l = tile_l * RG + rg;
+    step_l = 0;
+    tile_l = 0;
+    ++it_l;
   };
-  open_run();
+  u32x4 wring[D][RB];
+  uint32_t sring[D][RB];
   auto issue = [&](int d) {
     const uint32_t c = (uint32_t)(ksl + (step_l << p.ks_log));
-    const uint32_t sub = (uint32_t)(tile_l * RG + rg);
-    const bool ok = run_l > 0 && c < nch && sub < (uint32_t)nsub;
+    const bool ok = steps_l > 0 && step_l < cpw && c < nch && sub_l < nsub;
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
-      const uint32_t blk = tile_block<SWIGLU, RB>(sub, b, nblk);
-      const bool in = ok && tile_block_in<SWIGLU, RB>(sub, b, nblk);
+      const uint32_t blk = tile_block<SWIGLU, RB>((uint32_t)sub_l, b, nblk);
+      const bool in = ok && (SWIGLU || blk < nblk);
       wring[d][b] = ld128(wr, settled(16u * lane + (in ? (blk * nch + c) * 1024u : kOOB)), 0);
       sring[d][b] = ld32(sr, settled(16u * lane + (in ? scale_off<MX>(blk, nch, c) : kOOB)));
     }
     // (arithmetic instead of branches: a branch here would send the position through memory)
-    const int real = run_l > 0 ? 1 : 0, wrap = real && step_l + 1 == cpw ? 1 : 0;
-    run_l -= real;
-    pad_l -= 1 - real;
-    step_l = wrap ? 0 : step_l + real;
-    tile_l += wrap;
-    if (run_l == 0 && pad_l == 0 && tiles_l > 0) {
-      tile_l = 0;
-      ++it_l;
-      open_run();
-    }
+    const int wrap = step_l + 1 == spt ? 1 : 0;
+    step_l = wrap ? 0 : step_l + 1;
+    sub_l += wrap * RG;
+    --steps_l;
   };
 
-  int it = it_l, tile = tile_l, step = 0, done = 0, buf = 0, left = t1 - t0;
-  if (!LAYER) __syncthreads();   // s_top is cleared
-  if (!MX && !LAYER) pass(find_top, 0, tid, kNT);
+  int it = it_l, tile = tile_l, left = t1 - t0, buf = 0, done = 0;
+  open_run();
+  if (!LAYER) {
+    if (MX) {
+      load_batch(0, all, (uint32_t)tid, stn);
+    } else {
+      __syncthreads();   // s_top is cleared
+      find_tops(0, all, (uint32_t)tid, stn);
+      __syncthreads();
+    }
+  }
+  // Fill the ring. (After each turn the next run is opened where this one's loads have ended.)
+  auto next_run = [&]() {
+    if (steps_l <= 0 && tiles_l > 0) open_run();
+  };
+  // (The rows first: a wave whose loads find no room waits for the others' to return.)
+  if (all) {
+    if ((uint32_t)tid >= st0) put_rows(0, all, (uint32_t)tid - st0, stn);
+    __syncthreads();
+  }
 #pragma unroll
   for (int d = 0; d < D; ++d) issue(d);
+  next_run();
+  if constexpr (LAYER) {
+    if (blockIdx.x == gridDim.x - 1) write_plan();   // (this workgroup always has a tile)
+  }
 
   f32x4 tot[RB];
 #pragma unroll
@@ -467,20 +549,20 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
     const uint32_t word = item_word(it);
     const int ncol = __popc(word & 0xffffu);
     if (LAYER && !all_rows) {
+      const uint32_t m = word & 0xffffu, total = (uint32_t)ncol * ppr;
       if (!first) {
         __syncthreads();   // the last epilogue has read the last item's rows
         if (tid < NTOK) s_top[tid] = 0;
         __syncthreads();
       }
-      if (!MX) {
-        pass(find_top, word & 0xffffu, tid, kNT);
+      if (MX) {
+        load_batch(m, total, (uint32_t)tid, kNT);
+      } else {
+        find_tops(m, total, (uint32_t)tid, kNT);
         __syncthreads();
+        fp8_tops(ncol);
       }
-      pass(put, word & 0xffffu, tid, kNT);
-      __syncthreads();
-    } else if (first && (!LAYER || FP8)) {
-      if (!MX && !LAYER) __syncthreads();
-      pass(put, 0, tid, kNT);
+      put_rows(m, total, (uint32_t)tid, kNT);
       __syncthreads();
     }
     // The staged row of column col (the col-th token of the item; the last one past them).
@@ -493,78 +575,93 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
     };
     const uint32_t frow = settled(row_of(l16) * stride + 64u * g);
     const float alpha = MX ? 1.0f : ld_const(p.g, LAYER ? word >> 16 : 0);
-    const int run = min(left, tpi - tile), nst = run * cpw;
+    const int run = min(left, tpi - tile), nst = run * spt, turns = (nst + D - 1) / D;
     left -= run;
-    for (int s = 0; s < nst; s += D) {
+    int step = 0, sub = tile * RG + rg;
+    for (int turn = 0; turn < turns; ++turn) {
+      int ready = 0;
 #pragma unroll
       for (int d = 0; d < D; ++d) {
-        if (s + d < nst) {
-          const uint32_t c = (uint32_t)(ksl + (step << p.ks_log));
-          if (c < nch && tile * RG + rg < nsub) {
-            Op bf[4];
+        const uint32_t c = (uint32_t)(ksl + (step << p.ks_log));
+        if (turn * D + d < nst && step < cpw && c < nch && sub < nsub) {
+          Op bf[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) bf[j] = *reinterpret_cast<const Op*>(s_rows + frow + c * 256u + 16 * j);
+          for (int j = 0; j < 4; ++j) bf[j] = *reinterpret_cast<const Op*>(s_rows + frow + c * 256u + 16 * j);
 #pragma unroll
-            for (int b = 0; b < RB; ++b) {
-              Op wf[4];
-              Dec::run(wring[d][b], scale_of<MX>(sring[d][b], c), wf);
+          for (int b = 0; b < RB; ++b) {
+            Op wf[4];
+            Dec::run(wring[d][b], scale_of<MX>(sring[d][b], c), wf);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) tot[b] = Dec::mfma(wf[j], bf[j], tot[b]);
-            }
+            for (int j = 0; j < 4; ++j) tot[b] = Dec::mfma(wf[j], bf[j], tot[b]);
           }
         }
         issue(d);
-        step += s + d < nst ? 1 : 0;
-        if (step == cpw) {
-          // ---- a tile is complete: the waves' sums, then the epilogue
-          step = 0;
-          float* red = s_red[buf];
+        const int wrap = step + 1 == spt ? 1 : 0;
+        step = wrap ? 0 : step + 1;
+        sub += wrap * RG;
+        if (wrap && turn * D + d < nst) {   // a tile is complete: this wave's sums
+          ready = 1;
           if (l16 < NTOK) {
 #pragma unroll
             for (int b = 0; b < RB; ++b)
-              *reinterpret_cast<f32x4*>(&red[((wave * RB + b) * NTOK + l16) * 16 + 4 * g]) = tot[b];
+              *reinterpret_cast<f32x4*>(&s_red[buf][((wave * RB + b) * NTOK + l16) * 16 + 4 * g]) = tot[b];
           }
 #pragma unroll
           for (int b = 0; b < RB; ++b) tot[b] = (f32x4){0.f, 0.f, 0.f, 0.f};
-          __syncthreads();
-          constexpr int NB = SWIGLU ? 1 : RB;
-          const int total = RG * NB * ncol * 16;
-          // a different wave starts each tile, so that short epilogues spread over the SIMDs
-          for (int i = (tid + kWave * done) & (kNT - 1); i < total; i += kNT) {
-            const int r16 = i & 15, q = i >> 4;
-            const int grp = q / (NB * ncol), b = (q / ncol) % NB, col = q % ncol;
-            const int osub = tile * RG + grp;
-            float v = 0.0f, u = 0.0f;
-            for (int w = 0; w < KS; ++w) {
-              const float* a = &red[(((grp * KS + w) * RB + b) * NTOK + col) * 16 + r16];
-              v += a[0];
-              if (SWIGLU) u += a[NTOK * 16];
+        }
+      }
+      next_run();
+      if (ready) {
+        // ---- the waves' sums together, and the epilogue
+        __syncthreads();
+        const float* red = s_red[buf];
+        constexpr int NB = SWIGLU ? 1 : RB;
+        const int total = RG * NB * ncol * 16;
+        // a different wave starts each tile, so that short epilogues spread over the SIMDs
+        for (int i = (tid + kWave * done) & (kNT - 1); i < total; i += kNT) {
+          const int r16 = i & 15, q = i >> 4;
+          const int grp = q / (NB * ncol), b = (q / ncol) % NB, col = q % ncol;
+          const int osub = tile * RG + grp;
+          float v = 0.0f, u = 0.0f;
+          // (the waves' values are requested four at a time; what is past KS is not added)
+          for (int w0 = 0; w0 < KS; w0 += 4) {
+            float av[4], au[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const float* a = &red[(((grp * KS + (w0 + w < KS ? w0 + w : w0)) * RB + b) * NTOK + col) * 16 + r16];
+              av[w] = a[0];
+              au[w] = SWIGLU ? a[NTOK * 16] : 0.0f;
             }
-            const float un = MX ? 1.0f : row_unscale(s_top[row_of(col)]);
-            v = v * alpha * un;
-            if (SWIGLU) v = swiglu1(v, u * alpha * un);
-            if constexpr (LAYER) {
-              const uint32_t hr = (uint32_t)s_row0[it] + (uint32_t)col;
-              const int F = p.Nw / 2, f = osub * 16 + r16;
-              if (MX) {
-                if (osub < nsub) static_cast<__bf16*>(p.h)[(size_t)hr * F + f] = (__bf16)v;
-              } else {
-                const uint32_t top = row16_max(finite_abs_bits(v));
-                const int e2 = top ? max((int)(top >> 23) - 141, kNoExp) : kNoExp;
-                if (osub < nsub) {
-                  static_cast<f16*>(p.h)[(size_t)hr * F + f] = (f16)ldexpf(v, -e2);
-                  if (r16 == 0) p.hexp[(size_t)hr * (nch_of(F) * 8) + osub] = (int8_t)e2;
-                }
-              }
-            } else if (osub < nsub && tile_block_in<SWIGLU, RB>(osub, b, nblk)) {
-              put_matvec(p, col, (size_t)tile_block<SWIGLU, RB>(osub, b, nblk) * 16 + r16, v);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              v += w0 + w < KS ? av[w] : 0.0f;
+              if (SWIGLU) u += w0 + w < KS ? au[w] : 0.0f;
             }
           }
-          if (BUF == 1) __syncthreads();
-          else buf ^= 1;
-          ++done;
-          ++tile;
+          const float un = MX ? 1.0f : row_unscale(s_top[row_of(col)]);
+          v = v * alpha * un;
+          if (SWIGLU) v = swiglu1(v, u * alpha * un);
+          if constexpr (LAYER) {
+            const uint32_t hr = (uint32_t)s_row0[it] + (uint32_t)col;
+            const int F = p.Nw / 2, f = osub * 16 + r16;
+            if (MX) {
+              if (osub < nsub) static_cast<__bf16*>(p.h)[(size_t)hr * F + f] = (__bf16)v;
+            } else {
+              const uint32_t top = row16_max(finite_abs_bits(v));
+              const int e2 = top ? max((int)(top >> 23) - 141, kNoExp) : kNoExp;
+              if (osub < nsub) {
+                static_cast<f16*>(p.h)[(size_t)hr * F + f] = (f16)ldexpf(v, -e2);
+                if (r16 == 0) p.hexp[(size_t)hr * (nch_of(F) * 8) + osub] = (int8_t)e2;
+              }
+            }
+          } else if (osub < nsub && tile_block_in<SWIGLU, RB>(osub, b, nblk)) {
+            put_matvec(p, col, (size_t)tile_block<SWIGLU, RB>(osub, b, nblk) * 16 + r16, v);
+          }
         }
+        if (BUF == 1) __syncthreads();
+        else buf ^= 1;
+        ++done;
+        ++tile;
       }
     }
     tile = 0;
@@ -577,21 +674,21 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
 // its own, with a power of two for every (row, chunk). The turning costs about as much as the
 // decode of four weight tiles, so a wave takes up to RB = 8 row blocks a chunk.
 template <bool MX, bool SWIGLU, int RB, int D, int WPS>
-__global__ __launch_bounds__(kNT, WPS) void few_long_kernel(const FewArgs p) {
+__global__ __launch_bounds__(kLongNT, WPS) void few_long_kernel(const FewArgs p) {
   typedef Decode<MX> Dec;
   typedef typename Dec::Op Op;
   constexpr int R = kFewMaxTokens / 4;
   constexpr int HB = SWIGLU ? RB / 2 : RB;
-  __shared__ __attribute__((aligned(16))) unsigned char s_row[kW][kFewMaxTokens * kRowBytes];
-  __shared__ float s_unscale[kW][kFewMaxTokens];
-  __shared__ __attribute__((aligned(16))) float s_red[kW * RB][16 * 16];
+  __shared__ __attribute__((aligned(16))) unsigned char s_row[kLongW][kFewMaxTokens * kRowBytes];
+  __shared__ float s_unscale[kLongW][kFewMaxTokens];
+  __shared__ __attribute__((aligned(16))) float s_red[kLongW * RB][16 * 16];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   const int T = p.T, K = p.K;
   const uint32_t nch = (uint32_t)nch_of(K);
-  const int cpw = ((int)nch + kW - 1) / kW;
+  const int cpw = ((int)nch + kLongW - 1) / kLongW;
   const uint32_t nblk = (uint32_t)p.Nw / 16;
   const int ntiles = ((int)(SWIGLU ? nblk / 2 : nblk) + HB - 1) / HB;
   const uint32_t wbytes = nblk * nch * 1024u;
@@ -613,7 +710,7 @@ __global__ __launch_bounds__(kNT, WPS) void few_long_kernel(const FewArgs p) {
   uint32_t c_l = 0;
   bool ok_l = false;
   auto issue_rows = [&](int d) {
-    c_l = (uint32_t)(wave + step_l * kW);
+    c_l = (uint32_t)(wave + step_l * kLongW);
     ok_l = left_l > 0 && c_l < nch;
     const bool cols = ok_l && (int)(c_l * kChunk) + 8 * l16 < K;
 #pragma unroll
@@ -648,7 +745,7 @@ __global__ __launch_bounds__(kNT, WPS) void few_long_kernel(const FewArgs p) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
       // (chunks past the last have loaded zeros, rows and weights, and add nothing)
-      const uint32_t c = (uint32_t)(wave + step * kW);
+      const uint32_t c = (uint32_t)(wave + step * kLongW);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         if (4 * r < T) {
@@ -694,12 +791,12 @@ __global__ __launch_bounds__(kNT, WPS) void few_long_kernel(const FewArgs p) {
         }
         __syncthreads();
         const float alpha = MX ? 1.0f : ld_const(p.g, 0);
-        for (int i = tid; i < HB * T * 16; i += kNT) {
+        for (int i = tid; i < HB * T * 16; i += kLongNT) {
           const int r16 = i & 15, q = i >> 4, b = q / T, col = q - b * T;
           if (!tile_block_in<SWIGLU, RB>(tile, b, nblk)) continue;
           float v = 0.0f, u = 0.0f;
 #pragma unroll
-          for (int w = 0; w < kW; ++w) {
+          for (int w = 0; w < kLongW; ++w) {
             v += s_red[w * RB + b][col * 16 + r16];
             if (SWIGLU) u += s_red[w * RB + b + HB][col * 16 + r16];
           }
@@ -715,34 +812,81 @@ __global__ __launch_bounds__(kNT, WPS) void few_long_kernel(const FewArgs p) {
 }
 
 // ------------------------------------------------------------------ the layer's second launch
-// One workgroup per RB blocks of 16 output columns; its waves deal out the (item, chunk) pairs.
-template <bool MX, int RB, int D>
+// A tile is 32 output columns (RB = 2 row blocks); its work is the (item, chunk) pairs. The
+// pairs of all tiles form one sequence that the workgroups share evenly: a CU's share of the
+// memory rate is limited (the most reads it can have under way), so every CU has to take the
+// same number of bytes, which whole tiles seldom give (192 tiles on 256 CUs: three quarters of
+// the rate). A tile that several workgroups have part of is finished by the last of them to
+// arrive, which adds the parts in order; nobody waits.
+// Sequence positions of workgroup i of n: [i W / n, (i + 1) W / n) of W. The one that holds x:
+__device__ __forceinline__ int part_of(int64_t x, int64_t n, int64_t W) { return (int)(((x + 1) * n - 1) / W); }
+
+template <bool MX, int D>
 __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
   typedef Decode<MX> Dec;
   typedef typename Dec::Op Op;
+  constexpr int RB = kFewDownBlocks;
+  static_assert(kFewMaxSlots <= kNT, "a thread for each row and item");
   __shared__ __attribute__((aligned(16))) unsigned char s_row[kW][kItemTok * kRowBytes];
   __shared__ __attribute__((aligned(16))) float s_red[kW * RB][16 * 16];
   __shared__ uint32_t s_item[kFewMaxSlots];
   __shared__ uint16_t s_row0[kFewMaxSlots];
-  __shared__ float s_mul[kFewMaxSlots];      // what a row's products are multiplied with
-  __shared__ int8_t s_top[kFewMaxSlots];     // NVFP4: the largest exponent of a row's blocks
+  __shared__ float s_mul[kFewMaxSlots];   // what a row's products are multiplied with
+  __shared__ int s_top[kFewMaxSlots];     // NVFP4: the largest exponent of a row's blocks
+  __shared__ int s_last;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   const int T = p.T, F = p.K, S = T * p.k;
-  const uint32_t nch = (uint32_t)(F + kChunk - 1) / kChunk;
+  const uint32_t nch = (uint32_t)nch_of(F);
   const uint32_t nblk = (uint32_t)p.Nw / 16;
   const uint32_t wbytes = nblk * nch * 1024u;
   const uint32_t sbytes = nblk * (MX ? (nch + 15) >> 4 : (nch + 7) >> 3) * 1024u;
 
-  const int nitems = __builtin_amdgcn_readfirstlane(p.plan->n_items);
-  for (int i = tid; i < nitems; i += kNT) s_item[i] = p.plan->item[i];
-  for (int i = tid; i < nitems; i += kNT) s_row0[i] = p.plan->row0[i];
+  // The list of items (its first entries are read beside their number), and what each row is
+  // multiplied with: its weight, and for NVFP4 the largest of its blocks' exponents, to which
+  // its blocks are brought as they are read.
+  const int listed = p.plan->n_items;
+  const uint32_t item0 = tid < S ? p.plan->item[tid] : 0u;   // (S <= kFewMaxSlots = NT entries)
+  const uint16_t row0 = tid < S ? p.plan->row0[tid] : (uint16_t)0;
+  const float weight0 = tid < S ? p.plan->weight[tid] : 0.0f;
+  if (!MX && tid < S) s_top[tid] = kNoExp;
+  if (tid < S) {
+    s_item[tid] = item0;
+    s_row0[tid] = row0;
+  }
+  __syncthreads();
+  if (!MX) {
+    for (uint32_t i = tid; i < (uint32_t)S * nch; i += kNT) {
+      const uint32_t r = i / nch, c = i - r * nch;
+      const uint2 e = *reinterpret_cast<const uint2*>(p.hexp + (size_t)i * 8u);
+      const int used = F / 16 - (int)c * 8;
+      int top = kNoExp;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int e2 = (int)(int8_t)((j < 4 ? e.x : e.y) >> (8 * (j & 3)));
+        top = j < used ? max(top, e2) : top;
+      }
+      atomicMax(&s_top[r], top);
+    }
+    __syncthreads();
+  }
+  if (tid < S) s_mul[tid] = MX ? weight0 : ldexpf(weight0, s_top[tid]);
+  const int nitems = __builtin_amdgcn_readfirstlane(listed);
   __syncthreads();
 
-  const int npair = nitems * (int)nch;
-  const int nst = wave < npair ? (npair - wave + kW - 1) / kW : 0;   // this wave's pairs
+  // This workgroup's part of the sequence.
+  const int64_t P = (int64_t)nitems * nch, ntile = nblk / RB, Wk = P * ntile;
+  int64_t n = Wk / kDownLeast;   // workgroups that take part: not fewer than there are tiles
+  n = n < ntile ? ntile : n;
+  n = n < (int64_t)gridDim.x ? n : (int64_t)gridDim.x;
+  if ((int64_t)blockIdx.x >= n) return;
+  const int64_t x0 = blockIdx.x * Wk / n, x1 = (blockIdx.x + 1) * Wk / n;
+  int tile = (int)(x0 / P);
+  int q0 = (int)(x0 - tile * P);
+  int64_t left = x1 - x0;
+
   const __amdgpu_buffer_rsrc_t hr = make_rsrc(p.h, (uint32_t)S * (uint32_t)F * 2u);
   const __amdgpu_buffer_rsrc_t er = make_rsrc(p.hexp, (uint32_t)S * nch * 8u);
   __amdgpu_buffer_rsrc_t wr, sr;
@@ -759,60 +903,35 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
   u32x4 wring[D][RB], xring[D];
   uint32_t sring[D][RB];
   uint32_t ering[D];   // the exponents of four blocks of 16 columns, the lane's own among them
-  int a_l = wave / (int)nch, c_l = wave - a_l * (int)nch, left_l = nst;
-  if (nst > 0) open_item(a_l);
+  // The loads' position: item and chunk of this wave's next pair in the tile, and its steps left.
+  const int da = kW / (int)nch, dc = kW - da * (int)nch;
+  int a_l = 0, c_l = 0, run_l = 0;
+  auto open_tile = [&](int first, int m) {   // the m pairs of the tile from pair `first` on
+    run_l = wave < m ? (m - wave + kW - 1) / kW : 0;
+    a_l = (first + wave) / (int)nch;
+    c_l = first + wave - a_l * (int)nch;
+    if (run_l > 0) open_item(a_l);
+  };
   auto issue = [&](int d) {
-    const bool ok = left_l > 0;
+    const bool ok = run_l > 0;
     const uint32_t c = (uint32_t)c_l;
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
-      const uint32_t blk = blockIdx.x * RB + b;
-      const bool in = ok && blk < nblk;
-      wring[d][b] = ld128(wr, settled(16u * lane + (in ? (blk * nch + c) * 1024u : kOOB)), 0);
-      sring[d][b] = ld32(sr, settled(16u * lane + (in ? scale_off<MX>(blk, nch, c) : kOOB)));
+      const uint32_t blk = (uint32_t)tile * RB + b;
+      wring[d][b] = ld128(wr, settled(16u * lane + (ok ? (blk * nch + c) * 1024u : kOOB)), 0);
+      sring[d][b] = ld32(sr, settled(16u * lane + (ok ? scale_off<MX>(blk, nch, c) : kOOB)));
     }
     const bool in = ok && (int)(c * kChunk) + 8 * l16 < F;
     xring[d] = ld128(hr, settled(in ? hoff + c * 256u : kOOB), 0);
     if (!MX) ering[d] = ld32(er, settled(in ? eoff + c * 8u : kOOB));
-    --left_l;
-    c_l += kW;
-    if (c_l >= (int)nch) {
-      do {
-        c_l -= (int)nch;
-        ++a_l;
-      } while (c_l >= (int)nch);
-      if (left_l > 0) open_item(a_l);
-    }
+    const int a0 = a_l;
+    --run_l;
+    c_l += dc;
+    const int carry = c_l >= (int)nch ? 1 : 0;
+    c_l -= carry * (int)nch;
+    a_l += da + carry;
+    if (a_l != a0 && run_l > 0) open_item(a_l);
   };
-  if (nst > 0) {
-#pragma unroll
-    for (int d = 0; d < D; ++d) issue(d);
-  }
-
-  // What each row is multiplied with: its weight, and for NVFP4 the largest of its blocks'
-  // exponents, to which its blocks are brought as they are read.
-  for (int r = tid; r < S; r += kNT) {
-    int top = kNoExp;
-    if (!MX) {
-      for (uint32_t c = 0; c < nch; ++c) {
-        const uint2 q = *reinterpret_cast<const uint2*>(p.hexp + (size_t)r * (nch * 8u) + c * 8u);
-        const int used = min(8, F / 16 - (int)c * 8);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int e2 = (int)(int8_t)((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
-          top = j < used ? max(top, e2) : top;
-        }
-      }
-      s_top[r] = (int8_t)top;
-    }
-    s_mul[r] = MX ? p.plan->weight[r] : ldexpf(p.plan->weight[r], top);
-  }
-  __syncthreads();
-
-  f32x4 tot[RB], acc[RB];
-#pragma unroll
-  for (int b = 0; b < RB; ++b) tot[b] = acc[b] = (f32x4){0.f, 0.f, 0.f, 0.f};
-  int a = wave / (int)nch, c = wave - a * (int)nch;
   bool has = false;     // the lane's token is one of the item's
   uint32_t frow = 0;    // the bytes of its row in the wave's LDS
   float mul = 0.0f;     // and what its products are multiplied with
@@ -826,6 +945,7 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
     mul = has ? s_mul[r0 + fr] : 0.0f;
     if (!MX) top = g < __popc(w & 0xffffu) ? s_top[r0 + g] : 0;
   };
+  f32x4 tot[RB], acc[RB];
   // The item's sums into the token's: only the item's own tokens, the other columns hold
   // products that mean nothing.
   auto fold = [&]() {
@@ -836,81 +956,139 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
       acc[b] = (f32x4){0.f, 0.f, 0.f, 0.f};
     }
   };
-  if (nst > 0) take_item(a);
   unsigned char* row = s_row[wave];
-  for (int s = 0; s < nst; s += D) {
+  const int per = RB * 16 * T;   // values of a tile
+  for (;;) {
+    const int m = (int)(left < P - q0 ? left : P - q0);   // pairs of this tile
+    left -= m;
+    open_tile(q0, m);
+    const int nst = run_l, turns = ((m + kW - 1) / kW + D - 1) / D;
 #pragma unroll
-    for (int d = 0; d < D; ++d) {
-      // Steps past the last pair have loaded zeros and add nothing.
-      const uint32_t cc = (uint32_t)c;
-      if (MX) {
-        *reinterpret_cast<u32x4*>(row + g * kRowBytes + 16 * l16) = xring[d];
-      } else {
-        const int e2 = (int)(int8_t)(ering[d] >> (4u * (l16 & 6)));
-        const f16 f = (f16)ldexpf(1.0f, min(e2 - top, 0));   // (no exponent past the row's columns)
-        *reinterpret_cast<f16x8*>(row + g * kRowBytes + 16 * l16) = __builtin_bit_cast(f16x8, xring[d]) * f;
-      }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      Op bf[4];
+    for (int b = 0; b < RB; ++b) tot[b] = acc[b] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    int a = a_l, c = c_l;
+    has = false;
+    for (int turn = -1; turn < turns; ++turn) {   // turn -1 fills the ring
+      // The waves go through the ring together: the CU serves its older waves first, and the
+      // youngest would end up with most of its steps to do alone.
+      if (turn > 0) __builtin_amdgcn_s_barrier();
 #pragma unroll
-      for (int j = 0; j < 4; ++j) bf[j] = *reinterpret_cast<const Op*>(row + frow + 16 * j);
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      for (int d = 0; d < D; ++d) {
+        if (turn >= 0) {
+          // Steps past the last pair have loaded zeros and add nothing.
+          const uint32_t cc = (uint32_t)c;
+          if (MX) {
+            *reinterpret_cast<u32x4*>(row + g * kRowBytes + 16 * l16) = xring[d];
+          } else {
+            const int e2 = (int)(int8_t)(ering[d] >> (4u * (l16 & 6)));
+            const f16 f = (f16)ldexpf(1.0f, min(e2 - top, 0));   // (no exponent past the row's columns)
+            *reinterpret_cast<f16x8*>(row + g * kRowBytes + 16 * l16) = __builtin_bit_cast(f16x8, xring[d]) * f;
+          }
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          Op bf[4];
 #pragma unroll
-      for (int b = 0; b < RB; ++b) {
-        Op wf[4];
-        Dec::run(wring[d][b], scale_of<MX>(sring[d][b], cc), wf);
+          for (int j = 0; j < 4; ++j) bf[j] = *reinterpret_cast<const Op*>(row + frow + 16 * j);
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[b] = Dec::mfma(wf[j], bf[j], acc[b]);
-      }
-      c += kW;
-      if (c >= (int)nch) {
-        do {
-          c -= (int)nch;
-          ++a;
-        } while (c >= (int)nch);
-        if (s + d + 1 < nst) {   // (else the last item stays)
-          fold();
-          take_item(a);
+          for (int b = 0; b < RB; ++b) {
+            Op wf[4];
+            Dec::run(wring[d][b], scale_of<MX>(sring[d][b], cc), wf);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[b] = Dec::mfma(wf[j], bf[j], acc[b]);
+          }
+        }
+        issue(d);
+        if (turn >= 0) {
+          const int a0 = a;
+          c += dc;
+          const int carry = c >= (int)nch ? 1 : 0;
+          c -= carry * (int)nch;
+          a += da + carry;
+          if (a != a0 && turn * D + d + 1 < nst) {   // (else the last item stays)
+            fold();
+            take_item(a);
+          }
         }
       }
-      issue(d);
+      if (turn < 0 && nst > 0) take_item(a);
     }
-  }
-  fold();
+    fold();
 
+    // ---- the waves' sums, then the tile or its part
 #pragma unroll
-  for (int b = 0; b < RB; ++b) *reinterpret_cast<f32x4*>(&s_red[wave * RB + b][l16 * 16 + 4 * g]) = tot[b];
-  __syncthreads();
-  for (int i = tid; i < RB * T * 16; i += kNT) {
-    const int r16 = i & 15, q = i >> 4, b = q / T, t = q - b * T;
-    const uint32_t blk = blockIdx.x * RB + b;
-    if (blk >= nblk) continue;
-    float v = 0.0f;
+    for (int b = 0; b < RB; ++b) *reinterpret_cast<f32x4*>(&s_red[wave * RB + b][l16 * 16 + 4 * g]) = tot[b];
+    __syncthreads();
+    const int part0 = part_of(tile * P, n, Wk), parts = part_of((tile + 1) * P - 1, n, Wk) - part0 + 1;
+    float* mine = p.part + ((size_t)tile * p.most_parts + (blockIdx.x - part0)) * per;
+    auto put = [&](int i, float v) {
+      const int r16 = i & 15, q = i >> 4, b = q / T, t = q - b * T;
+      static_cast<__bf16*>(p.out)[(size_t)t * p.ld_out + ((size_t)tile * RB + b) * 16 + r16] = (__bf16)v;
+    };
+    for (int i = tid; i < per; i += kNT) {
+      const int r16 = i & 15, q = i >> 4, b = q / T, t = q - b * T;
+      float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kW; ++w) v += s_red[w * RB + b][t * 16 + r16];
-    static_cast<__bf16*>(p.out)[(size_t)t * p.ld_out + blk * 16 + r16] = (__bf16)v;
+      for (int w = 0; w < kW; ++w) v += s_red[w * RB + b][t * 16 + r16];
+      if (parts == 1)
+        put(i, v);
+      else
+        __hip_atomic_store(mine + i, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if (parts > 1) {
+      // Device-scope stores and loads; every wave's stores have completed (vmcnt 0) before the
+      // barrier that precedes the count, and the last arriver's loads follow the barrier after it.
+      __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+      __syncthreads();
+      if (tid == 0)
+        s_last = __hip_atomic_fetch_add(p.plan->arrived + tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
+      __syncthreads();
+      if (s_last) {
+        const float* base = p.part + (size_t)tile * p.most_parts * per;
+        for (int i = tid; i < per; i += kNT) {
+          float v = 0.0f;
+          for (int w = 0; w < parts; ++w)
+            v += __hip_atomic_load(base + (size_t)w * per + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          put(i, v);
+        }
+      }
+    }
+    if (left == 0) break;
+    __syncthreads();
+    q0 = 0;
+    ++tile;
   }
 }
 
-// Chunks dealt out at a time: 8 when every wave then has one, else fewer, so that the waves
-// left over take row blocks of their own.
-int ks_log_for(int K) {
+// Chunks dealt out at a time (log2): as many as leave every wave four or more of a tile's, and
+// more where the tiles would not fill the CUs otherwise. sub: row block groups of all items.
+int ks_log_for(int K, int64_t sub) {
   const int nch = nch_of(K);
-  return nch >= 8 ? 3 : nch >= 4 ? 2 : nch >= 2 ? 1 : 0;
+  int l = 0;
+  while (l < 4 && (nch >> (l + 1)) >= 4) ++l;
+  while (l < 4 && (1 << (l + 1)) <= nch && (sub << l) / kW < kGrid) ++l;
+  return l;
 }
 
-// LDS for resident rows: what two workgroups a CU leave of its 160 KB.
-constexpr int kResidentBytes = 64 * 1024;
+// LDS for resident rows: what the rest leaves of a CU's 160 KB.
+constexpr int kResidentBytes = 112 * 1024;
 int row_lds_bytes(int K) { return nch_of(K) * 256 + 16; }
 // Rows of K columns that fit.
 int resident_rows(int K) { return kResidentBytes / (nch_of(K) * 256); }
 
+// 2^32 / ppr rounded up, for pieces / ppr as the high half of a product: exact while the pieces
+// (16 rows' at most, 16 ppr) times the excess (below ppr) stay under 2^32, i.e. for ppr < 2^14;
+// one piece more than the last row's is never asked for.
+uint32_t ppr_inverse(int K) {
+  const uint32_t ppr = (uint32_t)nch_of(K) * 16u;
+  return (uint32_t)(((uint64_t(1) << 32) + ppr - 1) / ppr);
+}
+
 template <bool MX, bool LAYER, bool FP8, bool SWIGLU, int NTOK, int RB, int D>
-hipError_t launch_up(const FewArgs& a, int rows, int grid, hipStream_t stream) {
+hipError_t launch_up(FewArgs a, int rows, int grid, hipStream_t stream) {
   static std::atomic<uint64_t> done{0};
   auto* kernel = few_up_kernel<MX, LAYER, FP8, SWIGLU, NTOK, RB, D>;
   const hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(kernel), kResidentBytes + 16 * 16, done);
   if (e != hipSuccess) return e;
+  a.ppr_inv = ppr_inverse(a.K);
   kernel<<<grid, kNT, rows * row_lds_bytes(a.K), stream>>>(a);
   return hipGetLastError();
 }
@@ -927,7 +1105,7 @@ template <bool MX, bool SWIGLU, int RB, int D, int WPS>
 hipError_t launch_long(const FewArgs& a, hipStream_t stream) {
   const int hb = SWIGLU ? RB / 2 : RB;
   const int tiles = ((SWIGLU ? a.Nw / 32 : a.Nw / 16) + hb - 1) / hb, most = 128 * WPS / 2 * 2;
-  few_long_kernel<MX, SWIGLU, RB, D, WPS><<<tiles < most ? tiles : most, kNT, 0, stream>>>(a);
+  few_long_kernel<MX, SWIGLU, RB, D, WPS><<<tiles < most ? tiles : most, kLongNT, 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -941,14 +1119,25 @@ hipError_t launch_mv_rows(const FewArgs& a, hipStream_t stream) {
 
 }  // namespace
 
+int few_down_workgroups(int T, int k, int Nw, int K) {
+  const int64_t ntile = Nw / (16 * kFewDownBlocks), most = (int64_t)T * k * nch_of(K) * ntile / kDownLeast;
+  const int64_t n = most > ntile ? most : ntile;
+  return n < kGrid ? (int)n : kGrid;
+}
+int few_down_parts(int T, int k, int Nw, int K) {
+  // A tile of P pairs holds at most ceil(P n / W) + 1 of the n workgroups' parts, and P / W = 1 / ntile
+  const int ntile = Nw / (16 * kFewDownBlocks);
+  return (few_down_workgroups(T, k, Nw, K) + ntile - 1) / ntile + 1;
+}
+
 hipError_t launch_few_matvec(FewArgs a, bool mx, bool swiglu, hipStream_t stream) {
-  a.ks_log = ks_log_for(a.K);
+  a.ks_log = ks_log_for(a.K, a.Nw / 32);
   if (mx) return swiglu ? launch_mv_rows<true, true>(a, stream) : launch_mv_rows<true, false>(a, stream);
   return swiglu ? launch_mv_rows<false, true>(a, stream) : launch_mv_rows<false, false>(a, stream);
 }
 
 hipError_t launch_few_layer(FewArgs up, FewArgs down, bool mx, hipStream_t stream) {
-  up.ks_log = ks_log_for(up.K);
+  up.ks_log = ks_log_for(up.K, (int64_t)up.T * up.k * (up.Nw / 32));
   const int fit = resident_rows(up.K);   // >= 1 by the limit on H
   up.item_tok = fit < kItemTok ? fit : kItemTok;
   const int rg = kW >> up.ks_log, nsub = up.Nw / 32;
@@ -959,12 +1148,11 @@ hipError_t launch_few_layer(FewArgs up, FewArgs down, bool mx, hipStream_t strea
                        : up.fp8 ? launch_up<false, true, true, true, kItemTok, 2, 4>(up, rows, grid, stream)
                                 : launch_up<false, true, false, true, kItemTok, 2, 4>(up, rows, grid, stream);
   if (e != hipSuccess) return e;
-  constexpr int RB = 1;
-  const int wgs = (down.Nw / 16 + RB - 1) / RB;
+  const int wgs = few_down_workgroups(down.T, down.k, down.Nw, down.K);
   if (mx)
-    few_down_kernel<true, RB, 4><<<wgs, kNT, 0, stream>>>(down);
+    few_down_kernel<true, 3><<<wgs, kNT, 0, stream>>>(down);
   else
-    few_down_kernel<false, RB, 4><<<wgs, kNT, 0, stream>>>(down);
+    few_down_kernel<false, 3><<<wgs, kNT, 0, stream>>>(down);
   return hipGetLastError();
 }
 

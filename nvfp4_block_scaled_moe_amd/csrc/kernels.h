@@ -155,6 +155,7 @@ hipError_t launch_zero_f32(float* p, int n, hipStream_t stream);
 constexpr int kFewMaxTokens = 16;
 constexpr int kFewMaxSlots = kFewMaxTokens * kMaxTopK;
 constexpr int kFewMaxHidden = 32768;   // H of the layer: at least one row stays in LDS
+constexpr int kFewDownBlocks = 2;      // 16-column blocks of a tile of the layer's second launch
 // What the layer's first launch leaves for its second: the items (expert << 16 | mask of its
 // tokens) with the first of their rows in h, and for every row of h its routing weight (NVFP4:
 // times the global scale of the expert's second matrix).
@@ -163,6 +164,7 @@ struct FewPlan {
   uint32_t item[kFewMaxSlots];
   uint16_t row0[kFewMaxSlots];
   float weight[kFewMaxSlots];
+  int arrived[kFewMaxHidden / (16 * kFewDownBlocks)];   // parts of each tile that are there
 };
 struct FewArgs {
   const uint16_t* x;      // bf16 [T, K], rows ldx elements apart (matvec, the layer's first launch)
@@ -173,6 +175,7 @@ struct FewArgs {
   const float* g;         // their global scales (NVFP4)
   int Nw;
   int ks_log, item_tok;   // set by the launcher
+  uint32_t ppr_inv;
   const void* add;        // matvec: float32 or bf16 [T, n], rows ld_add apart, or null
   int add_bf16;
   int64_t ld_add;
@@ -185,9 +188,15 @@ struct FewArgs {
   int fp8;                // layer, NVFP4: the rows first take the FP8 E4M3 round trip
   FewPlan* plan;          // layer workspace
   void* h;                // [T * k, F] f16 (NVFP4) or bf16 (MXFP4)
+  int down_tiles;         // tiles of the second launch
+  float* part;            // [down_tiles, most_parts, 32 T] sums of a tile that workgroups share
+  int most_parts;
   int8_t* hexp;           // NVFP4: [T * k, 8 ceil(F / 128)] exponents of h's blocks of 16 columns
 };
 hipError_t launch_few_matvec(FewArgs a, bool mx, bool swiglu, hipStream_t stream);
+// Workgroups of the layer's second launch, and the most of them that share a tile.
+int few_down_workgroups(int T, int k, int Nw, int K);
+int few_down_parts(int T, int k, int Nw, int K);
 hipError_t launch_few_layer(FewArgs up, FewArgs down, bool mx, hipStream_t stream);
 
 // ---- reduce.hip
