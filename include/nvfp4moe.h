@@ -528,7 +528,7 @@ nvfp4moe_status mxfp4_matvec(nvfp4moe_epilogue epi, const void* x, int64_t ldx, 
  * GEMMs with the preparation of h between them, moe_unpermute_reduce) cost as much as the
  * weights' traffic. [P1] section 3 (launch overhead of many small kernels), [P3] "Discovering
  * the sgl_kernel Alternative" (a fused MoE). 16-bit activations with either weight format.
- *     ids, w as moe_route_permute(logits, T, E, k) gives them
+ *     ids as moe_route_permute(logits, T, E, k) gives them, w within 2^-21 of its weights
  *     h[t,j] = silu(x'_t W_gate^T) * (x'_t W_up^T) of expert ids[t,j]
  *     out[t] = bf16( sum_j w[t,j] * h[t,j] W_down^T )
  * with x' = x, or (fp8_act) x after the FP8 E4M3 round trip of act_fp8_e4m3_roundtrip, whose

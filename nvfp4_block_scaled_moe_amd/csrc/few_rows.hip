@@ -259,7 +259,8 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
   __shared__ uint32_t s_first[LAYER ? kMaxExperts : 1];     // token mask, then item << 16 | row
   __shared__ int s_ids[LAYER ? kFewMaxSlots : 1];
   __shared__ float s_w[LAYER ? kFewMaxSlots : 1];
-  __shared__ uint32_t s_n;
+  __shared__ uint32_t s_scan[kW];
+  __shared__ uint32_t s_amax;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -301,16 +302,19 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
     }
   };
   uint32_t amax = 0;   // FP8: the largest finite magnitude that this thread has seen
+  auto tops_of_batch = [&](uint32_t total, uint32_t i0, uint32_t nt) {
+#pragma unroll
+    for (int i = 0; i < kPassBatch; ++i) {
+      const uint32_t idx = i0 + i * nt;
+      const uint32_t top = row16_max(top_of(pv[i], FP8 ? 0x7f81u : 0x7f80u));   // (a row's pieces come in sixteens)
+      if (l16 == 0 && idx < total) atomicMax(&s_top[row_at(idx)], top);
+      if (FP8) amax = max(amax, top_of(pv[i], 0x7f80u));
+    }
+  };
   auto find_tops = [&](uint32_t mask, uint32_t total, uint32_t first, uint32_t nt) {
     for (uint32_t i0 = first; i0 < total; i0 += kPassBatch * nt) {
       load_batch(mask, total, i0, nt);
-#pragma unroll
-      for (int i = 0; i < kPassBatch; ++i) {
-        const uint32_t idx = i0 + i * nt;
-        const uint32_t top = row16_max(top_of(pv[i], FP8 ? 0x7f81u : 0x7f80u));   // (a row's pieces come in sixteens)
-        if (l16 == 0 && idx < total) atomicMax(&s_top[row_at(idx)], top);
-        if (FP8) amax = max(amax, top_of(pv[i], 0x7f80u));
-      }
+      tops_of_batch(total, i0, nt);
     }
   };
   float fp8_s = 1.0f;
@@ -368,17 +372,17 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
     static_assert(kFewMaxTokens <= kW, "a wave per token");
     const int E = p.E, k = p.k, S = T * k;
     for (int e = tid; e < E; e += kNT) s_first[e] = 0;
-    if (tid == 0) s_n = 0;
+    if (FP8 && tid == 0) s_amax = 0;
     __syncthreads();
     if (wave < T) {
       const float* row = p.logits + (size_t)wave * E;
       uint32_t* scratch = reinterpret_cast<uint32_t*>(&s_red[0][0]) + wave * 3 * kWave;
       if (E <= 256)
-        route_token_thresh<4>(row, E, k, lane, s_ids + wave * k, s_w + wave * k, nullptr, scratch);
+        route_token_thresh<4, float>(row, E, k, lane, s_ids + wave * k, s_w + wave * k, nullptr, scratch);
       else if (E <= 512)
-        route_token_thresh<8>(row, E, k, lane, s_ids + wave * k, s_w + wave * k, nullptr, scratch);
+        route_token_thresh<8, float>(row, E, k, lane, s_ids + wave * k, s_w + wave * k, nullptr, scratch);
       else
-        route_token_thresh<16>(row, E, k, lane, s_ids + wave * k, s_w + wave * k, nullptr, scratch);
+        route_token_thresh<16, float>(row, E, k, lane, s_ids + wave * k, s_w + wave * k, nullptr, scratch);
     }
     if (MX && all && (uint32_t)tid >= st0) load_batch(0, all, (uint32_t)tid - st0, stn);
     if (!MX && (uint32_t)tid >= st0) {
@@ -393,12 +397,12 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
       }
       if (FP8) {
         amax = row16_max(amax);
-        if (l16 == 0) atomicMax(&s_n, amax);
+        if (l16 == 0) atomicMax(&s_amax, amax);
       }
     }
     __syncthreads();
     if (FP8) {
-      fp8_s = fp8_scale(bf16_to_f32(s_n));
+      fp8_s = fp8_scale(bf16_to_f32(s_amax));
       fp8_inv = 1.0 / (double)fp8_s;
       if (all_rows) fp8_tops(T);
     }
@@ -412,42 +416,44 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
       // ---- the items in ascending expert order
       for (int s = tid; s < S; s += kNT) atomicOr(&s_first[s_ids[s]], 1u << (s / k));
       __syncthreads();
-      if (wave == 0) {
-        const int per = (E + kWave - 1) / kWave;
-        const uint32_t cap = (uint32_t)p.item_tok;
-        uint32_t cnt = 0;   // items << 16 | rows of this lane's experts
-        for (int i = 0; i < per; ++i) {
-          const int e = lane * per + i;
-          const uint32_t n = e < E ? (uint32_t)__popc(s_first[e]) : 0u;
-          cnt += ((n + cap - 1) / cap) << 16 | n;
-        }
-        uint32_t incl = cnt;
+      // a thread for each expert: the items and rows before its own by a scan over the threads
+      static_assert(kMaxExperts <= kNT, "a thread for each expert");
+      const uint32_t cap = (uint32_t)p.item_tok;
+      uint32_t m = tid < E ? s_first[tid] : 0u;
+      const uint32_t rows = (uint32_t)__popc(m);
+      // (ceil(rows / cap) for cap 1 .. 4 and at most 16 rows)
+      const uint32_t cnt = ((rows + cap - 1) * (cap == 1 ? 12u : cap == 2 ? 6u : cap == 3 ? 4u : 3u) / 12u) << 16 | rows;
+      uint32_t incl = cnt;
 #pragma unroll
-        for (int o = 1; o < kWave; o <<= 1) {
-          const uint32_t up = __shfl_up(incl, o, kWave);
-          if (lane >= o) incl += up;
+      for (int o = 1; o < kWave; o <<= 1) {
+        const uint32_t up = __shfl_up(incl, o, kWave);
+        if (lane >= o) incl += up;
+      }
+      if (lane == kWave - 1) s_scan[wave] = incl;
+      __syncthreads();
+      uint32_t at = incl - cnt, sum = 0;
+#pragma unroll
+      for (int w = 0; w < kW; ++w) {
+        const uint32_t v = s_scan[w];
+        at += w < wave ? v : 0u;
+        sum += v;
+      }
+      nitems = (int)(sum >> 16);
+      if (m) {
+        s_first[tid] = at;
+        while (m) {
+          uint32_t rest = m;   // m without its lowest `cap` tokens
+          for (uint32_t j = 0; j < cap; ++j) rest &= rest - 1;
+          const uint32_t part = m & ~rest;
+          s_item[at >> 16] = (uint32_t)tid << 16 | part;
+          s_row0[at >> 16] = (uint16_t)(at & 0xffffu);
+          at += 0x10000u + (uint32_t)__popc(part);
+          m = rest;
         }
-        uint32_t at = incl - cnt;
-        for (int i = 0; i < per; ++i) {
-          const int e = lane * per + i;
-          if (e >= E) break;
-          uint32_t m = s_first[e];
-          s_first[e] = at;
-          while (m) {
-            uint32_t rest = m;   // m without its lowest `cap` tokens
-            for (uint32_t j = 0; j < cap; ++j) rest &= rest - 1;
-            const uint32_t part = m & ~rest;
-            s_item[at >> 16] = (uint32_t)e << 16 | part;
-            s_row0[at >> 16] = (uint16_t)(at & 0xffffu);
-            at += 0x10000u + (uint32_t)__popc(part);
-            m = rest;
-          }
-        }
-        if (lane == kWave - 1) s_n = incl >> 16;
       }
     }
+    nitems = __builtin_amdgcn_readfirstlane(nitems);
     __syncthreads();
-    if (T > 1) nitems = __builtin_amdgcn_readfirstlane((int)s_n);
   }
 
   auto write_plan = [&]() {   // the list for the second launch
@@ -517,27 +523,30 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
 
   int it = it_l, tile = tile_l, left = t1 - t0, buf = 0, done = 0;
   open_run();
-  if (!LAYER) {
-    if (MX) {
-      load_batch(0, all, (uint32_t)tid, stn);
-    } else {
-      __syncthreads();   // s_top is cleared
-      find_tops(0, all, (uint32_t)tid, stn);
-      __syncthreads();
-    }
-  }
   // Fill the ring. (After each turn the next run is opened where this one's loads have ended.)
   auto next_run = [&]() {
     if (steps_l <= 0 && tiles_l > 0) open_run();
   };
-  // (The rows first: a wave whose loads find no room waits for the others' to return.)
-  if (all) {
+  // The layer's rows have arrived and go to LDS first (a wave whose loads find no room waits for
+  // the others' to return); a matvec's are requested first and looked at behind the ring's loads.
+  if (LAYER && all) {
     if ((uint32_t)tid >= st0) put_rows(0, all, (uint32_t)tid - st0, stn);
     __syncthreads();
   }
+  if (!LAYER) load_batch(0, all, (uint32_t)tid, stn);
 #pragma unroll
   for (int d = 0; d < D; ++d) issue(d);
   next_run();
+  if (!LAYER) {
+    if (!MX) {
+      __syncthreads();   // s_top is cleared
+      tops_of_batch(all, (uint32_t)tid, stn);
+      if (all > kPassBatch * stn) find_tops(0, all, (uint32_t)tid + kPassBatch * stn, stn);
+      __syncthreads();
+    }
+    put_rows(0, all, (uint32_t)tid, stn);
+    __syncthreads();
+  }
   if constexpr (LAYER) {
     if (blockIdx.x == gridDim.x - 1) write_plan();   // (this workgroup always has a tile)
   }
@@ -910,7 +919,7 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
     run_l = wave < m ? (m - wave + kW - 1) / kW : 0;
     a_l = (first + wave) / (int)nch;
     c_l = first + wave - a_l * (int)nch;
-    if (run_l > 0) open_item(a_l);
+    open_item(run_l > 0 ? a_l : 0);   // (a wave without a pair needs a descriptor, too: its loads are out of range)
   };
   auto issue = [&](int d) {
     const bool ok = run_l > 0;
