@@ -560,6 +560,39 @@ nvfp4moe_status moe_layer_few_mxfp4(const float* logits, const void* x, int32_t 
                                     size_t ws_bytes, void* stream);
 size_t moe_layer_few_mxfp4_workspace_size(int32_t T, int32_t E, int32_t k, int32_t H, int32_t F);
 
+/* ---------------------------------------------------------------------------
+ * moe_block_norm -- the norms before and after a block, fused with its gate and residual scale,
+ * in one launch over the T rows:
+ *     u    = y                                   or, with post_w, rms(y) * (w_offset + post_w)
+ *     r'   = resid + scale * gate * u            -> resid_out, rounded to r_dtype
+ *     next = bf16( rms(r') * (w_offset + pre_w) )   with pre_w; r' in float32, not yet rounded
+ * with rms(v) = v / sqrt(mean(v^2) + eps). All sums are float32.
+ *   resid, resid_out   device [T, H] of r_dtype (F32 or BF16), rows ld_r / ld_ro elements apart;
+ *                resid_out may be resid (same row distance).
+ *   y            device [T, H] of y_dtype, rows ld_y apart; with slot_to_row and topk_w the
+ *                experts' rows [T * k, H], and y_t = sum_j topk_w[t, j] y[slot_to_row[t*k+j]]
+ *                as moe_unpermute_reduce sums them (without its rounding). NULL: only next is
+ *                written (the norm before the first block); post_w, gate, slot_to_row are then
+ *                NULL, resid_out is not used, and pre_w is needed.
+ *   slot_to_row, topk_w, k   device int32 [T * k], float [T, k], 1 <= k <= 64, T * k < 2^31; or
+ *                both NULL.
+ *   post_w, pre_w   device [H] of w_dtype (F32 or BF16), or NULL (no norm of y; no next).
+ *   w_offset     added to both weights (1 for weights stored about zero).
+ *   gate         device, gate_dtype, element (t, h) at t * gate_row + h * gate_col, gate_col 0 or
+ *                1 (a full gate, a row's, a column's by gate_row = 0); or NULL.
+ *   T, H         T >= 1; H >= 8, H % 8 == 0, H <= 32768.
+ *   next, ld_next   device bf16 [T, H] (output); NULL without pre_w.
+ *   Every tensor that is read in columns is 16-byte aligned with row distances >= H, % 8 == 0
+ *   (gate_row: % 8 == 0 when gate_col is 1).
+ * ------------------------------------------------------------------------- */
+nvfp4moe_status moe_block_norm(const void* resid, nvfp4moe_dtype r_dtype, int64_t ld_r, const void* y,
+                               nvfp4moe_dtype y_dtype, int64_t ld_y, const int32_t* slot_to_row,
+                               const float* topk_w, int32_t k, const void* post_w, const void* pre_w,
+                               nvfp4moe_dtype w_dtype, float w_offset, float eps, const void* gate,
+                               nvfp4moe_dtype gate_dtype, int64_t gate_row, int32_t gate_col, float scale,
+                               int32_t T, int32_t H, void* resid_out, int64_t ld_ro, void* next, int64_t ld_next,
+                               void* stream);
+
 /* Thread-local message describing the last non-OK status ("" if none). Never NULL. */
 const char* nvfp4moe_last_error(void);
 /* nvfp4moe_path of the last moe_grouped_gemm_nvfp4 call on this thread. */

@@ -23,7 +23,7 @@ PATH_NONE, PATH_STREAM, PATH_MFMA = 0, 1, 2
 STATUS_NAMES = {0: "OK", 1: "ERR_INVALID_ARG", 2: "ERR_UNSUPPORTED", 3: "ERR_WORKSPACE", 4: "ERR_HIP"}
 
 _vp, _sz, _i32, _i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64
-_int = ctypes.c_int
+_int, _f32 = ctypes.c_int, ctypes.c_float
 
 #: name -> (restype, argtypes), one entry per function declared in include/nvfp4moe.h
 SIGNATURES = {
@@ -73,6 +73,8 @@ SIGNATURES = {
     "moe_layer_few_nvfp4_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32]),
     "moe_layer_few_mxfp4": (_int, [_vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "moe_layer_few_mxfp4_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32]),
+    "moe_block_norm": (_int, [_vp, _int, _i64, _vp, _int, _i64, _vp, _vp, _i32, _vp, _vp, _int, _f32, _f32, _vp, _int,
+                              _i64, _i32, _f32, _i32, _i32, _vp, _i64, _vp, _i64, _vp]),
     "nvfp4moe_last_error": (ctypes.c_char_p, []),
     "nvfp4moe_last_dispatch": (_int, []),
     "nvfp4moe_abi_version": (_int, []),

@@ -1078,3 +1078,67 @@ nvfp4moe_status moe_layer_few_mxfp4(const float* logits, const void* x, int32_t 
 }
 
 }  // extern "C"
+
+// ------------------------------------------------------------------ the norms around a block
+extern "C" nvfp4moe_status moe_block_norm(const void* resid, nvfp4moe_dtype r_dtype, int64_t ld_r, const void* y,
+                                          nvfp4moe_dtype y_dtype, int64_t ld_y, const int32_t* slot_to_row,
+                                          const float* topk_w, int32_t k, const void* post_w, const void* pre_w,
+                                          nvfp4moe_dtype w_dtype, float w_offset, float eps, const void* gate,
+                                          nvfp4moe_dtype gate_dtype, int64_t gate_row, int32_t gate_col, float scale,
+                                          int32_t T, int32_t H, void* resid_out, int64_t ld_ro, void* next,
+                                          int64_t ld_next, void* stream) {
+  const char* fn = "moe_block_norm";
+  auto known = [](nvfp4moe_dtype d) { return d == NVFP4MOE_F32 || d == NVFP4MOE_BF16; };
+  if (!known(r_dtype) || (y && !known(y_dtype)) || ((post_w || pre_w) && !known(w_dtype)) ||
+      (gate && !known(gate_dtype)))
+    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: every type must be F32 or BF16", fn);
+  if (!resid || (y && !resid_out) || (pre_w && !next)) return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: null tensor pointer", fn);
+  if (!y && !pre_w) return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: neither y nor pre_w is given", fn);
+  if (!y && (post_w || gate || slot_to_row || topk_w))
+    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: post_w, gate, slot_to_row and topk_w need y", fn);
+  if ((slot_to_row == nullptr) != (topk_w == nullptr))
+    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: slot_to_row and topk_w come together", fn);
+  if (T < 1 || H < 8 || H % 8 != 0 || H > kNormMaxH)
+    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: need T >= 1, 8 <= H <= %d, H %% 8 == 0 (T=%d H=%d)", fn, kNormMaxH, T, H);
+  if (slot_to_row && (k < 1 || k > kMaxTopK || (int64_t)T * k >= (int64_t(1) << 31)))
+    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: need 1 <= k <= %d and T * k < 2^31 (T=%d k=%d)", fn, kMaxTopK, T, k);
+  auto rows_ok = [&](const void* p, int64_t ld) { return !p || (aligned(p, 16) && ld >= H && ld % 8 == 0); };
+  if (!rows_ok(resid, ld_r) || !rows_ok(y, ld_y) || (y && !rows_ok(resid_out, ld_ro)) || (pre_w && !rows_ok(next, ld_next)) ||
+      !aligned(post_w, 16) || !aligned(pre_w, 16))
+    return fail(NVFP4MOE_ERR_INVALID_ARG,
+                "%s: tensors must be 16-byte aligned, row distances at least H and multiples of 8", fn);
+  if (gate && (gate_row < 0 || (gate_col != 0 && gate_col != 1) ||
+               (gate_col == 1 ? !aligned(gate, 16) || gate_row % 8 != 0 || (gate_row != 0 && gate_row < H)
+                              : !aligned(gate, gate_dtype == NVFP4MOE_F32 ? 4 : 2))))
+    return fail(NVFP4MOE_ERR_INVALID_ARG,
+                "%s: gate_col must be 0 or 1 and gate_row >= 0; a gate with columns 16-byte aligned, gate_row 0 or at "
+                "least H and a multiple of 8",
+                fn);
+  BlockNormArgs a{};
+  a.resid = resid;
+  a.r_bf16 = r_dtype == NVFP4MOE_BF16;
+  a.ld_r = ld_r;
+  a.y = y;
+  a.y_bf16 = y_dtype == NVFP4MOE_BF16;
+  a.ld_y = ld_y;
+  a.slot_to_row = slot_to_row;
+  a.topk_w = topk_w;
+  a.k = k;
+  a.post_w = post_w;
+  a.pre_w = pre_w;
+  a.w_bf16 = w_dtype == NVFP4MOE_BF16;
+  a.w_offset = w_offset;
+  a.eps = eps;
+  a.scale = scale;
+  a.gate = gate;
+  a.gate_bf16 = gate_dtype == NVFP4MOE_BF16;
+  a.gate_row = gate_row;
+  a.gate_col = gate_col;
+  a.T = T;
+  a.H = H;
+  a.resid_out = resid_out;
+  a.ld_ro = ld_ro;
+  a.next = next;
+  a.ld_next = ld_next;
+  return hip_status(launch_block_norm(a, static_cast<hipStream_t>(stream)), fn);
+}

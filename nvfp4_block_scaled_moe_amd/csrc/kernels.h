@@ -199,6 +199,34 @@ int few_down_workgroups(int T, int k, int Nw, int K);
 int few_down_parts(int T, int k, int Nw, int K);
 hipError_t launch_few_layer(FewArgs up, FewArgs down, bool mx, hipStream_t stream);
 
+// ---- block_norm.hip
+constexpr int kNormMaxH = 32768;
+struct BlockNormArgs {
+  const void* resid;          // [T, H], rows ld_r apart
+  int r_bf16;                 // type of resid and resid_out
+  int64_t ld_r;
+  const void* y;              // [T, H] or [T * k, H] (slot_to_row), rows ld_y apart, or null
+  int y_bf16;
+  int64_t ld_y;
+  const int* slot_to_row;     // [T * k] or null
+  const float* topk_w;        // [T, k]
+  int k;
+  const void* post_w;         // [H] or null
+  const void* pre_w;          // [H] or null
+  int w_bf16;
+  float w_offset, eps, scale;
+  const void* gate;           // element (t, h) at t * gate_row + h * gate_col (0 or 1), or null
+  int gate_bf16;
+  int64_t gate_row;
+  int gate_col;
+  int T, H;
+  void* resid_out;            // rows ld_ro apart
+  int64_t ld_ro;
+  void* next;                 // bf16, rows ld_next apart
+  int64_t ld_next;
+};
+hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t stream);
+
 // ---- reduce.hip
 hipError_t launch_unpermute_reduce(const void* y, bool y_bf16, const int* slot_to_row,
                                    const float* topk_w, int T, int k, int H, uint16_t* out,

@@ -576,5 +576,96 @@ def moe_layer_few_mxfp4(x: torch.Tensor, logits: torch.Tensor, k: int, w13: MxTi
     return _layer_few("moe_layer_few_mxfp4", x, logits, k, w13, w2, None, None, False, out)
 
 
+# ------------------------------------------------------------------ the norms around a block
+def moe_block_norm(resid: torch.Tensor, y: torch.Tensor | None = None, *, post_w: torch.Tensor | None = None,
+                   gate: torch.Tensor | None = None, scale: float = 1.0, pre_w: torch.Tensor | None = None,
+                   w_offset: float = 0.0, eps: float = 1e-6, slot_to_row: torch.Tensor | None = None,
+                   topk_w: torch.Tensor | None = None, resid_out: torch.Tensor | None = None,
+                   next_out: torch.Tensor | None = None):
+    """The norms after and before a block with its gate and residual scale, in one launch:
+    r' = resid + scale * gate * (rms(y) * (w_offset + post_w), or y), next = bf16(rms(r') *
+    (w_offset + pre_w)). Returns (r', next), with None for what is not asked for (without ``y``
+    only next, of ``resid``; without ``pre_w`` only r').
+
+    ``resid`` float32 or bf16 [T, H]; ``y`` [T, H], or with ``slot_to_row`` and ``topk_w`` the
+    experts' rows [T*k, H]; ``post_w``, ``pre_w`` [H] (of one type); ``gate`` [H], [T, 1] or
+    [T, H]. ``resid_out`` may be ``resid``."""
+    fn = "moe_block_norm"
+    idx = _gpu(fn, resid, y, post_w, gate, pre_w, slot_to_row, topk_w, resid_out, next_out)
+    if resid.dim() != 2:
+        raise ValueError(f"{fn}: resid must be [T, H], got {tuple(resid.shape)}")
+    T, H = resid.shape
+    for t in (resid, y, gate, post_w, pre_w):
+        if t is not None and t.dtype not in _DT:
+            raise ValueError(f"{fn}: resid, y, gate and the weights must be float32 or bf16, got {t.dtype}")
+    for w in (post_w, pre_w):
+        if w is not None and w.shape != (H,):
+            raise ValueError(f"{fn}: the weights must be [{H}], got {tuple(w.shape)}")
+    if post_w is not None and pre_w is not None and post_w.dtype != pre_w.dtype:
+        post_w, pre_w = post_w.float(), pre_w.float()
+    with _on(idx):
+        resid, ld_r = _rows(fn, "resid", resid, H, 8) if resid_out is not resid else (resid, resid.stride(0))
+        post_w, pre_w = _aligned(post_w), _aligned(pre_w)
+        ld_y = k = 0
+        if y is not None:
+            y, ld_y = _rows(fn, "y", y, H, 8)
+            if topk_w is not None and slot_to_row is not None:
+                topk_w, slot_to_row = topk_w.float().contiguous(), slot_to_row.contiguous()
+                if topk_w.dim() != 2 or topk_w.shape[0] != T or slot_to_row.dtype != torch.int32 or \
+                        slot_to_row.numel() != topk_w.numel() or y.shape[0] != topk_w.numel():
+                    raise ValueError(f"{fn}: topk_w must be [{T}, k], slot_to_row int32 [{T} * k] and y [{T} * k, {H}]")
+                k = topk_w.shape[1]
+            elif y.shape[0] != T:
+                raise ValueError(f"{fn}: y must be [{T}, {H}], got {tuple(y.shape)}")
+        gate_row = gate_col = 0
+        if gate is not None:
+            if gate.shape not in ((H,), (T, 1), (T, H)):
+                raise ValueError(f"{fn}: gate must be [{H}], [{T}, 1] or [{T}, {H}], got {tuple(gate.shape)}")
+            gate, gate_row, gate_col = _gate(gate, T, H)
+        ld_ro = ld_n = 0
+        if y is not None:
+            resid_out, ld_ro = _out_rows(fn, resid_out, T, H, resid.dtype, resid.device)
+            if resid_out.dtype != resid.dtype:
+                raise ValueError(f"{fn}: resid_out must have resid's type")
+        if pre_w is not None:
+            next_out, ld_n = _out_rows(fn, next_out, T, H, torch.bfloat16, resid.device)
+            if next_out.dtype != torch.bfloat16:
+                raise ValueError(f"{fn}: next_out must be bf16")
+        wt = post_w if post_w is not None else pre_w
+        ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        st = _lib.load().moe_block_norm(
+            resid.data_ptr(), _DT[resid.dtype], ld_r, ptr(y), F32 if y is None else _DT[y.dtype], ld_y,
+            ptr(slot_to_row), ptr(topk_w), k, ptr(post_w), ptr(pre_w), F32 if wt is None else _DT[wt.dtype], w_offset,
+            eps, ptr(gate), F32 if gate is None else _DT[gate.dtype], gate_row, gate_col, scale, T, H,
+            ptr(resid_out) if y is not None else None, ld_ro, ptr(next_out) if pre_w is not None else None, ld_n,
+            torch.cuda.current_stream().cuda_stream)
+    _lib.check(fn, st)
+    return (resid_out if y is not None else None), (next_out if pre_w is not None else None)
+
+
+def _aligned(t):
+    """A contiguous 16-byte-aligned vector (the tensor itself if it is one)."""
+    if t is None or (t.is_contiguous() and t.data_ptr() % 16 == 0):
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
+def _gate(gate: torch.Tensor, T: int, H: int):
+    """(gate, row distance, column distance 0 or 1) for moe_block_norm; a copy where columns lie
+    apart or an address does not allow 16-byte reads."""
+    if gate.dim() == 1:
+        return _aligned(gate), 0, 1
+    if gate.shape[1] == 1 and H != 1:
+        return gate, (gate.stride(0) if T > 1 else 0), 0
+    row, col = gate.stride()
+    row = 0 if T == 1 else row
+    if col == 0:                        # a row's value, expanded over the columns
+        return gate, row, 0
+    if col != 1 or gate.data_ptr() % 16 or row % 8 or (row != 0 and row < H):
+        gate = gate.clone(memory_format=torch.contiguous_format)
+        row = H
+    return gate, row, 1
+
+
 def last_dispatch() -> int:
     return _lib.load().nvfp4moe_last_dispatch()
