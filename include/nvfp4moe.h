@@ -563,7 +563,7 @@ size_t moe_layer_few_mxfp4_workspace_size(int32_t T, int32_t E, int32_t k, int32
 /* ---------------------------------------------------------------------------
  * moe_block_norm -- the norms before and after a block, fused with its gate and residual scale,
  * in one launch over the T rows:
- *     u    = y                                   or, with post_w, rms(y) * (w_offset + post_w)
+ *     u    = y + y_add                           or, with post_w, rms(y + y_add) * (w_offset + post_w)
  *     r'   = resid + scale * gate * u            -> resid_out, rounded to r_dtype
  *     next = bf16( rms(r') * (w_offset + pre_w) )   with pre_w; r' in float32, not yet rounded
  * with rms(v) = v / sqrt(mean(v^2) + eps). All sums are float32.
@@ -572,8 +572,9 @@ size_t moe_layer_few_mxfp4_workspace_size(int32_t T, int32_t E, int32_t k, int32
  *   y            device [T, H] of y_dtype, rows ld_y apart; with slot_to_row and topk_w the
  *                experts' rows [T * k, H], and y_t = sum_j topk_w[t, j] y[slot_to_row[t*k+j]]
  *                as moe_unpermute_reduce sums them (without its rounding). NULL: only next is
- *                written (the norm before the first block); post_w, gate, slot_to_row are then
- *                NULL, resid_out is not used, and pre_w is needed.
+ *                written (the norm before the first block); y_add, post_w, gate, slot_to_row are
+ *                then NULL, resid_out is not used, and pre_w is needed.
+ *   y_add        device [T, H] of y_add_dtype, rows ld_ya apart (a shared expert's output), or NULL.
  *   slot_to_row, topk_w, k   device int32 [T * k], float [T, k], 1 <= k <= 64, T * k < 2^31; or
  *                both NULL.
  *   post_w, pre_w   device [H] of w_dtype (F32 or BF16), or NULL (no norm of y; no next).
@@ -586,7 +587,8 @@ size_t moe_layer_few_mxfp4_workspace_size(int32_t T, int32_t E, int32_t k, int32
  *   (gate_row: % 8 == 0 when gate_col is 1).
  * ------------------------------------------------------------------------- */
 nvfp4moe_status moe_block_norm(const void* resid, nvfp4moe_dtype r_dtype, int64_t ld_r, const void* y,
-                               nvfp4moe_dtype y_dtype, int64_t ld_y, const int32_t* slot_to_row,
+                               nvfp4moe_dtype y_dtype, int64_t ld_y, const void* y_add,
+                               nvfp4moe_dtype y_add_dtype, int64_t ld_ya, const int32_t* slot_to_row,
                                const float* topk_w, int32_t k, const void* post_w, const void* pre_w,
                                nvfp4moe_dtype w_dtype, float w_offset, float eps, const void* gate,
                                nvfp4moe_dtype gate_dtype, int64_t gate_row, int32_t gate_col, float scale,

@@ -73,8 +73,8 @@ SIGNATURES = {
     "moe_layer_few_nvfp4_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32]),
     "moe_layer_few_mxfp4": (_int, [_vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "moe_layer_few_mxfp4_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32]),
-    "moe_block_norm": (_int, [_vp, _int, _i64, _vp, _int, _i64, _vp, _vp, _i32, _vp, _vp, _int, _f32, _f32, _vp, _int,
-                              _i64, _i32, _f32, _i32, _i32, _vp, _i64, _vp, _i64, _vp]),
+    "moe_block_norm": (_int, [_vp, _int, _i64, _vp, _int, _i64, _vp, _int, _i64, _vp, _vp, _i32, _vp, _vp, _int, _f32,
+                              _f32, _vp, _int, _i64, _i32, _f32, _i32, _i32, _vp, _i64, _vp, _i64, _vp]),
     "nvfp4moe_last_error": (ctypes.c_char_p, []),
     "nvfp4moe_last_dispatch": (_int, []),
     "nvfp4moe_abi_version": (_int, []),

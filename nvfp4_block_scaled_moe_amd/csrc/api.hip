@@ -1081,7 +1081,8 @@ nvfp4moe_status moe_layer_few_mxfp4(const float* logits, const void* x, int32_t 
 
 // ------------------------------------------------------------------ the norms around a block
 extern "C" nvfp4moe_status moe_block_norm(const void* resid, nvfp4moe_dtype r_dtype, int64_t ld_r, const void* y,
-                                          nvfp4moe_dtype y_dtype, int64_t ld_y, const int32_t* slot_to_row,
+                                          nvfp4moe_dtype y_dtype, int64_t ld_y, const void* y_add,
+                                          nvfp4moe_dtype y_add_dtype, int64_t ld_ya, const int32_t* slot_to_row,
                                           const float* topk_w, int32_t k, const void* post_w, const void* pre_w,
                                           nvfp4moe_dtype w_dtype, float w_offset, float eps, const void* gate,
                                           nvfp4moe_dtype gate_dtype, int64_t gate_row, int32_t gate_col, float scale,
@@ -1089,13 +1090,13 @@ extern "C" nvfp4moe_status moe_block_norm(const void* resid, nvfp4moe_dtype r_dt
                                           int64_t ld_next, void* stream) {
   const char* fn = "moe_block_norm";
   auto known = [](nvfp4moe_dtype d) { return d == NVFP4MOE_F32 || d == NVFP4MOE_BF16; };
-  if (!known(r_dtype) || (y && !known(y_dtype)) || ((post_w || pre_w) && !known(w_dtype)) ||
+  if (!known(r_dtype) || (y && !known(y_dtype)) || (y_add && !known(y_add_dtype)) || ((post_w || pre_w) && !known(w_dtype)) ||
       (gate && !known(gate_dtype)))
     return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: every type must be F32 or BF16", fn);
   if (!resid || (y && !resid_out) || (pre_w && !next)) return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: null tensor pointer", fn);
   if (!y && !pre_w) return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: neither y nor pre_w is given", fn);
-  if (!y && (post_w || gate || slot_to_row || topk_w))
-    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: post_w, gate, slot_to_row and topk_w need y", fn);
+  if (!y && (y_add || post_w || gate || slot_to_row || topk_w))
+    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: y_add, post_w, gate, slot_to_row and topk_w need y", fn);
   if ((slot_to_row == nullptr) != (topk_w == nullptr))
     return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: slot_to_row and topk_w come together", fn);
   if (T < 1 || H < 8 || H % 8 != 0 || H > kNormMaxH)
@@ -1103,7 +1104,7 @@ extern "C" nvfp4moe_status moe_block_norm(const void* resid, nvfp4moe_dtype r_dt
   if (slot_to_row && (k < 1 || k > kMaxTopK || (int64_t)T * k >= (int64_t(1) << 31)))
     return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: need 1 <= k <= %d and T * k < 2^31 (T=%d k=%d)", fn, kMaxTopK, T, k);
   auto rows_ok = [&](const void* p, int64_t ld) { return !p || (aligned(p, 16) && ld >= H && ld % 8 == 0); };
-  if (!rows_ok(resid, ld_r) || !rows_ok(y, ld_y) || (y && !rows_ok(resid_out, ld_ro)) || (pre_w && !rows_ok(next, ld_next)) ||
+  if (!rows_ok(resid, ld_r) || !rows_ok(y, ld_y) || !rows_ok(y_add, ld_ya) || (y && !rows_ok(resid_out, ld_ro)) || (pre_w && !rows_ok(next, ld_next)) ||
       !aligned(post_w, 16) || !aligned(pre_w, 16))
     return fail(NVFP4MOE_ERR_INVALID_ARG,
                 "%s: tensors must be 16-byte aligned, row distances at least H and multiples of 8", fn);
@@ -1121,6 +1122,9 @@ extern "C" nvfp4moe_status moe_block_norm(const void* resid, nvfp4moe_dtype r_dt
   a.y = y;
   a.y_bf16 = y_dtype == NVFP4MOE_BF16;
   a.ld_y = ld_y;
+  a.y_add = y_add;
+  a.ya_bf16 = y_add_dtype == NVFP4MOE_BF16;
+  a.ld_ya = ld_ya;
   a.slot_to_row = slot_to_row;
   a.topk_w = topk_w;
   a.k = k;

@@ -3,7 +3,8 @@
 //   r'   = r + scale * gate * u
 //   next = bf16( r' / sqrt(mean(r'^2) + eps) * (o + pre_w) )                               with pre_w
 // y is the block's output, or the experts' rows with their weights: y_t = sum_j w[t, j] Y[row of
-// slot (t, j)] in ascending j (the unpermute-reduce, whose bf16 output then never exists). Without
+// slot (t, j)] in ascending j (the unpermute-reduce, whose bf16 output then never exists); y_add
+// (a shared expert's output) is added to either. Without
 // y only next is written (the norm before the first block).
 //
 // Memory-bound: y (k rows of it for the experts' form), r and a full gate are read once, r' and
@@ -106,6 +107,15 @@ __global__ __launch_bounds__(kNormMaxThreads) void block_norm_kernel(const Block
 #pragma unroll
     for (int v = 0; v < V; ++v)
       if (p.y && col[v] < H) load8(p.y, p.y_bf16, t * p.ld_y + col[v], y[v]);
+  }
+  if (p.y_add) {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (col[v] < H) {
+        load8(p.y_add, p.ya_bf16, t * p.ld_ya + col[v], r[v]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[v][i] += r[v][i];
+      }
   }
 #pragma unroll
   for (int v = 0; v < V; ++v)

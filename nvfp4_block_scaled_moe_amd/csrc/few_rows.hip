@@ -120,9 +120,12 @@ struct Decode<true> {
 // tiled scales, and the bytes taken out of it. (Whole dwords: a narrower load's zero extension
 // would be placed, and waited for, at the end of the loop body instead of at its use.)
 template <bool MX>
+__device__ __forceinline__ uint32_t scale_off(uint32_t c) {   // in a row block's tiles
+  return MX ? (c >> 4) * 1024u + (c & 12) : (c >> 3) * 1024u + 2u * (c & 6);
+}
+template <bool MX>
 __device__ __forceinline__ uint32_t scale_off(uint32_t blk, uint32_t nch, uint32_t c) {
-  if (MX) return (blk * ((nch + 15) >> 4) + (c >> 4)) * 1024u + (c & 12);
-  return (blk * ((nch + 7) >> 3) + (c >> 3)) * 1024u + 2u * (c & 6);
+  return blk * (MX ? (nch + 15) >> 4 : (nch + 7) >> 3) * 1024u + scale_off<MX>(c);
 }
 template <bool MX>
 __device__ __forceinline__ uint32_t scale_of(uint32_t dword, uint32_t c) {
@@ -175,12 +178,17 @@ __device__ __forceinline__ float row_unscale(uint32_t top) { return __uint_as_fl
 // Largest magnitude below `end` of eight bf16 values, as bf16 bits (0x7f80: of the finite ones,
 // 0x7f81: Inf counts).
 __device__ __forceinline__ uint32_t top_of(const u32x4& v, uint32_t end) {
-  uint32_t t = 0;
+  u16x2 m = __builtin_bit_cast(u16x2, v[0] & 0x7fff7fffu);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = v[i] & 0x7fffu, hi = (v[i] >> 16) & 0x7fffu;
-    t = max(t, lo < end ? lo : 0u);
-    t = max(t, hi < end ? hi : 0u);
+  for (int i = 1; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[i] & 0x7fff7fffu));
+  uint32_t t = max((uint32_t)m[0], (uint32_t)m[1]);
+  if (__ballot(t >= end)) {   // some are not to be counted
+    t = 0;
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t w = i < 4 ? (i < 2 ? v[0] : v[1]) : (i < 6 ? v[2] : v[3]);
+      const uint32_t a = (i & 1 ? w >> 16 : w) & 0x7fffu;
+      t = max(t, a < end ? a : 0u);
+    }
   }
   return t;
 }
@@ -234,12 +242,27 @@ __device__ __forceinline__ void put_matvec(const FewArgs& p, int col, size_t n0,
     static_cast<float*>(p.out)[o] = v;
 }
 
+// An even split of `total` things over n takers, the first `more` of them with one more. In 32
+// bits: the kernels run this code once, from a cold instruction cache, and its length is time
+// (about 2 bytes a nanosecond before the first tile).
+struct Share {
+  uint32_t each, more;
+  __device__ __forceinline__ Share(uint32_t total, uint32_t n) : each(total / n), more(total - total / n * n) {}
+  __device__ __forceinline__ uint32_t begin(uint32_t i) const { return i * each + (i < more ? i : more); }
+  // The taker of thing x.
+  __device__ __forceinline__ uint32_t taker(uint32_t x) const {
+    const uint32_t edge = more * (each + 1);
+    return x < edge ? x / (each + 1) : more + (x - edge) / each;
+  }
+};
+
 // ------------------------------------------------------------------ resident rows: matvec, and the layer's first launch
 // The rows (the item's, or all of them once when they fit) stay in LDS as matrix operands, f16
 // with one power of two a row (NVFP4) or bf16 (MXFP4): turned once, they serve every tile of
 // the item. Waves deal out the chunks ks at a time (ks = 1 .. 16: kW / ks groups of
 // waves, each with RB row blocks of its own).
-constexpr int pass_batch(bool fp8) { return fp8 ? 2 : 4; }   // pieces a thread requests together
+// 16-byte pieces of the rows a thread requests together: one row seldom has more than one for each.
+constexpr int pass_batch(int ntok) { return ntok > 4 ? 4 : 1; }
 
 template <bool MX, bool LAYER, bool FP8, bool SWIGLU, int NTOK, int RB, int D>
 __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
@@ -249,7 +272,7 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
   static_assert(!LAYER || (SWIGLU && NTOK == kItemTok), "the layer's items");
   static_assert(!FP8 || (LAYER && !MX), "FP8 activations: the NVFP4 layer");
   constexpr int BUF = NTOK > 4 ? 1 : 2;
-  constexpr int kPassBatch = pass_batch(FP8);
+  constexpr int kPassBatch = pass_batch(NTOK);
   constexpr int REDF = kW * RB * NTOK * 16;
   extern __shared__ __attribute__((aligned(16))) unsigned char s_rows[];   // [rows][K128 * 2 + 16]
   __shared__ __attribute__((aligned(16))) float s_red[BUF][REDF];
@@ -478,9 +501,8 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
   // ---- this workgroup's tiles, in runs of one item's: a flat sequence of steps (a chunk of RB
   // weight tiles), D of them a turn of the ring. A tile takes at least D steps, so that at most
   // one is completed in a turn; a run is padded to whole turns.
-  const int64_t ntiles = (int64_t)nitems * tpi;
-  const int t0 = (int)(ntiles * blockIdx.x / gridDim.x);
-  const int t1 = (int)(ntiles * (blockIdx.x + 1) / gridDim.x);
+  const Share share((uint32_t)nitems * (uint32_t)tpi, gridDim.x);
+  const int t0 = (int)share.begin(blockIdx.x), t1 = (int)share.begin(blockIdx.x + 1);
   if (t0 >= t1) return;   // fewer tiles than workgroups
 
   __amdgpu_buffer_rsrc_t wr, sr;
@@ -490,6 +512,10 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
   const int spt = cpw > D ? cpw : D;   // steps of a tile
   // The loads' position: the item, its row block group and chunk, and the steps left of the run.
   int it_l = t0 / tpi, tile_l = t0 - it_l * tpi, tiles_l = t1 - t0, sub_l = 0, step_l = 0, steps_l = 0;
+  uint32_t c_l = 0, woff_l = 0, soff_l = 0;   // chunk; offsets of the group's first block
+  const uint32_t wrow = nch * 1024u, srow = (MX ? (nch + 15) >> 4 : (nch + 7) >> 3) * 1024u;   // of a row block
+  constexpr uint32_t NS = SWIGLU ? 1 : RB;      // a group's blocks (gate or up ones, or all)
+  const uint32_t next = SWIGLU ? nblk / 2 : 1;  // from a group's first block to its second
   auto open_run = [&]() {
     const size_t e = LAYER ? item_word(it_l) >> 16 : 0;
     wr = make_rsrc(p.codes + e * wbytes, wbytes);
@@ -499,25 +525,30 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
     steps_l = n * spt;
     sub_l = tile_l * RG + rg;
     step_l = 0;
+    c_l = (uint32_t)ksl;
+    woff_l = (uint32_t)sub_l * NS * wrow;
+    soff_l = (uint32_t)sub_l * NS * srow;
     tile_l = 0;
     ++it_l;
   };
   u32x4 wring[D][RB];
   uint32_t sring[D][RB];
   auto issue = [&](int d) {
-    const uint32_t c = (uint32_t)(ksl + (step_l << p.ks_log));
-    const bool ok = steps_l > 0 && step_l < cpw && c < nch && sub_l < nsub;
+    const bool ok = steps_l > 0 && c_l < nch && sub_l < nsub;
+    const uint32_t wo = woff_l + c_l * 1024u, so = soff_l + scale_off<MX>(c_l);
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
-      const uint32_t blk = tile_block<SWIGLU, RB>((uint32_t)sub_l, b, nblk);
-      const bool in = ok && (SWIGLU || blk < nblk);
-      wring[d][b] = ld128(wr, settled(16u * lane + (in ? (blk * nch + c) * 1024u : kOOB)), 0);
-      sring[d][b] = ld32(sr, settled(16u * lane + (in ? scale_off<MX>(blk, nch, c) : kOOB)));
+      const bool in = ok && (SWIGLU || b == 0 || (uint32_t)sub_l * RB + b < nblk);
+      wring[d][b] = ld128(wr, settled(16u * lane + (in ? wo + b * next * wrow : kOOB)), 0);
+      sring[d][b] = ld32(sr, settled(16u * lane + (in ? so + b * next * srow : kOOB)));
     }
     // (arithmetic instead of branches: a branch here would send the position through memory)
-    const int wrap = step_l + 1 == spt ? 1 : 0;
+    const bool wrap = step_l + 1 == spt;
     step_l = wrap ? 0 : step_l + 1;
-    sub_l += wrap * RG;
+    c_l = wrap ? (uint32_t)ksl : c_l + (uint32_t)KS;
+    sub_l += wrap ? RG : 0;
+    woff_l += wrap ? (uint32_t)RG * NS * wrow : 0u;
+    soff_l += wrap ? (uint32_t)RG * NS * srow : 0u;
     --steps_l;
   };
 
@@ -548,7 +579,7 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
     __syncthreads();
   }
   if constexpr (LAYER) {
-    if (blockIdx.x == gridDim.x - 1) write_plan();   // (this workgroup always has a tile)
+    if (blockIdx.x == 0) write_plan();   // (the first workgroup always has a tile)
   }
 
   f32x4 tot[RB];
@@ -587,12 +618,12 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
     const int run = min(left, tpi - tile), nst = run * spt, turns = (nst + D - 1) / D;
     left -= run;
     int step = 0, sub = tile * RG + rg;
+    uint32_t c = (uint32_t)ksl;
     for (int turn = 0; turn < turns; ++turn) {
       int ready = 0;
 #pragma unroll
       for (int d = 0; d < D; ++d) {
-        const uint32_t c = (uint32_t)(ksl + (step << p.ks_log));
-        if (turn * D + d < nst && step < cpw && c < nch && sub < nsub) {
+        if (turn * D + d < nst && c < nch && sub < nsub) {
           Op bf[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) bf[j] = *reinterpret_cast<const Op*>(s_rows + frow + c * 256u + 16 * j);
@@ -605,9 +636,10 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
           }
         }
         issue(d);
-        const int wrap = step + 1 == spt ? 1 : 0;
+        const bool wrap = step + 1 == spt;
         step = wrap ? 0 : step + 1;
-        sub += wrap * RG;
+        c = wrap ? (uint32_t)ksl : c + (uint32_t)KS;
+        sub += wrap ? RG : 0;
         if (wrap && turn * D + d < nst) {   // a tile is complete: this wave's sums
           ready = 1;
           if (l16 < NTOK) {
@@ -625,11 +657,13 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
         __syncthreads();
         const float* red = s_red[buf];
         constexpr int NB = SWIGLU ? 1 : RB;
-        const int total = RG * NB * ncol * 16;
+        const int lcol = ncol > 1 ? 32 - __builtin_clz(ncol - 1) : 0;   // columns, to a power of two
+        const int total = (RG * NB * 16) << lcol;
         // a different wave starts each tile, so that short epilogues spread over the SIMDs
         for (int i = (tid + kWave * done) & (kNT - 1); i < total; i += kNT) {
           const int r16 = i & 15, q = i >> 4;
-          const int grp = q / (NB * ncol), b = (q / ncol) % NB, col = q % ncol;
+          const int grp = (q >> lcol) / NB, b = (q >> lcol) % NB, col = q & ((1 << lcol) - 1);
+          if (col >= ncol) continue;   // (16 lanes at a time)
           const int osub = tile * RG + grp;
           float v = 0.0f, u = 0.0f;
           // (the waves' values are requested four at a time; what is past KS is not added)
@@ -827,9 +861,6 @@ __global__ __launch_bounds__(kLongNT, WPS) void few_long_kernel(const FewArgs p)
 // same number of bytes, which whole tiles seldom give (192 tiles on 256 CUs: three quarters of
 // the rate). A tile that several workgroups have part of is finished by the last of them to
 // arrive, which adds the parts in order; nobody waits.
-// Sequence positions of workgroup i of n: [i W / n, (i + 1) W / n) of W. The one that holds x:
-__device__ __forceinline__ int part_of(int64_t x, int64_t n, int64_t W) { return (int)(((x + 1) * n - 1) / W); }
-
 template <bool MX, int D>
 __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
   typedef Decode<MX> Dec;
@@ -885,16 +916,17 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
   const int nitems = __builtin_amdgcn_readfirstlane(listed);
   __syncthreads();
 
-  // This workgroup's part of the sequence.
-  const int64_t P = (int64_t)nitems * nch, ntile = nblk / RB, Wk = P * ntile;
-  int64_t n = Wk / kDownLeast;   // workgroups that take part: not fewer than there are tiles
+  // This workgroup's part of the sequence. (At most 1024 items x 256 chunks x 1024 tiles.)
+  const uint32_t P = (uint32_t)nitems * nch, ntile = nblk / RB, Wk = P * ntile;
+  uint32_t n = Wk / kDownLeast;   // workgroups that take part: not fewer than there are tiles
   n = n < ntile ? ntile : n;
-  n = n < (int64_t)gridDim.x ? n : (int64_t)gridDim.x;
-  if ((int64_t)blockIdx.x >= n) return;
-  const int64_t x0 = blockIdx.x * Wk / n, x1 = (blockIdx.x + 1) * Wk / n;
+  n = n < gridDim.x ? n : gridDim.x;
+  if (blockIdx.x >= n) return;
+  const Share share(Wk, n);
+  const uint32_t x0 = share.begin(blockIdx.x);
   int tile = (int)(x0 / P);
-  int q0 = (int)(x0 - tile * P);
-  int64_t left = x1 - x0;
+  int q0 = (int)(x0 - (uint32_t)tile * P);
+  int left = (int)(share.begin(blockIdx.x + 1) - x0);
 
   const __amdgpu_buffer_rsrc_t hr = make_rsrc(p.h, (uint32_t)S * (uint32_t)F * 2u);
   const __amdgpu_buffer_rsrc_t er = make_rsrc(p.hexp, (uint32_t)S * nch * 8u);
@@ -968,7 +1000,7 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
   unsigned char* row = s_row[wave];
   const int per = RB * 16 * T;   // values of a tile
   for (;;) {
-    const int m = (int)(left < P - q0 ? left : P - q0);   // pairs of this tile
+    const int m = min(left, (int)P - q0);   // pairs of this tile
     left -= m;
     open_tile(q0, m);
     const int nst = run_l, turns = ((m + kW - 1) / kW + D - 1) / D;
@@ -1026,7 +1058,8 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
 #pragma unroll
     for (int b = 0; b < RB; ++b) *reinterpret_cast<f32x4*>(&s_red[wave * RB + b][l16 * 16 + 4 * g]) = tot[b];
     __syncthreads();
-    const int part0 = part_of(tile * P, n, Wk), parts = part_of((tile + 1) * P - 1, n, Wk) - part0 + 1;
+    const int part0 = (int)share.taker((uint32_t)tile * P);
+    const int parts = m == (int)P ? 1 : (int)share.taker((uint32_t)tile * P + P - 1) - part0 + 1;
     float* mine = p.part + ((size_t)tile * p.most_parts + (blockIdx.x - part0)) * per;
     auto put = [&](int i, float v) {
       const int r16 = i & 15, q = i >> 4, b = q / T, t = q - b * T;
@@ -1102,6 +1135,16 @@ hipError_t launch_up(FewArgs a, int rows, int grid, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Depth of the ring: 4, and 2 where a wave has one or two chunks of a tile (a turn's code is then
+// half as long, and a tile always takes a turn).
+bool short_tiles(const FewArgs& a) { return (nch_of(a.K) - 1) >> a.ks_log < 2; }
+
+template <bool MX, bool FP8>
+hipError_t launch_layer_up(const FewArgs& a, int rows, int grid, hipStream_t stream) {
+  return short_tiles(a) ? launch_up<MX, true, FP8, true, kItemTok, 2, 2>(a, rows, grid, stream)
+                        : launch_up<MX, true, FP8, true, kItemTok, 2, 4>(a, rows, grid, stream);
+}
+
 template <bool MX, bool SWIGLU, int NTOK, int RB, int D>
 hipError_t launch_mv(const FewArgs& a, hipStream_t stream) {
   const int nblk = a.Nw / 16, rg = kW >> a.ks_log;
@@ -1121,7 +1164,9 @@ hipError_t launch_long(const FewArgs& a, hipStream_t stream) {
 template <bool MX, bool SWIGLU>
 hipError_t launch_mv_rows(const FewArgs& a, hipStream_t stream) {
   if (a.T <= resident_rows(a.K))
-    return a.T <= 4 ? launch_mv<MX, SWIGLU, 4, 2, 4>(a, stream) : launch_mv<MX, SWIGLU, 16, 2, 4>(a, stream);
+    return a.T > 4          ? launch_mv<MX, SWIGLU, 16, 2, 4>(a, stream)
+           : short_tiles(a) ? launch_mv<MX, SWIGLU, 4, 2, 2>(a, stream)
+                            : launch_mv<MX, SWIGLU, 4, 2, 4>(a, stream);
   if (a.Nw / 16 >= 8 * 256) return launch_long<MX, SWIGLU, 8, 1, 2>(a, stream);
   return launch_long<MX, SWIGLU, 2, 2, 4>(a, stream);
 }
@@ -1153,9 +1198,9 @@ hipError_t launch_few_layer(FewArgs up, FewArgs down, bool mx, hipStream_t strea
   const int64_t tiles = (int64_t)up.T * up.k * ((nsub + rg - 1) / rg);   // bound: every slot an item
   const int grid = tiles < kGrid ? (int)tiles : kGrid;
   const int rows = up.T < up.item_tok ? up.T : up.item_tok;
-  const hipError_t e = mx       ? launch_up<true, true, false, true, kItemTok, 2, 4>(up, rows, grid, stream)
-                       : up.fp8 ? launch_up<false, true, true, true, kItemTok, 2, 4>(up, rows, grid, stream)
-                                : launch_up<false, true, false, true, kItemTok, 2, 4>(up, rows, grid, stream);
+  const hipError_t e = mx       ? launch_layer_up<true, false>(up, rows, grid, stream)
+                       : up.fp8 ? launch_layer_up<false, true>(up, rows, grid, stream)
+                                : launch_layer_up<false, false>(up, rows, grid, stream);
   if (e != hipSuccess) return e;
   const int wgs = few_down_workgroups(down.T, down.k, down.Nw, down.K);
   if (mx)

@@ -208,6 +208,9 @@ struct BlockNormArgs {
   const void* y;              // [T, H] or [T * k, H] (slot_to_row), rows ld_y apart, or null
   int y_bf16;
   int64_t ld_y;
+  const void* y_add;          // [T, H] added to y, rows ld_ya apart, or null
+  int ya_bf16;
+  int64_t ld_ya;
   const int* slot_to_row;     // [T * k] or null
   const float* topk_w;        // [T, k]
   int k;

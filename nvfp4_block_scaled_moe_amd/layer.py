@@ -1,4 +1,5 @@
-"""The MoE layer as a sequence of C ABI calls (route -> up/gate + SwiGLU -> down -> reduce).
+"""The MoE layer as a sequence of C ABI calls (route -> up/gate + SwiGLU -> down -> reduce), the
+layer of a few tokens as one call, and the block around it (shared expert, norms, residual).
 
 This module only sequences the library calls and allocates their outputs with torch; all
 arithmetic runs in the HIP kernels behind include/nvfp4moe.h.
@@ -63,12 +64,13 @@ def quantize_experts(wl: inputs.Workload, device="cuda", experts=None) -> NVFP4E
 
 
 def moe_forward(x: torch.Tensor, logits: torch.Tensor, k: int, w: NVFP4Experts, mode: int = ops.W4A16,
-                fp8_acts: bool = False, keep: bool = False, combine: bool = False):
+                fp8_acts: bool = False, keep: bool = False, combine: bool = False, reduce: bool = True):
     """One MoE layer forward. ``x`` bf16 [T, H]; ``logits`` f32 [T, E].
 
     Returns the bf16 output [T, H]; with ``keep`` a dict of every stage's tensors. With
     ``combine`` the down GEMM and the weighted reduce run as one call
-    (moe_grouped_gemm_nvfp4_combine; same output bits, no Y in the stages).
+    (moe_grouped_gemm_nvfp4_combine; same output bits, no Y in the stages). Without ``reduce``
+    the experts' rows are returned unsummed: (Y f32 [T*k, H], slot_to_row, topk_w).
     """
     st = {}
     T = x.shape[0]
@@ -113,6 +115,8 @@ def moe_forward(x: torch.Tensor, logits: torch.Tensor, k: int, w: NVFP4Experts, 
         else:
             y = ops.moe_grouped_gemm_nvfp4(ops.W4A4, ops.EPI_NONE, hq, w.w2_t,
                                            a_scales=hs, a_g=hg, rows=S, out_dtype=torch.float32, **common)
+    if not reduce and not combine:
+        return y, r["slot_to_row"], r["topk_w"]
     if not combine:
         out = ops.moe_unpermute_reduce(y, r["slot_to_row"], r["topk_w"])
     if keep:
@@ -157,11 +161,11 @@ def quantize_experts_mxfp4(wl: inputs.Workload, device="cuda") -> MXFP4Experts:
 
 
 def moe_forward_mxfp4(x: torch.Tensor, logits: torch.Tensor, k: int, w: MXFP4Experts,
-                      keep: bool = False, combine: bool = False):
+                      keep: bool = False, combine: bool = False, reduce: bool = True):
     """One MoE layer forward in MXFP4 W4A4: token rows and h are MXFP4-quantized (one UE8M0
     scale per 32 elements, no per-tensor scale, so the up/gate GEMM's epilogue writes h as
     MXFP4 directly); both GEMMs run on the scaled FP4 matrix cores. ``x`` bf16 [T, H];
-    ``logits`` f32 [T, E]."""
+    ``logits`` f32 [T, E]. ``reduce`` as for moe_forward."""
     st = {}
     r = ops.moe_route_permute(logits, k)
     st.update(r)
@@ -176,8 +180,85 @@ def moe_forward_mxfp4(x: torch.Tensor, logits: torch.Tensor, k: int, w: MXFP4Exp
                                                  slot_to_row=r["slot_to_row"], topk_w=r["topk_w"], **common)
     else:
         y = ops.moe_grouped_gemm_mxfp4(ops.EPI_NONE, hq, hs, w.w2_t, rows=S, out_dtype=torch.float32, **common)
+        if not reduce:
+            return y, r["slot_to_row"], r["topk_w"]
         out = ops.moe_unpermute_reduce(y, r["slot_to_row"], r["topk_w"])
     if keep:
         st.update(xq=xq, xs=xs, hq=hq, hs=hs, out=out, **({} if combine else dict(y=y)))
         return out, st
     return out
+
+
+# ------------------------------------------------------------------ a few tokens, and the block
+#: rows up to which the few-row calls run (nvfp4_matvec, moe_layer_few_nvfp4 and their MXFP4 forms)
+FEW_TOKENS = 16
+
+
+def moe_forward_few(x: torch.Tensor, logits: torch.Tensor, k: int, w: NVFP4Experts | MXFP4Experts,
+                    fp8_acts: bool = False):
+    """The MoE layer of up to 16 tokens in two launches, with 16-bit activations (after the FP8
+    round trip with ``fp8_acts``, NVFP4 only) for either weight format -> bf16 [T, H]."""
+    if isinstance(w, MXFP4Experts):
+        if fp8_acts:
+            raise ValueError("moe_forward_few: fp8_acts goes with NVFP4 experts")
+        return ops.moe_layer_few_mxfp4(x, logits, k, w.w13_t, w.w2_t)
+    return ops.moe_layer_few_nvfp4(x, logits, k, w.w13_t, w.w2_t, fp8_acts=fp8_acts)
+
+
+@dataclass
+class SharedExpert:
+    """A SwiGLU expert that every token goes through: one tiled matrix [2F, H] (gate rows first)
+    and one [H, F], both NVFP4 or both MXFP4."""
+    w13: ops.TiledWeights | ops.MxTiledWeights
+    w2: ops.TiledWeights | ops.MxTiledWeights
+
+
+def shared_expert_forward(x: torch.Tensor, w: SharedExpert, add: torch.Tensor | None = None):
+    """f32 [T, H] of the shared expert for bf16 rows ``x`` [T, H]: two few-row products up to 16
+    rows, the second adding ``add`` (the routed experts' output); dense grouped GEMMs above
+    (NVFP4 with 16-bit activations, MXFP4 with MXFP4 ones), where ``add`` is not taken."""
+    T = x.shape[0]
+    nv = isinstance(w.w13, ops.TiledWeights)
+    if T <= FEW_TOKENS:
+        mv = ops.nvfp4_matvec if nv else ops.mxfp4_matvec
+        return mv(mv(x, w.w13, ops.EPI_SWIGLU), w.w2, add=add, out_dtype=torch.float32)
+    if add is not None:
+        raise ValueError(f"shared_expert_forward: add is taken up to {FEW_TOKENS} rows")
+    i32 = dict(dtype=torch.int32, device=x.device)
+    dense = dict(expert_offsets=torch.arange(0, 2 * T, T, **i32), active_experts=torch.zeros((1,), **i32),
+                 n_active=torch.ones((1,), **i32))
+    if nv:
+        h = ops.moe_grouped_gemm_nvfp4(ops.W4A16, ops.EPI_SWIGLU, x, w.w13, **dense)
+        return ops.moe_grouped_gemm_nvfp4(ops.W4A16, ops.EPI_NONE, h, w.w2, out_dtype=torch.float32, **dense)
+    hq, hs = ops.moe_grouped_gemm_mxfp4_swiglu_q(*ops.mxfp4_quantize(x), w.w13, **dense)
+    return ops.moe_grouped_gemm_mxfp4(ops.EPI_NONE, hq, hs, w.w2, out_dtype=torch.float32, **dense)
+
+
+def moe_block_forward(resid: torch.Tensor, x: torch.Tensor, k: int, w: NVFP4Experts | MXFP4Experts, router, *,
+                      shared: SharedExpert | None = None, post_w: torch.Tensor | None = None,
+                      gate: torch.Tensor | None = None, scale: float = 1.0, pre_w: torch.Tensor | None = None,
+                      w_offset: float = 0.0, eps: float = 1e-6, fp8_acts: bool = False):
+    """One MoE block and the norms around it: logits = ``router``(x), y = the routed experts (and
+    the ``shared`` one), then moe_block_norm's r' = resid + scale * gate * (post-norm of y) and
+    the next block's normed input. ``x`` bf16 [T, H] is this block's normed input: the next
+    of the call before, or ``ops.moe_block_norm(resid, pre_w=...)[1]`` at the start.
+
+    Up to 16 tokens the layer runs as two launches and the shared expert as two more; above, the
+    experts' rows go unsummed into the norm, which adds the shared expert's output. Returns
+    (r', next); next is None without ``pre_w``."""
+    T = x.shape[0]
+    logits = router(x)
+    norm = dict(post_w=post_w, gate=gate, scale=scale, pre_w=pre_w, w_offset=w_offset, eps=eps)
+    if T <= FEW_TOKENS:
+        y = moe_forward_few(x, logits, k, w, fp8_acts)
+        if shared is not None:
+            y = shared_expert_forward(x, shared, add=y)
+        return ops.moe_block_norm(resid, y, **norm)
+    if isinstance(w, MXFP4Experts):
+        if fp8_acts:
+            raise ValueError("moe_block_forward: fp8_acts goes with NVFP4 experts")
+        y, slot_to_row, topk_w = moe_forward_mxfp4(x, logits, k, w, reduce=False)
+    else:
+        y, slot_to_row, topk_w = moe_forward(x, logits, k, w, fp8_acts=fp8_acts, reduce=False)
+    ys = None if shared is None else shared_expert_forward(x, shared)
+    return ops.moe_block_norm(resid, y, slot_to_row=slot_to_row, topk_w=topk_w, y_add=ys, **norm)

@@ -445,16 +445,18 @@ def moe_grouped_gemm_mxfp8(epi: int, a: torch.Tensor, a_scales: torch.Tensor, w:
 
 
 # ------------------------------------------------------------------ a few rows
+# These calls run for a few microseconds each, so what the binding does around them counts: the
+# stream comes as a raw handle (2.5 us less than the Stream object) and pointers go as integers.
 _NO_GUARD = contextlib.nullcontext()
 
 
 def _gpu(fn: str, *ts) -> int:
     """Index of the GPU that holds every given tensor (None entries aside)."""
-    dev = ts[0].device
+    index = ts[0].get_device()
     for t in ts:
-        if t is not None and (t.device != dev or not t.is_cuda):
+        if t is not None and (t.get_device() != index or index < 0):
             raise ValueError(f"{fn}: all tensors must be on one GPU")
-    return dev.index
+    return index
 
 
 def _on(index: int):
@@ -462,11 +464,18 @@ def _on(index: int):
     return _NO_GUARD if torch.cuda.current_device() == index else torch.cuda.device(index)
 
 
+def _raw_stream(index: int) -> int:
+    """Handle of the GPU's current stream."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 def _rows(fn: str, what: str, t: torch.Tensor, n: int, align: int = 1):
     """(t, row distance): a 2-D tensor [rows, n] whose rows are contiguous, in place if its
     row distance and address allow, else as a contiguous copy."""
     if t.dim() != 2 or t.shape[1] != n:
         raise ValueError(f"{fn}: {what} must be [rows, {n}], got {tuple(t.shape)}")
+    if t.is_contiguous() and t.data_ptr() % (align * t.element_size()) == 0:
+        return t, n
     one = t.shape[0] <= 1
     if t.stride(1) != 1 or (not one and (t.stride(0) < n or t.stride(0) % align)) or \
             t.data_ptr() % (align * t.element_size()):
@@ -476,10 +485,11 @@ def _rows(fn: str, what: str, t: torch.Tensor, n: int, align: int = 1):
     return t, (n if one or t.is_contiguous() else t.stride(0))
 
 
-def _out_rows(fn: str, out, T: int, n: int, dtype, device):
-    """(out, row distance) of an output [T, n]: allocated, or the caller's with contiguous rows."""
+def _out_rows(fn: str, out, T: int, n: int, dtype, like):
+    """(out, row distance) of an output [T, n]: allocated where ``like`` is, or the caller's
+    with contiguous rows."""
     if out is None:
-        return torch.empty((T, n), dtype=dtype, device=device), n
+        return like.new_empty((T, n), dtype=dtype), n
     if out.shape != (T, n) or out.dtype not in _DT or (n > 1 and out.stride(1) != 1) or \
             (T > 1 and out.stride(0) < n):
         raise ValueError(f"{fn}: out must be float32 or bf16 [{T}, {n}] with contiguous rows")
@@ -504,9 +514,9 @@ def _matvec(fn: str, x, w, epi, add, out_dtype, out, g):
             raise ValueError(f"{fn}: add must be [{T}, {n}], got {tuple(add.shape)}")
         add, ld_add = _rows(fn, "add", add, n)
     with _on(idx):
-        out, ld_out = _out_rows(fn, out, T, n, out_dtype, x.device)
+        out, ld_out = _out_rows(fn, out, T, n, out_dtype, x)
         rest = (Nw, K, None if add is None else add.data_ptr(), F32 if add is None else _DT[add.dtype], ld_add,
-                out.data_ptr(), _DT[out.dtype], ld_out, torch.cuda.current_stream().cuda_stream)
+                out.data_ptr(), _DT[out.dtype], ld_out, _raw_stream(idx))
         lib = _lib.load()
         head = (epi, x.data_ptr(), ldx, T, w.codes.data_ptr(), w.scales.data_ptr())
         st = lib.nvfp4_matvec(*head, g.data_ptr(), *rest) if g is not None else lib.mxfp4_matvec(*head, *rest)
@@ -536,7 +546,8 @@ def _layer_few(fn: str, x, logits, k, w13, w2, g13, g2, fp8_acts, out):
         raise ValueError(f"{fn}: weights [{w13.B}, {w13.R}, {w13.C}] and [{w2.B}, {w2.R}, {w2.C}] do not fit "
                          f"logits [T, {E}] and x [T, {H}]")
     idx = _gpu(fn, x, logits, w13.codes, w13.scales, w2.codes, w2.scales, g13, g2, out)
-    logits = logits.contiguous().float()
+    if logits.dtype != torch.float32 or not logits.is_contiguous():
+        logits = logits.contiguous().float()
     x, ldx = _rows(fn, "x", x, H, 8)
     if ldx != H:
         x = x.contiguous()
@@ -545,16 +556,16 @@ def _layer_few(fn: str, x, logits, k, w13, w2, g13, g2, fp8_acts, out):
     lib = _lib.load()
     with _on(idx):
         if out is None:
-            out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
-        stream = torch.cuda.current_stream().cuda_stream
+            out = torch.empty_like(x)
+        stream = _raw_stream(idx)
         if g13 is not None:
-            ws = _ws(lib.moe_layer_few_nvfp4_workspace_size(T, E, k, H, F), x.device)
+            ws = x.new_empty((lib.moe_layer_few_nvfp4_workspace_size(T, E, k, H, F),), dtype=torch.uint8)
             st = lib.moe_layer_few_nvfp4(logits.data_ptr(), x.data_ptr(), T, E, k, H, F, int(fp8_acts),
                                          w13.codes.data_ptr(), w13.scales.data_ptr(), g13.data_ptr(),
                                          w2.codes.data_ptr(), w2.scales.data_ptr(), g2.data_ptr(), out.data_ptr(),
                                          ws.data_ptr(), ws.numel(), stream)
         else:
-            ws = _ws(lib.moe_layer_few_mxfp4_workspace_size(T, E, k, H, F), x.device)
+            ws = x.new_empty((lib.moe_layer_few_mxfp4_workspace_size(T, E, k, H, F),), dtype=torch.uint8)
             st = lib.moe_layer_few_mxfp4(logits.data_ptr(), x.data_ptr(), T, E, k, H, F, w13.codes.data_ptr(),
                                          w13.scales.data_ptr(), w2.codes.data_ptr(), w2.scales.data_ptr(),
                                          out.data_ptr(), ws.data_ptr(), ws.numel(), stream)
@@ -580,24 +591,24 @@ def moe_layer_few_mxfp4(x: torch.Tensor, logits: torch.Tensor, k: int, w13: MxTi
 def moe_block_norm(resid: torch.Tensor, y: torch.Tensor | None = None, *, post_w: torch.Tensor | None = None,
                    gate: torch.Tensor | None = None, scale: float = 1.0, pre_w: torch.Tensor | None = None,
                    w_offset: float = 0.0, eps: float = 1e-6, slot_to_row: torch.Tensor | None = None,
-                   topk_w: torch.Tensor | None = None, resid_out: torch.Tensor | None = None,
-                   next_out: torch.Tensor | None = None):
+                   topk_w: torch.Tensor | None = None, y_add: torch.Tensor | None = None,
+                   resid_out: torch.Tensor | None = None, next_out: torch.Tensor | None = None):
     """The norms after and before a block with its gate and residual scale, in one launch:
     r' = resid + scale * gate * (rms(y) * (w_offset + post_w), or y), next = bf16(rms(r') *
     (w_offset + pre_w)). Returns (r', next), with None for what is not asked for (without ``y``
     only next, of ``resid``; without ``pre_w`` only r').
 
     ``resid`` float32 or bf16 [T, H]; ``y`` [T, H], or with ``slot_to_row`` and ``topk_w`` the
-    experts' rows [T*k, H]; ``post_w``, ``pre_w`` [H] (of one type); ``gate`` [H], [T, 1] or
+    experts' rows [T*k, H]; ``y_add`` [T, H] is added to it (a shared expert); ``post_w``, ``pre_w`` [H] (of one type); ``gate`` [H], [T, 1] or
     [T, H]. ``resid_out`` may be ``resid``."""
     fn = "moe_block_norm"
-    idx = _gpu(fn, resid, y, post_w, gate, pre_w, slot_to_row, topk_w, resid_out, next_out)
+    idx = _gpu(fn, resid, y, post_w, gate, pre_w, slot_to_row, topk_w, y_add, resid_out, next_out)
     if resid.dim() != 2:
         raise ValueError(f"{fn}: resid must be [T, H], got {tuple(resid.shape)}")
     T, H = resid.shape
-    for t in (resid, y, gate, post_w, pre_w):
+    for t in (resid, y, y_add, gate, post_w, pre_w):
         if t is not None and t.dtype not in _DT:
-            raise ValueError(f"{fn}: resid, y, gate and the weights must be float32 or bf16, got {t.dtype}")
+            raise ValueError(f"{fn}: resid, y, y_add, gate and the weights must be float32 or bf16, got {t.dtype}")
     for w in (post_w, pre_w):
         if w is not None and w.shape != (H,):
             raise ValueError(f"{fn}: the weights must be [{H}], got {tuple(w.shape)}")
@@ -606,11 +617,17 @@ def moe_block_norm(resid: torch.Tensor, y: torch.Tensor | None = None, *, post_w
     with _on(idx):
         resid, ld_r = _rows(fn, "resid", resid, H, 8) if resid_out is not resid else (resid, resid.stride(0))
         post_w, pre_w = _aligned(post_w), _aligned(pre_w)
-        ld_y = k = 0
+        ld_y = ld_ya = k = 0
+        if y_add is not None:
+            y_add, ld_ya = _rows(fn, "y_add", y_add, H, 8)
+            if y_add.shape[0] != T:
+                raise ValueError(f"{fn}: y_add must be [{T}, {H}], got {tuple(y_add.shape)}")
         if y is not None:
             y, ld_y = _rows(fn, "y", y, H, 8)
             if topk_w is not None and slot_to_row is not None:
-                topk_w, slot_to_row = topk_w.float().contiguous(), slot_to_row.contiguous()
+                if topk_w.dtype != torch.float32 or not topk_w.is_contiguous():
+                    topk_w = topk_w.float().contiguous()
+                slot_to_row = slot_to_row.contiguous()
                 if topk_w.dim() != 2 or topk_w.shape[0] != T or slot_to_row.dtype != torch.int32 or \
                         slot_to_row.numel() != topk_w.numel() or y.shape[0] != topk_w.numel():
                     raise ValueError(f"{fn}: topk_w must be [{T}, k], slot_to_row int32 [{T} * k] and y [{T} * k, {H}]")
@@ -624,21 +641,21 @@ def moe_block_norm(resid: torch.Tensor, y: torch.Tensor | None = None, *, post_w
             gate, gate_row, gate_col = _gate(gate, T, H)
         ld_ro = ld_n = 0
         if y is not None:
-            resid_out, ld_ro = _out_rows(fn, resid_out, T, H, resid.dtype, resid.device)
+            resid_out, ld_ro = _out_rows(fn, resid_out, T, H, resid.dtype, resid)
             if resid_out.dtype != resid.dtype:
                 raise ValueError(f"{fn}: resid_out must have resid's type")
         if pre_w is not None:
-            next_out, ld_n = _out_rows(fn, next_out, T, H, torch.bfloat16, resid.device)
+            next_out, ld_n = _out_rows(fn, next_out, T, H, torch.bfloat16, resid)
             if next_out.dtype != torch.bfloat16:
                 raise ValueError(f"{fn}: next_out must be bf16")
         wt = post_w if post_w is not None else pre_w
         ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
         st = _lib.load().moe_block_norm(
             resid.data_ptr(), _DT[resid.dtype], ld_r, ptr(y), F32 if y is None else _DT[y.dtype], ld_y,
-            ptr(slot_to_row), ptr(topk_w), k, ptr(post_w), ptr(pre_w), F32 if wt is None else _DT[wt.dtype], w_offset,
+            ptr(y_add), F32 if y_add is None else _DT[y_add.dtype], ld_ya, ptr(slot_to_row), ptr(topk_w), k, ptr(post_w), ptr(pre_w), F32 if wt is None else _DT[wt.dtype], w_offset,
             eps, ptr(gate), F32 if gate is None else _DT[gate.dtype], gate_row, gate_col, scale, T, H,
             ptr(resid_out) if y is not None else None, ld_ro, ptr(next_out) if pre_w is not None else None, ld_n,
-            torch.cuda.current_stream().cuda_stream)
+            _raw_stream(idx))
     _lib.check(fn, st)
     return (resid_out if y is not None else None), (next_out if pre_w is not None else None)
 
