@@ -99,6 +99,11 @@ struct Decode<false> {
     o[2] = decode8(w[2], s1);
     o[3] = decode8(w[3], s1);
   }
+  // One quarter of it (dword j of the lane's codes).
+  static __device__ __forceinline__ Op part(uint32_t w, uint32_t sv, int j) {
+    const f16 s = (f16)e4m3_to_f32(j < 2 ? sv & 0xffu : (sv >> 8) & 0xffu);
+    return decode8(w, (f16x2){s, s});
+  }
   static __device__ __forceinline__ f32x4 mfma(const Op& a, const Op& b, const f32x4& c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
   }
@@ -111,6 +116,7 @@ struct Decode<true> {
 #pragma unroll
     for (int j = 0; j < 4; ++j) o[j] = decode8_mx(w[j], s);
   }
+  static __device__ __forceinline__ Op part(uint32_t w, uint32_t sv, int) { return decode8_mx(w, e8m0_to_f32(sv)); }
   static __device__ __forceinline__ f32x4 mfma(const Op& a, const Op& b, const f32x4& c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
@@ -141,33 +147,76 @@ __device__ __forceinline__ uint32_t settled(uint32_t off) {
   return off;
 }
 
-// Eight bf16 elements of a row's chunk, held by 16 lanes together, as f16 scaled by a power of
-// two of the chunk; unscale is the power that takes it back.
-__device__ __forceinline__ f16x8 chunk_to_f16(const u32x4& v, float& unscale) {
-  u16x2 m = __builtin_bit_cast(u16x2, v[0] & 0x7fff7fffu);
+// Eight bf16 elements of each of two rows' chunks, a chunk held by 16 lanes together, as f16
+// scaled by a power of two of the chunk; unscale is the power that takes it back. (Two rows a
+// call: the steps of one fill the waits of the other's reduction.)
+__device__ __forceinline__ void chunks_to_f16(const u32x4& v0, const u32x4& v1, f16x8 (&o)[2], float (&unscale)[2]) {
+  uint32_t top[2];
 #pragma unroll
-  for (int i = 1; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[i] & 0x7fff7fffu));
-  uint32_t top = row16_max(max((uint32_t)m[0], (uint32_t)m[1]));
-  if (__ballot(top >= 0x7f80u)) {   // an Inf or NaN somewhere: the maximum over the finite ones
-    uint32_t t = 0;
+  for (int r = 0; r < 2; ++r) {
+    const u32x4& v = r ? v1 : v0;
+    u16x2 m = __builtin_bit_cast(u16x2, v[0] & 0x7fff7fffu);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[i] & 0x7fff7fffu));
+    top[r] = max((uint32_t)m[0], (uint32_t)m[1]);
+  }
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    top[0] = dpp_max_u32(top[0], s);
+    top[1] = dpp_max_u32(top[1], s);
+  }
+  if (__ballot(max(top[0], top[1]) >= 0x7f80u)) {   // an Inf or NaN somewhere: the maximum over the finite ones
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const u32x4& v = r ? v1 : v0;
+      uint32_t t = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = v[i] & 0x7fffu, hi = (v[i] >> 16) & 0x7fffu;
+        t = max(t, lo < 0x7f80u ? lo : 0u);
+        t = max(t, hi < 0x7f80u ? hi : 0u);
+      }
+      top[r] = row16_max(t);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const u32x4& v = r ? v1 : v0;
+    const uint32_t eb = max(top[r] >> 7, 15u);   // biased exponent of the maximum
+    const float scale = __uint_as_float((268u - eb) << 23);
+    unscale[r] = __uint_as_float((eb - 14u) << 23);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = v[i] & 0x7fffu, hi = (v[i] >> 16) & 0x7fffu;
-      t = max(t, lo < 0x7f80u ? lo : 0u);
-      t = max(t, hi < 0x7f80u ? hi : 0u);
+      o[r][2 * i] = (f16)(bf16_to_f32(v[i] & 0xffffu) * scale);
+      o[r][2 * i + 1] = (f16)(__uint_as_float(v[i] & 0xffff0000u) * scale);
     }
-    top = row16_max(t);
   }
-  const uint32_t eb = max(top >> 7, 15u);   // biased exponent of the maximum
-  const float scale = __uint_as_float((268u - eb) << 23);
-  unscale = __uint_as_float((eb - 14u) << 23);
-  f16x8 o;
+}
+
+// A chunk of up to 16 rows, row 4 r + (lane >> 4) in x[r], as matrix operands to `row` (LDS, 16 rows
+// of kRowBytes) and its powers of two to `unscale`; x loaded as zeros past the T rows.
+template <bool MX>
+__device__ __forceinline__ void put_rows(const u32x4 (&x)[4], int T, int lane, unsigned char* row, float* unscale) {
+  const int l16 = lane & 15, g = lane >> 4;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    o[2 * i] = (f16)(bf16_to_f32(v[i] & 0xffffu) * scale);
-    o[2 * i + 1] = (f16)(__uint_as_float(v[i] & 0xffff0000u) * scale);
+  for (int r = 0; r < 4; r += 2) {
+    if (4 * r >= T) continue;
+    unsigned char* at = row + (4 * r + g) * kRowBytes + 16 * l16;
+    if (MX) {
+      *reinterpret_cast<u32x4*>(at) = x[r];
+      *reinterpret_cast<u32x4*>(at + 4 * kRowBytes) = x[r + 1];
+    } else {
+      f16x8 o[2];
+      float un[2];
+      chunks_to_f16(x[r], x[r + 1], o, un);
+      *reinterpret_cast<f16x8*>(at) = o[0];
+      *reinterpret_cast<f16x8*>(at + 4 * kRowBytes) = o[1];
+      if (l16 == 0) {
+        unscale[4 * r + g] = un[0];
+        unscale[4 * r + 4 + g] = un[1];
+      }
+    }
   }
-  return o;
 }
 
 // Power of two (as a float) that takes a row's largest finite magnitude, given as bf16 bits,
@@ -789,18 +838,7 @@ __global__ __launch_bounds__(kLongNT, WPS) void few_long_kernel(const FewArgs p)
     for (int d = 0; d < D; ++d) {
       // (chunks past the last have loaded zeros, rows and weights, and add nothing)
       const uint32_t c = (uint32_t)(wave + step * kLongW);
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        if (4 * r < T) {
-          if (MX) {
-            *reinterpret_cast<u32x4*>(row + (4 * r + g) * kRowBytes + 16 * l16) = xring[d][r];
-          } else {
-            float un;
-            *reinterpret_cast<f16x8*>(row + (4 * r + g) * kRowBytes + 16 * l16) = chunk_to_f16(xring[d][r], un);
-            if (l16 == 0) s_unscale[wave][4 * r + g] = un;
-          }
-        }
-      }
+      put_rows<MX>(xring[d], T, lane, row, s_unscale[wave]);
       issue_rows(d);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       Op bf[4];
@@ -849,6 +887,118 @@ __global__ __launch_bounds__(kLongNT, WPS) void few_long_kernel(const FewArgs p)
         }
         __syncthreads();
         ++tile;
+      }
+    }
+  }
+}
+
+// Rows that do not fit, many weight rows: a wave owns RB row blocks over all of K, so that no sums
+// cross waves, and the W waves of a workgroup share the rows: each of them turns one of the next W
+// chunks into operands, in the other half of a double-buffered piece of LDS.
+//
+// Bound by the vector units: a tile costs a wave 46 instructions (32 of them the decoding) and the
+// rows 16 a tile more; at four waves a SIMD that is 1200 cycles for every 18 KB a CU reads. 65536 x
+// 6144 at 16 rows: 48.2 us, 4.7 TB/s; few_long_kernel, in which every wave turns its own chunks,
+// 72; 16 waves sharing (half the turning, but all of a CU's waves at one barrier) 50; two row
+// blocks a wave 51; eight chunks in flight 50.
+template <bool MX, bool SWIGLU, int RB, int W, int D>
+__global__ __launch_bounds__(W* kWave, 4) void few_wide_kernel(const FewArgs p) {
+  typedef Decode<MX> Dec;
+  typedef typename Dec::Op Op;
+  static_assert(!SWIGLU || RB == 2, "a gate block and its up block");
+  static_assert(W % D == 0, "ring entries return to the same place in every group");
+  constexpr int R = kFewMaxTokens / 4;
+  __shared__ __attribute__((aligned(16))) unsigned char s_row[2][W][kFewMaxTokens * kRowBytes];
+  __shared__ float s_unscale[2][W][kFewMaxTokens];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, g = lane >> 4;
+  const int T = p.T, K = p.K;
+  const uint32_t nch = (uint32_t)nch_of(K);
+  const int ngroups = ((int)nch + W - 1) / W;
+  const uint32_t nblk = (uint32_t)p.Nw / 16;
+  const uint32_t wrow = nch * 1024u, srow = (MX ? (nch + 15) >> 4 : (nch + 7) >> 3) * 1024u;   // of a row block
+  const uint32_t sub = blockIdx.x * W + wave;                                                   // this wave's blocks
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(p.x, (uint32_t)((p.ldx * (T - 1) + K) * 2));
+  const __amdgpu_buffer_rsrc_t wr = make_rsrc(p.codes, nblk * wrow), sr = make_rsrc(p.scales, nblk * srow);
+  uint32_t xoff[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) xoff[r] = 4 * r + g < T ? (uint32_t)((4 * r + g) * p.ldx * 2) + 16u * l16 : kOOB;
+
+  u32x4 wring[D][RB], xv[R];
+  uint32_t sring[D][RB];
+  auto issue_rows = [&](uint32_t c) {
+    const bool cols = c * kChunk + 8 * l16 < (uint32_t)K;
+#pragma unroll
+    for (int r = 0; r < R; ++r) xv[r] = ld128(xr, settled(cols ? xoff[r] + c * 256u : kOOB), 0);
+  };
+  auto issue = [&](int d, uint32_t c) {
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      const uint32_t blk = tile_block<SWIGLU, RB>(sub, b, nblk);
+      const bool in = c < nch && tile_block_in<SWIGLU, RB>(sub, b, nblk);
+      wring[d][b] = ld128(wr, settled(16u * lane + (in ? blk * wrow + c * 1024u : kOOB)), 0);
+      sring[d][b] = ld32(sr, settled(16u * lane + (in ? blk * srow + scale_off<MX>(c) : kOOB)));
+    }
+  };
+  auto put_chunk = [&](int buf) { put_rows<MX>(xv, T, lane, s_row[buf][wave], s_unscale[buf][wave]); };
+  issue_rows((uint32_t)wave);
+#pragma unroll
+  for (int d = 0; d < D; ++d) issue(d, (uint32_t)d);
+  f32x4 tot[RB];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) tot[b] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  put_chunk(0);
+  __syncthreads();
+  for (int gr = 0; gr < ngroups; ++gr) {
+    const int buf = gr & 1;
+    // (chunks past the last have loaded zeros, rows and weights, and add nothing)
+    issue_rows((uint32_t)((gr + 1) * W + wave));
+#pragma unroll 1
+    for (int u0 = 0; u0 < W; u0 += D) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        const int u = u0 + d;
+        const uint32_t c = (uint32_t)(gr * W + u);
+        const float un = MX ? 1.0f : s_unscale[buf][u][l16];
+        f32x4 a[RB];
+#pragma unroll
+        for (int b = 0; b < RB; ++b) a[b] = MX ? tot[b] : (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const Op bf = *reinterpret_cast<const Op*>(s_row[buf][u] + l16 * kRowBytes + 64 * g + 16 * j);
+#pragma unroll
+          for (int b = 0; b < RB; ++b)
+            a[b] = Dec::mfma(Dec::part(wring[d][b][j], scale_of<MX>(sring[d][b], c), j), bf, a[b]);
+        }
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+          if (MX) {
+            tot[b] = a[b];
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tot[b][i] = fmaf(a[b][i], un, tot[b][i]);
+          }
+        }
+        issue(d, c + D);
+        __builtin_amdgcn_sched_barrier(0);   // (the next chunk's reads moved up here would cost the ring its registers)
+      }
+    }
+    put_chunk(buf ^ 1);
+    __syncthreads();
+  }
+  const float alpha = MX ? 1.0f : ld_const(p.g, 0);
+  if (l16 < T) {
+    constexpr int NB = SWIGLU ? 1 : RB;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      if (!tile_block_in<SWIGLU, RB>(sub, b, nblk)) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float v = tot[b][i] * alpha;
+        if (SWIGLU) v = swiglu1(v, tot[RB - 1][i] * alpha);
+        put_matvec(p, l16, (size_t)tile_block<SWIGLU, RB>(sub, b, nblk) * 16 + 4 * g + i, v);
       }
     }
   }
@@ -1161,13 +1311,27 @@ hipError_t launch_long(const FewArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <bool MX, bool SWIGLU, int RB, int W, int D>
+hipError_t launch_wide(const FewArgs& a, hipStream_t stream) {
+  const int sub = SWIGLU ? a.Nw / 32 : (a.Nw / 16 + RB - 1) / RB;
+  few_wide_kernel<MX, SWIGLU, RB, W, D><<<(sub + W - 1) / W, W * kWave, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
 template <bool MX, bool SWIGLU>
 hipError_t launch_mv_rows(const FewArgs& a, hipStream_t stream) {
   if (a.T <= resident_rows(a.K))
     return a.T > 4          ? launch_mv<MX, SWIGLU, 16, 2, 4>(a, stream)
            : short_tiles(a) ? launch_mv<MX, SWIGLU, 4, 2, 2>(a, stream)
                             : launch_mv<MX, SWIGLU, 4, 2, 4>(a, stream);
-  if (a.Nw / 16 >= 8 * 256) return launch_long<MX, SWIGLU, 8, 1, 2>(a, stream);
+  // Rows past the resident ones' LDS. More tiles than few_long_kernel has workgroups: the kernel
+  // whose waves share the rows. T = 16, K = 6144, cold weights, few_long / few_wide, us:
+  //   weight rows      16384       32768       65536       152064
+  //   NVFP4          23.0 / 25.7  41.1 / 28.6  73.4 / 50.7  167 / 118
+  //   MXFP4          18.1 / 19.6  34.0 / 24.6  61.5 / 46.0  143 / 107
+  //   SWIGLU, NVFP4  22.4 / 37    41.0 / 39.9  72.5 / 50.2  167 / 123
+  const int tiles = SWIGLU ? a.Nw / 64 : a.Nw / 32;
+  if (tiles > 512) return launch_wide<MX, SWIGLU, SWIGLU ? 2 : 1, 8, 4>(a, stream);
   return launch_long<MX, SWIGLU, 2, 2, 4>(a, stream);
 }
 
