@@ -510,8 +510,8 @@ size_t moe_grouped_gemm_mxfp8_workspace_size(int32_t rows, int32_t E, int32_t Nw
  *               elements apart; or NULL. May be out itself (same type and row distance).
  *   out, out_dtype, ld_out   device F32 or BF16 [T, n] (output), rows ld_out >= n elements
  *               apart; what lies between the rows is not written.
- * A row's result does not depend on the other rows, except that up to 4 and more than 4 rows
- * may sum in another order; a NaN or Inf in one row stays in that row.
+ * out must not overlap x. A row's result does not depend on the other rows' values (their number
+ * may change the order of the sums); a NaN or Inf in one row stays in that row.
  * ------------------------------------------------------------------------- */
 nvfp4moe_status nvfp4_matvec(nvfp4moe_epilogue epi, const void* x, int64_t ldx, int32_t T, const uint8_t* w_codes,
                              const uint8_t* w_scales, const float* w_g, int32_t Nw, int32_t K, const void* add,

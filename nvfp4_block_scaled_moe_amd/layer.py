@@ -72,6 +72,8 @@ def moe_forward(x: torch.Tensor, logits: torch.Tensor, k: int, w: NVFP4Experts, 
     (moe_grouped_gemm_nvfp4_combine; same output bits, no Y in the stages). Without ``reduce``
     the experts' rows are returned unsummed: (Y f32 [T*k, H], slot_to_row, topk_w).
     """
+    if not reduce and (combine or keep):
+        raise ValueError("moe_forward: reduce=False goes without combine and keep")
     st = {}
     T = x.shape[0]
     S = T * k
@@ -115,7 +117,7 @@ def moe_forward(x: torch.Tensor, logits: torch.Tensor, k: int, w: NVFP4Experts, 
         else:
             y = ops.moe_grouped_gemm_nvfp4(ops.W4A4, ops.EPI_NONE, hq, w.w2_t,
                                            a_scales=hs, a_g=hg, rows=S, out_dtype=torch.float32, **common)
-    if not reduce and not combine:
+    if not reduce:
         return y, r["slot_to_row"], r["topk_w"]
     if not combine:
         out = ops.moe_unpermute_reduce(y, r["slot_to_row"], r["topk_w"])
@@ -166,6 +168,8 @@ def moe_forward_mxfp4(x: torch.Tensor, logits: torch.Tensor, k: int, w: MXFP4Exp
     scale per 32 elements, no per-tensor scale, so the up/gate GEMM's epilogue writes h as
     MXFP4 directly); both GEMMs run on the scaled FP4 matrix cores. ``x`` bf16 [T, H];
     ``logits`` f32 [T, E]. ``reduce`` as for moe_forward."""
+    if not reduce and (combine or keep):
+        raise ValueError("moe_forward_mxfp4: reduce=False goes without combine and keep")
     st = {}
     r = ops.moe_route_permute(logits, k)
     st.update(r)

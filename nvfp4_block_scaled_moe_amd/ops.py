@@ -489,6 +489,8 @@ def _out_rows(fn: str, out, T: int, n: int, dtype, like):
     """(out, row distance) of an output [T, n]: allocated where ``like`` is, or the caller's
     with contiguous rows."""
     if out is None:
+        if like.shape == (T, n):
+            return torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format), n
         return like.new_empty((T, n), dtype=dtype), n
     if out.shape != (T, n) or out.dtype not in _DT or (n > 1 and out.stride(1) != 1) or \
             (T > 1 and out.stride(0) < n):
@@ -510,9 +512,9 @@ def _matvec(fn: str, x, w, epi, add, out_dtype, out, g):
     n = Nw // 2 if epi == EPI_SWIGLU else Nw
     ld_add = n
     if add is not None:
+        add, ld_add = _rows(fn, "add", add, n)
         if add.shape[0] != T:
             raise ValueError(f"{fn}: add must be [{T}, {n}], got {tuple(add.shape)}")
-        add, ld_add = _rows(fn, "add", add, n)
     with _on(idx):
         out, ld_out = _out_rows(fn, out, T, n, out_dtype, x)
         rest = (Nw, K, None if add is None else add.data_ptr(), F32 if add is None else _DT[add.dtype], ld_add,
@@ -599,8 +601,8 @@ def moe_block_norm(resid: torch.Tensor, y: torch.Tensor | None = None, *, post_w
     only next, of ``resid``; without ``pre_w`` only r').
 
     ``resid`` float32 or bf16 [T, H]; ``y`` [T, H], or with ``slot_to_row`` and ``topk_w`` the
-    experts' rows [T*k, H]; ``y_add`` [T, H] is added to it (a shared expert); ``post_w``, ``pre_w`` [H] (of one type); ``gate`` [H], [T, 1] or
-    [T, H]. ``resid_out`` may be ``resid``."""
+    experts' rows [T*k, H]; ``y_add`` [T, H] is added to it (a shared expert); ``post_w``,
+    ``pre_w`` [H]; ``gate`` [H], [T, 1] or [T, H]. ``resid_out`` may be ``resid``."""
     fn = "moe_block_norm"
     idx = _gpu(fn, resid, y, post_w, gate, pre_w, slot_to_row, topk_w, y_add, resid_out, next_out)
     if resid.dim() != 2:
@@ -615,7 +617,8 @@ def moe_block_norm(resid: torch.Tensor, y: torch.Tensor | None = None, *, post_w
     if post_w is not None and pre_w is not None and post_w.dtype != pre_w.dtype:
         post_w, pre_w = post_w.float(), pre_w.float()
     with _on(idx):
-        resid, ld_r = _rows(fn, "resid", resid, H, 8) if resid_out is not resid else (resid, resid.stride(0))
+        resid, ld_r = _rows(fn, "resid", resid, H, 8) if resid_out is not resid else \
+            (resid, resid.stride(0) if T > 1 else H)
         post_w, pre_w = _aligned(post_w), _aligned(pre_w)
         ld_y = ld_ya = k = 0
         if y_add is not None:
@@ -652,8 +655,9 @@ def moe_block_norm(resid: torch.Tensor, y: torch.Tensor | None = None, *, post_w
         ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
         st = _lib.load().moe_block_norm(
             resid.data_ptr(), _DT[resid.dtype], ld_r, ptr(y), F32 if y is None else _DT[y.dtype], ld_y,
-            ptr(y_add), F32 if y_add is None else _DT[y_add.dtype], ld_ya, ptr(slot_to_row), ptr(topk_w), k, ptr(post_w), ptr(pre_w), F32 if wt is None else _DT[wt.dtype], w_offset,
-            eps, ptr(gate), F32 if gate is None else _DT[gate.dtype], gate_row, gate_col, scale, T, H,
+            ptr(y_add), F32 if y_add is None else _DT[y_add.dtype], ld_ya, ptr(slot_to_row), ptr(topk_w), k,
+            ptr(post_w), ptr(pre_w), F32 if wt is None else _DT[wt.dtype], w_offset, eps, ptr(gate),
+            F32 if gate is None else _DT[gate.dtype], gate_row, gate_col, scale, T, H,
             ptr(resid_out) if y is not None else None, ld_ro, ptr(next_out) if pre_w is not None else None, ld_n,
             _raw_stream(idx))
     _lib.check(fn, st)

@@ -126,6 +126,34 @@ def test_block_norm_of_the_experts_rows(T, k, H, ydt):
             _check(resid, got, _want(resid, y, pw, None, 0.7, pre_w, 0.0, 1e-6, s2r, tw), pre_w, 0.0, 1e-6)
 
 
+@pytest.mark.parametrize("T,k,H", [(1, 0, 64), (5, 0, 1000), (260, 0, 2056), (2, 0, 32768), (1, 8, 6144), (7, 3, 264),
+                                   (300, 2, 8200)])
+@pytest.mark.parametrize("adt", [F32, BF])
+def test_block_norm_with_a_second_addend(T, k, H, adt):
+    """y_add beside y, and beside the experts' rows (k > 0); rows of it that lie apart."""
+    say("block norm y_add", T, k, H, adt)
+    y = inputs.random_fp32((T * max(k, 1), H), 3).to(BF).to(DEV)
+    base = torch.full((T, H + 16), float("nan"), dtype=adt, device=DEV)
+    base[:, 8:8 + H] = inputs.random_fp32((T, H), 4).to(adt).to(DEV)
+    y_add = base[:, 8:8 + H]
+    rows = {}
+    if k:
+        rows = dict(slot_to_row=torch.randperm(T * k, generator=torch.Generator().manual_seed(5)).to(torch.int32).to(DEV),
+                    topk_w=torch.softmax(inputs.random_fp32((T, k), 6), -1).to(DEV))
+    # in the formula y_add is one more row of every token, with weight 1
+    both = torch.cat([y.float(), y_add.float()])
+    own = torch.arange(T, dtype=torch.int32, device=DEV).view(T, 1)
+    s2r = torch.cat([rows["slot_to_row"].view(T, k) if k else own, own + y.shape[0]], 1)
+    tw = torch.cat([rows["topk_w"] if k else torch.ones((T, 1), device=DEV), torch.ones((T, 1), device=DEV)], 1)
+    post_w, pre_w = (1 + inputs.random_fp32((H,), s, std=0.1).to(DEV) for s in (7, 8))
+    for rdt in (F32, BF):
+        resid = inputs.random_fp32((T, H), 1).to(rdt).to(DEV)
+        for pw in (post_w, None):
+            got = ops.moe_block_norm(resid, y, y_add=y_add, post_w=pw, scale=0.7, pre_w=pre_w, **rows)
+            torch.cuda.synchronize()
+            _check(resid, got, _want(resid, both, pw, None, 0.7, pre_w, 0.0, 1e-6, s2r, tw), pre_w, 0.0, 1e-6)
+
+
 def test_block_norm_strides_in_place_and_expanded_gates():
     """Rows apart, outputs into views (nothing between the rows is written), resid updated in
     place, gates expanded or with columns apart, an address that 16-byte reads do not allow."""

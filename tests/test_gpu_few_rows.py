@@ -111,6 +111,72 @@ def test_matvec_swiglu_add(fmt, T, Nw, K):
         _check(np_(got), want, err, torch.float32)
 
 
+# Rows that do not fit in a CU's LDS beside each other (T * K too large): the waves of a workgroup
+# take parts of K, or, with more row blocks than such workgroups, row blocks of their own.
+LONG = [
+    # T, Nw, K, SwiGLU
+    (16, 16, 4096, False), (16, 80, 16416, False), (5, 2080, 12064, False), (9, 64, 7200, True), (2, 48, 40992, False),
+    (1, 64, 65568, True), (16, 16448, 3616, False), (11, 16624, 5152, False), (4, 16400, 14368, False),
+    (16, 32832, 3616, True), (7, 32896, 8320, True),
+]
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("T,Nw,K,swiglu", LONG)
+def test_matvec_long_rows(fmt, T, Nw, K, swiglu):
+    """A sample of the weight rows, the first and the last 40 among them, against float64."""
+    say("matvec long", fmt, T, Nw, K, swiglu)
+    gen = torch.Generator(device=DEV).manual_seed(K + T)
+    wf = torch.randn((1, Nw, K), generator=gen, device=DEV, dtype=torch.bfloat16) * 0.03
+    q = ops.nvfp4_quantize(wf) if fmt == "nvfp4" else ops.mxfp4_quantize(wf)
+    w = ops.nvfp4_weights_tile(*q) if fmt == "nvfp4" else ops.mxfp4_weights_tile(*q)
+    n = Nw // 2 if swiglu else Nw
+    rows = np.unique(np.concatenate([np.arange(min(40, n)), np.arange(max(0, n - 40), n),
+                                     np.random.default_rng(K).integers(0, n, 60)]))
+    sel = np.concatenate([rows, rows + n]) if swiglu else rows
+    part = [np_(t[0][torch.from_numpy(sel).to(DEV)]) for t in q[:2]]
+    W = nvfp4.dequantize(*part, np_(q[2][0])) if fmt == "nvfp4" else mxfp4.dequantize(*part)
+    x = _rows(T, K, 6 + T)
+    P, err = _product(x.double().numpy(), W)
+    if swiglu:
+        P, err = _swiglu(P, err)
+    add = inputs.random_fp32((T, n), 78).to(DEV)
+    got = _call(fmt)(x.to(DEV), w, ops.EPI_SWIGLU if swiglu else ops.EPI_NONE, add=add, out_dtype=torch.float32)
+    again = _call(fmt)(x.to(DEV), w, ops.EPI_SWIGLU if swiglu else ops.EPI_NONE, add=add, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    assert torch.equal(got, again)
+    _check(np_(got)[:, rows], P + np_(add)[:, rows].astype(np.float64), err, torch.float32)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("Nw", [64, 16448])
+def test_matvec_long_nonfinite_and_extreme_rows(fmt, Nw):
+    """As for short rows: NaN and Inf stay in their row, zero, tiny and huge rows keep their precision."""
+    T, K = 14, 4128
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    q = (ops.nvfp4_quantize if fmt == "nvfp4" else ops.mxfp4_quantize)(
+        torch.randn((1, Nw, K), generator=gen, device=DEV, dtype=torch.bfloat16) * 0.03)
+    w = (ops.nvfp4_weights_tile if fmt == "nvfp4" else ops.mxfp4_weights_tile)(*q)
+    part = [np_(t[0][-48:]) for t in q[:2]]
+    W = nvfp4.dequantize(*part, np_(q[2][0])) if fmt == "nvfp4" else mxfp4.dequantize(*part)
+    x = _rows(T, K, 8)
+    x[0, 4003] = float("nan")
+    x[1] = 0.0
+    x[2] = x[2] * 2.0 ** 100
+    x[3] = x[3] * 2.0 ** -100
+    x[5, 200] = float("inf")
+    x[6, ::2] = x[6, ::2] * 2.0 ** 20
+    got = np_(_call(fmt)(x.to(DEV), w, out_dtype=torch.float32))[:, -48:]
+    with np.errstate(invalid="ignore"):
+        P, err = _product(x.double().numpy(), W)
+    assert np.isnan(got[0]).all() and (got[1] == 0).all()
+    nz = W[:, 200] != 0
+    assert np.array_equal(got[5][nz], P[5][nz])
+    for t in range(2, T):
+        if t != 5:
+            _check(got[t], P[t], err[t], torch.float32)
+
+
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
 def test_matvec_strided_rows_and_in_place_add(fmt):
     """Rows of x, add and out that lie apart; add in place; nothing between the rows is written."""
