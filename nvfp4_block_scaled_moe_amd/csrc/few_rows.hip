@@ -305,6 +305,13 @@ struct Share {
   }
 };
 
+// The kernel's arguments, one of each 64 bytes of them, requested together: the first reading of
+// each misses every cache (a microsecond), and the compiler would leave some to where they are used.
+__device__ __forceinline__ void fetch_args(const FewArgs& p) {
+  static_assert(sizeof(FewArgs) <= 192, "three lines");
+  asm volatile("" ::"s"(p.K), "s"(p.grid), "s"(p.most_parts));
+}
+
 // ------------------------------------------------------------------ resident rows: matvec, and the layer's first launch
 // The rows (the item's, or all of them once when they fit) stay in LDS as matrix operands, f16
 // with one power of two a row (NVFP4) or bf16 (MXFP4): turned once, they serve every tile of
@@ -334,6 +341,7 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
   __shared__ uint32_t s_scan[kW];
   __shared__ uint32_t s_amax;
 
+  fetch_args(p);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
@@ -550,7 +558,7 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
   // ---- this workgroup's tiles, in runs of one item's: a flat sequence of steps (a chunk of RB
   // weight tiles), D of them a turn of the ring. A tile takes at least D steps, so that at most
   // one is completed in a turn; a run is padded to whole turns.
-  const Share share((uint32_t)nitems * (uint32_t)tpi, gridDim.x);
+  const Share share((uint32_t)nitems * (uint32_t)tpi, (uint32_t)p.grid);
   const int t0 = (int)share.begin(blockIdx.x), t1 = (int)share.begin(blockIdx.x + 1);
   if (t0 >= t1) return;   // fewer tiles than workgroups
 
@@ -775,6 +783,7 @@ __global__ __launch_bounds__(kLongNT, WPS) void few_long_kernel(const FewArgs p)
   __shared__ float s_unscale[kLongW][kFewMaxTokens];
   __shared__ __attribute__((aligned(16))) float s_red[kLongW * RB][16 * 16];
 
+  fetch_args(p);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
@@ -785,8 +794,8 @@ __global__ __launch_bounds__(kLongNT, WPS) void few_long_kernel(const FewArgs p)
   const int ntiles = ((int)(SWIGLU ? nblk / 2 : nblk) + HB - 1) / HB;
   const uint32_t wbytes = nblk * nch * 1024u;
   const uint32_t sbytes = nblk * (MX ? (nch + 15) >> 4 : (nch + 7) >> 3) * 1024u;
-  const int t0 = (int)((int64_t)ntiles * blockIdx.x / gridDim.x);
-  const int t1 = (int)((int64_t)ntiles * (blockIdx.x + 1) / gridDim.x);
+  const int t0 = (int)((int64_t)ntiles * blockIdx.x / p.grid);
+  const int t1 = (int)((int64_t)ntiles * (blockIdx.x + 1) / p.grid);
   const int nst = (t1 - t0) * cpw;
 
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(p.x, (uint32_t)((p.ldx * (T - 1) + K) * 2));
@@ -911,6 +920,7 @@ __global__ __launch_bounds__(W* kWave, 4) void few_wide_kernel(const FewArgs p) 
   __shared__ __attribute__((aligned(16))) unsigned char s_row[2][W][kFewMaxTokens * kRowBytes];
   __shared__ float s_unscale[2][W][kFewMaxTokens];
 
+  fetch_args(p);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
@@ -1025,6 +1035,7 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
   __shared__ int s_top[kFewMaxSlots];     // NVFP4: the largest exponent of a row's blocks
   __shared__ int s_last;
 
+  fetch_args(p);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
@@ -1070,7 +1081,7 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
   const uint32_t P = (uint32_t)nitems * nch, ntile = nblk / RB, Wk = P * ntile;
   uint32_t n = Wk / kDownLeast;   // workgroups that take part: not fewer than there are tiles
   n = n < ntile ? ntile : n;
-  n = n < gridDim.x ? n : gridDim.x;
+  n = n < (uint32_t)p.grid ? n : (uint32_t)p.grid;
   if (blockIdx.x >= n) return;
   const Share share(Wk, n);
   const uint32_t x0 = share.begin(blockIdx.x);
@@ -1281,6 +1292,7 @@ hipError_t launch_up(FewArgs a, int rows, int grid, hipStream_t stream) {
   const hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(kernel), kResidentBytes + 16 * 16, done);
   if (e != hipSuccess) return e;
   a.ppr_inv = ppr_inverse(a.K);
+  a.grid = grid;
   kernel<<<grid, kNT, rows * row_lds_bytes(a.K), stream>>>(a);
   return hipGetLastError();
 }
@@ -1304,10 +1316,11 @@ hipError_t launch_mv(const FewArgs& a, hipStream_t stream) {
 }
 
 template <bool MX, bool SWIGLU, int RB, int D, int WPS>
-hipError_t launch_long(const FewArgs& a, hipStream_t stream) {
+hipError_t launch_long(FewArgs a, hipStream_t stream) {
   const int hb = SWIGLU ? RB / 2 : RB;
   const int tiles = ((SWIGLU ? a.Nw / 32 : a.Nw / 16) + hb - 1) / hb, most = 128 * WPS / 2 * 2;
-  few_long_kernel<MX, SWIGLU, RB, D, WPS><<<tiles < most ? tiles : most, kLongNT, 0, stream>>>(a);
+  a.grid = tiles < most ? tiles : most;
+  few_long_kernel<MX, SWIGLU, RB, D, WPS><<<a.grid, kLongNT, 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -1367,6 +1380,7 @@ hipError_t launch_few_layer(FewArgs up, FewArgs down, bool mx, hipStream_t strea
                                 : launch_layer_up<false, false>(up, rows, grid, stream);
   if (e != hipSuccess) return e;
   const int wgs = few_down_workgroups(down.T, down.k, down.Nw, down.K);
+  down.grid = wgs;
   if (mx)
     few_down_kernel<true, 3><<<wgs, kNT, 0, stream>>>(down);
   else

@@ -178,6 +178,7 @@ struct FewArgs {
   uint32_t ppr_inv;
   const void* add;        // matvec: float32 or bf16 [T, n], rows ld_add apart, or null
   int add_bf16;
+  int grid;               // workgroups, set by the launcher (the launch's own count lies apart from the arguments)
   int64_t ld_add;
   void* out;              // matvec: float32 or bf16; the layer's second launch: bf16
   int out_bf16;
