@@ -4,15 +4,21 @@
 //   next = bf16( r' / sqrt(mean(r'^2) + eps) * (o + pre_w) )                               with pre_w
 // y is the block's output, or the experts' rows with their weights: y_t = sum_j w[t, j] Y[row of
 // slot (t, j)] in ascending j (the unpermute-reduce, whose bf16 output then never exists); y_add
-// (a shared expert's output) is added to either. Without
-// y only next is written (the norm before the first block).
+// (a shared expert's output) is added to either. Without y only next is written (the norm before
+// the first block).
 //
 // Memory-bound: y (k rows of it for the experts' form), r and a full gate are read once, r' and
 // next written once; everything between stays in registers. One workgroup a row: a thread holds
 // V groups of 8 consecutive columns (16- and 32-byte accesses), the two sums of squares meet in
-// LDS (float32: at most 32 squares a thread, then a tree over lanes and waves). Next is computed from r' in
-// float32, before r' is rounded to its stored type.
-#include "common.h"
+// LDS (float32: at most 32 squares a thread, then a tree over lanes and waves). Next is computed
+// from r' in float32, before r' is rounded to its stored type.
+//
+// 8192 rows of 7168 (y and next bf16, r float32: 704 MB): 145 us, 4.85 TB/s, where a copy reaches
+// 5.1-5.2; with one group a thread 165 us, with the weights requested ahead, too, 167 (fewer
+// workgroups a CU), with r requested behind y 152. One row of 8 x 6144: 5.7 us, of 37 x 1000: 3.2
+// us, bound by the latency of the launch and of two dependent reads; requested one after the other,
+// as they are used, the tensors took 6.7 and 3.9 us.
+#include "gemm_common.h"
 #include "kernels.h"
 
 namespace nvfp4moe {
@@ -20,26 +26,34 @@ namespace nvfp4moe {
 namespace {
 
 constexpr int kNormMaxThreads = 1024;
-constexpr int kNormBatch = 4;      // experts' rows requested together
 constexpr int kNormManyRows = 256; // rows from which a thread holds more columns
 
-// Eight consecutive values as float32 (o: element offset).
-__device__ __forceinline__ void load8(const void* p, bool bf16, int64_t o, float (&v)[8]) {
-  if (bf16) {
-    const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + o);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+// Eight consecutive values of a row as they lie in memory: 16 bytes of bf16, or 32 of float32.
+// The loads of both types are the same two (the second out of range for bf16, and both past the
+// row's end: such loads return zeros and touch no memory), so that they can all be requested
+// before the first is waited for; a branch on the type would wait in each of its sides.
+struct Raw8 {
+  u32x4 a, b;
+};
+struct Row {   // a row of H values of one tensor; bytes 0: absent, reads as zeros
+  __amdgpu_buffer_rsrc_t r;
+  bool bf16;
+  __device__ __forceinline__ Row(const void* p, bool is_bf16, int64_t first, int H)
+      : r(make_rsrc(static_cast<const char*>(p) + first * (is_bf16 ? 2 : 4), p ? (uint32_t)H * (is_bf16 ? 2u : 4u) : 0u)),
+        bf16(is_bf16) {}
+  __device__ __forceinline__ Raw8 load(int col) const {
+    const uint32_t o = (uint32_t)col * (bf16 ? 2u : 4u);
+    return {ld128(r, o, 0), ld128(r, bf16 ? kOOB : o + 16u, 0)};
+  }
+  __device__ __forceinline__ void values(const Raw8& q, float (&v)[8]) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      v[2 * i] = __uint_as_float(bf16 ? q.a[i] << 16 : i < 2 ? q.a[2 * i] : q.b[2 * i - 4]);
+      v[2 * i + 1] = __uint_as_float(bf16 ? q.a[i] & 0xffff0000u : i < 2 ? q.a[2 * i + 1] : q.b[2 * i - 3]);
     }
-  } else {
-    const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + o);
-    const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + o + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   }
-}
+};
+
 __device__ __forceinline__ void store8(void* p, bool bf16, int64_t o, const float (&v)[8]) {
   if (bf16) {
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + o) =
@@ -51,75 +65,127 @@ __device__ __forceinline__ void store8(void* p, bool bf16, int64_t o, const floa
   }
 }
 
-// Sum over the workgroup, in every thread; part: kNormMaxThreads / 64 floats of LDS of its own.
-__device__ __forceinline__ float block_sum(float v, float* part) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
-  const int nw = blockDim.x / kWave;
+// One step of a sum over lanes by DPP moves: 0-3 leave a row of 16's sum in all its lanes, 4 and 5
+// fold the four rows into lane 63.
+template <int S>
+__device__ __forceinline__ float dpp_add(float v) {
+  constexpr int ctrl[6] = {0xb1, 0x4e, 0x141, 0x140, 0x142, 0x143};
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl[S], S == 4 ? 0xa : S == 5 ? 0xc : 0xf,
+                                                        0xf, false));
+}
+__device__ __forceinline__ float row16_sum(float v) { return dpp_add<3>(dpp_add<2>(dpp_add<1>(dpp_add<0>(v)))); }
+
+// Sum over the workgroup of nw waves, in every thread; part: kNormMaxThreads / 64 floats of LDS of its own.
+__device__ __forceinline__ float block_sum(float v, float* part, int nw) {
+  v = dpp_add<5>(dpp_add<4>(row16_sum(v)));
+  v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
   if (nw == 1) return v;
   if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = v;
   __syncthreads();
-  float s = 0.0f;
-  for (int w = 0; w < nw; ++w) s += part[w];
-  return s;
+  const int l = threadIdx.x & 15;
+  return row16_sum(l < nw ? part[l] : 0.0f);
 }
 
 template <int V, bool ROWS>
 __global__ __launch_bounds__(kNormMaxThreads) void block_norm_kernel(const BlockNormArgs p) {
+  // The arguments, one of each 64 bytes of them, requested together (each misses every cache).
+  static_assert(sizeof(BlockNormArgs) <= 256, "four lines");
+  asm volatile("" ::"s"(p.r_bf16), "s"(p.k), "s"(p.gate_bf16), "s"(p.nt));
+  static_assert(kNormMaxThreads / kWave <= 16, "a row of lanes holds the waves' sums");
+  // One group of columns a thread (short rows, where latency counts): everything is requested
+  // before anything is waited for. More groups: registers allow less.
+  constexpr bool kAll = V == 1, kResid = !(ROWS && V == 4);
+  constexpr int kBatch = V == 4 ? 2 : 4;   // experts' rows requested together
   __shared__ float part[2][kNormMaxThreads / kWave];
   const int64_t t = blockIdx.x;
-  const int H = p.H;
+  const int H = p.H, nw = p.nt / kWave;
   int col[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) col[v] = ((int)threadIdx.x + v * (int)blockDim.x) * 8;
+  for (int v = 0; v < V; ++v) col[v] = ((int)threadIdx.x + v * p.nt) * 8;
 
+  // The experts' rows: a lane for each of the token's slots, its row and weight. (Requested first:
+  // loads return in order.)
+  static_assert(kMaxTopK <= kWave, "a lane for each slot");
+  const int lane = threadIdx.x % kWave;
+  int row_of = 0;
+  float slot_w = 0.0f;
+  if (ROWS) {
+    const int64_t slot = t * p.k + min(lane, p.k - 1);
+    row_of = p.slot_to_row[slot];
+    slot_w = p.topk_w[slot];
+  }
+  const Row resid(p.resid, p.r_bf16, t * p.ld_r, H), y_add(p.y_add, p.ya_bf16, t * p.ld_ya, H);
+  const Row post_w(p.post_w, p.w_bf16, 0, H), pre_w(p.pre_w, p.w_bf16, 0, H);
+  const Row gate(p.gate_col ? p.gate : nullptr, p.gate_bf16, t * p.gate_row, H);
+  Raw8 rq[V], aq[V], gq[V], oq[V], nq[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    if (kResid) rq[v] = resid.load(col[v]);
+    if (kAll) {
+      aq[v] = y_add.load(col[v]);
+      oq[v] = post_w.load(col[v]);
+      gq[v] = gate.load(col[v]);
+      nq[v] = pre_w.load(col[v]);
+    }
+  }
   float r[V][8], y[V][8];
   if (ROWS) {
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[v][i] = 0.0f;
-    for (int j0 = 0; j0 < p.k; j0 += kNormBatch) {
-      int64_t row[kNormBatch];
-      float w[kNormBatch];
+    const int weight_of = __float_as_int(lane < p.k ? slot_w : 0.0f);   // (with a row of zeros: adds nothing)
+    for (int j0 = 0; j0 < p.k; j0 += kBatch) {
+      int row[kBatch];
+      float w[kBatch];
 #pragma unroll
-      for (int j = 0; j < kNormBatch; ++j) {   // (the row is the workgroup's: scalar loads)
-        const bool in = j0 + j < p.k;
-        row[j] = in ? (int64_t)ld_const(p.slot_to_row, t * p.k + j0 + j) : 0;
-        w[j] = in ? ld_const(p.topk_w, t * p.k + j0 + j) : 0.0f;
+      for (int j = 0; j < kBatch; ++j) {
+        const int l = min(j0 + j, kWave - 1);
+        row[j] = __builtin_amdgcn_readlane(row_of, l);
+        w[j] = __int_as_float(__builtin_amdgcn_readlane(weight_of, l));
       }
-      float q[kNormBatch][V][8];
+      const Row first(p.y, p.y_bf16, 0, H);
+      Raw8 q[kBatch][V];
 #pragma unroll
-      for (int j = 0; j < kNormBatch; ++j)
+      for (int j = 0; j < kBatch; ++j) {
+        const Row yr(j0 + j < p.k ? p.y : nullptr, p.y_bf16, row[j] * p.ld_y, H);
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-          if (j0 + j < p.k && col[v] < H) load8(p.y, p.y_bf16, row[j] * p.ld_y + col[v], q[j][v]);
+        for (int v = 0; v < V; ++v) q[j][v] = yr.load(col[v]);
+      }
 #pragma unroll
-      for (int j = 0; j < kNormBatch; ++j)
+      for (int j = 0; j < kBatch; ++j)
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-          if (j0 + j < p.k && col[v] < H) {
+        for (int v = 0; v < V; ++v) {
+          float u[8];
+          first.values(q[j][v], u);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[v][i] = fmaf(w[j], q[j][v][i], y[v][i]);
-          }
+          for (int i = 0; i < 8; ++i) y[v][i] = fmaf(w[j], u[i], y[v][i]);
+        }
     }
   } else {
+    const Row yr(p.y, p.y_bf16, t * p.ld_y, H);
+    Raw8 q[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (p.y && col[v] < H) load8(p.y, p.y_bf16, t * p.ld_y + col[v], y[v]);
+    for (int v = 0; v < V; ++v) q[v] = yr.load(col[v]);
+#pragma unroll
+    for (int v = 0; v < V; ++v) yr.values(q[v], y[v]);
   }
   if (p.y_add) {
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (col[v] < H) {
-        load8(p.y_add, p.ya_bf16, t * p.ld_ya + col[v], r[v]);
+      if (!kAll) aq[v] = y_add.load(col[v]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[v][i] += r[v][i];
-      }
+    for (int v = 0; v < V; ++v) {
+      y_add.values(aq[v], r[v]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[v][i] += r[v][i];
+    }
   }
 #pragma unroll
-  for (int v = 0; v < V; ++v)
-    if (col[v] < H) load8(p.resid, p.r_bf16, t * p.ld_r + col[v], r[v]);
+  for (int v = 0; v < V; ++v) {
+    if (!kResid) rq[v] = resid.load(col[v]);
+    resid.values(rq[v], r[v]);
+  }
 
   if (p.y) {
     float mul = p.scale;
@@ -128,63 +194,62 @@ __global__ __launch_bounds__(kNormMaxThreads) void block_norm_kernel(const Block
                          : static_cast<const float*>(p.gate)[t * p.gate_row];
     float inv = 1.0f;
     if (p.post_w) {
-      float ss = 0.0f;
+      float ss = 0.0f;   // (columns past the row's end hold zeros)
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        if (col[v] < H) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) ss = fmaf(y[v][i], y[v][i], ss);
-        }
-      inv = rsqrtf(block_sum(ss, part[0]) / (float)H + p.eps);
+        for (int i = 0; i < 8; ++i) ss = fmaf(y[v][i], y[v][i], ss);
+      inv = rsqrtf(block_sum(ss, part[0], nw) / (float)H + p.eps);
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (col[v] < H) {
-        if (p.post_w) {
-          float w[8];
-          load8(p.post_w, p.w_bf16, col[v], w);
+    for (int v = 0; v < V; ++v) {
+      if (p.post_w) {
+        if (!kAll) oq[v] = post_w.load(col[v]);
+        float w[8];
+        post_w.values(oq[v], w);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[v][i] = y[v][i] * inv * (p.w_offset + w[i]);
-        }
-        if (p.gate && p.gate_col) {
-          float gt[8];
-          load8(p.gate, p.gate_bf16, t * p.gate_row + col[v], gt);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[v][i] *= gt[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r[v][i] = fmaf(mul, y[v][i], r[v][i]);
-        store8(p.resid_out, p.r_bf16, t * p.ld_ro + col[v], r[v]);
+        for (int i = 0; i < 8; ++i) y[v][i] = y[v][i] * inv * (p.w_offset + w[i]);
       }
+      if (p.gate && p.gate_col) {
+        if (!kAll) gq[v] = gate.load(col[v]);
+        float gt[8];
+        gate.values(gq[v], gt);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[v][i] *= gt[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r[v][i] = fmaf(mul, y[v][i], r[v][i]);
+      if (col[v] < H) store8(p.resid_out, p.r_bf16, t * p.ld_ro + col[v], r[v]);
+    }
   }
   if (p.pre_w) {
     float ss = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (col[v] < H) {
+      if (col[v] < H) {   // (past it: 0 times an infinite scale is NaN)
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = fmaf(r[v][i], r[v][i], ss);
       }
-    const float inv = rsqrtf(block_sum(ss, part[1]) / (float)H + p.eps);
+    const float inv = rsqrtf(block_sum(ss, part[1], nw) / (float)H + p.eps);
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (col[v] < H) {
-        float w[8], n[8];
-        load8(p.pre_w, p.w_bf16, col[v], w);
+    for (int v = 0; v < V; ++v) {
+      if (!kAll) nq[v] = pre_w.load(col[v]);
+      float w[8], n[8];
+      pre_w.values(nq[v], w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) n[i] = r[v][i] * inv * (p.w_offset + w[i]);
-        store8(p.next, true, t * p.ld_next + col[v], n);
-      }
+      for (int i = 0; i < 8; ++i) n[i] = r[v][i] * inv * (p.w_offset + w[i]);
+      if (col[v] < H) store8(p.next, true, t * p.ld_next + col[v], n);
+    }
   }
 }
 
 template <int V>
-hipError_t launch_v(const BlockNormArgs& a, hipStream_t stream) {
-  const int nt = ((a.H / 8 + V - 1) / V + kWave - 1) / kWave * kWave;
+hipError_t launch_v(BlockNormArgs a, hipStream_t stream) {
+  a.nt = ((a.H / 8 + V - 1) / V + kWave - 1) / kWave * kWave;
   if (a.slot_to_row)
-    block_norm_kernel<V, true><<<(unsigned)a.T, nt, 0, stream>>>(a);
+    block_norm_kernel<V, true><<<(unsigned)a.T, a.nt, 0, stream>>>(a);
   else
-    block_norm_kernel<V, false><<<(unsigned)a.T, nt, 0, stream>>>(a);
+    block_norm_kernel<V, false><<<(unsigned)a.T, a.nt, 0, stream>>>(a);
   return hipGetLastError();
 }
 

@@ -224,6 +224,7 @@ struct BlockNormArgs {
   int64_t gate_row;
   int gate_col;
   int T, H;
+  int nt;                     // threads of a workgroup, set by the launcher
   void* resid_out;            // rows ld_ro apart
   int64_t ld_ro;
   void* next;                 // bf16, rows ld_next apart
