@@ -93,6 +93,8 @@ class NVFP4MoEError(RuntimeError):
 def load(path: str = LIB_PATH):
     """Load (once) and return the ctypes library with every signature declared."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):

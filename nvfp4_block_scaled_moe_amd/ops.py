@@ -461,7 +461,7 @@ def _gpu(fn: str, *ts) -> int:
 
 def _on(index: int):
     """The tensors' GPU made current for the call (launches go to the current one)."""
-    return _NO_GUARD if torch.cuda.current_device() == index else torch.cuda.device(index)
+    return _NO_GUARD if torch._C._cuda_getDevice() == index else torch.cuda.device(index)
 
 
 def _raw_stream(index: int) -> int:
@@ -608,60 +608,80 @@ def moe_block_norm(resid: torch.Tensor, y: torch.Tensor | None = None, *, post_w
     if resid.dim() != 2:
         raise ValueError(f"{fn}: resid must be [T, H], got {tuple(resid.shape)}")
     T, H = resid.shape
-    for t in (resid, y, y_add, gate, post_w, pre_w):
-        if t is not None and t.dtype not in _DT:
-            raise ValueError(f"{fn}: resid, y, y_add, gate and the weights must be float32 or bf16, got {t.dtype}")
-    for w in (post_w, pre_w):
-        if w is not None and w.shape != (H,):
-            raise ValueError(f"{fn}: the weights must be [{H}], got {tuple(w.shape)}")
     if post_w is not None and pre_w is not None and post_w.dtype != pre_w.dtype:
         post_w, pre_w = post_w.float(), pre_w.float()
+    r_dt = _float_type(fn, resid)
+    p_y = p_add = p_rows = p_topk = p_post = p_pre = p_gate = p_ro = p_next = None
+    y_dt = add_dt = w_dt = gate_dt = F32
+    ld_y = ld_add = k = gate_row = gate_col = ld_ro = ld_next = 0
     with _on(idx):
         resid, ld_r = _rows(fn, "resid", resid, H, 8) if resid_out is not resid else \
             (resid, resid.stride(0) if T > 1 else H)
-        post_w, pre_w = _aligned(post_w), _aligned(pre_w)
-        ld_y = ld_ya = k = 0
+        if post_w is not None:
+            post_w, p_post, w_dt = _weight(fn, post_w, H)
+        if pre_w is not None:
+            pre_w, p_pre, w_dt = _weight(fn, pre_w, H)
+            next_out, ld_next = _out_rows(fn, next_out, T, H, torch.bfloat16, resid)
+            if next_out.dtype != torch.bfloat16:
+                raise ValueError(f"{fn}: next_out must be bf16")
+            p_next = next_out.data_ptr()
         if y_add is not None:
-            y_add, ld_ya = _rows(fn, "y_add", y_add, H, 8)
+            add_dt = _float_type(fn, y_add)
+            y_add, ld_add = _rows(fn, "y_add", y_add, H, 8)
             if y_add.shape[0] != T:
                 raise ValueError(f"{fn}: y_add must be [{T}, {H}], got {tuple(y_add.shape)}")
+            p_add = y_add.data_ptr()
         if y is not None:
+            y_dt = _float_type(fn, y)
             y, ld_y = _rows(fn, "y", y, H, 8)
+            p_y = y.data_ptr()
             if topk_w is not None and slot_to_row is not None:
                 if topk_w.dtype != torch.float32 or not topk_w.is_contiguous():
                     topk_w = topk_w.float().contiguous()
                 slot_to_row = slot_to_row.contiguous()
+                n = topk_w.numel()
                 if topk_w.dim() != 2 or topk_w.shape[0] != T or slot_to_row.dtype != torch.int32 or \
-                        slot_to_row.numel() != topk_w.numel() or y.shape[0] != topk_w.numel():
+                        slot_to_row.numel() != n or y.shape[0] != n:
                     raise ValueError(f"{fn}: topk_w must be [{T}, k], slot_to_row int32 [{T} * k] and y [{T} * k, {H}]")
                 k = topk_w.shape[1]
             elif y.shape[0] != T:
                 raise ValueError(f"{fn}: y must be [{T}, {H}], got {tuple(y.shape)}")
-        gate_row = gate_col = 0
-        if gate is not None:
-            if gate.shape not in ((H,), (T, 1), (T, H)):
-                raise ValueError(f"{fn}: gate must be [{H}], [{T}, 1] or [{T}, {H}], got {tuple(gate.shape)}")
-            gate, gate_row, gate_col = _gate(gate, T, H)
-        ld_ro = ld_n = 0
-        if y is not None:
             resid_out, ld_ro = _out_rows(fn, resid_out, T, H, resid.dtype, resid)
             if resid_out.dtype != resid.dtype:
                 raise ValueError(f"{fn}: resid_out must have resid's type")
-        if pre_w is not None:
-            next_out, ld_n = _out_rows(fn, next_out, T, H, torch.bfloat16, resid)
-            if next_out.dtype != torch.bfloat16:
-                raise ValueError(f"{fn}: next_out must be bf16")
-        wt = post_w if post_w is not None else pre_w
-        ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+            p_ro = resid_out.data_ptr()
+        if slot_to_row is not None:
+            p_rows = slot_to_row.data_ptr()
+        if topk_w is not None:
+            p_topk = topk_w.data_ptr()
+        if gate is not None:
+            if gate.shape not in ((H,), (T, 1), (T, H)):
+                raise ValueError(f"{fn}: gate must be [{H}], [{T}, 1] or [{T}, {H}], got {tuple(gate.shape)}")
+            gate_dt = _float_type(fn, gate)
+            gate, gate_row, gate_col = _gate(gate, T, H)
+            p_gate = gate.data_ptr()
         st = _lib.load().moe_block_norm(
-            resid.data_ptr(), _DT[resid.dtype], ld_r, ptr(y), F32 if y is None else _DT[y.dtype], ld_y,
-            ptr(y_add), F32 if y_add is None else _DT[y_add.dtype], ld_ya, ptr(slot_to_row), ptr(topk_w), k,
-            ptr(post_w), ptr(pre_w), F32 if wt is None else _DT[wt.dtype], w_offset, eps, ptr(gate),
-            F32 if gate is None else _DT[gate.dtype], gate_row, gate_col, scale, T, H,
-            ptr(resid_out) if y is not None else None, ld_ro, ptr(next_out) if pre_w is not None else None, ld_n,
+            resid.data_ptr(), r_dt, ld_r, p_y, y_dt, ld_y, p_add, add_dt, ld_add, p_rows, p_topk, k, p_post, p_pre,
+            w_dt, w_offset, eps, p_gate, gate_dt, gate_row, gate_col, scale, T, H, p_ro, ld_ro, p_next, ld_next,
             _raw_stream(idx))
-    _lib.check(fn, st)
-    return (resid_out if y is not None else None), (next_out if pre_w is not None else None)
+    if st:
+        _lib.check(fn, st)
+    return (None if y is None else resid_out), (None if pre_w is None else next_out)
+
+
+def _float_type(fn: str, t) -> int:
+    dt = _DT.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{fn}: resid, y, y_add, gate and the weights must be float32 or bf16, got {t.dtype}")
+    return dt
+
+
+def _weight(fn: str, w, H: int):
+    """(w, address, type) of a norm's weight [H]."""
+    if w.shape != (H,):
+        raise ValueError(f"{fn}: the weights must be [{H}], got {tuple(w.shape)}")
+    w = _aligned(w)
+    return w, w.data_ptr(), _float_type(fn, w)
 
 
 def _aligned(t):
