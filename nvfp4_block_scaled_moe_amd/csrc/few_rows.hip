@@ -137,14 +137,19 @@ template <bool MX>
 __device__ __forceinline__ uint32_t scale_of(uint32_t dword, uint32_t c) {
   return MX ? (dword >> (8u * (c & 3))) & 0xffu : dword >> (16u * (c & 1));
 }
-__device__ __forceinline__ uint32_t ld32(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-  return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+__device__ __forceinline__ uint32_t ld32(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff = 0) {
+  return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, voff, soff, 0);
 }
 // An offset as a value of its own: keeps the compiler from turning a select of offsets into
 // branches with a load in each, after which it could only wait for all loads at once.
 __device__ __forceinline__ uint32_t settled(uint32_t off) {
   asm("" : "+v"(off));
   return off;
+}
+__device__ __forceinline__ int settled_s(int v) {   // (the same in every lane)
+  v = __builtin_amdgcn_readfirstlane(v);
+  asm("" : "+s"(v));
+  return v;
 }
 
 // Eight bf16 elements of each of two rows' chunks, a chunk held by 16 lanes together, as f16
@@ -291,12 +296,23 @@ __device__ __forceinline__ void put_matvec(const FewArgs& p, int col, size_t n0,
     static_cast<float*>(p.out)[o] = v;
 }
 
-// An even split of `total` things over n takers, the first `more` of them with one more. In 32
-// bits: the kernels run this code once, from a cold instruction cache, and its length is time
-// (about 2 bytes a nanosecond before the first tile).
+// What every wave does once before its first load is paid sixteen times over: the four waves of a
+// SIMD share one scalar unit and take turns (four cycles an instruction), and the code comes from a
+// cold instruction cache (about 2 bytes a nanosecond). So: 32 bits, no division by a variable (25
+// instructions each).
+//
+// x / d from inv = floor(2^32 / d), at most 2^32 - 1 (inverse() below): x inv / 2^32 is less than
+// x / d by at most x / 2^32 < 1, so that its whole part is the quotient or one less.
+__device__ __forceinline__ uint32_t quotient(uint32_t x, uint32_t d, uint32_t inv) {
+  const uint32_t q = (uint32_t)(((uint64_t)x * inv) >> 32);
+  return q + (x - q * d >= d ? 1u : 0u);
+}
+
+// An even split of `total` things over n takers, the first `more` of them with one more.
 struct Share {
   uint32_t each, more;
-  __device__ __forceinline__ Share(uint32_t total, uint32_t n) : each(total / n), more(total - total / n * n) {}
+  __device__ __forceinline__ Share(uint32_t total, uint32_t n, uint32_t each_) : each(each_), more(total - each_ * n) {}
+  __device__ __forceinline__ Share(uint32_t total, uint32_t n) : Share(total, n, total / n) {}
   __device__ __forceinline__ uint32_t begin(uint32_t i) const { return i * each + (i < more ? i : more); }
   // The taker of thing x.
   __device__ __forceinline__ uint32_t taker(uint32_t x) const {
@@ -348,12 +364,13 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
   const int T = p.T, K = p.K;
   const uint32_t nch = (uint32_t)(K + kChunk - 1) / kChunk;
   const uint32_t stride = nch * 256u + 16u;              // LDS bytes of a row
-  const int KS = 1 << p.ks_log, RG = kW >> p.ks_log;
+  static_assert(kW == 16, "4 - ks_log");
+  const int KS = 1 << p.ks_log, rg_log = 4 - p.ks_log, RG = 1 << rg_log;
   const int ksl = wave & (KS - 1), rg = wave >> p.ks_log;
   const int cpw = ((int)nch + KS - 1) >> p.ks_log;       // chunks of a tile for each wave
   const uint32_t nblk = (uint32_t)p.Nw / 16;             // row blocks of a matrix
-  const int nsub = SWIGLU ? (int)nblk / 2 : ((int)nblk + RB - 1) / RB;
-  const int tpi = (nsub + RG - 1) / RG;                  // tiles of an item
+  const int nsub = (int)(SWIGLU ? nblk / 2 : (nblk + RB - 1) / RB);
+  const int tpi = (nsub + RG - 1) >> rg_log;             // tiles of an item
   const uint32_t wbytes = nblk * nch * 1024u;
   const uint32_t sbytes = nblk * (MX ? (nch + 15) >> 4 : (nch + 7) >> 3) * 1024u;
   const bool all_rows = !LAYER || T <= p.item_tok;       // every row fits: staged once
@@ -558,7 +575,8 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
   // ---- this workgroup's tiles, in runs of one item's: a flat sequence of steps (a chunk of RB
   // weight tiles), D of them a turn of the ring. A tile takes at least D steps, so that at most
   // one is completed in a turn; a run is padded to whole turns.
-  const Share share((uint32_t)nitems * (uint32_t)tpi, (uint32_t)p.grid);
+  const uint32_t ntile = (uint32_t)nitems * (uint32_t)tpi;
+  const Share share(ntile, (uint32_t)p.grid, quotient(ntile, (uint32_t)p.grid, p.grid_inv));
   const int t0 = (int)share.begin(blockIdx.x), t1 = (int)share.begin(blockIdx.x + 1);
   if (t0 >= t1) return;   // fewer tiles than workgroups
 
@@ -566,54 +584,69 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
   auto item_word = [&](int it) -> uint32_t {
     return LAYER ? (uint32_t)__builtin_amdgcn_readfirstlane((int)s_item[it]) : (1u << T) - 1u;
   };
-  const int spt = cpw > D ? cpw : D;   // steps of a tile
-  // The loads' position: the item, its row block group and chunk, and the steps left of the run.
-  int it_l = t0 / tpi, tile_l = t0 - it_l * tpi, tiles_l = t1 - t0, sub_l = 0, step_l = 0, steps_l = 0;
-  uint32_t c_l = 0, woff_l = 0, soff_l = 0;   // chunk; offsets of the group's first block
   const uint32_t wrow = nch * 1024u, srow = (MX ? (nch + 15) >> 4 : (nch + 7) >> 3) * 1024u;   // of a row block
   constexpr uint32_t NS = SWIGLU ? 1 : RB;      // a group's blocks (gate or up ones, or all)
   const uint32_t next = SWIGLU ? nblk / 2 : 1;  // from a group's first block to its second
+  // The chunk of a wave runs from ksl in steps of KS; a tile takes cpw of them, or D.
+  const uint32_t cend = (uint32_t)ksl + ((uint32_t)(cpw > D ? cpw : D) << p.ks_log);
+  const int spt = cpw > D ? cpw : D;   // steps of a tile
+  // Of a run of n tiles from `tile` on, those in which this wave has a group of row blocks (the
+  // last tile's groups may end before it), and those in which the group is whole.
+  auto tiles_of = [&](int tile, int n) { return min(n, (nsub - tile * RG - rg + RG - 1) >> rg_log); };
+  auto whole_of = [&](int tile, int n, int own) {
+    return !SWIGLU && RB > 1 && (nblk & 1) && (tile + own - 1) * RG + rg == nsub - 1 ? own - 1 : own;
+  };
+  static_assert(RB == 2, "a group is whole or lacks its second block");
+  // The loads' position: the item and the tiles left behind the run; in the run the tile, of n_l,
+  // and its first block's bytes; and the chunk.
+  int it_l = LAYER ? (int)quotient((uint32_t)t0, (uint32_t)tpi, p.tpi_inv) : 0;
+  int tile_l = t0 - it_l * tpi, tiles_l = t1 - t0, at_l = 0, n_l = 0, own_l = 0, whole_l = 0;
+  uint32_t c_l = 0, woff_l = 0, soff_l = 0;
+  const uint32_t wstep = (uint32_t)RG * NS * wrow, sstep = (uint32_t)RG * NS * srow;
   auto open_run = [&]() {
     const size_t e = LAYER ? item_word(it_l) >> 16 : 0;
     wr = make_rsrc(p.codes + e * wbytes, wbytes);
     sr = make_rsrc(p.scales + e * sbytes, sbytes);
-    const int n = min(tiles_l, tpi - tile_l);
-    tiles_l -= n;
-    steps_l = n * spt;
-    sub_l = tile_l * RG + rg;
-    step_l = 0;
+    n_l = min(tiles_l, tpi - tile_l);
+    tiles_l -= n_l;
+    at_l = 0;
+    own_l = tiles_of(tile_l, n_l);
+    whole_l = whole_of(tile_l, n_l, own_l);
     c_l = (uint32_t)ksl;
-    woff_l = (uint32_t)sub_l * NS * wrow;
-    soff_l = (uint32_t)sub_l * NS * srow;
+    woff_l = (uint32_t)(tile_l * RG + rg) * NS * wrow;
+    soff_l = (uint32_t)(tile_l * RG + rg) * NS * srow;
     tile_l = 0;
     ++it_l;
   };
   u32x4 wring[D][RB];
   uint32_t sring[D][RB];
+  const uint32_t lane16 = 16u * lane;
   auto issue = [&](int d) {
-    const bool ok = steps_l > 0 && c_l < nch && sub_l < nsub;
-    const uint32_t wo = woff_l + c_l * 1024u, so = soff_l + scale_off<MX>(c_l);
-#pragma unroll
-    for (int b = 0; b < RB; ++b) {
-      const bool in = ok && (SWIGLU || b == 0 || (uint32_t)sub_l * RB + b < nblk);
-      wring[d][b] = ld128(wr, settled(16u * lane + (in ? wo + b * next * wrow : kOOB)), 0);
-      sring[d][b] = ld32(sr, settled(16u * lane + (in ? so + b * next * srow : kOOB)));
-    }
-    // (arithmetic instead of branches: a branch here would send the position through memory)
-    const bool wrap = step_l + 1 == spt;
-    step_l = wrap ? 0 : step_l + 1;
-    c_l = wrap ? (uint32_t)ksl : c_l + (uint32_t)KS;
-    sub_l += wrap ? RG : 0;
-    woff_l += wrap ? (uint32_t)RG * NS * wrow : 0u;
-    soff_l += wrap ? (uint32_t)RG * NS * srow : 0u;
-    --steps_l;
+    // A step without a chunk loads from out of range. (Its scalar offset is 0: one past the
+    // resource's end would wrap the hardware's comparison.) All in sign masks: of selects the
+    // compiler makes branches, a load in each, or sends the position through memory.
+    const int in0 = settled_s((int)(c_l - nch) & (at_l - own_l));   // negative: there is a chunk,
+    const int in1 = SWIGLU ? in0 : settled_s((int)(c_l - nch) & (at_l - whole_l));   // also of the second block
+    const uint32_t v0 = settled(lane16 | (kOOB & ~(uint32_t)in0)), v1 = SWIGLU ? v0 : settled(lane16 | (kOOB & ~(uint32_t)in1));
+    const uint32_t w0 = (woff_l + c_l * 1024u) & (uint32_t)(in0 >> 31);
+    const uint32_t s0 = (soff_l + scale_off<MX>(c_l)) & (uint32_t)(in0 >> 31);
+    wring[d][0] = ld128(wr, v0, w0);
+    wring[d][1] = ld128(wr, v1, (w0 + next * wrow) & (uint32_t)(in1 >> 31));
+    sring[d][0] = ld32(sr, v0, s0);
+    sring[d][1] = ld32(sr, v1, (s0 + next * srow) & (uint32_t)(in1 >> 31));
+    c_l += (uint32_t)KS;
+    const uint32_t wrap = ~(uint32_t)settled_s((int)(c_l - cend) >> 31);   // all ones at the tile's end
+    c_l -= wrap & (cend - (uint32_t)ksl);
+    at_l -= (int)wrap;
+    woff_l += wrap & wstep;
+    soff_l += wrap & sstep;
   };
 
   int it = it_l, tile = tile_l, left = t1 - t0, buf = 0, done = 0;
   open_run();
   // Fill the ring. (After each turn the next run is opened where this one's loads have ended.)
   auto next_run = [&]() {
-    if (steps_l <= 0 && tiles_l > 0) open_run();
+    if (at_l >= n_l && tiles_l > 0) open_run();
   };
   // The layer's rows have arrived and go to LDS first (a wave whose loads find no room waits for
   // the others' to return); a matvec's are requested first and looked at behind the ring's loads.
@@ -672,15 +705,15 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
     };
     const uint32_t frow = settled(row_of(l16) * stride + 64u * g);
     const float alpha = MX ? 1.0f : ld_const(p.g, LAYER ? word >> 16 : 0);
-    const int run = min(left, tpi - tile), nst = run * spt, turns = (nst + D - 1) / D;
+    const int run = min(left, tpi - tile), own = tiles_of(tile, run);
     left -= run;
-    int step = 0, sub = tile * RG + rg;
+    int at = 0;
     uint32_t c = (uint32_t)ksl;
-    for (int turn = 0; turn < turns; ++turn) {
+    for (int steps = run * spt; steps > 0; steps -= D) {
       int ready = 0;
 #pragma unroll
       for (int d = 0; d < D; ++d) {
-        if (turn * D + d < nst && c < nch && sub < nsub) {
+        if (c < nch && at < own) {
           Op bf[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) bf[j] = *reinterpret_cast<const Op*>(s_rows + frow + c * 256u + 16 * j);
@@ -693,11 +726,10 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
           }
         }
         issue(d);
-        const bool wrap = step + 1 == spt;
-        step = wrap ? 0 : step + 1;
-        c = wrap ? (uint32_t)ksl : c + (uint32_t)KS;
-        sub += wrap ? RG : 0;
-        if (wrap && turn * D + d < nst) {   // a tile is complete: this wave's sums
+        c += (uint32_t)KS;
+        const bool wrap = c == cend;
+        c = wrap ? (uint32_t)ksl : c;
+        if (wrap && at++ < run) {   // a tile is complete: this wave's sums
           ready = 1;
           if (l16 < NTOK) {
 #pragma unroll
@@ -1285,6 +1317,9 @@ uint32_t ppr_inverse(int K) {
   return (uint32_t)(((uint64_t(1) << 32) + ppr - 1) / ppr);
 }
 
+// For quotient().
+uint32_t inverse(uint32_t d) { return d == 1 ? 0xffffffffu : (uint32_t)((uint64_t(1) << 32) / d); }
+
 template <bool MX, bool LAYER, bool FP8, bool SWIGLU, int NTOK, int RB, int D>
 hipError_t launch_up(FewArgs a, int rows, int grid, hipStream_t stream) {
   static std::atomic<uint64_t> done{0};
@@ -1293,6 +1328,9 @@ hipError_t launch_up(FewArgs a, int rows, int grid, hipStream_t stream) {
   if (e != hipSuccess) return e;
   a.ppr_inv = ppr_inverse(a.K);
   a.grid = grid;
+  a.grid_inv = inverse(grid);
+  const int rg = kW >> a.ks_log, nsub = SWIGLU ? a.Nw / 32 : (a.Nw / 16 + RB - 1) / RB;
+  a.tpi_inv = inverse((nsub + rg - 1) / rg);
   kernel<<<grid, kNT, rows * row_lds_bytes(a.K), stream>>>(a);
   return hipGetLastError();
 }

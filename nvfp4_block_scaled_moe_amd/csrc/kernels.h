@@ -182,14 +182,17 @@ struct FewArgs {
   int64_t ld_add;
   void* out;              // matvec: float32 or bf16; the layer's second launch: bf16
   int out_bf16;
+  uint32_t grid_inv;      // set by the launcher: inverse() of grid,
   int64_t ld_out;
   const float* logits;    // layer: [T, E]
   int E, k;
   const float* g_down;    // layer, NVFP4: global scales of the second matrices
   int fp8;                // layer, NVFP4: the rows first take the FP8 E4M3 round trip
+  uint32_t tpi_inv;       //   of an item's tiles (first launch), and
   FewPlan* plan;          // layer workspace
   void* h;                // [T * k, F] f16 (NVFP4) or bf16 (MXFP4)
   int down_tiles;         // tiles of the second launch
+  uint32_t nch_inv;       //   of the chunks of a row (second launch)
   float* part;            // [down_tiles, most_parts, 32 T] sums of a tile that workgroups share
   int most_parts;
   int8_t* hexp;           // NVFP4: [T * k, 8 ceil(F / 128)] exponents of h's blocks of 16 columns
