@@ -1019,7 +1019,7 @@ nvfp4moe_status few_layer(const char* fn, bool mx, const float* logits, const vo
   up.plan = reinterpret_cast<FewPlan*>(base);
   up.h = base + lay.plan;
   up.hexp = mx ? nullptr : reinterpret_cast<int8_t*>(base + lay.plan + lay.h);
-  up.down_tiles = H / (16 * kFewDownBlocks);
+  up.down_tiles = H / (16 * few_down_blocks(T, k, H, F));
   up.part = reinterpret_cast<float*>(base + lay.plan + lay.h + lay.hexp);
   up.most_parts = few_down_parts(T, k, H, F);
   FewArgs down = up;

@@ -336,11 +336,11 @@ __device__ __forceinline__ void fetch_args(const FewArgs& p) {
 // 16-byte pieces of the rows a thread requests together: one row seldom has more than one for each.
 constexpr int pass_batch(int ntok) { return ntok > 4 ? 4 : 1; }
 
-template <bool MX, bool LAYER, bool FP8, bool SWIGLU, int NTOK, int RB, int D>
+template <bool MX, bool LAYER, bool FP8, bool SWIGLU, int NTOK, int D>
 __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
   typedef Decode<MX> Dec;
   typedef typename Dec::Op Op;
-  static_assert(!SWIGLU || RB == 2, "a gate block and its up block");
+  constexpr int RB = SWIGLU ? 2 : 1;   // row blocks of a wave: one, or a gate block and its up block
   static_assert(!LAYER || (SWIGLU && NTOK == kItemTok), "the layer's items");
   static_assert(!FP8 || (LAYER && !MX), "FP8 activations: the NVFP4 layer");
   constexpr int BUF = NTOK > 4 ? 1 : 2;
@@ -369,7 +369,7 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
   const int ksl = wave & (KS - 1), rg = wave >> p.ks_log;
   const int cpw = ((int)nch + KS - 1) >> p.ks_log;       // chunks of a tile for each wave
   const uint32_t nblk = (uint32_t)p.Nw / 16;             // row blocks of a matrix
-  const int nsub = (int)(SWIGLU ? nblk / 2 : (nblk + RB - 1) / RB);
+  const int nsub = (int)nblk / RB;                       // groups: a row block, or a gate block and its up block
   const int tpi = (nsub + RG - 1) >> rg_log;             // tiles of an item
   const uint32_t wbytes = nblk * nch * 1024u;
   const uint32_t sbytes = nblk * (MX ? (nch + 15) >> 4 : (nch + 7) >> 3) * 1024u;
@@ -585,24 +585,19 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
     return LAYER ? (uint32_t)__builtin_amdgcn_readfirstlane((int)s_item[it]) : (1u << T) - 1u;
   };
   const uint32_t wrow = nch * 1024u, srow = (MX ? (nch + 15) >> 4 : (nch + 7) >> 3) * 1024u;   // of a row block
-  constexpr uint32_t NS = SWIGLU ? 1 : RB;      // a group's blocks (gate or up ones, or all)
-  const uint32_t next = SWIGLU ? nblk / 2 : 1;  // from a group's first block to its second
+  const uint32_t half = nblk / 2;   // SwiGLU: from a group's gate block to its up block
   // The chunk of a wave runs from ksl in steps of KS; a tile takes cpw of them, or D.
   const uint32_t cend = (uint32_t)ksl + ((uint32_t)(cpw > D ? cpw : D) << p.ks_log);
   const int spt = cpw > D ? cpw : D;   // steps of a tile
   // Of a run of n tiles from `tile` on, those in which this wave has a group of row blocks (the
-  // last tile's groups may end before it), and those in which the group is whole.
+  // last tile's groups may end before it).
   auto tiles_of = [&](int tile, int n) { return min(n, (nsub - tile * RG - rg + RG - 1) >> rg_log); };
-  auto whole_of = [&](int tile, int n, int own) {
-    return !SWIGLU && RB > 1 && (nblk & 1) && (tile + own - 1) * RG + rg == nsub - 1 ? own - 1 : own;
-  };
-  static_assert(RB == 2, "a group is whole or lacks its second block");
   // The loads' position: the item and the tiles left behind the run; in the run the tile, of n_l,
   // and its first block's bytes; and the chunk.
   int it_l = LAYER ? (int)quotient((uint32_t)t0, (uint32_t)tpi, p.tpi_inv) : 0;
-  int tile_l = t0 - it_l * tpi, tiles_l = t1 - t0, at_l = 0, n_l = 0, own_l = 0, whole_l = 0;
+  int tile_l = t0 - it_l * tpi, tiles_l = t1 - t0, at_l = 0, n_l = 0, own_l = 0;
   uint32_t c_l = 0, woff_l = 0, soff_l = 0;
-  const uint32_t wstep = (uint32_t)RG * NS * wrow, sstep = (uint32_t)RG * NS * srow;
+  const uint32_t wstep = (uint32_t)RG * wrow, sstep = (uint32_t)RG * srow;
   auto open_run = [&]() {
     const size_t e = LAYER ? item_word(it_l) >> 16 : 0;
     wr = make_rsrc(p.codes + e * wbytes, wbytes);
@@ -611,10 +606,9 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
     tiles_l -= n_l;
     at_l = 0;
     own_l = tiles_of(tile_l, n_l);
-    whole_l = whole_of(tile_l, n_l, own_l);
     c_l = (uint32_t)ksl;
-    woff_l = (uint32_t)(tile_l * RG + rg) * NS * wrow;
-    soff_l = (uint32_t)(tile_l * RG + rg) * NS * srow;
+    woff_l = (uint32_t)(tile_l * RG + rg) * wrow;
+    soff_l = (uint32_t)(tile_l * RG + rg) * srow;
     tile_l = 0;
     ++it_l;
   };
@@ -625,15 +619,14 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
     // A step without a chunk loads from out of range. (Its scalar offset is 0: one past the
     // resource's end would wrap the hardware's comparison.) All in sign masks: of selects the
     // compiler makes branches, a load in each, or sends the position through memory.
-    const int in0 = settled_s((int)(c_l - nch) & (at_l - own_l));   // negative: there is a chunk,
-    const int in1 = SWIGLU ? in0 : settled_s((int)(c_l - nch) & (at_l - whole_l));   // also of the second block
-    const uint32_t v0 = settled(lane16 | (kOOB & ~(uint32_t)in0)), v1 = SWIGLU ? v0 : settled(lane16 | (kOOB & ~(uint32_t)in1));
-    const uint32_t w0 = (woff_l + c_l * 1024u) & (uint32_t)(in0 >> 31);
-    const uint32_t s0 = (soff_l + scale_off<MX>(c_l)) & (uint32_t)(in0 >> 31);
-    wring[d][0] = ld128(wr, v0, w0);
-    wring[d][1] = ld128(wr, v1, (w0 + next * wrow) & (uint32_t)(in1 >> 31));
-    sring[d][0] = ld32(sr, v0, s0);
-    sring[d][1] = ld32(sr, v1, (s0 + next * srow) & (uint32_t)(in1 >> 31));
+    const int in = settled_s((int)(c_l - nch) & (at_l - own_l));   // negative: there is a chunk
+    const uint32_t v = settled(lane16 | (kOOB & ~(uint32_t)in)), all = (uint32_t)(in >> 31);
+    const uint32_t w0 = (woff_l + c_l * 1024u) & all, s0 = (soff_l + scale_off<MX>(c_l)) & all;
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      wring[d][b] = ld128(wr, v, w0 + (b ? half * wrow & all : 0u));
+      sring[d][b] = ld32(sr, v, s0 + (b ? half * srow & all : 0u));
+    }
     c_l += (uint32_t)KS;
     const uint32_t wrap = ~(uint32_t)settled_s((int)(c_l - cend) >> 31);   // all ones at the tile's end
     c_l -= wrap & (cend - (uint32_t)ksl);
@@ -745,13 +738,12 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
         // ---- the waves' sums together, and the epilogue
         __syncthreads();
         const float* red = s_red[buf];
-        constexpr int NB = SWIGLU ? 1 : RB;
         const int lcol = ncol > 1 ? 32 - __builtin_clz(ncol - 1) : 0;   // columns, to a power of two
-        const int total = (RG * NB * 16) << lcol;
+        const int total = (RG * 16) << lcol;
         // a different wave starts each tile, so that short epilogues spread over the SIMDs
         for (int i = (tid + kWave * done) & (kNT - 1); i < total; i += kNT) {
           const int r16 = i & 15, q = i >> 4;
-          const int grp = (q >> lcol) / NB, b = (q >> lcol) % NB, col = q & ((1 << lcol) - 1);
+          const int grp = q >> lcol, col = q & ((1 << lcol) - 1);
           if (col >= ncol) continue;   // (16 lanes at a time)
           const int osub = tile * RG + grp;
           float v = 0.0f, u = 0.0f;
@@ -760,7 +752,7 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
             float av[4], au[4];
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              const float* a = &red[(((grp * KS + (w0 + w < KS ? w0 + w : w0)) * RB + b) * NTOK + col) * 16 + r16];
+              const float* a = &red[(((grp * KS + (w0 + w < KS ? w0 + w : w0)) * RB) * NTOK + col) * 16 + r16];
               av[w] = a[0];
               au[w] = SWIGLU ? a[NTOK * 16] : 0.0f;
             }
@@ -786,8 +778,8 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
                 if (r16 == 0) p.hexp[(size_t)hr * (nch_of(F) * 8) + osub] = (int8_t)e2;
               }
             }
-          } else if (osub < nsub && tile_block_in<SWIGLU, RB>(osub, b, nblk)) {
-            put_matvec(p, col, (size_t)tile_block<SWIGLU, RB>(osub, b, nblk) * 16 + r16, v);
+          } else if (osub < nsub) {
+            put_matvec(p, col, (size_t)osub * 16 + r16, v);
           }
         }
         if (BUF == 1) __syncthreads();
@@ -805,8 +797,8 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
 // Up to 16 rows of any length: each wave turns its chunk of the rows itself, in a piece of LDS of
 // its own, with a power of two for every (row, chunk). The turning costs about as much as the
 // decode of four weight tiles, so a wave takes up to RB = 8 row blocks a chunk.
-template <bool MX, bool SWIGLU, int RB, int D, int WPS>
-__global__ __launch_bounds__(kLongNT, WPS) void few_long_kernel(const FewArgs p) {
+template <bool MX, bool SWIGLU, int RB, int D>
+__global__ __launch_bounds__(kLongNT, 4) void few_long_kernel(const FewArgs p) {
   typedef Decode<MX> Dec;
   typedef typename Dec::Op Op;
   constexpr int R = kFewMaxTokens / 4;
@@ -1053,11 +1045,11 @@ __global__ __launch_bounds__(W* kWave, 4) void few_wide_kernel(const FewArgs p) 
 // same number of bytes, which whole tiles seldom give (192 tiles on 256 CUs: three quarters of
 // the rate). A tile that several workgroups have part of is finished by the last of them to
 // arrive, which adds the parts in order; nobody waits.
-template <bool MX, int D>
+template <bool MX, int RB>
 __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
+  constexpr int D = 2;   // chunks of a wave under way (3: a per cent or two slower, 4: spills)
   typedef Decode<MX> Dec;
   typedef typename Dec::Op Op;
-  constexpr int RB = kFewDownBlocks;
   static_assert(kFewMaxSlots <= kNT, "a thread for each row and item");
   __shared__ __attribute__((aligned(16))) unsigned char s_row[kW][kItemTok * kRowBytes];
   __shared__ __attribute__((aligned(16))) float s_red[kW * RB][16 * 16];
@@ -1293,14 +1285,23 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
   }
 }
 
-// Chunks dealt out at a time (log2): as many as leave every wave four or more of a tile's, and
-// more where the tiles would not fill the CUs otherwise. sub: row block groups of all items.
+// Chunks dealt out at a time (log2): at least as many as leave every wave four or more of a tile's;
+// of those the one with which the busiest CU has the fewest row block groups (more chunks at a time
+// give more, smaller tiles), and of equal ones the one with the fewest tiles. sub: groups of all items.
+// (6144 x 2048, one row: 192 tiles of two groups 5.3 us, 384 tiles of one 6.7. Layer of 2 tokens, 60
+// experts, 2080 x 1376: 688 tiles of one group 25.5 us, 344 of two 26.4.)
 int ks_log_for(int K, int64_t sub) {
   const int nch = nch_of(K);
   int l = 0;
   while (l < 4 && (nch >> (l + 1)) >= 4) ++l;
-  while (l < 4 && (1 << (l + 1)) <= nch && (sub << l) / kW < kGrid) ++l;
-  return l;
+  auto most = [&](int k) {
+    const int64_t tiles = ((sub << k) + kW - 1) / kW;
+    return (tiles + kGrid - 1) / kGrid * (kW >> k);
+  };
+  int best = l;
+  while (l < 4 && (1 << (l + 1)) <= nch)
+    if (most(++l) < most(best)) best = l;
+  return best;
 }
 
 // LDS for resident rows: what the rest leaves of a CU's 160 KB.
@@ -1320,45 +1321,42 @@ uint32_t ppr_inverse(int K) {
 // For quotient().
 uint32_t inverse(uint32_t d) { return d == 1 ? 0xffffffffu : (uint32_t)((uint64_t(1) << 32) / d); }
 
-template <bool MX, bool LAYER, bool FP8, bool SWIGLU, int NTOK, int RB, int D>
+template <bool MX, bool LAYER, bool FP8, bool SWIGLU, int NTOK, int D>
 hipError_t launch_up(FewArgs a, int rows, int grid, hipStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  auto* kernel = few_up_kernel<MX, LAYER, FP8, SWIGLU, NTOK, RB, D>;
+  auto* kernel = few_up_kernel<MX, LAYER, FP8, SWIGLU, NTOK, D>;
   const hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(kernel), kResidentBytes + 16 * 16, done);
   if (e != hipSuccess) return e;
   a.ppr_inv = ppr_inverse(a.K);
   a.grid = grid;
   a.grid_inv = inverse(grid);
-  const int rg = kW >> a.ks_log, nsub = SWIGLU ? a.Nw / 32 : (a.Nw / 16 + RB - 1) / RB;
+  const int rg = kW >> a.ks_log, nsub = a.Nw / (SWIGLU ? 32 : 16);
   a.tpi_inv = inverse((nsub + rg - 1) / rg);
   kernel<<<grid, kNT, rows * row_lds_bytes(a.K), stream>>>(a);
   return hipGetLastError();
 }
 
-// Depth of the ring: 4, and 2 where a wave has one or two chunks of a tile (a turn's code is then
-// half as long, and a tile always takes a turn).
-bool short_tiles(const FewArgs& a) { return (nch_of(a.K) - 1) >> a.ks_log < 2; }
-
+// Depth of the ring (chunks of a wave under way): 2, and 3 for the layer where a wave has three or more
+// chunks of a tile (one token, 8 experts of 6144 x 2048: 47.1 us, 2 47.8, 4 49.1). Deeper rings bring no
+// more: 16 waves' two chunks are half of what a CU can have under way, and their code is longer.
 template <bool MX, bool FP8>
 hipError_t launch_layer_up(const FewArgs& a, int rows, int grid, hipStream_t stream) {
-  return short_tiles(a) ? launch_up<MX, true, FP8, true, kItemTok, 2, 2>(a, rows, grid, stream)
-                        : launch_up<MX, true, FP8, true, kItemTok, 2, 4>(a, rows, grid, stream);
+  return (nch_of(a.K) - 1) >> a.ks_log < 2 ? launch_up<MX, true, FP8, true, kItemTok, 2>(a, rows, grid, stream)
+                                           : launch_up<MX, true, FP8, true, kItemTok, 3>(a, rows, grid, stream);
 }
 
-template <bool MX, bool SWIGLU, int NTOK, int RB, int D>
+template <bool MX, bool SWIGLU, int NTOK>
 hipError_t launch_mv(const FewArgs& a, hipStream_t stream) {
-  const int nblk = a.Nw / 16, rg = kW >> a.ks_log;
-  const int nsub = SWIGLU ? nblk / 2 : (nblk + RB - 1) / RB;
-  const int tiles = (nsub + rg - 1) / rg;
-  return launch_up<MX, false, false, SWIGLU, NTOK, RB, D>(a, a.T, tiles < kGrid ? tiles : kGrid, stream);
+  const int rg = kW >> a.ks_log, nsub = a.Nw / (SWIGLU ? 32 : 16), tiles = (nsub + rg - 1) / rg;
+  return launch_up<MX, false, false, SWIGLU, NTOK, 2>(a, a.T, tiles < kGrid ? tiles : kGrid, stream);
 }
 
-template <bool MX, bool SWIGLU, int RB, int D, int WPS>
+template <bool MX, bool SWIGLU, int RB, int D>
 hipError_t launch_long(FewArgs a, hipStream_t stream) {
   const int hb = SWIGLU ? RB / 2 : RB;
-  const int tiles = ((SWIGLU ? a.Nw / 32 : a.Nw / 16) + hb - 1) / hb, most = 128 * WPS / 2 * 2;
+  const int tiles = ((SWIGLU ? a.Nw / 32 : a.Nw / 16) + hb - 1) / hb, most = 2 * kGrid;
   a.grid = tiles < most ? tiles : most;
-  few_long_kernel<MX, SWIGLU, RB, D, WPS><<<a.grid, kLongNT, 0, stream>>>(a);
+  few_long_kernel<MX, SWIGLU, RB, D><<<a.grid, kLongNT, 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -1371,10 +1369,12 @@ hipError_t launch_wide(const FewArgs& a, hipStream_t stream) {
 
 template <bool MX, bool SWIGLU>
 hipError_t launch_mv_rows(const FewArgs& a, hipStream_t stream) {
+  // One row block a wave (two, gate and up, with SwiGLU): twice the workgroups of two a wave, which
+  // bring twice the reads under way: 2048 x 6144, one row 9.0 -> 6.9 us, 16384 x 6144 16.1 -> 14.8,
+  // 2048 x 2048, 16 rows 9.0 -> 7.3; slower only at 32768 x 1024 (7.9 -> 8.1).
+  constexpr int RB = SWIGLU ? 2 : 1;
   if (a.T <= resident_rows(a.K))
-    return a.T > 4          ? launch_mv<MX, SWIGLU, 16, 2, 4>(a, stream)
-           : short_tiles(a) ? launch_mv<MX, SWIGLU, 4, 2, 2>(a, stream)
-                            : launch_mv<MX, SWIGLU, 4, 2, 4>(a, stream);
+    return a.T > 4 ? launch_mv<MX, SWIGLU, 16>(a, stream) : launch_mv<MX, SWIGLU, 4>(a, stream);
   // Rows past the resident ones' LDS. More tiles than few_long_kernel has workgroups: the kernel
   // whose waves share the rows. T = 16, K = 6144, cold weights, few_long / few_wide, us:
   //   weight rows      16384       32768       65536       152064
@@ -1382,25 +1382,34 @@ hipError_t launch_mv_rows(const FewArgs& a, hipStream_t stream) {
   //   MXFP4          18.1 / 19.6  34.0 / 24.6  61.5 / 46.0  143 / 107
   //   SWIGLU, NVFP4  22.4 / 37    41.0 / 39.9  72.5 / 50.2  167 / 123
   const int tiles = SWIGLU ? a.Nw / 64 : a.Nw / 32;
-  if (tiles > 512) return launch_wide<MX, SWIGLU, SWIGLU ? 2 : 1, 8, 4>(a, stream);
-  return launch_long<MX, SWIGLU, 2, 2, 4>(a, stream);
+  if (tiles > 512) return launch_wide<MX, SWIGLU, RB, 8, 4>(a, stream);
+  if constexpr (!SWIGLU)
+    if (a.Nw / 16 <= kGrid) return launch_long<MX, SWIGLU, 1, 2>(a, stream);
+  return launch_long<MX, SWIGLU, 2, 1>(a, stream);
 }
 
 }  // namespace
 
+// One row block a tile where such tiles, uncut, find a CU each and are short (at most 512 pairs a CU):
+// twice the CUs of two a tile. Layers with cold weights, one / two blocks, us: 2048 x 1024 with 8 / 64 /
+// 128 rows 18.3 / 21.6, 42.5 / 49.9, 53.0 / 57.6; 4096 x 2048 with 8 / 32 / 64 / 128 rows (128, 512, 1024,
+// 2048 pairs) 35.3 / 40.5, 85 / 85.5, 129 / 123, 177 / 161: two blocks read each row of h half as often.
+int few_down_blocks(int T, int k, int Nw, int K) {
+  return Nw / 16 <= kGrid && (int64_t)T * k * nch_of(K) * (Nw / 16) <= 512 * kGrid ? 1 : 2;
+}
 int few_down_workgroups(int T, int k, int Nw, int K) {
-  const int64_t ntile = Nw / (16 * kFewDownBlocks), most = (int64_t)T * k * nch_of(K) * ntile / kDownLeast;
+  const int64_t ntile = Nw / (16 * few_down_blocks(T, k, Nw, K)), most = (int64_t)T * k * nch_of(K) * ntile / kDownLeast;
   const int64_t n = most > ntile ? most : ntile;
   return n < kGrid ? (int)n : kGrid;
 }
 int few_down_parts(int T, int k, int Nw, int K) {
   // A tile of P pairs holds at most ceil(P n / W) + 1 of the n workgroups' parts, and P / W = 1 / ntile
-  const int ntile = Nw / (16 * kFewDownBlocks);
+  const int ntile = Nw / (16 * few_down_blocks(T, k, Nw, K));
   return (few_down_workgroups(T, k, Nw, K) + ntile - 1) / ntile + 1;
 }
 
 hipError_t launch_few_matvec(FewArgs a, bool mx, bool swiglu, hipStream_t stream) {
-  a.ks_log = ks_log_for(a.K, a.Nw / 32);
+  a.ks_log = ks_log_for(a.K, swiglu ? a.Nw / 32 : a.Nw / 16);
   if (mx) return swiglu ? launch_mv_rows<true, true>(a, stream) : launch_mv_rows<true, false>(a, stream);
   return swiglu ? launch_mv_rows<false, true>(a, stream) : launch_mv_rows<false, false>(a, stream);
 }
@@ -1419,10 +1428,10 @@ hipError_t launch_few_layer(FewArgs up, FewArgs down, bool mx, hipStream_t strea
   if (e != hipSuccess) return e;
   const int wgs = few_down_workgroups(down.T, down.k, down.Nw, down.K);
   down.grid = wgs;
-  if (mx)
-    few_down_kernel<true, 3><<<wgs, kNT, 0, stream>>>(down);
-  else
-    few_down_kernel<false, 3><<<wgs, kNT, 0, stream>>>(down);
+  const bool two = few_down_blocks(down.T, down.k, down.Nw, down.K) == 2;
+  auto* kernel = mx ? (two ? few_down_kernel<true, 2> : few_down_kernel<true, 1>)
+                    : (two ? few_down_kernel<false, 2> : few_down_kernel<false, 1>);
+  kernel<<<wgs, kNT, 0, stream>>>(down);
   return hipGetLastError();
 }
 

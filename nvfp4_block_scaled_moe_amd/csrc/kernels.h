@@ -155,7 +155,6 @@ hipError_t launch_zero_f32(float* p, int n, hipStream_t stream);
 constexpr int kFewMaxTokens = 16;
 constexpr int kFewMaxSlots = kFewMaxTokens * kMaxTopK;
 constexpr int kFewMaxHidden = 32768;   // H of the layer: at least one row stays in LDS
-constexpr int kFewDownBlocks = 2;      // 16-column blocks of a tile of the layer's second launch
 // What the layer's first launch leaves for its second: the items (expert << 16 | mask of its
 // tokens) with the first of their rows in h, and for every row of h its routing weight (NVFP4:
 // times the global scale of the expert's second matrix).
@@ -164,7 +163,7 @@ struct FewPlan {
   uint32_t item[kFewMaxSlots];
   uint16_t row0[kFewMaxSlots];
   float weight[kFewMaxSlots];
-  int arrived[kFewMaxHidden / (16 * kFewDownBlocks)];   // parts of each tile that are there
+  int arrived[kFewMaxHidden / 32];   // parts of each tile that are there
 };
 struct FewArgs {
   const uint16_t* x;      // bf16 [T, K], rows ldx elements apart (matvec, the layer's first launch)
@@ -198,7 +197,8 @@ struct FewArgs {
   int8_t* hexp;           // NVFP4: [T * k, 8 ceil(F / 128)] exponents of h's blocks of 16 columns
 };
 hipError_t launch_few_matvec(FewArgs a, bool mx, bool swiglu, hipStream_t stream);
-// Workgroups of the layer's second launch, and the most of them that share a tile.
+// The layer's second launch: 16-column blocks of a tile, workgroups, and the most that share a tile.
+int few_down_blocks(int T, int k, int Nw, int K);
 int few_down_workgroups(int T, int k, int Nw, int K);
 int few_down_parts(int T, int k, int Nw, int K);
 hipError_t launch_few_layer(FewArgs up, FewArgs down, bool mx, hipStream_t stream);
