@@ -1377,10 +1377,12 @@ hipError_t launch_mv_rows(const FewArgs& a, hipStream_t stream) {
     return a.T > 4 ? launch_mv<MX, SWIGLU, 16>(a, stream) : launch_mv<MX, SWIGLU, 4>(a, stream);
   // Rows past the resident ones' LDS. More tiles than few_long_kernel has workgroups: the kernel
   // whose waves share the rows. T = 16, K = 6144, cold weights, few_long / few_wide, us:
-  //   weight rows      16384       32768       65536       152064
-  //   NVFP4          23.0 / 25.7  41.1 / 28.6  73.4 / 50.7  167 / 118
-  //   MXFP4          18.1 / 19.6  34.0 / 24.6  61.5 / 46.0  143 / 107
-  //   SWIGLU, NVFP4  22.4 / 37    41.0 / 39.9  72.5 / 50.2  167 / 123
+  //   weight rows       8192        16384       24576       32768       65536       152064
+  //   NVFP4          12.6 / 23.1  21.3 / 24.9 36.9 / 26.9 38.0 / 28.6 71.2 / 50.6  165 / 119
+  //   MXFP4           9.0 / 16.3  17.7 / 19.6 30.9 / 22.7 33.3 / 24.5 60.6 / 45.7  141 / 106
+  //   SWIGLU, NVFP4  12.0 / 34.2  20.3 / 36.6 35.2 / 39.1 36.3 / 41.5 67.8 / 49.8  163 / 122
+  // few_long_kernel with one row block a wave (two chunks under way) while that finds every
+  // workgroup a CU of its own: 2048 rows 9.8, against 11.5 with two; from there on two (one chunk).
   const int tiles = SWIGLU ? a.Nw / 64 : a.Nw / 32;
   if (tiles > 512) return launch_wide<MX, SWIGLU, RB, 8, 4>(a, stream);
   if constexpr (!SWIGLU)
