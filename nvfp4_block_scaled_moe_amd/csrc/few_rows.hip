@@ -8,29 +8,29 @@
 //   layer, 2nd  out[t, n] = sum over t's experts of w(t, e) * sum_f h[r, f] W2_e[n, f]
 //
 // Every weight byte is used by at most 16 rows, so the bound is the HBM rate on codes and
-// scales (9/16 or 17/32 byte a weight); the kernels read each of them once and keep as many
-// of their loads in flight as registers allow:
+// scales (9/16 or 17/32 byte a weight), and for small matrices the latency of a chain of dependent
+// steps. The kernels read each weight once and keep two or three of each wave's loads under way:
 //
 //   * A wave streams 16-row x 128-column tiles (1 KB of codes in the order of the matrix
-//     core's operand, weights_tile.hip) into a register ring D chunks deep, with the lane's
-//     scale bytes and its piece of the activations beside them. The columns are dealt out to
-//     the waves of a workgroup chunk by chunk, so one 16- or 32-row tile already keeps 8 waves
-//     busy and a single token fills the chip; the waves' float32 sums meet in LDS once a tile,
-//     in a fixed order.
-//   * Persistent workgroups (2 a CU) walk a contiguous range of tiles as one flat sequence of
-//     chunks: the ring stays full across tiles and experts.
-//   * Activations: the wave itself turns its chunk of the rows into matrix-core operands in a
-//     piece of LDS of its own (no barrier). NVFP4 weights are decoded exactly to f16 (E2M1 *
-//     E4M3 has at most 6 significant bits), so the rows become f16, scaled by a power of two
-//     for each (row, chunk) so that the chunk's largest finite magnitude lies in [2^14, 2^15):
-//     exact for bf16 rows down to 2^-31 of that magnitude; the partial product takes the
-//     power back when it is added to the float32 sum. MXFP4 weights are decoded exactly to
+//     core's operand, weights_tile.hip) into a ring of registers, with the lane's scale bytes
+//     beside them. One workgroup of 16 waves a CU: what a CU can have under way is limited, so all
+//     256 have to take the same number of bytes, and its older waves are served first, so the
+//     waves meet at a barrier once a tile (or a turn of the ring).
+//   * The columns of a tile are dealt out to the waves chunk by chunk, so that a single 16-row
+//     tile keeps a CU busy; the waves' float32 sums meet in LDS once a tile, in a fixed order.
+//   * Persistent workgroups walk a contiguous range of tiles as one flat sequence of chunks: the
+//     ring stays full across tiles and experts.
+//   * NVFP4 weights are decoded exactly to f16 (E2M1 * E4M3 has at most 6 significant bits), so the
+//     rows become f16, scaled by a power of two so that a row's (or, where the row does not fit in
+//     LDS, its chunk's) largest finite magnitude lies in [2^14, 2^15): exact for bf16 values down
+//     to 2^-31 of that magnitude; the sums take the power back. MXFP4 weights are decoded exactly to
 //     bf16 (whose exponent holds every E8M0 scale), so bf16 rows are used as they are.
 //   * The layer's first launch routes in every workgroup (a wave per token; a few microseconds
 //     that replace a launch), the second reads the list that one of them left. An item is an
 //     expert with up to 4 of its tokens; an expert with more tokens takes several items.
-//   * h between the launches: f16 with a power of two for each 16 columns (NVFP4), bf16 (MXFP4,
-//     as its matrix operand needs; the same rounding as h of the W4A16 layer).
+//   * h between the launches: f16 with a power of two for each 16 columns (NVFP4: 11 bits of what
+//     is then summed in float32), bf16 (MXFP4, as its matrix operand needs; 8 bits, the same
+//     rounding as h of the grouped GEMMs).
 //   * The second launch adds a token's experts in its accumulators in ascending expert order: no
 //     float32 rows of the experts go through memory, and no reduce launch follows.
 #include <hip/hip_runtime.h>
@@ -54,7 +54,8 @@ constexpr int kGrid = 256;               // persistent workgroups: one on each o
 constexpr int kLongW = 8;                // waves per workgroup of few_long_kernel
 constexpr int kLongNT = kLongW * kWave;
 constexpr int kRowBytes = 256 + 16;      // LDS bytes of one row's chunk (padded: conflict-free reads)
-constexpr int kDownLeast = 128;          // pairs of the second launch that are worth a workgroup
+constexpr int kDownLeast = 128;          // pairs of the second launch that are worth a workgroup: sharing a
+                                         // tile costs 3-4 us (one token, 128 pairs a tile: 50.4 us, 54.6 shared)
 constexpr int kItemTok = 4;              // tokens of one item of the layer
 template <bool B>
 struct Flag {
@@ -333,6 +334,13 @@ __device__ __forceinline__ void fetch_args(const FewArgs& p) {
 // with one power of two a row (NVFP4) or bf16 (MXFP4): turned once, they serve every tile of
 // the item. Waves deal out the chunks ks at a time (ks = 1 .. 16: kW / ks groups of
 // waves, each with RB row blocks of its own).
+//
+// Measured (the kernel alone, weights cold). Products: 2048 x 6144, one row, 7.1 MB: 6.4 us;
+// 2064 x 1184, MXFP4, 5 rows, 1.3 MB: 5.1 us; SwiGLU 1024 x 256, one row: 4.8 us. These are
+// latency: ~1 us of launch and arguments, 2 us until the rows are operands, 2 us until the weights
+// are there, 1 us of sums and stores; a CU alone draws about 45 B/ns. The layer: 16 tokens of 256
+// experts, 6144 x 2048, 1.43 GB: 243 us, 5.9 TB/s, where plain reads reach 6.0-6.5; one token of it,
+// 113 MB: 26 us, of which 5 are routing and staging and 2 the last tile's sums.
 // 16-byte pieces of the rows a thread requests together: one row seldom has more than one for each.
 constexpr int pass_batch(int ntok) { return ntok > 4 ? 4 : 1; }
 
@@ -794,9 +802,10 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
 }
 
 // ------------------------------------------------------------------ matvec of rows that do not fit
-// Up to 16 rows of any length: each wave turns its chunk of the rows itself, in a piece of LDS of
-// its own, with a power of two for every (row, chunk). The turning costs about as much as the
-// decode of four weight tiles, so a wave takes up to RB = 8 row blocks a chunk.
+// Up to 16 rows of any length: the 8 waves of a workgroup (two a CU) deal out the chunks and each
+// turns its chunk of the rows itself, in a piece of LDS of its own, with a power of two for every
+// (row, chunk). The turning costs about as much as the decode of four weight tiles, and is most of
+// the time where there are few weight rows: 2048 x 6144 with 16 rows 9.8 us, MXFP4 6.1 (not turned).
 template <bool MX, bool SWIGLU, int RB, int D>
 __global__ __launch_bounds__(kLongNT, 4) void few_long_kernel(const FewArgs p) {
   typedef Decode<MX> Dec;
@@ -929,11 +938,11 @@ __global__ __launch_bounds__(kLongNT, 4) void few_long_kernel(const FewArgs p) {
 // cross waves, and the W waves of a workgroup share the rows: each of them turns one of the next W
 // chunks into operands, in the other half of a double-buffered piece of LDS.
 //
-// Bound by the vector units: a tile costs a wave 46 instructions (32 of them the decoding) and the
-// rows 16 a tile more; at four waves a SIMD that is 1200 cycles for every 18 KB a CU reads. 65536 x
-// 6144 at 16 rows: 48.2 us, 4.7 TB/s; few_long_kernel, in which every wave turns its own chunks,
-// 72; 16 waves sharing (half the turning, but all of a CU's waves at one barrier) 50; two row
-// blocks a wave 51; eight chunks in flight 50.
+// Between two bounds: the vector units are busy half the time (79 instructions a tile and wave, 32
+// of them the decoding, 25 the rows), and the reads go at three quarters of the memory's rate. 65536 x
+// 6144 at 16 rows: 48.3 us, 4.7 TB/s (MXFP4 45); few_long_kernel, in which every wave turns its own
+// chunks, 71; 16 waves sharing (half the turning, but all of a CU's waves at one barrier) 50; two
+// row blocks a wave 51; two or eight chunks under way 52 and 50.
 template <bool MX, bool SWIGLU, int RB, int W, int D>
 __global__ __launch_bounds__(W* kWave, 4) void few_wide_kernel(const FewArgs p) {
   typedef Decode<MX> Dec;
@@ -1039,12 +1048,18 @@ __global__ __launch_bounds__(W* kWave, 4) void few_wide_kernel(const FewArgs p) 
 }
 
 // ------------------------------------------------------------------ the layer's second launch
-// A tile is 32 output columns (RB = 2 row blocks); its work is the (item, chunk) pairs. The
-// pairs of all tiles form one sequence that the workgroups share evenly: a CU's share of the
-// memory rate is limited (the most reads it can have under way), so every CU has to take the
-// same number of bytes, which whole tiles seldom give (192 tiles on 256 CUs: three quarters of
-// the rate). A tile that several workgroups have part of is finished by the last of them to
-// arrive, which adds the parts in order; nobody waits.
+// A tile is RB row blocks, 16 or 32 output columns; its work is the (item, chunk) pairs. The
+// pairs of all tiles form one sequence that the workgroups share evenly (whole tiles seldom give
+// every CU the same number of bytes: 192 tiles on 256 CUs, three quarters of the rate), unless the
+// parts would be short (kDownLeast). A tile that several workgroups have part of is finished by the
+// last of them to arrive, which adds the parts in order; nobody waits.
+//
+// A wave's pair needs up to four rows' chunk of h beside the weights, brought to the row's common
+// exponent on its way through LDS. Measured: 16 tokens of 256 experts, 6144 x 2048, 0.71 GB:
+// 133 us, 5.4 TB/s; one token, 57 MB: 19 us, of which 3 pass until the list is read and the ring
+// is full and 2-3 in the last sums; 2 tokens of 60, 2080 x 1376, MXFP4, 12 MB: 9.1 us. Keeping the ring
+// full over a tile's end (the next tile's loads under its sums) brought nothing: 50.9 us for the
+// layer of one token against 50.4.
 template <bool MX, int RB>
 __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
   constexpr int D = 2;   // chunks of a wave under way (3: a per cent or two slower, 4: spills)
