@@ -1116,7 +1116,7 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
   const int nitems = __builtin_amdgcn_readfirstlane(listed);
   __syncthreads();
 
-  // This workgroup's part of the sequence. (At most 1024 items x 256 chunks x 1024 tiles.)
+  // This workgroup's part of the sequence. (Below 2^30 pairs by the limits on the sizes.)
   const uint32_t P = (uint32_t)nitems * nch, ntile = nblk / RB, Wk = P * ntile;
   uint32_t n = Wk / kDownLeast;   // workgroups that take part: not fewer than there are tiles
   n = n < ntile ? ntile : n;

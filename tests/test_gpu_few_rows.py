@@ -314,6 +314,34 @@ def test_layer_few(fmt, T, E, k, H, F):
     _check(np_(got), want, err, torch.bfloat16)
 
 
+# Wide layers, whose second launch has tiles of two row blocks (more than 256 blocks, or long lists),
+# whole and shared by several workgroups.
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("T,E,k,H,F", [(3, 8, 2, 4128, 96), (1, 4, 2, 6176, 160), (16, 24, 8, 4128, 416),
+                                       (16, 64, 32, 2080, 256), (4, 40, 16, 4096, 544), (2, 6, 3, 9248, 32)])
+def test_layer_few_wide(fmt, T, E, k, H, F):
+    test_layer_few(fmt, T, E, k, H, F)
+
+
+# Long rows, of which three, two and one fit in LDS: so many tokens an item.
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("T,E,k,H,F", [(8, 4, 2, 16384, 32), (5, 3, 2, 24576, 32), (3, 4, 2, 32768, 32), (1, 2, 1, 32768, 64)])
+def test_layer_few_long_rows(fmt, T, E, k, H, F):
+    test_layer_few(fmt, T, E, k, H, F)
+
+
+def test_layer_few_fp8_long_rows():
+    """The FP8 scale over all rows where the rows are staged an item at a time."""
+    T, E, k, H, F = 7, 3, 2, 16416, 32
+    w13, _ = _matrices("nvfp4", E, 2 * F, H, 510, std=0.05)
+    w2, _ = _matrices("nvfp4", E, H, F, 610, std=0.05)
+    x, lg = _rows(T, H, 13).to(DEV), inputs.random_fp32((T, E), 34).to(DEV)
+    got = ops.moe_layer_few_nvfp4(x, lg, k, w13, w2, fp8_acts=True)
+    same = ops.moe_layer_few_nvfp4(ops.act_fp8_e4m3_roundtrip(x), lg, k, w13, w2)
+    torch.cuda.synchronize()
+    assert torch.equal(got, same)
+
+
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
 @pytest.mark.parametrize("T", [4, 5, 16])
 def test_layer_few_one_expert_for_all_and_ties(fmt, T):
