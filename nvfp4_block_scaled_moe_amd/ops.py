@@ -604,64 +604,68 @@ def moe_block_norm(resid: torch.Tensor, y: torch.Tensor | None = None, *, post_w
     experts' rows [T*k, H]; ``y_add`` [T, H] is added to it (a shared expert); ``post_w``,
     ``pre_w`` [H]; ``gate`` [H], [T, 1] or [T, H]. ``resid_out`` may be ``resid``."""
     fn = "moe_block_norm"
-    idx = _gpu(fn, resid, y, post_w, gate, pre_w, slot_to_row, topk_w, y_add, resid_out, next_out)
+    idx = resid.get_device()
+    if idx < 0 or (resid_out is not None and resid_out.get_device() != idx) or \
+            (next_out is not None and next_out.get_device() != idx):
+        raise ValueError(f"{fn}: all tensors must be on one GPU")
     if resid.dim() != 2:
         raise ValueError(f"{fn}: resid must be [T, H], got {tuple(resid.shape)}")
     T, H = resid.shape
     if post_w is not None and pre_w is not None and post_w.dtype != pre_w.dtype:
         post_w, pre_w = post_w.float(), pre_w.float()
-    r_dt = _float_type(fn, resid)
     p_y = p_add = p_rows = p_topk = p_post = p_pre = p_gate = p_ro = p_next = None
     y_dt = add_dt = w_dt = gate_dt = F32
     ld_y = ld_add = k = gate_row = gate_col = ld_ro = ld_next = 0
     with _on(idx):
-        resid, ld_r = _rows(fn, "resid", resid, H, 8) if resid_out is not resid else \
-            (resid, resid.stride(0) if T > 1 else H)
+        if resid_out is not resid:
+            resid, p_resid, r_dt, ld_r = _operand(fn, "resid", resid, T, H, idx)
+        else:
+            p_resid, r_dt, ld_r = resid.data_ptr(), _float_type(fn, resid), resid.stride(0) if T > 1 else H
         if post_w is not None:
-            post_w, p_post, w_dt = _weight(fn, post_w, H)
+            post_w, p_post, w_dt, _ = _operand(fn, "post_w", post_w, None, H, idx)
         if pre_w is not None:
-            pre_w, p_pre, w_dt = _weight(fn, pre_w, H)
-            next_out, ld_next = _out_rows(fn, next_out, T, H, torch.bfloat16, resid)
-            if next_out.dtype != torch.bfloat16:
-                raise ValueError(f"{fn}: next_out must be bf16")
+            pre_w, p_pre, w_dt, _ = _operand(fn, "pre_w", pre_w, None, H, idx)
+            if next_out is None:
+                next_out, ld_next = torch.empty_like(resid, dtype=torch.bfloat16, memory_format=torch.contiguous_format), H
+            else:
+                next_out, ld_next = _out_rows(fn, next_out, T, H, torch.bfloat16, resid)
+                if next_out.dtype != torch.bfloat16:
+                    raise ValueError(f"{fn}: next_out must be bf16")
             p_next = next_out.data_ptr()
         if y_add is not None:
-            add_dt = _float_type(fn, y_add)
-            y_add, ld_add = _rows(fn, "y_add", y_add, H, 8)
-            if y_add.shape[0] != T:
-                raise ValueError(f"{fn}: y_add must be [{T}, {H}], got {tuple(y_add.shape)}")
-            p_add = y_add.data_ptr()
+            y_add, p_add, add_dt, ld_add = _operand(fn, "y_add", y_add, T, H, idx)
         if y is not None:
-            y_dt = _float_type(fn, y)
-            y, ld_y = _rows(fn, "y", y, H, 8)
-            p_y = y.data_ptr()
+            rows = T
             if topk_w is not None and slot_to_row is not None:
+                _gpu(fn, resid, slot_to_row, topk_w)
                 if topk_w.dtype != torch.float32 or not topk_w.is_contiguous():
                     topk_w = topk_w.float().contiguous()
                 slot_to_row = slot_to_row.contiguous()
-                n = topk_w.numel()
+                rows = topk_w.numel()
                 if topk_w.dim() != 2 or topk_w.shape[0] != T or slot_to_row.dtype != torch.int32 or \
-                        slot_to_row.numel() != n or y.shape[0] != n:
+                        slot_to_row.numel() != rows:
                     raise ValueError(f"{fn}: topk_w must be [{T}, k], slot_to_row int32 [{T} * k] and y [{T} * k, {H}]")
                 k = topk_w.shape[1]
-            elif y.shape[0] != T:
-                raise ValueError(f"{fn}: y must be [{T}, {H}], got {tuple(y.shape)}")
-            resid_out, ld_ro = _out_rows(fn, resid_out, T, H, resid.dtype, resid)
-            if resid_out.dtype != resid.dtype:
-                raise ValueError(f"{fn}: resid_out must have resid's type")
+            y, p_y, y_dt, ld_y = _operand(fn, "y", y, rows, H, idx)
+            if resid_out is None:
+                resid_out, ld_ro = torch.empty_like(resid, memory_format=torch.contiguous_format), H
+            else:
+                resid_out, ld_ro = _out_rows(fn, resid_out, T, H, resid.dtype, resid)
+                if resid_out.dtype != resid.dtype:
+                    raise ValueError(f"{fn}: resid_out must have resid's type")
             p_ro = resid_out.data_ptr()
         if slot_to_row is not None:
             p_rows = slot_to_row.data_ptr()
         if topk_w is not None:
             p_topk = topk_w.data_ptr()
         if gate is not None:
-            if gate.shape not in ((H,), (T, 1), (T, H)):
-                raise ValueError(f"{fn}: gate must be [{H}], [{T}, 1] or [{T}, {H}], got {tuple(gate.shape)}")
+            if gate.get_device() != idx or gate.shape not in ((H,), (T, 1), (T, H)):
+                raise ValueError(f"{fn}: gate must be [{H}], [{T}, 1] or [{T}, {H}] on resid's GPU, got {tuple(gate.shape)}")
             gate_dt = _float_type(fn, gate)
             gate, gate_row, gate_col = _gate(gate, T, H)
             p_gate = gate.data_ptr()
         st = _lib.load().moe_block_norm(
-            resid.data_ptr(), r_dt, ld_r, p_y, y_dt, ld_y, p_add, add_dt, ld_add, p_rows, p_topk, k, p_post, p_pre,
+            p_resid, r_dt, ld_r, p_y, y_dt, ld_y, p_add, add_dt, ld_add, p_rows, p_topk, k, p_post, p_pre,
             w_dt, w_offset, eps, p_gate, gate_dt, gate_row, gate_col, scale, T, H, p_ro, ld_ro, p_next, ld_next,
             _raw_stream(idx))
     if st:
@@ -669,19 +673,33 @@ def moe_block_norm(resid: torch.Tensor, y: torch.Tensor | None = None, *, post_w
     return (None if y is None else resid_out), (None if pre_w is None else next_out)
 
 
+def _operand(fn: str, what: str, t, rows, n: int, idx: int):
+    """(t, address, type, row distance) of an input [rows, n], or [n] where rows is None, as
+    moe_block_norm reads it: in place, or a copy whose addresses allow 16-byte reads."""
+    dt = _DT.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{fn}: {what} must be float32 or bf16, got {t.dtype}")
+    if t.get_device() != idx:
+        raise ValueError(f"{fn}: all tensors must be on one GPU")
+    shape = (n,) if rows is None else (rows, n)
+    if t.shape != shape:
+        raise ValueError(f"{fn}: {what} must be {list(shape)}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        p = t.data_ptr()
+        if p % 16 == 0:
+            return t, p, dt, n
+    if rows is None:
+        t, ld = _aligned(t), n
+    else:
+        t, ld = _rows(fn, what, t, n, 8)
+    return t, t.data_ptr(), dt, ld
+
+
 def _float_type(fn: str, t) -> int:
     dt = _DT.get(t.dtype)
     if dt is None:
         raise ValueError(f"{fn}: resid, y, y_add, gate and the weights must be float32 or bf16, got {t.dtype}")
     return dt
-
-
-def _weight(fn: str, w, H: int):
-    """(w, address, type) of a norm's weight [H]."""
-    if w.shape != (H,):
-        raise ValueError(f"{fn}: the weights must be [{H}], got {tuple(w.shape)}")
-    w = _aligned(w)
-    return w, w.data_ptr(), _float_type(fn, w)
 
 
 def _aligned(t):
