@@ -503,26 +503,35 @@ def _matvec(fn: str, x, w, epi, add, out_dtype, out, g):
         raise ValueError(f"{fn}: x must be bf16, got {x.dtype}")
     if w.B != 1:
         raise ValueError(f"{fn}: one weight matrix is needed, got {w.B}")
-    if out_dtype not in _DT or (add is not None and add.dtype not in _DT):
+    out_dt = _DT.get(out_dtype)
+    if out_dt is None or (add is not None and add.dtype not in _DT):
         raise ValueError(f"{fn}: out_dtype and add must be float32 or bf16")
     idx = _gpu(fn, x, w.codes, w.scales, g, add, out)
     Nw, K = w.R, w.C
     x, ldx = _rows(fn, "x", x, K, 8)
     T = x.shape[0]
     n = Nw // 2 if epi == EPI_SWIGLU else Nw
-    ld_add = n
+    p_add, add_dt, ld_add = None, F32, n
     if add is not None:
         add, ld_add = _rows(fn, "add", add, n)
         if add.shape[0] != T:
             raise ValueError(f"{fn}: add must be [{T}, {n}], got {tuple(add.shape)}")
+        p_add, add_dt = add.data_ptr(), _DT[add.dtype]
     with _on(idx):
-        out, ld_out = _out_rows(fn, out, T, n, out_dtype, x)
-        rest = (Nw, K, None if add is None else add.data_ptr(), F32 if add is None else _DT[add.dtype], ld_add,
-                out.data_ptr(), _DT[out.dtype], ld_out, _raw_stream(idx))
+        if out is None:
+            out, ld_out = x.new_empty((T, n), dtype=out_dtype), n
+        else:
+            out, ld_out = _out_rows(fn, out, T, n, out_dtype, x)
+            out_dt = _DT[out.dtype]
         lib = _lib.load()
-        head = (epi, x.data_ptr(), ldx, T, w.codes.data_ptr(), w.scales.data_ptr())
-        st = lib.nvfp4_matvec(*head, g.data_ptr(), *rest) if g is not None else lib.mxfp4_matvec(*head, *rest)
-    _lib.check(fn, st)
+        if g is not None:
+            st = lib.nvfp4_matvec(epi, x.data_ptr(), ldx, T, w.codes.data_ptr(), w.scales.data_ptr(), g.data_ptr(), Nw, K,
+                                  p_add, add_dt, ld_add, out.data_ptr(), out_dt, ld_out, _raw_stream(idx))
+        else:
+            st = lib.mxfp4_matvec(epi, x.data_ptr(), ldx, T, w.codes.data_ptr(), w.scales.data_ptr(), Nw, K, p_add, add_dt,
+                                  ld_add, out.data_ptr(), out_dt, ld_out, _raw_stream(idx))
+    if st:
+        _lib.check(fn, st)
     return out
 
 
