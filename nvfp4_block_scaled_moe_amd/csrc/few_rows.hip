@@ -476,18 +476,23 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
     static_assert(BUF * REDF >= kW * 3 * kWave, "the routing scratch fits");
     static_assert(kFewMaxTokens <= kW, "a wave per token");
     const int E = p.E, k = p.k, S = T * k;
-    for (int e = tid; e < E; e += kNT) s_first[e] = 0;
+    if (S > kWave)
+      for (int e = tid; e < E; e += kNT) s_first[e] = 0;
     if (FP8 && tid == 0) s_amax = 0;
     __syncthreads();
     if (wave < T) {
       const float* row = p.logits + (size_t)wave * E;
       uint32_t* scratch = reinterpret_cast<uint32_t*>(&s_red[0][0]) + wave * 3 * kWave;
       if (E <= 256)
-        route_token_thresh<4, float>(row, E, k, lane, s_ids + wave * k, s_w + wave * k, nullptr, scratch);
+        route_token_thresh<4, false>(row, E, k, lane, s_ids + wave * k, s_w + wave * k, nullptr, scratch);
       else if (E <= 512)
-        route_token_thresh<8, float>(row, E, k, lane, s_ids + wave * k, s_w + wave * k, nullptr, scratch);
+        route_token_thresh<8, false>(row, E, k, lane, s_ids + wave * k, s_w + wave * k, nullptr, scratch);
       else
-        route_token_thresh<16, float>(row, E, k, lane, s_ids + wave * k, s_w + wave * k, nullptr, scratch);
+        route_token_thresh<16, false>(row, E, k, lane, s_ids + wave * k, s_w + wave * k, nullptr, scratch);
+      if (T == 1 && lane < k) {   // an item for each kept expert (the wave's own LDS accesses keep their order)
+        s_item[lane] = (uint32_t)s_ids[lane] << 16 | 1u;
+        s_row0[lane] = (uint16_t)lane;
+      }
     }
     if (MX && all && (uint32_t)tid >= st0) load_batch(0, all, (uint32_t)tid - st0, stn);
     if (!MX && (uint32_t)tid >= st0) {
@@ -511,19 +516,53 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
       fp8_inv = 1.0 / (double)fp8_s;
       if (all_rows) fp8_tops(T);
     }
-    if (T == 1) {   // an item for each kept expert
-      if (tid < k) {
-        s_item[tid] = (uint32_t)s_ids[tid] << 16 | 1u;
-        s_row0[tid] = (uint16_t)tid;
-      }
+    const uint32_t cap = (uint32_t)p.item_tok;
+    if (T == 1) {
       nitems = k;
+    } else if (S <= kWave) {
+      // ---- the items in ascending expert order, by one wave with a lane for each slot (slots of
+      // an expert ascend with their tokens): for each slot the lanes with its expert, and with
+      // smaller ones; every cap-th slot of an expert starts an item
+      if (wave == 0) {
+        const uint32_t k_inv = 65536u / (uint32_t)k + 1u;   // (slots below 64: exact)
+        const int e = lane < S ? s_ids[lane] : 0x7fffffff;
+        uint32_t same[2] = {0, 0}, less[2] = {0, 0};
+        for (int j = 0; j < S; ++j) {
+          const int ej = __builtin_amdgcn_readlane(e, j);
+          const uint64_t eq = __ballot(e == ej), lt = __ballot(e < ej);
+          const bool mine = lane == j;
+          same[0] = mine ? (uint32_t)eq : same[0];
+          same[1] = mine ? (uint32_t)(eq >> 32) : same[1];
+          less[0] = mine ? (uint32_t)lt : less[0];
+          less[1] = mine ? (uint32_t)(lt >> 32) : less[1];
+        }
+        const uint64_t eq = (uint64_t)same[1] << 32 | same[0], lt = (uint64_t)less[1] << 32 | less[0];
+        const uint32_t before = (uint32_t)__popcll(eq & ((1ull << lane) - 1ull));
+        const uint32_t part = before * (cap == 1 ? 12u : cap == 2 ? 6u : cap == 3 ? 4u : 3u) / 12u;   // before / cap
+        const bool starts = lane < S && part * cap == before;
+        const uint64_t first = __ballot(starts);
+        if (starts) {
+          const uint32_t item = (uint32_t)__popcll(lt & first) + part, row = (uint32_t)__popcll(lt) + before;
+          uint64_t rest = eq >> lane << lane;   // the expert's slots from this one on
+          uint32_t tokens = 0;
+          for (uint32_t j = 0; j < cap && rest; ++j) {
+            tokens |= 1u << ((uint32_t)__builtin_ctzll(rest) * k_inv >> 16);
+            rest &= rest - 1;
+          }
+          s_item[item] = (uint32_t)e << 16 | tokens;
+          s_row0[item] = (uint16_t)row;
+          if (part == 0) s_first[e] = item << 16 | row;
+        }
+        if (lane == 0) s_scan[0] = (uint32_t)__popcll(first);
+      }
+      __syncthreads();
+      nitems = (int)s_scan[0];
     } else {
       // ---- the items in ascending expert order
       for (int s = tid; s < S; s += kNT) atomicOr(&s_first[s_ids[s]], 1u << (s / k));
       __syncthreads();
       // a thread for each expert: the items and rows before its own by a scan over the threads
       static_assert(kMaxExperts <= kNT, "a thread for each expert");
-      const uint32_t cap = (uint32_t)p.item_tok;
       uint32_t m = tid < E ? s_first[tid] : 0u;
       const uint32_t rows = (uint32_t)__popc(m);
       // (ceil(rows / cap) for cap 1 .. 4 and at most 16 rows)
@@ -556,13 +595,23 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
           m = rest;
         }
       }
+      __syncthreads();
     }
     nitems = __builtin_amdgcn_readfirstlane(nitems);
-    __syncthreads();
   }
 
   auto write_plan = [&]() {   // the list for the second launch
     const int k = p.k;
+    if (wave < T) {   // the kept experts' softmax, of the logits that the routing left (largest first)
+      const float x = lane < k ? s_w[wave * k + lane] : 0.0f;
+      const float top = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 0));
+      const float ex = lane < k ? expf(x - top) : 0.0f;
+      float sum = ex;
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
+      if (lane < k) s_w[wave * k + lane] = ex / sum;
+    }
+    __syncthreads();
     for (int i = tid; i < nitems; i += kNT) p.plan->item[i] = s_item[i];
     for (int i = tid; i < nitems; i += kNT) p.plan->row0[i] = s_row0[i];
     if (tid == 0) p.plan->n_items = nitems;

@@ -23,10 +23,9 @@ __device__ __forceinline__ int wave_count(bool pred) { return __popcll(__ballot(
 // equal to th fill the rest, the k kept (key, id, logit) go to the wave's LDS scratch in id
 // order, lane j takes entry j and counts the kept entries ahead of it (larger key, or equal
 // key and lower id), and lane r then takes the entry of rank r, as round r would have.
-// scratch: 3 x 64 words of the wave's own LDS. The weights are the kept experts' softmax, in
-// double (rounded once) or, W = float, in float32 (for code that runs before a kernel's first
-// load: a third of the instructions; off by at most a few 2^-24).
-template <int PL, typename W = double>
+// scratch: 3 x 64 words of the wave's own LDS. w: the kept experts' softmax, in double and rounded
+// once; without SOFTMAX their logits, largest first.
+template <int PL, bool SOFTMAX = true>
 __device__ __forceinline__ void route_token_thresh(const float* __restrict__ row, int E, int k, int lane,
                                                    int* __restrict__ ids, float* __restrict__ w, int* lds_ids,
                                                    uint32_t* scratch) {
@@ -90,13 +89,16 @@ __device__ __forceinline__ void route_token_thresh(const float* __restrict__ row
     my_e = (int)scratch[lane];
     my_x = __uint_as_float(scratch[kWave + lane]);
   }
-  const W m = (W)__uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(my_x), 0));
-  W ex = 0;
-  if (sizeof(W) == 8)
-    ex = lane < k ? (W)exp((double)my_x - (double)m) : (W)0;
-  else
-    ex = lane < k ? (W)expf((float)((W)my_x - m)) : (W)0;
-  W sum = ex;
+  if (!SOFTMAX) {
+    if (lane < k) {
+      ids[lane] = my_e;
+      w[lane] = my_x;
+    }
+    return;
+  }
+  const double m = (double)__uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(my_x), 0));
+  const double ex = lane < k ? exp((double)my_x - m) : 0.0;
+  double sum = ex;
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
   if (lane < k) {
