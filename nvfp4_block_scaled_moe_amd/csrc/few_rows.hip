@@ -483,7 +483,9 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
     if (wave < T) {
       const float* row = p.logits + (size_t)wave * E;
       uint32_t* scratch = reinterpret_cast<uint32_t*>(&s_red[0][0]) + wave * 3 * kWave;
-      if (E <= 256)
+      if (E <= kWave)
+        route_token_thresh<1, false>(row, E, k, lane, s_ids + wave * k, s_w + wave * k, nullptr, scratch);
+      else if (E <= 256)
         route_token_thresh<4, false>(row, E, k, lane, s_ids + wave * k, s_w + wave * k, nullptr, scratch);
       else if (E <= 512)
         route_token_thresh<8, false>(row, E, k, lane, s_ids + wave * k, s_w + wave * k, nullptr, scratch);
