@@ -1173,11 +1173,16 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
   n = n < ntile ? ntile : n;
   n = n < (uint32_t)p.grid ? n : (uint32_t)p.grid;
   if (blockIdx.x >= n) return;
-  const Share share(Wk, n);
-  const uint32_t x0 = share.begin(blockIdx.x);
-  int tile = (int)(x0 / P);
-  int q0 = (int)(x0 - (uint32_t)tile * P);
-  int left = (int)(share.begin(blockIdx.x + 1) - x0);
+  // (Whole tiles, the rule where little is to do, need no divisions.)
+  const bool whole = n == ntile;
+  const Share share(Wk, n, whole ? P : Wk / n);
+  int tile = (int)blockIdx.x, q0 = 0, left = (int)P;
+  if (!whole) {
+    const uint32_t x0 = share.begin(blockIdx.x);
+    tile = (int)(x0 / P);
+    q0 = (int)(x0 - (uint32_t)tile * P);
+    left = (int)(share.begin(blockIdx.x + 1) - x0);
+  }
 
   const __amdgpu_buffer_rsrc_t hr = make_rsrc(p.h, (uint32_t)S * (uint32_t)F * 2u);
   const __amdgpu_buffer_rsrc_t er = make_rsrc(p.hexp, (uint32_t)S * nch * 8u);
@@ -1196,11 +1201,11 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
   uint32_t sring[D][RB];
   uint32_t ering[D];   // the exponents of four blocks of 16 columns, the lane's own among them
   // The loads' position: item and chunk of this wave's next pair in the tile, and its steps left.
-  const int da = kW / (int)nch, dc = kW - da * (int)nch;
+  const int da = (int)quotient(kW, nch, p.nch_inv), dc = kW - da * (int)nch;
   int a_l = 0, c_l = 0, run_l = 0;
   auto open_tile = [&](int first, int m) {   // the m pairs of the tile from pair `first` on
     run_l = wave < m ? (m - wave + kW - 1) / kW : 0;
-    a_l = (first + wave) / (int)nch;
+    a_l = (int)quotient((uint32_t)(first + wave), nch, p.nch_inv);
     c_l = first + wave - a_l * (int)nch;
     open_item(run_l > 0 ? a_l : 0);   // (a wave without a pair needs a descriptor, too: its loads are out of range)
   };
@@ -1249,7 +1254,6 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
     }
   };
   unsigned char* row = s_row[wave];
-  const int per = RB * 16 * T;   // values of a tile
   for (;;) {
     const int m = min(left, (int)P - q0);   // pairs of this tile
     left -= m;
@@ -1309,15 +1313,19 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
 #pragma unroll
     for (int b = 0; b < RB; ++b) *reinterpret_cast<f32x4*>(&s_red[wave * RB + b][l16 * 16 + 4 * g]) = tot[b];
     __syncthreads();
-    const int part0 = (int)share.taker((uint32_t)tile * P);
-    const int parts = m == (int)P ? 1 : (int)share.taker((uint32_t)tile * P + P - 1) - part0 + 1;
-    float* mine = p.part + ((size_t)tile * p.most_parts + (blockIdx.x - part0)) * per;
+    // (settled: what only this part needs would be computed before the first load otherwise)
+    const int per = settled_s(T) * RB * 16, at = settled_s(tile);   // values of a tile: [T][RB * 16]
+    const int i0 = (int)settled((uint32_t)tid);
+    const bool one = m == (int)P;   // this workgroup has all of the tile
+    const int part0 = one ? 0 : (int)share.taker((uint32_t)at * P);
+    const int parts = one ? 1 : (int)share.taker((uint32_t)at * P + P - 1) - part0 + 1;
+    float* mine = p.part + ((size_t)at * p.most_parts + (blockIdx.x - part0)) * per;
     auto put = [&](int i, float v) {
-      const int r16 = i & 15, q = i >> 4, b = q / T, t = q - b * T;
-      static_cast<__bf16*>(p.out)[(size_t)t * p.ld_out + ((size_t)tile * RB + b) * 16 + r16] = (__bf16)v;
+      const int t = i / (RB * 16), n = i % (RB * 16);
+      static_cast<__bf16*>(p.out)[(size_t)t * p.ld_out + (size_t)at * (RB * 16) + n] = (__bf16)v;
     };
-    for (int i = tid; i < per; i += kNT) {
-      const int r16 = i & 15, q = i >> 4, b = q / T, t = q - b * T;
+    for (int i = i0; i < per; i += kNT) {
+      const int r16 = i & 15, b = (i >> 4) % RB, t = i / (RB * 16);
       float v = 0.0f;
 #pragma unroll
       for (int w = 0; w < kW; ++w) v += s_red[w * RB + b][t * 16 + r16];
@@ -1332,11 +1340,11 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
       __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
       __syncthreads();
       if (tid == 0)
-        s_last = __hip_atomic_fetch_add(p.plan->arrived + tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
+        s_last = __hip_atomic_fetch_add(p.plan->arrived + at, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
       __syncthreads();
       if (s_last) {
-        const float* base = p.part + (size_t)tile * p.most_parts * per;
-        for (int i = tid; i < per; i += kNT) {
+        const float* base = p.part + (size_t)at * p.most_parts * per;
+        for (int i = i0; i < per; i += kNT) {
           float v = 0.0f;
           for (int w = 0; w < parts; ++w)
             v += __hip_atomic_load(base + (size_t)w * per + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -1495,6 +1503,7 @@ hipError_t launch_few_layer(FewArgs up, FewArgs down, bool mx, hipStream_t strea
                                 : launch_layer_up<false, false>(up, rows, grid, stream);
   if (e != hipSuccess) return e;
   const int wgs = few_down_workgroups(down.T, down.k, down.Nw, down.K);
+  down.nch_inv = inverse((uint32_t)nch_of(down.K));
   down.grid = wgs;
   const bool two = few_down_blocks(down.T, down.k, down.Nw, down.K) == 2;
   auto* kernel = mx ? (two ? few_down_kernel<true, 2> : few_down_kernel<true, 1>)
