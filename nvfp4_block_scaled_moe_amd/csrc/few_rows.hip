@@ -313,7 +313,7 @@ __device__ __forceinline__ uint32_t quotient(uint32_t x, uint32_t d, uint32_t in
 struct Share {
   uint32_t each, more;
   __device__ __forceinline__ Share(uint32_t total, uint32_t n, uint32_t each_) : each(each_), more(total - each_ * n) {}
-  __device__ __forceinline__ Share(uint32_t total, uint32_t n) : Share(total, n, total / n) {}
+  __device__ __forceinline__ Share(uint32_t each_, uint32_t more_) : each(each_), more(more_) {}
   __device__ __forceinline__ uint32_t begin(uint32_t i) const { return i * each + (i < more ? i : more); }
   // The taker of thing x.
   __device__ __forceinline__ uint32_t taker(uint32_t x) const {
@@ -1150,7 +1150,7 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
   __syncthreads();
   if (!MX) {
     for (uint32_t i = tid; i < (uint32_t)S * nch; i += kNT) {
-      const uint32_t r = i / nch, c = i - r * nch;
+      const uint32_t r = quotient(i, nch, p.nch_inv), c = i - r * nch;
       const uint2 e = *reinterpret_cast<const uint2*>(p.hexp + (size_t)i * 8u);
       const int used = F / 16 - (int)c * 8;
       int top = kNoExp;
@@ -1186,12 +1186,15 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
 
   const __amdgpu_buffer_rsrc_t hr = make_rsrc(p.h, (uint32_t)S * (uint32_t)F * 2u);
   const __amdgpu_buffer_rsrc_t er = make_rsrc(p.hexp, (uint32_t)S * nch * 8u);
-  __amdgpu_buffer_rsrc_t wr, sr;
+  const uint32_t wrow = nch * 1024u, srow = (MX ? (nch + 15) >> 4 : (nch + 7) >> 3) * 1024u;   // of a row block
+  const uint32_t lane16 = 16u * lane;
+  const bool tail = (nch - 1) * kChunk + 8u * l16 >= (uint32_t)F;   // no columns in a row's last chunk
+  __amdgpu_buffer_rsrc_t wr, sr;       // the tile's row blocks of the item's matrix
   uint32_t hoff = kOOB, eoff = kOOB;   // this lane's place in a row of h and of its exponents
   auto open_item = [&](int a) {
     const uint32_t w = (uint32_t)__builtin_amdgcn_readfirstlane((int)s_item[a]);
-    wr = make_rsrc(p.codes + (size_t)(w >> 16) * wbytes, wbytes);
-    sr = make_rsrc(p.scales + (size_t)(w >> 16) * sbytes, sbytes);
+    wr = make_rsrc(p.codes + (size_t)(w >> 16) * wbytes + (uint32_t)tile * RB * wrow, RB * wrow);
+    sr = make_rsrc(p.scales + (size_t)(w >> 16) * sbytes + (uint32_t)tile * RB * srow, RB * srow);
     const bool in = g < __popc(w & 0xffffu);
     const uint32_t hrow = (uint32_t)s_row0[a] + (uint32_t)g;
     hoff = in ? (hrow * (uint32_t)F + 8u * l16) * 2u : kOOB;
@@ -1210,17 +1213,18 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
     open_item(run_l > 0 ? a_l : 0);   // (a wave without a pair needs a descriptor, too: its loads are out of range)
   };
   auto issue = [&](int d) {
-    const bool ok = run_l > 0;
-    const uint32_t c = (uint32_t)c_l;
+    // (A step without a pair: as in the first launch.)
+    const int in = settled_s(-run_l);   // negative: there is a pair
+    const uint32_t all = (uint32_t)(in >> 31), out = kOOB & ~(uint32_t)in, c = (uint32_t)c_l;
+    const uint32_t v = settled(lane16 | out), w0 = (c * 1024u) & all, s0 = scale_off<MX>(c) & all;
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
-      const uint32_t blk = (uint32_t)tile * RB + b;
-      wring[d][b] = ld128(wr, settled(16u * lane + (ok ? (blk * nch + c) * 1024u : kOOB)), 0);
-      sring[d][b] = ld32(sr, settled(16u * lane + (ok ? scale_off<MX>(blk, nch, c) : kOOB)));
+      wring[d][b] = ld128(wr, v, w0 + b * wrow);
+      sring[d][b] = ld32(sr, v, s0 + b * srow);
     }
-    const bool in = ok && (int)(c * kChunk) + 8 * l16 < F;
-    xring[d] = ld128(hr, settled(in ? hoff + c * 256u : kOOB), 0);
-    if (!MX) ering[d] = ld32(er, settled(in ? eoff + c * 8u : kOOB));
+    const bool last = c == nch - 1;
+    xring[d] = ld128(hr, settled((last && tail ? kOOB : hoff) | out), (c * 256u) & all);
+    if (!MX) ering[d] = ld32(er, settled(eoff | out), (c * 8u) & all);
     const int a0 = a_l;
     --run_l;
     c_l += dc;
@@ -1317,8 +1321,9 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
     const int per = settled_s(T) * RB * 16, at = settled_s(tile);   // values of a tile: [T][RB * 16]
     const int i0 = (int)settled((uint32_t)tid);
     const bool one = m == (int)P;   // this workgroup has all of the tile
-    const int part0 = one ? 0 : (int)share.taker((uint32_t)at * P);
-    const int parts = one ? 1 : (int)share.taker((uint32_t)at * P + P - 1) - part0 + 1;
+    const Share split((uint32_t)settled_s((int)share.each), (uint32_t)settled_s((int)share.more));
+    const int part0 = one ? 0 : (int)split.taker((uint32_t)at * P);
+    const int parts = one ? 1 : (int)split.taker((uint32_t)at * P + P - 1) - part0 + 1;
     float* mine = p.part + ((size_t)at * p.most_parts + (blockIdx.x - part0)) * per;
     auto put = [&](int i, float v) {
       const int t = i / (RB * 16), n = i % (RB * 16);
