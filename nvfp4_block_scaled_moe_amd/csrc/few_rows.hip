@@ -335,12 +335,13 @@ __device__ __forceinline__ void fetch_args(const FewArgs& p) {
 // the item. Waves deal out the chunks ks at a time (ks = 1 .. 16: kW / ks groups of
 // waves, each with RB row blocks of its own).
 //
-// Measured (the kernel alone, weights cold). Products: 2048 x 6144, one row, 7.1 MB: 6.4 us;
-// 2064 x 1184, MXFP4, 5 rows, 1.3 MB: 5.1 us; SwiGLU 1024 x 256, one row: 4.8 us. These are
+// Measured (the kernel alone, weights cold). Products: 2048 x 6144, one row, 7.1 MB: 6.2 us;
+// 2064 x 1184, MXFP4, 5 rows, 1.3 MB: 4.7 us; SwiGLU 1024 x 256, one row: 4.8 us. These are
 // latency: ~1 us of launch and arguments, 2 us until the rows are operands, 2 us until the weights
 // are there, 1 us of sums and stores; a CU alone draws about 45 B/ns. The layer: 16 tokens of 256
 // experts, 6144 x 2048, 1.43 GB: 243 us, 5.9 TB/s, where plain reads reach 6.0-6.5; one token of it,
-// 113 MB: 26 us, of which 5 are routing and staging and 2 the last tile's sums.
+// 113 MB: 26 us, of which 4-5 are routing and staging and 2 the last tile's sums; 3 tokens of 8, 256 x
+// 512: 7.8 us.
 // 16-byte pieces of the rows a thread requests together: one row seldom has more than one for each.
 constexpr int pass_batch(int ntok) { return ntok > 4 ? 4 : 1; }
 
@@ -1107,8 +1108,9 @@ __global__ __launch_bounds__(W* kWave, 4) void few_wide_kernel(const FewArgs p) 
 //
 // A wave's pair needs up to four rows' chunk of h beside the weights, brought to the row's common
 // exponent on its way through LDS. Measured: 16 tokens of 256 experts, 6144 x 2048, 0.71 GB:
-// 133 us, 5.4 TB/s; one token, 57 MB: 19 us, of which 3 pass until the list is read and the ring
-// is full and 2-3 in the last sums; 2 tokens of 60, 2080 x 1376, MXFP4, 12 MB: 9.1 us. Keeping the ring
+// 134 us, 5.3 TB/s; one token, 57 MB: 18 us, of which 3 pass until the list is read and the ring
+// is full and 2-3 in the last sums; 2 tokens of 60, 2080 x 1376, MXFP4, 12 MB: 8.2 us; 3 of 8, 256 x
+// 512: 5.4 us. Keeping the ring
 // full over a tile's end (the next tile's loads under its sums) brought nothing: 50.9 us for the
 // layer of one token against 50.4.
 template <bool MX, int RB>
