@@ -1066,6 +1066,7 @@ __global__ __launch_bounds__(W* kWave, 4) void few_wide_kernel(const FewArgs p) 
 #pragma unroll
           for (int b = 0; b < RB; ++b)
             a[b] = Dec::mfma(Dec::part(wring[d][b][j], scale_of<MX>(sring[d][b], c), j), bf, a[b]);
+          if (RB == 2 && j == 1) __builtin_amdgcn_sched_barrier(0);   // (all four operands at once would spill)
         }
 #pragma unroll
         for (int b = 0; b < RB; ++b) {

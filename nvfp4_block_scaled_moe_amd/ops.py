@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 from dataclasses import dataclass
 
@@ -549,6 +550,13 @@ def mxfp4_matvec(x: torch.Tensor, w: MxTiledWeights, epi: int = EPI_NONE, *, add
     return _matvec("mxfp4_matvec", x, w, epi, add, out_dtype, out, None)
 
 
+@functools.lru_cache(maxsize=1024)
+def _few_workspace(mx: bool, T: int, E: int, k: int, H: int, F: int) -> int:
+    lib = _lib.load()
+    size = lib.moe_layer_few_mxfp4_workspace_size if mx else lib.moe_layer_few_nvfp4_workspace_size
+    return size(T, E, k, H, F)
+
+
 def _layer_few(fn: str, x, logits, k, w13, w2, g13, g2, fp8_acts, out):
     if x.dtype != torch.bfloat16 or x.dim() != 2 or logits.dim() != 2 or logits.shape[0] != x.shape[0]:
         raise ValueError(f"{fn}: x must be bf16 [T, H] and logits [T, E]")
@@ -570,13 +578,13 @@ def _layer_few(fn: str, x, logits, k, w13, w2, g13, g2, fp8_acts, out):
             out = torch.empty_like(x)
         stream = _raw_stream(idx)
         if g13 is not None:
-            ws = x.new_empty((lib.moe_layer_few_nvfp4_workspace_size(T, E, k, H, F),), dtype=torch.uint8)
+            ws = x.new_empty((_few_workspace(False, T, E, k, H, F),), dtype=torch.uint8)
             st = lib.moe_layer_few_nvfp4(logits.data_ptr(), x.data_ptr(), T, E, k, H, F, int(fp8_acts),
                                          w13.codes.data_ptr(), w13.scales.data_ptr(), g13.data_ptr(),
                                          w2.codes.data_ptr(), w2.scales.data_ptr(), g2.data_ptr(), out.data_ptr(),
                                          ws.data_ptr(), ws.numel(), stream)
         else:
-            ws = x.new_empty((lib.moe_layer_few_mxfp4_workspace_size(T, E, k, H, F),), dtype=torch.uint8)
+            ws = x.new_empty((_few_workspace(True, T, E, k, H, F),), dtype=torch.uint8)
             st = lib.moe_layer_few_mxfp4(logits.data_ptr(), x.data_ptr(), T, E, k, H, F, w13.codes.data_ptr(),
                                          w13.scales.data_ptr(), w2.codes.data_ptr(), w2.scales.data_ptr(),
                                          out.data_ptr(), ws.data_ptr(), ws.numel(), stream)
