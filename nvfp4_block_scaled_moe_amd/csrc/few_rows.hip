@@ -322,6 +322,17 @@ struct Share {
   }
 };
 
+// Inclusive sum over the lanes before, by lane moves: within rows of 16, then the rows' totals.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xf, 0xf, false);   // row_shr 1, 2, 4, 8
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xf, 0xf, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xf, 0xf, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xf, 0xf, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xa, 0xf, false);   // row_bcast 15, 31
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xc, 0xf, false);
+  return v;
+}
+
 // The kernel's arguments, one of each 64 bytes of them, requested together: the first reading of
 // each misses every cache (a microsecond), and the compiler would leave some to where they are used.
 __device__ __forceinline__ void fetch_args(const FewArgs& p) {
@@ -484,14 +495,21 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
     if (wave < T) {
       const float* row = p.logits + (size_t)wave * E;
       uint32_t* scratch = reinterpret_cast<uint32_t*>(&s_red[0][0]) + wave * 3 * kWave;
+      auto route = [&](auto regs) {   // (top-16 and up without serial rounds, as the router does)
+        constexpr int PL = decltype(regs)::value;
+        if (k < 16)
+          route_token_rounds<PL, false>(row, E, k, lane, s_ids + wave * k, s_w + wave * k, nullptr);
+        else
+          route_token_thresh<PL, false>(row, E, k, lane, s_ids + wave * k, s_w + wave * k, nullptr, scratch);
+      };
       if (E <= kWave)
-        route_token_thresh<1, false>(row, E, k, lane, s_ids + wave * k, s_w + wave * k, nullptr, scratch);
+        route(Int<1>{});
       else if (E <= 256)
-        route_token_thresh<4, false>(row, E, k, lane, s_ids + wave * k, s_w + wave * k, nullptr, scratch);
+        route(Int<4>{});
       else if (E <= 512)
-        route_token_thresh<8, false>(row, E, k, lane, s_ids + wave * k, s_w + wave * k, nullptr, scratch);
+        route(Int<8>{});
       else
-        route_token_thresh<16, false>(row, E, k, lane, s_ids + wave * k, s_w + wave * k, nullptr, scratch);
+        route(Int<16>{});
       if (T == 1 && lane < k) {   // an item for each kept expert (the wave's own LDS accesses keep their order)
         s_item[lane] = (uint32_t)s_ids[lane] << 16 | 1u;
         s_row0[lane] = (uint16_t)lane;
@@ -570,12 +588,7 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
       const uint32_t rows = (uint32_t)__popc(m);
       // (ceil(rows / cap) for cap 1 .. 4 and at most 16 rows)
       const uint32_t cnt = ((rows + cap - 1) * (cap == 1 ? 12u : cap == 2 ? 6u : cap == 3 ? 4u : 3u) / 12u) << 16 | rows;
-      uint32_t incl = cnt;
-#pragma unroll
-      for (int o = 1; o < kWave; o <<= 1) {
-        const uint32_t up = __shfl_up(incl, o, kWave);
-        if (lane >= o) incl += up;
-      }
+      const uint32_t incl = wave_scan(cnt);
       if (lane == kWave - 1) s_scan[wave] = incl;
       __syncthreads();
       uint32_t at = incl - cnt, sum = 0;

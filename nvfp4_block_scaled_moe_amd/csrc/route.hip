@@ -310,56 +310,6 @@ __global__ __launch_bounds__(kPermThreads) void permute_kernel(const int* __rest
 // as permute_kernel does.
 constexpr int kSmallSlots = 1024;
 
-template <int PL>
-__device__ __forceinline__ void route_token_rounds(const float* __restrict__ row, int E, int k, int lane,
-                                                   int* __restrict__ ids, float* __restrict__ w, int* lds_ids) {
-  uint32_t key[PL];
-  float v[PL];
-#pragma unroll
-  for (int i = 0; i < PL; ++i) {
-    const int e = lane + kWave * i;
-    const float x = e < E ? row[e] : -INFINITY;
-    v[i] = (x != x) ? -INFINITY : x;
-    key[i] = e < E ? logit_key(x) : 0u;   // every real key is >= logit_key(-inf) > 0
-  }
-  int my_e = 0;
-  float my_x = 0.0f;
-  for (int j = 0; j < k; ++j) {
-    uint32_t best = key[0];
-#pragma unroll
-    for (int i = 1; i < PL; ++i) best = max(best, key[i]);
-    best = wave_max_u32_uniform(best);
-    int e = -1;
-    float x = 0.0f;
-#pragma unroll
-    for (int i = 0; i < PL; ++i) {
-      const uint64_t m = __ballot(key[i] == best);
-      if (e < 0 && m) {
-        const int l = __builtin_ctzll(m);
-        e = kWave * i + l;
-        x = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v[i]), l));
-      }
-    }
-    if (lane == j) {
-      my_e = e;
-      my_x = x;
-    }
-#pragma unroll
-    for (int i = 0; i < PL; ++i)
-      if (kWave * i + lane == e) key[i] = 0u;
-  }
-  const double m = (double)__uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(my_x), 0));
-  const double ex = lane < k ? exp((double)my_x - m) : 0.0;
-  double sum = ex;
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
-  if (lane < k) {
-    ids[lane] = my_e;
-    w[lane] = (float)(ex / sum);
-    lds_ids[lane] = my_e;
-  }
-}
-
 // Token row r of a few-token dispatch (workgroup r + 1 of the launch, kPermThreads threads,
 // H <= 8 * kPermThreads): the bf16 row, after the FP8 E4M3 round trip when asked (per-tensor
 // scale from the finite maximum over all T rows, which every such workgroup reads), is

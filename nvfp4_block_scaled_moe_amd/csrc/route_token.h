@@ -16,8 +16,68 @@ __device__ __forceinline__ uint32_t logit_key(float x) {
 
 __device__ __forceinline__ int wave_count(bool pred) { return __popcll(__ballot(pred)); }
 
-// Top-k of one token by one wave without k serial rounds (route.hip's few-token kernel
-// also has route_token_rounds; both give the same ids, order and weights):
+// Top-k of one token by one wave, in k rounds of wave argmax: each round takes the largest
+// order-preserving logit key (DPP max over the wave) and, among the experts holding it, the lowest
+// id (ballots; registers ascend in id, lanes within a register), and removes it. Lane r holds rank
+// r. w: the kept experts' softmax, in double and rounded once; without SOFTMAX their logits.
+template <int PL, bool SOFTMAX = true>
+__device__ __forceinline__ void route_token_rounds(const float* __restrict__ row, int E, int k, int lane,
+                                                   int* __restrict__ ids, float* __restrict__ w, int* lds_ids) {
+  uint32_t key[PL];
+  float v[PL];
+#pragma unroll
+  for (int i = 0; i < PL; ++i) {
+    const int e = lane + kWave * i;
+    const float x = e < E ? row[e] : -INFINITY;
+    v[i] = (x != x) ? -INFINITY : x;
+    key[i] = e < E ? logit_key(x) : 0u;   // every real key is >= logit_key(-inf) > 0
+  }
+  int my_e = 0;
+  float my_x = 0.0f;
+  for (int j = 0; j < k; ++j) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < PL; ++i) best = max(best, key[i]);
+    best = wave_max_u32_uniform(best);
+    int e = -1;
+    float x = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
+      const uint64_t m = __ballot(key[i] == best);
+      if (e < 0 && m) {
+        const int l = __builtin_ctzll(m);
+        e = kWave * i + l;
+        x = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v[i]), l));
+      }
+    }
+    if (lane == j) {
+      my_e = e;
+      my_x = x;
+    }
+#pragma unroll
+    for (int i = 0; i < PL; ++i)
+      if (kWave * i + lane == e) key[i] = 0u;
+  }
+  if (!SOFTMAX) {
+    if (lane < k) {
+      ids[lane] = my_e;
+      w[lane] = my_x;
+    }
+    return;
+  }
+  const double m = (double)__uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(my_x), 0));
+  const double ex = lane < k ? exp((double)my_x - m) : 0.0;
+  double sum = ex;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
+  if (lane < k) {
+    ids[lane] = my_e;
+    w[lane] = (float)(ex / sum);
+    lds_ids[lane] = my_e;
+  }
+}
+
+// The same without k serial rounds (same ids, order and weights; its cost does not grow with k):
 // the k-th largest key th is found bit by bit (the largest th with at least k keys >= th; a
 // ballot per register and bit), the keys above th are kept and the lowest ids among those
 // equal to th fill the rest, the k kept (key, id, logit) go to the wave's LDS scratch in id
