@@ -196,6 +196,11 @@ def moe_forward_mxfp4(x: torch.Tensor, logits: torch.Tensor, k: int, w: MXFP4Exp
 # ------------------------------------------------------------------ a few tokens, and the block
 #: rows up to which the few-row calls run (nvfp4_matvec, moe_layer_few_nvfp4 and their MXFP4 forms)
 FEW_TOKENS = 16
+#: tokens up to which the block takes NVFP4 layers as two launches: cold weights, two launches / the
+#: separate calls, 256 experts of 6144 x 2048 top-8 and 512 of 4096 x 1024 top-22 with FP8 rows, us:
+#: 1 token 45 / 52 and 46 / 54, 8 tokens 232 / 234 and 206 / 205, 16 tokens 388 / 382 and 343 / 323.
+#: (MXFP4: 43 / 76, 217 / 256 and 363 / 407; two launches up to FEW_TOKENS, with 16-bit activations.)
+FEW_TOKENS_NVFP4_BLOCK = 8
 
 
 def moe_forward_few(x: torch.Tensor, logits: torch.Tensor, k: int, w: NVFP4Experts | MXFP4Experts,
@@ -247,13 +252,13 @@ def moe_block_forward(resid: torch.Tensor, x: torch.Tensor, k: int, w: NVFP4Expe
     the next block's normed input. ``x`` bf16 [T, H] is this block's normed input: the next
     of the call before, or ``ops.moe_block_norm(resid, pre_w=...)[1]`` at the start.
 
-    Up to 16 tokens the layer runs as two launches and the shared expert as two more; above, the
-    experts' rows go unsummed into the norm, which adds the shared expert's output. Returns
-    (r', next); next is None without ``pre_w``."""
+    Up to 8 tokens (MXFP4: 16) the layer runs as two launches and the shared expert, up to 16, as
+    two more; above, the experts' rows go unsummed into the norm, which adds the shared expert's
+    output. Returns (r', next); next is None without ``pre_w``."""
     T = x.shape[0]
     logits = router(x)
     norm = dict(post_w=post_w, gate=gate, scale=scale, pre_w=pre_w, w_offset=w_offset, eps=eps)
-    if T <= FEW_TOKENS:
+    if T <= (FEW_TOKENS if isinstance(w, MXFP4Experts) else FEW_TOKENS_NVFP4_BLOCK):
         y = moe_forward_few(x, logits, k, w, fp8_acts)
         if shared is not None:
             y = shared_expert_forward(x, shared, add=y)
