@@ -228,3 +228,23 @@ def test_block_norm_in_a_graph_and_on_another_stream():
             assert torch.equal(a, b)
         call(*ins[1])
         torch.cuda.synchronize()
+
+
+def test_block_norm_refusals():
+    T, H, k = 3, 64, 2
+    r, y = torch.zeros((T, H), device=DEV), torch.zeros((T, H), dtype=BF, device=DEV)
+    w = torch.ones(H, device=DEV)
+    rows, s2r, tw = torch.zeros((T * k, H), device=DEV), torch.zeros(T * k, dtype=torch.int32, device=DEV), torch.ones((T, k), device=DEV)
+    f = ops.moe_block_norm
+    for bad in (lambda: f(r.cpu(), y), lambda: f(r[0], y), lambda: f(r, y.half()), lambda: f(r, y[:2]), lambda: f(r, y[:, :32]),
+                lambda: f(r, y, post_w=w[:32]), lambda: f(r, pre_w=w.cpu()), lambda: f(r, y, gate=w[:32]),
+                lambda: f(r, y, gate=w.cpu()), lambda: f(r, y, y_add=r[:2]), lambda: f(r, y, resid_out=torch.zeros_like(y)),
+                lambda: f(r, pre_w=w, next_out=torch.zeros_like(r)), lambda: f(r, rows[:5], slot_to_row=s2r, topk_w=tw),
+                lambda: f(r, rows, slot_to_row=s2r.long(), topk_w=tw), lambda: f(r, rows, slot_to_row=s2r, topk_w=tw[:2]),
+                lambda: f(r, rows, slot_to_row=s2r.cpu(), topk_w=tw)):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: f(r), lambda: f(r, post_w=w, pre_w=w), lambda: f(r, gate=w, pre_w=w), lambda: f(r, y_add=y, pre_w=w),
+                lambda: f(r, y, topk_w=tw), lambda: f(r[:0], y[:0]), lambda: f(r[:, :12].contiguous(), y[:, :12].contiguous())):
+        with pytest.raises(RuntimeError):
+            bad()

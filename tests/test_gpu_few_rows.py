@@ -452,3 +452,35 @@ def test_few_rows_in_a_graph_and_on_another_stream(fmt):
             assert torch.equal(a, b), f"replay on inputs {i}"
         both(xs[1], lgs[1])
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_few_rows_refusals(fmt):
+    """What the calls do not take is refused before anything is launched, with nothing written."""
+    E, k, H, F = 4, 2, 64, 32
+    w13, _ = _matrices(fmt, E, 2 * F, H, 21)
+    w2, _ = _matrices(fmt, E, H, F, 22)
+    w, _ = _matrices(fmt, 1, 48, H, 23)
+    x = _rows(3, H, 1).to(DEV)
+    lg = torch.zeros((3, E), device=DEV)
+    call = _call(fmt)
+    out = torch.full((3, 48), 7.0, device=DEV)
+    for bad in (lambda: call(x.float(), w), lambda: call(x.cpu(), w), lambda: call(x[0], w), lambda: call(x[:, :32], w),
+                lambda: call(x, w13), lambda: call(x, w, out_dtype=torch.float16),
+                lambda: call(x, w, add=torch.zeros((2, 48), device=DEV)), lambda: call(x, w, add=torch.zeros(48, device=DEV)),
+                lambda: call(x, w, add=out.half()), lambda: call(x, w, out=out[:2]), lambda: call(x, w, out=out.t()),
+                lambda: _layer_call(fmt, x, lg[:2], k, w13, w2), lambda: _layer_call(fmt, x, lg, k, w13, w13),
+                lambda: _layer_call(fmt, x.float(), lg, k, w13, w2), lambda: _layer_call(fmt, x, lg.cpu(), k, w13, w2),
+                lambda: _layer_call(fmt, x, lg[:, :3], k, w13, w2),
+                lambda: _layer_call(fmt, x, lg, k, w13, w2, out=torch.zeros((3, H), device=DEV))):
+        with pytest.raises(ValueError):
+            bad()
+    many = _rows(17, H, 2).to(DEV)
+    for bad in (lambda: call(many, w), lambda: call(x[:0], w), lambda: call(x, w, ops.EPI_SWIGLU), lambda: call(x, w, 7),
+                lambda: _layer_call(fmt, many, torch.zeros((17, E), device=DEV), k, w13, w2),
+                lambda: _layer_call(fmt, x, lg, 0, w13, w2), lambda: _layer_call(fmt, x, lg, E + 1, w13, w2),
+                lambda: _layer_call(fmt, x[:0], lg[:0], k, w13, w2)):
+        with pytest.raises(RuntimeError):
+            bad()
+    torch.cuda.synchronize()
+    assert (out == 7.0).all()
