@@ -12,7 +12,10 @@
  * plus nvfp4_quantize (weights offline; W4A4 activations and h per forward) and
  * act_fp8_e4m3_roundtrip (FP8 E4M3 activations dequantized to bf16); and the MXFP4 variant
  * (mxfp4_quantize, mxfp4_weights_tile, moe_grouped_gemm_mxfp4 and
- * moe_grouped_gemm_mxfp4_swiglu_q: group-32 UE8M0 scales, W4A4 on the scaled FP4 matrix cores).
+ * moe_grouped_gemm_mxfp4_swiglu_q: group-32 UE8M0 scales, W4A4 on the scaled FP4 matrix cores). For
+ * decode sizes: nvfp4_matvec and mxfp4_matvec (up to 16 rows with one matrix),
+ * moe_layer_few_nvfp4 and moe_layer_few_mxfp4 (the layer of up to 16 tokens in one call), and
+ * moe_block_norm (the norms before and after a block with its gate and residual).
  *
  * Sources for what is computed (web pages; section names):
  *   [P1] "Native FP4 Is Slower Than Emulated FP4: A Kernel-Maturity Measurement on
