@@ -30,7 +30,9 @@
 //     expert with up to 4 of its tokens; an expert with more tokens takes several items.
 //   * h between the launches: f16 with a power of two for each 16 columns (NVFP4: 11 bits of what
 //     is then summed in float32), bf16 (MXFP4, as its matrix operand needs; 8 bits, the same
-//     rounding as h of the grouped GEMMs).
+//     rounding as h of the grouped GEMMs; it takes the layer's error from the 0.0017 of its bf16
+//     output to 0.0024. Two bf16 values for each of h take it back for 4-7% of the time: measured,
+//     not taken).
 //   * The second launch adds a token's experts in its accumulators in ascending expert order: no
 //     float32 rows of the experts go through memory, and no reduce launch follows.
 #include <hip/hip_runtime.h>
