@@ -155,10 +155,28 @@ __device__ __forceinline__ int settled_s(int v) {   // (the same in every lane)
   return v;
 }
 
+// A matrix's global scale g = rest * power, power = 2^n, 1 <= |rest| < 2 (a normal g). Sums over
+// chunks that have powers of two of their own take `power` with each chunk, so that what they hold
+// is within a factor 2 of the result: without g it would be some 2^15 times that, and rows near
+// 2^118 whose result is finite would overflow. `least` is the smallest exponent of a chunk whose
+// power times 2^n is exact (2^-149, float32's smallest value): a chunk below it is scaled by less,
+// and what its f16 loses lies below float32's smallest values in the result, too.
+struct GlobalScale {
+  float power, rest;
+  uint32_t least;
+  __device__ __forceinline__ explicit GlobalScale(float g) {
+    const uint32_t e = min(__float_as_uint(g) >> 23 & 0xffu, 254u);   // n + 127
+    power = __uint_as_float(e ? e << 23 : 0x00400000u);
+    rest = ldexpf(g, 127 - (int)e);
+    least = (uint32_t)max(15, 119 - (int)e);
+  }
+};
+
 // Eight bf16 elements of each of two rows' chunks, a chunk held by 16 lanes together, as f16
-// scaled by a power of two of the chunk; unscale is the power that takes it back. (Two rows a
-// call: the steps of one fill the waits of the other's reduction.)
-__device__ __forceinline__ void chunks_to_f16(const u32x4& v0, const u32x4& v1, f16x8 (&o)[2], float (&unscale)[2]) {
+// scaled by a power of two of the chunk; unscale is the power that takes it back, times that of the
+// global scale. (Two rows a call: the steps of one fill the waits of the other's reduction.)
+__device__ __forceinline__ void chunks_to_f16(const u32x4& v0, const u32x4& v1, const GlobalScale& gs, f16x8 (&o)[2],
+                                              float (&unscale)[2]) {
   uint32_t top[2];
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
@@ -190,9 +208,9 @@ __device__ __forceinline__ void chunks_to_f16(const u32x4& v0, const u32x4& v1, 
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     const u32x4& v = r ? v1 : v0;
-    const uint32_t eb = max(top[r] >> 7, 15u);   // biased exponent of the maximum
+    const uint32_t eb = max(top[r] >> 7, gs.least);   // biased exponent of the maximum
     const float scale = __uint_as_float((268u - eb) << 23);
-    unscale[r] = __uint_as_float((eb - 14u) << 23);
+    unscale[r] = __uint_as_float((eb - 14u) << 23) * gs.power;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       o[r][2 * i] = (f16)(bf16_to_f32(v[i] & 0xffffu) * scale);
@@ -204,7 +222,8 @@ __device__ __forceinline__ void chunks_to_f16(const u32x4& v0, const u32x4& v1, 
 // A chunk of up to 16 rows, row 4 r + (lane >> 4) in x[r], as matrix operands to `row` (LDS, 16 rows
 // of kRowBytes) and its powers of two to `unscale`; x loaded as zeros past the T rows.
 template <bool MX>
-__device__ __forceinline__ void put_rows(const u32x4 (&x)[4], int T, int lane, unsigned char* row, float* unscale) {
+__device__ __forceinline__ void put_rows(const u32x4 (&x)[4], int T, int lane, const GlobalScale& gs, unsigned char* row,
+                                         float* unscale) {
   const int l16 = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int r = 0; r < 4; r += 2) {
@@ -216,7 +235,7 @@ __device__ __forceinline__ void put_rows(const u32x4 (&x)[4], int T, int lane, u
     } else {
       f16x8 o[2];
       float un[2];
-      chunks_to_f16(x[r], x[r + 1], o, un);
+      chunks_to_f16(x[r], x[r + 1], gs, o, un);
       *reinterpret_cast<f16x8*>(at) = o[0];
       *reinterpret_cast<f16x8*>(at + 4 * kRowBytes) = o[1];
       if (l16 == 0) {
@@ -937,6 +956,7 @@ __global__ __launch_bounds__(kLongNT, 4) void few_long_kernel(const FewArgs p) {
     issue_end();
   }
 
+  const GlobalScale gs(MX ? 1.0f : ld_const(p.g, 0));
   f32x4 tot[RB];
 #pragma unroll
   for (int b = 0; b < RB; ++b) tot[b] = (f32x4){0.f, 0.f, 0.f, 0.f};
@@ -947,7 +967,7 @@ __global__ __launch_bounds__(kLongNT, 4) void few_long_kernel(const FewArgs p) {
     for (int d = 0; d < D; ++d) {
       // (chunks past the last have loaded zeros, rows and weights, and add nothing)
       const uint32_t c = (uint32_t)(wave + step * kLongW);
-      put_rows<MX>(xring[d], T, lane, row, s_unscale[wave]);
+      put_rows<MX>(xring[d], T, lane, gs, row, s_unscale[wave]);
       issue_rows(d);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       Op bf[4];
@@ -980,7 +1000,6 @@ __global__ __launch_bounds__(kLongNT, 4) void few_long_kernel(const FewArgs p) {
           tot[b] = (f32x4){0.f, 0.f, 0.f, 0.f};
         }
         __syncthreads();
-        const float alpha = MX ? 1.0f : ld_const(p.g, 0);
         for (int i = tid; i < HB * T * 16; i += kLongNT) {
           const int r16 = i & 15, q = i >> 4, b = q / T, col = q - b * T;
           if (!tile_block_in<SWIGLU, RB>(tile, b, nblk)) continue;
@@ -990,8 +1009,8 @@ __global__ __launch_bounds__(kLongNT, 4) void few_long_kernel(const FewArgs p) {
             v += s_red[w * RB + b][col * 16 + r16];
             if (SWIGLU) u += s_red[w * RB + b + HB][col * 16 + r16];
           }
-          v *= alpha;
-          if (SWIGLU) v = swiglu1(v, u * alpha);
+          v *= gs.rest;
+          if (SWIGLU) v = swiglu1(v, u * gs.rest);
           put_matvec(p, col, (size_t)tile_block<SWIGLU, RB>(tile, b, nblk) * 16 + r16, v);
         }
         __syncthreads();
@@ -1052,7 +1071,8 @@ __global__ __launch_bounds__(W* kWave, 4) void few_wide_kernel(const FewArgs p) 
       sring[d][b] = ld32(sr, settled(16u * lane + (in ? blk * srow + scale_off<MX>(c) : kOOB)));
     }
   };
-  auto put_chunk = [&](int buf) { put_rows<MX>(xv, T, lane, s_row[buf][wave], s_unscale[buf][wave]); };
+  const GlobalScale gs(MX ? 1.0f : ld_const(p.g, 0));
+  auto put_chunk = [&](int buf) { put_rows<MX>(xv, T, lane, gs, s_row[buf][wave], s_unscale[buf][wave]); };
   issue_rows((uint32_t)wave);
 #pragma unroll
   for (int d = 0; d < D; ++d) issue(d, (uint32_t)d);
@@ -1099,7 +1119,6 @@ __global__ __launch_bounds__(W* kWave, 4) void few_wide_kernel(const FewArgs p) 
     put_chunk(buf ^ 1);
     __syncthreads();
   }
-  const float alpha = MX ? 1.0f : ld_const(p.g, 0);
   if (l16 < T) {
     constexpr int NB = SWIGLU ? 1 : RB;
 #pragma unroll
@@ -1107,8 +1126,8 @@ __global__ __launch_bounds__(W* kWave, 4) void few_wide_kernel(const FewArgs p) 
       if (!tile_block_in<SWIGLU, RB>(sub, b, nblk)) continue;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float v = tot[b][i] * alpha;
-        if (SWIGLU) v = swiglu1(v, tot[RB - 1][i] * alpha);
+        float v = tot[b][i] * gs.rest;
+        if (SWIGLU) v = swiglu1(v, tot[RB - 1][i] * gs.rest);
         put_matvec(p, l16, (size_t)tile_block<SWIGLU, RB>(sub, b, nblk) * 16 + 4 * g + i, v);
       }
     }

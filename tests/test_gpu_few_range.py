@@ -1,0 +1,79 @@
+"""The range of magnitudes that the products of a few rows keep (nvfp4_matvec, mxfp4_matvec):
+rows whose products come near float32's largest and smallest values, with as many rows as fit in
+LDS and with more (9 and 10 of 6144 columns), in each kernel.
+
+Tolerances as in the tests of the products: exact operands, so that the float32 sums
+(16 sqrt(K) 2^-24 sum |x w|) and the output's rounding are all there is, and 2^-126 for what
+float32 cannot hold normally.
+"""
+import numpy as np
+import pytest
+import torch
+
+from nvfp4_block_scaled_moe_amd import inputs, ops
+from oracle import mxfp4, nvfp4
+from tests.gpu_util import np_, say
+from tests.test_gpu_few_rows import _call, _check, _product, _rows, _swiglu
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def _matrix(fmt, Nw, K, std, seed, clear=None):
+    """(tiled weights, function: float64 rows of the matrix). clear: (rows, columns) set to zero."""
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    wf = torch.randn((1, Nw, K), generator=gen, device=DEV, dtype=torch.float32) * std
+    if clear is not None:
+        wf[0, :clear[0], :clear[1]] = 0.0
+    q = ops.nvfp4_quantize(wf) if fmt == "nvfp4" else ops.mxfp4_quantize(wf)
+    w = ops.nvfp4_weights_tile(*q) if fmt == "nvfp4" else ops.mxfp4_weights_tile(*q)
+
+    def rows(sel):
+        part = [np_(t[0][torch.from_numpy(sel).to(DEV)]) for t in q[:2]]
+        return nvfp4.dequantize(*part, np_(q[2][0])) if fmt == "nvfp4" else mxfp4.dequantize(*part)
+
+    return w, rows
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("T", [9, 10])
+@pytest.mark.parametrize("Nw", [64, 4160, 16448])
+@pytest.mark.parametrize("std,power", [(0.03, 118), (0.03, 121), (4.0, 113), (0.03, -112), (1e-5, -100), (1e-9, -90)])
+def test_matvec_rows_near_the_ends_of_the_range(fmt, T, Nw, std, power):
+    """Rows of 6144 columns around 2^power beside ordinary ones: finite, and as precise."""
+    say("matvec range", fmt, T, Nw, std, power)
+    K = 6144
+    w, rows = _matrix(fmt, Nw, K, std, 7)
+    x = _rows(T, K, 8)
+    x[2] = (inputs.random_fp32((K,), 9) * 2.0 ** power).to(torch.bfloat16)
+    x[T - 1, :128] = (inputs.random_fp32((128,), 10) * 2.0 ** power).to(torch.bfloat16)   # one chunk of it
+    sel = np.unique(np.concatenate([np.arange(32), np.arange(Nw - 32, Nw)]))
+    got = _call(fmt)(x.to(DEV), w, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    P, err = _product(x.double().numpy(), rows(sel))
+    assert (np.abs(P) < 2.0 ** 128).all()
+    _check(np_(got)[:, sel], P, err, torch.float32)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("Nw", [64, 4160, 33024])
+def test_matvec_swiglu_rows_near_the_end_of_the_range(fmt, Nw):
+    """SwiGLU of 10 such rows: up near 2^118, gate of ordinary size (its weights are zero where the
+    row is large)."""
+    say("matvec swiglu range", fmt, Nw)
+    T, K, n = 10, 6144, Nw // 2
+    w, rows = _matrix(fmt, Nw, K, 0.03, 11, clear=(n, 128))
+    x = _rows(T, K, 12)
+    x[3, :128] = (inputs.random_fp32((128,), 13) * 2.0 ** 118).to(torch.bfloat16)
+    sel = np.unique(np.concatenate([np.arange(16), np.arange(n - 16, n)]))
+    got = _call(fmt)(x.to(DEV), w, ops.EPI_SWIGLU, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    h, err = _swiglu(*_product(x.double().numpy(), rows(np.concatenate([sel, sel + n]))))
+    assert (np.abs(h) < 2.0 ** 128).all()
+    _check(np_(got)[:, sel], h, err, torch.float32)
