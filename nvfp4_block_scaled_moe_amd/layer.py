@@ -226,8 +226,12 @@ def shared_expert_forward(x: torch.Tensor, w: SharedExpert, add: torch.Tensor | 
     """f32 [T, H] of the shared expert for bf16 rows ``x`` [T, H]: two few-row products up to 16
     rows, the second adding ``add`` (the routed experts' output); dense grouped GEMMs above
     (NVFP4 with 16-bit activations, MXFP4 with MXFP4 ones), where ``add`` is not taken."""
-    T = x.shape[0]
     nv = isinstance(w.w13, ops.TiledWeights)
+    if type(w.w13) is not type(w.w2) or w.w13.B != 1 or w.w2.B != 1 or w.w13.R != 2 * w.w2.C:
+        raise ValueError("shared_expert_forward: w13 must be one matrix [2F, H] and w2 one [H, F] of the same format")
+    if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != w.w13.C:
+        raise ValueError(f"shared_expert_forward: x must be bf16 [T, {w.w13.C}], got {x.dtype} {tuple(x.shape)}")
+    T = x.shape[0]
     if T <= FEW_TOKENS:
         mv = ops.nvfp4_matvec if nv else ops.mxfp4_matvec
         return mv(mv(x, w.w13, ops.EPI_SWIGLU), w.w2, add=add, out_dtype=torch.float32)
