@@ -237,6 +237,8 @@ def shared_expert_forward(x: torch.Tensor, w: SharedExpert, add: torch.Tensor | 
         return mv(mv(x, w.w13, ops.EPI_SWIGLU), w.w2, add=add, out_dtype=torch.float32)
     if add is not None:
         raise ValueError(f"shared_expert_forward: add is taken up to {FEW_TOKENS} rows")
+    x, ldx = ops._rows("shared_expert_forward", "x", x, w.w13.C, 8)
+    x = x if ldx == w.w13.C else x.contiguous()   # (the grouped GEMM takes rows beside each other)
     i32 = dict(dtype=torch.int32, device=x.device)
     dense = dict(expert_offsets=torch.arange(0, 2 * T, T, **i32), active_experts=torch.zeros((1,), **i32),
                  n_active=torch.ones((1,), **i32))
