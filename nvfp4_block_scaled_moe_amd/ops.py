@@ -634,7 +634,7 @@ def moe_block_norm(resid: torch.Tensor, y: torch.Tensor | None = None, *, post_w
     y_dt = add_dt = w_dt = gate_dt = F32
     ld_y = ld_add = k = gate_row = gate_col = ld_ro = ld_next = 0
     with _on(idx):
-        if resid_out is not resid:
+        if y is None or resid_out is not resid:   # (without y resid_out is not used)
             resid, p_resid, r_dt, ld_r = _operand(fn, "resid", resid, T, H, idx)
         else:
             p_resid, r_dt, ld_r = resid.data_ptr(), _float_type(fn, resid), resid.stride(0) if T > 1 else H

@@ -40,3 +40,20 @@ def test_shared_expert_of_rows_that_lie_apart(fmt, T):
         got = layer.shared_expert_forward(y, sh)
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("T", [1, 4])
+@pytest.mark.parametrize("dt", [torch.float32, BF])
+def test_block_norm_of_resid_alone_reads_it_as_it_lies(T, dt):
+    """Without y resid is only read, also where the caller names it as the output."""
+    say("norm resid alone", T, dt)
+    H = 64
+    buf = inputs.random_fp32((T, 2 * H), 1).to(dt).to(DEV)
+    w = (1 + inputs.random_fp32((H,), 2, std=0.1)).to(DEV)
+    odd = inputs.random_fp32((T * H + 1,), 3).to(dt).to(DEV)[1:].view(T, H)
+    for resid in (buf[:, ::2], buf[:, 4:4 + H], buf.t().contiguous().t()[:, :H], odd):
+        want = ops.moe_block_norm(resid.contiguous().clone(), pre_w=w)[1]
+        before = resid.clone()
+        r, got = ops.moe_block_norm(resid, pre_w=w, resid_out=resid)
+        torch.cuda.synchronize()
+        assert r is None and torch.equal(got, want) and torch.equal(resid, before)
