@@ -629,6 +629,7 @@ def moe_block_norm(resid: torch.Tensor, y: torch.Tensor | None = None, *, post_w
         raise ValueError(f"{fn}: resid must be [T, H], got {tuple(resid.shape)}")
     T, H = resid.shape
     if post_w is not None and pre_w is not None and post_w.dtype != pre_w.dtype:
+        _float_type(fn, post_w), _float_type(fn, pre_w)
         post_w, pre_w = post_w.float(), pre_w.float()
     p_y = p_add = p_rows = p_topk = p_post = p_pre = p_gate = p_ro = p_next = None
     y_dt = add_dt = w_dt = gate_dt = F32

@@ -57,3 +57,14 @@ def test_block_norm_of_resid_alone_reads_it_as_it_lies(T, dt):
         r, got = ops.moe_block_norm(resid, pre_w=w, resid_out=resid)
         torch.cuda.synchronize()
         assert r is None and torch.equal(got, want) and torch.equal(resid, before)
+
+
+def test_block_norm_refuses_other_types_of_weights():
+    r, w = torch.zeros((2, 64), device=DEV), torch.ones(64, device=DEV)
+    for a, b in ((w.half(), w), (w, w.half()), (w.double(), w.to(BF)), (w.half(), w.half())):
+        with pytest.raises(ValueError, match="float32 or bf16"):
+            ops.moe_block_norm(r, r, post_w=a, pre_w=b)
+    both = ops.moe_block_norm(r + 1, r + 2, post_w=w, pre_w=w)
+    for a, b in ((w.to(BF), w), (w, w.to(BF))):   # one of each: as float32
+        for x, y in zip(ops.moe_block_norm(r + 1, r + 2, post_w=a, pre_w=b), both):
+            assert torch.equal(x, y)
