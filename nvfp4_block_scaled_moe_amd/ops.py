@@ -499,14 +499,29 @@ def _out_rows(fn: str, out, T: int, n: int, dtype, like):
     return out, (out.stride(0) if T > 1 else n)
 
 
-def _matvec(fn: str, x, w, epi, add, out_dtype, out, g):
+def _tiled(fn: str, w, mx: bool, n: int):
+    """Refuses weights that are not ``n`` matrices of the format, or whose bytes are not what their
+    sizes say (a kilobyte holds 16 rows' codes of 128 columns, or scales of 1024 or 2048)."""
+    if not isinstance(w, MxTiledWeights if mx else TiledWeights):
+        raise ValueError(f"{fn}: weights must be {'MX' if mx else 'NV'}FP4, got {type(w).__name__}")
+    rows = 64 * n * w.R
+    codes, scales = w.codes, w.scales
+    if codes.numel() != rows * ((w.C + 127) >> 7) or not codes.is_contiguous() or not scales.is_contiguous() or \
+            scales.numel() != rows * ((w.C + 2047) >> 11 if mx else (w.C + 1023) >> 10):
+        raise ValueError(f"{fn}: weights must be {n} contiguous tiled matrices [{w.R}, {w.C}], got codes "
+                         f"{tuple(codes.shape)} and scales {tuple(scales.shape)}")
+    if not mx and (w.g.numel() != n or w.g.dtype != torch.float32 or not w.g.is_contiguous()):
+        raise ValueError(f"{fn}: the global scales must be contiguous float32 [{n}]")
+
+
+def _matvec(fn: str, mx: bool, x, w, epi, add, out_dtype, out):
     if x.dtype != torch.bfloat16:
         raise ValueError(f"{fn}: x must be bf16, got {x.dtype}")
-    if w.B != 1:
-        raise ValueError(f"{fn}: one weight matrix is needed, got {w.B}")
+    _tiled(fn, w, mx, 1)
     out_dt = _DT.get(out_dtype)
     if out_dt is None or (add is not None and add.dtype not in _DT):
         raise ValueError(f"{fn}: out_dtype and add must be float32 or bf16")
+    g = None if mx else w.g
     idx = _gpu(fn, x, w.codes, w.scales, g, add, out)
     Nw, K = w.R, w.C
     x, ldx = _rows(fn, "x", x, K, 8)
@@ -525,7 +540,7 @@ def _matvec(fn: str, x, w, epi, add, out_dtype, out, g):
             out, ld_out = _out_rows(fn, out, T, n, out_dtype, x)
             out_dt = _DT[out.dtype]
         lib = _lib.load()
-        if g is not None:
+        if not mx:
             st = lib.nvfp4_matvec(epi, x.data_ptr(), ldx, T, w.codes.data_ptr(), w.scales.data_ptr(), g.data_ptr(), Nw, K,
                                   p_add, add_dt, ld_add, out.data_ptr(), out_dt, ld_out, _raw_stream(idx))
         else:
@@ -541,13 +556,13 @@ def nvfp4_matvec(x: torch.Tensor, w: TiledWeights, epi: int = EPI_NONE, *, add: 
     """Up to 16 bf16 rows ``x`` [T, K] times one NVFP4 matrix ``w`` [Nw, K] (tiled):
     x W^T (+ add), or with EPI_SWIGLU silu(gate) * up (+ add), in one launch. ``add`` [T, n]
     float32 or bf16 (may be ``out``); rows of x, add and out may lie apart."""
-    return _matvec("nvfp4_matvec", x, w, epi, add, out_dtype, out, w.g)
+    return _matvec("nvfp4_matvec", False, x, w, epi, add, out_dtype, out)
 
 
 def mxfp4_matvec(x: torch.Tensor, w: MxTiledWeights, epi: int = EPI_NONE, *, add: torch.Tensor | None = None,
                  out_dtype=torch.bfloat16, out: torch.Tensor | None = None):
     """nvfp4_matvec with one MXFP4 matrix ``w`` (mxfp4_weights_tile)."""
-    return _matvec("mxfp4_matvec", x, w, epi, add, out_dtype, out, None)
+    return _matvec("mxfp4_matvec", True, x, w, epi, add, out_dtype, out)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -557,13 +572,15 @@ def _few_workspace(mx: bool, T: int, E: int, k: int, H: int, F: int) -> int:
     return size(T, E, k, H, F)
 
 
-def _layer_few(fn: str, x, logits, k, w13, w2, g13, g2, fp8_acts, out):
+def _layer_few(fn: str, mx: bool, x, logits, k, w13, w2, fp8_acts, out):
     if x.dtype != torch.bfloat16 or x.dim() != 2 or logits.dim() != 2 or logits.shape[0] != x.shape[0]:
         raise ValueError(f"{fn}: x must be bf16 [T, H] and logits [T, E]")
     (T, H), E, F = x.shape, logits.shape[1], w2.C
-    if w13.B != E or w2.B != E or w13.C != H or w2.R != H or w13.R != 2 * F:
-        raise ValueError(f"{fn}: weights [{w13.B}, {w13.R}, {w13.C}] and [{w2.B}, {w2.R}, {w2.C}] do not fit "
-                         f"logits [T, {E}] and x [T, {H}]")
+    _tiled(fn, w13, mx, E)
+    _tiled(fn, w2, mx, E)
+    if w13.C != H or w2.R != H or w13.R != 2 * F:
+        raise ValueError(f"{fn}: weights [{w13.R}, {w13.C}] and [{w2.R}, {w2.C}] do not fit x [T, {H}]")
+    g13, g2 = (None, None) if mx else (w13.g, w2.g)
     idx = _gpu(fn, x, logits, w13.codes, w13.scales, w2.codes, w2.scales, g13, g2, out)
     if logits.dtype != torch.float32 or not logits.is_contiguous():
         logits = logits.contiguous().float()
@@ -577,7 +594,7 @@ def _layer_few(fn: str, x, logits, k, w13, w2, g13, g2, fp8_acts, out):
         if out is None:
             out = torch.empty_like(x)
         stream = _raw_stream(idx)
-        if g13 is not None:
+        if not mx:
             ws = x.new_empty((_few_workspace(False, T, E, k, H, F),), dtype=torch.uint8)
             st = lib.moe_layer_few_nvfp4(logits.data_ptr(), x.data_ptr(), T, E, k, H, F, int(fp8_acts),
                                          w13.codes.data_ptr(), w13.scales.data_ptr(), g13.data_ptr(),
@@ -597,13 +614,13 @@ def moe_layer_few_nvfp4(x: torch.Tensor, logits: torch.Tensor, k: int, w13: Tile
     """The whole MoE layer of up to 16 tokens in two launches: top-``k`` of ``logits`` [T, E],
     SwiGLU experts ``w13`` (E matrices [2F, H]) and ``w2`` (E matrices [H, F]), weighted sum.
     ``x`` bf16 [T, H] (after the FP8 E4M3 round trip with ``fp8_acts``) -> bf16 [T, H]."""
-    return _layer_few("moe_layer_few_nvfp4", x, logits, k, w13, w2, w13.g, w2.g, fp8_acts, out)
+    return _layer_few("moe_layer_few_nvfp4", False, x, logits, k, w13, w2, fp8_acts, out)
 
 
 def moe_layer_few_mxfp4(x: torch.Tensor, logits: torch.Tensor, k: int, w13: MxTiledWeights, w2: MxTiledWeights, *,
                         out: torch.Tensor | None = None):
     """moe_layer_few_nvfp4 with MXFP4 experts (16-bit activations)."""
-    return _layer_few("moe_layer_few_mxfp4", x, logits, k, w13, w2, None, None, False, out)
+    return _layer_few("moe_layer_few_mxfp4", True, x, logits, k, w13, w2, False, out)
 
 
 # ------------------------------------------------------------------ the norms around a block

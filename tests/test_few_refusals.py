@@ -30,3 +30,27 @@ def test_shared_expert_refuses_what_does_not_fit(mx, T):
     for y in (x[:, :32], x.float(), x[0], torch.zeros((T, 96), dtype=BF)):
         with pytest.raises(ValueError, match="x must be bf16"):
             layer.shared_expert_forward(y, layer.SharedExpert(w13, w2))
+
+
+def test_few_row_calls_refuse_weights_of_another_format():
+    """Also MXFP8 weights, which share MXFP4's class, and storage that is not what its sizes say."""
+    lib = _lib.load()
+    x, lg = torch.zeros((3, 64), dtype=BF), torch.zeros((3, 2))
+    nv, mx = _weights(64, 64), _weights(64, 64, mx=True)
+    mx8 = ops.MxTiledWeights(torch.zeros((1, lib.mxfp8_tiled_codes_bytes(64, 64)), dtype=torch.uint8), mx.scales, 64, 64)
+    short = ops.TiledWeights(nv.codes, nv.scales, nv.g, 128, 64)
+    apart = ops.TiledWeights(torch.zeros((2,) + nv.codes.shape[1:], dtype=torch.uint8)[::2].expand(2, -1), nv.scales, nv.g, 64, 64)
+    for call, bad in ((ops.nvfp4_matvec, (mx, mx8, short, apart)), (ops.mxfp4_matvec, (nv, mx8))):
+        for w in bad:
+            with pytest.raises(ValueError, match="weights must be"):
+                call(x, w)
+    for g in (nv.g.to(BF), torch.ones(2)):
+        with pytest.raises(ValueError, match="global scales"):
+            ops.nvfp4_matvec(x, ops.TiledWeights(nv.codes, nv.scales, g, 64, 64))
+    e13, e2 = _weights(64, 64, 2), _weights(64, 32, 2)
+    m13, m2 = _weights(64, 64, 2, mx=True), _weights(64, 32, 2, mx=True)
+    for call, pairs in ((ops.moe_layer_few_nvfp4, ((m13, e2), (e13, m2), (m13, m2))),
+                        (ops.moe_layer_few_mxfp4, ((m13, e2), (e13, m2), (e13, e2)))):
+        for a, b in pairs:
+            with pytest.raises(ValueError, match="weights must be"):
+                call(x, lg, 1, a, b)
