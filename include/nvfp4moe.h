@@ -513,7 +513,7 @@ size_t moe_grouped_gemm_mxfp8_workspace_size(int32_t rows, int32_t E, int32_t Nw
  *               elements apart; or NULL. May be out itself (same type and row distance).
  *   out, out_dtype, ld_out   device F32 or BF16 [T, n] (output), rows ld_out >= n elements
  *               apart; what lies between the rows is not written.
- * out must not overlap x. A row's result does not depend on the other rows' values (their number
+ * out must not overlap x, nor add unless it is add. A row's result does not depend on the other rows' values (their number
  * may change the order of the sums); a NaN or Inf in one row stays in that row.
  * ------------------------------------------------------------------------- */
 nvfp4moe_status nvfp4_matvec(nvfp4moe_epilogue epi, const void* x, int64_t ldx, int32_t T, const uint8_t* w_codes,
@@ -571,7 +571,9 @@ size_t moe_layer_few_mxfp4_workspace_size(int32_t T, int32_t E, int32_t k, int32
  *     next = bf16( rms(r') * (w_offset + pre_w) )   with pre_w; r' in float32, not yet rounded
  * with rms(v) = v / sqrt(mean(v^2) + eps). All sums are float32.
  *   resid, resid_out   device [T, H] of r_dtype (F32 or BF16), rows ld_r / ld_ro elements apart;
- *                resid_out may be resid (same row distance).
+ *                resid_out may be resid (same row distance). Outputs must not overlap each other
+ *                nor an input, unless they are the very rows of resid, y (not the experts' rows),
+ *                y_add or a full gate, with the same type and row distance.
  *   y            device [T, H] of y_dtype, rows ld_y apart; with slot_to_row and topk_w the
  *                experts' rows [T * k, H], and y_t = sum_j topk_w[t, j] y[slot_to_row[t*k+j]]
  *                as moe_unpermute_reduce sums them (without its rounding). NULL: only next is

@@ -900,6 +900,27 @@ nvfp4moe_status moe_grouped_gemm_mxfp8(nvfp4moe_epilogue epi, const uint8_t* a, 
 
 // ------------------------------------------------------------------ a few rows
 namespace {
+// t rows of n bytes, ld bytes apart.
+struct Rows {
+  uintptr_t p;
+  int64_t ld, t, n;
+  Rows(const void* at, int64_t ld_, int64_t t_, int64_t n_, int64_t size)
+      : p(reinterpret_cast<uintptr_t>(at)), ld(ld_ * size), t(t_), n(n_ * size) {}
+  // (rows of one length in bytes: of one type, too)
+  bool same(const Rows& o) const { return p == o.p && t == o.t && n == o.n && (t == 1 || ld == o.ld); }
+  // Whether they share a byte. (Rows with different distances whose ranges cross count as sharing.)
+  bool overlap(const Rows& o) const {
+    const uintptr_t end = p + (uintptr_t)((t - 1) * ld + n), o_end = o.p + (uintptr_t)((o.t - 1) * o.ld + o.n);
+    if (end <= o.p || o_end <= p) return false;
+    if ((t == 1 && o.t == 1) || (t > 1 && o.t > 1 && ld != o.ld)) return true;
+    const int64_t period = t > 1 ? ld : o.ld;
+    if (period <= 0) return true;
+    const int64_t d = o.p >= p ? (int64_t)((o.p - p) % period) : (period - (int64_t)((p - o.p) % period)) % period;
+    return d < n || d + o.n > period;
+  }
+};
+int64_t size_of(nvfp4moe_dtype d) { return d == NVFP4MOE_F32 ? 4 : 2; }
+
 // The checks shared by the products of a few rows: sizes of the matrices and their tiled storage.
 nvfp4moe_status few_matrix_checks(const char* fn, const char* what, const uint8_t* codes, const uint8_t* scales,
                                   int32_t Nw, int32_t K, int32_t step) {
@@ -941,6 +962,14 @@ nvfp4moe_status few_matvec(const char* fn, bool mx, nvfp4moe_epilogue epi, const
   if (!aligned(out, out_dtype == NVFP4MOE_F32 ? 4 : 2) || (add && !aligned(add, add_dtype == NVFP4MOE_F32 ? 4 : 2)) ||
       !aligned(w_g, 4))
     return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: out, add and w_g must be aligned to their elements", fn);
+  // (every workgroup reads all of x, also after another has written its part of out)
+  const Rows rx(x, ldx, T, K, 2), ro(out, ld_out, T, n, size_of(out_dtype));
+  if (rx.overlap(ro)) return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: out must not overlap x", fn);
+  if (add) {
+    const Rows ra(add, ld_add, T, n, size_of(add_dtype));
+    if (ra.overlap(ro) && !ra.same(ro))
+      return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: out must not overlap add unless it is add", fn);
+  }
   FewArgs a{};
   a.x = static_cast<const uint16_t*>(x);
   a.ldx = ldx;
@@ -1115,6 +1144,31 @@ extern "C" nvfp4moe_status moe_block_norm(const void* resid, nvfp4moe_dtype r_dt
                 "%s: gate_col must be 0 or 1 and gate_row >= 0; a gate with columns 16-byte aligned, gate_row 0 or at "
                 "least H and a multiple of 8",
                 fn);
+  // Outputs against each other and against what is read. (A thread reads its columns of a row before
+  // it writes them, and reads weights and a gate's columns or rows as it goes.)
+  {
+    const int64_t rs = size_of(r_dtype);
+    const Rows outs[2] = {Rows(resid_out, ld_ro, T, H, rs), Rows(next, ld_next, T, H, 2)};
+    const bool used[2] = {y != nullptr, pre_w != nullptr};
+    const int64_t gs = size_of(gate_dtype);
+    const struct {
+      Rows rows;
+      bool read, own;   // own: an output may be these very rows
+    } ins[6] = {{Rows(resid, ld_r, T, H, rs), true, true},
+                {Rows(y, ld_y, slot_to_row ? (int64_t)T * k : T, H, size_of(y_dtype)), y != nullptr, !slot_to_row},
+                {Rows(y_add, ld_ya, T, H, size_of(y_add_dtype)), y_add != nullptr, true},
+                {Rows(post_w, 0, 1, H, size_of(w_dtype)), post_w != nullptr, false},
+                {Rows(pre_w, 0, 1, H, size_of(w_dtype)), pre_w != nullptr, false},
+                {Rows(gate, gate_row, gate_row ? T : 1, gate_col ? H : 1, gs), gate != nullptr,
+                 gate_col == 1 && (gate_row > 0 || T == 1)}};
+    for (int o = 0; o < 2; ++o)
+      for (const auto& i : ins)
+        if (used[o] && i.read && i.rows.overlap(outs[o]) && !(i.own && i.rows.same(outs[o])))
+          return fail(NVFP4MOE_ERR_INVALID_ARG,
+                      "%s: an output overlaps what is read (it may be the very rows of resid, y, y_add or a full gate)", fn);
+    if (used[0] && used[1] && outs[0].overlap(outs[1]))
+      return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: resid_out and next overlap", fn);
+  }
   BlockNormArgs a{};
   a.resid = resid;
   a.r_bf16 = r_dtype == NVFP4MOE_BF16;

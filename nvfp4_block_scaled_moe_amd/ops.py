@@ -555,7 +555,8 @@ def nvfp4_matvec(x: torch.Tensor, w: TiledWeights, epi: int = EPI_NONE, *, add: 
                  out_dtype=torch.bfloat16, out: torch.Tensor | None = None):
     """Up to 16 bf16 rows ``x`` [T, K] times one NVFP4 matrix ``w`` [Nw, K] (tiled):
     x W^T (+ add), or with EPI_SWIGLU silu(gate) * up (+ add), in one launch. ``add`` [T, n]
-    float32 or bf16 (may be ``out``); rows of x, add and out may lie apart."""
+    float32 or bf16 (may be ``out``); rows of x, add and out may lie apart. ``out`` must not
+    overlap x."""
     return _matvec("nvfp4_matvec", False, x, w, epi, add, out_dtype, out)
 
 
@@ -636,7 +637,8 @@ def moe_block_norm(resid: torch.Tensor, y: torch.Tensor | None = None, *, post_w
 
     ``resid`` float32 or bf16 [T, H]; ``y`` [T, H], or with ``slot_to_row`` and ``topk_w`` the
     experts' rows [T*k, H]; ``y_add`` [T, H] is added to it (a shared expert); ``post_w``,
-    ``pre_w`` [H]; ``gate`` [H], [T, 1] or [T, H]. ``resid_out`` may be ``resid``."""
+    ``pre_w`` [H]; ``gate`` [H], [T, 1] or [T, H]. ``resid_out`` may be ``resid``; an output may be
+    any of resid, y [T, H], y_add and a full gate, of its type, and must not overlap the rest."""
     fn = "moe_block_norm"
     idx = resid.get_device()
     if idx < 0 or (resid_out is not None and resid_out.get_device() != idx) or \

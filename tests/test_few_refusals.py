@@ -54,3 +54,71 @@ def test_few_row_calls_refuse_weights_of_another_format():
         for a, b in pairs:
             with pytest.raises(ValueError, match="weights must be"):
                 call(x, lg, 1, a, b)
+
+
+def _touched(at, ld, t, n):
+    return {at + r * ld + i for r in range(t) for i in range(n)}
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_matvec_refuses_an_output_that_shares_bytes(fmt):
+    """Addresses that are never dereferenced: every layout in which out has a byte of x, or of add
+    without being add, is refused."""
+    lib = _lib.load()
+    at, far, seen = 1 << 30, 1 << 34, 0
+    g = (far,) if fmt == "nvfp4" else ()
+    call = getattr(lib, fmt + "_matvec")
+    for T, ldx, ld_out, od in ((1, 32, 16, _lib.F32), (3, 48, 24, _lib.F32), (3, 64, 64, _lib.BF16), (2, 32, 80, _lib.BF16)):
+        size = 4 if od == _lib.F32 else 2
+        for off in range(-192, 400, 16):
+            share = _touched(0, 2 * ldx, T, 64) & _touched(off, size * ld_out, T, 16 * size)
+            if share:
+                assert call(_lib.EPI_NONE, at, ldx, T, far, far, *g, 16, 32, None, _lib.F32, 16, at + off, od, ld_out,
+                            None) == _lib.ERR_INVALID_ARG, (T, ldx, ld_out, off)
+                assert b"overlap x" in lib.nvfp4moe_last_error()
+                seen += 1
+            for ad, ld_add in ((_lib.F32, ld_out), (_lib.BF16, ld_out), (od, ld_out + 8)):
+                asize = 4 if ad == _lib.F32 else 2
+                same = off == 0 and ad == od and (T == 1 or ld_add == ld_out)
+                if not same and _touched(0, asize * ld_add, T, 16 * asize) & _touched(off, size * ld_out, T, 16 * size):
+                    assert call(_lib.EPI_NONE, far, ldx, T, far, far, *g, 16, 32, at, ad, ld_add, at + off, od, ld_out,
+                                None) == _lib.ERR_INVALID_ARG, (T, ad, ld_add, ld_out, off)
+                    assert b"overlap add" in lib.nvfp4moe_last_error()
+                    seen += 1
+    assert seen > 100
+
+
+def test_block_norm_refuses_outputs_that_share_bytes():
+    lib = _lib.load()
+    far = [1 << 34 | i << 28 for i in range(12)]
+    at, H = 1 << 30, 16
+    names = ["resid", "y", "ya", "post", "pre", "gate"]
+    F, B = _lib.F32, _lib.BF16
+
+    def norm(T, k, place, gr, gc, out, nxt, ld_ro=24, ld_n=24):
+        p = dict(zip(names, far))
+        p.update(place)
+        rows = (far[8], far[9], k) if k else (None, None, 0)
+        return lib.moe_block_norm(p["resid"], F, 24, p["y"], F, 24, p["ya"], F, 24, *rows, p["post"], p["pre"], F, 0.0,
+                                  1e-6, p["gate"], F, gr, gc, 1.0, T, H, out, ld_ro, nxt, ld_n, None)
+
+    for T, k in ((1, 0), (3, 0), (3, 2)):
+        n = dict(resid=T, y=T * max(k, 1), ya=T, post=1, pre=1)
+        for gr, gc in ((24, 1), (0, 1), (8, 0)):
+            n["gate"] = T if gr else 1
+            for name in names:
+                wide = 4 * (1 if name == "gate" and not gc else H)
+                ld = 4 * (gr if name == "gate" else 24)
+                for off in range(-64, 256, 16):
+                    mine = _touched(0, ld, n[name], wide)
+                    own = name in ("resid", "ya") or (name == "y" and not k) or (name == "gate" and gc and (gr or T == 1))
+                    if mine & _touched(off, 96, T, 4 * H) and not (own and off == 0):
+                        assert norm(T, k, {name: at}, gr, gc, at + off, far[10]) == _lib.ERR_INVALID_ARG, (T, k, name, off)
+                        assert b"overlaps what is read" in lib.nvfp4moe_last_error()
+                    if mine & _touched(off, 48, T, 2 * H):
+                        assert norm(T, k, {name: at}, gr, gc, far[10], at + off) == _lib.ERR_INVALID_ARG, (T, k, name, off)
+                        assert b"overlaps what is read" in lib.nvfp4moe_last_error()
+        for off in range(-32, 64, 16):
+            if _touched(0, 96, T, 64) & _touched(off, 48, T, 32):
+                assert norm(T, k, {}, 24, 1, at, at + off) == _lib.ERR_INVALID_ARG
+                assert b"resid_out and next overlap" in lib.nvfp4moe_last_error()

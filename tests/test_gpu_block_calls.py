@@ -68,3 +68,59 @@ def test_block_norm_refuses_other_types_of_weights():
     for a, b in ((w.to(BF), w), (w, w.to(BF))):   # one of each: as float32
         for x, y in zip(ops.moe_block_norm(r + 1, r + 2, post_w=a, pre_w=b), both):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("T", [1, 5])
+def test_matvec_refuses_an_output_over_its_rows(fmt, T):
+    """out over x, or over add in another place: workgroups would read what others have written."""
+    say("matvec out over x", fmt, T)
+    H = 128
+    w, _ = _matrices(fmt, 1, H, H, 17)
+    call = ops.nvfp4_matvec if fmt == "nvfp4" else ops.mxfp4_matvec
+    buf = torch.zeros((T, 3 * H), dtype=BF, device=DEV)
+    buf[:, :H] = _rows(T, H, 3).to(DEV)
+    x, before = buf[:, :H], buf.clone()
+    flat = inputs.random_fp32((T * H + 8,), 4).to(DEV)
+    add, shifted = flat[:T * H].view(T, H), flat[8:].view(T, H)
+    for bad in (dict(out=x), dict(out=buf[:, 8:8 + H]), dict(add=add, out=shifted), dict(add=add.view(BF)[:, :H], out=add)):
+        with pytest.raises(RuntimeError, match="overlap"):
+            call(x, w, **bad)
+    torch.cuda.synchronize()
+    assert torch.equal(buf, before)
+    want = call(x, w)
+    got = call(x, w, out=buf[:, H:2 * H])     # beside x in the same rows
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(buf[:, :H], before[:, :H]) and (buf[:, 2 * H:] == 0).all()
+
+
+@pytest.mark.parametrize("T,H", [(1, 64), (5, 1000), (260, 12296)])
+def test_block_norm_outputs_over_inputs(T, H):
+    """Outputs in the very rows of an input give the same bits; other overlaps are refused."""
+    say("norm outputs over inputs", T, H)
+    r, y, a = (inputs.random_fp32((T, H), s).to(BF).to(DEV) for s in (1, 2, 3))
+    gate = inputs.random_fp32((T, H), 4).to(BF).to(DEV)
+    post, pre = ((1 + inputs.random_fp32((H,), s, std=0.1)).to(DEV) for s in (5, 6))
+    kw = dict(post_w=post, pre_w=pre, scale=0.5)
+    want = ops.moe_block_norm(r, y, y_add=a, gate=gate, **kw)
+    for names in (("r", "y"), ("y", "r"), ("a", "g"), ("g", "a"), (None, "r"), ("y", None)):
+        t = dict(r=r.clone(), y=y.clone(), a=a.clone(), g=gate.clone())
+        got = ops.moe_block_norm(t["r"], t["y"], y_add=t["a"], gate=t["g"], resid_out=t.get(names[0]),
+                                 next_out=t.get(names[1]), **kw)
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, w) for g, w in zip(got, want)), names
+    t = r.clone()
+    assert torch.equal(ops.moe_block_norm(t, pre_w=pre, next_out=t)[1], ops.moe_block_norm(r, pre_w=pre)[1])
+    big = torch.zeros((T + 1, H), dtype=BF, device=DEV)
+    rows = torch.zeros((2 * T, H), dtype=BF, device=DEV)
+    s2r = torch.arange(2 * T, dtype=torch.int32, device=DEV)
+    tw = torch.ones((T, 2), device=DEV)
+    bad = [(r, y, dict(resid_out=big[:T], next_out=big[:T], **kw)),
+           (r, rows, dict(slot_to_row=s2r, topk_w=tw, resid_out=rows[:T], **kw)),
+           (r, rows, dict(slot_to_row=s2r, topk_w=tw, next_out=rows[T:], **kw)),
+           (r, y, dict(post_w=big[0], pre_w=pre.to(BF), next_out=big[:T]))]
+    if T > 1:
+        bad += [(big[1:], y, dict(resid_out=big[:T], **kw)), (r, y, dict(gate=big[:1].expand(T, H), next_out=big[:T], **kw))]
+    for x, z, other in bad:
+        with pytest.raises(RuntimeError, match="overlap"):
+            ops.moe_block_norm(x, z, **other)
