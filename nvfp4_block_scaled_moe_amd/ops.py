@@ -453,10 +453,12 @@ _NO_GUARD = contextlib.nullcontext()
 
 def _gpu(fn: str, *ts) -> int:
     """Index of the GPU that holds every given tensor (None entries aside)."""
-    index = ts[0].get_device()
+    index = first = ts[0].get_device()
     for t in ts:
-        if t is not None and (t.get_device() != index or index < 0):
-            raise ValueError(f"{fn}: all tensors must be on one GPU")
+        if t is not None and t.get_device() != first:
+            index = -1
+    if index < 0:
+        raise ValueError(f"{fn}: all tensors must be on one GPU")
     return index
 
 
@@ -500,32 +502,39 @@ def _out_rows(fn: str, out, T: int, n: int, dtype, like):
 
 
 def _tiled(fn: str, w, mx: bool, n: int):
-    """Refuses weights that are not ``n`` matrices of the format, or whose bytes are not what their
-    sizes say (a kilobyte holds 16 rows' codes of 128 columns, or scales of 1024 or 2048)."""
+    """(codes, scales, global scales or None) of the weights. Refuses those that are not ``n``
+    matrices of the format, or whose bytes are not what their sizes say (a kilobyte holds 16 rows'
+    codes of 128 columns, or scales of 1024, MXFP4 2048)."""
     if not isinstance(w, MxTiledWeights if mx else TiledWeights):
         raise ValueError(f"{fn}: weights must be {'MX' if mx else 'NV'}FP4, got {type(w).__name__}")
-    rows = 64 * n * w.R
-    codes, scales = w.codes, w.scales
-    if codes.numel() != rows * ((w.C + 127) >> 7) or not codes.is_contiguous() or not scales.is_contiguous() or \
-            scales.numel() != rows * ((w.C + 2047) >> 11 if mx else (w.C + 1023) >> 10):
-        raise ValueError(f"{fn}: weights must be {n} contiguous tiled matrices [{w.R}, {w.C}], got codes "
+    codes, scales, rows, cols = w.codes, w.scales, 64 * n * w.R, w.C
+    if codes.numel() != rows * (cols + 127 >> 7) or \
+            scales.numel() != rows * (cols + 2047 >> 11 if mx else cols + 1023 >> 10) or \
+            (n > 1 and not (codes.is_contiguous() and scales.is_contiguous())):
+        raise ValueError(f"{fn}: weights must be {n} contiguous tiled matrices [{w.R}, {cols}], got codes "
                          f"{tuple(codes.shape)} and scales {tuple(scales.shape)}")
-    if not mx and (w.g.numel() != n or w.g.dtype != torch.float32 or not w.g.is_contiguous()):
+    if mx:
+        return codes, scales, None
+    g = w.g
+    if g.numel() != n or g.dtype != torch.float32 or (n > 1 and not g.is_contiguous()):
         raise ValueError(f"{fn}: the global scales must be contiguous float32 [{n}]")
+    return codes, scales, g
 
 
 def _matvec(fn: str, mx: bool, x, w, epi, add, out_dtype, out):
     if x.dtype != torch.bfloat16:
         raise ValueError(f"{fn}: x must be bf16, got {x.dtype}")
-    _tiled(fn, w, mx, 1)
+    codes, scales, g = _tiled(fn, w, mx, 1)
     out_dt = _DT.get(out_dtype)
     if out_dt is None or (add is not None and add.dtype not in _DT):
         raise ValueError(f"{fn}: out_dtype and add must be float32 or bf16")
-    g = None if mx else w.g
-    idx = _gpu(fn, x, w.codes, w.scales, g, add, out)
+    idx = _gpu(fn, x, codes, scales, g, add, out)
     Nw, K = w.R, w.C
-    x, ldx = _rows(fn, "x", x, K, 8)
-    T = x.shape[0]
+    shape, p_x, ldx = x.shape, x.data_ptr(), K
+    if len(shape) != 2 or shape[1] != K or p_x & 15 or not x.is_contiguous():
+        x, ldx = _rows(fn, "x", x, K, 8)
+        shape, p_x = x.shape, x.data_ptr()
+    T = shape[0]
     n = Nw // 2 if epi == EPI_SWIGLU else Nw
     p_add, add_dt, ld_add = None, F32, n
     if add is not None:
@@ -541,10 +550,10 @@ def _matvec(fn: str, mx: bool, x, w, epi, add, out_dtype, out):
             out_dt = _DT[out.dtype]
         lib = _lib.load()
         if not mx:
-            st = lib.nvfp4_matvec(epi, x.data_ptr(), ldx, T, w.codes.data_ptr(), w.scales.data_ptr(), g.data_ptr(), Nw, K,
+            st = lib.nvfp4_matvec(epi, p_x, ldx, T, codes.data_ptr(), scales.data_ptr(), g.data_ptr(), Nw, K,
                                   p_add, add_dt, ld_add, out.data_ptr(), out_dt, ld_out, _raw_stream(idx))
         else:
-            st = lib.mxfp4_matvec(epi, x.data_ptr(), ldx, T, w.codes.data_ptr(), w.scales.data_ptr(), Nw, K, p_add, add_dt,
+            st = lib.mxfp4_matvec(epi, p_x, ldx, T, codes.data_ptr(), scales.data_ptr(), Nw, K, p_add, add_dt,
                                   ld_add, out.data_ptr(), out_dt, ld_out, _raw_stream(idx))
     if st:
         _lib.check(fn, st)
@@ -577,12 +586,11 @@ def _layer_few(fn: str, mx: bool, x, logits, k, w13, w2, fp8_acts, out):
     if x.dtype != torch.bfloat16 or x.dim() != 2 or logits.dim() != 2 or logits.shape[0] != x.shape[0]:
         raise ValueError(f"{fn}: x must be bf16 [T, H] and logits [T, E]")
     (T, H), E, F = x.shape, logits.shape[1], w2.C
-    _tiled(fn, w13, mx, E)
-    _tiled(fn, w2, mx, E)
+    c13, s13, g13 = _tiled(fn, w13, mx, E)
+    c2, s2, g2 = _tiled(fn, w2, mx, E)
     if w13.C != H or w2.R != H or w13.R != 2 * F:
         raise ValueError(f"{fn}: weights [{w13.R}, {w13.C}] and [{w2.R}, {w2.C}] do not fit x [T, {H}]")
-    g13, g2 = (None, None) if mx else (w13.g, w2.g)
-    idx = _gpu(fn, x, logits, w13.codes, w13.scales, w2.codes, w2.scales, g13, g2, out)
+    idx = _gpu(fn, x, logits, c13, s13, c2, s2, g13, g2, out)
     if logits.dtype != torch.float32 or not logits.is_contiguous():
         logits = logits.contiguous().float()
     x, ldx = _rows(fn, "x", x, H, 8)
@@ -598,13 +606,13 @@ def _layer_few(fn: str, mx: bool, x, logits, k, w13, w2, fp8_acts, out):
         if not mx:
             ws = x.new_empty((_few_workspace(False, T, E, k, H, F),), dtype=torch.uint8)
             st = lib.moe_layer_few_nvfp4(logits.data_ptr(), x.data_ptr(), T, E, k, H, F, int(fp8_acts),
-                                         w13.codes.data_ptr(), w13.scales.data_ptr(), g13.data_ptr(),
-                                         w2.codes.data_ptr(), w2.scales.data_ptr(), g2.data_ptr(), out.data_ptr(),
+                                         c13.data_ptr(), s13.data_ptr(), g13.data_ptr(),
+                                         c2.data_ptr(), s2.data_ptr(), g2.data_ptr(), out.data_ptr(),
                                          ws.data_ptr(), ws.numel(), stream)
         else:
             ws = x.new_empty((_few_workspace(True, T, E, k, H, F),), dtype=torch.uint8)
-            st = lib.moe_layer_few_mxfp4(logits.data_ptr(), x.data_ptr(), T, E, k, H, F, w13.codes.data_ptr(),
-                                         w13.scales.data_ptr(), w2.codes.data_ptr(), w2.scales.data_ptr(),
+            st = lib.moe_layer_few_mxfp4(logits.data_ptr(), x.data_ptr(), T, E, k, H, F, c13.data_ptr(),
+                                         s13.data_ptr(), c2.data_ptr(), s2.data_ptr(),
                                          out.data_ptr(), ws.data_ptr(), ws.numel(), stream)
     _lib.check(fn, st)
     return out
