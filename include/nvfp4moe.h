@@ -526,14 +526,15 @@ nvfp4moe_status mxfp4_matvec(nvfp4moe_epilogue epi, const void* x, int64_t ldx, 
                              int64_t ld_out, void* stream);
 
 /* ---------------------------------------------------------------------------
- * moe_layer_few_nvfp4, moe_layer_few_mxfp4 -- the whole mixture-of-experts layer of up to 16
- * tokens in two launches, where the launches of the separate calls (moe_dispatch_w4a16, two
+ * moe_layer_few_nvfp4, moe_layer_few_mxfp4 (and _f32) -- the whole mixture-of-experts layer of up to
+ * 16 tokens in two launches, where the launches of the separate calls (moe_dispatch_w4a16, two
  * GEMMs with the preparation of h between them, moe_unpermute_reduce) cost as much as the
  * weights' traffic. [P1] section 3 (launch overhead of many small kernels), [P3] "Discovering
  * the sgl_kernel Alternative" (a fused MoE). 16-bit activations with either weight format.
  *     ids as moe_route_permute(logits, T, E, k) gives them, w within 2^-21 of its weights
  *     h[t,j] = silu(x'_t W_gate^T) * (x'_t W_up^T) of expert ids[t,j]
- *     out[t] = bf16( sum_j w[t,j] * h[t,j] W_down^T )
+ *     out[t] = bf16( sum_j w[t,j] * h[t,j] W_down^T ), with _f32 the float32 sum itself (for what
+ *              adds to it or norms it: a shared expert, moe_block_norm)
  * with x' = x, or (fp8_act) x after the FP8 E4M3 round trip of act_fp8_e4m3_roundtrip, whose
  * scale is taken over all T rows. Sums are float32; h is held between the launches as f16 with
  * a power of two for every 16 columns (NVFP4) or as bf16 (MXFP4); out is rounded once.
@@ -547,7 +548,7 @@ nvfp4moe_status mxfp4_matvec(nvfp4moe_epilogue epi, const void* x, int64_t ldx, 
  *   w13_*, w2_* device, the E matrices [2F, H] (gate rows first) and [H, F] in the tiled storage
  *               (nvfp4_weights_tile or mxfp4_weights_tile), 16-byte aligned; w13_g, w2_g
  *               device float [E].
- *   out         device bf16 [T, H] (output).
+ *   out         device bf16 (_f32: float32) [T, H] (output).
  *   ws          moe_layer_few_*_workspace_size(T, E, k, H, F) bytes, 16-byte aligned, caller-owned
  *               scratch (the sizes that the call refuses give 0). Calls that may overlap need
  *               a workspace each.
@@ -561,6 +562,15 @@ nvfp4moe_status moe_layer_few_mxfp4(const float* logits, const void* x, int32_t 
                                     int32_t F, const uint8_t* w13_codes, const uint8_t* w13_scales,
                                     const uint8_t* w2_codes, const uint8_t* w2_scales, void* out, void* ws,
                                     size_t ws_bytes, void* stream);
+nvfp4moe_status moe_layer_few_nvfp4_f32(const float* logits, const void* x, int32_t T, int32_t E, int32_t k, int32_t H,
+                                        int32_t F, int32_t fp8_act, const uint8_t* w13_codes,
+                                        const uint8_t* w13_scales, const float* w13_g, const uint8_t* w2_codes,
+                                        const uint8_t* w2_scales, const float* w2_g, float* out, void* ws,
+                                        size_t ws_bytes, void* stream);
+nvfp4moe_status moe_layer_few_mxfp4_f32(const float* logits, const void* x, int32_t T, int32_t E, int32_t k, int32_t H,
+                                        int32_t F, const uint8_t* w13_codes, const uint8_t* w13_scales,
+                                        const uint8_t* w2_codes, const uint8_t* w2_scales, float* out, void* ws,
+                                        size_t ws_bytes, void* stream);
 size_t moe_layer_few_mxfp4_workspace_size(int32_t T, int32_t E, int32_t k, int32_t H, int32_t F);
 
 /* ---------------------------------------------------------------------------

@@ -70,8 +70,11 @@ SIGNATURES = {
     "mxfp4_matvec": (_int, [_int, _vp, _i64, _i32, _vp, _vp, _i32, _i32, _vp, _int, _i64, _vp, _int, _i64, _vp]),
     "moe_layer_few_nvfp4": (_int, [_vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                    _vp, _sz, _vp]),
+    "moe_layer_few_nvfp4_f32": (_int, [_vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                       _vp, _sz, _vp]),
     "moe_layer_few_nvfp4_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32]),
     "moe_layer_few_mxfp4": (_int, [_vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_layer_few_mxfp4_f32": (_int, [_vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "moe_layer_few_mxfp4_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32]),
     "moe_block_norm": (_int, [_vp, _int, _i64, _vp, _int, _i64, _vp, _int, _i64, _vp, _vp, _i32, _vp, _vp, _int, _f32,
                               _f32, _vp, _int, _i64, _i32, _f32, _i32, _i32, _vp, _i64, _vp, _i64, _vp]),

@@ -1011,7 +1011,7 @@ FewLayerWs few_layer_ws(int32_t T, int32_t k, int32_t H, int32_t F, bool mx) {
 nvfp4moe_status few_layer(const char* fn, bool mx, const float* logits, const void* x, int32_t T, int32_t E, int32_t k,
                           int32_t H, int32_t F, int32_t fp8_act, const uint8_t* w13_codes, const uint8_t* w13_scales,
                           const float* w13_g, const uint8_t* w2_codes, const uint8_t* w2_scales, const float* w2_g,
-                          void* out, void* ws, size_t ws_bytes, void* stream) {
+                          void* out, bool out_bf16, void* ws, size_t ws_bytes, void* stream) {
   if (!logits || !x || !out || (!mx && (!w13_g || !w2_g)))
     return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: null tensor pointer", fn);
   if (T < 1 || T > kFewMaxTokens || E < 1 || E > kMaxExperts || k < 1 || k > E || k > kMaxTopK)
@@ -1024,7 +1024,7 @@ nvfp4moe_status few_layer(const char* fn, bool mx, const float* logits, const vo
   nvfp4moe_status chk = few_matrix_checks(fn, "w13", w13_codes, w13_scales, 2 * F, H, 64);
   if (chk == NVFP4MOE_OK) chk = few_matrix_checks(fn, "w2", w2_codes, w2_scales, H, F, 32);
   if (chk != NVFP4MOE_OK) return chk;
-  if (!aligned(x, 16) || !aligned(logits, 4) || !aligned(out, 2) || !aligned(w13_g, 4) || !aligned(w2_g, 4))
+  if (!aligned(x, 16) || !aligned(logits, 4) || !aligned(out, out_bf16 ? 2 : 4) || !aligned(w13_g, 4) || !aligned(w2_g, 4))
     return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: x must be 16-byte aligned, the others aligned to their elements", fn);
   const FewLayerWs lay = few_layer_ws(T, k, H, F, mx);
   if (!ws || ws_bytes < lay.total)
@@ -1058,7 +1058,7 @@ nvfp4moe_status few_layer(const char* fn, bool mx, const float* logits, const vo
   down.g = w2_g;
   down.Nw = H;
   down.out = out;
-  down.out_bf16 = 1;
+  down.out_bf16 = out_bf16;
   down.ld_out = H;
   return hip_status(launch_few_layer(up, down, mx, static_cast<hipStream_t>(stream)), fn);
 }
@@ -1095,7 +1095,15 @@ nvfp4moe_status moe_layer_few_nvfp4(const float* logits, const void* x, int32_t 
                                     const float* w13_g, const uint8_t* w2_codes, const uint8_t* w2_scales,
                                     const float* w2_g, void* out, void* ws, size_t ws_bytes, void* stream) {
   return few_layer("moe_layer_few_nvfp4", false, logits, x, T, E, k, H, F, fp8_act, w13_codes, w13_scales, w13_g,
-                   w2_codes, w2_scales, w2_g, out, ws, ws_bytes, stream);
+                   w2_codes, w2_scales, w2_g, out, true, ws, ws_bytes, stream);
+}
+
+nvfp4moe_status moe_layer_few_nvfp4_f32(const float* logits, const void* x, int32_t T, int32_t E, int32_t k, int32_t H,
+                                        int32_t F, int32_t fp8_act, const uint8_t* w13_codes, const uint8_t* w13_scales,
+                                        const float* w13_g, const uint8_t* w2_codes, const uint8_t* w2_scales,
+                                        const float* w2_g, float* out, void* ws, size_t ws_bytes, void* stream) {
+  return few_layer("moe_layer_few_nvfp4_f32", false, logits, x, T, E, k, H, F, fp8_act, w13_codes, w13_scales, w13_g,
+                   w2_codes, w2_scales, w2_g, out, false, ws, ws_bytes, stream);
 }
 
 nvfp4moe_status moe_layer_few_mxfp4(const float* logits, const void* x, int32_t T, int32_t E, int32_t k, int32_t H,
@@ -1103,7 +1111,15 @@ nvfp4moe_status moe_layer_few_mxfp4(const float* logits, const void* x, int32_t 
                                     const uint8_t* w2_codes, const uint8_t* w2_scales, void* out, void* ws,
                                     size_t ws_bytes, void* stream) {
   return few_layer("moe_layer_few_mxfp4", true, logits, x, T, E, k, H, F, 0, w13_codes, w13_scales, nullptr, w2_codes,
-                   w2_scales, nullptr, out, ws, ws_bytes, stream);
+                   w2_scales, nullptr, out, true, ws, ws_bytes, stream);
+}
+
+nvfp4moe_status moe_layer_few_mxfp4_f32(const float* logits, const void* x, int32_t T, int32_t E, int32_t k, int32_t H,
+                                        int32_t F, const uint8_t* w13_codes, const uint8_t* w13_scales,
+                                        const uint8_t* w2_codes, const uint8_t* w2_scales, float* out, void* ws,
+                                        size_t ws_bytes, void* stream) {
+  return few_layer("moe_layer_few_mxfp4_f32", true, logits, x, T, E, k, H, F, 0, w13_codes, w13_scales, nullptr, w2_codes,
+                   w2_scales, nullptr, out, false, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -1364,7 +1364,11 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
     float* mine = p.part + ((size_t)at * p.most_parts + (blockIdx.x - part0)) * per;
     auto put = [&](int i, float v) {
       const int t = i / (RB * 16), n = i % (RB * 16);
-      static_cast<__bf16*>(p.out)[(size_t)t * p.ld_out + (size_t)at * (RB * 16) + n] = (__bf16)v;
+      const size_t o = (size_t)t * p.ld_out + (size_t)at * (RB * 16) + n;
+      if (p.out_bf16)
+        static_cast<__bf16*>(p.out)[o] = (__bf16)v;
+      else
+        static_cast<float*>(p.out)[o] = v;
     };
     for (int i = i0; i < per; i += kNT) {
       const int r16 = i & 15, b = (i >> 4) % RB, t = i / (RB * 16);

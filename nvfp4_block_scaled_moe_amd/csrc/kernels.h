@@ -179,7 +179,7 @@ struct FewArgs {
   int add_bf16;
   int grid;               // workgroups, set by the launcher (the launch's own count lies apart from the arguments)
   int64_t ld_add;
-  void* out;              // matvec: float32 or bf16; the layer's second launch: bf16
+  void* out;              // matvec and the layer's second launch: float32 or bf16
   int out_bf16;
   uint32_t grid_inv;      // set by the launcher: inverse() of grid,
   int64_t ld_out;

@@ -204,14 +204,15 @@ FEW_TOKENS_NVFP4_BLOCK = 8
 
 
 def moe_forward_few(x: torch.Tensor, logits: torch.Tensor, k: int, w: NVFP4Experts | MXFP4Experts,
-                    fp8_acts: bool = False):
+                    fp8_acts: bool = False, out_dtype=torch.bfloat16):
     """The MoE layer of up to 16 tokens in two launches, with 16-bit activations (after the FP8
-    round trip with ``fp8_acts``, NVFP4 only) for either weight format -> bf16 [T, H]."""
+    round trip with ``fp8_acts``, NVFP4 only) for either weight format -> bf16 [T, H], or with
+    ``out_dtype`` float32 the experts' sums before that rounding."""
     if isinstance(w, MXFP4Experts):
         if fp8_acts:
             raise ValueError("moe_forward_few: fp8_acts goes with NVFP4 experts")
-        return ops.moe_layer_few_mxfp4(x, logits, k, w.w13_t, w.w2_t)
-    return ops.moe_layer_few_nvfp4(x, logits, k, w.w13_t, w.w2_t, fp8_acts=fp8_acts)
+        return ops.moe_layer_few_mxfp4(x, logits, k, w.w13_t, w.w2_t, out_dtype=out_dtype)
+    return ops.moe_layer_few_nvfp4(x, logits, k, w.w13_t, w.w2_t, fp8_acts=fp8_acts, out_dtype=out_dtype)
 
 
 @dataclass
@@ -265,7 +266,7 @@ def moe_block_forward(resid: torch.Tensor, x: torch.Tensor, k: int, w: NVFP4Expe
     logits = router(x)
     norm = dict(post_w=post_w, gate=gate, scale=scale, pre_w=pre_w, w_offset=w_offset, eps=eps)
     if T <= (FEW_TOKENS if isinstance(w, MXFP4Experts) else FEW_TOKENS_NVFP4_BLOCK):
-        y = moe_forward_few(x, logits, k, w, fp8_acts)
+        y = moe_forward_few(x, logits, k, w, fp8_acts, torch.float32)   # (not rounded before the norm)
         if shared is not None:
             y = shared_expert_forward(x, shared, add=y)
         return ops.moe_block_norm(resid, y, **norm)

@@ -582,10 +582,11 @@ def _few_workspace(mx: bool, T: int, E: int, k: int, H: int, F: int) -> int:
     return size(T, E, k, H, F)
 
 
-def _layer_few(fn: str, mx: bool, x, logits, k, w13, w2, fp8_acts, out):
-    if x.dtype != torch.bfloat16 or x.dim() != 2 or logits.dim() != 2 or logits.shape[0] != x.shape[0]:
+def _layer_few(fn: str, mx: bool, x, logits, k, w13, w2, fp8_acts, out_dtype, out):
+    shape, lshape, p_x = x.shape, logits.shape, x.data_ptr()
+    if x.dtype != torch.bfloat16 or len(shape) != 2 or len(lshape) != 2 or lshape[0] != shape[0]:
         raise ValueError(f"{fn}: x must be bf16 [T, H] and logits [T, E]")
-    (T, H), E, F = x.shape, logits.shape[1], w2.C
+    (T, H), E, F = shape, lshape[1], w2.C
     c13, s13, g13 = _tiled(fn, w13, mx, E)
     c2, s2, g2 = _tiled(fn, w2, mx, E)
     if w13.C != H or w2.R != H or w13.R != 2 * F:
@@ -593,43 +594,47 @@ def _layer_few(fn: str, mx: bool, x, logits, k, w13, w2, fp8_acts, out):
     idx = _gpu(fn, x, logits, c13, s13, c2, s2, g13, g2, out)
     if logits.dtype != torch.float32 or not logits.is_contiguous():
         logits = logits.contiguous().float()
-    x, ldx = _rows(fn, "x", x, H, 8)
-    if ldx != H:
-        x = x.contiguous()
-    if out is not None and (out.shape != (T, H) or out.dtype != torch.bfloat16 or not out.is_contiguous()):
-        raise ValueError(f"{fn}: out must be contiguous bf16 [{T}, {H}]")
+    if p_x & 15 or not x.is_contiguous():
+        x, ldx = _rows(fn, "x", x, H, 8)
+        if ldx != H:
+            x = x.contiguous()
+        p_x = x.data_ptr()
+    if out_dtype not in _DT:
+        raise ValueError(f"{fn}: out_dtype must be float32 or bf16")
+    if out is not None and (out.shape != shape or out.dtype != out_dtype or not out.is_contiguous()):
+        raise ValueError(f"{fn}: out must be contiguous {out_dtype} [{T}, {H}]")
     lib = _lib.load()
     with _on(idx):
         if out is None:
-            out = torch.empty_like(x)
-        stream = _raw_stream(idx)
+            out = x.new_empty(shape, dtype=out_dtype)
+        nbytes = _few_workspace(mx, T, E, k, H, F)
+        ws = x.new_empty((nbytes,), dtype=torch.uint8)
         if not mx:
-            ws = x.new_empty((_few_workspace(False, T, E, k, H, F),), dtype=torch.uint8)
-            st = lib.moe_layer_few_nvfp4(logits.data_ptr(), x.data_ptr(), T, E, k, H, F, int(fp8_acts),
-                                         c13.data_ptr(), s13.data_ptr(), g13.data_ptr(),
-                                         c2.data_ptr(), s2.data_ptr(), g2.data_ptr(), out.data_ptr(),
-                                         ws.data_ptr(), ws.numel(), stream)
+            call = lib.moe_layer_few_nvfp4 if out_dtype == torch.bfloat16 else lib.moe_layer_few_nvfp4_f32
+            st = call(logits.data_ptr(), p_x, T, E, k, H, F, int(fp8_acts), c13.data_ptr(), s13.data_ptr(), g13.data_ptr(),
+                      c2.data_ptr(), s2.data_ptr(), g2.data_ptr(), out.data_ptr(), ws.data_ptr(), nbytes, _raw_stream(idx))
         else:
-            ws = x.new_empty((_few_workspace(True, T, E, k, H, F),), dtype=torch.uint8)
-            st = lib.moe_layer_few_mxfp4(logits.data_ptr(), x.data_ptr(), T, E, k, H, F, c13.data_ptr(),
-                                         s13.data_ptr(), c2.data_ptr(), s2.data_ptr(),
-                                         out.data_ptr(), ws.data_ptr(), ws.numel(), stream)
-    _lib.check(fn, st)
+            call = lib.moe_layer_few_mxfp4 if out_dtype == torch.bfloat16 else lib.moe_layer_few_mxfp4_f32
+            st = call(logits.data_ptr(), p_x, T, E, k, H, F, c13.data_ptr(), s13.data_ptr(), c2.data_ptr(), s2.data_ptr(),
+                      out.data_ptr(), ws.data_ptr(), nbytes, _raw_stream(idx))
+    if st:
+        _lib.check(fn, st)
     return out
 
 
 def moe_layer_few_nvfp4(x: torch.Tensor, logits: torch.Tensor, k: int, w13: TiledWeights, w2: TiledWeights, *,
-                        fp8_acts: bool = False, out: torch.Tensor | None = None):
+                        fp8_acts: bool = False, out_dtype=torch.bfloat16, out: torch.Tensor | None = None):
     """The whole MoE layer of up to 16 tokens in two launches: top-``k`` of ``logits`` [T, E],
     SwiGLU experts ``w13`` (E matrices [2F, H]) and ``w2`` (E matrices [H, F]), weighted sum.
-    ``x`` bf16 [T, H] (after the FP8 E4M3 round trip with ``fp8_acts``) -> bf16 [T, H]."""
-    return _layer_few("moe_layer_few_nvfp4", False, x, logits, k, w13, w2, fp8_acts, out)
+    ``x`` bf16 [T, H] (after the FP8 E4M3 round trip with ``fp8_acts``) -> bf16 [T, H], or with
+    ``out_dtype`` float32 the sums before that rounding."""
+    return _layer_few("moe_layer_few_nvfp4", False, x, logits, k, w13, w2, fp8_acts, out_dtype, out)
 
 
 def moe_layer_few_mxfp4(x: torch.Tensor, logits: torch.Tensor, k: int, w13: MxTiledWeights, w2: MxTiledWeights, *,
-                        out: torch.Tensor | None = None):
+                        out_dtype=torch.bfloat16, out: torch.Tensor | None = None):
     """moe_layer_few_nvfp4 with MXFP4 experts (16-bit activations)."""
-    return _layer_few("moe_layer_few_mxfp4", True, x, logits, k, w13, w2, False, out)
+    return _layer_few("moe_layer_few_mxfp4", True, x, logits, k, w13, w2, False, out_dtype, out)
 
 
 # ------------------------------------------------------------------ the norms around a block

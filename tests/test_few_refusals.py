@@ -122,3 +122,18 @@ def test_block_norm_refuses_outputs_that_share_bytes():
             if _touched(0, 96, T, 64) & _touched(off, 48, T, 32):
                 assert norm(T, k, {}, 24, 1, at, at + off) == _lib.ERR_INVALID_ARG
                 assert b"resid_out and next overlap" in lib.nvfp4moe_last_error()
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_layer_few_float32_output_is_checked(fmt):
+    lib, at, nv = _lib.load(), 1 << 30, fmt == "nvfp4"
+    call = getattr(lib, f"moe_layer_few_{fmt}_f32")
+    size = getattr(lib, f"moe_layer_few_{fmt}_workspace_size")(4, 8, 2, 64, 32)
+
+    def status(out=at, ws=at, n=size, T=4):
+        w = (0, at, at, at, at, at, at) if nv else (at,) * 4
+        return call(at, at, T, 8, 2, 64, 32, *w, out, ws, n, None)
+
+    for kw, want in ((dict(out=at + 2), _lib.ERR_INVALID_ARG), (dict(out=None), _lib.ERR_INVALID_ARG),
+                     (dict(T=17), _lib.ERR_INVALID_ARG), (dict(n=size - 1), _lib.ERR_WORKSPACE)):
+        assert status(**kw) == want and lib.nvfp4moe_last_error().startswith(f"moe_layer_few_{fmt}_f32".encode()), kw

@@ -124,3 +124,50 @@ def test_block_norm_outputs_over_inputs(T, H):
     for x, z, other in bad:
         with pytest.raises(RuntimeError, match="overlap"):
             ops.moe_block_norm(x, z, **other)
+
+
+def _layer(fmt, x, lg, k, w13, w2, **kw):
+    return (ops.moe_layer_few_nvfp4 if fmt == "nvfp4" else ops.moe_layer_few_mxfp4)(x, lg, k, w13, w2, **kw)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("T,E,k,H,F", [(1, 8, 2, 256, 512), (5, 12, 3, 288, 96), (16, 24, 8, 4128, 416), (16, 64, 32, 2080, 256)])
+def test_layer_few_float32_sums(fmt, T, E, k, H, F):
+    """The float32 output is what the bf16 one rounds; tiles of one and two row blocks, whole and shared."""
+    say("layer few f32", fmt, T, E, k, H, F)
+    w13, w2 = _matrices(fmt, E, 2 * F, H, 100, std=0.05)[0], _matrices(fmt, E, H, F, 200, std=0.05)[0]
+    x, lg = _rows(T, H, 9).to(DEV), inputs.random_fp32((T, E), 31).to(DEV)
+    half = _layer(fmt, x, lg, k, w13, w2)
+    out = torch.full((T, H), 7.0, device=DEV)
+    for full in (_layer(fmt, x, lg, k, w13, w2, out_dtype=torch.float32),
+                 _layer(fmt, x, lg, k, w13, w2, out_dtype=torch.float32, out=out)):
+        torch.cuda.synchronize()
+        assert full.dtype == torch.float32 and torch.equal(full.to(BF), half)
+    assert full is out and (full.view(torch.int32) & 0xffff).bool().any()
+    for bad in (dict(out_dtype=torch.float16), dict(out=out), dict(out_dtype=torch.float32, out=half)):
+        with pytest.raises(ValueError):
+            _layer(fmt, x, lg, k, w13, w2, **bad)
+
+
+def _experts(fmt, E, H, F, seed):
+    w = object.__new__(layer.NVFP4Experts if fmt == "nvfp4" else layer.MXFP4Experts)
+    w.w13_t, w.w2_t = _matrices(fmt, E, 2 * F, H, seed, std=0.05)[0], _matrices(fmt, E, H, F, seed + 1000, std=0.05)[0]
+    return w
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("shared", [False, True])
+def test_block_of_a_few_tokens_keeps_the_experts_sum_in_float32(fmt, shared):
+    """The routed experts' sum goes into the shared expert's, the norm and the residual unrounded."""
+    T, E, k, H, F = 6, 12, 3, 288, 96
+    w, sh = _experts(fmt, E, H, F, 70), _shared(fmt, H, 64, 75) if shared else None
+    x, resid = _rows(T, H, 9).to(DEV), inputs.random_fp32((T, H), 1).to(DEV)
+    lg, post = inputs.random_fp32((T, E), 31).to(DEV), (1 + inputs.random_fp32((H,), 2, std=0.1)).to(DEV)
+    got = layer.moe_block_forward(resid, x, k, w, lambda _: lg, shared=sh, post_w=post, pre_w=post)
+    y = layer.moe_forward_few(x, lg, k, w, out_dtype=torch.float32)
+    if shared:
+        y = layer.shared_expert_forward(x, sh, add=y)
+    want = ops.moe_block_norm(resid, y, post_w=post, pre_w=post)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert torch.equal(layer.moe_forward_few(x, lg, k, w), layer.moe_forward_few(x, lg, k, w, out_dtype=torch.float32).to(BF))
