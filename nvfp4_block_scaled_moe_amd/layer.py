@@ -270,6 +270,12 @@ def moe_block_forward(resid: torch.Tensor, x: torch.Tensor, k: int, w: NVFP4Expe
         if shared is not None:
             y = shared_expert_forward(x, shared, add=y)
         return ops.moe_block_norm(resid, y, **norm)
+    # (the separate calls take their sizes from the weights alone)
+    w13, w2 = w.w13_t, w.w2_t
+    if x.dtype != torch.bfloat16 or x.shape != (T, w13.C) or logits.shape != (T, w13.B) or \
+            (w2.B, w2.R, w13.R) != (w13.B, w13.C, 2 * w2.C):
+        raise ValueError(f"moe_block_forward: weights {w13.B} x [{w13.R}, {w13.C}] and {w2.B} x [{w2.R}, {w2.C}], x "
+                         f"{x.dtype} {tuple(x.shape)} (bf16 [T, H]) and logits {tuple(logits.shape)} do not fit together")
     if isinstance(w, MXFP4Experts):
         if fp8_acts:
             raise ValueError("moe_block_forward: fp8_acts goes with NVFP4 experts")

@@ -137,3 +137,22 @@ def test_layer_few_float32_output_is_checked(fmt):
     for kw, want in ((dict(out=at + 2), _lib.ERR_INVALID_ARG), (dict(out=None), _lib.ERR_INVALID_ARG),
                      (dict(T=17), _lib.ERR_INVALID_ARG), (dict(n=size - 1), _lib.ERR_WORKSPACE)):
         assert status(**kw) == want and lib.nvfp4moe_last_error().startswith(f"moe_layer_few_{fmt}_f32".encode()), kw
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("T", [3, 40])
+def test_block_refuses_what_does_not_fit(mx, T):
+    """At every number of tokens: above the few-row calls the GEMMs take their sizes from the weights."""
+    def experts(a, b):
+        w = object.__new__(layer.MXFP4Experts if mx else layer.NVFP4Experts)
+        w.w13_t, w.w2_t = a, b
+        return w
+
+    x, lg, resid = torch.zeros((T, 64), dtype=BF), torch.zeros((T, 4)), torch.zeros((T, 64))
+    good = experts(_weights(64, 64, 4, mx), _weights(64, 32, 4, mx))
+    for w, y, logits in ((good, x.float(), lg), (good, x[:, :32], lg), (good, x[0], lg), (good, x, lg[:, :3]),
+                         (good, x, lg[1:]), (experts(good.w13_t, _weights(64, 32, 3, mx)), x, lg),
+                         (experts(good.w13_t, _weights(64, 64, 4, mx)), x, lg),
+                         (experts(good.w13_t, _weights(96, 32, 4, mx)), x, lg)):
+        with pytest.raises(ValueError, match=r"fit|bf16 \[T|contiguous tiled"):
+            layer.moe_block_forward(resid, y, 2, w, lambda _: logits)
