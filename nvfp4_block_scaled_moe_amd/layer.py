@@ -240,14 +240,15 @@ def shared_expert_forward(x: torch.Tensor, w: SharedExpert, add: torch.Tensor | 
         raise ValueError(f"shared_expert_forward: add is taken up to {FEW_TOKENS} rows")
     x, ldx = ops._rows("shared_expert_forward", "x", x, w.w13.C, 8)
     x = x if ldx == w.w13.C else x.contiguous()   # (the grouped GEMM takes rows beside each other)
-    i32 = dict(dtype=torch.int32, device=x.device)
-    dense = dict(expert_offsets=torch.arange(0, 2 * T, T, **i32), active_experts=torch.zeros((1,), **i32),
-                 n_active=torch.ones((1,), **i32))
-    if nv:
-        h = ops.moe_grouped_gemm_nvfp4(ops.W4A16, ops.EPI_SWIGLU, x, w.w13, **dense)
-        return ops.moe_grouped_gemm_nvfp4(ops.W4A16, ops.EPI_NONE, h, w.w2, out_dtype=torch.float32, **dense)
-    hq, hs = ops.moe_grouped_gemm_mxfp4_swiglu_q(*ops.mxfp4_quantize(x), w.w13, **dense)
-    return ops.moe_grouped_gemm_mxfp4(ops.EPI_NONE, hq, hs, w.w2, out_dtype=torch.float32, **dense)
+    with ops._on(ops._gpu("shared_expert_forward", x, w.w13.codes, w.w2.codes)):   # (the GEMMs launch on the current GPU)
+        i32 = dict(dtype=torch.int32, device=x.device)
+        dense = dict(expert_offsets=torch.arange(0, 2 * T, T, **i32), active_experts=torch.zeros((1,), **i32),
+                     n_active=torch.ones((1,), **i32))
+        if nv:
+            h = ops.moe_grouped_gemm_nvfp4(ops.W4A16, ops.EPI_SWIGLU, x, w.w13, **dense)
+            return ops.moe_grouped_gemm_nvfp4(ops.W4A16, ops.EPI_NONE, h, w.w2, out_dtype=torch.float32, **dense)
+        hq, hs = ops.moe_grouped_gemm_mxfp4_swiglu_q(*ops.mxfp4_quantize(x), w.w13, **dense)
+        return ops.moe_grouped_gemm_mxfp4(ops.EPI_NONE, hq, hs, w.w2, out_dtype=torch.float32, **dense)
 
 
 def moe_block_forward(resid: torch.Tensor, x: torch.Tensor, k: int, w: NVFP4Experts | MXFP4Experts, router, *,
@@ -276,11 +277,13 @@ def moe_block_forward(resid: torch.Tensor, x: torch.Tensor, k: int, w: NVFP4Expe
             (w2.B, w2.R, w13.R) != (w13.B, w13.C, 2 * w2.C):
         raise ValueError(f"moe_block_forward: weights {w13.B} x [{w13.R}, {w13.C}] and {w2.B} x [{w2.R}, {w2.C}], x "
                          f"{x.dtype} {tuple(x.shape)} (bf16 [T, H]) and logits {tuple(logits.shape)} do not fit together")
-    if isinstance(w, MXFP4Experts):
-        if fp8_acts:
-            raise ValueError("moe_block_forward: fp8_acts goes with NVFP4 experts")
-        y, slot_to_row, topk_w = moe_forward_mxfp4(x, logits, k, w, reduce=False)
-    else:
-        y, slot_to_row, topk_w = moe_forward(x, logits, k, w, fp8_acts=fp8_acts, reduce=False)
+    mx = isinstance(w, MXFP4Experts)
+    if mx and fp8_acts:
+        raise ValueError("moe_block_forward: fp8_acts goes with NVFP4 experts")
+    with ops._on(ops._gpu("moe_block_forward", x, logits, w13.codes, w2.codes)):
+        if mx:
+            y, slot_to_row, topk_w = moe_forward_mxfp4(x, logits, k, w, reduce=False)
+        else:
+            y, slot_to_row, topk_w = moe_forward(x, logits, k, w, fp8_acts=fp8_acts, reduce=False)
     ys = None if shared is None else shared_expert_forward(x, shared)
     return ops.moe_block_norm(resid, y, slot_to_row=slot_to_row, topk_w=topk_w, y_add=ys, **norm)

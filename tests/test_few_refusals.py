@@ -156,3 +156,37 @@ def test_block_refuses_what_does_not_fit(mx, T):
                          (experts(good.w13_t, _weights(96, 32, 4, mx)), x, lg)):
         with pytest.raises(ValueError, match=r"fit|bf16 \[T|contiguous tiled"):
             layer.moe_block_forward(resid, y, 2, w, lambda _: logits)
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_calls_above_the_few_rows_run_on_the_tensors_gpu(mx, monkeypatch):
+    """shared_expert_forward and moe_block_forward make the tensors' GPU current for the layer's
+    calls, which launch on the current one (as the few-row calls do for theirs)."""
+    import contextlib
+    current, used = [0], []
+
+    @contextlib.contextmanager
+    def on(index):
+        before, current[0] = current[0], index
+        yield
+        current[0] = before
+
+    monkeypatch.setattr(ops, "_gpu", lambda fn, *ts: 3)
+    monkeypatch.setattr(ops, "_on", on)
+
+    def call(result):
+        return lambda *a, **kw: used.append(current[0]) or result
+
+    x, t = torch.zeros((20, 64), dtype=BF), torch.zeros((20, 64))
+    for name, result in (("moe_grouped_gemm_nvfp4", t), ("moe_grouped_gemm_mxfp4", t), ("mxfp4_quantize", (t, t)),
+                         ("moe_grouped_gemm_mxfp4_swiglu_q", (t, t)), ("moe_block_norm", (t, t))):
+        monkeypatch.setattr(ops, name, call(result))
+    for name in ("moe_forward", "moe_forward_mxfp4"):
+        monkeypatch.setattr(layer, name, call((t, t, t)))
+    layer.shared_expert_forward(x, layer.SharedExpert(_weights(128, 64, 1, mx), _weights(64, 64, 1, mx)))
+    assert used == [3] * (3 if mx else 2) and current == [0]
+    used.clear()
+    w = object.__new__(layer.MXFP4Experts if mx else layer.NVFP4Experts)
+    w.w13_t, w.w2_t = _weights(128, 64, 4, mx), _weights(64, 64, 4, mx)
+    layer.moe_block_forward(t, x, 2, w, lambda _: torch.zeros((20, 4)))
+    assert used[0] == 3 and current == [0]
