@@ -203,6 +203,13 @@ FEW_TOKENS = 16
 FEW_TOKENS_NVFP4_BLOCK = 8
 
 
+def _few(fn: str, few: bool | None, T: int, limit: int) -> bool:
+    """Whether T rows take the few-row calls: as asked, or up to ``limit``."""
+    if few and T > FEW_TOKENS:
+        raise ValueError(f"{fn}: few goes up to {FEW_TOKENS} rows, got {T}")
+    return T <= limit if few is None else few
+
+
 def moe_forward_few(x: torch.Tensor, logits: torch.Tensor, k: int, w: NVFP4Experts | MXFP4Experts,
                     fp8_acts: bool = False, out_dtype=torch.bfloat16):
     """The MoE layer of up to 16 tokens in two launches, with 16-bit activations (after the FP8
@@ -223,21 +230,26 @@ class SharedExpert:
     w2: ops.TiledWeights | ops.MxTiledWeights
 
 
-def shared_expert_forward(x: torch.Tensor, w: SharedExpert, add: torch.Tensor | None = None):
+def shared_expert_forward(x: torch.Tensor, w: SharedExpert, add: torch.Tensor | None = None, few: bool | None = None):
     """f32 [T, H] of the shared expert for bf16 rows ``x`` [T, H]: two few-row products up to 16
-    rows, the second adding ``add`` (the routed experts' output); dense grouped GEMMs above
-    (NVFP4 with 16-bit activations, MXFP4 with MXFP4 ones), where ``add`` is not taken."""
+    rows, the second adding ``add`` (the routed experts' output); dense grouped GEMMs above,
+    where ``add`` is not taken. ``few`` asks for one of the two.
+
+    With NVFP4 weights both take 16-bit activations and round h to bf16. With MXFP4 weights the
+    products do, but the GEMMs quantize x and h to MXFP4: their result is a few percent off the
+    products', and a caller that needs every batch size to round alike passes few=False."""
     nv = isinstance(w.w13, ops.TiledWeights)
     if type(w.w13) is not type(w.w2) or w.w13.B != 1 or w.w2.B != 1 or w.w13.R != 2 * w.w2.C:
         raise ValueError("shared_expert_forward: w13 must be one matrix [2F, H] and w2 one [H, F] of the same format")
     if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != w.w13.C:
         raise ValueError(f"shared_expert_forward: x must be bf16 [T, {w.w13.C}], got {x.dtype} {tuple(x.shape)}")
     T = x.shape[0]
-    if T <= FEW_TOKENS:
+    few = _few("shared_expert_forward", few, T, FEW_TOKENS)
+    if few:
         mv = ops.nvfp4_matvec if nv else ops.mxfp4_matvec
         return mv(mv(x, w.w13, ops.EPI_SWIGLU), w.w2, add=add, out_dtype=torch.float32)
     if add is not None:
-        raise ValueError(f"shared_expert_forward: add is taken up to {FEW_TOKENS} rows")
+        raise ValueError(f"shared_expert_forward: add is taken by the few-row products, up to {FEW_TOKENS} rows")
     x, ldx = ops._rows("shared_expert_forward", "x", x, w.w13.C, 8)
     x = x if ldx == w.w13.C else x.contiguous()   # (the grouped GEMM takes rows beside each other)
     with ops._on(ops._gpu("shared_expert_forward", x, w.w13.codes, w.w2.codes)):   # (the GEMMs launch on the current GPU)
@@ -254,19 +266,31 @@ def shared_expert_forward(x: torch.Tensor, w: SharedExpert, add: torch.Tensor | 
 def moe_block_forward(resid: torch.Tensor, x: torch.Tensor, k: int, w: NVFP4Experts | MXFP4Experts, router, *,
                       shared: SharedExpert | None = None, post_w: torch.Tensor | None = None,
                       gate: torch.Tensor | None = None, scale: float = 1.0, pre_w: torch.Tensor | None = None,
-                      w_offset: float = 0.0, eps: float = 1e-6, fp8_acts: bool = False):
+                      w_offset: float = 0.0, eps: float = 1e-6, fp8_acts: bool = False, few: bool | None = None):
     """One MoE block and the norms around it: logits = ``router``(x), y = the routed experts (and
     the ``shared`` one), then moe_block_norm's r' = resid + scale * gate * (post-norm of y) and
     the next block's normed input. ``x`` bf16 [T, H] is this block's normed input: the next
     of the call before, or ``ops.moe_block_norm(resid, pre_w=...)[1]`` at the start.
 
-    Up to 8 tokens (MXFP4: 16) the layer runs as two launches and the shared expert, up to 16, as
-    two more; above, the experts' rows go unsummed into the norm, which adds the shared expert's
-    output. Returns (r', next); next is None without ``pre_w``."""
+    Up to 8 tokens (MXFP4: 16) the layer runs as two launches (moe_forward_few) and the shared
+    expert, up to 16, as two more; above, the separate calls' rows (moe_forward, W4A16, or
+    moe_forward_mxfp4) go unsummed into the norm, which adds the shared expert's output. ``few``
+    asks for one of the two for both: True goes up to 16 tokens. y stays float32 either way, but
+    what is rounded before it differs: with NVFP4 experts h (to 11 bits in two launches, to bf16
+    in the separate calls); with MXFP4 experts x and h, which the separate calls quantize to MXFP4
+    and two launches keep at 16 bits. A caller that needs a request's numbers not to change that
+    way with the batch it is in passes few=False. (The separate calls take MXFP4 experts, and an
+    MXFP4 shared one, with H a multiple of 256 and F of 128; two launches with any multiples of 32.)
+
+    ``fp8_acts``: the routed experts' rows take the FP8 round trip first (NVFP4 only); the shared
+    expert's do not. Returns (r', next); next is None without ``pre_w``."""
     T = x.shape[0]
+    mx = isinstance(w, MXFP4Experts)
+    limit = FEW_TOKENS if mx else FEW_TOKENS_NVFP4_BLOCK
+    two_launches = _few("moe_block_forward", few, T, limit)
     logits = router(x)
     norm = dict(post_w=post_w, gate=gate, scale=scale, pre_w=pre_w, w_offset=w_offset, eps=eps)
-    if T <= (FEW_TOKENS if isinstance(w, MXFP4Experts) else FEW_TOKENS_NVFP4_BLOCK):
+    if two_launches:
         y = moe_forward_few(x, logits, k, w, fp8_acts, torch.float32)   # (not rounded before the norm)
         if shared is not None:
             y = shared_expert_forward(x, shared, add=y)
@@ -277,7 +301,6 @@ def moe_block_forward(resid: torch.Tensor, x: torch.Tensor, k: int, w: NVFP4Expe
             (w2.B, w2.R, w13.R) != (w13.B, w13.C, 2 * w2.C):
         raise ValueError(f"moe_block_forward: weights {w13.B} x [{w13.R}, {w13.C}] and {w2.B} x [{w2.R}, {w2.C}], x "
                          f"{x.dtype} {tuple(x.shape)} (bf16 [T, H]) and logits {tuple(logits.shape)} do not fit together")
-    mx = isinstance(w, MXFP4Experts)
     if mx and fp8_acts:
         raise ValueError("moe_block_forward: fp8_acts goes with NVFP4 experts")
     with ops._on(ops._gpu("moe_block_forward", x, logits, w13.codes, w2.codes)):
@@ -285,5 +308,5 @@ def moe_block_forward(resid: torch.Tensor, x: torch.Tensor, k: int, w: NVFP4Expe
             y, slot_to_row, topk_w = moe_forward_mxfp4(x, logits, k, w, reduce=False)
         else:
             y, slot_to_row, topk_w = moe_forward(x, logits, k, w, fp8_acts=fp8_acts, reduce=False)
-    ys = None if shared is None else shared_expert_forward(x, shared)
+    ys = None if shared is None else shared_expert_forward(x, shared, few=few)
     return ops.moe_block_norm(resid, y, slot_to_row=slot_to_row, topk_w=topk_w, y_add=ys, **norm)

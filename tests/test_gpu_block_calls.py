@@ -171,3 +171,66 @@ def test_block_of_a_few_tokens_keeps_the_experts_sum_in_float32(fmt, shared):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert torch.equal(layer.moe_forward_few(x, lg, k, w), layer.moe_forward_few(x, lg, k, w, out_dtype=torch.float32).to(BF))
+
+
+def _block(fmt, T, seed=70, E=12, k=3, H=256, F=128):
+    w, sh = _experts(fmt, E, H, F, seed), _shared(fmt, H, 128, seed + 5)
+    x, resid = _rows(T, H, 9).to(DEV), inputs.random_fp32((T, H), 1).to(DEV)
+    return w, sh, x, resid, inputs.random_fp32((T, E), 31).to(DEV), (1 + inputs.random_fp32((H,), 2, std=0.1)).to(DEV), k
+
+
+@pytest.mark.parametrize("fmt,T", [("nvfp4", 3), ("nvfp4", 8), ("nvfp4", 12), ("nvfp4", 16), ("nvfp4", 20), ("mxfp4", 3),
+                                   ("mxfp4", 16), ("mxfp4", 20)])
+@pytest.mark.parametrize("few", [None, True, False])
+def test_block_by_the_way_asked_for(fmt, T, few):
+    """few: two launches and products, or the separate calls, at every number of tokens that they take."""
+    say("block few", fmt, T, few)
+    w, sh, x, resid, lg, post, k = _block(fmt, T)
+    run = lambda **kw: layer.moe_block_forward(resid, x, k, w, lambda _: lg, shared=sh, post_w=post, pre_w=post, **kw)  # noqa: E731
+    if few and T > 16:
+        with pytest.raises(ValueError, match="up to 16"):
+            run(few=True)
+        return
+    got = run(few=few)
+    if T <= (8 if fmt == "nvfp4" else 16) if few is None else few:
+        y = layer.shared_expert_forward(x, sh, add=layer.moe_forward_few(x, lg, k, w, out_dtype=torch.float32))
+        want = ops.moe_block_norm(resid, y, post_w=post, pre_w=post)
+    else:
+        forward = layer.moe_forward if fmt == "nvfp4" else layer.moe_forward_mxfp4
+        y, s2r, tw = forward(x, lg, k, w, reduce=False)
+        want = ops.moe_block_norm(resid, y, post_w=post, pre_w=post, slot_to_row=s2r, topk_w=tw,
+                                  y_add=layer.shared_expert_forward(x, sh, few=few))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_block_of_mxfp4_experts_that_the_separate_calls_do_not_take():
+    """F off the multiples of 128: two launches take it, the separate calls refuse it."""
+    w, sh, x, resid, lg, _, k = _block("mxfp4", 5, F=96)
+    run = lambda **kw: layer.moe_block_forward(resid, x, k, w, lambda _: lg, shared=sh, **kw)  # noqa: E731
+    assert torch.isfinite(run()[0]).all()
+    with pytest.raises(RuntimeError, match="Nw"):
+        run(few=False)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("T", [1, 7, 16])
+def test_shared_expert_by_the_way_asked_for(fmt, T):
+    """few=False at a few rows: the GEMMs that more rows take, a row's result the same in both batches
+    but for the order of its sums (MXFP4 quantizes each row by itself)."""
+    say("shared few", fmt, T)
+    H, F = 512, 256
+    sh = _shared(fmt, H, F, 60)
+    x = _rows(24, H, 4).to(DEV)
+    many = layer.shared_expert_forward(x, sh)
+    got = layer.shared_expert_forward(x[:T], sh, few=False)
+    products = layer.shared_expert_forward(x[:T], sh, few=True)
+    torch.cuda.synchronize()
+    # float32 sums of 512 and 256 products in another order may move single roundings of h, each to
+    # bf16 by 2^-8, or to its MXFP4 code by half of its distance to the next (at most a third) of itself
+    assert (got - many[:T]).norm() <= (2.0 ** -8 if fmt == "nvfp4" else 2.0 ** -5) * many[:T].norm()
+    assert torch.equal(products, layer.shared_expert_forward(x[:T], sh)) and not torch.equal(products, got)
+    with pytest.raises(ValueError, match="few-row products"):
+        layer.shared_expert_forward(x[:T], sh, add=got, few=False)
+    with pytest.raises(ValueError, match="up to 16"):
+        layer.shared_expert_forward(x, sh, few=True)
