@@ -234,3 +234,36 @@ def test_shared_expert_by_the_way_asked_for(fmt, T):
         layer.shared_expert_forward(x[:T], sh, add=got, few=False)
     with pytest.raises(ValueError, match="up to 16"):
         layer.shared_expert_forward(x, sh, few=True)
+
+
+@pytest.mark.parametrize("T", [1, 5, 8, 12, 16, 40])
+@pytest.mark.parametrize("shared", [False, True])
+def test_block_with_fp8_rows(T, shared):
+    """fp8_acts reaches the routed experts' rows, in two launches and in the separate calls, and not
+    the shared expert's: the block on rows that took the round trip before, the shared expert on x."""
+    say("block fp8", T, shared)
+    w, sh, x, resid, lg, post, k = _block("nvfp4", T)
+    got = layer.moe_block_forward(resid, x, k, w, lambda _: lg, shared=sh if shared else None, post_w=post, pre_w=post,
+                                  fp8_acts=True)
+    rows = ops.act_fp8_e4m3_roundtrip(x)
+    if T <= 8:
+        y = layer.moe_forward_few(rows, lg, k, w, out_dtype=torch.float32)
+        if shared:
+            y = layer.shared_expert_forward(x, sh, add=y)
+        want = ops.moe_block_norm(resid, y, post_w=post, pre_w=post)
+    else:
+        y, s2r, tw = layer.moe_forward(rows, lg, k, w, reduce=False)
+        ys = layer.shared_expert_forward(x, sh) if shared else None
+        want = ops.moe_block_norm(resid, y, post_w=post, pre_w=post, slot_to_row=s2r, topk_w=tw, y_add=ys)
+    plain = layer.moe_block_forward(resid, x, k, w, lambda _: lg, shared=sh if shared else None, post_w=post, pre_w=post)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and not torch.equal(got[0], plain[0])
+
+
+@pytest.mark.parametrize("T", [2, 13])
+def test_layer_few_with_fp8_rows_by_the_layer(T):
+    w, _, x, _, lg, _, k = _block("nvfp4", T)
+    got = layer.moe_forward_few(x, lg, k, w, fp8_acts=True)
+    want = layer.moe_forward_few(ops.act_fp8_e4m3_roundtrip(x), lg, k, w)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and not torch.equal(got, layer.moe_forward_few(x, lg, k, w))
