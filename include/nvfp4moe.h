@@ -497,7 +497,7 @@ size_t moe_grouped_gemm_mxfp8_workspace_size(int32_t rows, int32_t E, int32_t Nw
  * nvfp4_matvec, mxfp4_matvec -- products of up to 16 rows with one 4-bit weight matrix, for the
  * dense layers and the shared experts beside the routed ones at decode sizes; one launch, no
  * workspace, 16-bit activations with either weight format ([P2] "The NVFP4 Pivot": W4A16).
- *     P = X . W^T  (float32 accumulation of exact products; NVFP4: * w_g[0])
+ *     P = X . W^T  (products accumulated in float32; NVFP4: * w_g[0])
  *     EPI_NONE  : out = P + add                                 [T, Nw]
  *     EPI_SWIGLU: out = silu(P[:, :Nw/2]) * P[:, Nw/2:] + add   [T, Nw/2]
  * rounded once, to out_dtype.
@@ -513,8 +513,14 @@ size_t moe_grouped_gemm_mxfp8_workspace_size(int32_t rows, int32_t E, int32_t Nw
  *               elements apart; or NULL. May be out itself (same type and row distance).
  *   out, out_dtype, ld_out   device F32 or BF16 [T, n] (output), rows ld_out >= n elements
  *               apart; what lies between the rows is not written.
- * out must not overlap x, nor add unless it is add. A row's result does not depend on the other rows' values (their number
- * may change the order of the sums); a NaN or Inf in one row stays in that row.
+ * The products are exact: MXFP4 for every bf16 x; NVFP4, whose rows become f16 with a power of two
+ * for each row (for each 128 columns of it where T rows of K do not fit in LDS, T * K rounded up
+ * to 128 columns > 57344), for elements down to 2^-31 of the row's (those columns') largest finite
+ * magnitude. Smaller ones are rounded to multiples of 2^-38 of that magnitude's power of two, so that
+ * what is below 2^-39 of it counts as zero, also where the large element meets a zero weight.
+ * out must not overlap x, nor add unless it is add. A row's result does not depend on the other
+ * rows' values; their number may change the order of the sums and, for elements that small, which
+ * of the two scalings applies. A NaN or Inf in one row stays in that row.
  * ------------------------------------------------------------------------- */
 nvfp4moe_status nvfp4_matvec(nvfp4moe_epilogue epi, const void* x, int64_t ldx, int32_t T, const uint8_t* w_codes,
                              const uint8_t* w_scales, const float* w_g, int32_t Nw, int32_t K, const void* add,
@@ -537,7 +543,10 @@ nvfp4moe_status mxfp4_matvec(nvfp4moe_epilogue epi, const void* x, int64_t ldx, 
  *              adds to it or norms it: a shared expert, moe_block_norm)
  * with x' = x, or (fp8_act) x after the FP8 E4M3 round trip of act_fp8_e4m3_roundtrip, whose
  * scale is taken over all T rows. Sums are float32; h is held between the launches as f16 with
- * a power of two for every 16 columns (NVFP4) or as bf16 (MXFP4); out is rounded once.
+ * a power of two for every 16 columns (NVFP4) or as bf16 (MXFP4, as h of the grouped GEMMs); out is
+ * rounded once. NVFP4 rows x' become f16 as in nvfp4_matvec, with one power of two a row, and so
+ * do the rows of h when they are read: exact down to 2^-28 of the row's largest finite magnitude,
+ * smaller ones rounded to multiples of 2^-38 of its power of two.
  *
  *   logits      device float [T, E], finite.
  *   x           device bf16 [T, H], 16-byte aligned.

@@ -77,3 +77,28 @@ def test_matvec_swiglu_rows_near_the_end_of_the_range(fmt, Nw):
     h, err = _swiglu(*_product(x.double().numpy(), rows(np.concatenate([sel, sel + n]))))
     assert (np.abs(h) < 2.0 ** 128).all()
     _check(np_(got)[:, sel], h, err, torch.float32)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("T,Nw,K", [(1, 64, 544), (9, 48, 6144), (10, 48, 6144), (12, 16448, 5152)])
+@pytest.mark.parametrize("down", [20, 31, 36, 45])
+def test_matvec_small_elements_beside_a_large_one(fmt, T, Nw, K, down):
+    """A large element that meets zero weights, the others 2^-down of it: NVFP4 products are exact down to
+    2^-31 (of the row's largest magnitude, or of the chunk's where the rows do not fit); below, each
+    element is off by at most half a step, 2^-39 of that magnitude's power of two. MXFP4 is exact."""
+    say("matvec small beside large", fmt, T, Nw, K, down)
+    w, rows = _matrix(fmt, Nw, K, 0.03, 15, clear=(Nw, 32))
+    # magnitudes from 2^(60 - down) up to twice that, with all eight bits in use
+    x = ((1 + torch.rand((T, K), generator=torch.Generator().manual_seed(4))) * 2.0 ** (60 - down)).to(torch.bfloat16)
+    x[:, ::3] *= -1
+    x[:, 5] = 1.5 * 2.0 ** 60
+    sel = np.unique(np.concatenate([np.arange(16), np.arange(Nw - 16, Nw)]))
+    got = _call(fmt)(x.to(DEV), w, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    W = rows(sel)
+    assert (W[:, 5] == 0).all()
+    P, err = _product(x.double().numpy(), W)
+    if fmt == "nvfp4" and down > 31:
+        fits = T * ((K + 127) // 128 * 128) <= 57344
+        err = err + 2.0 ** (60 - 39) * np.abs(W if fits else W[:, :128]).sum(1)
+    _check(np_(got)[:, sel], P, err, torch.float32)
