@@ -102,3 +102,28 @@ def test_matvec_small_elements_beside_a_large_one(fmt, T, Nw, K, down):
         fits = T * ((K + 127) // 128 * 128) <= 57344
         err = err + 2.0 ** (60 - 39) * np.abs(W if fits else W[:, :128]).sum(1)
     _check(np_(got)[:, sel], P, err, torch.float32)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("T,K", [(2, 416), (11, 416), (11, 6144)])
+def test_matvec_infinite_elements(fmt, T, K):
+    """An infinite element gives its row Inf of the product's sign where the weight it meets is not
+    zero, NaN where it is, and leaves the other rows as they are."""
+    say("matvec infinite", fmt, T, K)
+    w, rows = _matrix(fmt, 64, K, 0.03, 19)
+    W = rows(np.arange(64))
+    x = _rows(T, K, 8)
+    at = {0: (200, float("inf")), T - 1: (1, float("-inf"))}
+    for t, (c, v) in at.items():
+        x[t, c] = v
+        assert (W[:, c] != 0).sum() >= 32 and (W[:, c] == 0).any()
+    got = np_(_call(fmt)(x.to(DEV), w, out_dtype=torch.float32))
+    with np.errstate(invalid="ignore"):
+        P, err = _product(x.double().numpy(), W)
+    for t in range(T):
+        if t in at:
+            c, v = at[t]
+            nz = W[:, c] != 0
+            assert np.array_equal(got[t][nz], np.sign(W[nz, c]) * v) and np.isnan(got[t][~nz]).all()
+        else:
+            _check(got[t], P[t], err[t], torch.float32)
