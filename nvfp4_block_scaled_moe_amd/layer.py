@@ -196,10 +196,15 @@ def moe_forward_mxfp4(x: torch.Tensor, logits: torch.Tensor, k: int, w: MXFP4Exp
 # ------------------------------------------------------------------ a few tokens, and the block
 #: rows up to which the few-row calls run (nvfp4_matvec, moe_layer_few_nvfp4 and their MXFP4 forms)
 FEW_TOKENS = 16
-#: tokens up to which the block takes NVFP4 layers as two launches: cold weights, two launches / the
-#: separate calls, 256 experts of 6144 x 2048 top-8 and 512 of 4096 x 1024 top-22 with FP8 rows, us:
-#: 1 token 45 / 52 and 46 / 54, 8 tokens 232 / 234 and 206 / 205, 16 tokens 388 / 382 and 343 / 323.
-#: (MXFP4: 43 / 76, 217 / 256 and 363 / 407; two launches up to FEW_TOKENS, with 16-bit activations.)
+#: tokens up to which the block takes NVFP4 layers as two launches, set by layers of gigabytes. Cold
+#: weights in a graph, two launches / the separate calls, 256 experts of 6144 x 2048 top-8 and 512 of
+#: 4096 x 1024 top-22, us: 1 token 46 / 54 and 48 / 55, 8 tokens 237 / 238 and 210 / 208, 12 tokens
+#: 312 / 304 and 285 / 273, 16 tokens 390 / 381 and 346 / 328. Layers whose touched weights stay below a
+#: gigabyte are the faster in two launches up to FEW_TOKENS, and a caller with those passes few=True:
+#: 8 experts of 256 x 512 top-2, 16 tokens 17 / 26; 60 of 2080 x 1376 top-4 63 / 85; 128 of 2048 x 768
+#: top-8 60 / 67; 64 of 4096 x 1024 top-8 89 / 95; 128 of 4096 x 1536 top-8 (0.88 GB) 168 / 177.
+#: (MXFP4 is the faster at every size, 43 / 76, 221 / 261 and 361 / 407 for the first layer, with 16-bit
+#: activations: two launches up to FEW_TOKENS.)
 FEW_TOKENS_NVFP4_BLOCK = 8
 
 
