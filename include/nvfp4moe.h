@@ -543,7 +543,7 @@ nvfp4moe_status mxfp4_matvec(nvfp4moe_epilogue epi, const void* x, int64_t ldx, 
  *              adds to it or norms it: a shared expert, moe_block_norm)
  * with x' = x, or (fp8_act) x after the FP8 E4M3 round trip of act_fp8_e4m3_roundtrip, whose
  * scale is taken over all T rows. Sums are float32; h is held between the launches as f16 with
- * a power of two for every 16 columns (NVFP4) or as bf16 (MXFP4, as h of the grouped GEMMs); out is
+ * a power of two for every 16 columns (NVFP4: 11 bits) or as two bf16 values (MXFP4: 16 bits); out is
  * rounded once. NVFP4 rows x' become f16 as in nvfp4_matvec, with one power of two a row, and so
  * do the rows of h when they are read: exact down to 2^-28 of the row's largest finite magnitude,
  * smaller ones rounded to multiples of 2^-38 of its power of two.

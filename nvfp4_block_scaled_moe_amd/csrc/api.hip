@@ -1001,7 +1001,7 @@ struct FewLayerWs {
 FewLayerWs few_layer_ws(int32_t T, int32_t k, int32_t H, int32_t F, bool mx) {
   FewLayerWs w{};
   w.plan = round_up(sizeof(FewPlan));
-  w.h = round_up((size_t)T * k * F * 2);
+  w.h = round_up((size_t)T * k * F * (mx ? 4 : 2));   // MXFP4: two bf16 values for each
   w.hexp = mx ? 0 : round_up((size_t)T * k * ((F + 127) / 128) * 8);
   w.part = round_up((size_t)few_down_parts(T, k, H, F) * T * H * 4);
   w.total = w.plan + w.h + w.hexp + w.part;

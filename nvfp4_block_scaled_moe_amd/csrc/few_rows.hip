@@ -29,10 +29,10 @@
 //     that replace a launch), the second reads the list that one of them left. An item is an
 //     expert with up to 4 of its tokens; an expert with more tokens takes several items.
 //   * h between the launches: f16 with a power of two for each 16 columns (NVFP4: 11 bits of what
-//     is then summed in float32), bf16 (MXFP4: 8 bits, as h of the grouped GEMMs, because the
-//     weights' operand is bf16. It takes the layer's error from the 0.0017 of its bf16 output to 0.0024.
-//     Two bf16 values for each of h would take it back for 4-6%: 2 tokens of 60 experts 21.2 -> 22.5 us,
-//     one of 256 40.6 -> 42.4, 16 of 256 353 -> 373; not taken).
+//     is then summed in float32), or two bf16 values, the second what the first's rounding left
+//     (MXFP4: 16 bits; their matrix operand is bf16, and with its 8 bits alone the layer's error is
+//     0.0024 instead of the 0.0017 of its bf16 output. The second values' products cost 2-5%: 16
+//     tokens of 256 experts 353 -> 360 us, one 40.6 -> 41.4, 2 of 60 21.3 -> 22.1).
 //   * The second launch adds a token's experts in its accumulators, in a fixed order: no
 //     float32 rows of the experts go through memory, and no reduce launch follows.
 #include <hip/hip_runtime.h>
@@ -865,7 +865,12 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
             const uint32_t hr = (uint32_t)s_row0[it] + (uint32_t)col;
             const int F = p.Nw / 2, f = osub * 16 + r16;
             if (MX) {
-              if (osub < nsub) static_cast<__bf16*>(p.h)[(size_t)hr * F + f] = (__bf16)v;
+              if (osub < nsub) {   // (rows [2][F]: the value, and what its rounding left)
+                const __bf16 hi = (__bf16)v;
+                __bf16* at = static_cast<__bf16*>(p.h) + (size_t)hr * 2 * F + f;
+                at[0] = hi;
+                at[F] = fabsf((float)hi) < INFINITY ? (__bf16)(v - (float)hi) : (__bf16)0.0f;
+              }
             } else {
               const uint32_t top = row16_max(finite_abs_bits(v));
               const int e2 = top ? max((int)(top >> 23) - 141, kNoExp) : kNoExp;
@@ -1158,7 +1163,7 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
   typedef Decode<MX> Dec;
   typedef typename Dec::Op Op;
   static_assert(kFewMaxSlots <= kNT, "a thread for each row and item");
-  __shared__ __attribute__((aligned(16))) unsigned char s_row[kW][kItemTok * kRowBytes];
+  __shared__ __attribute__((aligned(16))) unsigned char s_row[kW][(MX ? 2 : 1) * kItemTok * kRowBytes];
   __shared__ __attribute__((aligned(16))) float s_red[kW * RB][16 * 16];
   __shared__ uint32_t s_item[kFewMaxSlots];
   __shared__ uint16_t s_row0[kFewMaxSlots];
@@ -1225,23 +1230,38 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
     left = (int)(share.begin(blockIdx.x + 1) - x0);
   }
 
-  const __amdgpu_buffer_rsrc_t hr = make_rsrc(p.h, (uint32_t)S * (uint32_t)F * 2u);
+  __amdgpu_buffer_rsrc_t hr = make_rsrc(p.h, (uint32_t)S * (uint32_t)F * 2u);   // MXFP4: the item's rows
   const __amdgpu_buffer_rsrc_t er = make_rsrc(p.hexp, (uint32_t)S * nch * 8u);
   const uint32_t wrow = nch * 1024u, srow = (MX ? (nch + 15) >> 4 : (nch + 7) >> 3) * 1024u;   // of a row block
   const uint32_t lane16 = 16u * lane;
   const bool tail = (nch - 1) * kChunk + 8u * l16 >= (uint32_t)F;   // no columns in a row's last chunk
   __amdgpu_buffer_rsrc_t wr, sr;       // the tile's row blocks of the item's matrix
   uint32_t hoff = kOOB, eoff = kOOB;   // this lane's place in a row of h and of its exponents
+  // MXFP4: one load holds two rows, the values in lane groups 0 and 1 and what their rounding left in
+  // 2 and 3; only items of more than two tokens need another. (A load costs its instruction, also out
+  // of range: two for every item take the layer of 16 tokens from 353 us to 371, one and a branch 361.)
+  uint32_t hoff2 = kOOB;
+  int pairs_l = 1;
   auto open_item = [&](int a) {
     const uint32_t w = (uint32_t)__builtin_amdgcn_readfirstlane((int)s_item[a]);
     wr = make_rsrc(p.codes + (size_t)(w >> 16) * wbytes + (uint32_t)tile * RB * wrow, RB * wrow);
     sr = make_rsrc(p.scales + (size_t)(w >> 16) * sbytes + (uint32_t)tile * RB * srow, RB * srow);
-    const bool in = g < __popc(w & 0xffffu);
-    const uint32_t hrow = (uint32_t)s_row0[a] + (uint32_t)g;
-    hoff = in ? (hrow * (uint32_t)F + 8u * l16) * 2u : kOOB;
-    eoff = in ? hrow * (nch * 8u) + (l16 >> 3) * 4u : kOOB;
+    const int ncol = __popc(w & 0xffffu);
+    if (MX) {
+      const uint32_t r0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)s_row0[a]), frow4 = (uint32_t)F * 4u;
+      hr = make_rsrc(static_cast<const char*>(p.h) + (size_t)r0 * frow4, (uint32_t)ncol * frow4);
+      const uint32_t at = (uint32_t)(g & 1) * frow4 + (uint32_t)(g >> 1) * (uint32_t)F * 2u + 16u * l16;
+      hoff = (g & 1) < ncol ? at : kOOB;
+      hoff2 = (g & 1) + 2 < ncol ? at + 2u * frow4 : kOOB;
+      pairs_l = (ncol + 1) >> 1;
+    } else {
+      const bool in = g < ncol;
+      const uint32_t hrow = (uint32_t)s_row0[a] + (uint32_t)g;
+      hoff = in ? (hrow * (uint32_t)F + 8u * l16) * 2u : kOOB;
+      eoff = in ? hrow * (nch * 8u) + (l16 >> 3) * 4u : kOOB;
+    }
   };
-  u32x4 wring[D][RB], xring[D];
+  u32x4 wring[D][RB], xring[D], yring[D] = {};
   uint32_t sring[D][RB];
   uint32_t ering[D];   // the exponents of four blocks of 16 columns, the lane's own among them
   // The loads' position: item and chunk of this wave's next pair in the tile, and its steps left.
@@ -1265,6 +1285,7 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
     }
     const bool last = c == nch - 1;
     xring[d] = ld128(hr, settled((last && tail ? kOOB : hoff) | out), (c * 256u) & all);
+    if (MX && pairs_l > 1) yring[d] = ld128(hr, settled((last && tail ? kOOB : hoff2) | out), (c * 256u) & all);
     if (!MX) ering[d] = ld32(er, settled(eoff | out), (c * 8u) & all);
     const int a0 = a_l;
     --run_l;
@@ -1277,13 +1298,15 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
   bool has = false;     // the lane's token is one of the item's
   uint32_t frow = 0;    // the bytes of its row in the wave's LDS
   float mul = 0.0f;     // and what its products are multiplied with
+  int pairs = 1;        // MXFP4: loads that hold the item's rows
   int top = 0;          // the exponent of the row that the lane reads (its 16-lane group's)
   auto take_item = [&](int i) {
     const uint32_t w = (uint32_t)__builtin_amdgcn_readfirstlane((int)s_item[i]);
     const uint32_t r0 = s_row0[i];
     has = (w >> l16) & 1u;
     const uint32_t fr = (uint32_t)__popc(w & ((1u << l16) - 1u)) & (kItemTok - 1);
-    frow = settled(fr * kRowBytes + 64u * g);
+    frow = settled((MX ? (fr & 1) + (fr >> 1) * kItemTok : fr) * kRowBytes + 64u * g);
+    pairs = (__popc(w & 0xffffu) + 1) >> 1;
     mul = has ? s_mul[r0 + fr] : 0.0f;
     if (!MX) top = g < __popc(w & 0xffffu) ? s_top[r0 + g] : 0;
   };
@@ -1319,22 +1342,29 @@ __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {
           const uint32_t cc = (uint32_t)c;
           if (MX) {
             *reinterpret_cast<u32x4*>(row + g * kRowBytes + 16 * l16) = xring[d];
+            if (pairs > 1) *reinterpret_cast<u32x4*>(row + (kItemTok + g) * kRowBytes + 16 * l16) = yring[d];
           } else {
             const int e2 = (int)(int8_t)(ering[d] >> (4u * (l16 & 6)));
             const f16 f = (f16)ldexpf(1.0f, min(e2 - top, 0));   // (no exponent past the row's columns)
             *reinterpret_cast<f16x8*>(row + g * kRowBytes + 16 * l16) = __builtin_bit_cast(f16x8, xring[d]) * f;
           }
           __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-          Op bf[4];
+          Op bf[4], rest[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) bf[j] = *reinterpret_cast<const Op*>(row + frow + 16 * j);
+          for (int j = 0; j < 4; ++j) {
+            bf[j] = *reinterpret_cast<const Op*>(row + frow + 16 * j);
+            if (MX) rest[j] = *reinterpret_cast<const Op*>(row + frow + 2 * kRowBytes + 16 * j);
+          }
           __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
           for (int b = 0; b < RB; ++b) {
             Op wf[4];
             Dec::run(wring[d][b], scale_of<MX>(sring[d][b], cc), wf);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[b] = Dec::mfma(wf[j], bf[j], acc[b]);
+            for (int j = 0; j < 4; ++j) {
+              acc[b] = Dec::mfma(wf[j], bf[j], acc[b]);
+              if (MX) acc[b] = Dec::mfma(wf[j], rest[j], acc[b]);
+            }
           }
         }
         issue(d);

@@ -189,7 +189,7 @@ struct FewArgs {
   int fp8;                // layer, NVFP4: the rows first take the FP8 E4M3 round trip
   uint32_t tpi_inv;       //   of an item's tiles (first launch), and
   FewPlan* plan;          // layer workspace
-  void* h;                // [T * k, F] f16 (NVFP4) or bf16 (MXFP4)
+  void* h;                // [T * k, F] f16 (NVFP4) or [T * k, 2, F] bf16 (MXFP4: values, and the rest)
   int down_tiles;         // tiles of the second launch
   uint32_t nch_inv;       //   of the chunks of a row (second launch)
   float* part;            // [down_tiles, most_parts, 32 T] sums of a tile that workgroups share
