@@ -16,8 +16,8 @@
 // 8192 rows of 7168 (y and next bf16, r float32: 704 MB): 144 us, 4.9 TB/s, where a copy reaches
 // 5.1-5.2; with one group a thread 165 us, with the weights requested ahead, too, 167 (fewer
 // workgroups a CU), with r requested behind y 152. The experts' rows (float32, 8 a token, 6144 columns,
-// bf16 r): 4096 tokens (957 MB) 193-196 us, 4.9 TB/s; 1024 57 us and 256 15.3 us, 0.8 of the copy rate.
-// One row of 8 x 6144: 6.1-6.6 us, of 37 x 1000: 3.0-3.8 us, bound by the latency of the launch and of
+// bf16 r): 4096 tokens (957 MB) 194 us, 4.9 TB/s; 1024 57 us and 256 15.0 us, 0.8 of the copy rate.
+// One row of 8 x 6144: 6.2 us, of 37 x 1000: 3.0 us, bound by the latency of the launch and of
 // two dependent reads; requested one after the other, as they are used, the tensors took 1.0 and 0.7
 // us more.
 #include "gemm_common.h"

@@ -369,13 +369,13 @@ __device__ __forceinline__ void fetch_args(const FewArgs& p) {
 // the item. Waves deal out the chunks ks at a time (ks = 1 .. 16: kW / ks groups of
 // waves, each with RB row blocks of its own).
 //
-// Measured (the kernel alone, weights cold). Products: 2048 x 6144, one row, 7.1 MB: 6.5-7.2 us;
-// 2064 x 1184, MXFP4, 5 rows, 1.3 MB: 4.8 us; SwiGLU 1024 x 256, one row: 4.4-5.2 us. These are
+// Measured (the kernel alone, weights cold). Products: 2048 x 6144, one row, 7.1 MB: 6.8 us;
+// 2064 x 1184, MXFP4, 5 rows, 1.3 MB: 4.9 us; SwiGLU 1024 x 256, one row: 4.7 us. These are
 // latency: ~1 us of launch and arguments, 2 us until the rows are operands, 2 us until the weights
 // are there, 1 us of sums and stores; a CU alone draws about 45 B/ns. The layer: 16 tokens of 256
-// experts, 6144 x 2048, 1.43 GB: 240-250 us, 5.9 TB/s, where plain reads reach 6.0-6.5; one token of it,
+// experts, 6144 x 2048, 1.43 GB: 245-251 us, 5.8 TB/s, where plain reads reach 6.0-6.5; one token of it,
 // 113 MB: 26 us, of which 4-5 are routing and staging and 2 the last tile's sums; 3 tokens of 8, 256 x
-// 512: 7.8 us.
+// 512: 7.3 us.
 // 16-byte pieces of the rows a thread requests together: one row seldom has more than one for each.
 constexpr int pass_batch(int ntok) { return ntok > 4 ? 4 : 1; }
 
@@ -899,8 +899,8 @@ __global__ __launch_bounds__(kNT, 4) void few_up_kernel(const FewArgs p) {
 // turns its chunk of the rows itself, in a piece of LDS of its own, with a power of two for every
 // (row, chunk). The turning costs about as much as the decode of four weight tiles, and is most of
 // the time where there are few weight rows: 2048 x 6144 with 16 rows 9.6 us, MXFP4 7.3 (not turned).
-// Far from the reads' bound at ordinary sizes, 6144 columns: 8192 weight rows 12.4 us (of 5.6), MXFP4
-// 10.5 (5.3), 16384 20.3 (11.2) and 17-18 (10.6): the rows are turned again for each tile, and with
+// Far from the reads' bound at ordinary sizes, 6144 columns: 8192 weight rows 12.2 us (of 5.6), MXFP4
+// 9-11 (5.3), 16384 20.9 (11.2) and 17-18 (10.6): the rows are turned again for each tile, and with
 // two row blocks a wave one chunk is under way.
 template <bool MX, bool SWIGLU, int RB, int D>
 __global__ __launch_bounds__(kLongNT, 4) void few_long_kernel(const FewArgs p) {
@@ -1036,7 +1036,7 @@ __global__ __launch_bounds__(kLongNT, 4) void few_long_kernel(const FewArgs p) {
 //
 // Between two bounds: the vector units are busy half the time (79 instructions a tile and wave, 32
 // of them the decoding, 25 the rows), and the reads go at three quarters of the memory's rate. 65536 x
-// 6144 at 16 rows: 48-50 us, 4.7 TB/s (MXFP4 46); few_long_kernel, in which every wave turns its own
+// 6144 at 16 rows: 47.7 us, 4.8 TB/s (MXFP4 43); few_long_kernel, in which every wave turns its own
 // chunks, 71; 16 waves sharing (half the turning, but all of a CU's waves at one barrier) 50; two
 // row blocks a wave 51; two or eight chunks under way 52 and 50.
 template <bool MX, bool SWIGLU, int RB, int W, int D>
@@ -1153,9 +1153,9 @@ __global__ __launch_bounds__(W* kWave, 4) void few_wide_kernel(const FewArgs p) 
 //
 // A wave's pair needs up to four rows' chunk of h beside the weights, brought to the row's common
 // exponent on its way through LDS. Measured: 16 tokens of 256 experts, 6144 x 2048, 0.71 GB:
-// 134-145 us, 5.0-5.3 TB/s; one token, 57 MB: 17.5 us, of which 3 pass until the list is read and the
-// ring is full and 2-3 in the last sums; 2 tokens of 60, 2080 x 1376, MXFP4, 12 MB: 8.6 us; 3 of 8,
-// 256 x 512: 5.6-6.0 us. Keeping the ring full over a tile's end (the next tile's loads under its sums)
+// 136 us, 5.2 TB/s; one token, 57 MB: 17.0 us, of which 3 pass until the list is read and the
+// ring is full and 2-3 in the last sums; 2 tokens of 60, 2080 x 1376, MXFP4, 12 MB: 9.3 us; 3 of 8,
+// 256 x 512: 5.3 us. Keeping the ring full over a tile's end (the next tile's loads under its sums)
 // brought nothing when the layer of one token took 50.4 us: 50.9.
 template <bool MX, int RB>
 __global__ __launch_bounds__(kNT, 4) void few_down_kernel(const FewArgs p) {

@@ -203,8 +203,8 @@ FEW_TOKENS = 16
 #: gigabyte are the faster in two launches up to FEW_TOKENS, and a caller with those passes few=True:
 #: 8 experts of 256 x 512 top-2, 16 tokens 17 / 26; 60 of 2080 x 1376 top-4 63 / 85; 128 of 2048 x 768
 #: top-8 60 / 67; 64 of 4096 x 1024 top-8 89 / 95; 128 of 4096 x 1536 top-8 (0.88 GB) 168 / 177.
-#: (MXFP4 is the faster at every size, 43 / 76, 221 / 261 and 361 / 407 for the first layer, with 16-bit
-#: activations: two launches up to FEW_TOKENS.)
+#: (MXFP4 is the faster at every size, 44 / 76, 225 / 258 and 364 / 402 at 1, 8 and 16 tokens of the first
+#: layer, with 16-bit activations: two launches up to FEW_TOKENS.)
 FEW_TOKENS_NVFP4_BLOCK = 8
 
 
