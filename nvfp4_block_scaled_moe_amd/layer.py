@@ -283,9 +283,10 @@ def moe_block_forward(resid: torch.Tensor, x: torch.Tensor, k: int, w: NVFP4Expe
     asks for one of the two for both: True goes up to 16 tokens. y stays float32 either way, but
     what is rounded before it differs: with NVFP4 experts h (to 11 bits in two launches, to bf16
     in the separate calls); with MXFP4 experts x and h, which the separate calls quantize to MXFP4
-    while two launches take x as it is and hold h in 16 bits. A caller that needs a request's numbers not to change that
-    way with the batch it is in passes few=False. (The separate calls take MXFP4 experts, and an
-    MXFP4 shared one, with H a multiple of 256 and F of 128; two launches with any multiples of 32.)
+    while two launches take x as it is and hold h in 16 bits. A caller that needs a request's
+    numbers not to change that way with the batch it is in passes few=False. (The separate calls
+    take MXFP4 experts, and an MXFP4 shared one, with H a multiple of 256 and F of 128; two
+    launches with any multiples of 32.)
 
     ``fp8_acts``: the routed experts' rows take the FP8 round trip first (NVFP4 only); the shared
     expert's do not. Returns (r', next); next is None without ``pre_w``."""
