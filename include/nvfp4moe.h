@@ -15,7 +15,9 @@
  * moe_grouped_gemm_mxfp4_swiglu_q: group-32 UE8M0 scales, W4A4 on the scaled FP4 matrix cores). For
  * decode sizes: nvfp4_matvec and mxfp4_matvec (up to 16 rows with one matrix),
  * moe_layer_few_nvfp4 and moe_layer_few_mxfp4 (the layer of up to 16 tokens in one call), and
- * moe_block_norm (the norms before and after a block with its gate and residual).
+ * moe_block_norm (the norms before and after a block with its gate and residual). For the block's
+ * attention half: rope_rotate (rotary positions), kv_cache_append (new keys and values into a paged
+ * cache, rotated on the way) and kv_cache_attention (attention of new tokens over that cache).
  *
  * Sources for what is computed (web pages; section names):
  *   [P1] "Native FP4 Is Slower Than Emulated FP4: A Kernel-Maturity Measurement on
@@ -618,6 +620,92 @@ nvfp4moe_status moe_block_norm(const void* resid, nvfp4moe_dtype r_dtype, int64_
                                nvfp4moe_dtype gate_dtype, int64_t gate_row, int32_t gate_col, float scale,
                                int32_t T, int32_t H, void* resid_out, int64_t ld_ro, void* next, int64_t ld_next,
                                void* stream);
+
+/* ---------------------------------------------------------------------------
+ * rope_rotate -- rotary positions: of every head the dims [start, start + rot) are turned in pairs
+ * (u, w), pair i by the angle a = positions[t] * freqs[i]:
+ *     u' = magnitude * (u cos a - w sin a)      w' = magnitude * (w cos a + u sin a)
+ * pairs being the dims (i, i + rot / 2) of that part or, interleaved, (2i, 2i + 1). The other dims
+ * are copied. With grad the rotation is transposed (by -a): x's gradient, of out's in x's place.
+ * Angles are taken in float64, their cosines and the products in float32, rounded once.
+ *   x, out       device [T, H, D] of dtype (F32 or BF16), element distances x_row and x_head (o_row,
+ *                o_head) between rows and heads, the dims of a head beside each other; the distance
+ *                of heads is at least D, that of rows at least (H - 1) * the heads' + D. out may be x
+ *                (same distances) and must not overlap it otherwise.
+ *   T, H, D      T >= 0 (0: nothing is done); H, D >= 1; T * H * D < 2^47, H * D < 2^24.
+ *   positions    device int32 (pos_bytes 4) or int64 (8) [T].
+ *   freqs        device float64 [rot / 2], radians a position.
+ *   rot, start   rot even, 2 <= rot <= 4096, start >= 0, start + rot <= D.
+ * ------------------------------------------------------------------------- */
+nvfp4moe_status rope_rotate(const void* x, nvfp4moe_dtype dtype, int64_t x_row, int64_t x_head, int32_t T, int32_t H,
+                            int32_t D, const void* positions, int32_t pos_bytes, const double* freqs, int32_t rot,
+                            int32_t start, int32_t interleaved, int32_t grad, float magnitude, void* out, int64_t o_row,
+                            int64_t o_head, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The paged cache of the two calls below. Keys and values of Hkv heads lie in `pages` pages of `page`
+ * tokens (a power of two from 16 to 1024):
+ *     k_cache [pages, Hkv, page, D]      v_cache [pages, Hkv, D, page]
+ * (values transposed: the attention reads both in its matrix operands' order), both BF16 or, with
+ * cache_fp8, E4M3FN with a positive float32 scale for each head, value = code * scale (NULL: 1).
+ * D is a multiple of 32 from 32 to 256. A batch is
+ *     page_table  int32 [B, cols], rows ld_table >= cols apart: entry (b, c) is the page of sequence
+ *                 b's tokens [c * page, (c + 1) * page)
+ *     lengths     int32 [B]: tokens of each sequence, its new ones among them
+ *     starts      int32 [B + 1], not decreasing: sequence b's new tokens are the rows
+ *                 [starts[b], starts[b + 1]) of the T rows of q, k, v and out; they are its last ones,
+ *                 so that row starts[b] + i has the position lengths[b] - (new tokens) + i.
+ * All three are device memory. Rows outside [starts[0], starts[B]) are not read, and left as they were in
+ * outputs. Entries that no visible token lies behind may hold anything.
+ *
+ * kv_cache_append -- the new tokens' keys, turned as in rope_rotate, and values into the cache, and
+ * their queries turned:
+ *   q, k, v, q_out   device bf16 [T, Hq, D], [T, Hkv, D] (k, v), with element distances of rows and
+ *                heads (views of one projection's rows). q and q_out may be NULL (both); q_out may be
+ *                q (same distances), and must not overlap anything else that is read or written.
+ *   positions    device int32 or int64 [T] for the angles, or NULL: the tokens' positions above.
+ *   freqs        NULL: nothing is turned (rot, start, interleaved, magnitude and positions are not
+ *                used). Otherwise as in rope_rotate.
+ *   cache_fp8    keys (in float32, turned) and values are divided by the head's scale and rounded to
+ *                E4M3 once, saturating at +-448; NaN stays NaN.
+ *   T, B         T >= 0 (0: nothing is done), B >= 1; T * Hq * D < 2^47, Hq * D < 2^24.
+ * Tokens whose position is negative or behind the page table's columns, or whose page is not in [0, pages),
+ * are not written to the cache. Two tokens of a batch must not share a place of it.
+ * ------------------------------------------------------------------------- */
+nvfp4moe_status kv_cache_append(const void* q, int64_t q_row, int64_t q_head, const void* k, int64_t k_row,
+                                int64_t k_head, const void* v, int64_t v_row, int64_t v_head, int32_t T, int32_t Hq,
+                                int32_t Hkv, int32_t D, const void* positions, int32_t pos_bytes, const double* freqs,
+                                int32_t rot, int32_t start, int32_t interleaved, float magnitude,
+                                const int32_t* page_table, int64_t ld_table, int32_t cols, const int32_t* lengths,
+                                const int32_t* starts, int32_t B, void* k_cache, void* v_cache, int32_t cache_fp8,
+                                int32_t pages, int32_t page, const float* k_scale, const float* v_scale, void* q_out,
+                                int64_t qo_row, int64_t qo_head, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * kv_cache_attention -- attention of the new tokens over the cache, which holds them already: the row
+ * of position p sees the keys j <= p and, with window > 0, j > p - window of its sequence:
+ *     out[t, h] = sum_j softmax_j(scale * q[t, h] . k[j, h / G]) * v[j, h / G]      G = Hq / Hkv
+ * From single tokens (the decode step) to whole prompts, of any lengths in one call.
+ *   q, out       device bf16 [T, Hq, D] with element distances of rows and heads, multiples of 8;
+ *                16-byte aligned. out must not overlap q or the cache.
+ *   scale        finite, > 0.      window   >= 0 (0: all keys).
+ *   T, B         T >= 0 (0: nothing is done), B >= 1; T * Hq + 16 * B * Hkv < 2^31.
+ *   ws           kv_cache_attention_workspace_size(T, B, Hq, Hkv, D) bytes, 16-byte aligned (0 for
+ *                sizes that the call refuses). Calls that may overlap need a workspace each.
+ * Scores, running maxima and sums are float32 and out is rounded once. Up to 16 rows (token, query
+ * head of a group) a sequence on average, the exponentials that weigh the values count as 16 bits;
+ * above, they are rounded to bf16. A row that sees no key (a position below 0) gives zeros. What a page holds behind a sequence's
+ * last token, and keys and values that a row does not see, do not reach it, NaN and Inf included; a visible
+ * value that is not finite makes its dim NaN or Inf in the rows that see it. A row that sees a key whose
+ * page is not in [0, pages), or whose position lies behind the page table's columns, gives NaN.
+ * ------------------------------------------------------------------------- */
+nvfp4moe_status kv_cache_attention(const void* q, int64_t q_row, int64_t q_head, int32_t T, int32_t Hq, int32_t Hkv,
+                                   int32_t D, const int32_t* page_table, int64_t ld_table, int32_t cols,
+                                   const int32_t* lengths, const int32_t* starts, int32_t B, const void* k_cache,
+                                   const void* v_cache, int32_t cache_fp8, int32_t pages, int32_t page,
+                                   const float* k_scale, const float* v_scale, float scale, int32_t window, void* out,
+                                   int64_t o_row, int64_t o_head, void* ws, size_t ws_bytes, void* stream);
+size_t kv_cache_attention_workspace_size(int32_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D);
 
 /* Thread-local message describing the last non-OK status ("" if none). Never NULL. */
 const char* nvfp4moe_last_error(void);

@@ -1216,3 +1216,202 @@ extern "C" nvfp4moe_status moe_block_norm(const void* resid, nvfp4moe_dtype r_dt
   a.ld_next = ld_next;
   return hip_status(launch_block_norm(a, static_cast<hipStream_t>(stream)), fn);
 }
+
+// ------------------------------------------------------------------ rotary positions, the paged cache
+namespace {
+
+constexpr int32_t kMaxRot = 4096;
+
+// A tensor [T, H, D] with distances of rows and heads, dims beside each other: what it spans, and why it
+// is refused (nullptr: it is not).
+struct Heads {
+  const void* p;
+  int64_t row, head, T, H, D, size;
+  const char* bad(int64_t step, uintptr_t align) const {
+    if (!p) return "null tensor pointer";
+    if (head < D || row < (H - 1) * head + D) return "distances of heads must be at least D, of rows at least their heads' span";
+    if (row >= (int64_t(1) << 40) || (row % step) != 0 || (head % step) != 0 || !aligned(p, align)) return "a tensor's distances or address do not fit";
+    return nullptr;
+  }
+  Rows rows() const { return Rows(p, row, T, (H - 1) * head + D, size); }
+  bool same(const Heads& o) const { return p == o.p && T == o.T && H == o.H && (T == 1 || row == o.row) && (H == 1 || head == o.head); }
+};
+
+// (the checks of a rotation; nullptr: fine)
+const char* rope_bad(const double* freqs, int32_t rot, int32_t start, int32_t D, int32_t interleaved, float magnitude) {
+  if (!aligned(freqs, 8)) return "freqs must be 8-byte aligned";
+  if (rot < 2 || rot % 2 != 0 || rot > kMaxRot || start < 0 || start > D - rot)
+    return "need an even rot, 2 <= rot <= 4096, and 0 <= start <= D - rot";
+  if (interleaved != 0 && interleaved != 1) return "interleaved must be 0 or 1";
+  if (!(magnitude - magnitude == 0.0f)) return "magnitude must be finite";
+  return nullptr;
+}
+
+// The checks that the cache's two calls share.
+const char* cache_bad(int32_t T, int32_t Hq, int32_t Hkv, int32_t D, const int32_t* page_table, int64_t ld_table, int32_t cols,
+                      const int32_t* lengths, const int32_t* starts, int32_t B, const void* k_cache, const void* v_cache,
+                      int32_t fp8, int32_t pages, int32_t page, const float* k_scale, const float* v_scale) {
+  if (T < 1 || B < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0) return "need T >= 0, B >= 1 and Hq a multiple of Hkv >= 1";
+  if (D < 32 || D % 32 != 0 || D > kCacheMaxD) return "D must be a multiple of 32 from 32 to 256";
+  if ((int64_t)Hq * D >= (int64_t(1) << 24)) return "need Hq * D < 2^24";
+  if (page < 16 || page > 1024 || (page & (page - 1)) != 0 || pages < 1) return "page must be a power of two from 16 to 1024, pages at least 1";
+  if (cols < 1 || ld_table < cols) return "need 1 <= cols <= ld_table";
+  if (!page_table || !lengths || !starts || !k_cache || !v_cache) return "null tensor pointer";
+  if (!aligned(page_table, 4) || !aligned(lengths, 4) || !aligned(starts, 4)) return "page_table, lengths and starts must be 4-byte aligned";
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return "the caches must be 16-byte aligned";
+  if (fp8 != 0 && fp8 != 1) return "cache_fp8 must be 0 or 1";
+  if (!fp8 && (k_scale || v_scale)) return "scales go with an FP8 cache";
+  if (!aligned(k_scale, 4) || !aligned(v_scale, 4)) return "scales must be 4-byte aligned";
+  return nullptr;
+}
+CacheBatchArgs batch_args(const int32_t* page_table, int64_t ld_table, int32_t cols, const int32_t* lengths, const int32_t* starts,
+                          int32_t B, int32_t T, int32_t pages, int32_t page) {
+  return {page_table, ld_table, cols, lengths, starts, B, T, pages, page, __builtin_ctz((unsigned)page)};
+}
+// One of the caches as rows of bytes.
+Rows cache_rows(const void* p, int32_t pages, int32_t Hkv, int32_t page, int32_t D, int32_t fp8) {
+  return Rows(p, 0, 1, (int64_t)pages * Hkv * page * D, fp8 ? 1 : 2);
+}
+
+}  // namespace
+
+extern "C" nvfp4moe_status rope_rotate(const void* x, nvfp4moe_dtype dtype, int64_t x_row, int64_t x_head, int32_t T, int32_t H,
+                                       int32_t D, const void* positions, int32_t pos_bytes, const double* freqs, int32_t rot,
+                                       int32_t start, int32_t interleaved, int32_t grad, float magnitude, void* out,
+                                       int64_t o_row, int64_t o_head, void* stream) {
+  const char* fn = "rope_rotate";
+  if (T == 0) return ok();
+  if (dtype != NVFP4MOE_F32 && dtype != NVFP4MOE_BF16) return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: dtype must be F32 or BF16", fn);
+  if (T < 0 || H < 1 || D < 1 || (int64_t)H * D >= (int64_t(1) << 24))
+    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: need T >= 0, H >= 1, D >= 1 and H * D < 2^24 (T=%d H=%d D=%d)", fn, T, H, D);
+  if (!positions || !freqs) return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: null tensor pointer", fn);
+  if ((pos_bytes != 4 && pos_bytes != 8) || !aligned(positions, (size_t)pos_bytes))
+    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: pos_bytes must be 4 or 8, and positions aligned to it", fn);
+  if (const char* why = rope_bad(freqs, rot, start, D, interleaved, magnitude)) return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: %s", fn, why);
+  if (grad != 0 && grad != 1) return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: grad must be 0 or 1", fn);
+  const int64_t size = size_of(dtype);
+  const Heads from{x, x_row, x_head, T, H, D, size}, to{out, o_row, o_head, T, H, D, size};
+  for (const Heads* t : {&from, &to})
+    if (const char* why = t->bad(1, (uintptr_t)size)) return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: %s", fn, why);
+  const bool in_place = from.same(to);
+  if (!in_place && from.rows().overlap(to.rows()))
+    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: out overlaps x (it may be x itself)", fn);
+  RopeArgs a{};
+  a.x = {x, x_row, x_head};
+  a.out = {out, o_row, o_head};
+  a.bf16 = dtype == NVFP4MOE_BF16;
+  a.T = T;
+  a.H = H;
+  a.D = D;
+  a.positions = positions;
+  a.pos64 = pos_bytes == 8;
+  a.turn = {freqs, rot, start, interleaved, magnitude, grad ? -1.0f : 1.0f};
+  a.copy = !in_place;
+  return hip_status(launch_rope(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+extern "C" nvfp4moe_status kv_cache_append(const void* q, int64_t q_row, int64_t q_head, const void* k, int64_t k_row,
+                                           int64_t k_head, const void* v, int64_t v_row, int64_t v_head, int32_t T, int32_t Hq,
+                                           int32_t Hkv, int32_t D, const void* positions, int32_t pos_bytes, const double* freqs,
+                                           int32_t rot, int32_t start, int32_t interleaved, float magnitude,
+                                           const int32_t* page_table, int64_t ld_table, int32_t cols, const int32_t* lengths,
+                                           const int32_t* starts, int32_t B, void* k_cache, void* v_cache, int32_t cache_fp8,
+                                           int32_t pages, int32_t page, const float* k_scale, const float* v_scale, void* q_out,
+                                           int64_t qo_row, int64_t qo_head, void* stream) {
+  const char* fn = "kv_cache_append";
+  if (T == 0) return ok();
+  if (const char* why = cache_bad(T, q ? Hq : Hkv, Hkv, D, page_table, ld_table, cols, lengths, starts, B, k_cache, v_cache, cache_fp8,
+                                  pages, page, k_scale, v_scale))
+    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: %s (T=%d Hq=%d Hkv=%d D=%d B=%d pages=%d page=%d)", fn, why, T, Hq, Hkv, D, B, pages, page);
+  if ((q == nullptr) != (q_out == nullptr)) return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: q and q_out come together", fn);
+  if (freqs) {
+    if (const char* why = rope_bad(freqs, rot, start, D, interleaved, magnitude)) return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: %s", fn, why);
+    if (positions && ((pos_bytes != 4 && pos_bytes != 8) || !aligned(positions, (size_t)pos_bytes)))
+      return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: pos_bytes must be 4 or 8, and positions aligned to it", fn);
+  }
+  const Heads ks{k, k_row, k_head, T, Hkv, D, 2}, vs{v, v_row, v_head, T, Hkv, D, 2};
+  const Heads qs{q, q_row, q_head, T, Hq, D, 2}, os{q_out, qo_row, qo_head, T, Hq, D, 2};
+  for (const Heads* t : {&ks, &vs, &qs, &os})
+    if (t->p || t == &ks || t == &vs)
+      if (const char* why = t->bad(1, 2)) return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: %s", fn, why);
+  const Rows kc = cache_rows(k_cache, pages, Hkv, page, D, cache_fp8), vc = cache_rows(v_cache, pages, Hkv, page, D, cache_fp8);
+  bool clash = kc.overlap(vc);
+  for (const Heads* t : {&ks, &vs, &qs, &os})
+    if (t->p) clash = clash || t->rows().overlap(kc) || t->rows().overlap(vc);
+  const bool in_place = q && qs.same(os);
+  if (q) clash = clash || os.rows().overlap(ks.rows()) || os.rows().overlap(vs.rows()) || (!in_place && os.rows().overlap(qs.rows()));
+  if (clash) return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: an output overlaps what is read or another one (q_out may be q itself)", fn);
+  KvAppendArgs a{};
+  a.q = {q, q_row, q_head};
+  a.q_out = {q_out, qo_row, qo_head};
+  a.k = {k, k_row, k_head};
+  a.v = {v, v_row, v_head};
+  a.Hq = q ? Hq : 0;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.batch = batch_args(page_table, ld_table, cols, lengths, starts, B, T, pages, page);
+  a.positions = freqs ? positions : nullptr;
+  a.pos64 = pos_bytes == 8;
+  a.turn = {freqs, freqs ? rot : 0, freqs ? start : 0, freqs ? interleaved : 0, magnitude, 1.0f};
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.fp8 = cache_fp8;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.copy = !in_place;
+  return hip_status(launch_kv_append(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+extern "C" size_t kv_cache_attention_workspace_size(int32_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D) {
+  if (T < 1 || B < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || D < 32 || D % 32 != 0 || D > kCacheMaxD || (int64_t)Hq * D >= (int64_t(1) << 24) ||
+      (int64_t)T * Hq + (int64_t)16 * B * Hkv >= (int64_t(1) << 31))
+    return 0;
+  return kv_attention_ws_bytes(T, B, Hq, Hkv, D);
+}
+
+extern "C" nvfp4moe_status kv_cache_attention(const void* q, int64_t q_row, int64_t q_head, int32_t T, int32_t Hq, int32_t Hkv,
+                                              int32_t D, const int32_t* page_table, int64_t ld_table, int32_t cols,
+                                              const int32_t* lengths, const int32_t* starts, int32_t B, const void* k_cache,
+                                              const void* v_cache, int32_t cache_fp8, int32_t pages, int32_t page,
+                                              const float* k_scale, const float* v_scale, float scale, int32_t window, void* out,
+                                              int64_t o_row, int64_t o_head, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "kv_cache_attention";
+  if (T == 0) return ok();
+  if (const char* why = cache_bad(T, Hq, Hkv, D, page_table, ld_table, cols, lengths, starts, B, k_cache, v_cache, cache_fp8, pages, page,
+                                  k_scale, v_scale))
+    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: %s (T=%d Hq=%d Hkv=%d D=%d B=%d pages=%d page=%d)", fn, why, T, Hq, Hkv, D, B, pages, page);
+  if ((int64_t)T * Hq + (int64_t)16 * B * Hkv >= (int64_t(1) << 31))
+    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: need T * Hq + 16 * B * Hkv < 2^31", fn);
+  if (!(scale > 0.0f) || !(scale - scale == 0.0f) || window < 0)
+    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: scale must be finite and positive, window at least 0", fn);
+  const Heads qs{q, q_row, q_head, T, Hq, D, 2}, os{out, o_row, o_head, T, Hq, D, 2};
+  for (const Heads* t : {&qs, &os})
+    if (const char* why = t->bad(8, 16)) return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: %s (multiples of 8, 16 bytes)", fn, why);
+  if (os.rows().overlap(qs.rows()) || os.rows().overlap(cache_rows(k_cache, pages, Hkv, page, D, cache_fp8)) ||
+      os.rows().overlap(cache_rows(v_cache, pages, Hkv, page, D, cache_fp8)))
+    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: out overlaps what is read", fn);
+  const size_t need = kv_attention_ws_bytes(T, B, Hq, Hkv, D);
+  if (!ws || ws_bytes < need || !aligned(ws, 16))
+    return fail(NVFP4MOE_ERR_WORKSPACE, "%s: need a 16-byte aligned workspace of %zu bytes, got %zu", fn, need, ws ? ws_bytes : (size_t)0);
+  KvAttnArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_row = q_row;
+  a.q_head = q_head;
+  a.out = static_cast<uint16_t*>(out);
+  a.o_row = o_row;
+  a.o_head = o_head;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.G = Hq / Hkv;
+  a.batch = batch_args(page_table, ld_table, cols, lengths, starts, B, T, pages, page);
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.fp8 = cache_fp8;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.scale = scale;
+  a.window = window;
+  a.ws = ws;
+  return hip_status(launch_kv_attention(a, static_cast<hipStream_t>(stream)), fn);
+}

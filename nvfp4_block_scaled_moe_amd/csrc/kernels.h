@@ -240,4 +240,79 @@ hipError_t launch_unpermute_reduce(const void* y, bool y_bf16, const int* slot_t
                                    const float* topk_w, int T, int k, int H, uint16_t* out,
                                    hipStream_t stream);
 
+// ---- rope_append.hip: rotary positions, and the paged cache's append
+// The turn of part of a head: pair i of dims [start, start + rot) by position * freqs[i] radians.
+struct RopeTurn {
+  const double* freqs;   // [rot / 2], or null: nothing is turned
+  int rot, start;
+  int interleaved;       // pairs (2i, 2i + 1), else (i, i + rot / 2)
+  float magnitude;       // factor of the turned dims
+  float sign;            // 1, or -1 for the transposed rotation
+};
+// Rows of a tensor [T, H, D] whose heads are contiguous: element distances of rows and heads.
+struct HeadRows {
+  const void* p;
+  int64_t row, head;
+};
+struct RopeArgs {
+  HeadRows x, out;
+  int bf16;                // type of both (else float32)
+  int T, H, D;
+  const void* positions;   // [T] int32 or int64
+  int pos64;
+  RopeTurn turn;
+  int copy;                // dims that are not turned are copied (out is not x)
+};
+hipError_t launch_rope(const RopeArgs& a, hipStream_t stream);
+
+// A batch of sequences whose keys and values lie in pages of `page` tokens.
+struct CacheBatchArgs {
+  const int* page_table;   // [B, cols], rows ld_table apart: page of a sequence's tokens [c * page, ...)
+  int64_t ld_table;
+  int cols;
+  const int* lengths;      // [B] tokens of each sequence, its new ones among them
+  const int* starts;       // [B + 1] row of each sequence's first new token
+  int B, T;                // sequences; rows of the tensors of new tokens
+  int pages, page, page_log;
+};
+struct KvAppendArgs {
+  HeadRows q, q_out, k, v;   // bf16; q.p null: no queries
+  int Hq, Hkv, D;
+  CacheBatchArgs batch;
+  const void* positions;     // [T] int32 or int64, or null: the tokens' places in their sequences
+  int pos64;
+  RopeTurn turn;
+  void* k_cache;             // [pages, Hkv, page, D]
+  void* v_cache;             // [pages, Hkv, D, page]
+  int fp8;                   // caches in E4M3, else bf16
+  const float* k_scale;      // [Hkv] or null (FP8)
+  const float* v_scale;
+  int copy;                  // as in RopeArgs, for q
+};
+hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t stream);
+
+// ---- kv_attention.hip, kv_attention_few.hip: attention of new tokens over the paged cache
+constexpr int kCacheMaxD = 256;
+struct KvAttnArgs {
+  const uint16_t* q;         // bf16 [T, Hq, D]
+  int64_t q_row, q_head;
+  uint16_t* out;             // bf16 [T, Hq, D]
+  int64_t o_row, o_head;
+  int Hq, Hkv, D, G;         // G = Hq / Hkv
+  CacheBatchArgs batch;
+  const void* k_cache;
+  const void* v_cache;
+  int fp8;
+  const float* k_scale;
+  const float* v_scale;
+  float scale;               // of the scores
+  int window;                // keys that a token sees, itself among them; 0: all
+  void* ws;
+};
+size_t kv_attention_ws_bytes(int T, int B, int Hq, int Hkv, int D);
+hipError_t launch_kv_attention(const KvAttnArgs& a, hipStream_t stream);
+// its form for tiles of 16 rows (kv_attention_few.hip)
+size_t kv_attention_few_ws_bytes(int Hkv, int D);
+hipError_t launch_kv_attention_few(const KvAttnArgs& a, hipStream_t stream);
+
 }  // namespace nvfp4moe

@@ -1,0 +1,566 @@
+// Attention of many new tokens over the paged cache (gfx950): prompts, chunks of prompts, and batches
+// that mix them with sequences that decode; and the choice between this and kv_attention_few.hip.
+//   out[t, h] = sum_j softmax_j(scale q[t, h] . k[j, h / G]) v[j, h / G]   over the keys j that t sees
+//
+// Bound by the matrix cores (4 D flops for each pair of row and key) and, beside them, by the
+// exponentials: 32 x 32 scores take 64 D / 8 matrix cycles for both products and about 500 vector
+// cycles, so that two waves a SIMD keep both busy. A tile is 128 rows (token, head of the group) of
+// one key head, 32 a wave; keys and values of 64 tokens at a time lie in LDS, twice, and are
+// requested one block ahead (bf16: straight into LDS; E4M3: through registers, where they become
+// bf16, which holds them exactly). Scores are transposed, S^T = K Q^T: a lane holds the scores of
+// one row, and with K's rows in LDS in the right order these are, after the exponential, the operand
+// of O^T = V^T P^T without another move. The rows of LDS are not padded; their 16-byte words are
+// permuted by the row, so that neither side has bank conflicts.
+//
+// Weights of the second product are exponentials rounded to bf16 (2^-9 of each, about as much again
+// as the rounding of the output; two bf16 values each would cost half the second product again).
+// Their sum is taken before that rounding. The running maximum is moved only when a score exceeds it
+// by 2^8: until then weights of up to 2^8 keep their relative precision.
+//
+// The rows' tiles and their blocks of keys are listed on the device by a first launch (lengths are
+// known there alone), tiles with many blocks in equal segments, which a last launch joins in a
+// fixed order.
+#include "kv_attention.h"
+
+namespace nvfp4moe {
+
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kRows = 32 * kWaves;    // rows of a tile
+constexpr int kBlockLog = 6, kBlock = 1 << kBlockLog;   // keys of a block
+constexpr int kTarget = 1024;         // segments that the work is divided into
+constexpr int kMinBlocks = 4;         // least blocks of a segment
+
+// What the first launch leaves in the workspace.
+struct Header {
+  int segments, splits;   // entries of the two lists
+  int pad[2];
+};
+struct PlanTile {       // one row tile of a sequence (heads aside)
+  int seq, tile, parts, slot;
+};
+struct PlanSegment {    // blocks [block0, block0 + blocks) of a tile
+  int tile, part, block0, blocks;
+};
+int64_t tiles_bound(int T, int B, int G) { return ((int64_t)T * G + kRows - 1) / kRows + (B < T ? B : T); }
+struct PlanLayout {
+  int64_t tiles, segments, splits;   // most of each
+  size_t at_tiles, at_segments, at_splits, at_first, at_sums, total;
+  PlanLayout(int T, int B, int Hkv, int G, int D) {
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    const int64_t whole = (kTarget + Hkv - 1) / Hkv;   // whole segments of the work, heads aside
+    tiles = tiles_bound(T, B, G);
+    segments = tiles + whole;
+    splits = tiles < whole ? tiles : whole;
+    at_tiles = up(sizeof(Header));
+    at_segments = at_tiles + up((size_t)tiles * sizeof(PlanTile));
+    at_splits = at_segments + up((size_t)segments * sizeof(PlanSegment));
+    at_first = at_splits + up((size_t)splits * 4);
+    at_sums = at_first + up((size_t)(B + 1) * 4);
+    // a tile in parts has more blocks than a whole segment: fewer than twice as many parts as whole segments
+    const int64_t slots = 2 * whole < segments ? 2 * whole : segments;
+    total = at_sums + (size_t)slots * Hkv * kRows * (D + 2) * sizeof(float);
+  }
+};
+struct Plan {
+  Header* head;
+  PlanTile* tiles;
+  PlanSegment* segments;
+  int* splits;      // tiles in parts
+  int* first;       // [B + 1] first tile of each sequence
+  float* sums;      // [slot, head] of [kRows, D] outputs, then [kRows, 2] maxima and sums
+  int max_tiles, max_segments, max_splits;
+};
+Plan plan_of(void* ws, const PlanLayout& l) {
+  char* p = static_cast<char*>(ws);
+  return {reinterpret_cast<Header*>(p),        reinterpret_cast<PlanTile*>(p + l.at_tiles), reinterpret_cast<PlanSegment*>(p + l.at_segments),
+          reinterpret_cast<int*>(p + l.at_splits), reinterpret_cast<int*>(p + l.at_first), reinterpret_cast<float*>(p + l.at_sums),
+          (int)l.tiles, (int)l.segments, (int)l.splits};
+}
+
+// ---------------------------------------------------------------- the list
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanWaves = kPlanThreads / kWave;
+
+// Exclusive sum over the workgroup (and its total).
+__device__ __forceinline__ int block_scan(int v, int& total, int* s_wave) {
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int upto = wave_scan(v, lane);
+  __syncthreads();   // (s_wave may still be read)
+  if (lane == kWave - 1) s_wave[wave] = upto;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanWaves; ++w) {
+    before += w < wave ? s_wave[w] : 0;
+    total += s_wave[w];
+  }
+  return before + upto - v;
+}
+
+// The blocks that the rows of a tile see.
+__device__ __forceinline__ void tile_blocks(const KvAttnArgs& p, const Sequence& q, int tile, int& block0, int& blocks) {
+  const int t0 = (int)((int64_t)tile * kRows / p.G), t1 = min((int)(((int64_t)tile * kRows + kRows - 1) / p.G), q.n - 1);
+  const Seen a = seen_by(q.position(t0), p.window, q.cap), z = seen_by(q.position(t1), p.window, q.cap);
+  block0 = a.lo >> kBlockLog;
+  blocks = max(((z.hi + kBlock - 1) >> kBlockLog) - block0, 0);
+}
+
+__global__ __launch_bounds__(kPlanThreads) void plan_kernel(const KvAttnArgs p, const Plan plan) {
+  __shared__ int s_wave[kPlanWaves];
+  __shared__ int64_t s_work[kPlanWaves];
+  const CacheBatchArgs& b = p.batch;
+  const int tid = threadIdx.x;
+  auto tiles_of = [&](const Sequence& q) { return (int)(((int64_t)q.n * p.G + kRows - 1) / kRows); };
+  int tiles = 0;
+  for (int s0 = 0; s0 < b.B; s0 += kPlanThreads) {
+    const int s = s0 + tid;
+    const int n = s < b.B ? tiles_of(sequence_of(b, p.window, s, kBlockLog)) : 0;
+    int total;
+    const int before = block_scan(n, total, s_wave);
+    if (s < b.B) plan.first[s] = tiles + before;
+    tiles += total;
+  }
+  if (tid == 0) plan.first[b.B] = tiles;
+  __threadfence_block();
+  __syncthreads();
+  tiles = min(tiles, plan.max_tiles);   // (starts that overlap would give more)
+  // The sequence of tile i, the later tiles of a sequence (which see the most) first, and their blocks.
+  auto tile_at = [&](int i, int& s, int& tile, int& block0, int& blocks) {
+    int lo = 0, hi = b.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (plan.first[mid] <= i)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    s = lo;
+    const Sequence q = sequence_of(b, p.window, s, kBlockLog);
+    tile = plan.first[s + 1] - 1 - i;
+    tile_blocks(p, q, tile, block0, blocks);
+  };
+  int64_t work = 0;
+  for (int i = tid; i < tiles; i += kPlanThreads) {
+    int s, tile, block0, blocks;
+    tile_at(i, s, tile, block0, blocks);
+    work += blocks;
+  }
+  work = wave_sum(work);
+  if (tid % kWave == 0) s_work[tid / kWave] = work;
+  __syncthreads();
+  work = 0;
+  for (int w = 0; w < kPlanWaves; ++w) work += s_work[w];
+  const int64_t even = (work * p.Hkv + kTarget - 1) / kTarget;
+  const int chunk = (int)(even > kMinBlocks ? even : kMinBlocks);
+  int segments = 0, slots = 0, splits = 0;
+  for (int i0 = 0; i0 < tiles; i0 += kPlanThreads) {
+    const int i = i0 + tid;
+    int s = 0, tile = 0, block0 = 0, blocks = 0, parts = 0;
+    if (i < tiles) {
+      tile_at(i, s, tile, block0, blocks);
+      parts = max((blocks + chunk - 1) / chunk, 1);
+    }
+    int n_segments, n_slots, n_splits;
+    const int first = segments + block_scan(parts, n_segments, s_wave);
+    const int slot = slots + block_scan(parts > 1 ? parts : 0, n_slots, s_wave);
+    const int split = splits + block_scan(parts > 1 ? 1 : 0, n_splits, s_wave);
+    if (i < tiles) {
+      plan.tiles[i] = {s, tile, parts, slot};
+      for (int j = 0; j < parts; ++j)
+        if (first + j < plan.max_segments)
+          plan.segments[first + j] = {i, j, block0 + j * chunk, min(chunk, blocks - j * chunk)};
+      if (parts > 1 && split < plan.max_splits) plan.splits[split] = i;
+    }
+    segments += n_segments;
+    slots += n_slots;
+    splits += n_splits;
+  }
+  if (tid == 0) {
+    plan.head->segments = min(segments, plan.max_segments);
+    plan.head->splits = min(splits, plan.max_splits);
+  }
+}
+
+// ---------------------------------------------------------------- the tiles
+// 16 bytes a lane from global memory straight into LDS (lane l at lds + 16 l).
+__device__ __forceinline__ void dma16(const char* from, char* lds) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                   (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+}
+
+// max (or sum) of a lane's value and that of the lane 32 away
+__device__ __forceinline__ float max_across(float v) {
+  const u32x2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+template <int D, bool FP8>
+struct Chunk {
+  static constexpr int kWords = D / 8;               // 16-byte words of a key in LDS
+  static constexpr int kBytes = kBlock * D * 2;      // of a block's keys, and of its values
+  static constexpr int kSteps = D / 16;              // of the first product
+  static constexpr int kDTiles = D / 32;             // of the second
+  // Word w of row r of K lies at w ^ swizzle(r): 8 rows' words of one column then lie in 8 different
+  // 16-byte columns of LDS (rows of 64 bytes short of 128 put every other one half a line on).
+  static __device__ __forceinline__ int swizzle(int r) { return kWords % 8 == 0 ? r % 8 : r / 2 % 4; }
+};
+
+// Key, of 16, of K's row r in LDS: row 8x + 4y + z holds key 8y + 4x + z, so that the scores of a lane
+// (rows 8 (i / 4) + 4 half + i % 4) are those of 8 consecutive keys.
+__device__ __forceinline__ int key_of_row(int r) { return r / 4 % 2 * 8 + r / 8 * 4 + r % 4; }
+
+template <int D, bool FP8>
+__global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(const KvAttnArgs p, const Plan plan) {
+  using C = Chunk<D, FP8>;
+  extern __shared__ __attribute__((aligned(16))) char smem[];   // two of: keys [64, D], values [D, 64]
+  const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int col = lane % 32, half = lane / 32;
+  const int h = blockIdx.x % p.Hkv, at = blockIdx.x / p.Hkv;
+  if (at >= plan.head->segments) return;
+  const PlanSegment sg = plan.segments[at];
+  const PlanTile tl = plan.tiles[sg.tile];
+  const CacheBatchArgs& b = p.batch;
+  const Sequence seq = sequence_of(b, p.window, tl.seq, kBlockLog);
+
+  // This lane's row, and the keys that it sees; and those that all of this wave's rows see.
+  const int rows = seq.n * p.G, row0 = tl.tile * kRows + 32 * wave;
+  const int row = min(row0 + col, rows - 1), token = row / p.G, head = h * p.G + row - token * p.G;
+  const Seen mine = seen_by(seq.position(token), p.window, seq.cap);
+  const int t0 = min(row0, rows - 1) / p.G, t1 = min(row0 + 31, rows - 1) / p.G;
+  const int all_lo = seen_by(seq.position(t1), p.window, seq.cap).lo, all_hi = seen_by(seq.position(t0), p.window, seq.cap).hi;
+
+  bf16x8 q[C::kSteps];
+  {
+    const uint16_t* from = p.q + (seq.row0 + token) * p.q_row + head * p.q_head + 8 * half;
+#pragma unroll
+    for (int i = 0; i < C::kSteps; ++i) q[i] = *reinterpret_cast<const bf16x8*>(from + 16 * i);
+  }
+  const float log2_scale = p.scale * kLog2e * (FP8 && p.k_scale ? p.k_scale[h] : 1.0f);
+
+  // Staging. Wave w brings the keys 16 w and on of a block (one page's: pages are whole multiples of
+  // 16), and D / 4 rows of V^T, of which a lane always takes the same 16 bytes (bf16: 8 keys; E4M3: 16).
+  constexpr int kSize = FP8 ? 1 : 2;
+  const int page = b.page, page_mask = page - 1;
+  const int64_t head_bytes = (int64_t)page * D * kSize;
+  const int* table = b.page_table + tl.seq * b.ld_table;
+  const int v_word = FP8 ? lane % 4 : (lane % 8) ^ (lane / 8);        // of the 4 or 8 words of a row of V^T
+  const int v_key = FP8 ? 16 * v_word : 8 * v_word, v_row = FP8 ? lane / 4 : lane / 8;
+  struct Pages {
+    int k, v;   // of this wave's keys; of this lane's values
+  };
+  auto pages_of = [&](int block) {
+    const int key = block << kBlockLog, kc = (key + 16 * wave) >> b.page_log, vc = (key + v_key) >> b.page_log;
+    Pages r = {-1, -1};
+    if (kc < b.cols) r.k = ld_const(table, kc);
+    if (vc < b.cols) r.v = table[vc];
+    return r;
+  };
+  constexpr int kKLoads = FP8 ? (D + 63) / 64 : D / 32, kVLoads = kKLoads;
+  u32x4v raw_k[FP8 ? kKLoads : 1], raw_v[FP8 ? kVLoads : 1];
+  // Requests block's keys and values (bf16: into LDS buffer `to`; E4M3: into registers); the pages that are not.
+  auto request = [&](int block, const Pages& pg, char* to) {
+    const int key = block << kBlockLog;
+    const bool k_ok = pg.k >= 0 && pg.k < b.pages, v_ok = pg.v >= 0 && pg.v < b.pages;
+    const char* k = static_cast<const char*>(p.k_cache) + ((int64_t)(k_ok ? pg.k : 0) * p.Hkv + h) * head_bytes +
+                    (int64_t)((key + 16 * wave) & page_mask) * (D * kSize);
+    const char* v = static_cast<const char*>(p.v_cache) + ((int64_t)(v_ok ? pg.v : 0) * p.Hkv + h) * head_bytes +
+                    (((key + v_key) & page_mask) + v_row * page) * kSize;
+    if constexpr (FP8) {
+      // words of 16 dims: a key has D / 16, 16 keys D
+#pragma unroll
+      for (int j = 0; j < kKLoads; ++j) {
+        const int i = 64 * j + lane;
+        raw_k[j] = (u32x4v){0u, 0u, 0u, 0u};
+        if (D % 64 == 0 || i < D) raw_k[j] = *reinterpret_cast<const u32x4v*>(k + i / (D / 16) * D + i % (D / 16) * 16);
+      }
+#pragma unroll
+      for (int j = 0; j < kVLoads; ++j) {
+        const int d = (wave * kVLoads + j) * 16;
+        raw_v[j] = (u32x4v){0u, 0u, 0u, 0u};
+        if (D % 64 == 0 || d + v_row < D) raw_v[j] = *reinterpret_cast<const u32x4v*>(v + (int64_t)d * page);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kKLoads; ++j) {
+        const int i = 64 * j + lane, r = i / C::kWords;
+        dma16(k + key_of_row(r) * (2 * D) + ((i % C::kWords) ^ C::swizzle(r)) * 16, to + wave * 32 * D + 1024 * j);
+      }
+#pragma unroll
+      for (int j = 0; j < kVLoads; ++j) {
+        const int d = (wave * kVLoads + j) * 8;
+        dma16(v + (int64_t)d * page * 2, to + C::kBytes + d * 128);
+      }
+    }
+    const uint64_t bad = __ballot(!v_ok);   // (lanes of the first row of V^T: of each 16 keys one)
+    return FP8 ? (uint32_t)(bad & 15u) : (uint32_t)((bad & 1u) | (bad >> 1 & 2u) | (bad >> 2 & 4u) | (bad >> 3 & 8u));
+  };
+  // E4M3: what request() brought, as bf16, into LDS.
+  auto place = [&](char* to) {
+    if constexpr (FP8) {
+      auto put = [&](char* at0, char* at1, const u32x4v& w) {
+        *reinterpret_cast<bf16x8*>(at0) = e4m3x8_to_bf16(w[0], w[1]);
+        *reinterpret_cast<bf16x8*>(at1) = e4m3x8_to_bf16(w[2], w[3]);
+      };
+#pragma unroll
+      for (int j = 0; j < kKLoads; ++j) {
+        const int i = 64 * j + lane, r = key_of_row(i / (D / 16)), w = i % (D / 16) * 2;   // (key_of_row is its own inverse)
+        char* line = to + (wave * 16 + r) * (2 * D);
+        if (D % 64 == 0 || i < D) put(line + (w ^ C::swizzle(r)) * 16, line + ((w + 1) ^ C::swizzle(r)) * 16, raw_k[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < kVLoads; ++j) {
+        const int d = (wave * kVLoads + j) * 16 + v_row;
+        char* line = to + C::kBytes + d * 128;
+        if (D % 64 == 0 || d < D) put(line + ((2 * v_word) ^ (d % 8)) * 16, line + ((2 * v_word + 1) ^ (d % 8)) * 16, raw_v[j]);
+      }
+    }
+  };
+
+  float m = -INFINITY, l = 0.0f;
+  f32x16 o[C::kDTiles];
+#pragma unroll
+  for (int d = 0; d < C::kDTiles; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
+
+  auto use = [&](int block, const char* from, uint32_t bad_pages) {
+    f32x16 s[2];
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[a][i] = 0.0f;
+      const char* line = from + (32 * a + col) * (2 * D);
+#pragma unroll
+      for (int i = 0; i < C::kSteps; ++i) {
+        const bf16x8 k = *reinterpret_cast<const bf16x8*>(line + ((2 * i + half) ^ C::swizzle(col)) * 16);
+        s[a] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[i], s[a], 0, 0, 0);
+      }
+    }
+    const int begin = block << kBlockLog;
+    const bool edge = begin < all_lo || begin + kBlock > all_hi || bad_pages != 0u;
+    // score i of tile a: key 32a + 16 (i / 8) + 8 half + i % 8 of the block
+    if (edge) {
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int key = begin + 32 * a + 16 * (i / 8) + 8 * half + i % 8;
+          const bool sees = key >= mine.lo && key < mine.hi;
+          s[a][i] = !sees ? -INFINITY : bad_pages >> (2 * a + i / 8) & 1u ? NAN : s[a][i];
+        }
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[a][i]);
+    top = max_across(top) * log2_scale;
+    if (__any(top > m + 8.0f)) {
+      // (this row's maximum moves by its own scores alone, so that no row's bits depend on another's)
+      const float next = top > m + 8.0f ? top : m, shrink = next == m ? 1.0f : __builtin_amdgcn_exp2f(m - next);
+      m = next;
+      l *= shrink;
+#pragma unroll
+      for (int d = 0; d < C::kDTiles; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] *= shrink;
+    }
+    const float base = m == -INFINITY ? 0.0f : m;
+    bf16x8 w[4];
+    float sum = 0.0f;
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[a][i], log2_scale, -base));
+        sum += e;
+        w[2 * a + i / 8][i % 8] = (__bf16)e;
+      }
+    l += sum;
+    const char* values = from + C::kBytes + col * 128;
+    if (!edge) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int d = 0; d < C::kDTiles; ++d) {
+          const bf16x8 v = *reinterpret_cast<const bf16x8*>(values + d * 4096 + ((2 * u + half) ^ (col % 8)) * 16);
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w[u], o[d], 0, 0, 0);
+        }
+    } else {
+      // values that some row does not see (or no row: what a page holds behind its last token)
+#pragma unroll 1
+      for (int u = 0; u < 4; ++u) {
+        bf16x8 sees, wu = u == 0 ? w[0] : u == 1 ? w[1] : u == 2 ? w[2] : w[3];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int key = begin + 16 * u + 8 * half + i;
+          sees[i] = key >= mine.lo && key < mine.hi ? (__bf16)1.0f : (__bf16)0.0f;
+        }
+#pragma unroll
+        for (int d = 0; d < C::kDTiles; ++d) {
+          u32x4v f = *reinterpret_cast<const u32x4v*>(values + d * 4096 + ((2 * u + half) ^ (col % 8)) * 16), bad;
+          uint32_t any = 0u;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t bits;
+            f[i] = finite_bf16x2(f[i], bits);
+            bad[i] = bits & 0x3f803f80u;   // 1.0 where one was taken out
+            any |= bits;
+          }
+          if (__any(any != 0u)) {
+            f32x16 n;   // how many of them each row sees
+#pragma unroll
+            for (int i = 0; i < 16; ++i) n[i] = 0.0f;
+            n = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, bad), sees, n, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[d][i] = n[i] > 0.0f ? NAN : o[d][i];
+          }
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, f), wu, o[d], 0, 0, 0);
+        }
+      }
+    }
+  };
+
+  if (sg.blocks > 0) {
+    const int end = sg.block0 + sg.blocks;
+    char* now = smem;
+    char* then = smem + 2 * C::kBytes;
+    uint32_t bad = request(sg.block0, pages_of(sg.block0), now);
+    Pages pg = pages_of(min(sg.block0 + 1, end - 1));
+    place(now);
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): the words are in LDS
+    __syncthreads();
+    for (int block = sg.block0; block < end; ++block) {
+      uint32_t next_bad = 0u;
+      if (block + 1 < end) {
+        next_bad = request(block + 1, pg, then);
+        pg = pages_of(min(block + 2, end - 1));
+      }
+      use(block, now, bad);
+      if (block + 1 < end) place(then);
+      __builtin_amdgcn_s_waitcnt(0x0F70);
+      __syncthreads();
+      char* t = now;
+      now = then;
+      then = t;
+      bad = next_bad;
+    }
+  }
+  {
+    const u32x2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
+    l = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  if (row0 + col >= rows) return;
+  // this lane: dims 32 d + 8 (i / 4) + 4 half + i % 4 of its row
+  if (tl.parts > 1) {
+    float* sums = plan.sums + ((int64_t)(tl.slot + sg.part) * p.Hkv + h) * kRows * (D + 2);
+    const int r = 32 * wave + col;
+#pragma unroll
+    for (int d = 0; d < C::kDTiles; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<float4*>(sums + r * D + 32 * d + 2 * i + 4 * half) = make_float4(o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]);
+    if (half == 0) {
+      sums[kRows * D + 2 * r] = m;
+      sums[kRows * D + 2 * r + 1] = l;
+    }
+  } else {
+    float f = l == 0.0f ? 0.0f : (FP8 && p.v_scale ? p.v_scale[h] : 1.0f) / l;
+    if (seq.position(token) >= seq.cap) f = NAN;
+    uint16_t* to = p.out + (seq.row0 + token) * p.o_row + head * p.o_head + 4 * half;
+#pragma unroll
+    for (int d = 0; d < C::kDTiles; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<uint2*>(to + 32 * d + 2 * i) =
+            make_uint2(bf16x2(o[d][i] * f, o[d][i + 1] * f), bf16x2(o[d][i + 2] * f, o[d][i + 3] * f));
+  }
+}
+
+// Joins the parts of tiles that have more than one: a workgroup a few rows of a tile and head.
+constexpr int kJoinThreads = 256, kJoinRows = 16;
+template <bool FP8>
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(const KvAttnArgs p, const Plan plan) {
+  constexpr int kGroups = kRows / kJoinRows;
+  const int at = blockIdx.x / (kGroups * p.Hkv), h = blockIdx.x / kGroups % p.Hkv, D = p.D;
+  if (at >= plan.head->splits) return;
+  const PlanTile tl = plan.tiles[plan.splits[at]];
+  const Sequence seq = sequence_of(p.batch, p.window, tl.seq, kBlockLog);
+  const float v_scale = FP8 && p.v_scale ? p.v_scale[h] : 1.0f;
+  for (int i = threadIdx.x; i < kJoinRows * (D / 4); i += kJoinThreads) {
+    const int r = blockIdx.x % kGroups * kJoinRows + i / (D / 4), d = i % (D / 4) * 4, row = tl.tile * kRows + r;
+    if (row >= seq.n * p.G) continue;
+    float m = -INFINITY, l = 0.0f;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int j = 0; j < tl.parts; ++j) {
+      const float* sums = plan.sums + ((int64_t)(tl.slot + j) * p.Hkv + h) * kRows * (D + 2);
+      const float2 ml = *reinterpret_cast<const float2*>(sums + kRows * D + 2 * r);
+      const float4 x = *reinterpret_cast<const float4*>(sums + r * D + d);
+      const float next = fmaxf(m, ml.x), base = next == -INFINITY ? 0.0f : next;
+      const float f = __builtin_amdgcn_exp2f(m - base), g = ml.x == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(ml.x - base);
+      m = next;
+      l = l * f + ml.y * g;
+      v.x = v.x * f + x.x * g, v.y = v.y * f + x.y * g, v.z = v.z * f + x.z * g, v.w = v.w * f + x.w * g;
+    }
+    const int token = row / p.G;
+    float f = l == 0.0f ? 0.0f : v_scale / l;
+    if (seq.position(token) >= seq.cap) f = NAN;
+    uint16_t* to = p.out + (seq.row0 + token) * p.o_row + (h * p.G + row - token * p.G) * p.o_head + d;
+    *reinterpret_cast<uint2*>(to) = make_uint2(bf16x2(v.x * f, v.y * f), bf16x2(v.z * f, v.w * f));
+  }
+}
+
+template <int D, bool FP8>
+hipError_t launch(const KvAttnArgs& a, hipStream_t stream) {
+  const PlanLayout l(a.batch.T, a.batch.B, a.Hkv, a.G, D);
+  const Plan plan = plan_of(a.ws, l);
+  constexpr int lds = 4 * Chunk<D, FP8>::kBytes;
+  static std::atomic<uint64_t> done{0};
+  if (lds > 65536) {
+    const hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(chunk_kernel<D, FP8>), lds, done);
+    if (e != hipSuccess) return e;
+  }
+  plan_kernel<<<dim3(1), kPlanThreads, 0, stream>>>(a, plan);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  chunk_kernel<D, FP8><<<dim3((unsigned)(l.segments * a.Hkv)), kWaves * kWave, lds, stream>>>(a, plan);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  join_kernel<FP8><<<dim3((unsigned)(l.splits * a.Hkv * (kRows / kJoinRows))), kJoinThreads, 0, stream>>>(a, plan);
+  return hipGetLastError();
+}
+
+template <bool FP8>
+hipError_t launch_d(const KvAttnArgs& a, hipStream_t stream) {
+  switch (a.D / 32) {
+    case 1: return launch<32, FP8>(a, stream);
+    case 2: return launch<64, FP8>(a, stream);
+    case 3: return launch<96, FP8>(a, stream);
+    case 4: return launch<128, FP8>(a, stream);
+    case 5: return launch<160, FP8>(a, stream);
+    case 6: return launch<192, FP8>(a, stream);
+    case 7: return launch<224, FP8>(a, stream);
+    case 8: return launch<256, FP8>(a, stream);
+  }
+  return hipErrorInvalidValue;
+}
+
+// Rows of a sequence, on average, up to which its tiles of 16 rows are few.
+bool few(int T, int B, int G) { return (int64_t)T * G <= (int64_t)16 * B; }
+
+}  // namespace
+
+size_t kv_attention_ws_bytes(int T, int B, int Hq, int Hkv, int D) {
+  if (few(T, B, Hq / Hkv)) return kv_attention_few_ws_bytes(Hkv, D);
+  return PlanLayout(T, B, Hkv, Hq / Hkv, D).total;
+}
+
+hipError_t launch_kv_attention(const KvAttnArgs& a, hipStream_t stream) {
+  if (few(a.batch.T, a.batch.B, a.G)) return launch_kv_attention_few(a, stream);
+  return a.fp8 ? launch_d<true>(a, stream) : launch_d<false>(a, stream);
+}
+
+}  // namespace nvfp4moe

@@ -1,0 +1,471 @@
+// Attention of a few new tokens of each sequence over the paged cache (gfx950): the decode step.
+//   out[t, h] = sum_j softmax_j(scale q[t, h] . k[j, h / G]) v[j, h / G]   over the keys j that t sees
+//
+// Bound by the cache's bytes: each visible key and value is read once for the G query heads that
+// share it (and for up to 16 / G new tokens): a tile is 16 rows (token, head of the group), the
+// width of a matrix instruction. Scores are taken transposed, S^T = K Q^T, so that a lane holds the
+// scores of one row; the keys of a block are dealt to the rows of K's operand such that these
+// scores are, after the exponential, the operand of the second product O^T = V^T P^T as they lie:
+// neither goes through LDS. K and V^T are loaded from the cache straight into operand registers,
+// 16 bytes a lane (this is why the cache holds values transposed), a block ahead of its use.
+//
+// Weights of the second product are two bf16 values each (the rounded exponential, and the rest), so
+// that they count as 16 bits; the matrix cores have the time. Running maxima and sums are float32.
+//
+// The work (blocks of keys over all sequences, tiles and heads) is divided into equal segments on the
+// device, from the lengths, which the host does not know; a workgroup of four waves takes one
+// segment, its waves every fourth block. Where a tile has more than one segment, they leave
+// unnormalised sums, which a second launch joins in a fixed order.
+#include "kv_attention.h"
+
+namespace nvfp4moe {
+
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kRows = 16;          // rows of a tile
+constexpr int kTarget = 1024;      // segments that the work is divided into
+constexpr int kMinBlocks = 4;      // least blocks of a segment (one a wave)
+
+// The segment of workgroup `at` (over the tiles' segments, heads aside), found by every wave by itself.
+struct Segment {
+  Sequence seq;
+  int tile;               // row tile of the sequence
+  int block0, blocks;     // its keys
+  int parts, part;        // segments of its tile, which of them
+  int slot;               // place of its sums, where parts > 1
+  bool found;
+};
+__device__ __forceinline__ Segment segment_of(const KvAttnArgs& p, int block_log, int at, bool by_tile) {
+  // Work of all sequences, then the segments before each one: a lane a sequence.
+  const CacheBatchArgs& b = p.batch;
+  const int lane = threadIdx.x % kWave;
+  Sequence mine{};
+  int64_t work = 0;
+  for (int s0 = 0; s0 < b.B; s0 += kWave) {
+    const int s = s0 + lane;
+    if (s < b.B) {
+      mine = sequence_of(b, p.window, s, block_log);
+      work += (int64_t)((mine.n * p.G + kRows - 1) / kRows) * mine.blocks;
+    }
+  }
+  work = wave_sum(work) * p.Hkv;
+  const int64_t even = (work + kTarget - 1) / kTarget;
+  const int chunk = (int)(even > kMinBlocks ? (even + kWaves - 1) / kWaves * kWaves : kMinBlocks);
+  Segment r{};
+  int before = 0, slots = 0;
+  for (int s0 = 0; s0 < b.B; s0 += kWave) {
+    const int s = s0 + lane;
+    if (b.B > kWave) mine = s < b.B ? sequence_of(b, p.window, s, block_log) : Sequence{};
+    const int tiles = s < b.B ? (mine.n * p.G + kRows - 1) / kRows : 0;
+    const int parts = max((mine.blocks + chunk - 1) / chunk, 1), count = by_tile ? tiles : tiles * parts;
+    const int split = parts > 1 ? tiles * parts : 0;
+    const int upto = wave_scan(count, lane), split_upto = wave_scan(split, lane);
+    const uint64_t hit = __ballot(before + upto > at);
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      auto get = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+      r.seq = {get(mine.row0), get(mine.n), get(mine.len), get(mine.cap), get(mine.block0), get(mine.blocks)};
+      r.parts = get(parts);
+      const int in = at - before - (get(upto) - get(count));
+      r.tile = by_tile ? in : in / r.parts;
+      r.part = by_tile ? 0 : in - r.tile * r.parts;
+      r.slot = slots + get(split_upto) - get(split) + r.tile * r.parts + r.part;
+      r.block0 = r.seq.block0 + r.part * chunk;
+      r.blocks = min(chunk, r.seq.blocks - r.part * chunk);
+      r.found = true;
+      // (which sequence: its page table's row)
+      r.seq.block0 = s0 + l;
+      return r;
+    }
+    before += __builtin_amdgcn_readlane(upto, kWave - 1);
+    slots += __builtin_amdgcn_readlane(split_upto, kWave - 1);
+  }
+  return r;
+}
+
+// Sums of a segment in the workspace: [slot, head] of [kRows, D] unnormalised outputs, then of
+// [kRows] maxima (of base 2 logits) and sums.
+struct Parts {
+  float* o;
+  float* ml;
+  __device__ __forceinline__ Parts(const KvAttnArgs& p, int64_t slot, int h) {
+    const int64_t i = slot * p.Hkv + h;
+    o = static_cast<float*>(p.ws) + i * kRows * (p.D + 2);
+    ml = o + kRows * p.D;
+  }
+};
+
+template <int D, bool FP8>
+struct Few {
+  static constexpr int kBlockLog = FP8 ? 6 : 5, kBlock = 1 << kBlockLog;   // keys of a block
+  static constexpr int kTiles = kBlock / 16;       // tiles of 16 keys in the first product
+  static constexpr int kDSteps = D / 32;           // its steps
+  static constexpr int kPSteps = kBlock / 32;      // steps of the second product
+  static constexpr int kDTiles = D / 16;           // its tiles
+  // 16-byte words a lane loads of a tile of keys: 32 dims (bf16) or 64 (E4M3, the last one half where
+  // 64 does not divide D).
+  static constexpr int kKWords = FP8 ? (D + 63) / 64 : D / 32;
+};
+
+template <int D, bool FP8>
+__global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void few_kernel(const KvAttnArgs p) {
+  using F = Few<D, FP8>;
+  extern __shared__ float lds[];   // [kWaves, kRows, D + 1] outputs, then [kWaves, kRows, 2] maxima and sums
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, c = lane & 15, g = lane >> 4;
+  const int h = blockIdx.x % p.Hkv;
+  const Segment sg = segment_of(p, F::kBlockLog, blockIdx.x / p.Hkv, false);
+  if (!sg.found) return;
+  const int s = sg.seq.block0;
+  const CacheBatchArgs& b = p.batch;
+
+  // This lane's row: new token, query head, and the keys that it sees. (Rows behind the last one see
+  // what that one sees, and are not written.)
+  const int rows = sg.seq.n * p.G;
+  const int row = min(sg.tile * kRows + c, rows - 1), token = row / p.G, head = h * p.G + row - token * p.G;
+  const Seen mine = seen_by(sg.seq.position(token), p.window, sg.seq.cap);
+  const int first_token = sg.tile * kRows / p.G, last_token = min((sg.tile * kRows + kRows - 1) / p.G, sg.seq.n - 1);
+  // Keys that every row sees: blocks within need no mask.
+  const int all_lo = seen_by(sg.seq.position(last_token), p.window, sg.seq.cap).lo;
+  const int all_hi = seen_by(sg.seq.position(first_token), p.window, sg.seq.cap).hi;
+
+  bf16x8 q[F::kDSteps];
+  {
+    const uint16_t* at = p.q + (sg.seq.row0 + token) * p.q_row + head * p.q_head;
+#pragma unroll
+    for (int i = 0; i < F::kDSteps; ++i) {
+      // (the order of dims that K's words give)
+      const int d = FP8 && i < D / 64 * 2 ? 64 * (i / 2) + 16 * g + 8 * (i % 2) : 32 * i + 8 * g;
+      q[i] = *reinterpret_cast<const bf16x8*>(at + d);
+    }
+  }
+  const float log2_scale = p.scale * kLog2e * (FP8 && p.k_scale ? p.k_scale[h] : 1.0f);
+
+  // This lane's places in a block: for K the key of row c of each tile (rows 4a + i of tile t are key
+  // 8a + 4t + i, E4M3 16a + 4t + i), for V and the scores the keys 8g (16g) and on.
+  const int page = b.page, page_mask = page - 1;
+  const int k_key = (F::kBlock / 4) * (c / 4) + c % 4, v_key = (F::kBlock / 4) * g;
+  const int* table = b.page_table + s * b.ld_table;
+  const int64_t head_size = (int64_t)page * D;
+  struct Pages {
+    int k, v;
+  };
+  auto pages_of = [&](int block) {
+    // (columns are checked against the table: a block may end behind it)
+    const int kc = ((block << F::kBlockLog) + k_key) >> b.page_log, vc = ((block << F::kBlockLog) + v_key) >> b.page_log;
+    Pages r = {-1, -1};
+    if (kc < b.cols) r.k = table[kc];
+    if (vc < b.cols) r.v = table[vc];
+    return r;
+  };
+  struct Words {
+    u32x4v k[F::kTiles][F::kKWords], v[F::kDTiles];
+    bool bad;   // this lane's keys have no page
+  };
+  auto load = [&](int block, const Pages& pg, Words& w) {
+    const bool k_ok = pg.k >= 0 && pg.k < b.pages, v_ok = pg.v >= 0 && pg.v < b.pages;
+    w.bad = !v_ok;
+    const int key = block << F::kBlockLog;
+    const int64_t ks = ((int64_t)(k_ok ? pg.k : 0) * p.Hkv + h) * head_size + (int64_t)((key + k_key) & page_mask) * D;
+    const int64_t vs = ((int64_t)(v_ok ? pg.v : 0) * p.Hkv + h) * head_size + ((key + v_key) & page_mask) + (int64_t)c * page;
+    if constexpr (FP8) {
+      const uint8_t* ka = static_cast<const uint8_t*>(p.k_cache) + ks + 16 * g;
+      const uint8_t* va = static_cast<const uint8_t*>(p.v_cache) + vs;
+#pragma unroll
+      for (int t = 0; t < F::kTiles; ++t)
+#pragma unroll
+        for (int i = 0; i < F::kKWords; ++i) {
+          if (64 * i + 64 <= D) {
+            w.k[t][i] = *reinterpret_cast<const u32x4v*>(ka + 4 * t * D + 64 * i);
+          } else {
+            const u32x2 x = *reinterpret_cast<const u32x2*>(ka - 8 * g + 4 * t * D + 64 * i);
+            w.k[t][i] = (u32x4v){x[0], x[1], 0u, 0u};
+          }
+        }
+#pragma unroll
+      for (int d = 0; d < F::kDTiles; ++d) w.v[d] = *reinterpret_cast<const u32x4v*>(va + 16 * d * page);
+    } else {
+      const uint16_t* ka = static_cast<const uint16_t*>(p.k_cache) + ks + 8 * g;
+      const uint16_t* va = static_cast<const uint16_t*>(p.v_cache) + vs;
+#pragma unroll
+      for (int t = 0; t < F::kTiles; ++t)
+#pragma unroll
+        for (int i = 0; i < F::kKWords; ++i) w.k[t][i] = *reinterpret_cast<const u32x4v*>(ka + 4 * t * D + 32 * i);
+#pragma unroll
+      for (int d = 0; d < F::kDTiles; ++d) w.v[d] = *reinterpret_cast<const u32x4v*>(va + 16 * d * page);
+    }
+  };
+
+  float m = -INFINITY, l = 0.0f;
+  f32x4 o[F::kDTiles];
+#pragma unroll
+  for (int d = 0; d < F::kDTiles; ++d) o[d] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+
+  auto use = [&](int block, const Words& w) {
+    const int key0 = (block << F::kBlockLog) + v_key;   // the key of this lane's first score
+    f32x4 sc[F::kTiles];
+#pragma unroll
+    for (int t = 0; t < F::kTiles; ++t) {
+      sc[t] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < F::kDSteps; ++i) {
+        bf16x8 a;
+        if constexpr (FP8) {
+          const u32x4v x = w.k[t][i / 2];
+          a = i % 2 ? e4m3x8_to_bf16(x[2], x[3]) : e4m3x8_to_bf16(x[0], x[1]);
+        } else {
+          a = __builtin_bit_cast(bf16x8, w.k[t][i]);
+        }
+        sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, q[i], sc[t], 0, 0, 0);
+      }
+    }
+    const int begin = block << F::kBlockLog;
+    const bool edge = begin < all_lo || begin + F::kBlock > all_hi || __any(w.bad);
+    float x[F::kTiles][4], top = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < F::kTiles; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[t][i] = sc[t][i] * log2_scale;
+        if (edge) {
+          const int key = key0 + 4 * t + i;
+          const bool sees = key >= mine.lo && key < mine.hi;
+          x[t][i] = !sees ? -INFINITY : w.bad ? NAN : x[t][i];
+        }
+        top = fmaxf(top, x[t][i]);
+      }
+    top = fmaxf(top, __shfl_xor(top, 16, kWave));
+    top = fmaxf(top, __shfl_xor(top, 32, kWave));
+    // (fmaxf leaves NaN out: a row with one gets it from its exponential)
+    const float next = fmaxf(m, top), base = next == -INFINITY ? 0.0f : next;
+    const float shrink = __builtin_amdgcn_exp2f(m - base);
+    m = next;
+    float sum = 0.0f;
+    bf16x8 hi[F::kPSteps], lo[F::kPSteps];
+#pragma unroll
+    for (int t = 0; t < F::kTiles; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float e = __builtin_amdgcn_exp2f(x[t][i] - base);
+        sum += e;
+        const __bf16 r = (__bf16)e;
+        hi[t / 2][4 * (t % 2) + i] = r;
+        lo[t / 2][4 * (t % 2) + i] = (__bf16)(e - (float)r);
+      }
+    l = l * shrink + sum;
+#pragma unroll
+    for (int d = 0; d < F::kDTiles; ++d) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[d][i] *= shrink;
+#pragma unroll
+      for (int u = 0; u < F::kPSteps; ++u) {
+        bf16x8 v;
+        if constexpr (FP8)
+          v = u ? e4m3x8_to_bf16(w.v[d][2], w.v[d][3]) : e4m3x8_to_bf16(w.v[d][0], w.v[d][1]);
+        else
+          v = __builtin_bit_cast(bf16x8, w.v[d]);
+        if (edge) {   // values that some row does not see (or no row: what a page holds behind its last token)
+          u32x4v f = __builtin_bit_cast(u32x4v, v), bad;
+          uint32_t any = 0u;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t bits;
+            f[i] = finite_bf16x2(f[i], bits);
+            bad[i] = bits & 0x3f803f80u;   // 1.0 where one was taken out
+            any |= bits;
+          }
+          v = __builtin_bit_cast(bf16x8, f);
+          if (__any(any != 0u)) {
+            // how many of them each row sees
+            bf16x8 sees;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int key = key0 + 8 * u + i;
+              sees[i] = key >= mine.lo && key < mine.hi ? (__bf16)1.0f : (__bf16)0.0f;
+            }
+            const f32x4 n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, bad), sees,
+                                                                    (f32x4){0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[d][i] = n[i] > 0.0f ? NAN : o[d][i];
+          }
+        }
+        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, hi[u], o[d], 0, 0, 0);
+        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, lo[u], o[d], 0, 0, 0);
+      }
+    }
+  };
+
+  // This wave's blocks: every kWaves-th. Pages are looked up two of them ahead, words loaded one.
+  {
+    const int end = sg.block0 + sg.blocks;
+    int block = sg.block0 + wave;
+    if (block < end) {
+      Words a, z;
+      load(block, pages_of(block), a);
+      Pages pg = pages_of(min(block + kWaves, end - 1));
+      while (true) {
+        if (block + kWaves < end) {
+          load(block + kWaves, pg, z);
+          pg = pages_of(min(block + 2 * kWaves, end - 1));
+        }
+        use(block, a);
+        block += kWaves;
+        if (block >= end) break;
+        if (block + kWaves < end) {
+          load(block + kWaves, pg, a);
+          pg = pages_of(min(block + 2 * kWaves, end - 1));
+        }
+        use(block, z);
+        block += kWaves;
+        if (block >= end) break;
+      }
+    }
+  }
+  l += __shfl_xor(l, 16, kWave);
+  l += __shfl_xor(l, 32, kWave);
+
+  // Join the waves' sums (this lane: row c, dims 16d + 4g and on).
+  constexpr int kPitch = D + 4;
+  float* s_ml = lds + kWaves * kRows * kPitch;
+  float* s_o = lds + (wave * kRows + c) * kPitch;
+#pragma unroll
+  for (int d = 0; d < F::kDTiles; ++d) *reinterpret_cast<f32x4*>(s_o + 16 * d + 4 * g) = o[d];
+  if (g == 0) {
+    s_ml[(wave * kRows + c) * 2] = m;
+    s_ml[(wave * kRows + c) * 2 + 1] = l;
+  }
+  __syncthreads();
+  const float v_scale = FP8 && p.v_scale ? p.v_scale[h] : 1.0f;
+  const int in_tile = min(rows - sg.tile * kRows, kRows);
+  for (int i = threadIdx.x; i < in_tile * (D / 8); i += kWaves * kWave) {
+    const int r = i / (D / 8), d = (i - r * (D / 8)) * 8;
+    float top = -INFINITY, factor[kWaves], total = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, s_ml[(w * kRows + r) * 2]);
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      factor[w] = top == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(s_ml[(w * kRows + r) * 2] - top);
+      total += s_ml[(w * kRows + r) * 2 + 1] * factor[w];
+    }
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) v[j] += lds[(w * kRows + r) * kPitch + d + j] * factor[w];
+    }
+    if (sg.parts > 1) {
+      const Parts part(p, sg.slot, h);
+      *reinterpret_cast<float4*>(part.o + r * D + d) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(part.o + r * D + d + 4) = make_float4(v[4], v[5], v[6], v[7]);
+      if (d == 0) {
+        part.ml[2 * r] = top;
+        part.ml[2 * r + 1] = total;
+      }
+    } else {
+      const int at = sg.tile * kRows + r, t = at / p.G;
+      // no key seen: zeros; a position that the page table has no column for: NaN
+      float f = total == 0.0f ? 0.0f : v_scale / total;
+      if (sg.seq.position(t) >= sg.seq.cap) f = NAN;
+      uint16_t* to = p.out + (sg.seq.row0 + t) * p.o_row + (h * p.G + at - t * p.G) * p.o_head + d;
+      *reinterpret_cast<uint4*>(to) = make_uint4(bf16x2(v[0] * f, v[1] * f), bf16x2(v[2] * f, v[3] * f),
+                                                 bf16x2(v[4] * f, v[5] * f), bf16x2(v[6] * f, v[7] * f));
+    }
+  }
+}
+
+// Joins the segments of a tile: a workgroup a row of a tile and head; its threads hold 4 dims of
+// every kGroups-th segment.
+constexpr int kJoinThreads = 256;
+template <bool FP8>
+__global__ __launch_bounds__(kJoinThreads) void few_join_kernel(const KvAttnArgs p, int block_log) {
+  __shared__ float4 s_o[kJoinThreads];
+  __shared__ float s_f[2 * kTarget];   // factors of the segments
+  const int r = blockIdx.x % kRows, h = blockIdx.x / kRows % p.Hkv;
+  const Segment sg = segment_of(p, block_log, blockIdx.x / kRows / p.Hkv, true);
+  const int rows = sg.seq.n * p.G, at = sg.tile * kRows + r;
+  if (!sg.found || sg.parts < 2 || at >= rows) return;
+  const int lanes = p.D / 4, groups = kJoinThreads / lanes, group = threadIdx.x / lanes, d = threadIdx.x % lanes * 4;
+  // every wave: the row's maximum and sum over the segments
+  const int lane = threadIdx.x % kWave;
+  float top = -INFINITY, total = 0.0f;
+  for (int i = lane; i < sg.parts; i += kWave) top = fmaxf(top, Parts(p, sg.slot + i, h).ml[2 * r]);
+  top = wave_max(top);
+  for (int i = lane; i < sg.parts; i += kWave) {
+    const Parts part(p, sg.slot + i, h);
+    const float f = top == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(part.ml[2 * r] - top);
+    total += part.ml[2 * r + 1] * f;
+    s_f[i] = f;   // (the same from every wave)
+  }
+  total = wave_sum(total);
+  __syncthreads();
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (group < groups)
+    for (int i = group; i < sg.parts; i += groups) {
+      const float4 x = *reinterpret_cast<const float4*>(Parts(p, sg.slot + i, h).o + r * p.D + d);
+      const float f = s_f[i];
+      v.x += x.x * f, v.y += x.y * f, v.z += x.z * f, v.w += x.w * f;
+    }
+  s_o[threadIdx.x] = v;
+  __syncthreads();
+  if (threadIdx.x >= lanes) return;
+  for (int i = 1; i < groups; ++i) {
+    const float4 x = s_o[i * lanes + threadIdx.x];
+    v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+  }
+  const int t = at / p.G;
+  float f = total == 0.0f ? 0.0f : (FP8 && p.v_scale ? p.v_scale[h] : 1.0f) / total;
+  if (sg.seq.position(t) >= sg.seq.cap) f = NAN;
+  uint16_t* to = p.out + (sg.seq.row0 + t) * p.o_row + (h * p.G + at - t * p.G) * p.o_head + d;
+  *reinterpret_cast<uint2*>(to) = make_uint2(bf16x2(v.x * f, v.y * f), bf16x2(v.z * f, v.w * f));
+}
+
+int64_t tiles_bound(int T, int B, int G) { return ((int64_t)T * G + kRows - 1) / kRows + (B < T ? B : T); }
+
+template <int D, bool FP8>
+hipError_t launch(const KvAttnArgs& a, hipStream_t stream) {
+  using F = Few<D, FP8>;
+  const int64_t tiles = tiles_bound(a.batch.T, a.batch.B, a.G);
+  // each tile one segment, and as many more as the work has whole segments
+  const int64_t groups = (tiles + (kTarget + a.Hkv - 1) / a.Hkv) * a.Hkv;
+  const size_t lds = (size_t)kWaves * kRows * (D + 4 + 2) * sizeof(float);
+  static std::atomic<uint64_t> done{0};
+  if (lds > 65536) {
+    const hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(few_kernel<D, FP8>), (int)lds, done);
+    if (e != hipSuccess) return e;
+  }
+  few_kernel<D, FP8><<<dim3((unsigned)groups), kWaves * kWave, lds, stream>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  few_join_kernel<FP8><<<dim3((unsigned)(tiles * a.Hkv * kRows)), kJoinThreads, 0, stream>>>(a, F::kBlockLog);
+  return hipGetLastError();
+}
+
+template <bool FP8>
+hipError_t launch_d(const KvAttnArgs& a, hipStream_t stream) {
+  switch (a.D / 32) {
+    case 1: return launch<32, FP8>(a, stream);
+    case 2: return launch<64, FP8>(a, stream);
+    case 3: return launch<96, FP8>(a, stream);
+    case 4: return launch<128, FP8>(a, stream);
+    case 5: return launch<160, FP8>(a, stream);
+    case 6: return launch<192, FP8>(a, stream);
+    case 7: return launch<224, FP8>(a, stream);
+    case 8: return launch<256, FP8>(a, stream);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+// A tile has more than one segment only where its keys are more than a segment's, so the segments of
+// such tiles are less than twice as many as the work has whole segments.
+size_t kv_attention_few_ws_bytes(int Hkv, int D) {
+  return (size_t)(2 * kTarget + Hkv) * kRows * (D + 2) * sizeof(float);
+}
+
+hipError_t launch_kv_attention_few(const KvAttnArgs& a, hipStream_t stream) {
+  return a.fp8 ? launch_d<true>(a, stream) : launch_d<false>(a, stream);
+}
+
+}  // namespace nvfp4moe

@@ -776,5 +776,285 @@ def _gate(gate: torch.Tensor, T: int, H: int):
     return gate, row, 1
 
 
+# ------------------------------------------------------------------ rotary positions, the paged cache
+@dataclass
+class Rope:
+    """A rotation by position: the pairs of a head's dims [start, start + 2 * len(freqs)) turn by ``freqs``
+    radians a position (rope_frequencies makes them) and are scaled by ``magnitude``. Pairs are (i, i + half)
+    of that part or, interleaved, (2i, 2i + 1)."""
+    freqs: torch.Tensor         # float64 [rot / 2], on the GPU
+    start: int = 0
+    interleaved: bool = False
+    magnitude: float = 1.0
+
+    @property
+    def rot(self) -> int:
+        return 2 * self.freqs.shape[0]
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: str | None = None, factor: float = 1.0,
+                     original: int = 0, fast: float = 32.0, slow: float = 1.0, device="cuda"):
+    """(freqs, magnitude) of Rope for ``rot`` turned dims: freqs[i] = base^(-2i / rot), stretched for contexts
+    ``factor`` times as long as the ``original`` one by ``scaling``:
+
+    - None: as they are. "linear": all divided by factor.
+    - "base": the base times factor^(rot / (rot - 2)), which divides the slowest by factor and leaves the fastest.
+    - "ramp": pairs that turn at least ``fast`` times in ``original`` positions as they are, those of at most
+      ``slow`` turns divided by factor, between them a ramp over the pairs' index; magnitude 0.1 ln(factor) + 1.
+    - "bands": the same ends, between them a ramp over the turns; magnitude 1."""
+    fn = "rope_frequencies"
+    if rot < 2 or rot % 2 or not (base > 1.0 and factor >= 1.0 and math.isfinite(base) and math.isfinite(factor)):
+        raise ValueError(f"{fn}: need an even rot >= 2, base > 1 and factor >= 1")
+    if scaling not in (None, "linear", "base", "ramp", "bands"):
+        raise ValueError(f"{fn}: scaling must be None, 'linear', 'base', 'ramp' or 'bands', got {scaling!r}")
+    if scaling in ("ramp", "bands") and not (original >= 1 and fast > slow > 0.0):
+        raise ValueError(f"{fn}: {scaling!r} needs original >= 1 and fast > slow > 0")
+    if scaling == "base" and rot == 2:
+        raise ValueError(f"{fn}: 'base' needs rot > 2")
+    if scaling == "base":
+        base = base * factor ** (rot / (rot - 2))
+    i = torch.arange(rot // 2, dtype=torch.float64)
+    f = base ** (-2.0 * i / rot)
+    magnitude = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "ramp":
+        # the pair that turns n times in the original context
+        pair = lambda n: rot * math.log(original / (2.0 * math.pi * n)) / (2.0 * math.log(base))  # noqa: E731
+        low, high = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), rot - 1)
+        part = ((i - low) / max(high - low, 0.001)).clamp(0.0, 1.0)
+        f = f * (1.0 - part) + f / factor * part
+        magnitude = 0.1 * math.log(factor) + 1.0
+    elif scaling == "bands":
+        turns = original * f / (2.0 * math.pi)
+        part = ((fast - turns) / (fast - slow)).clamp(0.0, 1.0)
+        f = f * (1.0 - part) + f / factor * part
+    return f.to(device), magnitude
+
+
+def _heads(fn: str, what: str, t, H: int, D: int, T: int, align: int = 1):
+    """(t, address, row distance, head distance) of a tensor [T, H, D] whose dims lie beside each other: in
+    place where its distances and address allow, else a contiguous copy."""
+    if t.dim() != 3 or t.shape != (T, H, D):
+        raise ValueError(f"{fn}: {what} must be [{T}, {H}, {D}], got {tuple(t.shape)}")
+    row, head, one = t.stride()
+    if H == 1:
+        head = D if align == 1 else -(-D // align) * align
+    if T == 1:
+        row = (H - 1) * head + D
+    p = t.data_ptr()
+    if (one != 1 and D > 1) or head < D or row < (H - 1) * head + D or \
+            (align > 1 and (p % 16 or (row % align and T > 1) or (head % align and H > 1))):
+        t = t.clone(memory_format=torch.contiguous_format)
+        return t, t.data_ptr(), H * D, D
+    return t, p, row, head
+
+
+def _heads_out(fn: str, what: str, t, like, H: int, D: int, T: int, align: int = 1):
+    """_heads of an output: allocated where there is none, and never a copy."""
+    if t is None:
+        t = like.new_empty((T, H, D))
+        return t, t.data_ptr(), H * D, D
+    if t.dtype != like.dtype:
+        raise ValueError(f"{fn}: {what} must be {like.dtype}, got {t.dtype}")
+    r = _heads(fn, what, t, H, D, T, align)
+    if r[0] is not t:
+        raise ValueError(f"{fn}: the dims of {what}'s heads must lie beside each other, rows and heads apart"
+                         + (f", at multiples of {align}" if align > 1 else ""))
+    return r
+
+
+def _positions(fn: str, t, T: int, idx: int):
+    """(t, address, bytes of an element) of int32 or int64 positions [T]."""
+    if t.shape != (T,) or t.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"{fn}: positions must be int32 or int64 [{T}], got {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != idx:
+        raise ValueError(f"{fn}: all tensors must be on one GPU")
+    t = t.contiguous()
+    return t, t.data_ptr(), t.element_size()
+
+
+def _rope(fn: str, rope: Rope, D: int, idx: int):
+    f = rope.freqs
+    if f.dtype != torch.float64 or f.dim() != 1 or not f.is_contiguous():
+        raise ValueError(f"{fn}: the rotation's freqs must be contiguous float64 [rot / 2], got {f.dtype} {tuple(f.shape)}")
+    if f.get_device() != idx:
+        raise ValueError(f"{fn}: all tensors must be on one GPU")
+    rot = 2 * f.shape[0]
+    if rot < 2 or rope.start < 0 or rope.start + rot > D:
+        raise ValueError(f"{fn}: the rotation's dims [{rope.start}, {rope.start + rot}) must lie in a head of {D}")
+    return f.data_ptr(), rot
+
+
+def rope_rotate(x: torch.Tensor, positions: torch.Tensor, rope: Rope, *, grad: bool = False, out: torch.Tensor | None = None):
+    """Rotary positions: the heads of ``x`` [T, H, D] (float32 or bf16) turned by ``rope`` at ``positions``
+    [T] (int32 or int64). ``grad``: the transposed rotation, which takes the output's gradient to x's.
+    Rows and heads of x and out may lie apart; ``out`` may be x."""
+    fn = "rope_rotate"
+    idx = _gpu(fn, x, positions, rope.freqs, out)
+    dt = _DT.get(x.dtype)
+    if dt is None or x.dim() != 3:
+        raise ValueError(f"{fn}: x must be float32 or bf16 [T, H, D], got {x.dtype} {tuple(x.shape)}")
+    T, H, D = x.shape
+    p_f, rot = _rope(fn, rope, D, idx)
+    with _on(idx):
+        positions, p_pos, pos_bytes = _positions(fn, positions, T, idx)
+        if T == 0 or H == 0:
+            return x.new_empty((T, H, D)) if out is None else out
+        same = out is x
+        x, p_x, x_row, x_head = _heads(fn, "x", x, H, D, T)
+        out, p_o, o_row, o_head = _heads_out(fn, "out", out, x, H, D, T)
+        if same and p_x != p_o:
+            raise ValueError(f"{fn}: x's dims must lie beside each other to be turned in place")
+        st = _lib.load().rope_rotate(p_x, dt, x_row, x_head, T, H, D, p_pos, pos_bytes, p_f, rot, rope.start,
+                                     int(rope.interleaved), int(grad), rope.magnitude, p_o, o_row, o_head, _raw_stream(idx))
+    if st:
+        _lib.check(fn, st)
+    return out
+
+
+@dataclass
+class KVCache:
+    """A paged cache of keys [pages, heads, page, D] and values [pages, heads, D, page] (transposed in their
+    pages), bf16 or float8_e4m3fn with a float32 scale for each head (None: 1). kv_cache makes an empty one."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor | None = None   # float32 [heads], positive
+    v_scale: torch.Tensor | None = None
+
+
+def kv_cache(pages: int, heads: int, page: int, D: int, dtype=torch.bfloat16, *, k_scale: torch.Tensor | None = None,
+             v_scale: torch.Tensor | None = None, device="cuda") -> KVCache:
+    """A cache of zeros."""
+    bits = torch.uint8 if dtype == torch.float8_e4m3fn else dtype
+    zeros = lambda *shape: torch.zeros(shape, dtype=bits, device=device).view(dtype)  # noqa: E731
+    return KVCache(zeros(pages, heads, page, D), zeros(pages, heads, D, page), k_scale, v_scale)
+
+
+@dataclass
+class CacheBatch:
+    """Sequences of a cache and their new tokens, int32 on the GPU: ``page_table`` [B, n] (page of the tokens
+    [c * page, (c + 1) * page) at column c), ``lengths`` [B] (tokens, the new ones among them) and ``starts``
+    [B + 1] (row of each sequence's first new token, and the end of the last one's)."""
+    page_table: torch.Tensor
+    lengths: torch.Tensor
+    starts: torch.Tensor
+
+
+def _cache(fn: str, c: KVCache, idx: int):
+    """(heads, D, page, pages, fp8, addresses of the scales) of a cache."""
+    k, v = c.k, c.v
+    if k.dim() != 4 or v.dim() != 4 or k.dtype != v.dtype or k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise ValueError(f"{fn}: the cache must be bf16 or float8_e4m3fn [pages, heads, page, D] and [pages, heads, D, page]")
+    pages, heads, page, D = k.shape
+    if v.shape != (pages, heads, D, page) or not (k.is_contiguous() and v.is_contiguous()):
+        raise ValueError(f"{fn}: the cache's values must be [pages, heads, D, page] beside keys [pages, heads, page, D], "
+                         f"both contiguous, got {tuple(v.shape)} and {tuple(k.shape)}")
+    fp8 = k.dtype != torch.bfloat16
+    scales = []
+    for s in (c.k_scale, c.v_scale):
+        if s is not None and (not fp8 or s.shape != (heads,) or s.dtype != torch.float32 or not s.is_contiguous()):
+            raise ValueError(f"{fn}: scales go with an FP8 cache, float32 [{heads}]")
+        scales.append(None if s is None else s.data_ptr())
+    return heads, D, page, pages, fp8, scales
+
+
+def _batch(fn: str, b: CacheBatch):
+    """(B, columns, row distance of the page table)."""
+    t, lengths, starts = b.page_table, b.lengths, b.starts
+    B = lengths.shape[0] if lengths.dim() == 1 else -1
+    if t.dtype != torch.int32 or lengths.dtype != torch.int32 or starts.dtype != torch.int32 or t.dim() != 2 or \
+            B < 1 or t.shape[0] != B or t.shape[1] < 1 or starts.shape != (B + 1,):
+        raise ValueError(f"{fn}: a batch is int32 page_table [B, n], lengths [B] and starts [B + 1] with B, n >= 1, got "
+                         f"{tuple(t.shape)}, {tuple(lengths.shape)} and {tuple(starts.shape)}")
+    cols = t.shape[1]
+    ld = t.stride(0) if B > 1 else cols
+    if (t.stride(1) != 1 and cols > 1) or ld < cols or not lengths.is_contiguous() or not starts.is_contiguous():
+        raise ValueError(f"{fn}: page_table's rows, lengths and starts must be contiguous")
+    return B, cols, ld
+
+
+def kv_cache_append(cache: KVCache, batch: CacheBatch, k: torch.Tensor, v: torch.Tensor, *, q: torch.Tensor | None = None,
+                    rope: Rope | None = None, positions: torch.Tensor | None = None, q_out: torch.Tensor | None = None):
+    """The new tokens' keys ``k`` and values ``v`` (bf16 [T, heads, D]) into the cache, keys turned by
+    ``rope`` at their places in their sequences (or at ``positions`` [T]), and their queries ``q`` bf16 [T, Hq, D]
+    turned likewise. Returns the turned queries (``q_out``, which may be q), or None without q. k, v and q may be
+    views of one projection's rows. Rows behind the last sequence's are left as they were."""
+    fn = "kv_cache_append"
+    idx = _gpu(fn, cache.k, cache.v, cache.k_scale, cache.v_scale, batch.page_table, batch.lengths, batch.starts, k, v, q,
+               q_out)
+    heads, D, page, pages, fp8, (p_ks, p_vs) = _cache(fn, cache, idx)
+    B, cols, ld = _batch(fn, batch)
+    if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or (q is not None and q.dtype != torch.bfloat16):
+        raise ValueError(f"{fn}: k, v and q must be bf16")
+    if q is None and q_out is not None:
+        raise ValueError(f"{fn}: q_out needs q")
+    if q is not None and q.dim() != 3:
+        raise ValueError(f"{fn}: q must be [T, Hq, D], got {tuple(q.shape)}")
+    T = k.shape[0]
+    Hq = 0 if q is None else q.shape[1]
+    p_f, rot, start, inter, mag = None, 0, 0, 0, 1.0
+    if rope is not None:
+        p_f, rot = _rope(fn, rope, D, idx)
+        start, inter, mag = rope.start, int(rope.interleaved), rope.magnitude
+    with _on(idx):
+        p_pos, pos_bytes = None, 4
+        if positions is not None:
+            positions, p_pos, pos_bytes = _positions(fn, positions, T, idx)
+        k, p_k, k_row, k_head = _heads(fn, "k", k, heads, D, T)
+        v, p_v, v_row, v_head = _heads(fn, "v", v, heads, D, T)
+        p_q = p_o = None
+        q_row = q_head = o_row = o_head = 0
+        if q is not None:
+            same = q_out is q
+            q, p_q, q_row, q_head = _heads(fn, "q", q, Hq, D, T)
+            q_out, p_o, o_row, o_head = _heads_out(fn, "q_out", q_out, q, Hq, D, T)
+            if same and p_q != p_o:
+                raise ValueError(f"{fn}: q's dims must lie beside each other to be turned in place")
+        if T == 0:
+            return q_out
+        st = _lib.load().kv_cache_append(
+            p_q, q_row, q_head, p_k, k_row, k_head, p_v, v_row, v_head, T, Hq, heads, D, p_pos, pos_bytes, p_f, rot, start,
+            inter, mag, batch.page_table.data_ptr(), ld, cols, batch.lengths.data_ptr(), batch.starts.data_ptr(), B,
+            cache.k.data_ptr(), cache.v.data_ptr(), int(fp8), pages, page, p_ks, p_vs, p_o, o_row, o_head, _raw_stream(idx))
+    if st:
+        _lib.check(fn, st)
+    return q_out
+
+
+@functools.lru_cache(maxsize=1024)
+def _attention_workspace(T: int, B: int, Hq: int, Hkv: int, D: int) -> int:
+    return _lib.load().kv_cache_attention_workspace_size(T, B, Hq, Hkv, D)
+
+
+def kv_cache_attention(q: torch.Tensor, cache: KVCache, batch: CacheBatch, *, scale: float | None = None, window: int = 0,
+                       out: torch.Tensor | None = None):
+    """Attention of the new tokens' queries ``q`` bf16 [T, Hq, D] over the cache, which holds their keys and
+    values already (kv_cache_append): each sees its sequence's tokens up to itself, with ``window`` > 0 the last
+    ``window`` of them. ``scale`` of the scores: D^-0.5 unless given. Returns bf16 [T, Hq, D] (``out``, which
+    must not overlap q); rows behind the last sequence's are left as they were."""
+    fn = "kv_cache_attention"
+    idx = _gpu(fn, q, cache.k, cache.v, cache.k_scale, cache.v_scale, batch.page_table, batch.lengths, batch.starts, out)
+    heads, D, page, pages, fp8, (p_ks, p_vs) = _cache(fn, cache, idx)
+    B, cols, ld = _batch(fn, batch)
+    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != D or q.shape[1] == 0 or q.shape[1] % heads:
+        raise ValueError(f"{fn}: q must be bf16 [T, Hq, {D}], Hq a multiple of {heads}, got {q.dtype} {tuple(q.shape)}")
+    T, Hq, _ = q.shape
+    with _on(idx):
+        q, p_q, q_row, q_head = _heads(fn, "q", q, Hq, D, T, 8)
+        out, p_o, o_row, o_head = _heads_out(fn, "out", out, q, Hq, D, T, 8)
+        if T == 0:
+            return out
+        nbytes = _attention_workspace(T, B, Hq, heads, D)
+        ws = q.new_empty((nbytes,), dtype=torch.uint8)
+        st = _lib.load().kv_cache_attention(
+            p_q, q_row, q_head, T, Hq, heads, D, batch.page_table.data_ptr(), ld, cols, batch.lengths.data_ptr(),
+            batch.starts.data_ptr(), B, cache.k.data_ptr(), cache.v.data_ptr(), int(fp8), pages, page, p_ks, p_vs,
+            D ** -0.5 if scale is None else scale, window, p_o, o_row, o_head, ws.data_ptr(), nbytes, _raw_stream(idx))
+    if st:
+        _lib.check(fn, st)
+    return out
+
+
 def last_dispatch() -> int:
     return _lib.load().nvfp4moe_last_dispatch()
