@@ -20,6 +20,9 @@
 // The rows' tiles and their blocks of keys are listed on the device by a first launch (lengths are
 // known there alone), tiles with many blocks in equal segments, which a last launch joins in a
 // fixed order.
+#include <type_traits>
+
+#include "gemm_common.h"
 #include "kv_attention.h"
 
 namespace nvfp4moe {
@@ -185,7 +188,11 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const KvAttnArgs p, 
 }
 
 // ---------------------------------------------------------------- the tiles
-// 16 bytes a lane from global memory straight into LDS (lane l at lds + 16 l).
+// 16 bytes a lane straight into LDS (lane l at lds + 16 l), from global memory or from a buffer (whose base
+// and offset `soff` are the wave's: no address arithmetic in the lanes).
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, char* lds, uint32_t voff, uint32_t soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, voff, soff, 0, 0);
+}
 __device__ __forceinline__ void dma16(const char* from, char* lds) {
   __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
                                    (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
@@ -225,12 +232,14 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
   const CacheBatchArgs& b = p.batch;
   const Sequence seq = sequence_of(b, p.window, tl.seq, kBlockLog);
 
-  // This lane's row, and the keys that it sees; and those that all of this wave's rows see.
+  // This lane's row, and the keys that it sees; those that all rows of the tile see; those that any of this
+  // wave's rows sees.
   const int rows = seq.n * p.G, row0 = tl.tile * kRows + 32 * wave;
   const int row = min(row0 + col, rows - 1), token = row / p.G, head = h * p.G + row - token * p.G;
   const Seen mine = seen_by(seq.position(token), p.window, seq.cap);
-  const int t0 = min(row0, rows - 1) / p.G, t1 = min(row0 + 31, rows - 1) / p.G;
-  const int all_lo = seen_by(seq.position(t1), p.window, seq.cap).lo, all_hi = seen_by(seq.position(t0), p.window, seq.cap).hi;
+  auto seen_of = [&](int r) { return seen_by(seq.position(min(r, rows - 1) / p.G), p.window, seq.cap); };
+  const int all_lo = seen_of(tl.tile * kRows + kRows - 1).lo, all_hi = seen_of(tl.tile * kRows).hi;
+  const int any_lo = seen_of(row0).lo, any_hi = row0 < rows ? seen_of(row0 + 31).hi : 0;
 
   bf16x8 q[C::kSteps];
   {
@@ -251,47 +260,72 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
   struct Pages {
     int k, v;   // of this wave's keys; of this lane's values
   };
+  const bool whole = b.page_log >= kBlockLog;   // a block lies in one page
   auto pages_of = [&](int block) {
-    const int key = block << kBlockLog, kc = (key + 16 * wave) >> b.page_log, vc = (key + v_key) >> b.page_log;
+    const int key = block << kBlockLog, kc = (key + 16 * wave) >> b.page_log;
     Pages r = {-1, -1};
     if (kc < b.cols) r.k = ld_const(table, kc);
-    if (vc < b.cols) r.v = table[vc];
+    r.v = r.k;
+    if (!whole) {
+      const int vc = (key + v_key) >> b.page_log;
+      r.v = vc < b.cols ? table[vc] : -1;
+    }
     return r;
   };
   constexpr int kKLoads = FP8 ? (D + 63) / 64 : D / 32, kVLoads = kKLoads;
   u32x4v raw_k[FP8 ? kKLoads : 1], raw_v[FP8 ? kVLoads : 1];
+  uint32_t k_off[kKLoads];   // this lane's words among its wave's 16 keys: bytes from the first key
+#pragma unroll
+  for (int j = 0; j < kKLoads; ++j) {
+    const int i = 64 * j + lane;
+    if (FP8) {
+      k_off[j] = i < D ? i / (D / 16) * D + i % (D / 16) * 16 : kOOB;
+    } else {
+      const int r = i / C::kWords;
+      k_off[j] = key_of_row(r) * (2 * D) + ((i % C::kWords) ^ C::swizzle(r)) * 16;
+    }
+  }
+  const uint32_t v_off = (uint32_t)((v_row * page + (whole ? v_key : v_key & page_mask)) * kSize);
   // Requests block's keys and values (bf16: into LDS buffer `to`; E4M3: into registers); the pages that are not.
   auto request = [&](int block, const Pages& pg, char* to) {
     const int key = block << kBlockLog;
     const bool k_ok = pg.k >= 0 && pg.k < b.pages, v_ok = pg.v >= 0 && pg.v < b.pages;
-    const char* k = static_cast<const char*>(p.k_cache) + ((int64_t)(k_ok ? pg.k : 0) * p.Hkv + h) * head_bytes +
-                    (int64_t)((key + 16 * wave) & page_mask) * (D * kSize);
-    const char* v = static_cast<const char*>(p.v_cache) + ((int64_t)(v_ok ? pg.v : 0) * p.Hkv + h) * head_bytes +
-                    (((key + v_key) & page_mask) + v_row * page) * kSize;
-    if constexpr (FP8) {
-      // words of 16 dims: a key has D / 16, 16 keys D
+    const __amdgpu_buffer_rsrc_t k = make_rsrc(
+        static_cast<const char*>(p.k_cache) + ((int64_t)(k_ok ? pg.k : 0) * p.Hkv + h) * head_bytes, (uint32_t)head_bytes);
+    const uint32_t k_first = (uint32_t)((key + 16 * wave) & page_mask) * (D * kSize);
 #pragma unroll
-      for (int j = 0; j < kKLoads; ++j) {
-        const int i = 64 * j + lane;
-        raw_k[j] = (u32x4v){0u, 0u, 0u, 0u};
-        if (D % 64 == 0 || i < D) raw_k[j] = *reinterpret_cast<const u32x4v*>(k + i / (D / 16) * D + i % (D / 16) * 16);
-      }
+    for (int j = 0; j < kKLoads; ++j) {
+      if constexpr (FP8)
+        raw_k[j] = __builtin_amdgcn_raw_buffer_load_b128(k, k_off[j], k_first, 0);
+      else
+        dma16(k, to + wave * 32 * D + 1024 * j, k_off[j], k_first);
+    }
+    constexpr int kVRows = FP8 ? 16 : 8;   // of V^T a load
+    if (whole) {
+      const __amdgpu_buffer_rsrc_t v = make_rsrc(
+          static_cast<const char*>(p.v_cache) + ((int64_t)(k_ok ? pg.k : 0) * p.Hkv + h) * head_bytes, (uint32_t)head_bytes);
+      const uint32_t v_first = (uint32_t)(key & page_mask) * kSize;
 #pragma unroll
       for (int j = 0; j < kVLoads; ++j) {
-        const int d = (wave * kVLoads + j) * 16;
-        raw_v[j] = (u32x4v){0u, 0u, 0u, 0u};
-        if (D % 64 == 0 || d + v_row < D) raw_v[j] = *reinterpret_cast<const u32x4v*>(v + (int64_t)d * page);
+        const int d = (wave * kVLoads + j) * kVRows;
+        if constexpr (FP8)
+          raw_v[j] = __builtin_amdgcn_raw_buffer_load_b128(v, D % 64 == 0 || d + v_row < D ? v_off : kOOB,
+                                                           D % 64 == 0 || d < D ? v_first + (uint32_t)(d * page) : 0u, 0);
+        else
+          dma16(v, to + C::kBytes + d * 128, v_off, v_first + (uint32_t)(d * page) * 2);
       }
     } else {
-#pragma unroll
-      for (int j = 0; j < kKLoads; ++j) {
-        const int i = 64 * j + lane, r = i / C::kWords;
-        dma16(k + key_of_row(r) * (2 * D) + ((i % C::kWords) ^ C::swizzle(r)) * 16, to + wave * 32 * D + 1024 * j);
-      }
+      // (a page's rows are whole multiples of the block's distance from a page's start)
+      const char* v = static_cast<const char*>(p.v_cache) + ((int64_t)(v_ok ? pg.v : 0) * p.Hkv + h) * head_bytes + v_off;
 #pragma unroll
       for (int j = 0; j < kVLoads; ++j) {
-        const int d = (wave * kVLoads + j) * 8;
-        dma16(v + (int64_t)d * page * 2, to + C::kBytes + d * 128);
+        const int d = (wave * kVLoads + j) * kVRows;
+        if constexpr (FP8) {
+          raw_v[j] = (u32x4v){0u, 0u, 0u, 0u};
+          if (D % 64 == 0 || d + v_row < D) raw_v[j] = *reinterpret_cast<const u32x4v*>(v + (int64_t)d * page);
+        } else {
+          dma16(v + (int64_t)d * page * 2, to + C::kBytes + d * 128);
+        }
       }
     }
     const uint64_t bad = __ballot(!v_ok);   // (lanes of the first row of V^T: of each 16 keys one)
@@ -326,31 +360,37 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
 
-  auto use = [&](int block, const char* from, uint32_t bad_pages) {
+  // One block in LDS; EDGE: keys that some row of the tile does not see are among its 64.
+  auto use = [&](auto edge_t, int block, const char* from, uint32_t bad_pages) {
+    constexpr bool EDGE = decltype(edge_t)::value;
+    const int begin = block << kBlockLog;
+    if (EDGE && (begin >= any_hi || begin + kBlock <= any_lo)) return;   // none that this wave's rows see
     f32x16 s[2];
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[a][i] = 0.0f;
-      const char* line = from + (32 * a + col) * (2 * D);
+    }
 #pragma unroll
-      for (int i = 0; i < C::kSteps; ++i) {
-        const bf16x8 k = *reinterpret_cast<const bf16x8*>(line + ((2 * i + half) ^ C::swizzle(col)) * 16);
+    for (int i = 0; i < C::kSteps; ++i)
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        const bf16x8 k = *reinterpret_cast<const bf16x8*>(from + (32 * a + col) * (2 * D) + ((2 * i + half) ^ C::swizzle(col)) * 16);
         s[a] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[i], s[a], 0, 0, 0);
       }
-    }
-    const int begin = block << kBlockLog;
-    const bool edge = begin < all_lo || begin + kBlock > all_hi || bad_pages != 0u;
     // score i of tile a: key 32a + 16 (i / 8) + 8 half + i % 8 of the block
-    if (edge) {
+    if constexpr (EDGE) {
 #pragma unroll
       for (int a = 0; a < 2; ++a)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int key = begin + 32 * a + 16 * (i / 8) + 8 * half + i % 8;
-          const bool sees = key >= mine.lo && key < mine.hi;
-          s[a][i] = !sees ? -INFINITY : bad_pages >> (2 * a + i / 8) & 1u ? NAN : s[a][i];
+          const bool sees = (key >= mine.lo) & (key < mine.hi);
+          const float x = bad_pages >> (2 * a + i / 8) & 1u ? NAN : s[a][i];
+          s[a][i] = sees ? x : -INFINITY;
         }
+    } else if (bad_pages != 0u) {   // every row sees every key
+      l = NAN;
     }
     float top = s[0][0];
 #pragma unroll
@@ -370,38 +410,32 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
     }
     const float base = m == -INFINITY ? 0.0f : m;
     bf16x8 w[4];
-    float sum = 0.0f;
+    float sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int a = 0; a < 2; ++a)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[a][i], log2_scale, -base));
-        sum += e;
+        sum[a] += e;
         w[2 * a + i / 8][i % 8] = (__bf16)e;
       }
-    l += sum;
+    l += sum[0] + sum[1];
     const char* values = from + C::kBytes + col * 128;
-    if (!edge) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int d = 0; d < C::kDTiles; ++d) {
-          const bf16x8 v = *reinterpret_cast<const bf16x8*>(values + d * 4096 + ((2 * u + half) ^ (col % 8)) * 16);
-          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w[u], o[d], 0, 0, 0);
-        }
-    } else {
-      // values that some row does not see (or no row: what a page holds behind its last token)
-#pragma unroll 1
-      for (int u = 0; u < 4; ++u) {
-        bf16x8 sees, wu = u == 0 ? w[0] : u == 1 ? w[1] : u == 2 ? w[2] : w[3];
+    for (int u = 0; u < 4; ++u) {
+      bf16x8 sees;
+      if constexpr (EDGE) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int key = begin + 16 * u + 8 * half + i;
           sees[i] = key >= mine.lo && key < mine.hi ? (__bf16)1.0f : (__bf16)0.0f;
         }
+      }
 #pragma unroll
-        for (int d = 0; d < C::kDTiles; ++d) {
-          u32x4v f = *reinterpret_cast<const u32x4v*>(values + d * 4096 + ((2 * u + half) ^ (col % 8)) * 16), bad;
+      for (int d = 0; d < C::kDTiles; ++d) {
+        bf16x8 v = *reinterpret_cast<const bf16x8*>(values + d * 4096 + ((2 * u + half) ^ (col % 8)) * 16);
+        if constexpr (EDGE) {   // values that some row does not see (or no row: what a page holds behind its last token)
+          u32x4v f = __builtin_bit_cast(u32x4v, v), bad;
           uint32_t any = 0u;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -410,6 +444,7 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
             bad[i] = bits & 0x3f803f80u;   // 1.0 where one was taken out
             any |= bits;
           }
+          v = __builtin_bit_cast(bf16x8, f);
           if (__any(any != 0u)) {
             f32x16 n;   // how many of them each row sees
 #pragma unroll
@@ -418,8 +453,8 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[d][i] = n[i] > 0.0f ? NAN : o[d][i];
           }
-          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, f), wu, o[d], 0, 0, 0);
         }
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w[u], o[d], 0, 0, 0);
       }
     }
   };
@@ -433,13 +468,14 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
     place(now);
     __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): the words are in LDS
     __syncthreads();
-    for (int block = sg.block0; block < end; ++block) {
+    int block = sg.block0;
+    auto step = [&](auto edge) {
       uint32_t next_bad = 0u;
       if (block + 1 < end) {
         next_bad = request(block + 1, pg, then);
         pg = pages_of(min(block + 2, end - 1));
       }
-      use(block, now, bad);
+      use(edge, block, now, bad);
       if (block + 1 < end) place(then);
       __builtin_amdgcn_s_waitcnt(0x0F70);
       __syncthreads();
@@ -447,7 +483,13 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
       now = then;
       then = t;
       bad = next_bad;
-    }
+      ++block;
+    };
+    // the blocks of which every row of the tile sees all keys, and those before and behind them
+    const int lead = min(max((all_lo + kBlock - 1) >> kBlockLog, sg.block0), end), full = min(max(all_hi >> kBlockLog, lead), end);
+    while (block < lead) step(std::true_type{});
+    while (block < full) step(std::false_type{});
+    while (block < end) step(std::true_type{});
   }
   {
     const u32x2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
