@@ -10,7 +10,7 @@
 // bf16, which holds them exactly). Scores are transposed, S^T = K Q^T: a lane holds the scores of
 // one row, and with K's rows in LDS in the right order these are, after the exponential, the operand
 // of O^T = V^T P^T without another move. The rows of LDS are not padded; their 16-byte words are
-// permuted by the row, so that neither side has bank conflicts.
+// permuted by the row, so that reads have no bank conflicts.
 //
 // Weights of the second product are exponentials rounded to bf16 (2^-9 of each, about as much again
 // as the rounding of the output; two bf16 values each would cost half the second product again).
@@ -61,7 +61,7 @@ struct PlanLayout {
     at_splits = at_segments + up((size_t)segments * sizeof(PlanSegment));
     at_first = at_splits + up((size_t)splits * 4);
     at_sums = at_first + up((size_t)(B + 1) * 4);
-    // a tile in parts has more blocks than a whole segment: fewer than twice as many parts as whole segments
+    // a tile in parts has 1.5 times the blocks of a whole segment or more: its parts are at most 4 / 3 of its whole segments
     const int64_t slots = 2 * whole < segments ? 2 * whole : segments;
     total = at_sums + (size_t)slots * Hkv * kRows * (D + 2) * sizeof(float);
   }
@@ -164,7 +164,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const KvAttnArgs p, 
     int s = 0, tile = 0, block0 = 0, blocks = 0, parts = 0;
     if (i < tiles) {
       tile_at(i, s, tile, block0, blocks);
-      parts = max((blocks + chunk - 1) / chunk, 1);
+      parts = max((blocks + chunk / 2) / chunk, 1);   // (parts of equal sizes, near a whole segment's)
     }
     int n_segments, n_slots, n_splits;
     const int first = segments + block_scan(parts, n_segments, s_wave);
@@ -172,9 +172,10 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const KvAttnArgs p, 
     const int split = splits + block_scan(parts > 1 ? 1 : 0, n_splits, s_wave);
     if (i < tiles) {
       plan.tiles[i] = {s, tile, parts, slot};
+      const int per = (blocks + parts - 1) / parts;
       for (int j = 0; j < parts; ++j)
         if (first + j < plan.max_segments)
-          plan.segments[first + j] = {i, j, block0 + j * chunk, min(chunk, blocks - j * chunk)};
+          plan.segments[first + j] = {i, j, block0 + j * per, min(per, blocks - j * per)};   // (the last may be empty)
       if (parts > 1 && split < plan.max_splits) plan.splits[split] = i;
     }
     segments += n_segments;
@@ -210,9 +211,13 @@ struct Chunk {
   static constexpr int kBytes = kBlock * D * 2;      // of a block's keys, and of its values
   static constexpr int kSteps = D / 16;              // of the first product
   static constexpr int kDTiles = D / 32;             // of the second
-  // Word w of row r of K lies at w ^ swizzle(r): 8 rows' words of one column then lie in 8 different
-  // 16-byte columns of LDS (rows of 64 bytes short of 128 put every other one half a line on).
-  static __device__ __forceinline__ int swizzle(int r) { return kWords % 8 == 0 ? r % 8 : r / 2 % 4; }
+  // LDS serves 16 lanes' 16-byte words a cycle where they lie in different 16ths of its 256-byte lines. A
+  // product reads one word of 16 rows at once, so word w of row r lies at w ^ swizzle(r): the rows' own
+  // places in the lines (kWords 16ths apart) and the swizzle make 16 different ones.
+  static __device__ __forceinline__ int swizzle(int r) {
+    return kWords % 16 == 0 ? r % 16 : kWords % 8 == 0 ? r / 2 % 8 : r / 4 % 4;
+  }
+  static __device__ __forceinline__ int v_swizzle(int d) { return d / 2 % 8; }   // rows of V^T have 8 words
 };
 
 // Key, of 16, of K's row r in LDS: row 8x + 4y + z holds key 8y + 4x + z, so that the scores of a lane
@@ -250,25 +255,28 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
   const float log2_scale = p.scale * kLog2e * (FP8 && p.k_scale ? p.k_scale[h] : 1.0f);
 
   // Staging. Wave w brings the keys 16 w and on of a block (one page's: pages are whole multiples of
-  // 16), and D / 4 rows of V^T, of which a lane always takes the same 16 bytes (bf16: 8 keys; E4M3: 16).
+  // 16), and D / 4 rows of V^T, of which a lane takes 16 bytes (bf16: 8 keys; E4M3: 16).
   constexpr int kSize = FP8 ? 1 : 2;
   const int page = b.page, page_mask = page - 1;
   const int64_t head_bytes = (int64_t)page * D * kSize;
   const int* table = b.page_table + tl.seq * b.ld_table;
-  const int v_word = FP8 ? lane % 4 : (lane % 8) ^ (lane / 8);        // of the 4 or 8 words of a row of V^T
+  // (bf16: a load is 8 rows of V^T, whose swizzle is the lane's and, in every second load, 4: the lane's word
+  // is then one of the block's other half)
+  const int v_word = FP8 ? lane % 4 : (lane % 8) ^ (lane / 16);       // of the 4 or 8 words of a row of V^T
   const int v_key = FP8 ? 16 * v_word : 8 * v_word, v_row = FP8 ? lane / 4 : lane / 8;
   struct Pages {
-    int k, v;   // of this wave's keys; of this lane's values
+    int k, v, v2;   // of this wave's keys; of this lane's values, in the two kinds of load
   };
   const bool whole = b.page_log >= kBlockLog;   // a block lies in one page
   auto pages_of = [&](int block) {
     const int key = block << kBlockLog, kc = (key + 16 * wave) >> b.page_log;
-    Pages r = {-1, -1};
+    Pages r = {-1, -1, -1};
     if (kc < b.cols) r.k = ld_const(table, kc);
-    r.v = r.k;
+    r.v = r.v2 = r.k;
     if (!whole) {
-      const int vc = (key + v_key) >> b.page_log;
+      const int vc = (key + v_key) >> b.page_log, vc2 = (key + (v_key ^ 32)) >> b.page_log;
       r.v = vc < b.cols ? table[vc] : -1;
+      if (!FP8) r.v2 = vc2 < b.cols ? table[vc2] : -1;
     }
     return r;
   };
@@ -312,11 +320,12 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
           raw_v[j] = __builtin_amdgcn_raw_buffer_load_b128(v, D % 64 == 0 || d + v_row < D ? v_off : kOOB,
                                                            D % 64 == 0 || d < D ? v_first + (uint32_t)(d * page) : 0u, 0);
         else
-          dma16(v, to + C::kBytes + d * 128, v_off, v_first + (uint32_t)(d * page) * 2);
+          dma16(v, to + C::kBytes + d * 128, d / 8 % 2 ? v_off ^ 64u : v_off, v_first + (uint32_t)(d * page) * 2);
       }
-    } else {
-      // (a page's rows are whole multiples of the block's distance from a page's start)
+    } else {   // (pages of 16 and 32: 32 keys on, a lane's place in its page is the same)
+      const bool v2_ok = pg.v2 >= 0 && pg.v2 < b.pages;
       const char* v = static_cast<const char*>(p.v_cache) + ((int64_t)(v_ok ? pg.v : 0) * p.Hkv + h) * head_bytes + v_off;
+      const char* v2 = static_cast<const char*>(p.v_cache) + ((int64_t)(v2_ok ? pg.v2 : 0) * p.Hkv + h) * head_bytes + v_off;
 #pragma unroll
       for (int j = 0; j < kVLoads; ++j) {
         const int d = (wave * kVLoads + j) * kVRows;
@@ -324,7 +333,7 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
           raw_v[j] = (u32x4v){0u, 0u, 0u, 0u};
           if (D % 64 == 0 || d + v_row < D) raw_v[j] = *reinterpret_cast<const u32x4v*>(v + (int64_t)d * page);
         } else {
-          dma16(v + (int64_t)d * page * 2, to + C::kBytes + d * 128);
+          dma16((d / 8 % 2 ? v2 : v) + (int64_t)d * page * 2, to + C::kBytes + d * 128);
         }
       }
     }
@@ -348,7 +357,8 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
       for (int j = 0; j < kVLoads; ++j) {
         const int d = (wave * kVLoads + j) * 16 + v_row;
         char* line = to + C::kBytes + d * 128;
-        if (D % 64 == 0 || d < D) put(line + ((2 * v_word) ^ (d % 8)) * 16, line + ((2 * v_word + 1) ^ (d % 8)) * 16, raw_v[j]);
+        const int x = C::v_swizzle(d);
+        if (D % 64 == 0 || d < D) put(line + ((2 * v_word) ^ x) * 16, line + ((2 * v_word + 1) ^ x) * 16, raw_v[j]);
       }
     }
   };
@@ -433,7 +443,7 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
       }
 #pragma unroll
       for (int d = 0; d < C::kDTiles; ++d) {
-        bf16x8 v = *reinterpret_cast<const bf16x8*>(values + d * 4096 + ((2 * u + half) ^ (col % 8)) * 16);
+        bf16x8 v = *reinterpret_cast<const bf16x8*>(values + d * 4096 + ((2 * u + half) ^ C::v_swizzle(col)) * 16);
         if constexpr (EDGE) {   // values that some row does not see (or no row: what a page holds behind its last token)
           u32x4v f = __builtin_bit_cast(u32x4v, v), bad;
           uint32_t any = 0u;

@@ -58,7 +58,7 @@ __device__ __forceinline__ Segment segment_of(const KvAttnArgs& p, int block_log
     const int s = s0 + lane;
     if (b.B > kWave) mine = s < b.B ? sequence_of(b, p.window, s, block_log) : Sequence{};
     const int tiles = s < b.B ? (mine.n * p.G + kRows - 1) / kRows : 0;
-    const int parts = max((mine.blocks + chunk - 1) / chunk, 1), count = by_tile ? tiles : tiles * parts;
+    const int parts = max((mine.blocks + chunk / 2) / chunk, 1), count = by_tile ? tiles : tiles * parts;
     const int split = parts > 1 ? tiles * parts : 0;
     const int upto = wave_scan(count, lane), split_upto = wave_scan(split, lane);
     const uint64_t hit = __ballot(before + upto > at);
@@ -71,8 +71,9 @@ __device__ __forceinline__ Segment segment_of(const KvAttnArgs& p, int block_log
       r.tile = by_tile ? in : in / r.parts;
       r.part = by_tile ? 0 : in - r.tile * r.parts;
       r.slot = slots + get(split_upto) - get(split) + r.tile * r.parts + r.part;
-      r.block0 = r.seq.block0 + r.part * chunk;
-      r.blocks = min(chunk, r.seq.blocks - r.part * chunk);
+      const int per = ((r.seq.blocks + r.parts - 1) / r.parts + kWaves - 1) / kWaves * kWaves;
+      r.block0 = r.seq.block0 + r.part * per;
+      r.blocks = max(min(per, r.seq.blocks - r.part * per), 0);
       r.found = true;
       // (which sequence: its page table's row)
       r.seq.block0 = s0 + l;
@@ -458,8 +459,8 @@ hipError_t launch_d(const KvAttnArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-// A tile has more than one segment only where its keys are more than a segment's, so the segments of
-// such tiles are less than twice as many as the work has whole segments.
+// A tile has more than one segment only from 1.5 times a whole segment's keys on, so the segments of
+// such tiles are at most 4 / 3 as many as the work has whole segments.
 size_t kv_attention_few_ws_bytes(int Hkv, int D) {
   return (size_t)(2 * kTarget + Hkv) * kRows * (D + 2) * sizeof(float);
 }
