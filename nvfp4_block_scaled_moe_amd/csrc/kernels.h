@@ -311,7 +311,8 @@ struct KvAttnArgs {
 };
 size_t kv_attention_ws_bytes(int T, int B, int Hq, int Hkv, int D);
 hipError_t launch_kv_attention(const KvAttnArgs& a, hipStream_t stream);
-// its form for tiles of 16 rows (kv_attention_few.hip)
+// its form for tiles of 16 rows (kv_attention_few.hip), and whether the sizes ask for it
+bool kv_attention_few_fits(int T, int B, int G);
 size_t kv_attention_few_ws_bytes(int Hkv, int D);
 hipError_t launch_kv_attention_few(const KvAttnArgs& a, hipStream_t stream);
 

@@ -47,17 +47,22 @@ __device__ __forceinline__ Seen seen_by(int position, int window, int cap) {
   return {window > 0 ? max(position + 1 - window, 0) : 0, min(max(position + 1, 0), cap)};
 }
 
-template <typename T>
-__device__ __forceinline__ T wave_sum(T v) {
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
+// Inclusive sums over the lanes by DPP moves (no LDS round trips): within rows of 16, then rows 1 and 3
+// take the row before, then rows 2 and 3 the first half's.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);    // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row_bcast15
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // row_bcast31
   return v;
 }
-__device__ __forceinline__ int wave_scan(int v, int lane) {   // inclusive
-  for (int o = 1; o < kWave; o <<= 1) {
-    const int u = __shfl_up(v, o, kWave);
-    if (lane >= o) v += u;
-  }
-  return v;
+// Sum over the lanes of values in [0, 2^55), the same in all.
+__device__ __forceinline__ int64_t wave_sum(int64_t v) {
+  const int lo = __builtin_amdgcn_readlane(wave_scan((int)(v & 0xffffff)), kWave - 1);
+  const int hi = __builtin_amdgcn_readlane(wave_scan((int)(v >> 24)), kWave - 1);
+  return ((int64_t)hi << 24) + lo;
 }
 
 // Four E4M3 bytes as bf16 (exact).
@@ -78,6 +83,20 @@ __device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w, uint32_t& bad) {
   const uint32_t lo = (w & 0x7f80u) == 0x7f80u ? 0xffffu : 0u, hi = (w & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u;
   bad = lo | hi;
   return w & ~bad;
+}
+
+// Four E4M3 bytes with NaN (0x7f, 0xff) replaced by 0.
+__device__ __forceinline__ uint32_t finite_e4m3x4(uint32_t w) {
+  uint32_t nan = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;   // bit 7 of each that is NaN
+  return w & ~(nan | (nan - (nan >> 7)));
+}
+
+// max of a lane's value and those of the lanes 16, 32 and 48 on
+__device__ __forceinline__ float max_of_groups(float v) {
+  const u32x2 a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const u32x2 b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 
 }  // namespace nvfp4moe

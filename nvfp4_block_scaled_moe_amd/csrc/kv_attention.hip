@@ -89,7 +89,7 @@ constexpr int kPlanWaves = kPlanThreads / kWave;
 // Exclusive sum over the workgroup (and its total).
 __device__ __forceinline__ int block_scan(int v, int& total, int* s_wave) {
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  const int upto = wave_scan(v, lane);
+  const int upto = wave_scan(v);
   __syncthreads();   // (s_wave may still be read)
   if (lane == kWave - 1) s_wave[wave] = upto;
   __syncthreads();
@@ -374,7 +374,8 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
   auto use = [&](auto edge_t, int block, const char* from, uint32_t bad_pages) {
     constexpr bool EDGE = decltype(edge_t)::value;
     const int begin = block << kBlockLog;
-    if (EDGE && (begin >= any_hi || begin + kBlock <= any_lo)) return;   // none that this wave's rows see
+    if (row0 >= rows) return;                                            // this wave has no rows: it brings words alone
+    if (EDGE && (begin >= any_hi || begin + kBlock <= any_lo)) return;   // none that its rows see
     f32x16 s[2];
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
@@ -600,18 +601,15 @@ hipError_t launch_d(const KvAttnArgs& a, hipStream_t stream) {
   return hipErrorInvalidValue;
 }
 
-// Rows of a sequence, on average, up to which its tiles of 16 rows are few.
-bool few(int T, int B, int G) { return (int64_t)T * G <= (int64_t)16 * B; }
-
 }  // namespace
 
 size_t kv_attention_ws_bytes(int T, int B, int Hq, int Hkv, int D) {
-  if (few(T, B, Hq / Hkv)) return kv_attention_few_ws_bytes(Hkv, D);
+  if (kv_attention_few_fits(T, B, Hq / Hkv)) return kv_attention_few_ws_bytes(Hkv, D);
   return PlanLayout(T, B, Hkv, Hq / Hkv, D).total;
 }
 
 hipError_t launch_kv_attention(const KvAttnArgs& a, hipStream_t stream) {
-  if (few(a.batch.T, a.batch.B, a.G)) return launch_kv_attention_few(a, stream);
+  if (kv_attention_few_fits(a.batch.T, a.batch.B, a.G)) return launch_kv_attention_few(a, stream);
   return a.fp8 ? launch_d<true>(a, stream) : launch_d<false>(a, stream);
 }
 

@@ -16,6 +16,7 @@
 // device, from the lengths, which the host does not know; a workgroup of four waves takes one
 // segment, its waves every fourth block. Where a tile has more than one segment, they leave
 // unnormalised sums, which a second launch joins in a fixed order.
+#include "gemm_common.h"
 #include "kv_attention.h"
 
 namespace nvfp4moe {
@@ -25,7 +26,10 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kRows = 16;          // rows of a tile
 constexpr int kTarget = 1024;      // segments that the work is divided into
-constexpr int kMinBlocks = 4;      // least blocks of a segment (one a wave)
+// Least blocks of a segment: joining costs a second launch, so that a few blocks more a wave cost less.
+constexpr int kMinBlocks = 16;
+// Blocks from which a tile may be split (parts are rounded: 1.5 segments make two).
+constexpr int kSplitBlocks = kMinBlocks + kMinBlocks / 2;
 
 // The segment of workgroup `at` (over the tiles' segments, heads aside), found by every wave by itself.
 struct Segment {
@@ -60,7 +64,7 @@ __device__ __forceinline__ Segment segment_of(const KvAttnArgs& p, int block_log
     const int tiles = s < b.B ? (mine.n * p.G + kRows - 1) / kRows : 0;
     const int parts = max((mine.blocks + chunk / 2) / chunk, 1), count = by_tile ? tiles : tiles * parts;
     const int split = parts > 1 ? tiles * parts : 0;
-    const int upto = wave_scan(count, lane), split_upto = wave_scan(split, lane);
+    const int upto = wave_scan(count), split_upto = wave_scan(split);
     const uint64_t hit = __ballot(before + upto > at);
     if (hit) {
       const int l = __builtin_ctzll(hit);
@@ -85,8 +89,8 @@ __device__ __forceinline__ Segment segment_of(const KvAttnArgs& p, int block_log
   return r;
 }
 
-// Sums of a segment in the workspace: [slot, head] of [kRows, D] unnormalised outputs, then of
-// [kRows] maxima (of base 2 logits) and sums.
+// Sums of a segment in the workspace: [slot, head] of [kRows, D] unnormalised outputs, then of [kRows]
+// maxima (of base 2 logits) and sums.
 struct Parts {
   float* o;
   float* ml;
@@ -109,11 +113,12 @@ struct Few {
   static constexpr int kKWords = FP8 ? (D + 63) / 64 : D / 32;
 };
 
-template <int D, bool FP8>
+// WHOLE: a block lies in one page, so that its addresses are the wave's; otherwise each lane looks up its keys' pages.
+template <int D, bool FP8, bool WHOLE>
 __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void few_kernel(const KvAttnArgs p) {
   using F = Few<D, FP8>;
-  extern __shared__ float lds[];   // [kWaves, kRows, D + 1] outputs, then [kWaves, kRows, 2] maxima and sums
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, c = lane & 15, g = lane >> 4;
+  extern __shared__ float lds[];   // [kWaves, 16, D + 4] outputs, then [kWaves, 16, 2] maxima and sums
+  const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), c = lane & 15, g = lane >> 4;
   const int h = blockIdx.x % p.Hkv;
   const Segment sg = segment_of(p, F::kBlockLog, blockIdx.x / p.Hkv, false);
   if (!sg.found) return;
@@ -125,11 +130,105 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void few_kernel(con
   const int rows = sg.seq.n * p.G;
   const int row = min(sg.tile * kRows + c, rows - 1), token = row / p.G, head = h * p.G + row - token * p.G;
   const Seen mine = seen_by(sg.seq.position(token), p.window, sg.seq.cap);
-  const int first_token = sg.tile * kRows / p.G, last_token = min((sg.tile * kRows + kRows - 1) / p.G, sg.seq.n - 1);
   // Keys that every row sees: blocks within need no mask.
+  const int first_token = sg.tile * kRows / p.G, last_token = min((sg.tile * kRows + kRows - 1) / p.G, sg.seq.n - 1);
   const int all_lo = seen_by(sg.seq.position(last_token), p.window, sg.seq.cap).lo;
   const int all_hi = seen_by(sg.seq.position(first_token), p.window, sg.seq.cap).hi;
 
+  // This lane's places in a block: for K the key of row c of each tile (rows 4a + i of tile t are key
+  // 8a + 4t + i, E4M3 16a + 4t + i), for V and the scores the keys 8g (16g) and on.
+  constexpr int kSize = FP8 ? 1 : 2;
+  const int page = b.page, page_mask = page - 1;
+  const int k_key = (F::kBlock / 4) * (c / 4) + c % 4, v_key = (F::kBlock / 4) * g;
+  const int* table = b.page_table + s * b.ld_table;
+  const int64_t head_bytes = (int64_t)page * D * kSize;
+  struct Pages {
+    int k, v;   // of this lane's keys, and values (WHOLE: the same, and the wave's)
+  };
+  // (columns are checked against the table: a block may end behind it)
+  auto pages_of = [&](int block) {
+    Pages r = {-1, -1};
+    if constexpr (WHOLE) {
+      const int col = (block << F::kBlockLog) >> b.page_log;
+      if (col < b.cols) r.k = ld_const(table, col);
+      r.v = r.k;
+    } else {
+      // (2 or 4 pages of 16 or 32 keys, in scalar registers)
+      const int col = (block << F::kBlockLog) >> b.page_log, k_page = k_key >> b.page_log, v_page = v_key >> b.page_log;
+#pragma unroll
+      for (int i = 0; i < F::kBlock / 16; ++i) {
+        const int at = i < F::kBlock >> b.page_log && col + i < b.cols ? ld_const(table, col + i) : -1;
+        r.k = k_page == i ? at : r.k;
+        r.v = v_page == i ? at : r.v;
+      }
+    }
+    return r;
+  };
+  struct Words {
+    u32x4v k[F::kTiles][F::kKWords], v[F::kDTiles];
+    bool bad;   // this lane's keys have no page
+  };
+  const uint32_t k_off = (uint32_t)(((WHOLE ? k_key : k_key & page_mask) * D) * kSize + 16 * g);
+  const uint32_t v_off = (uint32_t)(((WHOLE ? v_key : v_key & page_mask) + c * page) * kSize);
+  const char* k_cache = static_cast<const char*>(p.k_cache) + h * head_bytes;
+  const char* v_cache = static_cast<const char*>(p.v_cache) + h * head_bytes;
+  auto page_at = [&](int pg) { return (int64_t)(pg >= 0 && pg < b.pages ? pg : 0) * (p.Hkv * head_bytes); };
+  auto load_k = [&](int block, const Pages& pg, Words& w) {
+    const uint32_t first = (uint32_t)((block << F::kBlockLog) & page_mask) * (D * kSize);   // (not WHOLE: pages start with blocks, or 0)
+    const char* at = k_cache + page_at(pg.k);
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(at, (uint32_t)head_bytes);
+#pragma unroll
+    for (int t = 0; t < F::kTiles; ++t)
+#pragma unroll
+      for (int i = 0; i < F::kKWords; ++i) {
+        const uint32_t o = (uint32_t)(4 * t * D * kSize + 64 * i);
+        if (!FP8 || 64 * i + 64 <= D) {
+          if constexpr (WHOLE)
+            w.k[t][i] = __builtin_bit_cast(u32x4v, __builtin_amdgcn_raw_buffer_load_b128(r, k_off + o, first, 0));
+          else
+            w.k[t][i] = *reinterpret_cast<const u32x4v*>(at + (k_off + first + o));
+        } else {   // E4M3, the last 32 dims: 8 bytes a lane
+          u32x2 x;
+          if constexpr (WHOLE)
+            x = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, k_off - 8 * g + o, first, 0));
+          else
+            x = *reinterpret_cast<const u32x2*>(at + (k_off - 8 * g + first + o));
+          w.k[t][i] = (u32x4v){x[0], x[1], 0u, 0u};
+        }
+      }
+  };
+  auto load_v = [&](int block, const Pages& pg, Words& w) {
+    const uint32_t first = (uint32_t)((block << F::kBlockLog) & page_mask) * kSize;
+    const char* at = v_cache + page_at(pg.v);
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(at, (uint32_t)head_bytes);
+    w.bad = pg.v < 0 || pg.v >= b.pages;
+#pragma unroll
+    for (int d = 0; d < F::kDTiles; ++d) {
+      const uint32_t o = (uint32_t)(16 * d * page * kSize);
+      if constexpr (WHOLE)
+        w.v[d] = __builtin_bit_cast(u32x4v, __builtin_amdgcn_raw_buffer_load_b128(r, v_off, first + o, 0));
+      else
+        w.v[d] = *reinterpret_cast<const u32x4v*>(at + (v_off + first + o));
+    }
+  };
+
+  // This wave's blocks: every kWaves-th. Two of them are in registers or on their way: as soon as the keys
+  // (values) of one are used up, those of the block two on are requested into their registers.
+  const int end = sg.block0 + sg.blocks, block0 = sg.block0 + wave;
+  auto ahead = [&](int block) { return min(block, end - 1); };
+  Words words[2];
+  Pages pages[2];   // of the blocks two and three on
+  if (block0 < end) {
+    const Pages p0 = pages_of(block0), p1 = pages_of(ahead(block0 + kWaves));
+    pages[0] = pages_of(ahead(block0 + 2 * kWaves));
+    pages[1] = pages_of(ahead(block0 + 3 * kWaves));
+    load_k(block0, p0, words[0]);
+    load_v(block0, p0, words[0]);
+    if (block0 + kWaves < end) {
+      load_k(block0 + kWaves, p1, words[1]);
+      load_v(block0 + kWaves, p1, words[1]);
+    }
+  }
   bf16x8 q[F::kDSteps];
   {
     const uint16_t* at = p.q + (sg.seq.row0 + token) * p.q_row + head * p.q_head;
@@ -142,67 +241,13 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void few_kernel(con
   }
   const float log2_scale = p.scale * kLog2e * (FP8 && p.k_scale ? p.k_scale[h] : 1.0f);
 
-  // This lane's places in a block: for K the key of row c of each tile (rows 4a + i of tile t are key
-  // 8a + 4t + i, E4M3 16a + 4t + i), for V and the scores the keys 8g (16g) and on.
-  const int page = b.page, page_mask = page - 1;
-  const int k_key = (F::kBlock / 4) * (c / 4) + c % 4, v_key = (F::kBlock / 4) * g;
-  const int* table = b.page_table + s * b.ld_table;
-  const int64_t head_size = (int64_t)page * D;
-  struct Pages {
-    int k, v;
-  };
-  auto pages_of = [&](int block) {
-    // (columns are checked against the table: a block may end behind it)
-    const int kc = ((block << F::kBlockLog) + k_key) >> b.page_log, vc = ((block << F::kBlockLog) + v_key) >> b.page_log;
-    Pages r = {-1, -1};
-    if (kc < b.cols) r.k = table[kc];
-    if (vc < b.cols) r.v = table[vc];
-    return r;
-  };
-  struct Words {
-    u32x4v k[F::kTiles][F::kKWords], v[F::kDTiles];
-    bool bad;   // this lane's keys have no page
-  };
-  auto load = [&](int block, const Pages& pg, Words& w) {
-    const bool k_ok = pg.k >= 0 && pg.k < b.pages, v_ok = pg.v >= 0 && pg.v < b.pages;
-    w.bad = !v_ok;
-    const int key = block << F::kBlockLog;
-    const int64_t ks = ((int64_t)(k_ok ? pg.k : 0) * p.Hkv + h) * head_size + (int64_t)((key + k_key) & page_mask) * D;
-    const int64_t vs = ((int64_t)(v_ok ? pg.v : 0) * p.Hkv + h) * head_size + ((key + v_key) & page_mask) + (int64_t)c * page;
-    if constexpr (FP8) {
-      const uint8_t* ka = static_cast<const uint8_t*>(p.k_cache) + ks + 16 * g;
-      const uint8_t* va = static_cast<const uint8_t*>(p.v_cache) + vs;
-#pragma unroll
-      for (int t = 0; t < F::kTiles; ++t)
-#pragma unroll
-        for (int i = 0; i < F::kKWords; ++i) {
-          if (64 * i + 64 <= D) {
-            w.k[t][i] = *reinterpret_cast<const u32x4v*>(ka + 4 * t * D + 64 * i);
-          } else {
-            const u32x2 x = *reinterpret_cast<const u32x2*>(ka - 8 * g + 4 * t * D + 64 * i);
-            w.k[t][i] = (u32x4v){x[0], x[1], 0u, 0u};
-          }
-        }
-#pragma unroll
-      for (int d = 0; d < F::kDTiles; ++d) w.v[d] = *reinterpret_cast<const u32x4v*>(va + 16 * d * page);
-    } else {
-      const uint16_t* ka = static_cast<const uint16_t*>(p.k_cache) + ks + 8 * g;
-      const uint16_t* va = static_cast<const uint16_t*>(p.v_cache) + vs;
-#pragma unroll
-      for (int t = 0; t < F::kTiles; ++t)
-#pragma unroll
-        for (int i = 0; i < F::kKWords; ++i) w.k[t][i] = *reinterpret_cast<const u32x4v*>(ka + 4 * t * D + 32 * i);
-#pragma unroll
-      for (int d = 0; d < F::kDTiles; ++d) w.v[d] = *reinterpret_cast<const u32x4v*>(va + 16 * d * page);
-    }
-  };
-
   float m = -INFINITY, l = 0.0f;
   f32x4 o[F::kDTiles];
 #pragma unroll
   for (int d = 0; d < F::kDTiles; ++d) o[d] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
 
-  auto use = [&](int block, const Words& w) {
+  auto use = [&](int block, Words& w, Pages& pg) {
+    const int then = block + 2 * kWaves;
     const int key0 = (block << F::kBlockLog) + v_key;   // the key of this lane's first score
     f32x4 sc[F::kTiles];
 #pragma unroll
@@ -220,6 +265,7 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void few_kernel(con
         sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, q[i], sc[t], 0, 0, 0);
       }
     }
+    if (then < end) load_k(then, pg, w);
     const int begin = block << F::kBlockLog;
     const bool edge = begin < all_lo || begin + F::kBlock > all_hi || __any(w.bad);
     float x[F::kTiles][4], top = -INFINITY;
@@ -235,8 +281,7 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void few_kernel(con
         }
         top = fmaxf(top, x[t][i]);
       }
-    top = fmaxf(top, __shfl_xor(top, 16, kWave));
-    top = fmaxf(top, __shfl_xor(top, 32, kWave));
+    top = max_of_groups(top);
     // (fmaxf leaves NaN out: a row with one gets it from its exponential)
     const float next = fmaxf(m, top), base = next == -INFINITY ? 0.0f : next;
     const float shrink = __builtin_amdgcn_exp2f(m - base);
@@ -255,19 +300,21 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void few_kernel(con
       }
     l = l * shrink + sum;
 #pragma unroll
-    for (int d = 0; d < F::kDTiles; ++d) {
+    for (int d = 0; d < F::kDTiles; ++d)
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[d][i] *= shrink;
+    if (edge) {   // values that some row does not see (or no row: what a page holds behind its last token)
 #pragma unroll
-      for (int u = 0; u < F::kPSteps; ++u) {
-        bf16x8 v;
-        if constexpr (FP8)
-          v = u ? e4m3x8_to_bf16(w.v[d][2], w.v[d][3]) : e4m3x8_to_bf16(w.v[d][0], w.v[d][1]);
-        else
-          v = __builtin_bit_cast(bf16x8, w.v[d]);
-        if (edge) {   // values that some row does not see (or no row: what a page holds behind its last token)
-          u32x4v f = __builtin_bit_cast(u32x4v, v), bad;
+      for (int d = 0; d < F::kDTiles; ++d) {
+#pragma unroll
+        for (int u = 0; u < F::kPSteps; ++u) {
+          u32x4v bad;
           uint32_t any = 0u;
+          u32x4v f;
+          if constexpr (FP8)
+            f = __builtin_bit_cast(u32x4v, u ? e4m3x8_to_bf16(w.v[d][2], w.v[d][3]) : e4m3x8_to_bf16(w.v[d][0], w.v[d][1]));
+          else
+            f = w.v[d];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t bits;
@@ -275,52 +322,48 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void few_kernel(con
             bad[i] = bits & 0x3f803f80u;   // 1.0 where one was taken out
             any |= bits;
           }
-          v = __builtin_bit_cast(bf16x8, f);
           if (__any(any != 0u)) {
-            // how many of them each row sees
+            // how many of them each row sees; a NaN in the sum where it is any, a zero in their place
             bf16x8 sees;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const int key = key0 + 8 * u + i;
               sees[i] = key >= mine.lo && key < mine.hi ? (__bf16)1.0f : (__bf16)0.0f;
             }
-            const f32x4 n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, bad), sees,
-                                                                    (f32x4){0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+            const f32x4 count = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, bad), sees,
+                                                                        (f32x4){0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[d][i] = n[i] > 0.0f ? NAN : o[d][i];
+            for (int i = 0; i < 4; ++i) o[d][i] = count[i] > 0.0f ? NAN : o[d][i];
+            if constexpr (FP8) {   // (E4M3's only ones are its two NaN codes)
+              w.v[d][2 * u] = finite_e4m3x4(w.v[d][2 * u]);
+              w.v[d][2 * u + 1] = finite_e4m3x4(w.v[d][2 * u + 1]);
+            } else {
+              w.v[d] = f;
+            }
           }
         }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < F::kPSteps; ++u)
+#pragma unroll
+      for (int d = 0; d < F::kDTiles; ++d) {
+        bf16x8 v;
+        if constexpr (FP8)
+          v = u ? e4m3x8_to_bf16(w.v[d][2], w.v[d][3]) : e4m3x8_to_bf16(w.v[d][0], w.v[d][1]);
+        else
+          v = __builtin_bit_cast(bf16x8, w.v[d]);
         o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, hi[u], o[d], 0, 0, 0);
         o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, lo[u], o[d], 0, 0, 0);
       }
+    if (then < end) {
+      load_v(then, pg, w);
+      pg = pages_of(ahead(then + 2 * kWaves));
     }
   };
-
-  // This wave's blocks: every kWaves-th. Pages are looked up two of them ahead, words loaded one.
-  {
-    const int end = sg.block0 + sg.blocks;
-    int block = sg.block0 + wave;
-    if (block < end) {
-      Words a, z;
-      load(block, pages_of(block), a);
-      Pages pg = pages_of(min(block + kWaves, end - 1));
-      while (true) {
-        if (block + kWaves < end) {
-          load(block + kWaves, pg, z);
-          pg = pages_of(min(block + 2 * kWaves, end - 1));
-        }
-        use(block, a);
-        block += kWaves;
-        if (block >= end) break;
-        if (block + kWaves < end) {
-          load(block + kWaves, pg, a);
-          pg = pages_of(min(block + 2 * kWaves, end - 1));
-        }
-        use(block, z);
-        block += kWaves;
-        if (block >= end) break;
-      }
-    }
+  for (int block = block0; block < end; block += 2 * kWaves) {
+    use(block, words[0], pages[0]);
+    if (block + kWaves < end) use(block + kWaves, words[1], pages[1]);
   }
   l += __shfl_xor(l, 16, kWave);
   l += __shfl_xor(l, 32, kWave);
@@ -337,8 +380,7 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void few_kernel(con
   }
   __syncthreads();
   const float v_scale = FP8 && p.v_scale ? p.v_scale[h] : 1.0f;
-  const int in_tile = min(rows - sg.tile * kRows, kRows);
-  for (int i = threadIdx.x; i < in_tile * (D / 8); i += kWaves * kWave) {
+  for (int i = threadIdx.x; i < min(rows - sg.tile * kRows, kRows) * (D / 8); i += kWaves * kWave) {
     const int r = i / (D / 8), d = (i - r * (D / 8)) * 8;
     float top = -INFINITY, factor[kWaves], total = 0.0f;
 #pragma unroll
@@ -375,89 +417,100 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void few_kernel(con
   }
 }
 
-// Joins the segments of a tile: a workgroup a row of a tile and head; its threads hold 4 dims of
-// every kGroups-th segment.
+// Joins the segments of a tile: a workgroup a few rows of a tile and head, at a time `together` of them; a row's
+// threads hold 4 dims each of every groups-th segment.
 constexpr int kJoinThreads = 256;
 template <bool FP8>
-__global__ __launch_bounds__(kJoinThreads) void few_join_kernel(const KvAttnArgs p, int block_log) {
+__global__ __launch_bounds__(kJoinThreads) void few_join_kernel(const KvAttnArgs p, int block_log, int together) {
   __shared__ float4 s_o[kJoinThreads];
-  __shared__ float s_f[2 * kTarget];   // factors of the segments
-  const int r = blockIdx.x % kRows, h = blockIdx.x / kRows % p.Hkv;
-  const Segment sg = segment_of(p, block_log, blockIdx.x / kRows / p.Hkv, true);
+  __shared__ float2 s_ml[kJoinThreads];
+  const int sets = kRows / together;
+  const int h = blockIdx.x / sets % p.Hkv;
+  const Segment sg = segment_of(p, block_log, blockIdx.x / sets / p.Hkv, true);
+  if (!sg.found || sg.parts < 2) return;
+  const int lanes = p.D / 4, groups = kJoinThreads / (lanes * together);
+  const int lane = threadIdx.x % lanes, group = threadIdx.x / lanes % groups, r = blockIdx.x % sets * together + threadIdx.x / (lanes * groups);
   const int rows = sg.seq.n * p.G, at = sg.tile * kRows + r;
-  if (!sg.found || sg.parts < 2 || at >= rows) return;
-  const int lanes = p.D / 4, groups = kJoinThreads / lanes, group = threadIdx.x / lanes, d = threadIdx.x % lanes * 4;
-  // every wave: the row's maximum and sum over the segments
-  const int lane = threadIdx.x % kWave;
-  float top = -INFINITY, total = 0.0f;
-  for (int i = lane; i < sg.parts; i += kWave) top = fmaxf(top, Parts(p, sg.slot + i, h).ml[2 * r]);
-  top = wave_max(top);
-  for (int i = lane; i < sg.parts; i += kWave) {
-    const Parts part(p, sg.slot + i, h);
-    const float f = top == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(part.ml[2 * r] - top);
-    total += part.ml[2 * r + 1] * f;
-    s_f[i] = f;   // (the same from every wave)
-  }
-  total = wave_sum(total);
-  __syncthreads();
+  const bool mine = threadIdx.x < lanes * groups * together && at < rows;
+  float m = -INFINITY, l = 0.0f;
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (group < groups)
+  auto add = [&](float2 ml, float4 x) {
+    const float next = fmaxf(m, ml.x), base = next == -INFINITY ? 0.0f : next;
+    const float f = __builtin_amdgcn_exp2f(m - base), e = ml.x == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(ml.x - base);
+    m = next;
+    l = l * f + ml.y * e;
+    v.x = v.x * f + x.x * e, v.y = v.y * f + x.y * e, v.z = v.z * f + x.z * e, v.w = v.w * f + x.w * e;
+  };
+  if (mine)
+#pragma unroll 4
     for (int i = group; i < sg.parts; i += groups) {
-      const float4 x = *reinterpret_cast<const float4*>(Parts(p, sg.slot + i, h).o + r * p.D + d);
-      const float f = s_f[i];
-      v.x += x.x * f, v.y += x.y * f, v.z += x.z * f, v.w += x.w * f;
+      const Parts part(p, sg.slot + i, h);
+      add(*reinterpret_cast<const float2*>(part.ml + 2 * r), *reinterpret_cast<const float4*>(part.o + r * p.D + 4 * lane));
     }
-  s_o[threadIdx.x] = v;
-  __syncthreads();
-  if (threadIdx.x >= lanes) return;
-  for (int i = 1; i < groups; ++i) {
-    const float4 x = s_o[i * lanes + threadIdx.x];
-    v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+  if (groups > 1) {
+    s_o[threadIdx.x] = v;
+    s_ml[threadIdx.x] = make_float2(m, l);
+    __syncthreads();
   }
+  if (!mine || group > 0) return;
+  for (int i = 1; i < groups; ++i) add(s_ml[threadIdx.x + i * lanes], s_o[threadIdx.x + i * lanes]);
   const int t = at / p.G;
-  float f = total == 0.0f ? 0.0f : (FP8 && p.v_scale ? p.v_scale[h] : 1.0f) / total;
+  float f = l == 0.0f ? 0.0f : (FP8 && p.v_scale ? p.v_scale[h] : 1.0f) / l;
   if (sg.seq.position(t) >= sg.seq.cap) f = NAN;
-  uint16_t* to = p.out + (sg.seq.row0 + t) * p.o_row + (h * p.G + at - t * p.G) * p.o_head + d;
+  uint16_t* to = p.out + (sg.seq.row0 + t) * p.o_row + (h * p.G + at - t * p.G) * p.o_head + 4 * lane;
   *reinterpret_cast<uint2*>(to) = make_uint2(bf16x2(v.x * f, v.y * f), bf16x2(v.z * f, v.w * f));
 }
 
-int64_t tiles_bound(int T, int B, int G) { return ((int64_t)T * G + kRows - 1) / kRows + (B < T ? B : T); }
-
-template <int D, bool FP8>
+template <int D, bool FP8, bool WHOLE>
 hipError_t launch(const KvAttnArgs& a, hipStream_t stream) {
   using F = Few<D, FP8>;
-  const int64_t tiles = tiles_bound(a.batch.T, a.batch.B, a.G);
+  const CacheBatchArgs& b = a.batch;
+  const int64_t tiles = ((int64_t)b.T * a.G + kRows - 1) / kRows + (b.B < b.T ? b.B : b.T);   // at most
   // each tile one segment, and as many more as the work has whole segments
   const int64_t groups = (tiles + (kTarget + a.Hkv - 1) / a.Hkv) * a.Hkv;
   const size_t lds = (size_t)kWaves * kRows * (D + 4 + 2) * sizeof(float);
   static std::atomic<uint64_t> done{0};
   if (lds > 65536) {
-    const hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(few_kernel<D, FP8>), (int)lds, done);
+    const hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(few_kernel<D, FP8, WHOLE>), (int)lds, done);
     if (e != hipSuccess) return e;
   }
-  few_kernel<D, FP8><<<dim3((unsigned)groups), kWaves * kWave, lds, stream>>>(a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  few_join_kernel<FP8><<<dim3((unsigned)(tiles * a.Hkv * kRows)), kJoinThreads, 0, stream>>>(a, F::kBlockLog);
+  few_kernel<D, FP8, WHOLE><<<dim3((unsigned)groups), kWaves * kWave, lds, stream>>>(a);
+  const hipError_t e = hipGetLastError();
+  // the blocks that a sequence can have
+  if (e != hipSuccess || ((int64_t)b.cols << b.page_log >> F::kBlockLog) < kSplitBlocks) return e;
+  // rows that a workgroup joins: one, or as many as its threads hold where that leaves a few workgroups a CU
+  int together = 1;
+  while (together * 2 * (D / 4) <= kJoinThreads && tiles * a.Hkv * (kRows / (2 * together)) >= 1024) together *= 2;
+  few_join_kernel<FP8><<<dim3((unsigned)(tiles * a.Hkv * (kRows / together))), kJoinThreads, 0, stream>>>(a, F::kBlockLog, together);
   return hipGetLastError();
+}
+
+template <int D, bool FP8>
+hipError_t launch_w(const KvAttnArgs& a, hipStream_t stream) {
+  return a.batch.page_log >= Few<D, FP8>::kBlockLog ? launch<D, FP8, true>(a, stream) : launch<D, FP8, false>(a, stream);
 }
 
 template <bool FP8>
 hipError_t launch_d(const KvAttnArgs& a, hipStream_t stream) {
   switch (a.D / 32) {
-    case 1: return launch<32, FP8>(a, stream);
-    case 2: return launch<64, FP8>(a, stream);
-    case 3: return launch<96, FP8>(a, stream);
-    case 4: return launch<128, FP8>(a, stream);
-    case 5: return launch<160, FP8>(a, stream);
-    case 6: return launch<192, FP8>(a, stream);
-    case 7: return launch<224, FP8>(a, stream);
-    case 8: return launch<256, FP8>(a, stream);
+    case 1: return launch_w<32, FP8>(a, stream);
+    case 2: return launch_w<64, FP8>(a, stream);
+    case 3: return launch_w<96, FP8>(a, stream);
+    case 4: return launch_w<128, FP8>(a, stream);
+    case 5: return launch_w<160, FP8>(a, stream);
+    case 6: return launch_w<192, FP8>(a, stream);
+    case 7: return launch_w<224, FP8>(a, stream);
+    case 8: return launch_w<256, FP8>(a, stream);
   }
   return hipErrorInvalidValue;
 }
 
 }  // namespace
+
+// Up to 16 rows (token, head of the group) a sequence on average. Tiles of 32 and 64 rows here, one wave a
+// SIMD for their sums, were slower than the tiles of 128 rows with most of them empty: 16 sequences of 4
+// tokens over 8000 keys (64 heads of 8 groups, D 128, bf16) 155 / 126 us, of 8 tokens 262 / 129 us.
+bool kv_attention_few_fits(int T, int B, int G) { return (int64_t)T * G <= (int64_t)kRows * B; }
 
 // A tile has more than one segment only from 1.5 times a whole segment's keys on, so the segments of
 // such tiles are at most 4 / 3 as many as the work has whole segments.

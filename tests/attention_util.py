@@ -76,9 +76,9 @@ class Case:
         self.starts = starts
         self.batch = ops.CacheBatch(dv(table), dv(torch.tensor(total, dtype=torch.int32)), dv(torch.tensor(starts, dtype=torch.int32)))
 
-    def few(self):
-        """Whether the mean rows of a sequence go to the tiles of 16 rows."""
-        return self.q.shape[0] * (self.Hq // self.Hkv) <= 16 * len(self.new)
+    def rows(self):
+        """Rows (token, head of the group) of a sequence, on average."""
+        return self.q.shape[0] * (self.Hq // self.Hkv) / len(self.new)
 
     def attention(self, scale=None, window=0):
         """float64 outputs of the new tokens' rows, and how far each may be off."""
@@ -86,7 +86,7 @@ class Case:
         G = self.Hq // self.Hkv
         out = torch.zeros((self.T, self.Hq, self.D), dtype=torch.float64)
         tol = torch.zeros_like(out)
-        weight_step = 2.0 ** -15 if self.few() else 2.0 ** -8
+        weight_step = 2.0 ** -15 if self.rows() <= 16 else 2.0 ** -8
         for b, (n, c) in enumerate(zip(self.new, self.ctx)):
             if n == 0 or self.total[b] == 0:
                 continue
