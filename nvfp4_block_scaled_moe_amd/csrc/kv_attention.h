@@ -15,12 +15,12 @@ typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.44269504088896341f;
 
-// One sequence's new tokens, and the blocks of keys that any of them sees.
+// One sequence's new tokens.
 struct Sequence {
   int row0, n;       // first row, new tokens (rows within the tensor only)
   int len;           // tokens, the new ones among them
   int cap;           // keys that the page table has columns for
-  int block0, blocks;
+  int blocks;        // of the keys that any of them sees
   // Position of new token i, and the first key that it sees.
   __device__ __forceinline__ int position(int i) const { return len - n + i; }
 };
@@ -34,8 +34,7 @@ __device__ __forceinline__ Sequence sequence_of(const CacheBatchArgs& b, int win
   q.len = max(len, 0);
   q.cap = (int)min((int64_t)b.cols << b.page_log, (int64_t)0x7fffff00);
   const int last = min(q.len, q.cap), first = window > 0 ? max(q.len - q.n + 1 - window, 0) : 0;
-  q.block0 = first >> block_log;
-  q.blocks = max(((last + (1 << block_log) - 1) >> block_log) - q.block0, 0);
+  q.blocks = max(((last + (1 << block_log) - 1) >> block_log) - (first >> block_log), 0);
   return q;
 }
 
@@ -64,6 +63,166 @@ __device__ __forceinline__ int64_t wave_sum(int64_t v) {
   const int hi = __builtin_amdgcn_readlane(wave_scan((int)(v >> 24)), kWave - 1);
   return ((int64_t)hi << 24) + lo;
 }
+
+// How the work is divided. Rows (token, head of a group) of a sequence and key head are taken in tiles, their
+// keys in blocks; the tiles of a sequence are split into as many parts each as its blocks are whole segments,
+// rounded, a segment being the target's share of all blocks of all tiles (counted as if every tile saw what its
+// sequence sees), or min_blocks. Every wave finds its segment by itself from the lengths: they are known
+// on the device alone, and a launch that lists the segments costs more (6 to 9 us).
+struct Division {
+  int tile_rows, block_log;
+  int target;       // segments that the work is divided into
+  int min_blocks;   // least blocks of one
+  int step;         // parts are multiples of it
+  // A sequence is split from 1.5 segments on, so at most 2 / 3 of the target's tiles are split, into at
+  // most 4 / 3 of its segments; all segments are at most the tiles and the target.
+  __host__ __device__ constexpr int split_blocks() const { return min_blocks + min_blocks / 2; }
+  int64_t tiles(int T, int B, int G) const { return ((int64_t)T * G + tile_rows - 1) / tile_rows + (B < T ? B : T); }
+  int64_t whole(int Hkv) const { return (target + Hkv - 1) / Hkv; }   // of the target, heads aside
+  int64_t segments(int T, int B, int Hkv, int G) const { return tiles(T, B, G) + whole(Hkv); }
+  int64_t split_tiles(int T, int B, int Hkv, int G) const {
+    const int64_t n = tiles(T, B, G), w = whole(Hkv);
+    return n < w ? n : w;
+  }
+  size_t ws_bytes(int Hkv, int D) const { return (size_t)(4 * whole(Hkv) / 3 + 1) * Hkv * tile_rows * (D + 2) * sizeof(float); }
+};
+// Whether any sequence can be split: the page table bounds their lengths.
+inline bool can_split(const Division& v, const CacheBatchArgs& b) {
+  return ((int64_t)b.cols << b.page_log >> v.block_log) >= v.split_blocks();
+}
+
+struct Segment {
+  Sequence seq;
+  int s, tile;            // the sequence, its row tile
+  int parts, part;        // of the tile's keys
+  int slot;               // place of this part's sums, where parts > 1 (heads aside)
+  int block0, blocks;     // this part's keys
+  bool found;
+};
+// Segment `at` (heads aside), or with SPLIT tile `at` of those that are split (part 0).
+template <bool SPLIT>
+__device__ __forceinline__ Segment segment_of(const KvAttnArgs& p, const Division& v, int at) {
+  const CacheBatchArgs& b = p.batch;
+  const int lane = threadIdx.x % kWave;   // a lane a sequence
+  auto tiles_of = [&](const Sequence& q) { return (int)(((int64_t)q.n * p.G + v.tile_rows - 1) / v.tile_rows); };
+  Sequence mine{};
+  int64_t work = 0;
+  for (int s0 = 0; s0 < b.B; s0 += kWave) {
+    const int s = s0 + lane;
+    if (s < b.B) {
+      mine = sequence_of(b, p.window, s, v.block_log);
+      work += (int64_t)tiles_of(mine) * mine.blocks;
+    }
+  }
+  work = wave_sum(work) * p.Hkv;
+  const int64_t even = (work + v.target - 1) / v.target;
+  const int chunk = (int)min((even > v.min_blocks ? even : v.min_blocks), (int64_t)1 << 30);
+  Segment r{};
+  int before = 0, slots = 0;
+  for (int s0 = 0; s0 < b.B; s0 += kWave) {
+    const int s = s0 + lane;
+    if (b.B > kWave) mine = s < b.B ? sequence_of(b, p.window, s, v.block_log) : Sequence{};
+    const int tiles = s < b.B ? tiles_of(mine) : 0, parts = max((int)(((int64_t)mine.blocks + chunk / 2) / chunk), 1);
+    const int split = parts > 1 ? tiles * parts : 0, count = SPLIT ? (parts > 1 ? tiles : 0) : tiles * parts;
+    const int upto = wave_scan(count), split_upto = wave_scan(split);
+    const uint64_t hit = __ballot(before + upto > at);
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      auto get = [&](int x) { return __builtin_amdgcn_readlane(x, l); };
+      r.seq = {get(mine.row0), get(mine.n), get(mine.len), get(mine.cap), get(mine.blocks)};
+      r.s = s0 + l;
+      r.parts = get(parts);
+      const int in = at - before - (get(upto) - get(count)), nth = SPLIT ? in : in / r.parts;
+      r.part = SPLIT ? 0 : in - nth * r.parts;
+      r.tile = get(tiles) - 1 - nth;   // (the later ones, which see the most, first)
+      r.slot = slots + get(split_upto) - get(split) + nth * r.parts + r.part;
+      // the blocks that the tile's rows see
+      const int t0 = (int)((int64_t)r.tile * v.tile_rows / p.G);
+      const int t1 = min((int)(((int64_t)r.tile * v.tile_rows + v.tile_rows - 1) / p.G), r.seq.n - 1);
+      const Seen a = seen_by(r.seq.position(t0), p.window, r.seq.cap), z = seen_by(r.seq.position(t1), p.window, r.seq.cap);
+      r.block0 = a.lo >> v.block_log;
+      r.blocks = max(((z.hi + (1 << v.block_log) - 1) >> v.block_log) - r.block0, 0);
+      if (!SPLIT) {
+        const int per = ((r.blocks + r.parts - 1) / r.parts + v.step - 1) / v.step * v.step;
+        r.block0 += r.part * per;
+        r.blocks = max(min(per, r.blocks - r.part * per), 0);   // (the last parts may have none)
+      }
+      r.found = true;
+      return r;
+    }
+    before += __builtin_amdgcn_readlane(upto, kWave - 1);
+    slots += __builtin_amdgcn_readlane(split_upto, kWave - 1);
+  }
+  return r;
+}
+
+// Sums of a part in the workspace: [slot, head] of [tile_rows, D] unnormalised outputs, then of
+// [tile_rows] maxima (of base 2 logits) and sums.
+struct Sums {
+  float* o;
+  float* ml;
+  __device__ __forceinline__ Sums(const KvAttnArgs& p, const Division& v, int64_t slot, int h) {
+    const int64_t i = slot * p.Hkv + h;
+    o = static_cast<float*>(p.ws) + i * v.tile_rows * (p.D + 2);
+    ml = o + v.tile_rows * p.D;
+  }
+};
+
+// Joins the parts of a tile: a workgroup `together` of its rows for one head, of which each thread holds 4 dims
+// of every groups-th part; in a fixed order.
+constexpr int kJoinThreads = 256;
+namespace {   // (a kernel of each file's own)
+template <bool FP8>
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(const KvAttnArgs p, const Division v, int together) {
+  __shared__ float4 s_o[kJoinThreads];
+  __shared__ float2 s_ml[kJoinThreads];
+  const int sets = v.tile_rows / together, h = blockIdx.x / sets % p.Hkv;
+  const Segment sg = segment_of<true>(p, v, blockIdx.x / sets / p.Hkv);
+  if (!sg.found) return;
+  const int lanes = p.D / 4, groups = kJoinThreads / (lanes * together);
+  const int lane = threadIdx.x % lanes, group = threadIdx.x / lanes % groups, r = blockIdx.x % sets * together + threadIdx.x / (lanes * groups);
+  const int rows = sg.seq.n * p.G, at = sg.tile * v.tile_rows + r;
+  if (sg.tile * v.tile_rows + blockIdx.x % sets * together >= rows) return;
+  const bool mine = (int)threadIdx.x < lanes * groups * together && at < rows;
+  float m = -INFINITY, l = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  auto add = [&](float2 ml, float4 x) {
+    const float next = fmaxf(m, ml.x), base = next == -INFINITY ? 0.0f : next;
+    const float f = __builtin_amdgcn_exp2f(m - base), e = ml.x == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(ml.x - base);
+    m = next;
+    l = l * f + ml.y * e;
+    o.x = o.x * f + x.x * e, o.y = o.y * f + x.y * e, o.z = o.z * f + x.z * e, o.w = o.w * f + x.w * e;
+  };
+  if (mine)
+#pragma unroll 4
+    for (int i = group; i < sg.parts; i += groups) {
+      const Sums part(p, v, sg.slot + i, h);
+      add(*reinterpret_cast<const float2*>(part.ml + 2 * r), *reinterpret_cast<const float4*>(part.o + r * p.D + 4 * lane));
+    }
+  if (groups > 1) {
+    s_o[threadIdx.x] = o;
+    s_ml[threadIdx.x] = make_float2(m, l);
+    __syncthreads();
+  }
+  if (!mine || group > 0) return;
+  for (int i = 1; i < groups; ++i) add(s_ml[threadIdx.x + i * lanes], s_o[threadIdx.x + i * lanes]);
+  const int t = at / p.G;
+  float f = l == 0.0f ? 0.0f : (FP8 && p.v_scale ? p.v_scale[h] : 1.0f) / l;
+  if (sg.seq.position(t) >= sg.seq.cap) f = NAN;
+  uint16_t* to = p.out + (sg.seq.row0 + t) * p.o_row + (h * p.G + at - t * p.G) * p.o_head + 4 * lane;
+  *reinterpret_cast<uint2*>(to) = make_uint2(bf16x2(o.x * f, o.y * f), bf16x2(o.z * f, o.w * f));
+}
+template <bool FP8>
+hipError_t launch_join(const KvAttnArgs& a, const Division& v, hipStream_t stream) {
+  if (!can_split(v, a.batch)) return hipSuccess;
+  const int64_t tiles = v.split_tiles(a.batch.T, a.batch.B, a.Hkv, a.G);
+  // rows that a workgroup joins: one, or as many as its threads hold where that leaves a few workgroups a CU
+  int together = 1;
+  while (together * 2 * (a.D / 4) <= kJoinThreads && tiles * a.Hkv * (v.tile_rows / (2 * together)) >= 1024) together *= 2;
+  join_kernel<FP8><<<dim3((unsigned)(tiles * a.Hkv * (v.tile_rows / together))), kJoinThreads, 0, stream>>>(a, v, together);
+  return hipGetLastError();
+}
+}  // namespace
 
 // Four E4M3 bytes as bf16 (exact).
 __device__ __forceinline__ u32x2 e4m3x4_to_bf16(uint32_t w) {

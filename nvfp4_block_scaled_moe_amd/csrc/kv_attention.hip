@@ -17,9 +17,8 @@
 // Their sum is taken before that rounding. The running maximum is moved only when a score exceeds it
 // by 2^8: until then weights of up to 2^8 keep their relative precision.
 //
-// The rows' tiles and their blocks of keys are listed on the device by a first launch (lengths are
-// known there alone), tiles with many blocks in equal segments, which a last launch joins in a
-// fixed order.
+// The work is divided as Division says; where a tile is split, its parts leave unnormalised sums, which a
+// second launch joins.
 #include <type_traits>
 
 #include "gemm_common.h"
@@ -32,163 +31,8 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kRows = 32 * kWaves;    // rows of a tile
 constexpr int kBlockLog = 6, kBlock = 1 << kBlockLog;   // keys of a block
-constexpr int kTarget = 1024;         // segments that the work is divided into
-constexpr int kMinBlocks = 4;         // least blocks of a segment
+constexpr Division kDivision = {kRows, kBlockLog, 1024, 8, 1};
 
-// What the first launch leaves in the workspace.
-struct Header {
-  int segments, splits;   // entries of the two lists
-  int pad[2];
-};
-struct PlanTile {       // one row tile of a sequence (heads aside)
-  int seq, tile, parts, slot;
-};
-struct PlanSegment {    // blocks [block0, block0 + blocks) of a tile
-  int tile, part, block0, blocks;
-};
-int64_t tiles_bound(int T, int B, int G) { return ((int64_t)T * G + kRows - 1) / kRows + (B < T ? B : T); }
-struct PlanLayout {
-  int64_t tiles, segments, splits;   // most of each
-  size_t at_tiles, at_segments, at_splits, at_first, at_sums, total;
-  PlanLayout(int T, int B, int Hkv, int G, int D) {
-    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    const int64_t whole = (kTarget + Hkv - 1) / Hkv;   // whole segments of the work, heads aside
-    tiles = tiles_bound(T, B, G);
-    segments = tiles + whole;
-    splits = tiles < whole ? tiles : whole;
-    at_tiles = up(sizeof(Header));
-    at_segments = at_tiles + up((size_t)tiles * sizeof(PlanTile));
-    at_splits = at_segments + up((size_t)segments * sizeof(PlanSegment));
-    at_first = at_splits + up((size_t)splits * 4);
-    at_sums = at_first + up((size_t)(B + 1) * 4);
-    // a tile in parts has 1.5 times the blocks of a whole segment or more: its parts are at most 4 / 3 of its whole segments
-    const int64_t slots = 2 * whole < segments ? 2 * whole : segments;
-    total = at_sums + (size_t)slots * Hkv * kRows * (D + 2) * sizeof(float);
-  }
-};
-struct Plan {
-  Header* head;
-  PlanTile* tiles;
-  PlanSegment* segments;
-  int* splits;      // tiles in parts
-  int* first;       // [B + 1] first tile of each sequence
-  float* sums;      // [slot, head] of [kRows, D] outputs, then [kRows, 2] maxima and sums
-  int max_tiles, max_segments, max_splits;
-};
-Plan plan_of(void* ws, const PlanLayout& l) {
-  char* p = static_cast<char*>(ws);
-  return {reinterpret_cast<Header*>(p),        reinterpret_cast<PlanTile*>(p + l.at_tiles), reinterpret_cast<PlanSegment*>(p + l.at_segments),
-          reinterpret_cast<int*>(p + l.at_splits), reinterpret_cast<int*>(p + l.at_first), reinterpret_cast<float*>(p + l.at_sums),
-          (int)l.tiles, (int)l.segments, (int)l.splits};
-}
-
-// ---------------------------------------------------------------- the list
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanWaves = kPlanThreads / kWave;
-
-// Exclusive sum over the workgroup (and its total).
-__device__ __forceinline__ int block_scan(int v, int& total, int* s_wave) {
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  const int upto = wave_scan(v);
-  __syncthreads();   // (s_wave may still be read)
-  if (lane == kWave - 1) s_wave[wave] = upto;
-  __syncthreads();
-  int before = 0;
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < kPlanWaves; ++w) {
-    before += w < wave ? s_wave[w] : 0;
-    total += s_wave[w];
-  }
-  return before + upto - v;
-}
-
-// The blocks that the rows of a tile see.
-__device__ __forceinline__ void tile_blocks(const KvAttnArgs& p, const Sequence& q, int tile, int& block0, int& blocks) {
-  const int t0 = (int)((int64_t)tile * kRows / p.G), t1 = min((int)(((int64_t)tile * kRows + kRows - 1) / p.G), q.n - 1);
-  const Seen a = seen_by(q.position(t0), p.window, q.cap), z = seen_by(q.position(t1), p.window, q.cap);
-  block0 = a.lo >> kBlockLog;
-  blocks = max(((z.hi + kBlock - 1) >> kBlockLog) - block0, 0);
-}
-
-__global__ __launch_bounds__(kPlanThreads) void plan_kernel(const KvAttnArgs p, const Plan plan) {
-  __shared__ int s_wave[kPlanWaves];
-  __shared__ int64_t s_work[kPlanWaves];
-  const CacheBatchArgs& b = p.batch;
-  const int tid = threadIdx.x;
-  auto tiles_of = [&](const Sequence& q) { return (int)(((int64_t)q.n * p.G + kRows - 1) / kRows); };
-  int tiles = 0;
-  for (int s0 = 0; s0 < b.B; s0 += kPlanThreads) {
-    const int s = s0 + tid;
-    const int n = s < b.B ? tiles_of(sequence_of(b, p.window, s, kBlockLog)) : 0;
-    int total;
-    const int before = block_scan(n, total, s_wave);
-    if (s < b.B) plan.first[s] = tiles + before;
-    tiles += total;
-  }
-  if (tid == 0) plan.first[b.B] = tiles;
-  __threadfence_block();
-  __syncthreads();
-  tiles = min(tiles, plan.max_tiles);   // (starts that overlap would give more)
-  // The sequence of tile i, the later tiles of a sequence (which see the most) first, and their blocks.
-  auto tile_at = [&](int i, int& s, int& tile, int& block0, int& blocks) {
-    int lo = 0, hi = b.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (plan.first[mid] <= i)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    s = lo;
-    const Sequence q = sequence_of(b, p.window, s, kBlockLog);
-    tile = plan.first[s + 1] - 1 - i;
-    tile_blocks(p, q, tile, block0, blocks);
-  };
-  int64_t work = 0;
-  for (int i = tid; i < tiles; i += kPlanThreads) {
-    int s, tile, block0, blocks;
-    tile_at(i, s, tile, block0, blocks);
-    work += blocks;
-  }
-  work = wave_sum(work);
-  if (tid % kWave == 0) s_work[tid / kWave] = work;
-  __syncthreads();
-  work = 0;
-  for (int w = 0; w < kPlanWaves; ++w) work += s_work[w];
-  const int64_t even = (work * p.Hkv + kTarget - 1) / kTarget;
-  const int chunk = (int)(even > kMinBlocks ? even : kMinBlocks);
-  int segments = 0, slots = 0, splits = 0;
-  for (int i0 = 0; i0 < tiles; i0 += kPlanThreads) {
-    const int i = i0 + tid;
-    int s = 0, tile = 0, block0 = 0, blocks = 0, parts = 0;
-    if (i < tiles) {
-      tile_at(i, s, tile, block0, blocks);
-      parts = max((blocks + chunk / 2) / chunk, 1);   // (parts of equal sizes, near a whole segment's)
-    }
-    int n_segments, n_slots, n_splits;
-    const int first = segments + block_scan(parts, n_segments, s_wave);
-    const int slot = slots + block_scan(parts > 1 ? parts : 0, n_slots, s_wave);
-    const int split = splits + block_scan(parts > 1 ? 1 : 0, n_splits, s_wave);
-    if (i < tiles) {
-      plan.tiles[i] = {s, tile, parts, slot};
-      const int per = (blocks + parts - 1) / parts;
-      for (int j = 0; j < parts; ++j)
-        if (first + j < plan.max_segments)
-          plan.segments[first + j] = {i, j, block0 + j * per, min(per, blocks - j * per)};   // (the last may be empty)
-      if (parts > 1 && split < plan.max_splits) plan.splits[split] = i;
-    }
-    segments += n_segments;
-    slots += n_slots;
-    splits += n_splits;
-  }
-  if (tid == 0) {
-    plan.head->segments = min(segments, plan.max_segments);
-    plan.head->splits = min(splits, plan.max_splits);
-  }
-}
-
-// ---------------------------------------------------------------- the tiles
 // 16 bytes a lane straight into LDS (lane l at lds + 16 l), from global memory or from a buffer (whose base
 // and offset `soff` are the wave's: no address arithmetic in the lanes).
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, char* lds, uint32_t voff, uint32_t soff) {
@@ -225,25 +69,24 @@ struct Chunk {
 __device__ __forceinline__ int key_of_row(int r) { return r / 4 % 2 * 8 + r / 8 * 4 + r % 4; }
 
 template <int D, bool FP8>
-__global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(const KvAttnArgs p, const Plan plan) {
+__global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(const KvAttnArgs p) {
   using C = Chunk<D, FP8>;
   extern __shared__ __attribute__((aligned(16))) char smem[];   // two of: keys [64, D], values [D, 64]
   const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int col = lane % 32, half = lane / 32;
-  const int h = blockIdx.x % p.Hkv, at = blockIdx.x / p.Hkv;
-  if (at >= plan.head->segments) return;
-  const PlanSegment sg = plan.segments[at];
-  const PlanTile tl = plan.tiles[sg.tile];
+  const int h = blockIdx.x % p.Hkv;
+  const Segment sg = segment_of<false>(p, kDivision, blockIdx.x / p.Hkv);
+  if (!sg.found) return;
   const CacheBatchArgs& b = p.batch;
-  const Sequence seq = sequence_of(b, p.window, tl.seq, kBlockLog);
+  const Sequence& seq = sg.seq;
 
   // This lane's row, and the keys that it sees; those that all rows of the tile see; those that any of this
   // wave's rows sees.
-  const int rows = seq.n * p.G, row0 = tl.tile * kRows + 32 * wave;
+  const int rows = seq.n * p.G, row0 = sg.tile * kRows + 32 * wave;
   const int row = min(row0 + col, rows - 1), token = row / p.G, head = h * p.G + row - token * p.G;
   const Seen mine = seen_by(seq.position(token), p.window, seq.cap);
   auto seen_of = [&](int r) { return seen_by(seq.position(min(r, rows - 1) / p.G), p.window, seq.cap); };
-  const int all_lo = seen_of(tl.tile * kRows + kRows - 1).lo, all_hi = seen_of(tl.tile * kRows).hi;
+  const int all_lo = seen_of(sg.tile * kRows + kRows - 1).lo, all_hi = seen_of(sg.tile * kRows).hi;
   const int any_lo = seen_of(row0).lo, any_hi = row0 < rows ? seen_of(row0 + 31).hi : 0;
 
   bf16x8 q[C::kSteps];
@@ -259,7 +102,7 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
   constexpr int kSize = FP8 ? 1 : 2;
   const int page = b.page, page_mask = page - 1;
   const int64_t head_bytes = (int64_t)page * D * kSize;
-  const int* table = b.page_table + tl.seq * b.ld_table;
+  const int* table = b.page_table + sg.s * b.ld_table;
   // (bf16: a load is 8 rows of V^T, whose swizzle is the lane's and, in every second load, 4: the lane's word
   // is then one of the block's other half)
   const int v_word = FP8 ? lane % 4 : (lane % 8) ^ (lane / 16);       // of the 4 or 8 words of a row of V^T
@@ -508,17 +351,17 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
   }
   if (row0 + col >= rows) return;
   // this lane: dims 32 d + 8 (i / 4) + 4 half + i % 4 of its row
-  if (tl.parts > 1) {
-    float* sums = plan.sums + ((int64_t)(tl.slot + sg.part) * p.Hkv + h) * kRows * (D + 2);
+  if (sg.parts > 1) {
+    const Sums part(p, kDivision, sg.slot, h);
     const int r = 32 * wave + col;
 #pragma unroll
     for (int d = 0; d < C::kDTiles; ++d)
 #pragma unroll
       for (int i = 0; i < 16; i += 4)
-        *reinterpret_cast<float4*>(sums + r * D + 32 * d + 2 * i + 4 * half) = make_float4(o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]);
+        *reinterpret_cast<float4*>(part.o + r * D + 32 * d + 2 * i + 4 * half) = make_float4(o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]);
     if (half == 0) {
-      sums[kRows * D + 2 * r] = m;
-      sums[kRows * D + 2 * r + 1] = l;
+      part.ml[2 * r] = m;
+      part.ml[2 * r + 1] = l;
     }
   } else {
     float f = l == 0.0f ? 0.0f : (FP8 && p.v_scale ? p.v_scale[h] : 1.0f) / l;
@@ -533,57 +376,18 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
   }
 }
 
-// Joins the parts of tiles that have more than one: a workgroup a few rows of a tile and head.
-constexpr int kJoinThreads = 256, kJoinRows = 16;
-template <bool FP8>
-__global__ __launch_bounds__(kJoinThreads) void join_kernel(const KvAttnArgs p, const Plan plan) {
-  constexpr int kGroups = kRows / kJoinRows;
-  const int at = blockIdx.x / (kGroups * p.Hkv), h = blockIdx.x / kGroups % p.Hkv, D = p.D;
-  if (at >= plan.head->splits) return;
-  const PlanTile tl = plan.tiles[plan.splits[at]];
-  const Sequence seq = sequence_of(p.batch, p.window, tl.seq, kBlockLog);
-  const float v_scale = FP8 && p.v_scale ? p.v_scale[h] : 1.0f;
-  for (int i = threadIdx.x; i < kJoinRows * (D / 4); i += kJoinThreads) {
-    const int r = blockIdx.x % kGroups * kJoinRows + i / (D / 4), d = i % (D / 4) * 4, row = tl.tile * kRows + r;
-    if (row >= seq.n * p.G) continue;
-    float m = -INFINITY, l = 0.0f;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int j = 0; j < tl.parts; ++j) {
-      const float* sums = plan.sums + ((int64_t)(tl.slot + j) * p.Hkv + h) * kRows * (D + 2);
-      const float2 ml = *reinterpret_cast<const float2*>(sums + kRows * D + 2 * r);
-      const float4 x = *reinterpret_cast<const float4*>(sums + r * D + d);
-      const float next = fmaxf(m, ml.x), base = next == -INFINITY ? 0.0f : next;
-      const float f = __builtin_amdgcn_exp2f(m - base), g = ml.x == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(ml.x - base);
-      m = next;
-      l = l * f + ml.y * g;
-      v.x = v.x * f + x.x * g, v.y = v.y * f + x.y * g, v.z = v.z * f + x.z * g, v.w = v.w * f + x.w * g;
-    }
-    const int token = row / p.G;
-    float f = l == 0.0f ? 0.0f : v_scale / l;
-    if (seq.position(token) >= seq.cap) f = NAN;
-    uint16_t* to = p.out + (seq.row0 + token) * p.o_row + (h * p.G + row - token * p.G) * p.o_head + d;
-    *reinterpret_cast<uint2*>(to) = make_uint2(bf16x2(v.x * f, v.y * f), bf16x2(v.z * f, v.w * f));
-  }
-}
-
 template <int D, bool FP8>
 hipError_t launch(const KvAttnArgs& a, hipStream_t stream) {
-  const PlanLayout l(a.batch.T, a.batch.B, a.Hkv, a.G, D);
-  const Plan plan = plan_of(a.ws, l);
   constexpr int lds = 4 * Chunk<D, FP8>::kBytes;
   static std::atomic<uint64_t> done{0};
   if (lds > 65536) {
     const hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(chunk_kernel<D, FP8>), lds, done);
     if (e != hipSuccess) return e;
   }
-  plan_kernel<<<dim3(1), kPlanThreads, 0, stream>>>(a, plan);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  chunk_kernel<D, FP8><<<dim3((unsigned)(l.segments * a.Hkv)), kWaves * kWave, lds, stream>>>(a, plan);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  join_kernel<FP8><<<dim3((unsigned)(l.splits * a.Hkv * (kRows / kJoinRows))), kJoinThreads, 0, stream>>>(a, plan);
-  return hipGetLastError();
+  const int64_t groups = kDivision.segments(a.batch.T, a.batch.B, a.Hkv, a.G) * a.Hkv;
+  chunk_kernel<D, FP8><<<dim3((unsigned)groups), kWaves * kWave, lds, stream>>>(a);
+  const hipError_t e = hipGetLastError();
+  return e != hipSuccess ? e : launch_join<FP8>(a, kDivision, stream);
 }
 
 template <bool FP8>
@@ -604,8 +408,8 @@ hipError_t launch_d(const KvAttnArgs& a, hipStream_t stream) {
 }  // namespace
 
 size_t kv_attention_ws_bytes(int T, int B, int Hq, int Hkv, int D) {
-  if (kv_attention_few_fits(T, B, Hq / Hkv)) return kv_attention_few_ws_bytes(Hkv, D);
-  return PlanLayout(T, B, Hkv, Hq / Hkv, D).total;
+  const int G = Hq / Hkv;
+  return kv_attention_few_fits(T, B, G) ? kv_attention_few_ws_bytes(Hkv, D) : kDivision.ws_bytes(Hkv, D);
 }
 
 hipError_t launch_kv_attention(const KvAttnArgs& a, hipStream_t stream) {

@@ -12,10 +12,8 @@
 // Weights of the second product are two bf16 values each (the rounded exponential, and the rest), so
 // that they count as 16 bits; the matrix cores have the time. Running maxima and sums are float32.
 //
-// The work (blocks of keys over all sequences, tiles and heads) is divided into equal segments on the
-// device, from the lengths, which the host does not know; a workgroup of four waves takes one
-// segment, its waves every fourth block. Where a tile has more than one segment, they leave
-// unnormalised sums, which a second launch joins in a fixed order.
+// The work is divided as Division says; a workgroup of four waves takes one segment, its waves every fourth
+// block. Where a tile is split, its parts leave unnormalised sums, which a second launch joins.
 #include "gemm_common.h"
 #include "kv_attention.h"
 
@@ -25,85 +23,13 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kRows = 16;          // rows of a tile
-constexpr int kTarget = 1024;      // segments that the work is divided into
-// Least blocks of a segment: joining costs a second launch, so that a few blocks more a wave cost less.
-constexpr int kMinBlocks = 16;
-// Blocks from which a tile may be split (parts are rounded: 1.5 segments make two).
-constexpr int kSplitBlocks = kMinBlocks + kMinBlocks / 2;
-
-// The segment of workgroup `at` (over the tiles' segments, heads aside), found by every wave by itself.
-struct Segment {
-  Sequence seq;
-  int tile;               // row tile of the sequence
-  int block0, blocks;     // its keys
-  int parts, part;        // segments of its tile, which of them
-  int slot;               // place of its sums, where parts > 1
-  bool found;
-};
-__device__ __forceinline__ Segment segment_of(const KvAttnArgs& p, int block_log, int at, bool by_tile) {
-  // Work of all sequences, then the segments before each one: a lane a sequence.
-  const CacheBatchArgs& b = p.batch;
-  const int lane = threadIdx.x % kWave;
-  Sequence mine{};
-  int64_t work = 0;
-  for (int s0 = 0; s0 < b.B; s0 += kWave) {
-    const int s = s0 + lane;
-    if (s < b.B) {
-      mine = sequence_of(b, p.window, s, block_log);
-      work += (int64_t)((mine.n * p.G + kRows - 1) / kRows) * mine.blocks;
-    }
-  }
-  work = wave_sum(work) * p.Hkv;
-  const int64_t even = (work + kTarget - 1) / kTarget;
-  const int chunk = (int)(even > kMinBlocks ? (even + kWaves - 1) / kWaves * kWaves : kMinBlocks);
-  Segment r{};
-  int before = 0, slots = 0;
-  for (int s0 = 0; s0 < b.B; s0 += kWave) {
-    const int s = s0 + lane;
-    if (b.B > kWave) mine = s < b.B ? sequence_of(b, p.window, s, block_log) : Sequence{};
-    const int tiles = s < b.B ? (mine.n * p.G + kRows - 1) / kRows : 0;
-    const int parts = max((mine.blocks + chunk / 2) / chunk, 1), count = by_tile ? tiles : tiles * parts;
-    const int split = parts > 1 ? tiles * parts : 0;
-    const int upto = wave_scan(count), split_upto = wave_scan(split);
-    const uint64_t hit = __ballot(before + upto > at);
-    if (hit) {
-      const int l = __builtin_ctzll(hit);
-      auto get = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
-      r.seq = {get(mine.row0), get(mine.n), get(mine.len), get(mine.cap), get(mine.block0), get(mine.blocks)};
-      r.parts = get(parts);
-      const int in = at - before - (get(upto) - get(count));
-      r.tile = by_tile ? in : in / r.parts;
-      r.part = by_tile ? 0 : in - r.tile * r.parts;
-      r.slot = slots + get(split_upto) - get(split) + r.tile * r.parts + r.part;
-      const int per = ((r.seq.blocks + r.parts - 1) / r.parts + kWaves - 1) / kWaves * kWaves;
-      r.block0 = r.seq.block0 + r.part * per;
-      r.blocks = max(min(per, r.seq.blocks - r.part * per), 0);
-      r.found = true;
-      // (which sequence: its page table's row)
-      r.seq.block0 = s0 + l;
-      return r;
-    }
-    before += __builtin_amdgcn_readlane(upto, kWave - 1);
-    slots += __builtin_amdgcn_readlane(split_upto, kWave - 1);
-  }
-  return r;
-}
-
-// Sums of a segment in the workspace: [slot, head] of [kRows, D] unnormalised outputs, then of [kRows]
-// maxima (of base 2 logits) and sums.
-struct Parts {
-  float* o;
-  float* ml;
-  __device__ __forceinline__ Parts(const KvAttnArgs& p, int64_t slot, int h) {
-    const int64_t i = slot * p.Hkv + h;
-    o = static_cast<float*>(p.ws) + i * kRows * (p.D + 2);
-    ml = o + kRows * p.D;
-  }
-};
+// (Least blocks of a segment: joining costs a second launch, so that a few blocks more a wave cost less.)
+constexpr Division division(bool fp8) { return {kRows, fp8 ? 6 : 5, 1024, 16, kWaves}; }
 
 template <int D, bool FP8>
 struct Few {
-  static constexpr int kBlockLog = FP8 ? 6 : 5, kBlock = 1 << kBlockLog;   // keys of a block
+  static constexpr Division kDivision = division(FP8);
+  static constexpr int kBlockLog = kDivision.block_log, kBlock = 1 << kBlockLog;   // keys of a block
   static constexpr int kTiles = kBlock / 16;       // tiles of 16 keys in the first product
   static constexpr int kDSteps = D / 32;           // its steps
   static constexpr int kPSteps = kBlock / 32;      // steps of the second product
@@ -120,9 +46,8 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void few_kernel(con
   extern __shared__ float lds[];   // [kWaves, 16, D + 4] outputs, then [kWaves, 16, 2] maxima and sums
   const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), c = lane & 15, g = lane >> 4;
   const int h = blockIdx.x % p.Hkv;
-  const Segment sg = segment_of(p, F::kBlockLog, blockIdx.x / p.Hkv, false);
+  const Segment sg = segment_of<false>(p, F::kDivision, blockIdx.x / p.Hkv);
   if (!sg.found) return;
-  const int s = sg.seq.block0;
   const CacheBatchArgs& b = p.batch;
 
   // This lane's row: new token, query head, and the keys that it sees. (Rows behind the last one see
@@ -140,7 +65,7 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void few_kernel(con
   constexpr int kSize = FP8 ? 1 : 2;
   const int page = b.page, page_mask = page - 1;
   const int k_key = (F::kBlock / 4) * (c / 4) + c % 4, v_key = (F::kBlock / 4) * g;
-  const int* table = b.page_table + s * b.ld_table;
+  const int* table = b.page_table + sg.s * b.ld_table;
   const int64_t head_bytes = (int64_t)page * D * kSize;
   struct Pages {
     int k, v;   // of this lane's keys, and values (WHOLE: the same, and the wave's)
@@ -398,7 +323,7 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void few_kernel(con
       for (int w = 0; w < kWaves; ++w) v[j] += lds[(w * kRows + r) * kPitch + d + j] * factor[w];
     }
     if (sg.parts > 1) {
-      const Parts part(p, sg.slot, h);
+      const Sums part(p, F::kDivision, sg.slot, h);
       *reinterpret_cast<float4*>(part.o + r * D + d) = make_float4(v[0], v[1], v[2], v[3]);
       *reinterpret_cast<float4*>(part.o + r * D + d + 4) = make_float4(v[4], v[5], v[6], v[7]);
       if (d == 0) {
@@ -417,57 +342,10 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void few_kernel(con
   }
 }
 
-// Joins the segments of a tile: a workgroup a few rows of a tile and head, at a time `together` of them; a row's
-// threads hold 4 dims each of every groups-th segment.
-constexpr int kJoinThreads = 256;
-template <bool FP8>
-__global__ __launch_bounds__(kJoinThreads) void few_join_kernel(const KvAttnArgs p, int block_log, int together) {
-  __shared__ float4 s_o[kJoinThreads];
-  __shared__ float2 s_ml[kJoinThreads];
-  const int sets = kRows / together;
-  const int h = blockIdx.x / sets % p.Hkv;
-  const Segment sg = segment_of(p, block_log, blockIdx.x / sets / p.Hkv, true);
-  if (!sg.found || sg.parts < 2) return;
-  const int lanes = p.D / 4, groups = kJoinThreads / (lanes * together);
-  const int lane = threadIdx.x % lanes, group = threadIdx.x / lanes % groups, r = blockIdx.x % sets * together + threadIdx.x / (lanes * groups);
-  const int rows = sg.seq.n * p.G, at = sg.tile * kRows + r;
-  const bool mine = threadIdx.x < lanes * groups * together && at < rows;
-  float m = -INFINITY, l = 0.0f;
-  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  auto add = [&](float2 ml, float4 x) {
-    const float next = fmaxf(m, ml.x), base = next == -INFINITY ? 0.0f : next;
-    const float f = __builtin_amdgcn_exp2f(m - base), e = ml.x == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(ml.x - base);
-    m = next;
-    l = l * f + ml.y * e;
-    v.x = v.x * f + x.x * e, v.y = v.y * f + x.y * e, v.z = v.z * f + x.z * e, v.w = v.w * f + x.w * e;
-  };
-  if (mine)
-#pragma unroll 4
-    for (int i = group; i < sg.parts; i += groups) {
-      const Parts part(p, sg.slot + i, h);
-      add(*reinterpret_cast<const float2*>(part.ml + 2 * r), *reinterpret_cast<const float4*>(part.o + r * p.D + 4 * lane));
-    }
-  if (groups > 1) {
-    s_o[threadIdx.x] = v;
-    s_ml[threadIdx.x] = make_float2(m, l);
-    __syncthreads();
-  }
-  if (!mine || group > 0) return;
-  for (int i = 1; i < groups; ++i) add(s_ml[threadIdx.x + i * lanes], s_o[threadIdx.x + i * lanes]);
-  const int t = at / p.G;
-  float f = l == 0.0f ? 0.0f : (FP8 && p.v_scale ? p.v_scale[h] : 1.0f) / l;
-  if (sg.seq.position(t) >= sg.seq.cap) f = NAN;
-  uint16_t* to = p.out + (sg.seq.row0 + t) * p.o_row + (h * p.G + at - t * p.G) * p.o_head + 4 * lane;
-  *reinterpret_cast<uint2*>(to) = make_uint2(bf16x2(v.x * f, v.y * f), bf16x2(v.z * f, v.w * f));
-}
-
 template <int D, bool FP8, bool WHOLE>
 hipError_t launch(const KvAttnArgs& a, hipStream_t stream) {
   using F = Few<D, FP8>;
-  const CacheBatchArgs& b = a.batch;
-  const int64_t tiles = ((int64_t)b.T * a.G + kRows - 1) / kRows + (b.B < b.T ? b.B : b.T);   // at most
-  // each tile one segment, and as many more as the work has whole segments
-  const int64_t groups = (tiles + (kTarget + a.Hkv - 1) / a.Hkv) * a.Hkv;
+  const int64_t groups = F::kDivision.segments(a.batch.T, a.batch.B, a.Hkv, a.G) * a.Hkv;
   const size_t lds = (size_t)kWaves * kRows * (D + 4 + 2) * sizeof(float);
   static std::atomic<uint64_t> done{0};
   if (lds > 65536) {
@@ -476,13 +354,7 @@ hipError_t launch(const KvAttnArgs& a, hipStream_t stream) {
   }
   few_kernel<D, FP8, WHOLE><<<dim3((unsigned)groups), kWaves * kWave, lds, stream>>>(a);
   const hipError_t e = hipGetLastError();
-  // the blocks that a sequence can have
-  if (e != hipSuccess || ((int64_t)b.cols << b.page_log >> F::kBlockLog) < kSplitBlocks) return e;
-  // rows that a workgroup joins: one, or as many as its threads hold where that leaves a few workgroups a CU
-  int together = 1;
-  while (together * 2 * (D / 4) <= kJoinThreads && tiles * a.Hkv * (kRows / (2 * together)) >= 1024) together *= 2;
-  few_join_kernel<FP8><<<dim3((unsigned)(tiles * a.Hkv * (kRows / together))), kJoinThreads, 0, stream>>>(a, F::kBlockLog, together);
-  return hipGetLastError();
+  return e != hipSuccess ? e : launch_join<FP8>(a, F::kDivision, stream);
 }
 
 template <int D, bool FP8>
@@ -512,11 +384,7 @@ hipError_t launch_d(const KvAttnArgs& a, hipStream_t stream) {
 // tokens over 8000 keys (64 heads of 8 groups, D 128, bf16) 155 / 126 us, of 8 tokens 262 / 129 us.
 bool kv_attention_few_fits(int T, int B, int G) { return (int64_t)T * G <= (int64_t)kRows * B; }
 
-// A tile has more than one segment only from 1.5 times a whole segment's keys on, so the segments of
-// such tiles are at most 4 / 3 as many as the work has whole segments.
-size_t kv_attention_few_ws_bytes(int Hkv, int D) {
-  return (size_t)(2 * kTarget + Hkv) * kRows * (D + 2) * sizeof(float);
-}
+size_t kv_attention_few_ws_bytes(int Hkv, int D) { return division(false).ws_bytes(Hkv, D); }
 
 hipError_t launch_kv_attention_few(const KvAttnArgs& a, hipStream_t stream) {
   return a.fp8 ? launch_d<true>(a, stream) : launch_d<false>(a, stream);

@@ -777,7 +777,8 @@ def _gate(gate: torch.Tensor, T: int, H: int):
 
 
 # ------------------------------------------------------------------ rotary positions, the paged cache
-@dataclass
+# (The handles below are checked when they are made, once for all the calls that take them, and cannot be changed.)
+@dataclass(frozen=True)
 class Rope:
     """A rotation by position: the pairs of a head's dims [start, start + 2 * len(freqs)) turn by ``freqs``
     radians a position (rope_frequencies makes them) and are scaled by ``magnitude``. Pairs are (i, i + half)
@@ -786,6 +787,13 @@ class Rope:
     start: int = 0
     interleaved: bool = False
     magnitude: float = 1.0
+
+    def __post_init__(self):
+        f = self.freqs
+        if f.dtype != torch.float64 or f.dim() != 1 or f.shape[0] < 1 or not f.is_contiguous():
+            raise ValueError(f"Rope: freqs must be contiguous float64 [rot / 2], got {f.dtype} {tuple(f.shape)}")
+        if self.start < 0 or not math.isfinite(self.magnitude):
+            raise ValueError(f"Rope: need start >= 0 and a finite magnitude, got {self.start} and {self.magnitude}")
 
     @property
     def rot(self) -> int:
@@ -874,16 +882,12 @@ def _positions(fn: str, t, T: int, idx: int):
     return t, t.data_ptr(), t.element_size()
 
 
-def _rope(fn: str, rope: Rope, D: int, idx: int):
-    f = rope.freqs
-    if f.dtype != torch.float64 or f.dim() != 1 or not f.is_contiguous():
-        raise ValueError(f"{fn}: the rotation's freqs must be contiguous float64 [rot / 2], got {f.dtype} {tuple(f.shape)}")
-    if f.get_device() != idx:
-        raise ValueError(f"{fn}: all tensors must be on one GPU")
-    rot = 2 * f.shape[0]
-    if rot < 2 or rope.start < 0 or rope.start + rot > D:
+def _rope(fn: str, rope: Rope, D: int):
+    """(address, turned dims) of a rotation's frequencies."""
+    rot = 2 * rope.freqs.shape[0]
+    if rope.start + rot > D:
         raise ValueError(f"{fn}: the rotation's dims [{rope.start}, {rope.start + rot}) must lie in a head of {D}")
-    return f.data_ptr(), rot
+    return rope.freqs.data_ptr(), rot
 
 
 def rope_rotate(x: torch.Tensor, positions: torch.Tensor, rope: Rope, *, grad: bool = False, out: torch.Tensor | None = None):
@@ -896,7 +900,7 @@ def rope_rotate(x: torch.Tensor, positions: torch.Tensor, rope: Rope, *, grad: b
     if dt is None or x.dim() != 3:
         raise ValueError(f"{fn}: x must be float32 or bf16 [T, H, D], got {x.dtype} {tuple(x.shape)}")
     T, H, D = x.shape
-    p_f, rot = _rope(fn, rope, D, idx)
+    p_f, rot = _rope(fn, rope, D)
     with _on(idx):
         positions, p_pos, pos_bytes = _positions(fn, positions, T, idx)
         if T == 0 or H == 0:
@@ -913,7 +917,7 @@ def rope_rotate(x: torch.Tensor, positions: torch.Tensor, rope: Rope, *, grad: b
     return out
 
 
-@dataclass
+@dataclass(frozen=True)
 class KVCache:
     """A paged cache of keys [pages, heads, page, D] and values [pages, heads, D, page] (transposed in their
     pages), bf16 or float8_e4m3fn with a float32 scale for each head (None: 1). kv_cache makes an empty one."""
@@ -921,6 +925,26 @@ class KVCache:
     v: torch.Tensor
     k_scale: torch.Tensor | None = None   # float32 [heads], positive
     v_scale: torch.Tensor | None = None
+
+    def __post_init__(self):
+        k, v = self.k, self.v
+        if k.dim() != 4 or k.dtype != v.dtype or k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise ValueError("KVCache: the cache must be bf16 or float8_e4m3fn [pages, heads, page, D] and [pages, heads, D, page]")
+        pages, heads, page, D = k.shape
+        if v.shape != (pages, heads, D, page) or not (k.is_contiguous() and v.is_contiguous()):
+            raise ValueError(f"KVCache: values must be [pages, heads, D, page] beside keys [pages, heads, page, D], both "
+                             f"contiguous, got {tuple(v.shape)} and {tuple(k.shape)}")
+        fp8 = k.dtype != torch.bfloat16
+        for s in (self.k_scale, self.v_scale):
+            if s is not None and (not fp8 or s.shape != (heads,) or s.dtype != torch.float32 or not s.is_contiguous()):
+                raise ValueError(f"KVCache: scales go with an FP8 cache, contiguous float32 [{heads}]")
+        _one_device("KVCache", k, v, self.k_scale, self.v_scale)
+        object.__setattr__(self, "_sizes", (k.shape, v.shape, heads, D, page, pages, int(fp8)))
+
+
+def _one_device(fn: str, *ts):
+    if len({t.device for t in ts if t is not None}) != 1:
+        raise ValueError(f"{fn}: all tensors must be on one GPU")
 
 
 def kv_cache(pages: int, heads: int, page: int, D: int, dtype=torch.bfloat16, *, k_scale: torch.Tensor | None = None,
@@ -931,46 +955,45 @@ def kv_cache(pages: int, heads: int, page: int, D: int, dtype=torch.bfloat16, *,
     return KVCache(zeros(pages, heads, page, D), zeros(pages, heads, D, page), k_scale, v_scale)
 
 
-@dataclass
+@dataclass(frozen=True)
 class CacheBatch:
     """Sequences of a cache and their new tokens, int32 on the GPU: ``page_table`` [B, n] (page of the tokens
     [c * page, (c + 1) * page) at column c), ``lengths`` [B] (tokens, the new ones among them) and ``starts``
-    [B + 1] (row of each sequence's first new token, and the end of the last one's)."""
+    [B + 1] (row of each sequence's first new token, and the end of the last one's). What they hold may change
+    from call to call."""
     page_table: torch.Tensor
     lengths: torch.Tensor
     starts: torch.Tensor
 
+    def __post_init__(self):
+        t, lengths, starts = self.page_table, self.lengths, self.starts
+        B = lengths.shape[0] if lengths.dim() == 1 else -1
+        if t.dtype != torch.int32 or lengths.dtype != torch.int32 or starts.dtype != torch.int32 or t.dim() != 2 or \
+                B < 1 or t.shape[0] != B or t.shape[1] < 1 or starts.shape != (B + 1,):
+            raise ValueError(f"CacheBatch: needs int32 page_table [B, n], lengths [B] and starts [B + 1] with B, n >= 1, got "
+                             f"{tuple(t.shape)}, {tuple(lengths.shape)} and {tuple(starts.shape)}")
+        cols = t.shape[1]
+        ld = t.stride(0) if B > 1 else cols
+        if (t.stride(1) != 1 and cols > 1) or ld < cols or not lengths.is_contiguous() or not starts.is_contiguous():
+            raise ValueError("CacheBatch: page_table's rows, lengths and starts must be contiguous")
+        _one_device("CacheBatch", t, lengths, starts)
+        object.__setattr__(self, "_sizes", (t.shape, lengths.shape, starts.shape, B, cols, ld))
 
-def _cache(fn: str, c: KVCache, idx: int):
+
+def _cache(fn: str, c: KVCache):
     """(heads, D, page, pages, fp8, addresses of the scales) of a cache."""
-    k, v = c.k, c.v
-    if k.dim() != 4 or v.dim() != 4 or k.dtype != v.dtype or k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
-        raise ValueError(f"{fn}: the cache must be bf16 or float8_e4m3fn [pages, heads, page, D] and [pages, heads, D, page]")
-    pages, heads, page, D = k.shape
-    if v.shape != (pages, heads, D, page) or not (k.is_contiguous() and v.is_contiguous()):
-        raise ValueError(f"{fn}: the cache's values must be [pages, heads, D, page] beside keys [pages, heads, page, D], "
-                         f"both contiguous, got {tuple(v.shape)} and {tuple(k.shape)}")
-    fp8 = k.dtype != torch.bfloat16
-    scales = []
-    for s in (c.k_scale, c.v_scale):
-        if s is not None and (not fp8 or s.shape != (heads,) or s.dtype != torch.float32 or not s.is_contiguous()):
-            raise ValueError(f"{fn}: scales go with an FP8 cache, float32 [{heads}]")
-        scales.append(None if s is None else s.data_ptr())
-    return heads, D, page, pages, fp8, scales
+    k_shape, v_shape, heads, D, page, pages, fp8 = c._sizes
+    if c.k.shape != k_shape or c.v.shape != v_shape:
+        raise ValueError(f"{fn}: the cache's tensors were resized")
+    return (heads, D, page, pages, fp8, None if c.k_scale is None else c.k_scale.data_ptr(),
+            None if c.v_scale is None else c.v_scale.data_ptr())
 
 
 def _batch(fn: str, b: CacheBatch):
     """(B, columns, row distance of the page table)."""
-    t, lengths, starts = b.page_table, b.lengths, b.starts
-    B = lengths.shape[0] if lengths.dim() == 1 else -1
-    if t.dtype != torch.int32 or lengths.dtype != torch.int32 or starts.dtype != torch.int32 or t.dim() != 2 or \
-            B < 1 or t.shape[0] != B or t.shape[1] < 1 or starts.shape != (B + 1,):
-        raise ValueError(f"{fn}: a batch is int32 page_table [B, n], lengths [B] and starts [B + 1] with B, n >= 1, got "
-                         f"{tuple(t.shape)}, {tuple(lengths.shape)} and {tuple(starts.shape)}")
-    cols = t.shape[1]
-    ld = t.stride(0) if B > 1 else cols
-    if (t.stride(1) != 1 and cols > 1) or ld < cols or not lengths.is_contiguous() or not starts.is_contiguous():
-        raise ValueError(f"{fn}: page_table's rows, lengths and starts must be contiguous")
+    t_shape, l_shape, s_shape, B, cols, ld = b._sizes
+    if b.page_table.shape != t_shape or b.lengths.shape != l_shape or b.starts.shape != s_shape:
+        raise ValueError(f"{fn}: the batch's tensors were resized")
     return B, cols, ld
 
 
@@ -981,9 +1004,8 @@ def kv_cache_append(cache: KVCache, batch: CacheBatch, k: torch.Tensor, v: torch
     turned likewise. Returns the turned queries (``q_out``, which may be q), or None without q. k, v and q may be
     views of one projection's rows. Rows behind the last sequence's are left as they were."""
     fn = "kv_cache_append"
-    idx = _gpu(fn, cache.k, cache.v, cache.k_scale, cache.v_scale, batch.page_table, batch.lengths, batch.starts, k, v, q,
-               q_out)
-    heads, D, page, pages, fp8, (p_ks, p_vs) = _cache(fn, cache, idx)
+    idx = _gpu(fn, cache.k, batch.lengths, k, v, q, q_out, None if rope is None else rope.freqs)
+    heads, D, page, pages, fp8, p_ks, p_vs = _cache(fn, cache)
     B, cols, ld = _batch(fn, batch)
     if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or (q is not None and q.dtype != torch.bfloat16):
         raise ValueError(f"{fn}: k, v and q must be bf16")
@@ -995,7 +1017,7 @@ def kv_cache_append(cache: KVCache, batch: CacheBatch, k: torch.Tensor, v: torch
     Hq = 0 if q is None else q.shape[1]
     p_f, rot, start, inter, mag = None, 0, 0, 0, 1.0
     if rope is not None:
-        p_f, rot = _rope(fn, rope, D, idx)
+        p_f, rot = _rope(fn, rope, D)
         start, inter, mag = rope.start, int(rope.interleaved), rope.magnitude
     with _on(idx):
         p_pos, pos_bytes = None, 4
@@ -1016,7 +1038,7 @@ def kv_cache_append(cache: KVCache, batch: CacheBatch, k: torch.Tensor, v: torch
         st = _lib.load().kv_cache_append(
             p_q, q_row, q_head, p_k, k_row, k_head, p_v, v_row, v_head, T, Hq, heads, D, p_pos, pos_bytes, p_f, rot, start,
             inter, mag, batch.page_table.data_ptr(), ld, cols, batch.lengths.data_ptr(), batch.starts.data_ptr(), B,
-            cache.k.data_ptr(), cache.v.data_ptr(), int(fp8), pages, page, p_ks, p_vs, p_o, o_row, o_head, _raw_stream(idx))
+            cache.k.data_ptr(), cache.v.data_ptr(), fp8, pages, page, p_ks, p_vs, p_o, o_row, o_head, _raw_stream(idx))
     if st:
         _lib.check(fn, st)
     return q_out
@@ -1034,8 +1056,8 @@ def kv_cache_attention(q: torch.Tensor, cache: KVCache, batch: CacheBatch, *, sc
     ``window`` of them. ``scale`` of the scores: D^-0.5 unless given. Returns bf16 [T, Hq, D] (``out``, which
     must not overlap q); rows behind the last sequence's are left as they were."""
     fn = "kv_cache_attention"
-    idx = _gpu(fn, q, cache.k, cache.v, cache.k_scale, cache.v_scale, batch.page_table, batch.lengths, batch.starts, out)
-    heads, D, page, pages, fp8, (p_ks, p_vs) = _cache(fn, cache, idx)
+    idx = _gpu(fn, q, cache.k, batch.lengths, out)
+    heads, D, page, pages, fp8, p_ks, p_vs = _cache(fn, cache)
     B, cols, ld = _batch(fn, batch)
     if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != D or q.shape[1] == 0 or q.shape[1] % heads:
         raise ValueError(f"{fn}: q must be bf16 [T, Hq, {D}], Hq a multiple of {heads}, got {q.dtype} {tuple(q.shape)}")
@@ -1049,7 +1071,7 @@ def kv_cache_attention(q: torch.Tensor, cache: KVCache, batch: CacheBatch, *, sc
         ws = q.new_empty((nbytes,), dtype=torch.uint8)
         st = _lib.load().kv_cache_attention(
             p_q, q_row, q_head, T, Hq, heads, D, batch.page_table.data_ptr(), ld, cols, batch.lengths.data_ptr(),
-            batch.starts.data_ptr(), B, cache.k.data_ptr(), cache.v.data_ptr(), int(fp8), pages, page, p_ks, p_vs,
+            batch.starts.data_ptr(), B, cache.k.data_ptr(), cache.v.data_ptr(), fp8, pages, page, p_ks, p_vs,
             D ** -0.5 if scale is None else scale, window, p_o, o_row, o_head, ws.data_ptr(), nbytes, _raw_stream(idx))
     if st:
         _lib.check(fn, st)
