@@ -244,9 +244,12 @@ __device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w, uint32_t& bad) {
   return w & ~bad;
 }
 
+// Bits that are not zero where one of two bf16 (a word) is NaN or Inf.
+__device__ __forceinline__ uint32_t not_finite_bf16x2(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+
 // Four E4M3 bytes with NaN (0x7f, 0xff) replaced by 0.
 __device__ __forceinline__ uint32_t finite_e4m3x4(uint32_t w) {
-  uint32_t nan = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;   // bit 7 of each that is NaN
+  const uint32_t nan = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;   // bit 7 of each that is NaN
   return w & ~(nan | (nan - (nan >> 7)));
 }
 

@@ -31,7 +31,10 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kRows = 32 * kWaves;    // rows of a tile
 constexpr int kBlockLog = 6, kBlock = 1 << kBlockLog;   // keys of a block
-constexpr Division kDivision = {kRows, kBlockLog, 1024, 8, 1};
+// (512 segments: two workgroups on each CU at once. With 1024, 8192 new tokens of 32 heads 567 / 556 us, 128 new ones
+// over 30000 keys 153 / 138, 16 sequences of 4 over 8000 112 / 105; 640 and 768, which leave a part round, are
+// slower yet: 125 and 115 us the last.)
+constexpr Division kDivision = {kRows, kBlockLog, 512, 8, 1};
 
 // 16 bytes a lane straight into LDS (lane l at lds + 16 l), from global memory or from a buffer (whose base
 // and offset `soff` are the wave's: no address arithmetic in the lanes).
@@ -71,7 +74,8 @@ __device__ __forceinline__ int key_of_row(int r) { return r / 4 % 2 * 8 + r / 8 
 template <int D, bool FP8>
 __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(const KvAttnArgs p) {
   using C = Chunk<D, FP8>;
-  extern __shared__ __attribute__((aligned(16))) char smem[];   // two of: keys [64, D], values [D, 64]
+  extern __shared__ __attribute__((aligned(16))) char smem[];   // two of: keys [64, D], values [D, 64]; then
+  uint32_t* s_any = reinterpret_cast<uint32_t*>(smem + 4 * Chunk<D, FP8>::kBytes);   // a flag a wave
   const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int col = lane % 32, half = lane / 32;
   const int h = blockIdx.x % p.Hkv;
@@ -234,15 +238,17 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
       }
     // score i of tile a: key 32a + 16 (i / 8) + 8 half + i % 8 of the block
     if constexpr (EDGE) {
+      if (bad_pages != 0u) {   // (a page holds 16 keys or more) a row that sees one of a page that is none
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          if ((bad_pages >> g & 1u) && mine.lo < begin + 16 * g + 16 && mine.hi > begin + 16 * g) l = NAN;
+      }
+      const uint32_t from_lo = (uint32_t)(begin + 8 * half - mine.lo), seen = (uint32_t)max(mine.hi - mine.lo, 0);
 #pragma unroll
       for (int a = 0; a < 2; ++a)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int key = begin + 32 * a + 16 * (i / 8) + 8 * half + i % 8;
-          const bool sees = (key >= mine.lo) & (key < mine.hi);
-          const float x = bad_pages >> (2 * a + i / 8) & 1u ? NAN : s[a][i];
-          s[a][i] = sees ? x : -INFINITY;
-        }
+        for (int i = 0; i < 16; ++i)
+          s[a][i] = from_lo + (uint32_t)(32 * a + 16 * (i / 8) + i % 8) < seen ? s[a][i] : -INFINITY;
     } else if (bad_pages != 0u) {   // every row sees every key
       l = NAN;
     }
@@ -276,41 +282,65 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
     l += sum[0] + sum[1];
     const char* values = from + C::kBytes + col * 128;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      bf16x8 sees;
-      if constexpr (EDGE) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int key = begin + 16 * u + 8 * half + i;
-          sees[i] = key >= mine.lo && key < mine.hi ? (__bf16)1.0f : (__bf16)0.0f;
-        }
-      }
+    for (int u = 0; u < 4; ++u)
 #pragma unroll
       for (int d = 0; d < C::kDTiles; ++d) {
-        bf16x8 v = *reinterpret_cast<const bf16x8*>(values + d * 4096 + ((2 * u + half) ^ C::v_swizzle(col)) * 16);
-        if constexpr (EDGE) {   // values that some row does not see (or no row: what a page holds behind its last token)
-          u32x4v f = __builtin_bit_cast(u32x4v, v), bad;
-          uint32_t any = 0u;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t bits;
-            f[i] = finite_bf16x2(f[i], bits);
-            bad[i] = bits & 0x3f803f80u;   // 1.0 where one was taken out
-            any |= bits;
-          }
-          v = __builtin_bit_cast(bf16x8, f);
-          if (__any(any != 0u)) {
-            f32x16 n;   // how many of them each row sees
-#pragma unroll
-            for (int i = 0; i < 16; ++i) n[i] = 0.0f;
-            n = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, bad), sees, n, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[d][i] = n[i] > 0.0f ? NAN : o[d][i];
-          }
-        }
+        const bf16x8 v = *reinterpret_cast<const bf16x8*>(values + d * 4096 + ((2 * u + half) ^ C::v_swizzle(col)) * 16);
         o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w[u], o[d], 0, 0, 0);
       }
+  };
+
+  // Values that some row does not see (or no row: what a page holds behind its last token) must not reach it,
+  // NaN and Inf included, which a zero weight does not hold back. Where a block with such keys has any: a NaN
+  // into the sums of the rows that see them, and zeros in their place. (Each wave looks at a quarter of V^T.)
+  auto clean = [&](int block, char* in) {
+    uint32_t any = 0u;
+    char* mine_v = in + C::kBytes + wave * (C::kBytes / 4) + lane * 16;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const u32x4v v = *reinterpret_cast<const u32x4v*>(mine_v + 1024 * i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) any |= not_finite_bf16x2(v[j]);
     }
+    if (lane == 0) s_any[wave] = 0u;
+    if (__any(any != 0u) && lane == 0) s_any[wave] = 1u;
+    __syncthreads();
+    if ((s_any[0] | s_any[1] | s_any[2] | s_any[3]) == 0u) return;
+    const uint32_t from_lo = (uint32_t)((block << kBlockLog) + 8 * half - mine.lo), seen = (uint32_t)max(mine.hi - mine.lo, 0);
+#pragma unroll 1
+    for (int u = 0; u < 4; ++u) {
+      bf16x8 sees;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sees[i] = from_lo + (uint32_t)(16 * u + i) < seen ? (__bf16)1.0f : (__bf16)0.0f;
+#pragma unroll
+      for (int d = 0; d < C::kDTiles; ++d) {
+        u32x4v bad = *reinterpret_cast<const u32x4v*>(in + C::kBytes + (32 * d + col) * 128 + ((2 * u + half) ^ C::v_swizzle(col)) * 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t bits;
+          finite_bf16x2(bad[i], bits);
+          bad[i] = bits & 0x3f803f80u;   // 1.0 for each
+        }
+        f32x16 n;   // how many of them each row sees
+#pragma unroll
+        for (int i = 0; i < 16; ++i) n[i] = 0.0f;
+        n = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, bad), sees, n, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] = n[i] > 0.0f ? NAN : o[d][i];
+      }
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int i = 0; i < D / 32; ++i) {
+      u32x4v v = *reinterpret_cast<const u32x4v*>(mine_v + 1024 * i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t bits;
+        v[j] = finite_bf16x2(v[j], bits);
+      }
+      *reinterpret_cast<u32x4v*>(mine_v + 1024 * i) = v;
+    }
+    __syncthreads();
   };
 
   if (sg.blocks > 0) {
@@ -329,6 +359,7 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
         next_bad = request(block + 1, pg, then);
         pg = pages_of(min(block + 2, end - 1));
       }
+      if constexpr (decltype(edge)::value) clean(block, now);
       use(edge, block, now, bad);
       if (block + 1 < end) place(then);
       __builtin_amdgcn_s_waitcnt(0x0F70);
@@ -378,7 +409,7 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
 
 template <int D, bool FP8>
 hipError_t launch(const KvAttnArgs& a, hipStream_t stream) {
-  constexpr int lds = 4 * Chunk<D, FP8>::kBytes;
+  constexpr int lds = 4 * Chunk<D, FP8>::kBytes + kWaves * 4;
   static std::atomic<uint64_t> done{0};
   if (lds > 65536) {
     const hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(chunk_kernel<D, FP8>), lds, done);
