@@ -1,5 +1,6 @@
 """The MoE layer as a sequence of C ABI calls (route -> up/gate + SwiGLU -> down -> reduce), the
-layer of a few tokens as one call, and the block around it (shared expert, norms, residual).
+layer of a few tokens as one call, the block around it (shared expert, norms, residual), and the
+attention block before it (projections, rotary positions, paged cache, attention, norms).
 
 This module only sequences the library calls and allocates their outputs with torch; all
 arithmetic runs in the HIP kernels behind include/nvfp4moe.h.
@@ -316,3 +317,74 @@ def moe_block_forward(resid: torch.Tensor, x: torch.Tensor, k: int, w: NVFP4Expe
             y, slot_to_row, topk_w = moe_forward(x, logits, k, w, fp8_acts=fp8_acts, reduce=False)
     ys = None if shared is None else shared_expert_forward(x, shared, few=few)
     return ops.moe_block_norm(resid, y, slot_to_row=slot_to_row, topk_w=topk_w, y_add=ys, **norm)
+
+
+# ------------------------------------------------------------------ the attention block
+@dataclass
+class AttentionWeights:
+    """An attention block's projections, each one tiled matrix, both NVFP4 or both MXFP4: qkv
+    [(heads + 2 * key heads) * D, H] (queries' heads first, then the keys', then the values') and o
+    [H, heads * D]. The cache says how many key heads there are and their D. A layer that reads the cache of
+    an earlier one, and brings no keys of its own, has queries alone: qkv [heads * D, H]."""
+    qkv: ops.TiledWeights | ops.MxTiledWeights
+    o: ops.TiledWeights | ops.MxTiledWeights
+    heads: int
+
+
+def _projection(x: torch.Tensor, w, out_dtype, few: bool):
+    """x W^T of rows [T, K]: a few-row product, or a grouped GEMM of one matrix."""
+    nv = isinstance(w, ops.TiledWeights)
+    if few:
+        return (ops.nvfp4_matvec if nv else ops.mxfp4_matvec)(x, w, out_dtype=out_dtype)
+    T = x.shape[0]
+    i32 = dict(dtype=torch.int32, device=x.device)
+    dense = dict(expert_offsets=torch.arange(0, 2 * T, T, **i32), active_experts=torch.zeros((1,), **i32),
+                 n_active=torch.ones((1,), **i32), out_dtype=out_dtype)
+    if nv:
+        return ops.moe_grouped_gemm_nvfp4(ops.W4A16, ops.EPI_NONE, x, w, **dense)
+    return ops.moe_grouped_gemm_mxfp4(ops.EPI_NONE, *ops.mxfp4_quantize(x), w, **dense)
+
+
+def attention_block_forward(resid: torch.Tensor, x: torch.Tensor, w: AttentionWeights, cache: ops.KVCache,
+                            batch: ops.CacheBatch, *, rope: ops.Rope | None = None, positions: torch.Tensor | None = None,
+                            attention_scale: float | None = None, window: int = 0, post_w: torch.Tensor | None = None,
+                            gate: torch.Tensor | None = None, scale: float = 1.0, pre_w: torch.Tensor | None = None,
+                            w_offset: float = 0.0, eps: float = 1e-6, few: bool | None = None):
+    """One attention block and the norms around it, the other half of the decoder layer that
+    moe_block_forward ends: queries, keys and values of the new tokens ``x`` bf16 [T, H] (this block's
+    normed input) by one projection, kv_cache_append with ``rope``, kv_cache_attention, the output
+    projection to float32, and moe_block_norm's r' = resid + scale * gate * (post-norm of it) with the
+    next block's normed input. Returns (r', next): what moe_block_forward takes as ``resid`` and ``x``.
+
+    Up to 16 rows the projections are few-row products, above grouped GEMMs of one matrix; ``few`` asks
+    for one of the two, as in shared_expert_forward (MXFP4 GEMMs quantize their rows, products do not).
+    Queries, keys, values and the attention's output are bf16. With queries alone (AttentionWeights) nothing is
+    appended and the queries are turned by rope_rotate, at ``positions``, which it needs then. Rows behind the batch's last sequence
+    (a padded batch) give no keys, and what comes back in them is of no meaning."""
+    fn = "attention_block_forward"
+    heads, D = cache.k.shape[1], cache.k.shape[3]
+    H, Hq = w.o.R, w.heads
+    queries_alone = w.qkv.R == Hq * D
+    if type(w.qkv) is not type(w.o) or w.qkv.B != 1 or w.o.B != 1 or w.qkv.C != H or w.o.C != Hq * D or \
+            not (queries_alone or w.qkv.R == (Hq + 2 * heads) * D):
+        raise ValueError(f"{fn}: qkv must be one matrix [{(Hq + 2 * heads) * D}, H] (or [{Hq * D}, H]) and o one [H, {Hq * D}] "
+                         f"of the same format, got [{w.qkv.R}, {w.qkv.C}] and [{w.o.R}, {w.o.C}]")
+    if queries_alone and rope is not None and positions is None:
+        raise ValueError(f"{fn}: a layer with queries alone needs their positions")
+    if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != H:
+        raise ValueError(f"{fn}: x must be bf16 [T, {H}], got {x.dtype} {tuple(x.shape)}")
+    T = x.shape[0]
+    few = _few(fn, few, T, FEW_TOKENS)
+    x, ldx = ops._rows(fn, "x", x, H, 8)
+    x = x if few or ldx == H else x.contiguous()   # (the grouped GEMM takes rows beside each other)
+    with ops._on(ops._gpu(fn, x, w.qkv.codes, w.o.codes)):   # (the GEMMs launch on the current GPU)
+        qkv = _projection(x, w.qkv, torch.bfloat16, few).view(T, -1, D)
+        q = qkv[:, :Hq]
+        if queries_alone and rope is not None:
+            ops.rope_rotate(q, positions, rope, out=q)
+        elif not queries_alone:
+            ops.kv_cache_append(cache, batch, qkv[:, Hq:Hq + heads], qkv[:, Hq + heads:], q=q, rope=rope,
+                                positions=positions, q_out=q)
+        a = ops.kv_cache_attention(q, cache, batch, scale=attention_scale, window=window)
+        y = _projection(a.view(T, Hq * D), w.o, torch.float32, few)
+    return ops.moe_block_norm(resid, y, post_w=post_w, gate=gate, scale=scale, pre_w=pre_w, w_offset=w_offset, eps=eps)
