@@ -28,13 +28,14 @@ namespace nvfp4moe {
 
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kRows = 32 * kWaves;    // rows of a tile
+constexpr float kSlack = 8.0f;        // base 2 logits by which a score may exceed the running maximum,
+constexpr float kHigh = 1099511627776.0f;   // and, where that is looked at by the sums alone, sum of 16 exponentials (2^40)
 constexpr int kBlockLog = 6, kBlock = 1 << kBlockLog;   // keys of a block
-// (512 segments: two workgroups on each CU at once. With 1024, 8192 new tokens of 32 heads 567 / 556 us, 128 new ones
-// over 30000 keys 153 / 138, 16 sequences of 4 over 8000 112 / 105; 640 and 768, which leave a part round, are
-// slower yet: 125 and 115 us the last.)
-constexpr Division kDivision = {kRows, kBlockLog, 512, 8, 1};
+// Waves of a workgroup (W): 4, two workgroups a CU, or 8, one a CU, whose tiles of 256 rows bring half the words for
+// a row. The segments are as many as workgroups that a CU holds at once (with W 4 and 1024 segments, 8192 new
+// tokens of 32 heads took 567 instead of 556 us, 128 new ones over 30000 keys 153 instead of 138, 16 sequences of 4
+// over 8000 112 instead of 105; 640 and 768, which leave a part round, are slower yet: 125 and 115 us the last).
+constexpr Division division(int W) { return {32 * W, kBlockLog, W == 8 ? 256 : 512, 8, 1}; }
 
 // 16 bytes a lane straight into LDS (lane l at lds + 16 l), from global memory or from a buffer (whose base
 // and offset `soff` are the wave's: no address arithmetic in the lanes).
@@ -58,6 +59,7 @@ struct Chunk {
   static constexpr int kBytes = kBlock * D * 2;      // of a block's keys, and of its values
   static constexpr int kSteps = D / 16;              // of the first product
   static constexpr int kDTiles = D / 32;             // of the second
+  static constexpr bool kPipelined = D <= 224;       // (its sums and queries leave registers for two halves' scores)
   // LDS serves 16 lanes' 16-byte words a cycle where they lie in different 16ths of its 256-byte lines. A
   // product reads one word of 16 rows at once, so word w of row r lies at w ^ swizzle(r): the rows' own
   // places in the lines (kWords 16ths apart) and the swizzle make 16 different ones.
@@ -71,9 +73,11 @@ struct Chunk {
 // (rows 8 (i / 4) + 4 half + i % 4) are those of 8 consecutive keys.
 __device__ __forceinline__ int key_of_row(int r) { return r / 4 % 2 * 8 + r / 8 * 4 + r % 4; }
 
-template <int D, bool FP8>
-__global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(const KvAttnArgs p) {
+template <int D, bool FP8, int W>
+__global__ __launch_bounds__(W* kWave, D > 128 ? 1 : 2) void chunk_kernel(const KvAttnArgs p) {
   using C = Chunk<D, FP8>;
+  constexpr Division kDivision = division(W);
+  constexpr int kRows = kDivision.tile_rows;
   extern __shared__ __attribute__((aligned(16))) char smem[];   // two of: keys [64, D], values [D, 64]; then
   uint32_t* s_any = reinterpret_cast<uint32_t*>(smem + 4 * Chunk<D, FP8>::kBytes);   // a flag a wave
   const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -89,7 +93,7 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
   const int rows = seq.n * p.G, row0 = sg.tile * kRows + 32 * wave;
   const int row = min(row0 + col, rows - 1), token = row / p.G, head = h * p.G + row - token * p.G;
   const Seen mine = seen_by(seq.position(token), p.window, seq.cap);
-  auto seen_of = [&](int r) { return seen_by(seq.position(min(r, rows - 1) / p.G), p.window, seq.cap); };
+  auto seen_of = [&](int r) __attribute__((always_inline)) { return seen_by(seq.position(min(r, rows - 1) / p.G), p.window, seq.cap); };
   const int all_lo = seen_of(sg.tile * kRows + kRows - 1).lo, all_hi = seen_of(sg.tile * kRows).hi;
   const int any_lo = seen_of(row0).lo, any_hi = row0 < rows ? seen_of(row0 + 31).hi : 0;
 
@@ -101,8 +105,8 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
   }
   const float log2_scale = p.scale * kLog2e * (FP8 && p.k_scale ? p.k_scale[h] : 1.0f);
 
-  // Staging. Wave w brings the keys 16 w and on of a block (one page's: pages are whole multiples of
-  // 16), and D / 4 rows of V^T, of which a lane takes 16 bytes (bf16: 8 keys; E4M3: 16).
+  // Staging: a block's keys and V^T in loads of a wave, dealt to the waves in order. A load of keys is of 16 keys
+  // (one page's: pages are whole multiples of 16), of V^T 8 rows (E4M3: 16), of which a lane takes 16 bytes.
   constexpr int kSize = FP8 ? 1 : 2;
   const int page = b.page, page_mask = page - 1;
   const int64_t head_bytes = (int64_t)page * D * kSize;
@@ -111,28 +115,39 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
   // is then one of the block's other half)
   const int v_word = FP8 ? lane % 4 : (lane % 8) ^ (lane / 16);       // of the 4 or 8 words of a row of V^T
   const int v_key = FP8 ? 16 * v_word : 8 * v_word, v_row = FP8 ? lane / 4 : lane / 8;
+  constexpr int kKParts = FP8 ? (D + 63) / 64 : D / 32;                         // loads of 16 keys
+  constexpr int kKAll = 4 * kKParts, kKLoads = (kKAll + W - 1) / W;             // of a block; of a wave
+  constexpr int kVRows = FP8 ? 16 : 8, kVAll = D / kVRows, kVLoads = (kVAll + W - 1) / W;
+  const int k_load0 = wave * kKLoads, v_load0 = wave * kVLoads;
   struct Pages {
-    int k, v, v2;   // of this wave's keys; of this lane's values, in the two kinds of load
+    int k[kKLoads], v, v2;   // of this wave's loads of keys; of this lane's values, in the two kinds of load
   };
   const bool whole = b.page_log >= kBlockLog;   // a block lies in one page
-  auto pages_of = [&](int block) {
-    const int key = block << kBlockLog, kc = (key + 16 * wave) >> b.page_log;
-    Pages r = {-1, -1, -1};
-    if (kc < b.cols) r.k = ld_const(table, kc);
-    r.v = r.v2 = r.k;
-    if (!whole) {
+  auto pages_of = [&](int block) __attribute__((always_inline)) {
+    const int key = block << kBlockLog;
+    Pages r;
+    if (whole) {
+      const int c = key >> b.page_log, at = c < b.cols ? ld_const(table, c) : -1;
+#pragma unroll
+      for (int j = 0; j < kKLoads; ++j) r.k[j] = at;
+      r.v = r.v2 = at;
+    } else {
+#pragma unroll
+      for (int j = 0; j < kKLoads; ++j) {
+        const int kc = (key + (k_load0 + j) / kKParts * 16) >> b.page_log;
+        r.k[j] = kc < b.cols ? ld_const(table, kc) : -1;
+      }
       const int vc = (key + v_key) >> b.page_log, vc2 = (key + (v_key ^ 32)) >> b.page_log;
       r.v = vc < b.cols ? table[vc] : -1;
-      if (!FP8) r.v2 = vc2 < b.cols ? table[vc2] : -1;
+      r.v2 = FP8 ? -1 : vc2 < b.cols ? table[vc2] : -1;
     }
     return r;
   };
-  constexpr int kKLoads = FP8 ? (D + 63) / 64 : D / 32, kVLoads = kKLoads;
   u32x4v raw_k[FP8 ? kKLoads : 1], raw_v[FP8 ? kVLoads : 1];
-  uint32_t k_off[kKLoads];   // this lane's words among its wave's 16 keys: bytes from the first key
+  uint32_t k_off[kKLoads];   // this lane's words among a load's 16 keys: bytes from the first key
 #pragma unroll
   for (int j = 0; j < kKLoads; ++j) {
-    const int i = 64 * j + lane;
+    const int i = (k_load0 + j) % kKParts * 64 + lane;
     if (FP8) {
       k_off[j] = i < D ? i / (D / 16) * D + i % (D / 16) * 16 : kOOB;
     } else {
@@ -141,31 +156,37 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
     }
   }
   const uint32_t v_off = (uint32_t)((v_row * page + (whole ? v_key : v_key & page_mask)) * kSize);
-  // Requests block's keys and values (bf16: into LDS buffer `to`; E4M3: into registers); the pages that are not.
-  auto request = [&](int block, const Pages& pg, char* to) {
-    const int key = block << kBlockLog;
-    const bool k_ok = pg.k >= 0 && pg.k < b.pages, v_ok = pg.v >= 0 && pg.v < b.pages;
-    const __amdgpu_buffer_rsrc_t k = make_rsrc(
-        static_cast<const char*>(p.k_cache) + ((int64_t)(k_ok ? pg.k : 0) * p.Hkv + h) * head_bytes, (uint32_t)head_bytes);
-    const uint32_t k_first = (uint32_t)((key + 16 * wave) & page_mask) * (D * kSize);
+  // Requests a block's keys or values (bf16: into LDS buffer `to`; E4M3: into registers).
+  auto request_k = [&](int block, const Pages& pg, char* to) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < kKLoads; ++j) {
+      const int n = k_load0 + j, g = n / kKParts;
+      if (kKAll % W != 0 && n >= kKAll) break;
+      const int at = whole ? pg.k[0] : pg.k[j];
+      const bool ok = at >= 0 && at < b.pages;
+      const __amdgpu_buffer_rsrc_t k =
+          make_rsrc(static_cast<const char*>(p.k_cache) + ((int64_t)(ok ? at : 0) * p.Hkv + h) * head_bytes, (uint32_t)head_bytes);
+      const uint32_t first = (uint32_t)(((block << kBlockLog) + 16 * g) & page_mask) * (D * kSize);
       if constexpr (FP8)
-        raw_k[j] = __builtin_amdgcn_raw_buffer_load_b128(k, k_off[j], k_first, 0);
+        raw_k[j] = __builtin_amdgcn_raw_buffer_load_b128(k, k_off[j], first, 0);
       else
-        dma16(k, to + wave * 32 * D + 1024 * j, k_off[j], k_first);
+        dma16(k, to + g * 32 * D + n % kKParts * 1024, k_off[j], first);
     }
-    constexpr int kVRows = FP8 ? 16 : 8;   // of V^T a load
+  };
+  // (and says which of the block's 16s of keys have no page, a bit each)
+  auto request_v = [&](int block, const Pages& pg, char* to) __attribute__((always_inline)) {
+    const int key = block << kBlockLog;
+    const bool v_ok = pg.v >= 0 && pg.v < b.pages;
     if (whole) {
       const __amdgpu_buffer_rsrc_t v = make_rsrc(
-          static_cast<const char*>(p.v_cache) + ((int64_t)(k_ok ? pg.k : 0) * p.Hkv + h) * head_bytes, (uint32_t)head_bytes);
+          static_cast<const char*>(p.v_cache) + ((int64_t)(v_ok ? pg.k[0] : 0) * p.Hkv + h) * head_bytes, (uint32_t)head_bytes);
       const uint32_t v_first = (uint32_t)(key & page_mask) * kSize;
 #pragma unroll
       for (int j = 0; j < kVLoads; ++j) {
-        const int d = (wave * kVLoads + j) * kVRows;
+        const int d = (v_load0 + j) * kVRows;
+        if (kVAll % W != 0 && d >= D) break;
         if constexpr (FP8)
-          raw_v[j] = __builtin_amdgcn_raw_buffer_load_b128(v, D % 64 == 0 || d + v_row < D ? v_off : kOOB,
-                                                           D % 64 == 0 || d < D ? v_first + (uint32_t)(d * page) : 0u, 0);
+          raw_v[j] = __builtin_amdgcn_raw_buffer_load_b128(v, v_off, v_first + (uint32_t)(d * page), 0);
         else
           dma16(v, to + C::kBytes + d * 128, d / 8 % 2 ? v_off ^ 64u : v_off, v_first + (uint32_t)(d * page) * 2);
       }
@@ -175,10 +196,10 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
       const char* v2 = static_cast<const char*>(p.v_cache) + ((int64_t)(v2_ok ? pg.v2 : 0) * p.Hkv + h) * head_bytes + v_off;
 #pragma unroll
       for (int j = 0; j < kVLoads; ++j) {
-        const int d = (wave * kVLoads + j) * kVRows;
+        const int d = (v_load0 + j) * kVRows;
+        if (kVAll % W != 0 && d >= D) break;
         if constexpr (FP8) {
-          raw_v[j] = (u32x4v){0u, 0u, 0u, 0u};
-          if (D % 64 == 0 || d + v_row < D) raw_v[j] = *reinterpret_cast<const u32x4v*>(v + (int64_t)d * page);
+          raw_v[j] = *reinterpret_cast<const u32x4v*>(v + (int64_t)d * page);
         } else {
           dma16((d / 8 % 2 ? v2 : v) + (int64_t)d * page * 2, to + C::kBytes + d * 128);
         }
@@ -187,117 +208,149 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
     const uint64_t bad = __ballot(!v_ok);   // (lanes of the first row of V^T: of each 16 keys one)
     return FP8 ? (uint32_t)(bad & 15u) : (uint32_t)((bad & 1u) | (bad >> 1 & 2u) | (bad >> 2 & 4u) | (bad >> 3 & 8u));
   };
-  // E4M3: what request() brought, as bf16, into LDS.
-  auto place = [&](char* to) {
+  // E4M3: what they brought, as bf16, into LDS.
+  auto put = [&](char* at0, char* at1, const u32x4v& w) __attribute__((always_inline)) {
+    *reinterpret_cast<bf16x8*>(at0) = e4m3x8_to_bf16(w[0], w[1]);
+    *reinterpret_cast<bf16x8*>(at1) = e4m3x8_to_bf16(w[2], w[3]);
+  };
+  auto place_k = [&](char* to) __attribute__((always_inline)) {
     if constexpr (FP8) {
-      auto put = [&](char* at0, char* at1, const u32x4v& w) {
-        *reinterpret_cast<bf16x8*>(at0) = e4m3x8_to_bf16(w[0], w[1]);
-        *reinterpret_cast<bf16x8*>(at1) = e4m3x8_to_bf16(w[2], w[3]);
-      };
 #pragma unroll
       for (int j = 0; j < kKLoads; ++j) {
-        const int i = 64 * j + lane, r = key_of_row(i / (D / 16)), w = i % (D / 16) * 2;   // (key_of_row is its own inverse)
-        char* line = to + (wave * 16 + r) * (2 * D);
+        const int n = k_load0 + j, i = n % kKParts * 64 + lane;
+        if (kKAll % W != 0 && n >= kKAll) break;
+        const int r = key_of_row(i / (D / 16)), w = i % (D / 16) * 2;   // (key_of_row is its own inverse)
+        char* line = to + (n / kKParts * 16 + r) * (2 * D);
         if (D % 64 == 0 || i < D) put(line + (w ^ C::swizzle(r)) * 16, line + ((w + 1) ^ C::swizzle(r)) * 16, raw_k[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < kVLoads; ++j) {
-        const int d = (wave * kVLoads + j) * 16 + v_row;
-        char* line = to + C::kBytes + d * 128;
-        const int x = C::v_swizzle(d);
-        if (D % 64 == 0 || d < D) put(line + ((2 * v_word) ^ x) * 16, line + ((2 * v_word + 1) ^ x) * 16, raw_v[j]);
       }
     }
   };
+  auto place_v = [&](char* to) __attribute__((always_inline)) {
+    if constexpr (FP8) {
+#pragma unroll
+      for (int j = 0; j < kVLoads; ++j) {
+        const int d = (v_load0 + j) * 16 + v_row, x = C::v_swizzle(d);
+        if (kVAll % W != 0 && (v_load0 + j) * 16 >= D) break;
+        char* line = to + C::kBytes + d * 128;
+        put(line + ((2 * v_word) ^ x) * 16, line + ((2 * v_word + 1) ^ x) * 16, raw_v[j]);
+      }
+    }
+  };
+  // Every wave's words are in LDS (and, direct ones, waited for).
+  auto arrive = [&]() __attribute__((always_inline)) {
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+    __syncthreads();
+  };
 
-  float m = -INFINITY, l = 0.0f;
+  float m = -INFINITY, base = 0.0f, l = 0.0f;   // base: what exponentials are taken from, m or (before any key) 0
   f32x16 o[C::kDTiles];
 #pragma unroll
   for (int d = 0; d < C::kDTiles; ++d)
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
 
-  // One block in LDS; EDGE: keys that some row of the tile does not see are among its 64.
-  auto use = [&](auto edge_t, int block, const char* from, uint32_t bad_pages) {
-    constexpr bool EDGE = decltype(edge_t)::value;
+  // The pieces of a step, for half a block (32 keys): scores; their exponentials as weights of the second product;
+  // that product. Score i of tile a: key 32a + 16 (i / 8) + 8 half + i % 8 of the block.
+  struct Weights {
+    bf16x8 w[2];
+  };
+  auto score_step = [&](const char* in, int a, int i, const f32x16& s) __attribute__((always_inline)) {
+    const bf16x8 k = *reinterpret_cast<const bf16x8*>(in + (32 * a + col) * (2 * D) + ((2 * i + half) ^ C::swizzle(col)) * 16);
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[i], s, 0, 0, 0);
+  };
+  auto scores = [&](const char* in, int a, f32x16& s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < C::kSteps; ++i) s = score_step(in, a, i, s);
+  };
+  auto exponentials = [&](const f32x16& s, Weights& w, float& sum) __attribute__((always_inline)) {
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], log2_scale, -base));
+      sum += e;
+      w.w[i / 8][i % 8] = (__bf16)e;
+    }
+  };
+  auto values = [&](const char* in, int a, const Weights& w) __attribute__((always_inline)) {
+    const char* rows_at = in + C::kBytes + col * 128;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int d = 0; d < C::kDTiles; ++d) {
+        const bf16x8 v = *reinterpret_cast<const bf16x8*>(rows_at + d * 4096 + ((4 * a + 2 * u + half) ^ C::v_swizzle(col)) * 16);
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w.w[u], o[d], 0, 0, 0);
+      }
+  };
+  // Largest score of each row, times the scale.
+  auto largest = [&](const f32x16& s) __attribute__((always_inline)) {
+    float top = s[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+    return max_across(top) * log2_scale;
+  };
+  // The row's maximum moves to `next`.
+  auto move_maximum = [&](float next) __attribute__((always_inline)) {
+    const float shrink = next == m ? 1.0f : __builtin_amdgcn_exp2f(m - next);
+    m = next;
+    base = m == -INFINITY ? 0.0f : m;
+    l *= shrink;
+#pragma unroll
+    for (int d = 0; d < C::kDTiles; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[d][i] *= shrink;
+  };
+
+  // A block in LDS; EDGE: with keys that some row of the tile does not see.
+  auto use = [&](auto edge, int block, const char* in, uint32_t bad_pages) __attribute__((always_inline)) {
+    constexpr bool EDGE = decltype(edge)::value;
     const int begin = block << kBlockLog;
     if (row0 >= rows) return;                                            // this wave has no rows: it brings words alone
     if (EDGE && (begin >= any_hi || begin + kBlock <= any_lo)) return;   // none that its rows see
-    f32x16 s[2];
+    if (bad_pages != 0u) {   // (a page holds 16 keys or more) a row that sees one of a page that is none
 #pragma unroll
-    for (int a = 0; a < 2; ++a) {
+      for (int g = 0; g < 4; ++g)
+        if ((bad_pages >> g & 1u) && mine.lo < begin + 16 * g + 16 && mine.hi > begin + 16 * g) l = NAN;
+    }
+    const uint32_t from_lo = (uint32_t)(begin + 8 * half - mine.lo), seen = (uint32_t)max(mine.hi - mine.lo, 0);
+    f32x16 s[2];
+    Weights w[2];
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[a][i] = 0.0f;
-    }
 #pragma unroll
     for (int i = 0; i < C::kSteps; ++i)
 #pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        const bf16x8 k = *reinterpret_cast<const bf16x8*>(from + (32 * a + col) * (2 * D) + ((2 * i + half) ^ C::swizzle(col)) * 16);
-        s[a] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[i], s[a], 0, 0, 0);
-      }
-    // score i of tile a: key 32a + 16 (i / 8) + 8 half + i % 8 of the block
+      for (int a = 0; a < 2; ++a) s[a] = score_step(in, a, i, s[a]);
     if constexpr (EDGE) {
-      if (bad_pages != 0u) {   // (a page holds 16 keys or more) a row that sees one of a page that is none
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          if ((bad_pages >> g & 1u) && mine.lo < begin + 16 * g + 16 && mine.hi > begin + 16 * g) l = NAN;
-      }
-      const uint32_t from_lo = (uint32_t)(begin + 8 * half - mine.lo), seen = (uint32_t)max(mine.hi - mine.lo, 0);
 #pragma unroll
       for (int a = 0; a < 2; ++a)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           s[a][i] = from_lo + (uint32_t)(32 * a + 16 * (i / 8) + i % 8) < seen ? s[a][i] : -INFINITY;
-    } else if (bad_pages != 0u) {   // every row sees every key
-      l = NAN;
     }
-    float top = s[0][0];
+    const float top = fmaxf(largest(s[0]), largest(s[1]));
+    if (__any(top > m + kSlack)) move_maximum(top > m + kSlack ? top : m);
+    float sum[2];
 #pragma unroll
-    for (int a = 0; a < 2; ++a)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[a][i]);
-    top = max_across(top) * log2_scale;
-    if (__any(top > m + 8.0f)) {
-      // (this row's maximum moves by its own scores alone, so that no row's bits depend on another's)
-      const float next = top > m + 8.0f ? top : m, shrink = next == m ? 1.0f : __builtin_amdgcn_exp2f(m - next);
-      m = next;
-      l *= shrink;
-#pragma unroll
-      for (int d = 0; d < C::kDTiles; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[d][i] *= shrink;
-    }
-    const float base = m == -INFINITY ? 0.0f : m;
-    bf16x8 w[4];
-    float sum[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int a = 0; a < 2; ++a)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[a][i], log2_scale, -base));
-        sum[a] += e;
-        w[2 * a + i / 8][i % 8] = (__bf16)e;
-      }
+    for (int a = 0; a < 2; ++a) exponentials(s[a], w[a], sum[a]);
     l += sum[0] + sum[1];
-    const char* values = from + C::kBytes + col * 128;
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int d = 0; d < C::kDTiles; ++d) {
-        const bf16x8 v = *reinterpret_cast<const bf16x8*>(values + d * 4096 + ((2 * u + half) ^ C::v_swizzle(col)) * 16);
-        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w[u], o[d], 0, 0, 0);
-      }
+    for (int a = 0; a < 2; ++a) values(in, a, w[a]);
   };
 
   // Values that some row does not see (or no row: what a page holds behind its last token) must not reach it,
   // NaN and Inf included, which a zero weight does not hold back. Where a block with such keys has any: a NaN
-  // into the sums of the rows that see them, and zeros in their place. (Each wave looks at a quarter of V^T.)
-  auto clean = [&](int block, char* in) {
+  // into the sums of the rows that see them, and zeros in their place. (Each wave looks at its part of V^T.)
+  auto clean = [&](int block, char* in) __attribute__((always_inline)) {
+    constexpr int kCleanLoads = D / (8 * W);
+    static_assert(D % (8 * W) == 0, "waves share V^T evenly");
     uint32_t any = 0u;
-    char* mine_v = in + C::kBytes + wave * (C::kBytes / 4) + lane * 16;
+    char* mine_v = in + C::kBytes + wave * (C::kBytes / W) + lane * 16;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
+    for (int i = 0; i < kCleanLoads; ++i) {
       const u32x4v v = *reinterpret_cast<const u32x4v*>(mine_v + 1024 * i);
 #pragma unroll
       for (int j = 0; j < 4; ++j) any |= not_finite_bf16x2(v[j]);
@@ -305,7 +358,10 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
     if (lane == 0) s_any[wave] = 0u;
     if (__any(any != 0u) && lane == 0) s_any[wave] = 1u;
     __syncthreads();
-    if ((s_any[0] | s_any[1] | s_any[2] | s_any[3]) == 0u) return;
+    any = 0u;
+#pragma unroll
+    for (int i = 0; i < W; ++i) any |= s_any[i];
+    if (any == 0u) return;
     const uint32_t from_lo = (uint32_t)((block << kBlockLog) + 8 * half - mine.lo), seen = (uint32_t)max(mine.hi - mine.lo, 0);
 #pragma unroll 1
     for (int u = 0; u < 4; ++u) {
@@ -331,7 +387,7 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
     }
     __syncthreads();
 #pragma unroll 1
-    for (int i = 0; i < D / 32; ++i) {
+    for (int i = 0; i < kCleanLoads; ++i) {
       u32x4v v = *reinterpret_cast<const u32x4v*>(mine_v + 1024 * i);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -345,35 +401,133 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
 
   if (sg.blocks > 0) {
     const int end = sg.block0 + sg.blocks;
-    char* now = smem;
-    char* then = smem + 2 * C::kBytes;
-    uint32_t bad = request(sg.block0, pages_of(sg.block0), now);
-    Pages pg = pages_of(min(sg.block0 + 1, end - 1));
-    place(now);
-    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): the words are in LDS
-    __syncthreads();
+    // The blocks of which every row of the tile sees all keys, [lead, full), and those before and behind them.
+    const int lead = min(max((all_lo + kBlock - 1) >> kBlockLog, sg.block0), end), full = min(max(all_hi >> kBlockLog, lead), end);
+    char* now = smem;                     // the block in use
+    char* then = smem + 2 * C::kBytes;    // the next one
     int block = sg.block0;
-    auto step = [&](auto edge) {
+    auto ahead = [&](int i) __attribute__((always_inline)) { return min(i, end - 1); };
+    Pages pg = pages_of(block);
+    request_k(block, pg, now);
+    uint32_t bad = request_v(block, pg, now);
+    pg = pages_of(ahead(block + 1));
+    place_k(now);
+    place_v(now);
+    arrive();
+    auto step = [&](auto edge) __attribute__((always_inline)) {
       uint32_t next_bad = 0u;
       if (block + 1 < end) {
-        next_bad = request(block + 1, pg, then);
-        pg = pages_of(min(block + 2, end - 1));
+        request_k(block + 1, pg, then);
+        next_bad = request_v(block + 1, pg, then);
+        pg = pages_of(ahead(block + 2));
       }
       if constexpr (decltype(edge)::value) clean(block, now);
       use(edge, block, now, bad);
-      if (block + 1 < end) place(then);
-      __builtin_amdgcn_s_waitcnt(0x0F70);
-      __syncthreads();
+      if (block + 1 < end) {
+        place_k(then);
+        place_v(then);
+      }
+      arrive();
       char* t = now;
       now = then;
       then = t;
       bad = next_bad;
       ++block;
     };
-    // the blocks of which every row of the tile sees all keys, and those before and behind them
-    const int lead = min(max((all_lo + kBlock - 1) >> kBlockLog, sg.block0), end), full = min(max(all_hi >> kBlockLog, lead), end);
     while (block < lead) step(std::true_type{});
-    while (block < full) step(std::false_type{});
+    if constexpr (!C::kPipelined) {
+      while (block < full) step(std::false_type{});
+    } else if (block < full) {
+      // Half a block at a time, in one stretch of code without branches: the scores of the next half, the
+      // exponentials of this one and the second product of the one before, which do not wait for each other, so
+      // that the matrix cores work while the exponentials are taken. Keys run a block ahead of values: K of the
+      // block two on is requested with V of the next one. The maximum stays, unless the sum of a half's
+      // exponentials shows that scores are far above it; then these are taken again.
+      uint32_t missing = bad;   // any key without a page: every row sees it
+      Pages pg2 = pages_of(ahead(block + 2));
+      if (block + 1 < end) request_k(block + 1, pg, then);
+      auto turn = [&]() __attribute__((always_inline)) {
+        char* t = now;
+        now = then;
+        then = t;
+      };
+      auto bring = [&]() __attribute__((always_inline)) {   // V of the next block, K of the one after it
+        bad = request_v(block + 1, pg, then);
+        missing |= bad;
+        if (block + 2 < end) request_k(block + 2, pg2, now);
+        pg = pg2;
+        pg2 = pages_of(ahead(block + 3));
+      };
+      auto have = [&]() __attribute__((always_inline)) {
+        place_v(then);
+        if (block + 2 < end) place_k(now);
+        arrive();
+        turn();
+        ++block;
+      };
+      auto bring_last = [&]() __attribute__((always_inline)) {   // (what follows brings its keys with its values)
+        if (block + 1 < end) bad = request_v(block + 1, pg, then);
+      };
+      auto have_last = [&]() __attribute__((always_inline)) {
+        if (block + 1 < end) place_v(then);
+        arrive();
+        pg = pg2;
+        turn();
+        ++block;
+      };
+      if (row0 < rows) {
+        f32x16 s0, s1;
+        Weights w0, w1;
+        float sum;
+        auto settle = [&](const f32x16& s, Weights& w) __attribute__((always_inline)) {
+          if (__any(sum > kHigh)) {
+            // (a row's maximum moves by its own scores alone, so that no row's bits depend on another's)
+            const float top = largest(s);
+            move_maximum(max_across(sum) > kHigh ? top : m);
+            exponentials(s, w, sum);
+          }
+          l += sum;
+        };
+        // from s1, the scores of the second half of `block`, and w0, the weights of its first, to the next block's
+        auto advance = [&]() __attribute__((always_inline)) {
+          bring();
+          scores(then, 0, s0);
+          exponentials(s1, w1, sum);
+          values(now, 0, w0);
+          settle(s1, w1);
+          scores(then, 1, s1);
+          exponentials(s0, w0, sum);
+          values(now, 1, w1);
+          settle(s0, w0);
+          have();
+        };
+        scores(now, 0, s0);
+        const float top = largest(s0);
+        if (__any(top > m + kSlack)) move_maximum(top > m + kSlack ? top : m);
+        scores(now, 1, s1);
+        exponentials(s0, w0, sum);
+        settle(s0, w0);
+        if (block + 1 < end) place_k(then);
+        arrive();
+        while (block + 1 < full) advance();
+        bring_last();
+        exponentials(s1, w1, sum);
+        values(now, 0, w0);
+        settle(s1, w1);
+        values(now, 1, w1);
+        have_last();
+      } else {   // a wave without rows brings words alone
+        if (block + 1 < end) place_k(then);
+        arrive();
+        while (block + 1 < full) {
+          bring();
+          have();
+        }
+        bring_last();
+        have_last();
+      }
+      if (missing != 0u) l = NAN;
+    }
     while (block < end) step(std::true_type{});
   }
   {
@@ -407,31 +561,43 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void chunk_kernel(c
   }
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, int W>
 hipError_t launch(const KvAttnArgs& a, hipStream_t stream) {
-  constexpr int lds = 4 * Chunk<D, FP8>::kBytes + kWaves * 4;
+  constexpr int lds = 4 * Chunk<D, FP8>::kBytes + W * 4;
   static std::atomic<uint64_t> done{0};
   if (lds > 65536) {
-    const hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(chunk_kernel<D, FP8>), lds, done);
+    const hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(chunk_kernel<D, FP8, W>), lds, done);
     if (e != hipSuccess) return e;
   }
-  const int64_t groups = kDivision.segments(a.batch.T, a.batch.B, a.Hkv, a.G) * a.Hkv;
-  chunk_kernel<D, FP8><<<dim3((unsigned)groups), kWaves * kWave, lds, stream>>>(a);
+  const int64_t groups = division(W).segments(a.batch.T, a.batch.B, a.Hkv, a.G) * a.Hkv;
+  chunk_kernel<D, FP8, W><<<dim3((unsigned)groups), W * kWave, lds, stream>>>(a);
   const hipError_t e = hipGetLastError();
-  return e != hipSuccess ? e : launch_join<FP8>(a, kDivision, stream);
+  return e != hipSuccess ? e : launch_join<FP8>(a, division(W), stream);
+}
+
+// Waves of a workgroup, by the rows of a sequence on average: many enough that tiles of 256 are whole ones, and
+// the head size where it is the faster (D 64 has three waves a SIMD with W 4: 614 us, 657 with 8).
+int waves_of(int T, int B, int G, int D) { return D == 128 && (int64_t)T * G >= (int64_t)1024 * B ? 8 : 4; }
+
+template <int D, bool FP8>
+hipError_t launch_w(const KvAttnArgs& a, hipStream_t stream) {
+  if constexpr (D == 128) {
+    if (waves_of(a.batch.T, a.batch.B, a.G, D) == 8) return launch<D, FP8, 8>(a, stream);
+  }
+  return launch<D, FP8, 4>(a, stream);
 }
 
 template <bool FP8>
 hipError_t launch_d(const KvAttnArgs& a, hipStream_t stream) {
   switch (a.D / 32) {
-    case 1: return launch<32, FP8>(a, stream);
-    case 2: return launch<64, FP8>(a, stream);
-    case 3: return launch<96, FP8>(a, stream);
-    case 4: return launch<128, FP8>(a, stream);
-    case 5: return launch<160, FP8>(a, stream);
-    case 6: return launch<192, FP8>(a, stream);
-    case 7: return launch<224, FP8>(a, stream);
-    case 8: return launch<256, FP8>(a, stream);
+    case 1: return launch_w<32, FP8>(a, stream);
+    case 2: return launch_w<64, FP8>(a, stream);
+    case 3: return launch_w<96, FP8>(a, stream);
+    case 4: return launch_w<128, FP8>(a, stream);
+    case 5: return launch_w<160, FP8>(a, stream);
+    case 6: return launch_w<192, FP8>(a, stream);
+    case 7: return launch_w<224, FP8>(a, stream);
+    case 8: return launch_w<256, FP8>(a, stream);
   }
   return hipErrorInvalidValue;
 }
@@ -440,7 +606,7 @@ hipError_t launch_d(const KvAttnArgs& a, hipStream_t stream) {
 
 size_t kv_attention_ws_bytes(int T, int B, int Hq, int Hkv, int D) {
   const int G = Hq / Hkv;
-  return kv_attention_few_fits(T, B, G) ? kv_attention_few_ws_bytes(Hkv, D) : kDivision.ws_bytes(Hkv, D);
+  return kv_attention_few_fits(T, B, G) ? kv_attention_few_ws_bytes(Hkv, D) : division(waves_of(T, B, G, D)).ws_bytes(Hkv, D);
 }
 
 hipError_t launch_kv_attention(const KvAttnArgs& a, hipStream_t stream) {
