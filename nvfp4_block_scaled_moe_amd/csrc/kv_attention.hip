@@ -59,7 +59,9 @@ struct Chunk {
   static constexpr int kBytes = kBlock * D * 2;      // of a block's keys, and of its values
   static constexpr int kSteps = D / 16;              // of the first product
   static constexpr int kDTiles = D / 32;             // of the second
-  static constexpr bool kPipelined = D <= 224;       // (its sums and queries leave registers for two halves' scores)
+  // (E4M3 of D 256: the words on their way leave no registers for two halves' scores; 752 us, 809 pipelined, for 2048
+  // new tokens over 6000; bf16 696 pipelined, 820 not)
+  static constexpr bool kPipelined = !FP8 || D <= 224;
   // LDS serves 16 lanes' 16-byte words a cycle where they lie in different 16ths of its 256-byte lines. A
   // product reads one word of 16 rows at once, so word w of row r lies at w ^ swizzle(r): the rows' own
   // places in the lines (kWords 16ths apart) and the swizzle make 16 different ones.
@@ -244,6 +246,7 @@ __global__ __launch_bounds__(W* kWave, D > 128 ? 1 : 2) void chunk_kernel(const 
 
   float m = -INFINITY, base = 0.0f, l = 0.0f;   // base: what exponentials are taken from, m or (before any key) 0
   f32x16 o[C::kDTiles];
+  uint32_t lost[(C::kDTiles + 1) / 2] = {};   // bit 16 (d % 2) + i: o[d][i] is to be NaN
 #pragma unroll
   for (int d = 0; d < C::kDTiles; ++d)
 #pragma unroll
@@ -342,8 +345,8 @@ __global__ __launch_bounds__(W* kWave, D > 128 ? 1 : 2) void chunk_kernel(const 
   };
 
   // Values that some row does not see (or no row: what a page holds behind its last token) must not reach it,
-  // NaN and Inf included, which a zero weight does not hold back. Where a block with such keys has any: a NaN
-  // into the sums of the rows that see them, and zeros in their place. (Each wave looks at its part of V^T.)
+  // NaN and Inf included, which a zero weight does not hold back. Where a block with such keys has any: zeros in
+  // their place, and the dims that they spoil in the rows that see them are kept as bits, for the end. (Each wave looks at its part of V^T.)
   auto clean = [&](int block, char* in) __attribute__((always_inline)) {
     constexpr int kCleanLoads = D / (8 * W);
     static_assert(D % (8 * W) == 0, "waves share V^T evenly");
@@ -382,7 +385,7 @@ __global__ __launch_bounds__(W* kWave, D > 128 ? 1 : 2) void chunk_kernel(const 
         for (int i = 0; i < 16; ++i) n[i] = 0.0f;
         n = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, bad), sees, n, 0, 0, 0);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[d][i] = n[i] > 0.0f ? NAN : o[d][i];
+        for (int i = 0; i < 16; ++i) lost[d / 2] |= n[i] > 0.0f ? 1u << (16 * (d % 2) + i) : 0u;
       }
     }
     __syncthreads();
@@ -534,6 +537,15 @@ __global__ __launch_bounds__(W* kWave, D > 128 ? 1 : 2) void chunk_kernel(const 
     const u32x2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
     l = __uint_as_float(r[0]) + __uint_as_float(r[1]);
   }
+  uint32_t any_lost = 0u;
+#pragma unroll
+  for (int d = 0; d < (C::kDTiles + 1) / 2; ++d) any_lost |= lost[d];
+  if (any_lost != 0u) {
+#pragma unroll
+    for (int d = 0; d < C::kDTiles; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[d][i] = lost[d / 2] >> (16 * (d % 2) + i) & 1u ? NAN : o[d][i];
+  }
   if (row0 + col >= rows) return;
   // this lane: dims 32 d + 8 (i / 4) + 4 half + i % 4 of its row
   if (sg.parts > 1) {
@@ -575,14 +587,18 @@ hipError_t launch(const KvAttnArgs& a, hipStream_t stream) {
   return e != hipSuccess ? e : launch_join<FP8>(a, division(W), stream);
 }
 
-// Waves of a workgroup, by the rows of a sequence on average: many enough that tiles of 256 are whole ones, and
-// the head size where it is the faster (D 64 has three waves a SIMD with W 4: 614 us, 657 with 8).
-int waves_of(int T, int B, int G, int D) { return D == 128 && (int64_t)T * G >= (int64_t)1024 * B ? 8 : 4; }
+// Waves of a workgroup. 8 for D 128 (D 64 has three waves a SIMD with W 4: 614 us, 657 with 8), where sequences have
+// rows for whole tiles of 256, on average, and keys enough that what these bring is most of the time: 2048 new tokens
+// over 14000 keys 950 us, 1013 with 4, 128 over 30000 136 and 146; but 8 prompts of 1024 tokens 222, 215 with 4.
+bool many_rows(int T, int B, int G, int D) { return D == 128 && (int64_t)T * G >= (int64_t)1024 * B; }
+int waves_of(const KvAttnArgs& a) {
+  return many_rows(a.batch.T, a.batch.B, a.G, a.D) && (int64_t)a.batch.cols << a.batch.page_log >= 4096 ? 8 : 4;
+}
 
 template <int D, bool FP8>
 hipError_t launch_w(const KvAttnArgs& a, hipStream_t stream) {
   if constexpr (D == 128) {
-    if (waves_of(a.batch.T, a.batch.B, a.G, D) == 8) return launch<D, FP8, 8>(a, stream);
+    if (waves_of(a) == 8) return launch<D, FP8, 8>(a, stream);
   }
   return launch<D, FP8, 4>(a, stream);
 }
@@ -606,7 +622,9 @@ hipError_t launch_d(const KvAttnArgs& a, hipStream_t stream) {
 
 size_t kv_attention_ws_bytes(int T, int B, int Hq, int Hkv, int D) {
   const int G = Hq / Hkv;
-  return kv_attention_few_fits(T, B, G) ? kv_attention_few_ws_bytes(Hkv, D) : division(waves_of(T, B, G, D)).ws_bytes(Hkv, D);
+  if (kv_attention_few_fits(T, B, G)) return kv_attention_few_ws_bytes(Hkv, D);
+  const size_t w4 = division(4).ws_bytes(Hkv, D), w8 = many_rows(T, B, G, D) ? division(8).ws_bytes(Hkv, D) : 0;
+  return w4 > w8 ? w4 : w8;   // (which of the two depends on the page table's columns, too)
 }
 
 hipError_t launch_kv_attention(const KvAttnArgs& a, hipStream_t stream) {
