@@ -108,6 +108,34 @@ __device__ __forceinline__ double position_at(const void* p, int pos64, int64_t 
   return pos64 ? (double)static_cast<const int64_t*>(p)[t] : (double)static_cast<const int*>(p)[t];
 }
 
+// A thread's walk over the items of a workgroup's tokens (token, head, item of the head), one of every kThreads:
+// divisions at its start alone.
+struct Walk {
+  int items, heads;   // of a head; of a token
+  int dt, dh, dj;     // kThreads items on
+};
+Walk walk_of(int items, int heads) {
+  const int token = items > 0 ? items * heads : 1, rest = kThreads % token;
+  return {items, heads, kThreads / token, items > 0 ? rest / items : 0, items > 0 ? rest % items : 0};
+}
+struct At {
+  int t, h, j;
+  __device__ __forceinline__ At(const Walk& w) {
+    const int i = threadIdx.x, token = w.items * w.heads;
+    t = i / token;
+    const int r = i - t * token;
+    h = r / w.items;
+    j = r - h * w.items;
+  }
+  __device__ __forceinline__ void next(const Walk& w) {
+    j += w.dj;
+    h += w.dh;
+    t += w.dt;
+    if (j >= w.items) j -= w.items, ++h;
+    if (h >= w.heads) h -= w.heads, ++t;
+  }
+};
+
 // One item of a head: VEC pairs that are turned, or VEC dims that are not. An item's places in the
 // head: the dims [a, a + VEC) and [b, b + VEC).
 template <int VEC>
@@ -148,7 +176,7 @@ __device__ __forceinline__ void turn_pairs(float (&u)[VEC], float (&w)[VEC], con
 }
 
 template <typename T, int VEC>
-__global__ __launch_bounds__(kThreads) void rope_kernel(const RopeArgs p, int tokens) {
+__global__ __launch_bounds__(kThreads) void rope_kernel(const RopeArgs p, int tokens, Walk walk) {
   extern __shared__ float2 cs[];   // [tokens, rot / 2]
   const int t0 = blockIdx.x * tokens, nt = min(tokens, p.T - t0), half = p.turn.rot / 2;
   for (int i = threadIdx.x; i < nt * half; i += kThreads) {
@@ -156,12 +184,12 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeArgs p, int to
     cs[i] = turn_of(position_at(p.positions, p.pos64, t0 + t), p.turn.freqs[i - t * half], p.turn);
   }
   __syncthreads();
-  const int per_head = p.turn.rot / (2 * VEC) + (p.copy ? (p.D - p.turn.rot) / VEC : 0), per_token = per_head * p.H;
   const T* x = static_cast<const T*>(p.x.p);
   T* out = static_cast<T*>(const_cast<void*>(p.out.p));
-  for (int i = threadIdx.x; i < nt * per_token; i += kThreads) {
-    const int t = i / per_token, h = (i - t * per_token) / per_head;
-    const Item<VEC> it(i - t * per_token - h * per_head, p.turn);
+  if (walk.items == 0) return;
+  for (At at(walk); at.t < nt; at.next(walk)) {
+    const int t = at.t, h = at.h;
+    const Item<VEC> it(at.j, p.turn);
     const T* from = x + (t0 + t) * p.x.row + h * p.x.head;
     T* to = out + (t0 + t) * p.out.row + h * p.out.head;
     float u[VEC], w[VEC];
@@ -215,7 +243,7 @@ __device__ __forceinline__ Place place_of(const KvAppendArgs& p, int t, const in
 // the values of v_tokens (a power of two) of one head each, which are not turned.
 template <int VEC, bool FP8>
 __global__ __launch_bounds__(kThreads) void kv_append_kernel(const KvAppendArgs p, int tokens, int turn_groups,
-                                                             int v_tokens_log) {
+                                                             int v_tokens_log, Walk walk) {
   extern __shared__ float2 cs[];
   __shared__ Place place[kTokens];
   __shared__ int s_starts[kStarts];
@@ -234,12 +262,10 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(const KvAppendArgs 
       cs[i] = turn_of(place[t].position, p.turn.freqs[i - t * half], p.turn);
     }
     __syncthreads();
-    const int per_turn = 2 * half / (2 * VEC), per_head = per_turn + (D - 2 * half) / VEC;
-    const int heads = p.Hkv + (p.q.p ? p.Hq : 0), per_token = per_head * heads;
-    for (int i = threadIdx.x; i < nt * per_token; i += kThreads) {
-      const int t = i / per_token;
-      int h = (i - t * per_token) / per_head;
-      const Item<VEC> it(i - t * per_token - h * per_head, p.turn);
+    for (At at(walk); at.t < nt; at.next(walk)) {
+      const int t = at.t;
+      int h = at.h;   // key heads, then query heads
+      const Item<VEC> it(at.j, p.turn);
       const Place w = place[t];
       const bool key = h < p.Hkv;
       if (w.row < 0 || (key && w.page_first < 0) || (!key && !p.copy && it.pair < 0)) continue;
@@ -288,17 +314,19 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(const KvAppendArgs 
     }
     __syncthreads();
     const float s = FP8 && p.v_scale ? p.v_scale[h] : 1.0f;
-    for (int i = threadIdx.x; i < D << v_tokens_log; i += kThreads) {
-      const int t = i & (v_tokens - 1), d = i >> v_tokens_log;
-      const Place& w = place[t];
-      if (w.page_first < 0) continue;
-      const int64_t at = w.page_first + ((int64_t)h * D + d) * b.page + w.slot;
-      const uint16_t x = tile[t * pitch + d];
+    // (a thread always has the same token: v_tokens divides kThreads)
+    const int t = threadIdx.x & (v_tokens - 1);
+    const Place w = place[t];
+    if (w.page_first < 0) return;
+    const int step = kThreads >> v_tokens_log;
+    int64_t at = w.page_first + ((int64_t)h * D + (threadIdx.x >> v_tokens_log)) * b.page + w.slot;
+    for (int d = threadIdx.x >> v_tokens_log; d < D; d += step, at += step * b.page) {
+      const uint16_t y = tile[t * pitch + d];
       if (FP8)
         static_cast<uint8_t*>(p.v_cache)[at] =
-            (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(to_e4m3_range(bf16_to_f32(x), s), 0.0f, 0, false);
+            (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(to_e4m3_range(bf16_to_f32(y), s), 0.0f, 0, false);
       else
-        static_cast<uint16_t*>(p.v_cache)[at] = x;
+        static_cast<uint16_t*>(p.v_cache)[at] = y;
     }
   }
 }
@@ -306,7 +334,7 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(const KvAppendArgs 
 // Columns that one access may take: 8, 4 or 1 elements, by the sizes, distances and addresses.
 int vector_of(const RopeTurn& t, int D, std::initializer_list<HeadRows> rows, int size) {
   const int rot = t.freqs ? t.rot : 0;
-  for (int v = 8; v > 1; v /= 2) {
+  for (int v = 8; v >= 4; v /= 2) {
     bool fits = rot % (2 * v) == 0 && (rot == 0 || t.start % v == 0) && D % v == 0;
     for (const HeadRows& r : rows)
       fits = fits && (!r.p || (r.row % v == 0 && r.head % v == 0 &&
@@ -333,12 +361,13 @@ hipError_t launch_rope(const RopeArgs& a, hipStream_t stream) {
   const int v = vector_of(a.turn, a.D, {a.x, a.out}, a.bf16 ? 2 : 4);
   const dim3 grid((unsigned)((a.T + tokens - 1) / tokens));
   const size_t lds = (size_t)tokens * half * sizeof(float2);
+  const Walk walk = walk_of(a.turn.rot / (2 * v) + (a.copy ? (a.D - a.turn.rot) / v : 0), a.H);
   if (a.bf16) {
     auto k = v == 8 ? rope_kernel<uint16_t, 8> : v == 4 ? rope_kernel<uint16_t, 4> : rope_kernel<uint16_t, 1>;
-    k<<<grid, kThreads, lds, stream>>>(a, tokens);
+    k<<<grid, kThreads, lds, stream>>>(a, tokens, walk);
   } else {
     auto k = v == 8 ? rope_kernel<float, 8> : v == 4 ? rope_kernel<float, 4> : rope_kernel<float, 1>;
-    k<<<grid, kThreads, lds, stream>>>(a, tokens);
+    k<<<grid, kThreads, lds, stream>>>(a, tokens, walk);
   }
   return hipGetLastError();
 }
@@ -357,7 +386,8 @@ hipError_t launch_kv_append(const KvAppendArgs& a0, hipStream_t stream) {
   if (v_lds > lds) lds = v_lds;
   auto k = a.fp8 ? (v == 8 ? kv_append_kernel<8, true> : v == 4 ? kv_append_kernel<4, true> : kv_append_kernel<1, true>)
                  : (v == 8 ? kv_append_kernel<8, false> : v == 4 ? kv_append_kernel<4, false> : kv_append_kernel<1, false>);
-  k<<<dim3((unsigned)(turn_groups + v_groups)), kThreads, lds, stream>>>(a, tokens, turn_groups, v_log);
+  k<<<dim3((unsigned)(turn_groups + v_groups)), kThreads, lds, stream>>>(
+      a, tokens, turn_groups, v_log, walk_of(half / v + (a.D - 2 * half) / v, a.Hkv + (a.q.p ? a.Hq : 0)));
   return hipGetLastError();
 }
 
