@@ -235,6 +235,13 @@ __device__ __forceinline__ bf16x8 e4m3x8_to_bf16(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(bf16x8, (u32x4v){x[0], x[1], y[0], y[1]});
 }
 
+// Eight E4M3 bytes as f16 (exact).
+__device__ __forceinline__ f16x8 e4m3x8_to_f16(uint32_t a, uint32_t b) {
+  const f16x2 p = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, false), q = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, true);
+  const f16x2 r = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false), s = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, true);
+  return (f16x8){p[0], p[1], q[0], q[1], r[0], r[1], s[0], s[1]};
+}
+
 // For values that only some of a tile's rows see: a product with a zero weight must not let a NaN or
 // Inf into the rows that do not see it. Two bf16 (a word) with those replaced by 0; `bad` gets a bit
 // pattern that is not zero for each of them.
@@ -243,9 +250,6 @@ __device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w, uint32_t& bad) {
   bad = lo | hi;
   return w & ~bad;
 }
-
-// Bits that are not zero where one of two bf16 (a word) is NaN or Inf.
-__device__ __forceinline__ uint32_t not_finite_bf16x2(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 
 // Four E4M3 bytes with NaN (0x7f, 0xff) replaced by 0.
 __device__ __forceinline__ uint32_t finite_e4m3x4(uint32_t w) {

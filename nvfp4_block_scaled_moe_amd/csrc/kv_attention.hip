@@ -12,10 +12,10 @@
 // of O^T = V^T P^T without another move. The rows of LDS are not padded; their 16-byte words are
 // permuted by the row, so that reads have no bank conflicts.
 //
-// Weights of the second product are exponentials rounded to bf16 (2^-9 of each, about as much again
-// as the rounding of the output; two bf16 values each would cost half the second product again).
-// Their sum is taken before that rounding. The running maximum is moved only when a score exceeds it
-// by 2^8: until then weights of up to 2^8 keep their relative precision.
+// Weights of the second product are exponentials rounded to bf16 (about as much again as the rounding of the
+// output; two bf16 values each would cost half the second product again) or, with an E4M3 cache, to f16. Their
+// sum is taken before that rounding. The running maximum is moved only when scores are far above it: until then
+// weights above 1 keep their relative precision.
 //
 // The work is divided as Division says; where a tile is split, its parts leave unnormalised sums, which a
 // second launch joins.
@@ -29,7 +29,7 @@ namespace nvfp4moe {
 namespace {
 
 constexpr float kSlack = 8.0f;        // base 2 logits by which a score may exceed the running maximum,
-constexpr float kHigh = 1099511627776.0f;   // and, where that is looked at by the sums alone, sum of 16 exponentials (2^40)
+constexpr float kHigh = 32768.0f;     // and, where that is looked at by the sums alone, sum of 16 weights (2^15)
 constexpr int kBlockLog = 6, kBlock = 1 << kBlockLog;   // keys of a block
 // Waves of a workgroup (W): 4, two workgroups a CU, or 8, one a CU, whose tiles of 256 rows bring half the words for
 // a row. The segments are as many as workgroups that a CU holds at once (with W 4 and 1024 segments, 8192 new
@@ -52,6 +52,33 @@ __device__ __forceinline__ float max_across(float v) {
   const u32x2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
+
+// Numbers of the second product: bf16 as the cache holds them, or f16 for E4M3, which f16 holds as exactly and whose
+// weights then have 11 bits instead of 8. f16 ends at 65504 and, below, at 2^-24: weights are taken times 2^kRaise,
+// which leaves kSlack above, and below the maximum 2^-31 (a million keys of less are together less than 2^-11).
+template <bool F16>
+struct Second {
+  typedef __bf16 T;
+  typedef bf16x8 V;
+  static constexpr float kRaise = 0.0f;
+  static constexpr uint32_t kExponent = 0x7f807f80u, kOne = 0x00800080u;
+  static __device__ __forceinline__ f32x16 product(V a, V b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
+};
+template <>
+struct Second<true> {
+  typedef _Float16 T;
+  typedef f16x8 V;
+  static constexpr float kRaise = 7.0f;
+  static constexpr uint32_t kExponent = 0x7c007c00u, kOne = 0x04000400u;
+  static __device__ __forceinline__ f32x16 product(V a, V b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
+};
+// Bit 15 and 31: those of two such numbers (a word) that are NaN or Inf.
+template <bool F16>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  return ((w & Second<F16>::kExponent) + Second<F16>::kOne) & 0x80008000u;
+}
+// All 16 bits of each of those.
+__device__ __forceinline__ uint32_t halves_of(uint32_t bits) { return (bits >> 15) * 0xffffu; }
 
 template <int D, bool FP8>
 struct Chunk {
@@ -78,6 +105,7 @@ __device__ __forceinline__ int key_of_row(int r) { return r / 4 % 2 * 8 + r / 8 
 template <int D, bool FP8, int W>
 __global__ __launch_bounds__(W* kWave, D > 128 ? 1 : 2) void chunk_kernel(const KvAttnArgs p) {
   using C = Chunk<D, FP8>;
+  using S2 = Second<FP8>;
   constexpr Division kDivision = division(W);
   constexpr int kRows = kDivision.tile_rows;
   extern __shared__ __attribute__((aligned(16))) char smem[];   // two of: keys [64, D], values [D, 64]; then
@@ -210,10 +238,14 @@ __global__ __launch_bounds__(W* kWave, D > 128 ? 1 : 2) void chunk_kernel(const 
     const uint64_t bad = __ballot(!v_ok);   // (lanes of the first row of V^T: of each 16 keys one)
     return FP8 ? (uint32_t)(bad & 15u) : (uint32_t)((bad & 1u) | (bad >> 1 & 2u) | (bad >> 2 & 4u) | (bad >> 3 & 8u));
   };
-  // E4M3: what they brought, as bf16, into LDS.
-  auto put = [&](char* at0, char* at1, const u32x4v& w) __attribute__((always_inline)) {
+  // E4M3: what they brought, keys as bf16 and values as f16, into LDS.
+  auto put_k = [&](char* at0, char* at1, const u32x4v& w) __attribute__((always_inline)) {
     *reinterpret_cast<bf16x8*>(at0) = e4m3x8_to_bf16(w[0], w[1]);
     *reinterpret_cast<bf16x8*>(at1) = e4m3x8_to_bf16(w[2], w[3]);
+  };
+  auto put_v = [&](char* at0, char* at1, const u32x4v& w) __attribute__((always_inline)) {
+    *reinterpret_cast<f16x8*>(at0) = e4m3x8_to_f16(w[0], w[1]);
+    *reinterpret_cast<f16x8*>(at1) = e4m3x8_to_f16(w[2], w[3]);
   };
   auto place_k = [&](char* to) __attribute__((always_inline)) {
     if constexpr (FP8) {
@@ -223,7 +255,7 @@ __global__ __launch_bounds__(W* kWave, D > 128 ? 1 : 2) void chunk_kernel(const 
         if (kKAll % W != 0 && n >= kKAll) break;
         const int r = key_of_row(i / (D / 16)), w = i % (D / 16) * 2;   // (key_of_row is its own inverse)
         char* line = to + (n / kKParts * 16 + r) * (2 * D);
-        if (D % 64 == 0 || i < D) put(line + (w ^ C::swizzle(r)) * 16, line + ((w + 1) ^ C::swizzle(r)) * 16, raw_k[j]);
+        if (D % 64 == 0 || i < D) put_k(line + (w ^ C::swizzle(r)) * 16, line + ((w + 1) ^ C::swizzle(r)) * 16, raw_k[j]);
       }
     }
   };
@@ -234,7 +266,7 @@ __global__ __launch_bounds__(W* kWave, D > 128 ? 1 : 2) void chunk_kernel(const 
         const int d = (v_load0 + j) * 16 + v_row, x = C::v_swizzle(d);
         if (kVAll % W != 0 && (v_load0 + j) * 16 >= D) break;
         char* line = to + C::kBytes + d * 128;
-        put(line + ((2 * v_word) ^ x) * 16, line + ((2 * v_word + 1) ^ x) * 16, raw_v[j]);
+        put_v(line + ((2 * v_word) ^ x) * 16, line + ((2 * v_word + 1) ^ x) * 16, raw_v[j]);
       }
     }
   };
@@ -244,7 +276,7 @@ __global__ __launch_bounds__(W* kWave, D > 128 ? 1 : 2) void chunk_kernel(const 
     __syncthreads();
   };
 
-  float m = -INFINITY, base = 0.0f, l = 0.0f;   // base: what exponentials are taken from, m or (before any key) 0
+  float m = -INFINITY, base = 0.0f, l = 0.0f;   // base: what exponentials are taken from (0 before any key)
   f32x16 o[C::kDTiles];
   uint32_t lost[(C::kDTiles + 1) / 2] = {};   // bit 16 (d % 2) + i: o[d][i] is to be NaN
 #pragma unroll
@@ -255,7 +287,7 @@ __global__ __launch_bounds__(W* kWave, D > 128 ? 1 : 2) void chunk_kernel(const 
   // The pieces of a step, for half a block (32 keys): scores; their exponentials as weights of the second product;
   // that product. Score i of tile a: key 32a + 16 (i / 8) + 8 half + i % 8 of the block.
   struct Weights {
-    bf16x8 w[2];
+    typename S2::V w[2];
   };
   auto score_step = [&](const char* in, int a, int i, const f32x16& s) __attribute__((always_inline)) {
     const bf16x8 k = *reinterpret_cast<const bf16x8*>(in + (32 * a + col) * (2 * D) + ((2 * i + half) ^ C::swizzle(col)) * 16);
@@ -273,7 +305,7 @@ __global__ __launch_bounds__(W* kWave, D > 128 ? 1 : 2) void chunk_kernel(const 
     for (int i = 0; i < 16; ++i) {
       const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], log2_scale, -base));
       sum += e;
-      w.w[i / 8][i % 8] = (__bf16)e;
+      w.w[i / 8][i % 8] = (typename S2::T)e;
     }
   };
   auto values = [&](const char* in, int a, const Weights& w) __attribute__((always_inline)) {
@@ -282,8 +314,9 @@ __global__ __launch_bounds__(W* kWave, D > 128 ? 1 : 2) void chunk_kernel(const 
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int d = 0; d < C::kDTiles; ++d) {
-        const bf16x8 v = *reinterpret_cast<const bf16x8*>(rows_at + d * 4096 + ((4 * a + 2 * u + half) ^ C::v_swizzle(col)) * 16);
-        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w.w[u], o[d], 0, 0, 0);
+        const typename S2::V v =
+            *reinterpret_cast<const typename S2::V*>(rows_at + d * 4096 + ((4 * a + 2 * u + half) ^ C::v_swizzle(col)) * 16);
+        o[d] = S2::product(v, w.w[u], o[d]);
       }
   };
   // Largest score of each row, times the scale.
@@ -297,7 +330,7 @@ __global__ __launch_bounds__(W* kWave, D > 128 ? 1 : 2) void chunk_kernel(const 
   auto move_maximum = [&](float next) __attribute__((always_inline)) {
     const float shrink = next == m ? 1.0f : __builtin_amdgcn_exp2f(m - next);
     m = next;
-    base = m == -INFINITY ? 0.0f : m;
+    base = m == -INFINITY ? 0.0f : m - S2::kRaise;
     l *= shrink;
 #pragma unroll
     for (int d = 0; d < C::kDTiles; ++d)
@@ -356,7 +389,7 @@ __global__ __launch_bounds__(W* kWave, D > 128 ? 1 : 2) void chunk_kernel(const 
     for (int i = 0; i < kCleanLoads; ++i) {
       const u32x4v v = *reinterpret_cast<const u32x4v*>(mine_v + 1024 * i);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) any |= not_finite_bf16x2(v[j]);
+      for (int j = 0; j < 4; ++j) any |= not_finite<FP8>(v[j]);
     }
     if (lane == 0) s_any[wave] = 0u;
     if (__any(any != 0u) && lane == 0) s_any[wave] = 1u;
@@ -375,11 +408,7 @@ __global__ __launch_bounds__(W* kWave, D > 128 ? 1 : 2) void chunk_kernel(const 
       for (int d = 0; d < C::kDTiles; ++d) {
         u32x4v bad = *reinterpret_cast<const u32x4v*>(in + C::kBytes + (32 * d + col) * 128 + ((2 * u + half) ^ C::v_swizzle(col)) * 16);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t bits;
-          finite_bf16x2(bad[i], bits);
-          bad[i] = bits & 0x3f803f80u;   // 1.0 for each
-        }
+        for (int i = 0; i < 4; ++i) bad[i] = halves_of(not_finite<FP8>(bad[i])) & 0x3f803f80u;   // a bf16 1 for each
         f32x16 n;   // how many of them each row sees
 #pragma unroll
         for (int i = 0; i < 16; ++i) n[i] = 0.0f;
@@ -393,10 +422,7 @@ __global__ __launch_bounds__(W* kWave, D > 128 ? 1 : 2) void chunk_kernel(const 
     for (int i = 0; i < kCleanLoads; ++i) {
       u32x4v v = *reinterpret_cast<const u32x4v*>(mine_v + 1024 * i);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t bits;
-        v[j] = finite_bf16x2(v[j], bits);
-      }
+      for (int j = 0; j < 4; ++j) v[j] &= ~halves_of(not_finite<FP8>(v[j]));
       *reinterpret_cast<u32x4v*>(mine_v + 1024 * i) = v;
     }
     __syncthreads();

@@ -235,3 +235,98 @@ def test_pages_past_32_bits():
         want, tol = c.attention()
         got = ops.kv_cache_attention(c.q.cuda(), cache, ops.CacheBatch(table.cuda(), c.batch.lengths, c.batch.starts))
         check(got, want, tol)
+
+
+# Tiles of 256 rows: heads of 128 dims, 1024 rows or more of a sequence on average, page tables of 4096 tokens or more.
+WIDE = [
+    ([150], [4200], 8, 1, 128, 64),
+    ([128], [4000], 8, 1, 128, 16),          # the last tile whole
+    ([300, 10, 0], [4100, 33, 0], 16, 1, 128, 32),
+    ([257], [5000], 12, 3, 128, 128),
+    ([1030], [3500], 1, 1, 128, 1024),
+    ([40], [9000], 32, 1, 128, 64),
+]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("case", range(len(WIDE)))
+def test_tiles_of_256_rows(case, fp8):
+    c = Case(*WIDE[case], fp8=fp8, seed=200 + case)
+    assert c.rows() >= 1024 and c.table.shape[1] * c.page >= 4096
+    _run(c)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("window", [1, 63, 130, 1000])
+def test_windows_of_tiles_of_256_rows(window, fp8):
+    c = Case([150, 140], [4000, 30], 8, 1, 128, 16, fp8=fp8, seed=window)
+    _run(c, window=window)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_what_tiles_of_256_rows_do_not_see(fp8):
+    c = Case([160], [4000], 8, 1, 128, 64, fp8=fp8, seed=12)
+    clean = ops.kv_cache_attention(c.q.cuda(), c.cache, c.batch).cpu()
+    p = 4000 + 100
+    v = c.cache.v.clone()
+    v.view(torch.uint8 if fp8 else torch.int16)[int(c.table[0, p // 64]), 0, 77, p % 64] = 0x7F if fp8 else 0x7FC0
+    got = ops.kv_cache_attention(c.q.cuda(), ops.KVCache(c.cache.k, v, c.cache.k_scale, c.cache.v_scale), c.batch).cpu()
+    keep = [d for d in range(128) if d != 77]
+    assert torch.equal(got[:100], clean[:100]) and torch.equal(got[100:, :, keep], clean[100:, :, keep])
+    assert torch.isnan(got[100:, :, 77]).all()
+    for page, window in ((3, 0), (60, 150)):
+        table = c.table.clone()
+        table[0, page] = -1
+        batch = ops.CacheBatch(table.cuda(), c.batch.lengths, c.batch.starts)
+        want = ops.kv_cache_attention(c.q.cuda(), c.cache, c.batch, window=window).cpu()
+        got = ops.kv_cache_attention(c.q.cuda(), c.cache, batch, window=window).cpu()
+        sees = torch.tensor([not window or 4000 + i - window + 1 < 64 * page + 64 for i in range(160)])
+        assert torch.isnan(got[sees]).all() and torch.equal(got[~sees], want[~sees])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("new", [[1], [40], [150]])
+def test_scores_that_grow(new, fp8):
+    """Scores that rise along the keys by far more than exponentials hold, and fall again."""
+    c = Case(new, [4200], 8, 1, 128, 64, fp8=fp8, seed=13)
+    n = c.total[0]
+    ramp = torch.cat((torch.linspace(0.0, 1.0, n // 2), torch.linspace(1.0, -1.0, n - n // 2)))
+    if fp8:
+        ramp = ramp / 0.02
+    k = torch.zeros_like(c.cache.k).float()
+    at = torch.arange(n)
+    k[c.table[0].long()[at // 64].cuda(), 0, (at % 64).cuda(), 0] = ramp.cuda()
+    k = k.to(c.cache.k.dtype)
+    c.q[..., 0] = 8.0
+    c.keys = [torch.zeros((n, 1, 128), dtype=torch.float64)]
+    scale = c.k_scale.double() if fp8 else torch.ones(1).double()
+    c.keys[0][:, 0, 0] = k.float().cpu()[c.table[0].long()[at // 64], 0, at % 64, 0].double() * scale
+    c.cache = ops.KVCache(k, c.cache.v, c.cache.k_scale, c.cache.v_scale)
+    _run(c, scale=12.0)      # up to about 100 above the first
+    _run(c, scale=0.5)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("new", [[1], [40], [150]])
+def test_many_small_weights_beside_a_large_one(new, fp8):
+    """The first key takes nearly all of each row, with a value of zero; the others, 2^-23 of it each, are the output."""
+    c = Case(new, [4200], 8, 1, 128, 64, fp8=fp8, seed=14)
+    n = c.total[0]
+    k, v = torch.zeros_like(c.cache.k).float(), c.cache.v.float()
+    first = int(c.table[0, 0])
+    k[first, 0, 0, 0] = 16.0
+    v[first, 0, :, 0] = 0.0
+    c.q[..., 0] = 1.0
+    scale = c.k_scale.double() if fp8 else torch.ones(1).double()
+    c.keys = [torch.zeros((n, 1, 128), dtype=torch.float64)]
+    c.keys[0][0, 0, 0] = 16.0 * scale[0]
+    c.values[0][0] = 0.0
+    c.cache = ops.KVCache(k.to(c.cache.k.dtype), v.to(c.cache.v.dtype), c.cache.k_scale, c.cache.v_scale)
+    _run(c, scale=float(1.0 / scale[0]))
+
+
+@pytest.mark.parametrize("new", [[1], [40], [150]])
+def test_large_values(new):
+    """Values near the end of bf16 (3.4e38), as far from it as 2^16 weights of up to 2^8 need."""
+    c = Case(new, [4200], 8, 1, 128, 64, seed=15, v_spread=1e30)
+    _run(c, scale=1.0)
