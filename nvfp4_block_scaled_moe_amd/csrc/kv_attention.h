@@ -168,58 +168,65 @@ struct Sums {
   }
 };
 
-// Joins the parts of a tile: a workgroup `together` of its rows for one head, of which each thread holds 4 dims
-// of every groups-th part; in a fixed order.
-constexpr int kJoinThreads = 256;
+// Joins the parts of a tile: a workgroup takes `turns` times `together` of its rows for one head, of which each
+// thread holds 4 dims of every groups-th part; in a fixed order. Where little is split, what this costs is finding
+// that out in every workgroup (8192 of them 13 us, 2048 6 to 8), so there are no more than the CUs hold at once.
+constexpr int kJoinThreads = 256, kJoinGroups = 2048;
 namespace {   // (a kernel of each file's own)
 template <bool FP8>
-__global__ __launch_bounds__(kJoinThreads) void join_kernel(const KvAttnArgs p, const Division v, int together) {
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(const KvAttnArgs p, const Division v, int together, int turns) {
   __shared__ float4 s_o[kJoinThreads];
   __shared__ float2 s_ml[kJoinThreads];
-  const int sets = v.tile_rows / together, h = blockIdx.x / sets % p.Hkv;
+  const int sets = v.tile_rows / (together * turns), h = blockIdx.x / sets % p.Hkv;
   const Segment sg = segment_of<true>(p, v, blockIdx.x / sets / p.Hkv);
   if (!sg.found) return;
   const int lanes = p.D / 4, groups = kJoinThreads / (lanes * together);
-  const int lane = threadIdx.x % lanes, group = threadIdx.x / lanes % groups, r = blockIdx.x % sets * together + threadIdx.x / (lanes * groups);
-  const int rows = sg.seq.n * p.G, at = sg.tile * v.tile_rows + r;
-  if (sg.tile * v.tile_rows + blockIdx.x % sets * together >= rows) return;
-  const bool mine = (int)threadIdx.x < lanes * groups * together && at < rows;
-  float m = -INFINITY, l = 0.0f;
-  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  auto add = [&](float2 ml, float4 x) {
-    const float next = fmaxf(m, ml.x), base = next == -INFINITY ? 0.0f : next;
-    const float f = __builtin_amdgcn_exp2f(m - base), e = ml.x == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(ml.x - base);
-    m = next;
-    l = l * f + ml.y * e;
-    o.x = o.x * f + x.x * e, o.y = o.y * f + x.y * e, o.z = o.z * f + x.z * e, o.w = o.w * f + x.w * e;
-  };
-  if (mine)
+  const int lane = threadIdx.x % lanes, group = threadIdx.x / lanes % groups;
+  const int rows = sg.seq.n * p.G - sg.tile * v.tile_rows;   // of the tile and those behind it
+  for (int turn = 0; turn < turns; ++turn) {
+    const int r0 = (blockIdx.x % sets * turns + turn) * together, r = r0 + threadIdx.x / (lanes * groups);
+    if (r0 >= rows) return;
+    const bool mine = (int)threadIdx.x < lanes * groups * together && r < rows;
+    float m = -INFINITY, l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto add = [&](float2 ml, float4 x) {
+      const float next = fmaxf(m, ml.x), base = next == -INFINITY ? 0.0f : next;
+      const float f = __builtin_amdgcn_exp2f(m - base), e = ml.x == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(ml.x - base);
+      m = next;
+      l = l * f + ml.y * e;
+      o.x = o.x * f + x.x * e, o.y = o.y * f + x.y * e, o.z = o.z * f + x.z * e, o.w = o.w * f + x.w * e;
+    };
+    if (mine)
 #pragma unroll 4
-    for (int i = group; i < sg.parts; i += groups) {
-      const Sums part(p, v, sg.slot + i, h);
-      add(*reinterpret_cast<const float2*>(part.ml + 2 * r), *reinterpret_cast<const float4*>(part.o + r * p.D + 4 * lane));
+      for (int i = group; i < sg.parts; i += groups) {
+        const Sums part(p, v, sg.slot + i, h);
+        add(*reinterpret_cast<const float2*>(part.ml + 2 * r), *reinterpret_cast<const float4*>(part.o + r * p.D + 4 * lane));
+      }
+    if (groups > 1) {
+      if (turn > 0) __syncthreads();   // what the turn before left is read
+      s_o[threadIdx.x] = o;
+      s_ml[threadIdx.x] = make_float2(m, l);
+      __syncthreads();
     }
-  if (groups > 1) {
-    s_o[threadIdx.x] = o;
-    s_ml[threadIdx.x] = make_float2(m, l);
-    __syncthreads();
+    if (!mine || group > 0) continue;
+    for (int i = 1; i < groups; ++i) add(s_ml[threadIdx.x + i * lanes], s_o[threadIdx.x + i * lanes]);
+    const int at = sg.tile * v.tile_rows + r, t = at / p.G;
+    float f = l == 0.0f ? 0.0f : (FP8 && p.v_scale ? p.v_scale[h] : 1.0f) / l;
+    if (sg.seq.position(t) >= sg.seq.cap) f = NAN;
+    uint16_t* to = p.out + (sg.seq.row0 + t) * p.o_row + (h * p.G + at - t * p.G) * p.o_head + 4 * lane;
+    *reinterpret_cast<uint2*>(to) = make_uint2(bf16x2(o.x * f, o.y * f), bf16x2(o.z * f, o.w * f));
   }
-  if (!mine || group > 0) return;
-  for (int i = 1; i < groups; ++i) add(s_ml[threadIdx.x + i * lanes], s_o[threadIdx.x + i * lanes]);
-  const int t = at / p.G;
-  float f = l == 0.0f ? 0.0f : (FP8 && p.v_scale ? p.v_scale[h] : 1.0f) / l;
-  if (sg.seq.position(t) >= sg.seq.cap) f = NAN;
-  uint16_t* to = p.out + (sg.seq.row0 + t) * p.o_row + (h * p.G + at - t * p.G) * p.o_head + 4 * lane;
-  *reinterpret_cast<uint2*>(to) = make_uint2(bf16x2(o.x * f, o.y * f), bf16x2(o.z * f, o.w * f));
 }
 template <bool FP8>
 hipError_t launch_join(const KvAttnArgs& a, const Division& v, hipStream_t stream) {
   if (!can_split(v, a.batch)) return hipSuccess;
   const int64_t tiles = v.split_tiles(a.batch.T, a.batch.B, a.Hkv, a.G);
-  // rows that a workgroup joins: one, or as many as its threads hold where that leaves a few workgroups a CU
-  int together = 1;
+  // rows that a workgroup joins at once: one, or as many as its threads hold where that leaves a few workgroups a CU
+  int together = 1, turns = 1;
   while (together * 2 * (a.D / 4) <= kJoinThreads && tiles * a.Hkv * (v.tile_rows / (2 * together)) >= 1024) together *= 2;
-  join_kernel<FP8><<<dim3((unsigned)(tiles * a.Hkv * (v.tile_rows / together))), kJoinThreads, 0, stream>>>(a, v, together);
+  while (together * turns < v.tile_rows && tiles * a.Hkv * (v.tile_rows / (together * turns)) > kJoinGroups) turns *= 2;
+  const int64_t sets = tiles * a.Hkv * (v.tile_rows / (together * turns));
+  join_kernel<FP8><<<dim3((unsigned)sets), kJoinThreads, 0, stream>>>(a, v, together, turns);
   return hipGetLastError();
 }
 }  // namespace
