@@ -631,7 +631,7 @@ nvfp4moe_status moe_block_norm(const void* resid, nvfp4moe_dtype r_dtype, int64_
  *   x, out       device [T, H, D] of dtype (F32 or BF16), element distances x_row and x_head (o_row,
  *                o_head) between rows and heads, the dims of a head beside each other; the distance
  *                of heads is at least D, that of rows at least (H - 1) * the heads' + D. out may be x
- *                (same distances) and must not overlap it otherwise.
+ *                (same distances) and must not overlap it otherwise, nor positions or freqs.
  *   T, H, D      T >= 0 (0: nothing is done); H, D >= 1; T * H * D < 2^47, H * D < 2^24.
  *   positions    device int32 (pos_bytes 4) or int64 (8) [T].
  *   freqs        device float64 [rot / 2], radians a position.
@@ -687,17 +687,18 @@ nvfp4moe_status kv_cache_append(const void* q, int64_t q_row, int64_t q_head, co
  *     out[t, h] = sum_j softmax_j(scale * q[t, h] . k[j, h / G]) * v[j, h / G]      G = Hq / Hkv
  * From single tokens (the decode step) to whole prompts, of any lengths in one call.
  *   q, out       device bf16 [T, Hq, D] with element distances of rows and heads, multiples of 8;
- *                16-byte aligned. out must not overlap q or the cache.
+ *                16-byte aligned. Neither out nor ws may overlap the other or anything that is read.
  *   scale        finite, > 0.      window   >= 0 (0: all keys).
- *   T, B         T >= 0 (0: nothing is done), B >= 1; T * Hq + 16 * B * Hkv < 2^31.
+ *   T, B         T >= 0 (0: nothing is done), B >= 1; T * Hq + 16 * B * Hkv < 2^27.
  *   ws           kv_cache_attention_workspace_size(T, B, Hq, Hkv, D) bytes, 16-byte aligned (0 for
  *                sizes that the call refuses). Calls that may overlap need a workspace each.
  * Scores, running maxima and sums are float32 and out is rounded once. Up to 16 rows (token, query
  * head of a group) a sequence on average, the exponentials that weigh the values count as 16 bits;
- * above, they are rounded to bf16. A row that sees no key (a position below 0) gives zeros. What a page holds behind a sequence's
- * last token, and keys and values that a row does not see, do not reach it, NaN and Inf included; a visible
- * value that is not finite makes its dim NaN or Inf in the rows that see it. A row that sees a key whose
- * page is not in [0, pages), or whose position lies behind the page table's columns, gives NaN.
+ * above, they are rounded to bf16, or to f16 with an FP8 cache. A row that sees no key (a position below 0)
+ * gives zeros. What a page holds behind a sequence's last token, and keys and values that a row does not
+ * see, do not reach it, NaN and Inf included; a visible value that is not finite makes its dim NaN or Inf in
+ * the rows that see it. A row that sees a key whose page is not in [0, pages), or whose position lies behind
+ * the page table's columns, gives NaN.
  * ------------------------------------------------------------------------- */
 nvfp4moe_status kv_cache_attention(const void* q, int64_t q_row, int64_t q_head, int32_t T, int32_t Hq, int32_t Hkv,
                                    int32_t D, const int32_t* page_table, int64_t ld_table, int32_t cols,

@@ -1237,6 +1237,8 @@ struct Heads {
   bool same(const Heads& o) const { return p == o.p && T == o.T && H == o.H && (T == 1 || row == o.row) && (H == 1 || head == o.head); }
 };
 
+constexpr int64_t kCacheMaxRows = int64_t(1) << 27;   // (a launch holds fewer than 2^32 threads)
+
 // (the checks of a rotation; nullptr: fine)
 const char* rope_bad(const double* freqs, int32_t rot, int32_t start, int32_t D, int32_t interleaved, float magnitude) {
   if (!aligned(freqs, 8)) return "freqs must be 8-byte aligned";
@@ -1268,6 +1270,14 @@ CacheBatchArgs batch_args(const int32_t* page_table, int64_t ld_table, int32_t c
                           int32_t B, int32_t T, int32_t pages, int32_t page) {
   return {page_table, ld_table, cols, lengths, starts, B, T, pages, page, __builtin_ctz((unsigned)page)};
 }
+// Whether what a call writes shares a byte with `size` ones at p (null: nothing).
+bool touches(const Rows& written, const void* p, int64_t size) { return p && written.overlap(Rows(p, 0, 1, size, 1)); }
+// ... with what the cache's calls read beside rows and the cache.
+bool touches(const Rows& written, const CacheBatchArgs& b, int64_t ld_table, int32_t Hkv, const float* k_scale, const float* v_scale) {
+  return touches(written, b.page_table, ((b.B - 1) * ld_table + b.cols) * 4) || touches(written, b.lengths, (int64_t)b.B * 4) ||
+         touches(written, b.starts, ((int64_t)b.B + 1) * 4) || touches(written, k_scale, (int64_t)Hkv * 4) ||
+         touches(written, v_scale, (int64_t)Hkv * 4);
+}
 // One of the caches as rows of bytes.
 Rows cache_rows(const void* p, int32_t pages, int32_t Hkv, int32_t page, int32_t D, int32_t fp8) {
   return Rows(p, 0, 1, (int64_t)pages * Hkv * page * D, fp8 ? 1 : 2);
@@ -1296,6 +1306,8 @@ extern "C" nvfp4moe_status rope_rotate(const void* x, nvfp4moe_dtype dtype, int6
   const bool in_place = from.same(to);
   if (!in_place && from.rows().overlap(to.rows()))
     return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: out overlaps x (it may be x itself)", fn);
+  if (touches(to.rows(), positions, (int64_t)T * pos_bytes) || touches(to.rows(), freqs, (int64_t)rot / 2 * 8))
+    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: out overlaps positions or freqs", fn);
   RopeArgs a{};
   a.x = {x, x_row, x_head};
   a.out = {out, o_row, o_head};
@@ -1340,8 +1352,14 @@ extern "C" nvfp4moe_status kv_cache_append(const void* q, int64_t q_row, int64_t
     if (t->p) clash = clash || t->rows().overlap(kc) || t->rows().overlap(vc);
   const bool in_place = q && qs.same(os);
   if (q) clash = clash || os.rows().overlap(ks.rows()) || os.rows().overlap(vs.rows()) || (!in_place && os.rows().overlap(qs.rows()));
-  if (clash) return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: an output overlaps what is read or another one (q_out may be q itself)", fn);
   KvAppendArgs a{};
+  a.batch = batch_args(page_table, ld_table, cols, lengths, starts, B, T, pages, page);
+  const auto also = [&](const Rows& w) {
+    return touches(w, a.batch, ld_table, Hkv, k_scale, v_scale) || (freqs && touches(w, freqs, (int64_t)rot / 2 * 8)) ||
+           (freqs && touches(w, positions, (int64_t)T * pos_bytes));
+  };
+  clash = clash || also(kc) || also(vc) || (q && also(os.rows()));
+  if (clash) return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: an output overlaps what is read or another one (q_out may be q itself)", fn);
   a.q = {q, q_row, q_head};
   a.q_out = {q_out, qo_row, qo_head};
   a.k = {k, k_row, k_head};
@@ -1349,7 +1367,6 @@ extern "C" nvfp4moe_status kv_cache_append(const void* q, int64_t q_row, int64_t
   a.Hq = q ? Hq : 0;
   a.Hkv = Hkv;
   a.D = D;
-  a.batch = batch_args(page_table, ld_table, cols, lengths, starts, B, T, pages, page);
   a.positions = freqs ? positions : nullptr;
   a.pos64 = pos_bytes == 8;
   a.turn = {freqs, freqs ? rot : 0, freqs ? start : 0, freqs ? interleaved : 0, magnitude, 1.0f};
@@ -1364,7 +1381,7 @@ extern "C" nvfp4moe_status kv_cache_append(const void* q, int64_t q_row, int64_t
 
 extern "C" size_t kv_cache_attention_workspace_size(int32_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D) {
   if (T < 1 || B < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || D < 32 || D % 32 != 0 || D > kCacheMaxD || (int64_t)Hq * D >= (int64_t(1) << 24) ||
-      (int64_t)T * Hq + (int64_t)16 * B * Hkv >= (int64_t(1) << 31))
+      (int64_t)T * Hq + (int64_t)16 * B * Hkv >= kCacheMaxRows)
     return 0;
   return kv_attention_ws_bytes(T, B, Hq, Hkv, D);
 }
@@ -1380,20 +1397,26 @@ extern "C" nvfp4moe_status kv_cache_attention(const void* q, int64_t q_row, int6
   if (const char* why = cache_bad(T, Hq, Hkv, D, page_table, ld_table, cols, lengths, starts, B, k_cache, v_cache, cache_fp8, pages, page,
                                   k_scale, v_scale))
     return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: %s (T=%d Hq=%d Hkv=%d D=%d B=%d pages=%d page=%d)", fn, why, T, Hq, Hkv, D, B, pages, page);
-  if ((int64_t)T * Hq + (int64_t)16 * B * Hkv >= (int64_t(1) << 31))
-    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: need T * Hq + 16 * B * Hkv < 2^31", fn);
+  if ((int64_t)T * Hq + (int64_t)16 * B * Hkv >= kCacheMaxRows)
+    return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: need T * Hq + 16 * B * Hkv < 2^27", fn);
   if (!(scale > 0.0f) || !(scale - scale == 0.0f) || window < 0)
     return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: scale must be finite and positive, window at least 0", fn);
   const Heads qs{q, q_row, q_head, T, Hq, D, 2}, os{out, o_row, o_head, T, Hq, D, 2};
   for (const Heads* t : {&qs, &os})
     if (const char* why = t->bad(8, 16)) return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: %s (multiples of 8, 16 bytes)", fn, why);
-  if (os.rows().overlap(qs.rows()) || os.rows().overlap(cache_rows(k_cache, pages, Hkv, page, D, cache_fp8)) ||
-      os.rows().overlap(cache_rows(v_cache, pages, Hkv, page, D, cache_fp8)))
+  const Rows kc = cache_rows(k_cache, pages, Hkv, page, D, cache_fp8), vc = cache_rows(v_cache, pages, Hkv, page, D, cache_fp8);
+  KvAttnArgs a{};
+  a.batch = batch_args(page_table, ld_table, cols, lengths, starts, B, T, pages, page);
+  const auto clash = [&](const Rows& w) {
+    return w.overlap(qs.rows()) || w.overlap(kc) || w.overlap(vc) || touches(w, a.batch, ld_table, Hkv, k_scale, v_scale);
+  };
+  if (clash(os.rows()))
     return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: out overlaps what is read", fn);
   const size_t need = kv_attention_ws_bytes(T, B, Hq, Hkv, D);
   if (!ws || ws_bytes < need || !aligned(ws, 16))
     return fail(NVFP4MOE_ERR_WORKSPACE, "%s: need a 16-byte aligned workspace of %zu bytes, got %zu", fn, need, ws ? ws_bytes : (size_t)0);
-  KvAttnArgs a{};
+  const Rows room(ws, 0, 1, (int64_t)need, 1);
+  if (clash(room) || room.overlap(os.rows())) return fail(NVFP4MOE_ERR_INVALID_ARG, "%s: the workspace overlaps a tensor", fn);
   a.q = static_cast<const uint16_t*>(q);
   a.q_row = q_row;
   a.q_head = q_head;
@@ -1404,14 +1427,13 @@ extern "C" nvfp4moe_status kv_cache_attention(const void* q, int64_t q_row, int6
   a.Hkv = Hkv;
   a.D = D;
   a.G = Hq / Hkv;
-  a.batch = batch_args(page_table, ld_table, cols, lengths, starts, B, T, pages, page);
   a.k_cache = k_cache;
   a.v_cache = v_cache;
   a.fp8 = cache_fp8;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
   a.scale = scale;
-  a.window = window;
+  a.window = window < (int64_t)cols * page ? window : 0;   // (a row sees no more than the table has columns for)
   a.ws = ws;
   return hip_status(launch_kv_attention(a, static_cast<hipStream_t>(stream)), fn);
 }

@@ -15,6 +15,11 @@ typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.44269504088896341f;
 
+// First key that the row of a position sees (no sum here passes 32 bits, whatever the window).
+__device__ __forceinline__ int first_seen(int position, int window) {
+  return window > 0 && position >= window ? position - window + 1 : 0;
+}
+
 // One sequence's new tokens.
 struct Sequence {
   int row0, n;       // first row, new tokens (rows within the tensor only)
@@ -33,7 +38,7 @@ __device__ __forceinline__ Sequence sequence_of(const CacheBatchArgs& b, int win
   q.n = max(min(end, b.T) - q.row0, 0);
   q.len = max(len, 0);
   q.cap = (int)min((int64_t)b.cols << b.page_log, (int64_t)0x7fffff00);
-  const int last = min(q.len, q.cap), first = window > 0 ? max(q.len - q.n + 1 - window, 0) : 0;
+  const int last = min(q.len, q.cap), first = first_seen(q.len - q.n, window);
   q.blocks = max(((last + (1 << block_log) - 1) >> block_log) - (first >> block_log), 0);
   return q;
 }
@@ -43,7 +48,7 @@ struct Seen {
   int lo, hi;
 };
 __device__ __forceinline__ Seen seen_by(int position, int window, int cap) {
-  return {window > 0 ? max(position + 1 - window, 0) : 0, min(max(position + 1, 0), cap)};
+  return {first_seen(position, window), min(max(position + 1, 0), cap)};
 }
 
 // Inclusive sums over the lanes by DPP moves (no LDS round trips): within rows of 16, then rows 1 and 3

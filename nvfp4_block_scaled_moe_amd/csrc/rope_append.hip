@@ -350,16 +350,21 @@ int tokens_of(int T, int elements, int half) {
   n = n < 1 ? 1 : n > kTokens ? kTokens : n;
   if (half > 0 && n * half > kPairs) n = kPairs / half;
   // at least a workgroup for each CU, where there are tokens for them
-  const int even = (T + 255) / 256;
+  const int even = (int)(((int64_t)T + 255) / 256);
   return n < even ? n : even > 0 ? even : 1;
 }
+
+// Most workgroups of a launch, which holds fewer than 2^32 threads.
+constexpr int64_t kMaxGroups = (int64_t(1) << 32) / kThreads - 1;
 
 }  // namespace
 
 hipError_t launch_rope(const RopeArgs& a, hipStream_t stream) {
   const int half = a.turn.rot / 2, tokens = tokens_of(a.T, a.H * a.D, half);
   const int v = vector_of(a.turn, a.D, {a.x, a.out}, a.bf16 ? 2 : 4);
-  const dim3 grid((unsigned)((a.T + tokens - 1) / tokens));
+  const int64_t groups = ((int64_t)a.T + tokens - 1) / tokens;
+  if (groups > kMaxGroups) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)groups);
   const size_t lds = (size_t)tokens * half * sizeof(float2);
   const Walk walk = walk_of(a.turn.rot / (2 * v) + (a.copy ? (a.D - a.turn.rot) / v : 0), a.H);
   if (a.bf16) {
@@ -380,14 +385,16 @@ hipError_t launch_kv_append(const KvAppendArgs& a0, hipStream_t stream) {
   const int v = vector_of(a.turn, a.D, {a.q, a.q_out, a.k, a.v}, 2);
   int v_log = 0;
   while ((1 << v_log) < kTokens && (1 << v_log) < T) ++v_log;
-  const int turn_groups = (T + tokens - 1) / tokens, v_groups = ((T + (1 << v_log) - 1) >> v_log) * a.Hkv;
+  const int64_t turn_groups = ((int64_t)T + tokens - 1) / tokens;
+  const int64_t groups = turn_groups + (((int64_t)T + (1 << v_log) - 1) >> v_log) * a.Hkv;
+  if (groups > kMaxGroups) return hipErrorInvalidConfiguration;
   size_t lds = (size_t)tokens * half * sizeof(float2);
   const size_t v_lds = (size_t)(a.D + 2) * 2 << v_log;
   if (v_lds > lds) lds = v_lds;
   auto k = a.fp8 ? (v == 8 ? kv_append_kernel<8, true> : v == 4 ? kv_append_kernel<4, true> : kv_append_kernel<1, true>)
                  : (v == 8 ? kv_append_kernel<8, false> : v == 4 ? kv_append_kernel<4, false> : kv_append_kernel<1, false>);
-  k<<<dim3((unsigned)(turn_groups + v_groups)), kThreads, lds, stream>>>(
-      a, tokens, turn_groups, v_log, walk_of(half / v + (a.D - 2 * half) / v, a.Hkv + (a.q.p ? a.Hq : 0)));
+  k<<<dim3((unsigned)groups), kThreads, lds, stream>>>(
+      a, tokens, (int)turn_groups, v_log, walk_of(half / v + (a.D - 2 * half) / v, a.Hkv + (a.q.p ? a.Hq : 0)));
   return hipGetLastError();
 }
 

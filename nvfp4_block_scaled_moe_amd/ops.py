@@ -845,6 +845,8 @@ def _heads(fn: str, what: str, t, H: int, D: int, T: int, align: int = 1):
     place where its distances and address allow, else a contiguous copy."""
     if t.dim() != 3 or t.shape != (T, H, D):
         raise ValueError(f"{fn}: {what} must be [{T}, {H}, {D}], got {tuple(t.shape)}")
+    if T >= 1 << 31 or H * D >= 1 << 24:
+        raise ValueError(f"{fn}: {what} needs T < 2^31 and H * D < 2^24, got {tuple(t.shape)}")
     row, head, one = t.stride()
     if H == 1:
         head = D if align == 1 else -(-D // align) * align
@@ -969,8 +971,8 @@ class CacheBatch:
         t, lengths, starts = self.page_table, self.lengths, self.starts
         B = lengths.shape[0] if lengths.dim() == 1 else -1
         if t.dtype != torch.int32 or lengths.dtype != torch.int32 or starts.dtype != torch.int32 or t.dim() != 2 or \
-                B < 1 or t.shape[0] != B or t.shape[1] < 1 or starts.shape != (B + 1,):
-            raise ValueError(f"CacheBatch: needs int32 page_table [B, n], lengths [B] and starts [B + 1] with B, n >= 1, got "
+                not 1 <= B < 1 << 31 or t.shape[0] != B or not 1 <= t.shape[1] < 1 << 31 or starts.shape != (B + 1,):
+            raise ValueError(f"CacheBatch: needs int32 page_table [B, n], lengths [B] and starts [B + 1], 1 <= B, n < 2^31, got "
                              f"{tuple(t.shape)}, {tuple(lengths.shape)} and {tuple(starts.shape)}")
         cols = t.shape[1]
         ld = t.stride(0) if B > 1 else cols
@@ -1061,6 +1063,8 @@ def kv_cache_attention(q: torch.Tensor, cache: KVCache, batch: CacheBatch, *, sc
     B, cols, ld = _batch(fn, batch)
     if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != D or q.shape[1] == 0 or q.shape[1] % heads:
         raise ValueError(f"{fn}: q must be bf16 [T, Hq, {D}], Hq a multiple of {heads}, got {q.dtype} {tuple(q.shape)}")
+    if not 0 <= window < 1 << 31:
+        raise ValueError(f"{fn}: window must be from 0 to 2^31 - 1, got {window}")
     T, Hq, _ = q.shape
     with _on(idx):
         q, p_q, q_row, q_head = _heads(fn, "q", q, Hq, D, T, 8)

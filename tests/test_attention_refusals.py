@@ -38,7 +38,7 @@ def _refused(name, base, change, word=""):
     dict(freqs=P + 4), dict(rot=0), dict(rot=63), dict(rot=66), dict(rot=4098, D=8192, x_head=8192, x_row=1 << 17, o_head=8192, o_row=1 << 17),
     dict(start=-1), dict(start=2), dict(interleaved=2), dict(grad=2), dict(magnitude=math.inf), dict(magnitude=math.nan),
     dict(x_head=63), dict(x_row=511), dict(o_head=63), dict(o_row=100), dict(x_row=-512), dict(out=P + 128), dict(out=P, o_row=1024),
-    dict(out=P + 64 * 2), dict(x_row=1 << 40)])
+    dict(out=P + 64 * 2), dict(x_row=1 << 40), dict(freqs=2 * P + 1024), dict(positions=2 * P - 8)])
 def test_rope_refuses(change):
     _refused("rope_rotate", ROPE, change)
 
@@ -51,7 +51,8 @@ def test_rope_refuses(change):
     dict(rot=66), dict(rot=7), dict(start=1), dict(interleaved=-1), dict(magnitude=math.nan), dict(positions=P, pos_bytes=3),
     dict(positions=P + 4, pos_bytes=8), dict(k_row=64), dict(v_head=32), dict(q_row=64), dict(qo_row=64), dict(page_table=P + 2),
     dict(q_out=P + 128, qo_row=1024), dict(q_out=P + 1024, qo_row=1024), dict(q_out=4 * P), dict(k_cache=P - 1024), dict(v_cache=4 * P + 64),
-    dict(k=8 * P + 256)])
+    dict(k=8 * P + 256), dict(freqs=2 * P + 512), dict(positions=4 * P + 4, pos_bytes=4), dict(page_table=8 * P - 4), dict(lengths=2 * P),
+    dict(starts=4 * P + 16), dict(fp8=1, k_scale=8 * P + 4)])
 def test_append_refuses(change):
     _refused("kv_cache_append", APPEND, change)
 
@@ -62,7 +63,8 @@ def test_append_refuses(change):
     dict(cols=0), dict(ld_table=1), dict(fp8=-1), dict(k_scale=P), dict(scale=0.0), dict(scale=-1.0), dict(scale=math.nan),
     dict(scale=math.inf), dict(window=-1), dict(q=P + 8), dict(out=2 * P + 2), dict(q_row=516), dict(q_head=68), dict(o_head=68, o_row=552),
     dict(q_row=448), dict(out=P), dict(out=P + 128), dict(out=4 * P), dict(out=8 * P + 16), dict(T=1 << 28), dict(B=1 << 27),
-    dict(ws=None), dict(ws=16 * P + 8), dict(ws_bytes=1000)])
+    dict(ws=None), dict(ws=16 * P + 8), dict(ws_bytes=1000), dict(ws=P + 256), dict(ws=2 * P + 4080), dict(ws=8 * P), dict(page_table=16 * P + 4),
+    dict(lengths=2 * P + 4), dict(starts=2 * P - 4), dict(fp8=1, v_scale=2 * P + 8), dict(T=1 << 24)])
 def test_attention_refuses(change):
     _refused("kv_cache_attention", ATTEND, change)
 
@@ -176,3 +178,23 @@ def test_frequencies():
                 dict(rot=8, scaling="bands", original=10, fast=1.0, slow=1.0), dict(rot=2, scaling="base"), dict(rot=8, base=math.inf)):
         with pytest.raises(ValueError, match="rope_frequencies"):
             ops.rope_frequencies(**bad, device="cpu")
+
+
+def test_numbers_that_a_call_cannot_hold():
+    """Sizes past 31 bits are refused, not cut. (Tensors of stride 0 on the meta device: nothing is held.)"""
+    one = torch.zeros((1,), dtype=torch.int32)
+    with pytest.raises(ValueError, match="2\\^31"):
+        ops.CacheBatch(torch.empty((1, 1 << 31), dtype=torch.int32, device="meta"), one, torch.zeros((2,), dtype=torch.int32))
+    big = torch.empty((1 << 31, 1, 64), dtype=BF, device="meta")
+    with pytest.raises(ValueError, match="2\\^31"):
+        ops._heads("f", "x", big, 1, 64, 1 << 31)
+    with pytest.raises(ValueError, match="2\\^24"):
+        ops._heads("f", "x", torch.empty((1, 1 << 20, 16), dtype=BF, device="meta"), 1 << 20, 16, 1)
+
+
+def test_window_is_refused_before_it_is_cut(monkeypatch):
+    monkeypatch.setattr(ops, "_gpu", lambda fn, *ts: 0)
+    x = torch.zeros((2, 4, 64), dtype=BF)
+    for window in (-1, 1 << 31, (1 << 32) + 5):
+        with pytest.raises(ValueError, match="window"):
+            ops.kv_cache_attention(x, _cache(), _batch(), window=window)

@@ -330,3 +330,74 @@ def test_large_values(new):
     """Values near the end of bf16 (3.4e38), as far from it as 2^16 weights of up to 2^8 need."""
     c = Case(new, [4200], 8, 1, 128, 64, seed=15, v_spread=1e30)
     _run(c, scale=1.0)
+
+
+# Groups of more query heads than a tile has rows.
+GROUPS = [
+    ([1, 0, 0], [200, 5, 0], 40, 1, 64, 16),
+    ([1, 0], [900, 3], 32, 1, 128, 64),
+    ([1, 2], [500, 30], 300, 1, 32, 16),
+    ([1], [70], 514, 2, 96, 32),
+    ([5], [4200], 320, 1, 128, 64),
+]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("case", range(len(GROUPS)))
+def test_groups_larger_than_a_tile(case, fp8):
+    _run(Case(*GROUPS[case], fp8=fp8, seed=300 + case))
+
+
+@pytest.mark.parametrize("new", [[1, 1, 1], [90, 40]])
+def test_windows_as_long_as_numbers(new):
+    """A window past every sequence's length is none, and a length below the new tokens leaves rows before it empty."""
+    c = Case(new, [100, 60, 5][:len(new)], 8, 2, 64, 16, seed=16)
+    q = c.q.cuda()
+    n = new[0]
+    whole = ops.kv_cache_attention(q, c.cache, c.batch)
+    short = ops.CacheBatch(c.batch.page_table, c.batch.lengths.clone(), c.batch.starts)
+    short.lengths[0] = max(n // 2, 1)
+    part = ops.kv_cache_attention(q, c.cache, short)
+    assert (part[:n - max(n // 2, 1)] == 0).all() and torch.equal(part[n:], whole[n:])
+    for window in (c.table.shape[1] * 16, 1 << 30, (1 << 31) - 1):
+        assert torch.equal(ops.kv_cache_attention(q, c.cache, c.batch, window=window), whole)
+        assert torch.equal(ops.kv_cache_attention(q, c.cache, short, window=window), part)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("new", [[3], [90], [600]])
+def test_a_row_that_is_not_finite_stays_alone(new, fp8):
+    c = Case(new, [1000], 8, 2, 128, 64, fp8=fp8, seed=17)
+    q = c.q.cuda()
+    want = ops.kv_cache_attention(q, c.cache, c.batch)
+    for bad in (float("nan"), float("inf")):
+        spoiled = q.clone()
+        spoiled[1, 3, 7] = bad
+        got = ops.kv_cache_attention(spoiled, c.cache, c.batch)
+        assert not torch.isfinite(got[1, 3]).any()
+        got[1, 3] = want[1, 3]
+        assert torch.equal(got, want)
+
+
+def test_many_sequences():
+    """More sequences than a wave's lanes, some of them split, in both kernels."""
+    for first in (1, 2200):
+        c = Case([first] + [i % 3 for i in range(299)], [4000] + [(37 * i) % 300 for i in range(299)], 4, 2, 64, 16, seed=first)
+        _run(c)
+
+
+def test_two_calls_at_once():
+    """Two streams at work on the same cache and batch, each with its workspace."""
+    c = Case([300, 1, 5], [3000, 4000, 90], 8, 1, 128, 64, seed=18)
+    q = c.q.cuda()
+    want = ops.kv_cache_attention(q, c.cache, c.batch)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(10):
+        for s, g in zip(streams, got):
+            with torch.cuda.stream(s):
+                g.append(ops.kv_cache_attention(q, c.cache, c.batch))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) for g in got for x in g)
