@@ -7,7 +7,12 @@
 // scores of one row; the keys of a block are dealt to the rows of K's operand such that these
 // scores are, after the exponential, the operand of the second product O^T = V^T P^T as they lie:
 // neither goes through LDS. K and V^T are loaded from the cache straight into operand registers,
-// 16 bytes a lane (this is why the cache holds values transposed), a block ahead of its use.
+// 16 bytes a lane (this is why the cache holds values transposed), two blocks ahead of their use: what a CU has
+// under way decides the rate, and registers hold more of it than LDS would.
+//
+// 64 sequences of 16000 keys, 64 heads over 8 of 128: 719 us in bf16, 5.84 TB/s (plain reads reach 6.0 to 6.5); of
+// 500 to 8100 keys 147 us (4.8 TB/s) and 81 us in E4M3 (4.4 TB/s); a sequence of 8000 keys 19 us. What is missing
+// there is the start (lengths, page table, first words: 4 us), the last segments' tail and the join (5 to 7 us).
 //
 // Weights of the second product are two bf16 values each (the rounded exponential, and the rest), so
 // that they count as 16 bits; the matrix cores have the time. Running maxima and sums are float32.
