@@ -75,21 +75,22 @@ __device__ __forceinline__ int64_t wave_sum(int64_t v) {
 // sequence sees), or min_blocks. Every wave finds its segment by itself from the lengths: they are known
 // on the device alone, and a launch that lists the segments costs more (6 to 9 us).
 struct Division {
-  int tile_rows, block_log;
-  int target;       // segments that the work is divided into
+  int tile_log, block_log;
+  int target_log;   // segments that the work is divided into
   int min_blocks;   // least blocks of one
   int step;         // parts are multiples of it
   // A sequence is split from 1.5 segments on, so at most 2 / 3 of the target's tiles are split, into at
   // most 4 / 3 of its segments; all segments are at most the tiles and the target.
+  __host__ __device__ constexpr int tile_rows() const { return 1 << tile_log; }
   __host__ __device__ constexpr int split_blocks() const { return min_blocks + min_blocks / 2; }
-  int64_t tiles(int T, int B, int G) const { return ((int64_t)T * G + tile_rows - 1) / tile_rows + (B < T ? B : T); }
-  int64_t whole(int Hkv) const { return (target + Hkv - 1) / Hkv; }   // of the target, heads aside
+  int64_t tiles(int T, int B, int G) const { return ((int64_t)T * G + tile_rows() - 1) / tile_rows() + (B < T ? B : T); }
+  int64_t whole(int Hkv) const { return ((int64_t(1) << target_log) + Hkv - 1) / Hkv; }   // of the target, heads aside
   int64_t segments(int T, int B, int Hkv, int G) const { return tiles(T, B, G) + whole(Hkv); }
   int64_t split_tiles(int T, int B, int Hkv, int G) const {
     const int64_t n = tiles(T, B, G), w = whole(Hkv);
     return n < w ? n : w;
   }
-  size_t ws_bytes(int Hkv, int D) const { return (size_t)(4 * whole(Hkv) / 3 + 1) * Hkv * tile_rows * (D + 2) * sizeof(float); }
+  size_t ws_bytes(int Hkv, int D) const { return (size_t)(4 * whole(Hkv) / 3 + 1) * Hkv * tile_rows() * (D + 2) * sizeof(float); }
 };
 // Whether any sequence can be split: the page table bounds their lengths.
 inline bool can_split(const Division& v, const CacheBatchArgs& b) {
@@ -104,12 +105,13 @@ struct Segment {
   int block0, blocks;     // this part's keys
   bool found;
 };
-// Segment `at` (heads aside), or with SPLIT tile `at` of those that are split (part 0).
+// Segment `at` (heads aside), or with SPLIT tile `at` of those that are split (part 0). (Rows of a sequence are below
+// 2^27 and blocks below 2^27: every division is of 32 bits.)
 template <bool SPLIT>
 __device__ __forceinline__ Segment segment_of(const KvAttnArgs& p, const Division& v, int at) {
   const CacheBatchArgs& b = p.batch;
   const int lane = threadIdx.x % kWave;   // a lane a sequence
-  auto tiles_of = [&](const Sequence& q) { return (int)(((int64_t)q.n * p.G + v.tile_rows - 1) / v.tile_rows); };
+  auto tiles_of = [&](const Sequence& q) { return (q.n * p.G + v.tile_rows() - 1) >> v.tile_log; };
   Sequence mine{};
   int64_t work = 0;
   for (int s0 = 0; s0 < b.B; s0 += kWave) {
@@ -120,14 +122,14 @@ __device__ __forceinline__ Segment segment_of(const KvAttnArgs& p, const Divisio
     }
   }
   work = wave_sum(work) * p.Hkv;
-  const int64_t even = (work + v.target - 1) / v.target;
-  const int chunk = (int)min((even > v.min_blocks ? even : v.min_blocks), (int64_t)1 << 30);
+  const int64_t even = (work + (1 << v.target_log) - 1) >> v.target_log;
+  const uint32_t chunk = (uint32_t)min((even > v.min_blocks ? even : v.min_blocks), (int64_t)1 << 30);
   Segment r{};
   int before = 0, slots = 0;
   for (int s0 = 0; s0 < b.B; s0 += kWave) {
     const int s = s0 + lane;
     if (b.B > kWave) mine = s < b.B ? sequence_of(b, p.window, s, v.block_log) : Sequence{};
-    const int tiles = s < b.B ? tiles_of(mine) : 0, parts = max((int)(((int64_t)mine.blocks + chunk / 2) / chunk), 1);
+    const int tiles = s < b.B ? tiles_of(mine) : 0, parts = max((int)(((uint32_t)mine.blocks + chunk / 2) / chunk), 1);
     const int split = parts > 1 ? tiles * parts : 0, count = SPLIT ? (parts > 1 ? tiles : 0) : tiles * parts;
     const int upto = wave_scan(count), split_upto = wave_scan(split);
     const uint64_t hit = __ballot(before + upto > at);
@@ -142,8 +144,8 @@ __device__ __forceinline__ Segment segment_of(const KvAttnArgs& p, const Divisio
       r.tile = get(tiles) - 1 - nth;   // (the later ones, which see the most, first)
       r.slot = slots + get(split_upto) - get(split) + nth * r.parts + r.part;
       // the blocks that the tile's rows see
-      const int t0 = (int)((int64_t)r.tile * v.tile_rows / p.G);
-      const int t1 = min((int)(((int64_t)r.tile * v.tile_rows + v.tile_rows - 1) / p.G), r.seq.n - 1);
+      const int t0 = (int)((uint32_t)(r.tile << v.tile_log) / (uint32_t)p.G);
+      const int t1 = min((int)((uint32_t)((r.tile << v.tile_log) + v.tile_rows() - 1) / (uint32_t)p.G), r.seq.n - 1);
       const Seen a = seen_by(r.seq.position(t0), p.window, r.seq.cap), z = seen_by(r.seq.position(t1), p.window, r.seq.cap);
       r.block0 = a.lo >> v.block_log;
       r.blocks = max(((z.hi + (1 << v.block_log) - 1) >> v.block_log) - r.block0, 0);
@@ -168,8 +170,8 @@ struct Sums {
   float* ml;
   __device__ __forceinline__ Sums(const KvAttnArgs& p, const Division& v, int64_t slot, int h) {
     const int64_t i = slot * p.Hkv + h;
-    o = static_cast<float*>(p.ws) + i * v.tile_rows * (p.D + 2);
-    ml = o + v.tile_rows * p.D;
+    o = static_cast<float*>(p.ws) + i * v.tile_rows() * (p.D + 2);
+    ml = o + v.tile_rows() * p.D;
   }
 };
 
@@ -178,16 +180,17 @@ struct Sums {
 // that out in every workgroup (8192 of them 13 us, 2048 6 to 8), so there are no more than the CUs hold at once.
 constexpr int kJoinThreads = 256, kJoinGroups = 2048;
 namespace {   // (a kernel of each file's own)
-template <bool FP8>
-__global__ __launch_bounds__(kJoinThreads) void join_kernel(const KvAttnArgs p, const Division v, int together, int turns) {
+template <bool FP8, class Of>   // Of::kDivision
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(const KvAttnArgs p, int together, int turns) {
+  constexpr Division v = Of::kDivision;
   __shared__ float4 s_o[kJoinThreads];
   __shared__ float2 s_ml[kJoinThreads];
-  const int sets = v.tile_rows / (together * turns), h = blockIdx.x / sets % p.Hkv;
+  const int sets = v.tile_rows() / (together * turns), h = blockIdx.x / sets % p.Hkv;
   const Segment sg = segment_of<true>(p, v, blockIdx.x / sets / p.Hkv);
   if (!sg.found) return;
   const int lanes = p.D / 4, groups = kJoinThreads / (lanes * together);
   const int lane = threadIdx.x % lanes, group = threadIdx.x / lanes % groups;
-  const int rows = sg.seq.n * p.G - sg.tile * v.tile_rows;   // of the tile and those behind it
+  const int rows = sg.seq.n * p.G - (sg.tile << v.tile_log);   // of the tile and those behind it
   for (int turn = 0; turn < turns; ++turn) {
     const int r0 = (blockIdx.x % sets * turns + turn) * together, r = r0 + threadIdx.x / (lanes * groups);
     if (r0 >= rows) return;
@@ -215,23 +218,24 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(const KvAttnArgs p, 
     }
     if (!mine || group > 0) continue;
     for (int i = 1; i < groups; ++i) add(s_ml[threadIdx.x + i * lanes], s_o[threadIdx.x + i * lanes]);
-    const int at = sg.tile * v.tile_rows + r, t = at / p.G;
+    const int at = (sg.tile << v.tile_log) + r, t = at / p.G;
     float f = l == 0.0f ? 0.0f : (FP8 && p.v_scale ? p.v_scale[h] : 1.0f) / l;
     if (sg.seq.position(t) >= sg.seq.cap) f = NAN;
     uint16_t* to = p.out + (sg.seq.row0 + t) * p.o_row + (h * p.G + at - t * p.G) * p.o_head + 4 * lane;
     *reinterpret_cast<uint2*>(to) = make_uint2(bf16x2(o.x * f, o.y * f), bf16x2(o.z * f, o.w * f));
   }
 }
-template <bool FP8>
-hipError_t launch_join(const KvAttnArgs& a, const Division& v, hipStream_t stream) {
+template <bool FP8, class Of>
+hipError_t launch_join(const KvAttnArgs& a, hipStream_t stream) {
+  constexpr Division v = Of::kDivision;
   if (!can_split(v, a.batch)) return hipSuccess;
   const int64_t tiles = v.split_tiles(a.batch.T, a.batch.B, a.Hkv, a.G);
   // rows that a workgroup joins at once: one, or as many as its threads hold where that leaves a few workgroups a CU
   int together = 1, turns = 1;
-  while (together * 2 * (a.D / 4) <= kJoinThreads && tiles * a.Hkv * (v.tile_rows / (2 * together)) >= 1024) together *= 2;
-  while (together * turns < v.tile_rows && tiles * a.Hkv * (v.tile_rows / (together * turns)) > kJoinGroups) turns *= 2;
-  const int64_t sets = tiles * a.Hkv * (v.tile_rows / (together * turns));
-  join_kernel<FP8><<<dim3((unsigned)sets), kJoinThreads, 0, stream>>>(a, v, together, turns);
+  while (together * 2 * (a.D / 4) <= kJoinThreads && tiles * a.Hkv * (v.tile_rows() / (2 * together)) >= 1024) together *= 2;
+  while (together * turns < v.tile_rows() && tiles * a.Hkv * (v.tile_rows() / (together * turns)) > kJoinGroups) turns *= 2;
+  const int64_t sets = tiles * a.Hkv * (v.tile_rows() / (together * turns));
+  join_kernel<FP8, Of><<<dim3((unsigned)sets), kJoinThreads, 0, stream>>>(a, together, turns);
   return hipGetLastError();
 }
 }  // namespace

@@ -44,7 +44,11 @@ constexpr int kBlockLog = 6, kBlock = 1 << kBlockLog;   // keys of a block
 // a row. The segments are as many as workgroups that a CU holds at once (with W 4 and 1024 segments, 8192 new
 // tokens of 32 heads took 567 instead of 556 us, 128 new ones over 30000 keys 153 instead of 138, 16 sequences of 4
 // over 8000 112 instead of 105; 640 and 768, which leave a part round, are slower yet: 125 and 115 us the last).
-constexpr Division division(int W) { return {32 * W, kBlockLog, W == 8 ? 256 : 512, 8, 1}; }
+constexpr Division division(int W) { return {W == 8 ? 8 : 7, kBlockLog, W == 8 ? 8 : 9, 8, 1}; }
+template <int W>
+struct OfWaves {
+  static constexpr Division kDivision = division(W);
+};
 
 // 16 bytes a lane straight into LDS (lane l at lds + 16 l), from global memory or from a buffer (whose base
 // and offset `soff` are the wave's: no address arithmetic in the lanes).
@@ -116,7 +120,7 @@ __global__ __launch_bounds__(W* kWave, D > 128 ? 1 : 2) void chunk_kernel(const 
   using C = Chunk<D, FP8>;
   using S2 = Second<FP8>;
   constexpr Division kDivision = division(W);
-  constexpr int kRows = kDivision.tile_rows;
+  constexpr int kRows = kDivision.tile_rows();
   extern __shared__ __attribute__((aligned(16))) char smem[];   // two of: keys [64, D], values [D, 64]; then
   uint32_t* s_any = reinterpret_cast<uint32_t*>(smem + 4 * Chunk<D, FP8>::kBytes);   // a flag a wave
   const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -619,7 +623,7 @@ hipError_t launch(const KvAttnArgs& a, hipStream_t stream) {
   const int64_t groups = division(W).segments(a.batch.T, a.batch.B, a.Hkv, a.G) * a.Hkv;
   chunk_kernel<D, FP8, W><<<dim3((unsigned)groups), W * kWave, lds, stream>>>(a);
   const hipError_t e = hipGetLastError();
-  return e != hipSuccess ? e : launch_join<FP8>(a, division(W), stream);
+  return e != hipSuccess ? e : launch_join<FP8, OfWaves<W>>(a, stream);
 }
 
 // Waves of a workgroup. 8 for D 128 (D 64 has three waves a SIMD with W 4: 614 us, 657 with 8), where sequences have

@@ -29,7 +29,11 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kRows = 16;          // rows of a tile
 // (Least blocks of a segment: joining costs a second launch, so that a few blocks more a wave cost less.)
-constexpr Division division(bool fp8) { return {kRows, fp8 ? 6 : 5, 1024, 16, kWaves}; }
+constexpr Division division(bool fp8) { return {4, fp8 ? 6 : 5, 10, 16, kWaves}; }
+template <bool FP8>
+struct OfCache {
+  static constexpr Division kDivision = division(FP8);
+};
 
 template <int D, bool FP8>
 struct Few {
@@ -359,7 +363,7 @@ hipError_t launch(const KvAttnArgs& a, hipStream_t stream) {
   }
   few_kernel<D, FP8, WHOLE><<<dim3((unsigned)groups), kWaves * kWave, lds, stream>>>(a);
   const hipError_t e = hipGetLastError();
-  return e != hipSuccess ? e : launch_join<FP8>(a, F::kDivision, stream);
+  return e != hipSuccess ? e : launch_join<FP8, OfCache<FP8>>(a, stream);
 }
 
 template <int D, bool FP8>
