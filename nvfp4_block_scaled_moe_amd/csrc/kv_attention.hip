@@ -289,7 +289,10 @@ __global__ __launch_bounds__(W* kWave, D > 128 ? 1 : 2) void chunk_kernel(const 
     __syncthreads();
   };
 
-  float m = -INFINITY, base = 0.0f, l = 0.0f;   // base: what exponentials are taken from (0 before any key)
+  // base: what exponentials are taken from. Before any score above -Inf it lies so far down that the first one shows
+  // in the sums (and -Inf less it is still -Inf: a weight of 0).
+  constexpr float kNone = -3e38f;
+  float m = -INFINITY, base = kNone, l = 0.0f;
   f32x16 o[C::kDTiles];
   uint32_t lost[(C::kDTiles + 1) / 2] = {};   // bit 16 (d % 2) + i: o[d][i] is to be NaN
 #pragma unroll
@@ -343,7 +346,7 @@ __global__ __launch_bounds__(W* kWave, D > 128 ? 1 : 2) void chunk_kernel(const 
   auto move_maximum = [&](float next) __attribute__((always_inline)) {
     const float shrink = next == m ? 1.0f : __builtin_amdgcn_exp2f(m - next);
     m = next;
-    base = m == -INFINITY ? 0.0f : m - S2::kRaise;
+    base = m == -INFINITY ? kNone : m - S2::kRaise;
     l *= shrink;
 #pragma unroll
     for (int d = 0; d < C::kDTiles; ++d)

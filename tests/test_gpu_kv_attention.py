@@ -401,3 +401,21 @@ def test_two_calls_at_once():
                 g.append(ops.kv_cache_attention(q, c.cache, c.batch))
     torch.cuda.synchronize()
     assert all(torch.equal(x, want) for g in got for x in g)
+
+
+@pytest.mark.parametrize("new", [[1], [40], [150]])
+def test_keys_of_minus_infinity_count_for_nothing(new):
+    """The first keys' scores are -Inf, those of all others far below what exponentials hold."""
+    c = Case(new, [4200], 8, 1, 128, 64, seed=19)
+    q = c.q.cuda()
+    q[..., 0], q[..., 1] = 1.0, 8.0
+    got = []
+    for low in (float("-inf"), -1e4):    # (weights of exactly 0 either way)
+        k = c.cache.k.clone()
+        at = torch.arange(c.total[0])
+        page, slot = c.table[0].long()[at // 64].cuda(), (at % 64).cuda()
+        k[page, 0, slot, 1] = -8.0
+        k[page[:100], 0, slot[:100], 0] = low
+        got.append(ops.kv_cache_attention(q, ops.KVCache(k, c.cache.v), c.batch, scale=4.0))
+    assert torch.isfinite(got[0]).all() and (got[0] != 0).any(-1).all()
+    assert torch.equal(*got)
