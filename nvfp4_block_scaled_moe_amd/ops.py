@@ -843,16 +843,18 @@ def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: str | None = N
 def _heads(fn: str, what: str, t, H: int, D: int, T: int, align: int = 1):
     """(t, address, row distance, head distance) of a tensor [T, H, D] whose dims lie beside each other: in
     place where its distances and address allow, else a contiguous copy."""
-    if t.dim() != 3 or t.shape != (T, H, D):
+    if t.shape != (T, H, D):
         raise ValueError(f"{fn}: {what} must be [{T}, {H}, {D}], got {tuple(t.shape)}")
     if T >= 1 << 31 or H * D >= 1 << 24:
         raise ValueError(f"{fn}: {what} needs T < 2^31 and H * D < 2^24, got {tuple(t.shape)}")
     row, head, one = t.stride()
+    p = t.data_ptr()
+    if one == 1 and align == 1 and head >= D and row >= (H - 1) * head + D:   # (the common case: views of wider rows)
+        return t, p, row, head
     if H == 1:
         head = D if align == 1 else -(-D // align) * align
     if T == 1:
         row = (H - 1) * head + D
-    p = t.data_ptr()
     if (one != 1 and D > 1) or head < D or row < (H - 1) * head + D or \
             (align > 1 and (p % 16 or (row % align and T > 1) or (head % align and H > 1))):
         t = t.clone(memory_format=torch.contiguous_format)
@@ -861,9 +863,9 @@ def _heads(fn: str, what: str, t, H: int, D: int, T: int, align: int = 1):
 
 
 def _heads_out(fn: str, what: str, t, like, H: int, D: int, T: int, align: int = 1):
-    """_heads of an output: allocated where there is none, and never a copy."""
+    """_heads of an output: allocated, as ``like`` [T, H, D], where there is none, and never a copy."""
     if t is None:
-        t = like.new_empty((T, H, D))
+        t = torch.empty_like(like, memory_format=torch.contiguous_format)
         return t, t.data_ptr(), H * D, D
     if t.dtype != like.dtype:
         raise ValueError(f"{fn}: {what} must be {like.dtype}, got {t.dtype}")
@@ -1072,7 +1074,7 @@ def kv_cache_attention(q: torch.Tensor, cache: KVCache, batch: CacheBatch, *, sc
         if T == 0:
             return out
         nbytes = _attention_workspace(T, B, Hq, heads, D)
-        ws = q.new_empty((nbytes,), dtype=torch.uint8)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
         st = _lib.load().kv_cache_attention(
             p_q, q_row, q_head, T, Hq, heads, D, batch.page_table.data_ptr(), ld, cols, batch.lengths.data_ptr(),
             batch.starts.data_ptr(), B, cache.k.data_ptr(), cache.v.data_ptr(), fp8, pages, page, p_ks, p_vs,
