@@ -4,6 +4,7 @@
 
 #include "common.h"
 #include "kernels.h"
+#include "kv_division.h"
 
 namespace nvfp4moe {
 
@@ -39,7 +40,7 @@ __device__ __forceinline__ Sequence sequence_of(const CacheBatchArgs& b, int win
   q.len = max(len, 0);
   q.cap = (int)min((int64_t)b.cols << b.page_log, (int64_t)0x7fffff00);
   const int last = min(q.len, q.cap), first = first_seen(q.len - q.n, window);
-  q.blocks = max(((last + (1 << block_log) - 1) >> block_log) - (first >> block_log), 0);
+  q.blocks = max(blocks_of(last, block_log) - (first >> block_log), 0);
   return q;
 }
 
@@ -67,34 +68,6 @@ __device__ __forceinline__ int64_t wave_sum(int64_t v) {
   const int lo = __builtin_amdgcn_readlane(wave_scan((int)(v & 0xffffff)), kWave - 1);
   const int hi = __builtin_amdgcn_readlane(wave_scan((int)(v >> 24)), kWave - 1);
   return ((int64_t)hi << 24) + lo;
-}
-
-// How the work is divided. Rows (token, head of a group) of a sequence and key head are taken in tiles, their
-// keys in blocks; the tiles of a sequence are split into as many parts each as its blocks are whole segments,
-// rounded, a segment being the target's share of all blocks of all tiles (counted as if every tile saw what its
-// sequence sees), or min_blocks. Every wave finds its segment by itself from the lengths: they are known
-// on the device alone, and a launch that lists the segments costs more (6 to 9 us).
-struct Division {
-  int tile_log, block_log;
-  int target_log;   // segments that the work is divided into
-  int min_blocks;   // least blocks of one
-  int step;         // parts are multiples of it
-  // A sequence is split from 1.5 segments on, so at most 2 / 3 of the target's tiles are split, into at
-  // most 4 / 3 of its segments; all segments are at most the tiles and the target.
-  __host__ __device__ constexpr int tile_rows() const { return 1 << tile_log; }
-  __host__ __device__ constexpr int split_blocks() const { return min_blocks + min_blocks / 2; }
-  int64_t tiles(int T, int B, int G) const { return ((int64_t)T * G + tile_rows() - 1) / tile_rows() + (B < T ? B : T); }
-  int64_t whole(int Hkv) const { return ((int64_t(1) << target_log) + Hkv - 1) / Hkv; }   // of the target, heads aside
-  int64_t segments(int T, int B, int Hkv, int G) const { return tiles(T, B, G) + whole(Hkv); }
-  int64_t split_tiles(int T, int B, int Hkv, int G) const {
-    const int64_t n = tiles(T, B, G), w = whole(Hkv);
-    return n < w ? n : w;
-  }
-  size_t ws_bytes(int Hkv, int D) const { return (size_t)(4 * whole(Hkv) / 3 + 1) * Hkv * tile_rows() * (D + 2) * sizeof(float); }
-};
-// Whether any sequence can be split: the page table bounds their lengths.
-inline bool can_split(const Division& v, const CacheBatchArgs& b) {
-  return ((int64_t)b.cols << b.page_log >> v.block_log) >= v.split_blocks();
 }
 
 struct Segment {
@@ -129,7 +102,7 @@ __device__ __forceinline__ Segment segment_of(const KvAttnArgs& p, const Divisio
   for (int s0 = 0; s0 < b.B; s0 += kWave) {
     const int s = s0 + lane;
     if (b.B > kWave) mine = s < b.B ? sequence_of(b, p.window, s, v.block_log) : Sequence{};
-    const int tiles = s < b.B ? tiles_of(mine) : 0, parts = max((int)(((uint32_t)mine.blocks + chunk / 2) / chunk), 1);
+    const int tiles = s < b.B ? tiles_of(mine) : 0, parts = parts_of((uint32_t)mine.blocks, chunk);
     const int split = parts > 1 ? tiles * parts : 0, count = SPLIT ? (parts > 1 ? tiles : 0) : tiles * parts;
     const int upto = wave_scan(count), split_upto = wave_scan(split);
     const uint64_t hit = __ballot(before + upto > at);
@@ -148,7 +121,7 @@ __device__ __forceinline__ Segment segment_of(const KvAttnArgs& p, const Divisio
       const int t1 = min((int)((uint32_t)((r.tile << v.tile_log) + v.tile_rows() - 1) / (uint32_t)p.G), r.seq.n - 1);
       const Seen a = seen_by(r.seq.position(t0), p.window, r.seq.cap), z = seen_by(r.seq.position(t1), p.window, r.seq.cap);
       r.block0 = a.lo >> v.block_log;
-      r.blocks = max(((z.hi + (1 << v.block_log) - 1) >> v.block_log) - r.block0, 0);
+      r.blocks = max(blocks_of(z.hi, v.block_log) - r.block0, 0);
       if (!SPLIT) {
         const int per = ((r.blocks + r.parts - 1) / r.parts + v.step - 1) / v.step * v.step;
         r.block0 += r.part * per;
@@ -228,7 +201,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(const KvAttnArgs p, 
 template <bool FP8, class Of>
 hipError_t launch_join(const KvAttnArgs& a, hipStream_t stream) {
   constexpr Division v = Of::kDivision;
-  if (!can_split(v, a.batch)) return hipSuccess;
+  if (!v.can_split((int64_t)a.batch.cols << a.batch.page_log)) return hipSuccess;
   const int64_t tiles = v.split_tiles(a.batch.T, a.batch.B, a.Hkv, a.G);
   // rows that a workgroup joins at once: one, or as many as its threads hold where that leaves a few workgroups a CU
   int together = 1, turns = 1;

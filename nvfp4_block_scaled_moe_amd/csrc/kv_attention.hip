@@ -39,15 +39,10 @@ namespace {
 
 constexpr float kSlack = 8.0f;        // base 2 logits by which a score may exceed the running maximum,
 constexpr float kHigh = 32768.0f;     // and, where that is looked at by the sums alone, sum of 16 weights (2^15)
-constexpr int kBlockLog = 6, kBlock = 1 << kBlockLog;   // keys of a block
-// Waves of a workgroup (W): 4, two workgroups a CU, or 8, one a CU, whose tiles of 256 rows bring half the words for
-// a row. The segments are as many as workgroups that a CU holds at once (with W 4 and 1024 segments, 8192 new
-// tokens of 32 heads took 567 instead of 556 us, 128 new ones over 30000 keys 153 instead of 138, 16 sequences of 4
-// over 8000 112 instead of 105; 640 and 768, which leave a part round, are slower yet: 125 and 115 us the last).
-constexpr Division division(int W) { return {W == 8 ? 8 : 7, kBlockLog, W == 8 ? 8 : 9, 8, 1}; }
+constexpr int kBlockLog = kChunkBlockLog, kBlock = 1 << kBlockLog;   // keys of a block
 template <int W>
 struct OfWaves {
-  static constexpr Division kDivision = division(W);
+  static constexpr Division kDivision = chunk_division(W);
 };
 
 // 16 bytes a lane straight into LDS (lane l at lds + 16 l), from global memory or from a buffer (whose base
@@ -119,7 +114,7 @@ template <int D, bool FP8, int W>
 __global__ __launch_bounds__(W* kWave, D > 128 ? 1 : 2) void chunk_kernel(const KvAttnArgs p) {
   using C = Chunk<D, FP8>;
   using S2 = Second<FP8>;
-  constexpr Division kDivision = division(W);
+  constexpr Division kDivision = chunk_division(W);
   constexpr int kRows = kDivision.tile_rows();
   extern __shared__ __attribute__((aligned(16))) char smem[];   // two of: keys [64, D], values [D, 64]; then
   uint32_t* s_any = reinterpret_cast<uint32_t*>(smem + 4 * Chunk<D, FP8>::kBytes);   // a flag a wave
@@ -623,7 +618,7 @@ hipError_t launch(const KvAttnArgs& a, hipStream_t stream) {
     const hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(chunk_kernel<D, FP8, W>), lds, done);
     if (e != hipSuccess) return e;
   }
-  const int64_t groups = division(W).segments(a.batch.T, a.batch.B, a.Hkv, a.G) * a.Hkv;
+  const int64_t groups = chunk_division(W).segments(a.batch.T, a.batch.B, a.Hkv, a.G) * a.Hkv;
   chunk_kernel<D, FP8, W><<<dim3((unsigned)groups), W * kWave, lds, stream>>>(a);
   const hipError_t e = hipGetLastError();
   return e != hipSuccess ? e : launch_join<FP8, OfWaves<W>>(a, stream);
@@ -665,7 +660,7 @@ hipError_t launch_d(const KvAttnArgs& a, hipStream_t stream) {
 size_t kv_attention_ws_bytes(int T, int B, int Hq, int Hkv, int D) {
   const int G = Hq / Hkv;
   if (kv_attention_few_fits(T, B, G)) return kv_attention_few_ws_bytes(Hkv, D);
-  const size_t w4 = division(4).ws_bytes(Hkv, D), w8 = many_rows(T, B, G, D) ? division(8).ws_bytes(Hkv, D) : 0;
+  const size_t w4 = chunk_division(4).ws_bytes(Hkv, D), w8 = many_rows(T, B, G, D) ? chunk_division(8).ws_bytes(Hkv, D) : 0;
   return w4 > w8 ? w4 : w8;   // (which of the two depends on the page table's columns, too)
 }
 

@@ -26,18 +26,16 @@ namespace nvfp4moe {
 
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kWaves = kFewWaves;
 constexpr int kRows = 16;          // rows of a tile
-// (Least blocks of a segment: joining costs a second launch, so that a few blocks more a wave cost less.)
-constexpr Division division(bool fp8) { return {4, fp8 ? 6 : 5, 10, 16, kWaves}; }
 template <bool FP8>
 struct OfCache {
-  static constexpr Division kDivision = division(FP8);
+  static constexpr Division kDivision = few_division(FP8);
 };
 
 template <int D, bool FP8>
 struct Few {
-  static constexpr Division kDivision = division(FP8);
+  static constexpr Division kDivision = few_division(FP8);
   static constexpr int kBlockLog = kDivision.block_log, kBlock = 1 << kBlockLog;   // keys of a block
   static constexpr int kTiles = kBlock / 16;       // tiles of 16 keys in the first product
   static constexpr int kDSteps = D / 32;           // its steps
@@ -393,7 +391,7 @@ hipError_t launch_d(const KvAttnArgs& a, hipStream_t stream) {
 // tokens over 8000 keys (64 heads of 8 groups, D 128, bf16) 155 / 126 us, of 8 tokens 262 / 129 us.
 bool kv_attention_few_fits(int T, int B, int G) { return (int64_t)T * G <= (int64_t)kRows * B; }
 
-size_t kv_attention_few_ws_bytes(int Hkv, int D) { return division(false).ws_bytes(Hkv, D); }
+size_t kv_attention_few_ws_bytes(int Hkv, int D) { return few_division(false).ws_bytes(Hkv, D); }
 
 hipError_t launch_kv_attention_few(const KvAttnArgs& a, hipStream_t stream) {
   return a.fp8 ? launch_d<true>(a, stream) : launch_d<false>(a, stream);
