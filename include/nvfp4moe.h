@@ -654,7 +654,8 @@ nvfp4moe_status rope_rotate(const void* x, nvfp4moe_dtype dtype, int64_t x_row, 
  *     lengths     int32 [B]: tokens of each sequence, its new ones among them
  *     starts      int32 [B + 1], not decreasing: sequence b's new tokens are the rows
  *                 [starts[b], starts[b + 1]) of the T rows of q, k, v and out; they are its last ones,
- *                 so that row starts[b] + i has the position lengths[b] - (new tokens) + i.
+ *                 so that row starts[b] + i has the position lengths[b] - (new tokens) + i. Starts below 0
+ *                 or above T count as 0 or T.
  * All three are device memory. Rows outside [starts[0], starts[B]) are not read, and left as they were in
  * outputs. Entries that no visible token lies behind may hold anything.
  *

@@ -230,7 +230,8 @@ __device__ __forceinline__ Place place_of(const KvAppendArgs& p, int t, const in
     else
       hi = mid;
   }
-  const int64_t pos = (int64_t)b.lengths[lo] - start(lo + 1) + t;
+  // (counted from the sequence's last row that is there, as the attention counts)
+  const int64_t pos = (int64_t)b.lengths[lo] - min(start(lo + 1), b.T) + t;
   w.row = t;
   w.position = p.positions ? position_at(p.positions, p.pos64, t) : (double)pos;
   const int64_t col = pos >> b.page_log;
