@@ -52,6 +52,14 @@ __device__ __forceinline__ Seen seen_by(int position, int window, int cap) {
   return {first_seen(position, window), min(max(position + 1, 0), cap)};
 }
 
+// What the sums of new token i's row are multiplied by, `total` being that of its weights: zeros where it sees no key, which
+// is where it lies before its sequence; NaN where the page table has no column for it. A row that sees keys has a
+// total above 0 unless all its scores are -Inf: 0 / 0, NaN, as its softmax.
+__device__ __forceinline__ float normalize(const Sequence& q, int i, float total, float v_scale) {
+  const int p = q.position(i);
+  return p < 0 ? 0.0f : p >= q.cap ? NAN : v_scale / total;
+}
+
 // Inclusive sums over the lanes by DPP moves (no LDS round trips): within rows of 16, then rows 1 and 3
 // take the row before, then rows 2 and 3 the first half's.
 __device__ __forceinline__ int wave_scan(int v) {
@@ -192,8 +200,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(const KvAttnArgs p, 
     if (!mine || group > 0) continue;
     for (int i = 1; i < groups; ++i) add(s_ml[threadIdx.x + i * lanes], s_o[threadIdx.x + i * lanes]);
     const int at = (sg.tile << v.tile_log) + r, t = at / p.G;
-    float f = l == 0.0f ? 0.0f : (FP8 && p.v_scale ? p.v_scale[h] : 1.0f) / l;
-    if (sg.seq.position(t) >= sg.seq.cap) f = NAN;
+    const float f = normalize(sg.seq, t, l, FP8 && p.v_scale ? p.v_scale[h] : 1.0f);
     uint16_t* to = p.out + (sg.seq.row0 + t) * p.o_row + (h * p.G + at - t * p.G) * p.o_head + 4 * lane;
     *reinterpret_cast<uint2*>(to) = make_uint2(bf16x2(o.x * f, o.y * f), bf16x2(o.z * f, o.w * f));
   }

@@ -598,8 +598,7 @@ __global__ __launch_bounds__(W* kWave, D > 128 ? 1 : 2) void chunk_kernel(const 
       part.ml[2 * r + 1] = l;
     }
   } else {
-    float f = l == 0.0f ? 0.0f : (FP8 && p.v_scale ? p.v_scale[h] : 1.0f) / l;
-    if (seq.position(token) >= seq.cap) f = NAN;
+    const float f = normalize(seq, token, l, FP8 && p.v_scale ? p.v_scale[h] : 1.0f);
     uint16_t* to = p.out + (seq.row0 + token) * p.o_row + head * p.o_head + 4 * half;
 #pragma unroll
     for (int d = 0; d < C::kDTiles; ++d)

@@ -339,9 +339,7 @@ __global__ __launch_bounds__(kWaves* kWave, D > 128 ? 1 : 2) void few_kernel(con
       }
     } else {
       const int at = sg.tile * kRows + r, t = at / p.G;
-      // no key seen: zeros; a position that the page table has no column for: NaN
-      float f = total == 0.0f ? 0.0f : v_scale / total;
-      if (sg.seq.position(t) >= sg.seq.cap) f = NAN;
+      const float f = normalize(sg.seq, t, total, v_scale);
       uint16_t* to = p.out + (sg.seq.row0 + t) * p.o_row + (h * p.G + at - t * p.G) * p.o_head + d;
       *reinterpret_cast<uint4*>(to) = make_uint4(bf16x2(v[0] * f, v[1] * f), bf16x2(v[2] * f, v[3] * f),
                                                  bf16x2(v[4] * f, v[5] * f), bf16x2(v[6] * f, v[7] * f));

@@ -1,4 +1,4 @@
-"""The attention half at the ends of what its calls take: starts outside the rows."""
+"""The attention half at the ends of what its calls take: starts outside the rows, rows whose scores are all -Inf."""
 import pytest
 import torch
 
@@ -28,3 +28,26 @@ def test_starts_outside_the_rows(new, ctx, fp8):
     assert torch.isfinite(got[0][3]).all()
     for other in got[1:]:
         assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("new,ctx", [([3], 70), ([2], 4200), ([40], 70), ([40], 4200), ([150], 4200)])
+def test_rows_whose_scores_are_all_minus_infinity(new, ctx, fp8):
+    """The softmax of such a row is NaN, in one part and across a join, and its neighbours' is theirs; the same row before its
+    sequence, where it sees no key, gives zeros."""
+    c = Case(new, [ctx], 8, 1, 128, 64, fp8=fp8, seed=20)
+    n, head = new[0], 3
+    k = c.cache.k.clone()
+    k[:, :, :, 0] = torch.tensor(1.0).to(k.dtype)
+    cache = ops.KVCache(k, c.cache.v, c.cache.k_scale, c.cache.v_scale)
+    q = c.q.cuda()
+    want = ops.kv_cache_attention(q, cache, c.batch)
+    low = q.clone()
+    low[n // 2, head, 0] = float("-inf")
+    got = ops.kv_cache_attention(low, cache, c.batch)
+    assert torch.isnan(got[n // 2, head]).all()
+    got[n // 2, head] = want[n // 2, head]
+    assert torch.equal(got, want)
+    short = ops.CacheBatch(c.batch.page_table, torch.full_like(c.batch.lengths, n - n // 2 - 1), c.batch.starts)
+    got = ops.kv_cache_attention(low, cache, short)
+    assert (got[:n // 2 + 1] == 0).all() and torch.isfinite(got).all() and (got[n // 2 + 1:] != 0).any(-1).all()
