@@ -695,11 +695,12 @@ nvfp4moe_status kv_cache_append(const void* q, int64_t q_row, int64_t q_head, co
  *                sizes that the call refuses). Calls that may overlap need a workspace each.
  * Scores, running maxima and sums are float32 and out is rounded once. Up to 16 rows (token, query
  * head of a group) a sequence on average, the exponentials that weigh the values count as 16 bits;
- * above, they are rounded to bf16, or to f16 with an FP8 cache. A row that sees no key (a position below 0)
- * gives zeros, one all of whose visible keys have a score of -Inf NaN. What a page holds behind a sequence's last
- * token, and keys and values that a row does not see, do not reach it, NaN and Inf included; a visible value that
- * is not finite makes its dim NaN or Inf in the rows that see it. A row that sees a key whose page is not in
- * [0, pages), or whose position lies behind the page table's columns, gives NaN.
+ * above, they are rounded to bf16, or to f16 with an FP8 cache. Sums are divided by the weights' at the end:
+ * finite values whose largest times the number of keys is below 2^116 do not overflow. A row that sees no key (a
+ * position below 0) gives zeros, one all of whose visible keys have a score of -Inf NaN. What a page holds behind a
+ * sequence's last token, and keys and values that a row does not see, do not reach it, NaN and Inf included; a
+ * visible value that is not finite makes its dim NaN or Inf in the rows that see it. A row that sees a key whose
+ * page is not in [0, pages), or whose position lies behind the page table's columns, gives NaN.
  * ------------------------------------------------------------------------- */
 nvfp4moe_status kv_cache_attention(const void* q, int64_t q_row, int64_t q_head, int32_t T, int32_t Hq, int32_t Hkv,
                                    int32_t D, const int32_t* page_table, int64_t ld_table, int32_t cols,

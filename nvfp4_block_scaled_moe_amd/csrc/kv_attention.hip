@@ -14,7 +14,7 @@
 // at a time through three stages that do not wait for each other (below); the others, at the diagonal and a
 // window's start, are masked and taken one after another.
 //
-// 2048 tokens over 14000 keys, 64 heads over 8, bf16: D 128 916 to 987 us by card, 1.02 to 1.10 PFLOP/s (a large
+// 2048 tokens over 14000 keys, 64 heads over 8, bf16: D 128 915 to 987 us by card, 1.02 to 1.10 PFLOP/s (a large
 // matrix product reaches 1.42), D 64 600 us (0.84: twice the exponentials for a flop); E4M3 2 to 5% more. 32 heads
 // of 96 / 160 / 192 / 224 / 256 over 6000: 0.85 / 0.69 / 0.67 / 0.65 / 0.70 PFLOP/s (one wave a SIMD from D 160 on:
 // the outputs fill the registers). The matrix cores are busy half of the time at a clock that the power limit holds
@@ -624,8 +624,10 @@ hipError_t launch(const KvAttnArgs& a, hipStream_t stream) {
 }
 
 // Waves of a workgroup. 8 for D 128 (D 64 has three waves a SIMD with W 4: 614 us, 657 with 8), where sequences have
-// rows for whole tiles of 256, on average, and keys enough that what these bring is most of the time: 2048 new tokens
-// over 14000 keys 950 us, 1013 with 4, 128 over 30000 136 and 146; but 8 prompts of 1024 tokens 222, 215 with 4.
+// rows for whole tiles of 256, on average, and the page table has columns for keys enough that what these bring is most
+// of the time: 2048 new tokens over 14000 keys 930 us, 995 with 4, 128 over 30000 139 and 149; but 8 prompts of 1024
+// tokens 222, 215 with 4. What a sequence has of those keys, and what a window leaves of them, is not looked at: these
+// prompts in a table of 33000 tokens take 215, 206 with 4, and the first case with a window of 1000 103, 97 with 4.
 bool many_rows(int T, int B, int G, int D) { return D == 128 && (int64_t)T * G >= (int64_t)1024 * B; }
 int waves_of(const KvAttnArgs& a) {
   return many_rows(a.batch.T, a.batch.B, a.G, a.D) && (int64_t)a.batch.cols << a.batch.page_log >= 4096 ? 8 : 4;

@@ -387,6 +387,9 @@ hipError_t launch_d(const KvAttnArgs& a, hipStream_t stream) {
 // Up to 16 rows (token, head of the group) a sequence on average. Tiles of 32 and 64 rows here, one wave a
 // SIMD for their sums, were slower than the tiles of 128 rows with most of them empty: 16 sequences of 4
 // tokens over 8000 keys (64 heads of 8 groups, D 128, bf16) 155 / 126 us, of 8 tokens 262 / 129 us.
+// The host knows the average alone. In batches that mix single tokens (over 200 to 3500 keys each) with one prompt's
+// chunk, by tiles of 16 rows / of 128: 32 beside 500 tokens, G 4, E4M3 111 / 77 us, bf16 176 / 81; 63 beside 100, G 8,
+// 150 / 92; 95 beside 1400, G 1, which the average sends here, E4M3 232 / 234, but bf16 509 / 266.
 bool kv_attention_few_fits(int T, int B, int G) { return (int64_t)T * G <= (int64_t)kRows * B; }
 
 size_t kv_attention_few_ws_bytes(int Hkv, int D) { return few_division(false).ws_bytes(Hkv, D); }

@@ -57,9 +57,10 @@ constexpr int kFewWaves = 4;
 constexpr Division few_division(bool fp8) { return {4, fp8 ? 6 : 5, 10, 16, kFewWaves}; }
 
 // Of tiles of 128 and 256 rows (kv_attention.hip), W waves to a workgroup: 4, two workgroups a CU, or 8, one a CU, whose
-// tiles bring half the words for a row. The segments are as many as workgroups that a CU holds at once (with W 4 and
-// 1024 segments, 16 sequences of 4 tokens over 8000 keys took 112 instead of 105 us; 640 and 768, which leave a part
-// round, are slower yet: 125 and 115).
+// tiles bring half the words for a row. The segments are as many as workgroups that the CUs hold at once. With W 4, 512
+// and 1024 of them: 16 sequences of 4 tokens over 8000 keys 103 and 111 us, E4M3 66 and 74; two E4M3 sequences of 1 and
+// 4 tokens over 90000 to 130000 109 and 117; 2048 tokens over 6000 of D 256 668 and 716; whole prompts, windows and D 64
+// the same. (640 and 768, which leave a part round: 125 and 115 us for the first, which took 105 then.)
 constexpr int kChunkBlockLog = 6;   // keys of a block
 constexpr Division chunk_division(int W) { return {W == 8 ? 8 : 7, kChunkBlockLog, W == 8 ? 8 : 9, 8, 1}; }
 

@@ -16,7 +16,7 @@
 // Bound by memory: x is read once and written once. 8192 tokens of 64 heads of 128 in bf16 (268 MB in and out)
 // take 51 to 55 us, 4.9 to 5.3 TB/s, what a large copy reaches; a float32 gradient of 25 MB 8.5 us. The append of
 // 13 thousand tokens of 64 + 2 x 8 heads of 128 (536 MB) takes 114 to 120 us, 4.5 to 4.7 TB/s: its keys and queries
-// alone 104, its transposed values 13. There the vector units are half busy beside the reads (angles, turns, the
+// alone 104, its transposed values 13; into E4M3 (510 MB) 116, a byte a lane in the values' stores. There the vector units are half busy beside the reads (angles, turns, the
 // walk over items), so the walk has no divisions (122 us with them) and angles are computed once for all heads.
 // A single token is one dependent chain (sequence, length, page, angles, rows): 3.5 us to turn, 5.2 to append.
 #include "common.h"
