@@ -627,7 +627,8 @@ nvfp4moe_status moe_block_norm(const void* resid, nvfp4moe_dtype r_dtype, int64_
  *     u' = magnitude * (u cos a - w sin a)      w' = magnitude * (w cos a + u sin a)
  * pairs being the dims (i, i + rot / 2) of that part or, interleaved, (2i, 2i + 1). The other dims
  * are copied. With grad the rotation is transposed (by -a): x's gradient, of out's in x's place.
- * Angles are taken in float64, their cosines and the products in float32, rounded once.
+ * Angles are taken in float64, with F32 their cosines, too, with BF16 these in float32, of a float32 angle
+ * beyond whole turns; the products in float32, rounded once.
  *   x, out       device [T, H, D] of dtype (F32 or BF16), element distances x_row and x_head (o_row,
  *                o_head) between rows and heads, the dims of a head beside each other; the distance
  *                of heads is at least D, that of rows at least (H - 1) * the heads' + D. out may be x
