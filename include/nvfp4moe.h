@@ -668,8 +668,8 @@ nvfp4moe_status rope_rotate(const void* x, nvfp4moe_dtype dtype, int64_t x_row, 
  *   positions    device int32 or int64 [T] for the angles, or NULL: the tokens' positions above.
  *   freqs        NULL: nothing is turned (rot, start, interleaved, magnitude and positions are not
  *                used). Otherwise as in rope_rotate.
- *   cache_fp8    keys (in float32, turned) and values are divided by the head's scale and rounded to
- *                E4M3 once, saturating at +-448; NaN stays NaN.
+ *   cache_fp8    keys (in float32, turned) and values are divided by the head's scale in float32 and the
+ *                quotients rounded to E4M3, saturating at +-448; NaN stays NaN.
  *   T, B         T >= 0 (0: nothing is done), B >= 1; T * Hq * D < 2^47, Hq * D < 2^24.
  * Tokens whose position is negative or behind the page table's columns, or whose page is not in [0, pages),
  * are not written to the cache. Two tokens of a batch must not share a place of it.
