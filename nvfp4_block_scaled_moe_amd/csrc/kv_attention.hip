@@ -14,7 +14,7 @@
 // at a time through three stages that do not wait for each other (below); the others, at the diagonal and a
 // window's start, are masked and taken one after another.
 //
-// 2048 tokens over 14000 keys, 64 heads over 8, bf16: D 128 915 to 987 us by card, 1.02 to 1.10 PFLOP/s (a large
+// 2048 tokens over 14000 keys, 64 heads over 8, bf16: D 128 915 to 991 us by card, 1.02 to 1.10 PFLOP/s (a large
 // matrix product reaches 1.42), D 64 600 us (0.84: twice the exponentials for a flop); E4M3 2 to 5% more. 32 heads
 // of 96 / 160 / 192 / 224 / 256 over 6000: 0.85 / 0.69 / 0.67 / 0.65 / 0.70 PFLOP/s (one wave a SIMD from D 160 on:
 // the outputs fill the registers). The matrix cores are busy half of the time at a clock that the power limit holds
